@@ -3,7 +3,11 @@
 ``forward``/``backward``/``decode`` take torch CUDA tensors; ``fa_*`` are the raw C-ABI
 calls with the names of include/fa.h.  The library is loaded on first use.
 """
-from .fa import (FaError, backward, backward_varlen, decode, decode_paged, fa_bwd,  # noqa: F401
+from .fa import (FaError, append_paged_fp8, backward, backward_varlen, compact_pages,  # noqa: F401
+                 copy_pages, decode, decode_paged, decode_paged_fp8, fa_append_paged_fp8, fa_bwd,
+                 fa_compact_pages, fa_copy_pages, fa_decode_paged_fp8,
+                 fa_decode_paged_fp8_workspace_bytes, fa_fork_pages, fa_free_pages, fork_pages,
+                 free_pages,
                  fa_bwd_workspace_bytes, fa_decode, fa_decode_num_splits, fa_decode_paged,
                  fa_decode_uses_tensor_cores,
                  fa_decode_paged_num_splits, fa_decode_paged_workspace_bytes,

@@ -907,18 +907,272 @@ extern "C" int fa_decode_paged(const void *q, const void *k_cache, const void *v
     return decode_launch(p, B, num_splits, workspace, workspace_bytes, stream);
 }
 
+namespace fa {
+namespace {
+
+// Sizes of a paged e4m3 cache and its table.
+int check_cache8(int B, int Hkv, int d, int page_size, int max_pages, int num_pages,
+                 int scale_group) {
+    if (B < 1 || Hkv < 1 || page_size < 1 || max_pages < 1 || num_pages < 1 || scale_group < 1)
+        return FA_ERR_INVALID_ARG;
+    if (page_size % scale_group != 0) return FA_ERR_INVALID_ARG;
+    if ((long long)page_size * max_pages >= (1LL << 31) || (long long)B * max_pages >= (1LL << 31) ||
+        (long long)num_pages * Hkv >= (1LL << 31))
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 96 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cache,
+                                   float *k_scale, float *v_scale, const int *block_table,
+                                   const int *seq_lens, const int *cu_seqlens, int B, int T, int Hkv,
+                                   int d, int page_size, int max_pages_per_seq, int num_pages,
+                                   int scale_group, long long k_stride, long long v_stride,
+                                   void *stream) {
+    if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_cache8(B, Hkv, d, page_size, max_pages_per_seq, num_pages, scale_group);
+    if (rc != FA_OK) return rc;
+    if (T < 1 || scale_group > 128 || (!cu_seqlens && T != B)) return FA_ERR_INVALID_ARG;
+    const long long row = (long long)Hkv * d;
+    if (k_stride < row || v_stride < row) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scale) || !aligned4(v_scale) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_seqlens))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    AppendParams p{};
+    p.k = k;
+    p.v = v;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = static_cast<uint8_t *>(k_cache);
+    p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.cu_seqlens = cu_seqlens;
+    p.B = B;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.group = scale_group;
+    // rows per window: about what one group gets of this call (T / B rows per sequence)
+    const int per_seq = T / B < 1 ? 1 : T / B;
+    p.window = per_seq < scale_group ? per_seq : scale_group;
+    p.status = dc->status;
+    return launch_append(p, static_cast<cudaStream_t>(stream));
+}
+
+namespace fa {
+namespace {
+
+int check_decode8(int B, int H, int Hkv, int Nq, int d, int page_size, int max_pages, int num_pages,
+                  int scale_group) {
+    int rc = check_cache8(B, Hkv, d, page_size, max_pages, num_pages, scale_group);
+    if (rc == FA_ERR_INVALID_ARG) return rc;
+    const int rc2 = check_decode_sizes(B, H, Hkv, Nq, 1, d);
+    return rc2 != FA_OK ? rc2 : rc;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" size_t fa_decode_paged_fp8_workspace_bytes(int B, int H, int Hkv, int Nq, int d,
+                                                      int page_size, int max_pages_per_seq) {
+    if (check_decode8(B, H, Hkv, Nq, d, page_size, max_pages_per_seq, 1, 1) != FA_OK) return 0;
+    return 16;
+}
+
+extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                   const float *k_scale, const float *v_scale,
+                                   const int *block_table, const int *seq_lens, void *o, float *lse,
+                                   int B, int H, int Hkv, int Nq, int d, int page_size,
+                                   int max_pages_per_seq, int num_pages, int scale_group, int causal,
+                                   float scale, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !o || !lse)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_decode8(B, H, Hkv, Nq, d, page_size, max_pages_per_seq, num_pages, scale_group);
+    if (rc != FA_OK) return rc;
+    if ((rc = check_scale(scale)) != FA_OK) return rc;
+    const size_t need =
+        fa_decode_paged_fp8_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages_per_seq);
+    if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+        !aligned4(lse) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned16(workspace))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    Decode8Params p{};
+    p.q = q;
+    p.k = static_cast<const uint8_t *>(k_cache);
+    p.v = static_cast<const uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.group = scale_group;
+    p.causal = causal ? 1 : 0;
+    p.scale_log2 = scale * kLog2e;
+    p.status = dc->status;
+    p.num_sms = dc->num_sms;
+    return launch_decode8(p, static_cast<cudaStream_t>(stream));
+}
+
+namespace fa {
+namespace {
+
+int check_pages(int B, int max_pages, int page_size, int num_pages) {
+    if (B < 1 || max_pages < 1 || page_size < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+    if ((long long)B * max_pages >= (1LL << 31) || (long long)page_size * max_pages >= (1LL << 31))
+        return FA_ERR_INVALID_ARG;
+    return num_pages <= kMaxPlanPages ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" int fa_free_pages(const int *block_table, const int *seq_lens, int *pages, int *count,
+                             int B, int max_pages_per_seq, int page_size, int num_pages,
+                             void *stream) {
+    if (!block_table || !seq_lens || !pages || !count) return FA_ERR_INVALID_ARG;
+    int rc = check_pages(B, max_pages_per_seq, page_size, num_pages);
+    if (rc != FA_OK) return rc;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(pages) || !aligned4(count))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    PagesParams p{};
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.pages = pages;
+    p.counts = count;
+    p.B = B;
+    p.max_pages = max_pages_per_seq;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.status = dc->status;
+    return launch_pages(p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa_fork_pages(const int *block_table, const int *seq_lens, const int *parents,
+                             const int *fresh, int *rows, int *lens, int *src, int *dst, int B, int n,
+                             int max_pages_per_seq, int page_size, int num_pages, void *stream) {
+    if (!block_table || !seq_lens || !parents || !fresh || !rows || !lens || !src || !dst || n < 1)
+        return FA_ERR_INVALID_ARG;
+    int rc = check_pages(B, max_pages_per_seq, page_size, num_pages);
+    if (rc != FA_OK) return rc;
+    if ((long long)n * max_pages_per_seq >= (1LL << 31)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(parents) || !aligned4(fresh) ||
+        !aligned4(rows) || !aligned4(lens) || !aligned4(src) || !aligned4(dst))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    ForkParams p{};
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.parents = parents;
+    p.fresh = fresh;
+    p.rows = rows;
+    p.lens = lens;
+    p.src = src;
+    p.dst = dst;
+    p.B = B;
+    p.n = n;
+    p.max_pages = max_pages_per_seq;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.status = dc->status;
+    return launch_fork(p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa_compact_pages(const int *block_table, const int *seq_lens, int *new_table, int *src,
+                                int *dst, int *counts, int B, int max_pages_per_seq, int page_size,
+                                int num_pages, void *stream) {
+    if (!block_table || !seq_lens || !new_table || !src || !dst || !counts) return FA_ERR_INVALID_ARG;
+    int rc = check_pages(B, max_pages_per_seq, page_size, num_pages);
+    if (rc != FA_OK) return rc;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_table) || !aligned4(src) ||
+        !aligned4(dst) || !aligned4(counts))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    PagesParams p{};
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.new_table = new_table;
+    p.src = src;
+    p.dst = dst;
+    p.counts = counts;
+    p.B = B;
+    p.max_pages = max_pages_per_seq;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.cap = num_pages / 2 > 1 ? num_pages / 2 : 1;
+    p.status = dc->status;
+    return launch_pages(p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa_copy_pages(void *const *caches, const size_t *page_bytes, int n_caches,
+                             int num_pages, const int *src, const int *dst, int n_pairs,
+                             const int *count, void *stream) {
+    if (!caches || !page_bytes || !src || !dst) return FA_ERR_INVALID_ARG;
+    if (n_caches < 1 || n_caches > FA_MAX_COPY_CACHES || num_pages < 1 || n_pairs < 1)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst) || !aligned4(count)) return FA_ERR_MISALIGNED;
+    CopyParams p{};
+    for (int c = 0; c < n_caches; ++c) {
+        if (!caches[c] || page_bytes[c] < 1 || page_bytes[c] >= ((size_t)1 << 40))
+            return FA_ERR_INVALID_ARG;
+        p.cache[c] = caches[c];
+        p.page_bytes[c] = page_bytes[c];
+    }
+    DeviceCache *dc = nullptr;
+    const int rc = current_device(&dc);
+    if (rc != FA_OK) return rc;
+    p.n_caches = n_caches;
+    p.num_pages = num_pages;
+    p.n_pairs = n_pairs;
+    p.src = src;
+    p.dst = dst;
+    p.count = count;
+    p.status = dc->status;
+    p.num_sms = dc->num_sms;
+    return launch_copy(p, static_cast<cudaStream_t>(stream));
+}
+
 extern "C" const char *fa_status_string(int status) {
     switch (status) {
         case FA_OK: return "FA_OK";
         case FA_ERR_INVALID_ARG: return "FA_ERR_INVALID_ARG: invalid argument";
-        case FA_ERR_UNSUPPORTED: return "FA_ERR_UNSUPPORTED: head dimension not supported";
+        case FA_ERR_UNSUPPORTED: return "FA_ERR_UNSUPPORTED: head dimension or size not supported";
         case FA_ERR_MISALIGNED: return "FA_ERR_MISALIGNED: pointer not aligned (16 bytes for tensors)";
         case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA runtime or driver call failed";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a bounded in-kernel wait ran out";
         case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE: workspace missing or too small";
         case FA_ERR_BAD_INDEX:
-            return "FA_ERR_BAD_INDEX: a block-table entry, sequence length or sequence offset "
-                   "was out of range";
+            return "FA_ERR_BAD_INDEX: a block-table entry, page, sequence length or sequence "
+                   "offset was out of range";
         default: return "unknown fa_status";
     }
 }

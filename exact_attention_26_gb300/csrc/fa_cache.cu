@@ -1,0 +1,567 @@
+// Filling and keeping a paged key/value cache: storing new tokens as e4m3 codes with a
+// power-of-two scale per group of tokens and head, and the upkeep of the pages (listing
+// the unused ones, forking sequences, compaction, copying).  The definitions are in fa.h.
+#include <cooperative_groups.h>
+
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ void flag_index(int *status, int site) {
+    atomicCAS(status + 1, 0, site);
+    atomicExch(status, FA_ERR_BAD_INDEX);
+}
+
+// ------------------------------------------------------------------ append
+//
+// A group's new codes need the group's largest magnitude first, so its rows are held in
+// registers between the maximum and the conversion and read once: 2 bytes in, 1 byte out
+// per element, bound by HBM.  A team of W warps owns one (group, head, key or value); warp
+// w of it takes rows w, w + W, ... (at most 16 of them), a lane E consecutive elements.
+// Teams are handed out by windows of `window` consecutive rows of the call: a team walks
+// the groups that begin in its window, which needs no list of the groups (their number is
+// only known on the device).  The host sets the window to about the rows a group gets, so a
+// window holds about one group whether the call stores prompts or one token per sequence.
+
+template <int D>
+struct RowLanes {
+    static constexpr int E = (D == 96) ? 4 : D / 32;  // d = 96: 24 lanes of 4
+    static constexpr int LANES = D / E;
+    static constexpr int WORDS = E / 2;  // 32-bit words of bf16 pairs per lane
+};
+
+constexpr int kRowsPerWarp = 16;
+constexpr int kAppendThreads = 256;
+
+template <int D>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, uint32_t (&u)[RowLanes<D>::WORDS]) {
+    if constexpr (RowLanes<D>::WORDS == 1) {
+        u[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (RowLanes<D>::WORDS == 2) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        u[0] = w.x; u[1] = w.y;
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+    }
+}
+
+// E e4m3 codes of a lane, in one access of E bytes.
+template <int E>
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&c)[(E + 3) / 4]) {
+    if constexpr (E == 2) *reinterpret_cast<uint16_t *>(p) = (uint16_t)c[0];
+    else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(p) = c[0];
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+}
+
+template <int E>
+__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&c)[(E + 3) / 4]) {
+    if constexpr (E == 2) c[0] = *reinterpret_cast<const uint16_t *>(p);
+    else if constexpr (E == 4) c[0] = *reinterpret_cast<const uint32_t *>(p);
+    else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        c[0] = w.x; c[1] = w.y;
+    }
+}
+
+// Value of an e4m3 code (in the low byte): e4m3's exponent bias is 7 and bf16's 127, so the
+// code's bits moved to a bf16's places read as value * 2^-120 (subnormals too).
+__device__ __forceinline__ float e4m3_float(uint32_t c) {
+    const uint32_t m = c & 0x7fu;
+    const float v = __uint_as_float(((c & 0x80u) << 24) | (m << 20)) * 0x1p120f;
+    return m == 0x7fu ? __uint_as_float(0x7fc00000u) : v;
+}
+
+template <int E>
+__device__ __forceinline__ void encode(const float (&y)[E], uint32_t (&c)[(E + 3) / 4]) {
+    if constexpr (E == 2) {
+        c[0] = pack_e4m3x4(y[0], y[1], 0.f, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+            c[i] = pack_e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    }
+}
+
+// The largest finite magnitude of a word's two bf16 values, as its 15 bits (bf16
+// magnitudes order like the integers of their bits; 0x7f80 and up are not finite).
+__device__ __forceinline__ uint32_t amax_bits(uint32_t u) {
+    const uint32_t a = u & 0x7fffu, b = (u >> 16) & 0x7fffu;
+    return max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
+}
+
+// The least power of two s >= 2^-126 with amax <= 448 s: amax = m 2^e, 448 = 1.75 * 2^8,
+// so s = 2^(e - 8) where m <= 1.75 (mantissa 0x60 of 7 bits) and 2^(e - 7) above.
+__device__ __forceinline__ float least_scale(uint32_t amax) {
+    const int e = (int)(amax >> 7) - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);  // biased by 127
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+
+template <int D, int W>
+__global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
+    using L = RowLanes<D>;
+    constexpr int E = L::E, CW = (E + 3) / 4;
+    constexpr int TEAMS = kAppendThreads / 32 / W;
+    __shared__ uint32_t s_amax[TEAMS][W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int team = warp / W, w = warp % W;
+    const bool on = lane < L::LANES;
+    // heads fastest: the CTAs that run together read whole rows of the call
+    const int job_ctas = (2 * p.Hkv + TEAMS - 1) / TEAMS;
+    const int job = (int)(blockIdx.x % job_ctas) * TEAMS + team;  // (head, key or value)
+    if (job >= 2 * p.Hkv) return;
+    const int h = job >> 1;
+    const bool is_v = job & 1;
+    const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(is_v ? p.v : p.k);
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    uint8_t *cache = is_v ? p.v_cache : p.k_cache;
+    float *scales = is_v ? p.v_scale : p.k_scale;
+    const int G = p.group, ps = p.page_size, groups = ps / G;
+
+    int t = (int)(blockIdx.x / job_ctas) * p.window;
+    const int t_end = (int)min((long long)p.T, (long long)t + p.window);
+    int b;
+    if (p.cu_seqlens == nullptr) {
+        b = t;
+    } else {
+        // the last b with cu[b] <= t (0 if there is none), by steps of 32 pivots
+        int lo = 0, n = p.B;
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const int i = lane * step;
+            const bool le = i < n && p.cu_seqlens[lo + i] <= t;
+            const unsigned m = __ballot_sync(kFull, le);
+            const int k = m ? 31 - __clz(m) : 0;
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
+        b = lo;
+        if (blockIdx.x == 0 && job == 0 && w == 0) {
+            bool ok = true;  // the offsets, checked once per call
+            for (int i = lane; i < p.B; i += 32) {
+                const int c0 = p.cu_seqlens[i], c1 = p.cu_seqlens[i + 1];
+                ok = ok && c0 >= 0 && c0 <= c1 && c1 <= p.T;
+            }
+            if (!__all_sync(kFull, ok) && lane == 0) flag_index(p.status, SITE_APPEND_BAD_SEQ);
+        }
+    }
+    // Walk the groups that begin at rows t .. t_end - 1 (all values are uniform over the team).
+    while (t < t_end && b < p.B) {
+        const int c0 = p.cu_seqlens ? p.cu_seqlens[b] : b;
+        const int c1 = p.cu_seqlens ? p.cu_seqlens[b + 1] : b + 1;
+        if (t >= c1) {  // an empty sequence, or the end of this one
+            ++b;
+            continue;
+        }
+        if (c0 < 0 || c1 > p.T) break;
+        if (t < c0) {  // rows before the first sequence
+            t = c0;
+            continue;
+        }
+        const int start = p.seq_lens[b];
+        const long long room = (long long)ps * p.max_pages;
+        if (start < 0 || start + (long long)(c1 - c0) > room) {
+            if (job == 0 && w == 0 && lane == 0) flag_index(p.status, SITE_APPEND_BAD_SEQ);
+            t = c1;
+            continue;
+        }
+        const int pos = start + (t - c0);
+        const int in_group = pos % G;
+        const int cnt = min(G - in_group, c1 - t);  // rows of this group from t on
+        if (t != c0 && in_group != 0) {             // begun in an earlier window
+            t += cnt;
+            continue;
+        }
+        const int page = p.block_table[(size_t)b * p.max_pages + pos / ps];
+        if (page < 0 || page >= p.num_pages) {
+            if (job == 0 && w == 0 && lane == 0) flag_index(p.status, SITE_APPEND_BAD_PAGE);
+            t += cnt;
+            continue;
+        }
+        const size_t ph = (size_t)page * p.Hkv + h;
+        const int g = pos % ps / G;
+        float *sc = scales + ph * groups + g;
+        uint8_t *rows = cache + (ph * ps + (size_t)g * G) * D + lane * E;  // of the group
+
+        uint32_t u[kRowsPerWarp][L::WORDS];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            const int r = w + i * W;
+            if (r < cnt && on) {
+                load_bf16<D>(x + (size_t)(t + r) * stride + (size_t)h * D + lane * E, u[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < L::WORDS; ++e) u[i][e] = 0u;
+            }
+        }
+        const float old = in_group ? *sc : 0.f;
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+            for (int e = 0; e < L::WORDS; ++e) amax = max(amax, amax_bits(u[i][e]));
+        amax = __reduce_max_sync(kFull, amax);
+        if constexpr (W > 1) {
+            if (lane == 0) s_amax[team][w] = amax;
+            named_barrier_sync(1 + team, 32 * W);
+#pragma unroll
+            for (int i = 0; i < W; ++i) amax = max(amax, s_amax[team][i]);
+            named_barrier_sync(1 + team, 32 * W);  // everyone has read before the next group's
+        }
+        const float least = least_scale(amax);
+        const float s = fmaxf(least, old);
+        if (in_group && s > old) {  // the codes that were there, at the larger scale
+            const float ratio = old / s;
+            for (int r = w; r < in_group; r += W) {
+                if (on) {
+                    uint32_t c[CW];
+                    load_codes<E>(rows + (size_t)r * D, c);
+                    float y[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = e4m3_float(c[e / 4] >> (8 * (e % 4))) * ratio;
+                    encode<E>(y, c);
+                    store_codes<E>(rows + (size_t)r * D, c);
+                }
+            }
+        }
+        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+        const float inv = 1.f / s;
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            const int r = w + i * W;
+            if (r < cnt && on) {
+                float y[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t q = u[i][e / 2];
+                    const float f = __uint_as_float(e % 2 ? (q & 0xffff0000u) : (q << 16));
+                    // f * 0 is NaN where f is NaN or infinite, and adds nothing elsewhere
+                    y[e] = __fmaf_rn(f, 0.f, pow2 ? f * inv : __fdiv_rn(f, s));
+                }
+                uint32_t c[CW];
+                encode<E>(y, c);
+                store_codes<E>(rows + (size_t)(in_group + r) * D, c);
+            }
+        }
+        if (w == 0 && lane == 0) *sc = s;
+        t += cnt;
+    }
+}
+
+template <int D, int W>
+int launch_append_t(const AppendParams &p, cudaStream_t stream) {
+    constexpr int TEAMS = kAppendThreads / 32 / W;
+    const long long ctas = (2LL * p.Hkv + TEAMS - 1) / TEAMS * ((p.T - 1LL) / p.window + 1);
+    if (ctas >= (1LL << 31)) return FA_ERR_INVALID_ARG;
+    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D>
+int launch_append_d(const AppendParams &p, cudaStream_t stream) {
+    if (p.group <= 16) return launch_append_t<D, 1>(p, stream);
+    if (p.group <= 32) return launch_append_t<D, 2>(p, stream);
+    if (p.group <= 64) return launch_append_t<D, 4>(p, stream);
+    return launch_append_t<D, 8>(p, stream);
+}
+
+// ------------------------------------------------------------- page bookkeeping
+//
+// Which pages are in use is a bitmap, and a page's new number a rank in it, so one cluster
+// of CTAs does the whole plan in one launch with the bitmap in its shared memory: mark the
+// pages of the table (atomics on the owner's words through distributed shared memory),
+// count the bits of the words before each word, then write the lists.  A launch that is
+// bound by latency: four cluster barriers and two passes over the table.
+
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 1024;
+
+struct Bitmap {
+    cg::cluster_group cluster;
+    uint32_t *words, *before;  // this CTA's part: bits, and bits set before the word (globally)
+    int per_cta;               // words per CTA
+
+    __device__ uint32_t *remote(uint32_t *base, int word) {
+        return cluster.map_shared_rank(base, word / per_cta) + word % per_cta;
+    }
+    __device__ void set(int page) { atomicOr(remote(words, page >> 5), 1u << (page & 31)); }
+    // pages in use below `page`, and whether it is in use itself
+    __device__ int rank(int page, bool *live) {
+        const int w = page >> 5;
+        const uint32_t bits = *remote(words, w);
+        *live = (bits >> (page & 31)) & 1u;
+        return (int)*remote(before, w) + __popc(bits & ((1u << (page & 31)) - 1u));
+    }
+};
+
+// Entries of a table row that are in use.
+__device__ __forceinline__ int used_entries(int len, int page_size, int max_pages, bool *bad) {
+    const int need = len <= 0 ? 0 : (int)(((long long)len + page_size - 1) / page_size);
+    *bad = len < 0 || need > max_pages;
+    return min(need, max_pages);
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    fa_pages_kernel(const PagesParams p, int per_cta) {
+    extern __shared__ uint32_t plan_smem[];
+    __shared__ int s_total, s_warp[kPlanThreads / 32];
+    Bitmap bm{cg::this_cluster(), plan_smem, plan_smem + per_cta, per_cta};
+    const int rank = (int)bm.cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long entries = (long long)p.B * p.max_pages;
+    const long long first = (long long)rank * kPlanThreads + tid;
+    constexpr long long kStep = (long long)kPlanCtas * kPlanThreads;
+
+    for (int i = tid; i < per_cta; i += kPlanThreads) bm.words[i] = 0u;
+    bm.cluster.sync();
+    for (long long i = first; i < entries; i += kStep) {
+        const int b = (int)(i / p.max_pages), col = (int)(i % p.max_pages);
+        bool bad;
+        const int need = used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad);
+        if (bad && col == 0) flag_index(p.status, SITE_PAGES_BAD_LEN);
+        if (col >= need) continue;
+        const int page = p.block_table[i];
+        if (page >= 0 && page < p.num_pages) bm.set(page);
+        else flag_index(p.status, SITE_PAGES_BAD_PAGE);
+    }
+    bm.cluster.sync();
+
+    // bits before each word: a thread's run of words, then the CTA's threads, then the CTAs
+    const int run = (per_cta + kPlanThreads - 1) / kPlanThreads;
+    const int w0 = min(tid * run, per_cta), w1 = min(w0 + run, per_cta);
+    int mine = 0;
+    for (int i = w0; i < w1; ++i) mine += __popc(bm.words[i]);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        int v = s_warp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, v, o);
+            if (lane >= o) v += y;
+        }
+        s_warp[lane] = v;
+        if (lane == 31) s_total = v;
+    }
+    __syncthreads();
+    int base = incl - mine + (warp > 0 ? s_warp[warp - 1] : 0);
+    bm.cluster.sync();
+    int n_live = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+        const int tot = *bm.cluster.map_shared_rank(&s_total, r);
+        if (r < rank) base += tot;
+        n_live += tot;
+    }
+    for (int i = w0; i < w1; ++i) {
+        bm.before[i] = (uint32_t)base;
+        base += __popc(bm.words[i]);
+    }
+    bm.cluster.sync();
+
+    if (p.pages) {
+        const int n_free = p.num_pages - n_live;
+        for (int i = warp; i < per_cta; i += kPlanThreads / 32) {
+            const int page = (rank * per_cta + i) * 32 + lane;
+            const uint32_t bits = bm.words[i];
+            if (page < p.num_pages && !((bits >> lane) & 1u))
+                p.pages[page - (int)bm.before[i] - __popc(bits & ((1u << lane) - 1u))] = page;
+        }
+        for (long long i = n_free + first; i < p.num_pages; i += kStep) p.pages[i] = -1;
+        if (first == 0) p.counts[0] = n_free;
+    } else {
+        bool live;
+        const int below = n_live < p.num_pages ? bm.rank(n_live, &live) : n_live;
+        const int moves = n_live - below;  // pages in use from n_live on = unused ones below it
+        for (int i = warp; i < per_cta; i += kPlanThreads / 32) {
+            const int page = (rank * per_cta + i) * 32 + lane;
+            const uint32_t bits = bm.words[i];
+            const bool in_use = (bits >> lane) & 1u;
+            const int r = (int)bm.before[i] + __popc(bits & ((1u << lane) - 1u));
+            if (page < n_live && !in_use) p.dst[page - r] = page;
+            if (page >= n_live && page < p.num_pages && in_use) p.src[r - below] = page;
+        }
+        for (long long i = moves + first; i < p.cap; i += kStep) p.src[i] = p.dst[i] = -1;
+        if (first == 0) {
+            p.counts[0] = n_live;
+            p.counts[1] = moves;
+        }
+        __threadfence();
+        bm.cluster.sync();  // dst is complete
+        for (long long i = first; i < entries; i += kStep) {
+            const int b = (int)(i / p.max_pages), col = (int)(i % p.max_pages);
+            bool bad;
+            int page = p.block_table[i];
+            if (page >= n_live && page < p.num_pages &&
+                col < used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad)) {
+                const int r = bm.rank(page, &live);
+                page = __ldcg(p.dst + (r - below));
+            }
+            p.new_table[i] = page;
+        }
+    }
+    bm.cluster.sync();  // nobody reads this CTA's words any more
+}
+
+// One CTA per child.
+__global__ void __launch_bounds__(128) fa_fork_kernel(const ForkParams p) {
+    const int i = blockIdx.x;
+    const int parent = p.parents[i];
+    const bool known = parent >= 0 && parent < p.B;
+    int need = 0, len = 0;
+    if (known) {
+        len = p.seq_lens[parent];
+        bool bad;
+        need = used_entries(len, p.page_size, p.max_pages, &bad);
+        if (bad) {
+            if (threadIdx.x == 0) flag_index(p.status, SITE_PAGES_BAD_LEN);
+            len = len < 0 ? 0 : p.page_size * p.max_pages;
+        }
+    } else if (threadIdx.x == 0) {
+        flag_index(p.status, SITE_PAGES_BAD_LEN);
+    }
+    const bool partial = need > 0 && len % p.page_size != 0;
+    const int *from = p.block_table + (size_t)(known ? parent : 0) * p.max_pages;
+    int *row = p.rows + (size_t)i * p.max_pages;
+    for (int c = threadIdx.x; c < p.max_pages; c += blockDim.x) {
+        int page = c < need ? from[c] : -1;
+        if (c < need && (page < 0 || page >= p.num_pages)) {
+            flag_index(p.status, SITE_PAGES_BAD_PAGE);
+            page = -1;
+        }
+        if (partial && c == need - 1) {
+            int to = p.fresh[i];
+            if (to < 0 || to >= p.num_pages) {
+                flag_index(p.status, SITE_PAGES_BAD_PAGE);
+                to = -1;
+            }
+            p.src[i] = to < 0 ? -1 : page;
+            p.dst[i] = page < 0 ? -1 : to;
+            page = to;
+        }
+        row[c] = page;
+    }
+    if (threadIdx.x == 0) {
+        p.lens[i] = len;
+        if (!partial) p.src[i] = p.dst[i] = -1;
+    }
+}
+
+// ---------------------------------------------------------------------- copies
+//
+// A copy is bound by HBM: 2 bytes of traffic per byte.  A page of all buffers is cut into
+// units of 4 KB, one warp each (8 independent 16-byte loads per lane in flight); the small
+// pages of the scales are units of their own.  Warps stride over the units, so one launch of
+// resident CTAs serves any number of pairs, with their number on the device if it must be.
+
+constexpr int kCopyUnit = 4096;
+constexpr int kCopyThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void copy_unit(const uint8_t *s, uint8_t *d, int bytes, int lane) {
+    constexpr int N = 8;
+    const T *a = reinterpret_cast<const T *>(s);
+    T *b = reinterpret_cast<T *>(d);
+    const int n = bytes / (int)sizeof(T);
+    for (int i = lane; i < n; i += 32 * N) {
+        T r[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i + 32 * k < n) r[k] = a[i + 32 * k];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (i + 32 * k < n) b[i + 32 * k] = r[k];
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) fa_copy_pages_kernel(const __grid_constant__ CopyParams p) {
+    const int lane = threadIdx.x & 31;
+    const int per_pair = p.first_unit[p.n_caches];
+    int n = p.n_pairs;
+    if (p.count) n = max(0, min(n, *p.count));
+    const long long units = (long long)n * per_pair;
+    const long long step = (long long)gridDim.x * (kCopyThreads / 32);
+    for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < units;
+         u += step) {
+        const int pair = (int)(u / per_pair), k = (int)(u % per_pair);
+        const int from = p.src[pair];
+        if (from == -1) continue;
+        const int to = p.dst[pair];
+        if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
+            if (lane == 0) flag_index(p.status, SITE_COPY_BAD_PAGE);
+            continue;
+        }
+        int lo = 0, hi = p.n_caches;  // the buffer of unit k: the last with first_unit <= k
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (p.first_unit[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        const unsigned long long pb = p.page_bytes[lo];
+        const unsigned long long off = (unsigned long long)(k - p.first_unit[lo]) * kCopyUnit;
+        const int bytes = (int)min((unsigned long long)kCopyUnit, pb - off);
+        uint8_t *base = static_cast<uint8_t *>(p.cache[lo]);
+        const uint8_t *s = base + (unsigned long long)from * pb + off;
+        uint8_t *d = base + (unsigned long long)to * pb + off;
+        const unsigned long long align = reinterpret_cast<uintptr_t>(base) | pb;
+        if ((align & 15) == 0) copy_unit<uint4>(s, d, bytes, lane);
+        else if ((align & 3) == 0) copy_unit<uint32_t>(s, d, bytes, lane);
+        else copy_unit<uint8_t>(s, d, bytes, lane);
+    }
+}
+
+}  // namespace
+
+int launch_append(const AppendParams &p, cudaStream_t stream) {
+    switch (p.d) {
+        case 64: return launch_append_d<64>(p, stream);
+        case 96: return launch_append_d<96>(p, stream);
+        case 128: return launch_append_d<128>(p, stream);
+        case 256: return launch_append_d<256>(p, stream);
+        default: return FA_ERR_UNSUPPORTED;
+    }
+}
+
+int launch_pages(const PagesParams &p, cudaStream_t stream) {
+    const int words = (p.num_pages + 31) / 32;
+    const int per_cta = (words + kPlanCtas - 1) / kPlanCtas;
+    const int smem = per_cta * 8;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(fa_pages_kernel), smem) != FA_OK)
+        return FA_ERR_CUDA;
+    fa_pages_kernel<<<kPlanCtas, kPlanThreads, smem, stream>>>(p, per_cta);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int launch_fork(const ForkParams &p, cudaStream_t stream) {
+    fa_fork_kernel<<<p.n, 128, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int launch_copy(CopyParams &p, cudaStream_t stream) {
+    long long per_pair = 0;
+    for (int c = 0; c < p.n_caches; ++c) {
+        p.first_unit[c] = (int)per_pair;
+        per_pair += (long long)((p.page_bytes[c] + kCopyUnit - 1) / kCopyUnit);
+        if (per_pair >= (1LL << 31)) return FA_ERR_INVALID_ARG;
+    }
+    p.first_unit[p.n_caches] = (int)per_pair;
+    constexpr int kWarps = kCopyThreads / 32;
+    const long long units = per_pair * p.n_pairs;
+    const long long most = (long long)p.num_sms * (2048 / kCopyThreads);
+    const long long ctas = (units + kWarps - 1) / kWarps;
+    fa_copy_pages_kernel<<<(unsigned)(ctas < most ? ctas : most), kCopyThreads, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace fa

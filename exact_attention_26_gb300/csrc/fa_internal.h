@@ -41,6 +41,13 @@ enum WaitSite : int {
     SITE_DEC_MMA = 28,
     SITE_BWD_ITEM = 29,
     SITE_SELFTEST = 30,
+    SITE_APPEND_BAD_SEQ = 31,
+    SITE_APPEND_BAD_PAGE = 32,
+    SITE_PAGES_BAD_LEN = 33,
+    SITE_PAGES_BAD_PAGE = 34,
+    SITE_COPY_BAD_PAGE = 35,
+    SITE_DEC8_BAD_LEN = 36,
+    SITE_DEC8_BAD_PAGE = 37,
 };
 
 // Default limit of one in-kernel wait.
@@ -160,6 +167,66 @@ struct DecodeParams {
     int *status;
     unsigned long long limit_ns;
 };
+
+// New tokens into the paged e4m3 cache.
+struct AppendParams {
+    const void *k, *v;               // bf16 rows [T][Hkv][d] at the strides below (elements)
+    long long k_stride, v_stride;
+    uint8_t *k_cache, *v_cache;      // e4m3 [num_pages][Hkv][page_size][d]
+    float *k_scale, *v_scale;        // [num_pages][Hkv][page_size / group]
+    const int *block_table, *seq_lens;
+    const int *cu_seqlens;           // [B+1], or null: one token each
+    int B, T, Hkv, d, page_size, max_pages, num_pages, group;
+    int window;                      // consecutive rows a team of warps looks after
+    int *status;
+};
+int launch_append(const AppendParams &p, cudaStream_t stream);
+
+// Page bookkeeping: the listing of unused pages (pages non-null) or the compaction plan.
+struct PagesParams {
+    const int *block_table, *seq_lens;
+    int *pages;                      // free list [num_pages], or null
+    int *new_table, *src, *dst;      // compaction: [B][max_pages], [cap], [cap]
+    int *counts;                     // free: [1]; compaction: [2]
+    int B, max_pages, page_size, num_pages, cap;
+    int *status;
+};
+constexpr int kMaxPlanPages = 1 << 22;
+int launch_pages(const PagesParams &p, cudaStream_t stream);
+
+struct ForkParams {
+    const int *block_table, *seq_lens, *parents, *fresh;
+    int *rows, *lens, *src, *dst;
+    int B, n, max_pages, page_size, num_pages;
+    int *status;
+};
+int launch_fork(const ForkParams &p, cudaStream_t stream);
+
+struct CopyParams {
+    void *cache[FA_MAX_COPY_CACHES];
+    unsigned long long page_bytes[FA_MAX_COPY_CACHES];
+    int first_unit[FA_MAX_COPY_CACHES + 1];  // copy units of one pair before cache c
+    int n_caches, num_pages, n_pairs;
+    const int *src, *dst, *count;
+    int *status;
+    int num_sms;
+};
+int launch_copy(CopyParams &p, cudaStream_t stream);  // fills first_unit
+
+// Attention over the paged e4m3 cache.
+struct Decode8Params {
+    const void *q;                   // bf16 [B][H][Nq][d]
+    const uint8_t *k, *v;            // e4m3 [num_pages][Hkv][page_size][d]
+    const float *k_scale, *v_scale;  // [num_pages][Hkv][page_size / group]
+    const int *block_table, *seq_lens;
+    void *o;                         // bf16 [B][H][Nq][d]
+    float *lse;                      // [B][H][Nq]
+    int B, H, Hkv, Nq, d, page_size, max_pages, num_pages, group, causal;
+    float scale_log2;
+    int *status;
+    int num_sms;
+};
+int launch_decode8(const Decode8Params &p, cudaStream_t stream);
 
 // Devices the per-device caches of the host code cover (ordinals 0..63).
 constexpr int kMaxCachedDevices = 64;

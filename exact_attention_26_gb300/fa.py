@@ -31,7 +31,9 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_status_string", "f
             "fa_decode_paged_workspace_bytes", "fa_fwd_gqa", "fa_bwd_gqa", "fa_fwd_varlen",
             "fa_bwd_varlen", "fa_quantize_fp8_workspace_bytes", "fa_quantize_fp8", "fa_fwd_fp8",
             "fa_probe_unit_rates", "fa_probe_read_bandwidth", "fa_fwd_ws", "fa_fwd_workspace_bytes",
-            "fa_fwd_split_segments")
+            "fa_fwd_split_segments", "fa_append_paged_fp8", "fa_decode_paged_fp8",
+            "fa_decode_paged_fp8_workspace_bytes", "fa_free_pages", "fa_fork_pages",
+            "fa_compact_pages", "fa_copy_pages")
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -99,6 +101,21 @@ def load() -> ctypes.CDLL:
         lib.fa_decode_paged_num_splits.restype = _int
         lib.fa_decode_paged_workspace_bytes.argtypes = [_int] * 8
         lib.fa_decode_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_append_paged_fp8.argtypes = [_vp] * 9 + [_int] * 8 + [ctypes.c_longlong] * 2 + [_vp]
+        lib.fa_append_paged_fp8.restype = _int
+        lib.fa_decode_paged_fp8_workspace_bytes.argtypes = [_int] * 7
+        lib.fa_decode_paged_fp8_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_decode_paged_fp8.argtypes = [_vp] * 9 + [_int] * 10 + [ctypes.c_float, _vp,
+                                                                    ctypes.c_size_t, _vp]
+        lib.fa_decode_paged_fp8.restype = _int
+        lib.fa_free_pages.argtypes = [_vp] * 4 + [_int] * 4 + [_vp]
+        lib.fa_free_pages.restype = _int
+        lib.fa_fork_pages.argtypes = [_vp] * 8 + [_int] * 5 + [_vp]
+        lib.fa_fork_pages.restype = _int
+        lib.fa_compact_pages.argtypes = [_vp] * 6 + [_int] * 4 + [_vp]
+        lib.fa_compact_pages.restype = _int
+        lib.fa_copy_pages.argtypes = [_vp, _vp, _int, _int, _vp, _vp, _int, _vp, _vp]
+        lib.fa_copy_pages.restype = _int
         _LIB = lib
     return _LIB
 
@@ -298,6 +315,51 @@ def fa_decode_paged_num_splits(B, H, Hkv, Nq, d, page_size, max_pages, num_split
 def fa_decode_paged_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages, num_splits=0) -> int:
     return load().fa_decode_paged_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages,
                                                   num_splits)
+
+
+def fa_append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
+                        B, T, Hkv, d, page_size, max_pages, num_pages, scale_group, k_stride,
+                        v_stride, stream) -> int:
+    return load().fa_append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                      cu_seqlens, B, T, Hkv, d, page_size, max_pages, num_pages,
+                                      scale_group, k_stride, v_stride, stream)
+
+
+def fa_decode_paged_fp8_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages) -> int:
+    return load().fa_decode_paged_fp8_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages)
+
+
+def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, B, H,
+                        Hkv, Nq, d, page_size, max_pages, num_pages, scale_group, causal, scale,
+                        workspace, workspace_bytes, stream) -> int:
+    return load().fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o,
+                                      lse, B, H, Hkv, Nq, d, page_size, max_pages, num_pages,
+                                      scale_group, int(bool(causal)), scale, workspace,
+                                      workspace_bytes, stream)
+
+
+def fa_free_pages(block_table, seq_lens, pages, count, B, max_pages, page_size, num_pages,
+                  stream) -> int:
+    return load().fa_free_pages(block_table, seq_lens, pages, count, B, max_pages, page_size,
+                                num_pages, stream)
+
+
+def fa_fork_pages(block_table, seq_lens, parents, fresh, rows, lens, src, dst, B, n, max_pages,
+                  page_size, num_pages, stream) -> int:
+    return load().fa_fork_pages(block_table, seq_lens, parents, fresh, rows, lens, src, dst, B, n,
+                                max_pages, page_size, num_pages, stream)
+
+
+def fa_compact_pages(block_table, seq_lens, new_table, src, dst, counts, B, max_pages, page_size,
+                     num_pages, stream) -> int:
+    return load().fa_compact_pages(block_table, seq_lens, new_table, src, dst, counts, B, max_pages,
+                                   page_size, num_pages, stream)
+
+
+def fa_copy_pages(caches, page_bytes, n_caches, num_pages, src, dst, n_pairs, count, stream) -> int:
+    """Raw call; `caches` and `page_bytes` are ctypes arrays of void* and size_t (host)."""
+    return load().fa_copy_pages(caches, page_bytes, n_caches, num_pages, src, dst, n_pairs, count,
+                                stream)
 
 
 def fa_status_string(status: int) -> str:
@@ -661,3 +723,214 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_fp8")
     return out, lse
+
+
+def _cache8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, di):
+    """Checks of a paged e4m3 cache and its table on device `di`; returns (B, num_pages, Hkv,
+    page_size, d, max_pages, scale_group)."""
+    _check("k_cache", k_cache, torch.uint8, dev=di)
+    if k_cache.dim() != 4 or 0 in k_cache.shape:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page_size, d = k_cache.shape
+    _check("v_cache", v_cache, torch.uint8, k_cache.shape, dev=di)
+    _check("k_scale", k_scale, torch.float32, dev=di)
+    groups = k_scale.shape[2] if k_scale.dim() == 3 else 0
+    if groups < 1 or page_size % groups or k_scale.shape[:2] != k_cache.shape[:2]:
+        raise ValueError("k_scale must be [num_pages, Hkv, page_size / group]")
+    _check("v_scale", v_scale, torch.float32, k_scale.shape, dev=di)
+    _check("block_table", block_table, torch.int32, dev=di)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _check("seq_lens", seq_lens, torch.int32, (B,), dev=di)
+    return B, num_pages, Hkv, page_size, d, max_pages, page_size // groups
+
+
+def _check_rows(name, t, dtype, shape, di):
+    """A CUDA tensor [T, Hkv, d] whose rows of Hkv * d elements are contiguous, at any stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != di:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{di}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1:] != shape or t.shape[0] < 1:
+        raise ValueError(f"{name} must be [T, {shape[0]}, {shape[1]}], T >= 1")
+    if t.stride(2) != 1 or (t.stride(1) != shape[1] and shape[0] > 1):
+        raise ValueError(f"{name}'s rows [Hkv, d] must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), shape[0] * shape[1])
+
+
+def append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                     cu_seqlens=None, stream=None):
+    """Store new tokens in a paged e4m3 cache, behind the seq_lens[b] tokens that sequence b
+    holds: k, v bf16 CUDA [T, Hkv, d] (rows contiguous, any row stride that is a multiple of
+    8), rows cu_seqlens[b] .. cu_seqlens[b+1]-1 belonging to sequence b (int32 [B+1]; None:
+    one new token each).  The cache is uint8 codes [num_pages, Hkv, page_size, d] and fp32
+    scales [num_pages, Hkv, page_size / group] for k and for v, changed in place; seq_lens is
+    not changed.  Returns None."""
+    di = k_cache.get_device() if isinstance(k_cache, torch.Tensor) else -1
+    B, num_pages, Hkv, page_size, d, max_pages, group = _cache8(k_cache, v_cache, k_scale, v_scale,
+                                                                block_table, seq_lens, di)
+    ks = _check_rows("k", k, torch.bfloat16, (Hkv, d), di)
+    vs = _check_rows("v", v, torch.bfloat16, (Hkv, d), di)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of rows")
+    cu = None
+    if cu_seqlens is not None:
+        _check("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev=di)
+        cu = cu_seqlens.data_ptr()
+    elif T != B:
+        raise ValueError("without cu_seqlens, k and v hold one row per sequence")
+    with _device(di):
+        rc = fa_append_paged_fp8(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                 k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                                 seq_lens.data_ptr(), cu, B, T, Hkv, d, page_size, max_pages,
+                                 num_pages, group, ks, vs, _stream(k, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_append_paged_fp8")
+
+
+def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, causal=False,
+                     scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Decode against a paged e4m3 cache: q bf16 CUDA [B,H,Nq,d]; k_cache, v_cache uint8 codes
+    [num_pages, Hkv, page_size, d] (Hkv divides H) with scales fp32 [num_pages, Hkv, page_size /
+    group]; block_table int32 [B, max_pages]; seq_lens int32 [B], 0 allowed.  causal: the Nq
+    queries are the sequence's last tokens, each sees the keys up to its own.  Rows that see
+    no key get o = 0 and lse = -inf.  Returns (o, lse)."""
+    _check("q", q, torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, Nq, d]")
+    B, H, Nq, d = q.shape
+    di = q.get_device()
+    B2, num_pages, Hkv, page_size, d2, max_pages, group = _cache8(k_cache, v_cache, k_scale, v_scale,
+                                                                  block_table, seq_lens, di)
+    if B2 != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    if d2 != d or H % Hkv:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d], Hkv dividing H")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check("out", out, torch.bfloat16, q.shape, dev=di)
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    else:
+        _check("lse", lse, torch.float32, (B, H, Nq), dev=di)
+    with _device(di):
+        need = _memo(fa_decode_paged_fp8_workspace_bytes, B, H, Hkv, Nq, d, page_size, max_pages)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _check("workspace", workspace, torch.uint8, dev=di)
+        rc = fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                 k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                                 seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
+                                 d, page_size, max_pages, num_pages, group, causal, scale,
+                                 workspace.data_ptr(), workspace.numel(), _stream(q, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_decode_paged_fp8")
+    return out, lse
+
+
+def _table(block_table, seq_lens):
+    _check("block_table", block_table, torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _check("seq_lens", seq_lens, torch.int32, block_table.shape[:1], dev=block_table.get_device())
+    return block_table.get_device(), *block_table.shape
+
+
+def _int32(shape, like):
+    return torch.empty(shape, dtype=torch.int32, device=like.device)
+
+
+def free_pages(block_table, seq_lens, page_size, num_pages, stream=None):
+    """The pages of a paged cache that no sequence uses: (pages int32 [num_pages], ascending,
+    then -1; count int32 [1])."""
+    di, B, max_pages = _table(block_table, seq_lens)
+    pages, count = _int32(max(int(num_pages), 0), block_table), _int32(1, block_table)
+    with _device(di):
+        rc = fa_free_pages(block_table.data_ptr(), seq_lens.data_ptr(), pages.data_ptr(),
+                           count.data_ptr(), B, max_pages, int(page_size), int(num_pages),
+                           _stream(block_table, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_free_pages")
+    return pages, count
+
+
+def fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages, stream=None):
+    """Children of the sequences `parents` (int32 [n], rows of block_table): they share the
+    parents' full pages, and child i takes page fresh[i] (int32 [n]) for a copy of a last page
+    that is not full.  Returns (rows int32 [n, max_pages], lens [n], src [n], dst [n]): the
+    children's table rows and lengths, and the pages to pass to copy_pages (-1: none)."""
+    di, B, max_pages = _table(block_table, seq_lens)
+    _check("parents", parents, torch.int32, dev=di)
+    if parents.dim() != 1:
+        raise ValueError("parents must be [n]")
+    _check("fresh", fresh, torch.int32, parents.shape, dev=di)
+    n = parents.shape[0]
+    rows, lens, src, dst = (_int32(s, block_table) for s in ((n, max_pages), n, n, n))
+    with _device(di):
+        rc = fa_fork_pages(block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
+                           fresh.data_ptr(), rows.data_ptr(), lens.data_ptr(), src.data_ptr(),
+                           dst.data_ptr(), B, n, max_pages, int(page_size), int(num_pages),
+                           _stream(block_table, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fork_pages")
+    return rows, lens, src, dst
+
+
+def compact_pages(block_table, seq_lens, page_size, num_pages, stream=None):
+    """Plan that packs the n pages in use into pages 0 .. n-1: (table int32 [B, max_pages] after
+    the moves, src, dst int32 [max(1, num_pages // 2)] ending in -1, counts int32 [2] = n and
+    the number of moves).  copy_pages(caches, src, dst, count=counts[1:]) makes the moves."""
+    di, B, max_pages = _table(block_table, seq_lens)
+    cap = max(1, int(num_pages) // 2)
+    table, src, dst, counts = (_int32(s, block_table) for s in ((B, max_pages), cap, cap, 2))
+    with _device(di):
+        rc = fa_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), table.data_ptr(),
+                              src.data_ptr(), dst.data_ptr(), counts.data_ptr(), B, max_pages,
+                              int(page_size), int(num_pages), _stream(block_table, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_compact_pages")
+    return table, src, dst, counts
+
+
+FA_MAX_COPY_CACHES = 128
+
+
+def copy_pages(caches, src, dst, count=None, stream=None):
+    """Copy page src[i] of every tensor of `caches` (contiguous CUDA tensors, their first
+    dimension num_pages: codes and scales, any number of layers up to 128 tensors) onto its page
+    dst[i], for every pair of int32 [n] src, dst with src[i] != -1; with `count` (int32 [1]) only
+    the first count pairs.  No page may be a destination twice, or destination and source."""
+    caches = list(caches)
+    if not 1 <= len(caches) <= FA_MAX_COPY_CACHES:
+        raise ValueError(f"caches must be 1 to {FA_MAX_COPY_CACHES} tensors")
+    di = src.get_device() if isinstance(src, torch.Tensor) else -1
+    _check("src", src, torch.int32)
+    if src.dim() != 1:
+        raise ValueError("src must be [n]")
+    _check("dst", dst, torch.int32, src.shape, dev=di)
+    if count is not None:
+        _check("count", count, torch.int32, (1,), dev=di)
+    num_pages = caches[0].shape[0] if isinstance(caches[0], torch.Tensor) and caches[0].dim() else 0
+    ptrs = (_vp * len(caches))()
+    sizes = (ctypes.c_size_t * len(caches))()
+    for i, t in enumerate(caches):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"caches[{i}] must be a CUDA tensor")
+        _check(f"caches[{i}]", t, t.dtype, dev=di)
+        if t.dim() < 2 or t.shape[0] != num_pages or not t.numel():
+            raise ValueError(f"caches[{i}] must be [num_pages, ...] like the first")
+        ptrs[i] = t.data_ptr()
+        sizes[i] = t.numel() // num_pages * t.element_size()
+    with _device(di):
+        rc = fa_copy_pages(ptrs, sizes, len(caches), num_pages, src.data_ptr(), dst.data_ptr(),
+                           src.shape[0], None if count is None else count.data_ptr(),
+                           _stream(src, stream))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_copy_pages")

@@ -47,14 +47,14 @@ extern "C" {
 typedef enum {
     FA_OK = 0,
     FA_ERR_INVALID_ARG = 1, /* null pointer, non-positive size, bad scale, ... */
-    FA_ERR_UNSUPPORTED = 2, /* head dimension not built */
+    FA_ERR_UNSUPPORTED = 2, /* head dimension not built, or a size beyond a stated limit */
     FA_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
     FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed */
     FA_ERR_TIMEOUT = 5,     /* a bounded in-kernel wait ran out (device status) */
     FA_ERR_WORKSPACE = 6,   /* workspace missing or smaller than required */
-    FA_ERR_BAD_INDEX = 7    /* device status: a block-table entry, sequence length or
-                               cu_seqlens offset out of range (paged decode, packed
-                               sequences); the affected work wrote nothing */
+    FA_ERR_BAD_INDEX = 7    /* device status: a block-table entry, page number, sequence
+                               length or cu_seqlens offset out of range (paged caches,
+                               packed sequences); the affected work wrote nothing */
 } fa_status;
 
 /*
@@ -380,6 +380,130 @@ int fa_decode_paged_num_splits(int B, int H, int Hkv, int Nq, int d, int page_si
 /* Workspace bytes fa_decode_paged needs (0 when one range suffices or sizes are invalid). */
 size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int page_size,
                                        int max_pages_per_seq, int num_splits);
+
+/*
+ * A paged key/value cache in e4m3 (8 bits per element, half the bytes a decode step
+ * streams from a bf16 cache).  The layout is fa_decode_paged's with codes for values
+ * and a scale for every group of scale_group consecutive tokens of a page and head:
+ *   k_cache, v_cache : uint8 e4m3 [num_pages][Hkv][page_size][d].
+ *   k_scale, v_scale : fp32 [num_pages][Hkv][page_size / scale_group]; the value of a
+ *                      code is value(code) * scale of its group.  Scales are finite and
+ *                      >= 0.
+ *   block_table      : int32 [B][max_pages_per_seq]; seq_lens int32 [B] (device memory).
+ *   d                : 64, 96, 128 or 256 (FA_ERR_UNSUPPORTED otherwise).
+ *   scale_group      : divides page_size; page_size * max_pages_per_seq < 2^31,
+ *                      num_pages * Hkv < 2^31.
+ * e4m3 is the OCP format (no infinities, one NaN code per sign, largest value 448).
+ *
+ * fa_append_paged_fp8 stores new tokens behind the cached ones.  Sequence b's new tokens
+ * are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of k and v; row cu_seqlens[b] + i becomes
+ * its token seq_lens[b] + i (seq_lens counts the tokens cached BEFORE the call and is not
+ * changed).  Per group and head that gets new tokens:
+ *   least = the smallest power of two s >= 2^-126 with |x| <= 448 s for the group's finite
+ *           new elements x;
+ *   scale = least in a group that held no token, else max(least, its scale so far), and
+ *           where that is larger than before, the codes that were there are rounded again,
+ *           e4m3(value(code) * old / new);
+ *   code  = e4m3(x / scale), to nearest even; a NaN or infinite x is stored as NaN and has
+ *           no part in the scale.
+ * Powers of two make x / scale exact and leave the second rounding exact too for every
+ * code that stays normal.  Rows of the cache that are not new tokens of the call (other
+ * pages, rows behind the last token) keep their bytes.
+ *   k, v       : bf16, element [t][h][c] at t * stride + h * d + c: k_stride, v_stride in
+ *                elements, >= Hkv * d and multiples of 8 (slices of a fused projection
+ *                are read in place); T rows.
+ *   cu_seqlens : int32 [B+1], 0 <= cu[b] <= cu[b+1] <= T, device memory; NULL means one
+ *                new token each (T = B).  Rows from cu[B] on belong to no sequence.
+ *   scale_group: at most 128 here.
+ * Two sequences of a call must not append to one page (copy a shared page first:
+ * fa_fork_pages).  A sequence with a bad offset or length, and a group whose page is out
+ * of range, is skipped and recorded as FA_ERR_BAD_INDEX (fa_device_status).
+ */
+int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cache,
+                        float *k_scale, float *v_scale, const int *block_table,
+                        const int *seq_lens, const int *cu_seqlens, int B, int T, int Hkv, int d,
+                        int page_size, int max_pages_per_seq, int num_pages, int scale_group,
+                        long long k_stride, long long v_stride, void *stream);
+
+/*
+ * Decode against the e4m3 cache above: fa_decode_paged's operation on the dequantised keys
+ * and values (fp32 accumulation, no 16-bit copy of the cache is made),
+ *     O[i] = softmax(q_i K^T * scale) V,   L[i] = m_i + ln(l_i)   (natural log).
+ *   q      : bf16 [B][H][Nq][d];  o : bf16 [B][H][Nq][d];  lse : fp32 [B][H][Nq].
+ *   seq_lens : 0 <= seq_lens[b] <= page_size * max_pages_per_seq cached tokens.
+ *   causal : 0: every query sees every cached key of its sequence.  Nonzero: the Nq
+ *            queries are the sequence's last tokens (their keys are in the cache), query i
+ *            sees keys 0 .. seq_lens[b] - Nq + i.
+ * A row that sees no key (an empty sequence, or a causal query before its first token)
+ * gets O = 0 and L = -infinity.  Keys a row does not see have no influence on it, whatever
+ * their codes are, with one exception: among the last Nq keys of a causal call, a NaN code
+ * of V reaches also the rows that do not see it.  A NaN or infinity in a query makes its row NaN.
+ * Rounding: q's 8 significant bits are kept, probabilities enter the product with V with a
+ * relative error of at most 2^-9 (absolute 2^-23 of the row's largest), sums are fp32.
+ *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31.
+ *   scale  : finite and > 0.
+ *   workspace : device buffer of fa_decode_paged_fp8_workspace_bytes(...) bytes, 16-byte
+ *            aligned, contents on entry irrelevant; calls that share one must not overlap.
+ * The work is cut evenly over the SMs on the device, from seq_lens: a captured call replays
+ * with other lengths.  A sequence with a bad length or page writes nothing and is recorded
+ * as FA_ERR_BAD_INDEX.
+ */
+size_t fa_decode_paged_fp8_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int page_size,
+                                           int max_pages_per_seq);
+int fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale, const int *block_table,
+                        const int *seq_lens, void *o, float *lse, int B, int H, int Hkv, int Nq,
+                        int d, int page_size, int max_pages_per_seq, int num_pages,
+                        int scale_group, int causal, float scale, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * Upkeep of the pages of a paged cache (bf16 or e4m3).  A page is in use when it stands
+ * among the first ceil(seq_lens[b] / page_size) entries of some sequence's table row; a
+ * sequence is released by setting its length to 0, and pages may be shared.  All arguments
+ * are int32 device memory; nothing is read back to the host, so the calls can be captured.
+ * Lengths below 0 count as 0 and above the row's room as all of it, entries out of range are
+ * passed over, each recorded as FA_ERR_BAD_INDEX.  num_pages <= 2^22 (FA_ERR_UNSUPPORTED).
+ *
+ * fa_free_pages lists the pages no sequence uses: pages [num_pages] gets them in ascending
+ * order, then -1; count [1] their number.
+ *
+ * fa_fork_pages lets n new sequences continue from copies of sequences parents[i] (rows of
+ * the table, the same one any number of times): rows [n][max_pages_per_seq] and lens [n]
+ * are the children's, sharing the parent's full pages; a last page that is not full is
+ * replaced by page fresh[i] and appears as the pair src[i] = parent's page, dst[i] =
+ * fresh[i], else src[i] = dst[i] = -1.  Row entries behind the last page are -1.  Pass the
+ * pairs to fa_copy_pages before anything is appended.
+ *
+ * fa_compact_pages packs the n pages in use into pages 0 .. n-1: the k-th page in use at or
+ * above n (ascending) moves to the k-th unused page below n.  src, dst [max(1, num_pages /
+ * 2)] get the moves, then -1; counts [2] = n and the number of moves; new_table
+ * [B][max_pages_per_seq] the table after the moves (entries not in use as they were).
+ * No page is both a source and a destination, so fa_copy_pages does the moves in any order.
+ */
+int fa_free_pages(const int *block_table, const int *seq_lens, int *pages, int *count, int B,
+                  int max_pages_per_seq, int page_size, int num_pages, void *stream);
+int fa_fork_pages(const int *block_table, const int *seq_lens, const int *parents,
+                  const int *fresh, int *rows, int *lens, int *src, int *dst, int B, int n,
+                  int max_pages_per_seq, int page_size, int num_pages, void *stream);
+int fa_compact_pages(const int *block_table, const int *seq_lens, int *new_table, int *src,
+                     int *dst, int *counts, int B, int max_pages_per_seq, int page_size,
+                     int num_pages, void *stream);
+
+/*
+ * Copies whole pages within each of n_caches buffers (all layers' codes and scales in one
+ * launch): for every pair i, page src[i] of each buffer onto its page dst[i].
+ *   caches     : HOST array of n_caches device pointers (1 .. FA_MAX_COPY_CACHES), buffer c
+ *                holding num_pages pages of page_bytes[c] >= 1 bytes (host array), any
+ *                alignment (16-byte aligned pages are copied fastest).
+ *   src, dst   : int32 [n_pairs], device memory; a pair with src[i] = -1 is passed over.
+ *                No page may be a destination twice, or a destination and a source.
+ *   count      : NULL, or device int32 [1]: only the first min(*count, n_pairs) pairs.
+ * Pages out of range are skipped and recorded as FA_ERR_BAD_INDEX.
+ */
+#define FA_MAX_COPY_CACHES 128
+int fa_copy_pages(void *const *caches, const size_t *page_bytes, int n_caches, int num_pages,
+                  const int *src, const int *dst, int n_pairs, const int *count, void *stream);
 
 /*
  * Diagnostic: launches one warp that waits, through the same bounded wait the

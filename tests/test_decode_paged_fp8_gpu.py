@@ -1,0 +1,316 @@
+"""Decode against the paged e4m3 cache (fa_decode_paged_fp8) against the float64 oracle, at
+every head dimension, head grouping, page and scale-group size, and at the lengths and masks
+where it can go wrong; what lies behind a sequence's last token is NaN in every test."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from cache_common import DEV, check_decode, make_cache, make_table, oracle_decode
+from gpu_common import load_fa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    return load_fa()
+
+
+def _problem(B, H, Hkv, Nq, d, ps, group, lens, seed=0, spread=1.0, extra=2, qmul=1.0):
+    """(q, kc, vc, ks, vs, table, lens) on the CPU; rows behind the last token and whole unused
+    pages hold NaN codes, their scales are NaN too, unused table entries point nowhere."""
+    num = sum(-(-n // ps) for n in lens) + extra
+    width = max(1, max(-(-n // ps) for n in lens)) + 1
+    table = make_table(lens, ps, width, num, seed, unused=1 << 30)
+    kc, ks = make_cache(num, Hkv, ps, d, group, seed + 1, spread)
+    vc, vs = make_cache(num, Hkv, ps, d, group, seed + 2, spread)
+    unused = torch.ones((num, ps), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // ps)):
+            unused[table[b, j], :max(0, n - j * ps)] = False
+    for codes, scale in ((kc, ks), (vc, vs)):
+        codes.permute(0, 2, 1, 3)[unused] = 0x7F
+        whole = unused.reshape(num, ps // group, group).all(-1)
+        scale.permute(0, 2, 1)[whole] = float("nan")
+    g = torch.Generator().manual_seed(seed + 3)
+    q = (qmul * torch.randn((B, H, Nq, d), generator=g)).to(torch.bfloat16)
+    return q, kc, vc, ks, vs, table, torch.tensor(lens, dtype=torch.int32)
+
+
+def _check(fa, prob, causal=False, scale=None, what="", **kw):
+    dev = [t.to(DEV) for t in prob]
+    o, lse = fa.decode_paged_fp8(*dev, causal=causal, scale=scale, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == 0
+    ref = oracle_decode(*prob, causal, scale or 1 / math.sqrt(prob[0].shape[3]))
+    check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), ref, what)
+    return o, lse
+
+
+LENS = [0, 1, 2, 15, 16, 17, 127, 128, 129, 255, 256, 257, 300, 500]
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 3), (8, 2), (7, 1)])
+def test_lengths_and_heads(fa, d, H, Hkv):
+    _check(fa, _problem(len(LENS), H, Hkv, 1, d, 16, 16, LENS, seed=d + H))
+
+
+@pytest.mark.parametrize("ps,group", [(1, 1), (2, 1), (5, 5), (8, 4), (24, 8), (48, 16), (64, 64), (100, 25),
+                                      (128, 32), (192, 64), (256, 128), (512, 512)])
+def test_page_and_group_sizes(fa, ps, group):
+    _check(fa, _problem(5, 4, 2, 1, 128, ps, group, [1, 130, 257, 700, 1025], seed=ps))
+    _check(fa, _problem(3, 4, 1, 2, 64, ps, group, [0, 97, 600], seed=ps + 1), causal=True)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("H,Hkv,Nq", [(2, 2, 2), (4, 1, 2), (8, 1, 1), (9, 1, 1), (4, 2, 4), (8, 2, 4),
+                                      (17, 1, 1), (16, 1, 2), (33, 1, 1), (8, 1, 8), (5, 1, 13), (16, 2, 16),
+                                      (64, 1, 3), (2, 1, 70)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_rows_per_head(fa, d, H, Hkv, Nq, causal):
+    _check(fa, _problem(4, H, Hkv, Nq, d, 32, 16, [0, Nq - 1, 150, 411], seed=d + H + Nq), causal=causal,
+           what=f"{d} {H} {Hkv} {Nq}")
+
+
+def test_causal_rows_before_the_first_token(fa):
+    prob = _problem(5, 4, 2, 6, 128, 16, 16, [0, 1, 4, 6, 131], seed=3)
+    o, lse = _check(fa, prob, causal=True)
+    assert np.isneginf(lse[1, :, :5].cpu().numpy()).all() and bool(torch.isfinite(lse[1, :, 5]).all())
+
+
+@pytest.mark.parametrize("B,H,Hkv,Nq,d,lens", [
+    (1, 8, 8, 1, 128, [20000]), (1, 4, 1, 1, 64, [33333]), (2, 16, 2, 2, 128, [9000, 12345]),
+    (3, 4, 4, 1, 256, [7000, 1, 5000]), (1, 2, 2, 3, 96, [15001])])
+def test_long_sequences_are_cut_and_merged(fa, B, H, Hkv, Nq, d, lens):
+    _check(fa, _problem(B, H, Hkv, Nq, d, 64, 32, lens, seed=d), causal=Nq > 1)
+
+
+def test_many_sequences(fa):
+    lens = [(b * 131) % 300 for b in range(400)]
+    _check(fa, _problem(400, 2, 1, 1, 64, 16, 16, lens, seed=1))
+
+
+def test_all_sequences_empty(fa):
+    o, lse = _check(fa, _problem(3, 4, 2, 1, 128, 16, 16, [0, 0, 0]))
+    assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("scale,qmul", [(1.5, 1.0), (1e-4, 1.0), (0.088, 30.0), (0.088, 1e-3)])
+def test_scales_of_the_scores(fa, scale, qmul):
+    _check(fa, _problem(2, 4, 2, 1, 128, 16, 16, [700, 300], seed=5, qmul=qmul), scale=scale)
+
+
+def test_queries_over_many_binades(fa):
+    """q elements far below the row's largest keep their place in the scores."""
+    prob = list(_problem(2, 4, 2, 2, 128, 16, 16, [400, 129], seed=6))
+    prob[0] = prob[0] * torch.exp2(-torch.arange(128) / 8).to(torch.bfloat16)
+    _check(fa, prob, scale=0.3)
+
+
+def test_a_sink_token_and_many_small_weights(fa):
+    """One key takes nearly all of the weight and has a small value; thousands of weights near
+    2^-12 of the largest make up the rest of the output."""
+    prob = list(_problem(1, 2, 1, 1, 128, 16, 16, [6000], seed=7, spread=0.0))
+    q, kc, vc, ks, vs, table, lens = prob
+    page = int(table[0, 0])
+    kc[page, 0, 0] = torch.where(q[0, 0, 0].float() > 0, 0x70, 0xF0).to(torch.uint8)
+    q[0, 1] = q[0, 0]
+    vs[page] *= 2.0 ** -8
+    _check(fa, prob, scale=0.02)
+    _check(fa, prob, scale=0.05)
+
+
+def test_value_scales_over_many_binades(fa):
+    _check(fa, _problem(2, 4, 2, 1, 128, 16, 8, [900, 333], seed=8, spread=3.0))
+
+
+def test_groups_of_zero_scale(fa):
+    prob = _problem(2, 4, 2, 1, 128, 16, 16, [300, 140], seed=9)
+    for b, n in ((0, 300), (1, 140)):
+        prob[3][prob[5][b, 1].long()] = 0.0
+        prob[4][prob[5][b, 2].long()] = 0.0
+        prob[4][prob[5][b, 0].long()] = 2.0 ** -126
+    _check(fa, prob)
+    prob[4][:] = 0.0  # every value is zero
+    o, _ = _check(fa, prob)
+    assert bool((o == 0).all())
+
+
+def test_nan_and_infinities_stay_in_their_rows(fa):
+    prob = list(_problem(3, 4, 2, 1, 128, 16, 16, [200, 300, 20], seed=10))
+    prob[0][0, 1, 0, 5] = float("nan")
+    prob[0][1, 2, 0, 7] = float("inf")
+    prob[1][int(prob[5][2, 0]), 1, 3, 9] = 0x7F  # a NaN key: heads 2 and 3 of sequence 2
+    prob[2][int(prob[5][1, 3]), 0, 2, 11] = 0xFF  # a NaN value: column 11, heads 0 and 1 of sequence 1
+    o, lse = fa.decode_paged_fp8(*[t.to(DEV) for t in prob])
+    o, lse = o.float().cpu(), lse.cpu()
+    nan = torch.zeros((3, 4), dtype=torch.bool)
+    nan[0, 1] = nan[1, 2] = nan[2, 2] = nan[2, 3] = True
+    assert torch.equal(torch.isnan(lse[:, :, 0]), nan)
+    expect = nan[:, :, None, None].expand_as(o).clone()
+    expect[1, :2, 0, 11] = True
+    assert torch.equal(torch.isnan(o), expect)
+    assert fa.fa_device_status(None) == 0
+
+
+def test_shared_pages_and_repeated_entries(fa):
+    prob = list(_problem(4, 4, 2, 1, 128, 16, 16, [100, 160, 33, 64], seed=11))
+    prob[5][1, :6] = prob[5][0, :6]
+    prob[5][3, :4] = prob[5][3, 0]
+    _check(fa, prob)
+
+
+def test_outputs_workspace_and_stream_given(fa):
+    prob = _problem(3, 8, 2, 1, 128, 16, 16, [4000, 100, 0], seed=12)
+    need = fa.fa_decode_paged_fp8_workspace_bytes(3, 8, 2, 1, 128, 16, prob[5].shape[1])
+    out = torch.full((3, 8, 1, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((3, 8, 1), float("nan"), device=DEV)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o, _ = _check(fa, prob, out=out, lse=lse, workspace=ws[:need], stream=s)
+    assert o is out and bool((ws[need:] == 0xFF).all())
+    again, _ = fa.decode_paged_fp8(*[t.to(DEV) for t in prob])
+    assert torch.equal(again, out)  # the same bits each time
+    with pytest.raises(fa.FaError):
+        fa.decode_paged_fp8(*[t.to(DEV) for t in prob], workspace=ws[:need - 1])
+
+
+def test_two_calls_at_once(fa):
+    probs = [_problem(2, 8, 8, 1, 128, 16, 16, [5000, 3000], seed=s) for s in (13, 14)]
+    dev = [[t.to(DEV) for t in p] for p in probs]
+    alone = [fa.decode_paged_fp8(*d) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    for _ in range(20):
+        both = []
+        for d, s in zip(dev, streams):
+            with torch.cuda.stream(s):
+                both.append(fa.decode_paged_fp8(*d))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_calls_follow_the_lengths(fa):
+    prob = _problem(4, 8, 2, 2, 128, 16, 16, [3000, 1000, 500, 64], seed=15)
+    dev = [t.to(DEV) for t in prob]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = fa.decode_paged_fp8(*dev, causal=True)
+    for lens in ([3000, 1000, 500, 64], [1, 0, 500, 63], [2999, 1, 2, 1], [0, 0, 0, 0], [7, 998, 129, 64]):
+        dev[6].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = oracle_decode(*prob[:6], torch.tensor(lens), True, 128 ** -0.5)
+        check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), ref, str(lens))
+    assert fa.fa_device_status(None) == 0
+
+
+@pytest.mark.parametrize("entry,length", [(-1, None), (1 << 30, None), (None, -1), (None, 100000)])
+def test_bad_index_is_reported_and_writes_nothing(fa, entry, length):
+    prob = _problem(3, 4, 2, 1, 128, 16, 16, [2000, 2500, 700], seed=16)
+    dev = [t.to(DEV) for t in prob]
+    if entry is not None:
+        dev[5][1, 100] = entry
+    else:
+        dev[6][1] = length
+    out = torch.full((3, 4, 1, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((3, 4, 1), 3.0, device=DEV)
+    fa.decode_paged_fp8(*dev, out=out, lse=lse)
+    assert fa.fa_device_status(None) == 7
+    assert bool((out[1] == 3.0).all()) and bool((lse[1] == 3.0).all())
+    ref = oracle_decode(*prob, False, 128 ** -0.5)
+    ok = [0, 2]
+    check_decode(out[ok].float().cpu().numpy(), lse[ok].cpu().numpy(),
+                 (ref[0][ok], ref[1][ok], tuple(x[ok] for x in ref[2])))
+
+
+def test_pages_beyond_four_gigabytes(fa):
+    """Pages whose bytes lie past 2^32 of the cache."""
+    Hkv, ps, d, group = 8, 128, 128, 128
+    num = (1 << 32) // (Hkv * ps * d) + 50
+    prob = list(_problem(2, 8, 8, 1, d, ps, group, [700, 1000], seed=17))
+    used = prob[1].shape[0]
+    big = []
+    for codes, scale in ((prob[1], prob[3]), (prob[2], prob[4])):
+        c = torch.empty((num, Hkv, ps, d), dtype=torch.uint8, device=DEV)
+        s = torch.zeros((num, Hkv, 1), device=DEV)
+        c[num - used:], s[num - used:] = codes.to(DEV), scale.to(DEV)
+        big.append((c, s))
+    table = torch.where(prob[5] < used, prob[5] + (num - used), prob[5])
+    o, lse = fa.decode_paged_fp8(prob[0].to(DEV), big[0][0], big[1][0], big[0][1], big[1][1],
+                                 table.to(DEV), prob[6].to(DEV))
+    assert fa.fa_device_status(None) == 0
+    check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), oracle_decode(*prob, False, d ** -0.5))
+
+
+def test_a_serving_loop(fa):
+    """Prefill, decode steps, a fork, more steps, a release with compaction, more steps: the
+    cache as the oracle keeps it, and attention over it, at every step."""
+    from oracle import cache as oc
+    H, Hkv, d, ps, group, num, width, layers = 4, 2, 128, 16, 8, 60, 12, 1
+    g = torch.Generator().manual_seed(20)
+    kc, ks = (t.to(DEV) for t in make_cache(num, Hkv, ps, d, group, 1, pow2=True))
+    vc, vs = (t.to(DEV) for t in make_cache(num, Hkv, ps, d, group, 2, pow2=True))
+    ref = [t.cpu().numpy() for t in (kc, ks, vc, vs)]
+    B = 4  # rows 2 and 3 begin empty
+    lens = np.array([37, 16, 0, 0])
+    table = np.full((B, width), -1)
+    table[0, :5], table[1, :5] = [50, 3, 44, 7, 30], [1, 59, 20, 21, 22]
+    dlens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    dtable = torch.as_tensor(table, dtype=torch.int32, device=DEV)
+
+    def step(counts):
+        cu = np.concatenate(([0], np.cumsum(counts)))
+        x = torch.randn((max(1, int(cu[-1])), 2 * Hkv, d), generator=g).to(torch.bfloat16)
+        xd = x.to(DEV)
+        fa.append_paged_fp8(xd[:, :Hkv], xd[:, Hkv:], kc, vc, ks, vs, dtable, dlens,
+                            cu_seqlens=torch.as_tensor(cu, dtype=torch.int32, device=DEV))
+        old = dlens.cpu().numpy()
+        for i in range(2):
+            ref[2 * i], ref[2 * i + 1] = oc.append(x[:, i * Hkv:(i + 1) * Hkv].double().numpy(), ref[2 * i],
+                                                   ref[2 * i + 1], dtable.cpu().numpy(), old, cu)
+        dlens.add_(torch.as_tensor(counts, dtype=torch.int32, device=DEV))
+        for t, r in zip((kc, ks, vc, vs), ref):
+            assert np.array_equal(t.cpu().numpy(), r)
+        q = torch.randn((B, H, 1, d), generator=g).to(torch.bfloat16)
+        o, lse = fa.decode_paged_fp8(q.to(DEV), kc, vc, ks, vs, dtable, dlens)
+        check_decode(o.float().cpu().numpy(), lse.cpu().numpy(),
+                     oc.decode(q.double().numpy(), ref[0], ref[2], ref[1], ref[3], dtable.cpu().numpy(),
+                               dlens.cpu().numpy(), False, d ** -0.5))
+
+    step(lens)
+    for _ in range(3):
+        step(np.array([1, 1, 0, 0]))
+    free, count = fa.free_pages(dtable, dlens, ps, num)
+    parents = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    rows, clens, src, dst = fa.fork_pages(dtable, dlens, parents, free[30:32], ps, num)
+    fa.copy_pages([kc, ks, vc, vs], src, dst)
+    dtable[2:], dlens[2:] = rows, clens
+    dtable[2, 3:5], dtable[3, 2:5] = free[32:34], free[34:37]  # room to grow
+    for s_, d_ in zip(src.tolist(), dst.tolist()):
+        if s_ >= 0:
+            for r in ref:
+                r[d_] = r[s_]
+    for n in ([1, 1, 1, 1], [3, 0, 2, 9], [1, 1, 1, 1]):
+        step(np.array(n))
+    dlens[1] = 0  # released
+    table2, src, dst, counts = fa.compact_pages(dtable, dlens, ps, num)
+    fa.copy_pages([kc, ks, vc, vs], src, dst, count=counts[1:])
+    for s_, d_ in zip(src.tolist(), dst.tolist()):
+        if s_ >= 0:
+            for r in ref:
+                r[d_] = r[s_]
+    dtable.copy_(table2)
+    free, _ = fa.free_pages(dtable, dlens, ps, num)
+    assert free[0].item() == counts[0].item()
+    for b in (0, 2, 3):  # the pages after the last one in use: fresh ones
+        need = -(-int(dlens[b]) // ps)
+        dtable[b, need:need + 2] = free[2 * b:2 * b + 2]
+    for n in ([1, 0, 1, 1], [20, 0, 1, 15], [1, 0, 1, 1]):
+        step(np.array(n))
+    assert fa.fa_device_status(None) == 0
