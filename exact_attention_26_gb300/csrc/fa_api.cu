@@ -916,8 +916,9 @@ int check_cache8(int B, int Hkv, int d, int page_size, int max_pages, int num_pa
     if (B < 1 || Hkv < 1 || page_size < 1 || max_pages < 1 || num_pages < 1 || scale_group < 1)
         return FA_ERR_INVALID_ARG;
     if (page_size % scale_group != 0) return FA_ERR_INVALID_ARG;
-    if ((long long)page_size * max_pages >= (1LL << 31) || (long long)B * max_pages >= (1LL << 31) ||
-        (long long)num_pages * Hkv >= (1LL << 31))
+    // the last key of a tile of 128 is an int too
+    if ((long long)page_size * max_pages > (1LL << 31) - 128 ||
+        (long long)B * max_pages >= (1LL << 31) || (long long)num_pages * Hkv >= (1LL << 31))
         return FA_ERR_INVALID_ARG;
     if (d != 64 && d != 96 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
     return FA_OK;
@@ -989,7 +990,18 @@ int check_decode8(int B, int H, int Hkv, int Nq, int d, int page_size, int max_p
 extern "C" size_t fa_decode_paged_fp8_workspace_bytes(int B, int H, int Hkv, int Nq, int d,
                                                       int page_size, int max_pages_per_seq) {
     if (check_decode8(B, H, Hkv, Nq, d, page_size, max_pages_per_seq, 1, 1) != FA_OK) return 0;
-    return 16;
+    DeviceCache *dc = nullptr;
+    if (current_device(&dc) != FA_OK) return 0;
+    Decode8Params p{};
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_sms = dc->num_sms;
+    return decode8_workspace_bytes(p);
 }
 
 extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
@@ -1004,25 +1016,22 @@ extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const voi
     int rc = check_decode8(B, H, Hkv, Nq, d, page_size, max_pages_per_seq, num_pages, scale_group);
     if (rc != FA_OK) return rc;
     if ((rc = check_scale(scale)) != FA_OK) return rc;
-    const size_t need =
-        fa_decode_paged_fp8_workspace_bytes(B, H, Hkv, Nq, d, page_size, max_pages_per_seq);
-    if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
         !aligned4(lse) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned16(workspace))
         return FA_ERR_MISALIGNED;
+    if (!workspace) return FA_ERR_WORKSPACE;
     DeviceCache *dc = nullptr;
     if ((rc = current_device(&dc)) != FA_OK) return rc;
     Decode8Params p{};
     p.q = q;
-    p.k = static_cast<const uint8_t *>(k_cache);
-    p.v = static_cast<const uint8_t *>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.o = o;
     p.lse = lse;
+    p.workspace = workspace;
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
@@ -1036,6 +1045,15 @@ extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const voi
     p.scale_log2 = scale * kLog2e;
     p.status = dc->status;
     p.num_sms = dc->num_sms;
+    if (workspace_bytes < decode8_workspace_bytes(p)) return FA_ERR_WORKSPACE;
+    // every head's rows of a page as one plane; boxes as wide as a swizzle span, columns from d
+    // on read as zeros
+    const uint64_t planes = (uint64_t)num_pages * Hkv, pitch = (uint64_t)d, plane = pitch * page_size;
+    const uint32_t box = (uint32_t)decode8_box_rows(page_size);
+    if ((rc = make_u8_map(&p.tm_k, k_cache, d, page_size, planes, pitch, plane, 128, box)) != FA_OK)
+        return rc;
+    if ((rc = make_u8_map(&p.tm_v, v_cache, d, page_size, planes, pitch, plane, 128, box)) != FA_OK)
+        return rc;
     return launch_decode8(p, static_cast<cudaStream_t>(stream));
 }
 

@@ -215,17 +215,21 @@ int launch_copy(CopyParams &p, cudaStream_t stream);  // fills first_unit
 
 // Attention over the paged e4m3 cache.
 struct Decode8Params {
+    CUtensorMap tm_k, tm_v;          // bytes (d, page_size, num_pages * Hkv), boxes of 128 x
+                                     // decode8_box_rows(page_size) x 1
     const void *q;                   // bf16 [B][H][Nq][d]
-    const uint8_t *k, *v;            // e4m3 [num_pages][Hkv][page_size][d]
     const float *k_scale, *v_scale;  // [num_pages][Hkv][page_size / group]
     const int *block_table, *seq_lens;
     void *o;                         // bf16 [B][H][Nq][d]
     float *lse;                      // [B][H][Nq]
+    void *workspace;
     int B, H, Hkv, Nq, d, page_size, max_pages, num_pages, group, causal;
     float scale_log2;
     int *status;
     int num_sms;
 };
+int decode8_box_rows(int page_size);
+size_t decode8_workspace_bytes(const Decode8Params &p);  // of its sizes and num_sms
 int launch_decode8(const Decode8Params &p, cudaStream_t stream);
 
 // Devices the per-device caches of the host code cover (ordinals 0..63).

@@ -391,8 +391,8 @@ size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int
  *                      >= 0.
  *   block_table      : int32 [B][max_pages_per_seq]; seq_lens int32 [B] (device memory).
  *   d                : 64, 96, 128 or 256 (FA_ERR_UNSUPPORTED otherwise).
- *   scale_group      : divides page_size; page_size * max_pages_per_seq < 2^31,
- *                      num_pages * Hkv < 2^31.
+ *   scale_group      : divides page_size; page_size * max_pages_per_seq <= 2^31 - 128,
+ *                      B * max_pages_per_seq and num_pages * Hkv < 2^31.
  * e4m3 is the OCP format (no infinities, one NaN code per sign, largest value 448).
  *
  * fa_append_paged_fp8 stores new tokens behind the cached ones.  Sequence b's new tokens
