@@ -13,13 +13,15 @@
 //   c1 + c2 / 16: e4m3 keeps 4 significant bits, and the remainder of rounding 8 bits to 4
 //   has 4.  The sum is exact down to 2^-14 of the row's largest element and off by at most
 //   2^-22 of it below.
-//   p, fp32, times its key's value scale, is c1 + c2 / 16 + c3 / 256: relative error 2^-13,
-//   and at most 2^-22 of the largest where the terms run into e4m3's smallest step.
+//   p, fp32, times its key's value scale, is rounded to f16's 11 bits and split exactly into
+//   c1 + c2 / 16 + c3 / 256: relative error 2^-11, and at most 2^-22 of the largest where the
+//   terms run into e4m3's smallest step.
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
-// reference by 2^3 (then P would leave e4m3's range): the four softmax warps vote once per
-// tile, and only a tile that does pass takes the maximum and rescales O^T.
+// reference by 2^3 (then P would leave e4m3's range): the softmax warps vote once per tile,
+// and only a tile that does pass takes the maximum and rescales O^T.  A thread's terms of one
+// key are contiguous in P (MN-major, like V), so they leave in 16-byte stores.
 //
 // Work: the tiles of 128 keys of all (sequence, key/value head, block of RB rows), laid end to
 // end, are cut evenly over the resident CTAs (a prefix sum over seq_lens on the device, so
@@ -27,9 +29,12 @@
 // rows directly and at most two partial results (the item its range begins in, the item it
 // ends in), which a second kernel merges by log-sum-exp.
 //
-// Warps: 0-3 softmax and epilogue, 4 MMA issue and tensor memory, 5 TMA, 6 query terms.
+// Warps: one or more softmax warpgroups of up to 16 rows each (they also write the results),
+// then MMA issue and tensor memory, TMA, and one that prepares query terms and key scales.
 // Per CTA: a ring of 16 KB slots (K_0 V_0 K_1 V_1 ...; 32 KB at d = 256) that runs across
-// items, two S slots, two P buffers, two query buffers.
+// items, two S slots, two P buffers, two query buffers, three tiles of scales.
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -43,25 +48,32 @@ constexpr float kUnseen = -3.0e38f;    // reference of a row that has seen no ke
 constexpr float kMoveLog2 = 3.0f;      // the reference moves when a score passes it by 2^3 ...
 constexpr float kOneP = 32.0f;         // ... so that p = 1 enters as 32 and at most 256 < 448
 constexpr uint32_t kBadPartial = 0x7fc0bad1u;  // L of a partial result of a rejected sequence
-constexpr int kThreads = 224;
+constexpr int kScaleStages = 3;
 
 // NCH: 128-byte chunks of a row (d <= 128: 1, d = 256: 2).  RB: query rows per CTA.
 template <int NCH, int RB>
 struct Dec8Tile {
+    static constexpr int RW = RB < 16 ? RB : 16;         // rows of a softmax warpgroup
+    static constexpr int NWG = RB / RW;
     static constexpr int NS = 2 * RB;                    // columns of S^T: two terms of q
     static constexpr int NP = (3 * RB + 15) / 16 * 16;   // columns of O^T: three terms of p
     static constexpr int CTAS = (NCH == 1 && RB <= 32) ? 2 : 1;  // resident per SM
+    static constexpr int THREADS = 32 * (4 * NWG + 3);
     static constexpr uint32_t CHUNK = kTile * 128;
     static constexpr uint32_t SLOT = NCH * CHUNK;
     static constexpr uint32_t Q_CHUNK = NS * 128;
     static constexpr uint32_t Q_BYTES = NCH * Q_CHUNK;   // of one of two buffers
-    static constexpr uint32_t P_BYTES = NP * 128;        // of one of two buffers
-    static constexpr uint32_t FIXED = 2 * Q_BYTES + 2 * P_BYTES;
-    static constexpr uint32_t BUDGET = (CTAS == 2 ? 113u : 226u) * 1024u - 1024u - 4096u;
-    static constexpr int STAGES = (int)((BUDGET - FIXED) / SLOT) > 10 ? 10 : (int)((BUDGET - FIXED) / SLOT);
+    static constexpr uint32_t P_CHUNK = kTile * 32;      // 32 columns of every key
+    static constexpr uint32_t P_BYTES = (NP + 31) / 32 * P_CHUNK;  // of one of two buffers
+    static constexpr uint32_t MISC = RB <= 16 ? 4096 : 8192;
+    static constexpr uint32_t FIXED = 2 * Q_BYTES + 2 * P_BYTES + MISC + 1024;
+    static constexpr uint32_t BUDGET = (CTAS == 2 ? 113u : 226u) * 1024u;
+    static constexpr int FIT = (int)((BUDGET - FIXED) / SLOT);
+    static constexpr int STAGES = FIT > 10 ? 10 : FIT;
     static constexpr uint32_t OFF_Q = STAGES * SLOT;
     static constexpr uint32_t OFF_P = OFF_Q + 2 * Q_BYTES;
     static constexpr uint32_t OFF_MISC = OFF_P + 2 * P_BYTES;
+    static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
     static constexpr uint32_t TM_O = 2 * NS;             // after two S slots
     static constexpr uint32_t TM_USED = TM_O + NCH * NP;
     static constexpr uint32_t TM_COLS = TM_USED <= 64 ? 64 : TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
@@ -71,22 +83,25 @@ struct Dec8Tile {
 };
 
 // Small per-CTA state behind the buffers.
-template <int RB, int STAGES>
+template <int RB, int STAGES, int NWG>
 struct Dec8Misc {
     unsigned long long full[STAGES], empty[STAGES];
     unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], done;
+    unsigned long long scale_full[kScaleStages], scale_empty[kScaleStages];
     uint32_t tmem;
     int abort;
-    int bad;                        // the segment met a page out of range
-    float vref;                     // power of two that the value scales are taken relative to
+    int bad[2];                     // per query buffer: the segment met a page out of range
     long long g0, g1, g_b;          // this CTA's tiles; tiles before sequence b0
     int b0;
+    alignas(16) float k_scale[kScaleStages][kTile];
+    alignas(16) float v_scale[kScaleStages][kTile];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
     alignas(16) int limit[2][RB];        // keys the row sees
     alignas(16) float mref[RB];          // reference of the row's scores, base 2
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
-    float vpart[4];
+    float vref[NWG];                // power of two that the value scales are taken relative to
+    float vpart[NWG][4];
 };
 
 struct FastDiv {  // n / d for 0 <= n < 2^31
@@ -128,57 +143,126 @@ struct Dec8Args {
 
 // ---------------------------------------------------------------- small PTX
 
-// Columns [taddr, taddr + 8) or + 16 of the calling warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+// Columns [taddr, taddr + N) of the calling warp's 32 lanes (N = 8, 16 or 32), without waiting.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
                    "=f"(r[6]), "=f"(r[7])
                  : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+        "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_wait8(float (&r)[8]) {  // ties the registers to the wait
+// Wait for this thread's tcgen05.ld; the registers are tied to the wait.
+__device__ __forceinline__ void tmem_wait(float (&r)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
                    "+f"(r[6]), "+f"(r[7])
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_wait(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                   "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                   "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :
+                 : "memory");
+}
 
-// Barrier 1 over the 128 softmax threads that also answers: does any of them say yes?
-__device__ __forceinline__ bool vote_softmax(bool yes) {
+// Barrier `id` over the 128 threads of a warpgroup that also answers: does any of them say yes?
+__device__ __forceinline__ bool vote_group(int id, bool yes) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)yes)
+        : "r"((uint32_t)yes), "r"(id)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sync_softmax() { named_barrier_sync(1, 128); }
 
-// e4m3 of two values (a in the low byte), and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+__device__ __forceinline__ float warp_max(float x) {  // NaN is passed over
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+
+// e4m3 of two f16 values (16 bits), and back, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t c) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-    float lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return make_float2(lo, hi);
+    return h;
+}
+// Two floats as f16x2 (a in the low half).
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+    return h;
+}
+// (h - c) * 16 on f16 pairs: exact for the remainder of rounding h to c.
+__device__ __forceinline__ uint32_t remainder16(uint32_t h, uint32_t c) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 m, k;\n\tmov.b32 k, 0x4c004c00;\n\tsub.rn.f16x2 m, %1, %2;\n\t"
+        "mul.rn.f16x2 %0, m, k;\n\t}"
+        : "=r"(r)
+        : "r"(h), "r"(c));
+    return r;
 }
 
-__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// (x0, x1) <- (x0, x1) * (a0, a1) - (c0, c1).
+__device__ __forceinline__ void fms_f32x2(float &x0, float &x1, float a0, float a1, float c0, float c1) {
+    asm("{\n\t.reg .b64 x, a, c;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
+        "mov.b64 c, {%4, %5};\n\tfma.rn.f32x2 x, x, a, c;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(a0), "f"(a1), "f"(-c0), "f"(-c1));
+}
+
+// 4-byte asynchronous copy global -> shared, or 4 zero bytes; the thread's earlier ones
+// arrive once on `bar` when they are done.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool copy) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(copy ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// MN-major operand with the 32-byte swizzle: rows of 32 bytes (32 columns of one key), 8 rows
+// per 256-byte atom (`sbo` between atoms), `lbo` between runs of 32 columns.
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)6 << 61;
+    return d;
+}
+// Address of the 16-byte column group c of a key in such an operand (the swizzle exchanges a
+// row's halves where bit 7 of the address is set: every other four rows).
+__device__ __forceinline__ uint32_t p_addr(uint32_t base, uint32_t chunk, int c, int key) {
+    return base + (c >> 1) * chunk + key * 32 + ((((uint32_t)c & 1u) ^ (((uint32_t)key >> 2) & 1u)) << 4);
 }
 
 // Byte `x` (0..127) of row n of an operand of 128-byte rows with the 128-byte swizzle.
@@ -269,12 +353,13 @@ struct Walk {
 // ---------------------------------------------------------------- the kernel
 
 template <int NCH, int RB>
-__global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
+__global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>::CTAS)
     fa_decode8_kernel(const __grid_constant__ Dec8Args a) {
     using T = Dec8Tile<NCH, RB>;
-    using Misc = Dec8Misc<RB, T::STAGES>;
-    static_assert(sizeof(Misc) <= 4096, "state fits behind the buffers");
-    constexpr int ST = T::STAGES;
+    using Misc = Dec8Misc<RB, T::STAGES, T::NWG>;
+    static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
+    constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG;
+    constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
     griddep_launch_dependents();  // the merge kernel may launch while the tiles run
     extern __shared__ uint8_t dec8_smem[];
     const uint32_t raw = smem_u32(dec8_smem);
@@ -292,24 +377,28 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(bar(ms.q_full[u]), 32);
-            mbar_init(bar(ms.q_empty[u]), 2);  // the MMAs that read it, the softmax warps
+            mbar_init(bar(ms.q_empty[u]), 1 + NWG);  // the MMAs that read it, the warpgroups
             mbar_init(bar(ms.s_full[u]), 1);
-            mbar_init(bar(ms.p_full[u]), 128);
+            mbar_init(bar(ms.p_full[u]), 4 * NWG);   // one arrival per softmax warp
             mbar_init(bar(ms.pv_done[u]), 1);
+        }
+        for (int u = 0; u < kScaleStages; ++u) {
+            mbar_init(bar(ms.scale_full[u]), 64);    // per lane: its copies, its other writes
+            mbar_init(bar(ms.scale_empty[u]), 1);
         }
         mbar_init(bar(ms.done), 1);
         ms.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(&ms.tmem), T::TM_COLS);
         tmem_relinquish();
     }
-    if (warp == 5 && lane == 0) {
+    if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_desc(&a.tm_k);
         tma_prefetch_desc(&a.tm_v);
     }
-    if (warp == 6) {
+    if (warp == kAuxWarp) {
         // this CTA's range of tiles, and the sequence it begins in
         long long pre;
         const long long ipb = (long long)a.Hkv * a.row_blocks;
@@ -356,11 +445,12 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
     walk.t = walk.left > 0 ? (int)((ms.g0 - ms.g_b) % walk.nt) : 0;
     Segment s;
 
-    if (warp == 5) {
+    if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA producer
         // The whole warp runs the loop.  A tile is a run of boxes of `box` rows (the largest
         // power of two that divides the page size, so a box never straddles two pages); lane i
         // looks up and copies boxes i, i + 32, ...  Boxes behind the last key are not copied.
+        // Page numbers are fetched one tile ahead and looked at only when they are used.
         const int per_tile = kTile / a.box;
         uint32_t n = 0;  // ring slots used so far
         bool ok = true;
@@ -372,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                 for (int i = 0; i < 4; ++i) {
                     const int bx = lane + 32 * i;
                     const long long key = (long long)t * kTile + (long long)bx * a.box;
-                    pg[i] = (bx < per_tile && t < s.t1 && key < len)
-                                ? __ldg(bt + a.by_page.div((uint32_t)key)) : -1;
-                    if (pg[i] >= a.num_pages) pg[i] = -1;
+                    pg[i] = -1;
+                    if (bx < per_tile && t < s.t1 && key < len)
+                        pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
                 }
             };
             int pg[4], pg_next[4];
@@ -383,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                 look(t + 1, pg_next);
                 int mine = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mine += pg[i] >= 0 ? 1 : 0;
+                for (int i = 0; i < 4; ++i) mine += pg[i] >= 0 && pg[i] < a.num_pages ? 1 : 0;
                 const uint32_t bytes =
                     (uint32_t)__reduce_add_sync(kFull, mine) * (uint32_t)a.box * 128u * NCH;
 #pragma unroll
@@ -400,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (pg[i] < 0) continue;
+                        if (pg[i] < 0 || pg[i] >= a.num_pages) continue;
                         const int row = (lane + 32 * i) * a.box;
                         const uint32_t key = (uint32_t)(t * kTile + row);
                         const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
@@ -423,10 +513,10 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
             for (uint32_t i = n > (uint32_t)ST ? n - ST : 0; i < n; ++i)
                 mbar_wait_warp(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
         }
-    } else if (warp == 4) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescS = idesc_e4m3_f32(128, T::NS);
-        constexpr uint32_t kIdescO = idesc_e4m3_f32(128, T::NP) | (1u << 15);  // A is MN-major
+        constexpr uint32_t kIdescO = idesc_e4m3_f32(128, T::NP) | (3u << 15);  // both MN-major
         const int ksteps = a.d / 32;
         Walk ahead = walk;   // segments of S, up to two tiles ahead of O
         Segment sa;
@@ -466,18 +556,20 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                 const int u = j & 1;
                 const uint32_t i = 2 * j + 1;
                 const int slot = (int)(i % ST);
-                ok = mbar_wait_warp(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA) &&
-                     mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                ok = mbar_wait_warp(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
+                // every softmax warp has read the tile's scales
+                if (lane == 0) mbar_arrive(bar(ms.scale_empty[j % kScaleStages]));
+                ok = ok && mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dv = sdesc_sw128(base + slot * T::SLOT, T::CHUNK, 1024);
-                const uint64_t dp = sdesc_sw128(sP + u * T::P_BYTES, 16, 1024);
+                const uint64_t dp = sdesc_sw32(sP + u * T::P_BYTES, T::P_CHUNK, 256);
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
                     for (int ks = 0; ks < kTile / 32; ++ks)
                         mma_ss_elect_f8(tmem + T::TM_O + c * T::NP, desc_add(dv, c * T::CHUNK + ks * 4096),
-                                        desc_add(dp, ks * 32), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
+                                        desc_add(dp, ks * 1024), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                 tc_commit_elect(bar(ms.pv_done[u]));
                 tc_commit_elect(bar(ms.empty[slot]));
                 if (more) issue_s();
@@ -488,20 +580,34 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
         volatile int never = 0;
         const Guard g2{a.status, &never, kWaitLimitNs};
         mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
-    } else if (warp == 6) {
-        // ------------------------------------------------------------ query terms
-        const int E = a.d == 96 ? 4 : a.d / 32;  // elements per lane
+    } else if (warp == kAuxWarp) {
+        // ------------------------------------------- query terms, key and value scales
+        const int E = a.d == 96 ? 4 : a.d / 32;  // elements of a query row per lane
         const bool on = lane * E < a.d;
-        uint32_t seg = 0;
+        uint32_t seg = 0, j = 0;
         bool ok = true;
         while (ok && walk.next(a, &s)) {
             const int qb = seg & 1;
             ok = seg < 2 || mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
             if (!ok) break;
             const int len = a.seq_lens[s.b];
+            const int *bt = a.block_table + (size_t)s.b * a.max_pages;
+            // lane i has keys i, i + 32, ... of a tile; pages are fetched one tile ahead
+            auto look = [&](int t, int (&pg)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const long long key = (long long)t * kTile + lane + 32 * i;
+                    pg[i] = 0;
+                    if (t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
+                }
+            };
+            int pg[4], pg_next[4];
+            look(s.t0, pg);
             const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
             const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
             const uint32_t sq = sQ + qb * T::Q_BYTES;
+            if (lane == 0) ms.bad[qb] = 0;
+            __syncwarp();
 #pragma unroll 1
             for (int r8 = 0; r8 < RB; r8 += 8) {
                 uint32_t w[8][NCH == 2 ? 4 : 2];
@@ -537,25 +643,23 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                     const bool finite = am < 0x7f80u;
 #pragma unroll
                     for (int i = 0; i < (NCH == 2 ? 4 : 2); i += 2) {
-                        float x[4], y[4];
+                        // 8 significant bits fit f16, and so do both remainders
+                        uint32_t h[2], c1 = 0, c2 = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t u = w[e][i + k / 2];
-                            x[k] = __uint_as_float(k % 2 ? (u & 0xffff0000u) : (u << 16)) * inv;
-                            if (!finite) x[k] = __uint_as_float(0x7fc00000u);
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t u = w[e][i + k];
+                            h[k] = pack_f16(__uint_as_float(u << 16) * inv,
+                                            __uint_as_float(u & 0xffff0000u) * inv);
+                            if (!finite) h[k] = 0x7fff7fffu;
+                            const uint32_t c = e4m3x2_of(h[k]);
+                            c1 |= c << (16 * k);
+                            c2 |= e4m3x2_of(remainder16(h[k], f16x2_of(c))) << (16 * k);
                         }
-                        const uint32_t c1 = pack_e4m3x4(x[0], x[1], x[2], x[3]);
-                        const float2 lo = from_e4m3x2(c1 & 0xffffu), hi = from_e4m3x2(c1 >> 16);
-                        y[0] = (x[0] - lo.x) * 16.f;
-                        y[1] = (x[1] - lo.y) * 16.f;
-                        y[2] = (x[2] - hi.x) * 16.f;
-                        y[3] = (x[3] - hi.y) * 16.f;
-                        const uint32_t c2 = pack_e4m3x4(y[0], y[1], y[2], y[3]);
                         if (on) {
                             const int col = lane * E + 2 * i;  // byte of the row
                             const uint32_t q0 = sq + (col >> 7) * T::Q_CHUNK;
-                            const int n1 = (r >> 3) * 16 + (r & 7);
-                            const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + 8, col & 127);
+                            const int n1 = r / RW * (2 * RW) + r % RW;
+                            const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + RW, col & 127);
                             if (NCH == 1 && E == 2) {
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(a1), "h"((uint16_t)c1) : "memory");
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(a2), "h"((uint16_t)c2) : "memory");
@@ -575,153 +679,188 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
             fence_proxy_async_smem();
             mbar_arrive(bar(ms.q_full[qb]));
             ++seg;
+            for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
+                look(t + 1, pg_next);
+                const int st = (int)(j % kScaleStages);
+                ok = j < kScaleStages || mbar_wait_warp(bar(ms.scale_empty[st]), ((j / kScaleStages) - 1) & 1,
+                                                        g, SITE_DEC_EMPTY);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = lane + 32 * i;
+                    const uint32_t key = (uint32_t)(t * kTile + kk);
+                    const bool valid = pg[i] >= 0 && pg[i] < a.num_pages;
+                    const bool copy = (int)key < len && valid;  // keys not there: scale 0
+                    if (!valid) ms.bad[qb] = 1;
+                    const uint32_t row = key - a.by_page.div(key) * (uint32_t)a.page_size;
+                    const size_t at = copy ? ((size_t)pg[i] * a.Hkv + s.kvh) * a.groups + a.by_group.div(row) : 0;
+                    cp_async4(smem_u32(&ms.k_scale[st][kk]), a.k_scale + at, copy);
+                    cp_async4(smem_u32(&ms.v_scale[st][kk]), a.v_scale + at, copy);
+                }
+                cp_async_arrive(bar(ms.scale_full[st]));
+                mbar_arrive(bar(ms.scale_full[st]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pg[i] = pg_next[i];
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ------------------------------------------------------------ softmax, epilogue
-        // All four warps run every step even after a wait has given up (waits then return at
+        // Every warp runs every step even after a wait has given up (waits then return at
         // once), so that none is left behind at a barrier.
-        const int tid = threadIdx.x;  // key of the tile; lane of O^T (head dimension)
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const int wg = warp >> 2, w4 = warp & 3;
+        const int kk = threadIdx.x & 127;  // key of the tile; lane of O^T (head dimension)
+        const int rw0 = wg * RW;           // this warpgroup's rows of the CTA's
+        const int id = 1 + wg;             // its named barrier
+        const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + wg * 2 * RW;
+        const uint32_t t_o = tmem + lane_base + T::TM_O + wg * 3 * RW;
         uint32_t j = 0, seg = 0;
-        float l[RB];
+        float l[RW];
         while (walk.next(a, &s)) {
             const int qb = seg & 1;
             const int len = a.seq_lens[s.b];
-            const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
-            const int *bt = a.block_table + (size_t)s.b * a.max_pages;
-            const int full_keys = a.causal ? len - a.Nq + 1 : len;  // keys that every row sees
-            // page of this thread's key of tile t (-1: none, -2: out of range), and its scales
-            auto page_of = [&](int t) {
-                const long long key = (long long)t * kTile + tid;
-                if (t >= s.t1 || key >= len) return -1;
-                const int pg = __ldg(bt + a.by_page.div((uint32_t)key));
-                return pg >= 0 && pg < a.num_pages ? pg : -2;
-            };
-            auto scales_of = [&](int t, int pg, float &ks, float &vs) {
-                ks = vs = 0.f;
-                if (pg < 0) return;
-                const uint32_t key = (uint32_t)(t * kTile + tid);
-                const uint32_t row = key - a.by_page.div(key) * (uint32_t)a.page_size;
-                const size_t at = ((size_t)pg * a.Hkv + s.kvh) * a.groups + a.by_group.div(row);
-                ks = __ldg(a.k_scale + at);
-                vs = __ldg(a.v_scale + at);
-            };
-            int pg = page_of(s.t0), pg1 = page_of(s.t0 + 1);
-            float ks, vs, ks1, vs1;
-            scales_of(s.t0, pg, ks, vs);
-            if (tid < RB) ms.mref[tid] = kUnseen;
-            if (tid == 0) {
-                ms.vref = 0.f;
-                ms.bad = 0;
-            }
+            const int r0 = s.rb * RB + rw0, rows = min(RW, a.R - r0);  // may be none
+            const int full_keys = a.causal ? len - a.Nq + 1 : len;     // keys that every row sees
+            if (kk < RW) ms.mref[rw0 + kk] = kUnseen;
+            if (kk == 0) ms.vref[wg] = 0.f;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) l[r] = 0.f;
+            for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
-            sync_softmax();
+            named_barrier_sync(id, 128);
             for (int t = s.t0; t < s.t1; ++t, ++j) {
                 const int u = j & 1;
-                const int key = t * kTile + tid;
-                const int pg2 = page_of(t + 2);
-                scales_of(t + 1, pg1, ks1, vs1);
+                const int key = t * kTile + kk;
+                const int st = (int)(j % kScaleStages);
+                mbar_wait_warp(bar(ms.scale_full[st]), (j / kScaleStages) & 1, g, SITE_DEC_FULL);
+                const float ks = ms.k_scale[st][kk], vs = ms.v_scale[st][kk];
                 mbar_wait_warp(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 tc_fence_after();
-                float x[RB];
+                const bool partly = (t + 1) * (long long)kTile > full_keys;  // some row sees less
+                // base-2 exponents of the rows' scores of this thread's key; with REF less the
+                // references
+                float x[RW];
+                auto scores = [&](auto ref) {
+                    float c1[RW];
+                    tmem_ld(t_s + u * T::NS, c1);
+                    tmem_ld(t_s + u * T::NS + RW, x);
+                    tmem_wait(c1);
+                    tmem_wait(x);
+                    const uint64_t k16 = f32x2_splat(0.0625f), ks2 = f32x2_splat(ks);
 #pragma unroll
-                for (int q = 0; q < RB / 8; ++q) {
-                    float c1[8], c2[8];
-                    tmem_ld8(tmem + lane_base + u * T::NS + q * 16, c1);
-                    tmem_ld8(tmem + lane_base + u * T::NS + q * 16 + 8, c2);
-                    tmem_wait8(c1);
-                    tmem_wait8(c2);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[q * 8 + e] = fmaf(c2[e], 0.0625f, c1[e]) * (ms.row_scale[qb][q * 8 + e] * ks);
-                }
-                if ((t + 1) * (long long)kTile > full_keys) {  // some row does not see every key
-#pragma unroll
-                    for (int r = 0; r < RB; ++r)
-                        if (key >= ms.limit[qb][r]) x[r] = -INFINITY;
-                }
-                bool move = vs > ms.vref || pg == -2;
-#pragma unroll
-                for (int r = 0; r < RB; ++r) move = move || x[r] > ms.mref[r] + kMoveLog2;
-                if (vote_softmax(move)) {
-                    // new references: the tile's maximum where it passes the old one by 2^3
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        float m = x[r];
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                        if (lane == (r & 31)) ms.part[warp][r] = m;
+                    for (int r = 0; r < RW; r += 4) {
+                        const float4 rs = *reinterpret_cast<const float4 *>(&ms.row_scale[qb][rw0 + r]);
+                        float f[4] = {rs.x, rs.y, rs.z, rs.w};
+                        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if constexpr (decltype(ref)::value)
+                            m = *reinterpret_cast<const float4 *>(&ms.mref[rw0 + r]);
+                        mul_f32x2(f[0], f[1], ks2);
+                        mul_f32x2(f[2], f[3], ks2);
+                        fma_f32x2(x[r], x[r + 1], k16, c1[r], c1[r + 1]);
+                        fma_f32x2(x[r + 2], x[r + 3], k16, c1[r + 2], c1[r + 3]);
+                        fms_f32x2(x[r], x[r + 1], f[0], f[1], m.x, m.y);
+                        fms_f32x2(x[r + 2], x[r + 3], f[2], f[3], m.z, m.w);
                     }
-                    float vm = vs;
+                    if (partly) {
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(kFull, vm, o));
-                    if (lane == 0) ms.vpart[warp] = vm;
-                    if (pg == -2) ms.bad = 1;
-                    const float v_old = ms.vref;
-                    sync_softmax();
-                    vm = fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3]));
+                        for (int r = 0; r < RW; ++r)
+                            if (key >= ms.limit[qb][rw0 + r]) x[r] = -INFINITY;
+                    }
+                };
+                scores(std::true_type());
+                float top = x[0];
+#pragma unroll
+                for (int r = 1; r < RW; ++r) top = fmaxf(top, x[r]);
+                if (vote_group(id, top > kMoveLog2 || vs > ms.vref[wg])) {
+                    // new references: the tile's maximum where it passes the old one by 2^3
+                    scores(std::false_type());
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) {
+                        const float m = warp_max(x[r]);
+                        if (lane == r) ms.part[w4][rw0 + r] = m;
+                    }
+                    const float vm_warp = warp_max(vs);
+                    if (lane == 0) ms.vpart[wg][w4] = vm_warp;
+                    const float v_old = ms.vref[wg];
+                    named_barrier_sync(id, 128);
+                    const float vm = fmaxf(fmaxf(ms.vpart[wg][0], ms.vpart[wg][1]),
+                                           fmaxf(ms.vpart[wg][2], ms.vpart[wg][3]));
                     float v_new = v_old;
                     if (vm > v_old)  // the power of two at or above, and kOneP / v_new stays finite
                         v_new = fmaxf(__uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u),
                                       0x1p-120f);
-                    if (tid < RB) {
-                        const float m_old = ms.mref[tid];
-                        const float m = fmaxf(fmaxf(ms.part[0][tid], ms.part[1][tid]),
-                                              fmaxf(ms.part[2][tid], ms.part[3][tid]));
+                    if (kk < RW) {
+                        const int r = rw0 + kk;
+                        const float m_old = ms.mref[r];
+                        const float m = fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]),
+                                              fmaxf(ms.part[2][r], ms.part[3][r]));
                         const bool up = m > m_old + kMoveLog2;
-                        ms.alpha[tid] = up ? ex2(m_old - m) : 1.f;
-                        if (up) ms.mref[tid] = m;
+                        ms.alpha[r] = up ? ex2(m_old - m) : 1.f;
+                        if (up) ms.mref[r] = m;
                     }
-                    if (tid == 0) ms.vref = v_new;
-                    sync_softmax();
+                    if (kk == 0) ms.vref[wg] = v_new;
+                    named_barrier_sync(id, 128);
 #pragma unroll
-                    for (int r = 0; r < RB; ++r) l[r] *= ms.alpha[r];
+                    for (int r = 0; r < RW; ++r) {
+                        l[r] *= ms.alpha[rw0 + r];
+                        x[r] -= ms.mref[rw0 + r];
+                    }
                     if (t > s.t0) {  // O^T to the new references, once PV of the tile before is done
-                        const float fv = v_new > 0.f ? v_old / v_new : 1.f;
+                        const float fo = v_new > 0.f ? v_old / v_new : 1.f;
                         mbar_wait_warp(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < NCH; ++c)
 #pragma unroll 1
-                            for (int n = 0; n < 3 * RB / 8; ++n) {
+                            for (int n = 0; n < 3 * RW; n += 8) {
                                 float o[8];
-                                const uint32_t at = tmem + lane_base + T::TM_O + c * T::NP + n * 8;
-                                tmem_ld8(at, o);
-                                tmem_wait8(o);
+                                const uint32_t at = t_o + c * T::NP + n;
+                                tmem_ld(at, o);
+                                tmem_wait(o);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] *= ms.alpha[n / 3 * 8 + e] * fv;
+                                for (int e = 0; e < 8; ++e) o[e] *= ms.alpha[rw0 + n % RW + e] * fo;
                                 tmem_st8(at, o);
                             }
                         tmem_wait_st();
                     }
                 }
-                if (j >= 2)  // the P buffer's last reader
-                    mbar_wait_warp(bar(ms.pv_done[u]), ((j >> 1) - 1) & 1, g, SITE_DEC_MMA);
-                const float vref = ms.vref;
+                const float vref = ms.vref[wg];
                 const float fv = vref > 0.f ? vs * (kOneP / vref) : 0.f;
-                const uint32_t p0 = sP + u * T::P_BYTES;
+                const uint64_t fv2 = f32x2_splat(fv);
+                uint32_t term[3][RW / 4];
 #pragma unroll
-                for (int r = 0; r < RB; r += 2) {
-                    const float pa = ex2(x[r] - ms.mref[r]), pb = ex2(x[r + 1] - ms.mref[r + 1]);
-                    l[r] += pa;
-                    l[r + 1] += pb;
-                    float wa = pa * fv, wb = pb * fv;
-                    const int n = (r >> 3) * 24 + (r & 7);
+                for (int r = 0; r < RW; r += 4) {
+                    uint32_t h[2];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t c = to_e4m3x2(wa, wb);
-                        sts8(swizzled(p0, n + 8 * k, tid), c & 0xffu);
-                        sts8(swizzled(p0, n + 8 * k + 1, tid), c >> 8);
-                        if (k < 2) {
-                            const float2 f = from_e4m3x2(c);
-                            wa = (wa - f.x) * 16.f;
-                            wb = (wb - f.y) * 16.f;
+                    for (int k = 0; k < 2; ++k) {
+                        float pa = ex2(x[r + 2 * k]), pb = ex2(x[r + 2 * k + 1]);
+                        add_f32x2(l[r + 2 * k], l[r + 2 * k + 1], pa, pb);
+                        mul_f32x2(pa, pb, fv2);
+                        h[k] = pack_f16(pa, pb);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        const uint32_t ca = e4m3x2_of(h[0]), cb = e4m3x2_of(h[1]);
+                        term[e][r / 4] = ca | cb << 16;
+                        if (e < 2) {
+                            h[0] = remainder16(h[0], f16x2_of(ca));
+                            h[1] = remainder16(h[1], f16x2_of(cb));
                         }
                     }
                 }
-                if ((t + 1) * (long long)kTile > len) {
+                if (j >= 2)  // the P buffer's last reader
+                    mbar_wait_warp(bar(ms.pv_done[u]), ((j >> 1) - 1) & 1, g, SITE_DEC_MMA);
+                const uint32_t p0 = sP + u * T::P_BYTES;
+                if constexpr (RW == 8) {
+                    sts128(p_addr(p0, T::P_CHUNK, 0, kk), term[0][0], term[0][1], term[1][0], term[1][1]);
+                    sts128(p_addr(p0, T::P_CHUNK, 1, kk), term[2][0], term[2][1], 0u, 0u);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        sts128(p_addr(p0, T::P_CHUNK, 3 * wg + e, kk), term[e][0], term[e][1], term[e][2],
+                               term[e][3]);
+                }
+                if (wg == 0 && (t + 1) * (long long)kTile > len) {
                     // rows of V behind the last key: whatever lies there, P is 0 and V must not be NaN
                     const uint32_t i = 2 * j + 1;
                     const int slot = (int)(i % ST);
@@ -731,76 +870,76 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
                         for (int c = 0; c < NCH; ++c)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4 *>(gbase + slot * T::SLOT + c * T::CHUNK + tid * 128 +
-                                                           e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                sts128(base + slot * T::SLOT + c * T::CHUNK + kk * 128 + e * 16, 0u, 0u, 0u, 0u);
                     }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(bar(ms.p_full[u]));
-                pg = pg1;
-                pg1 = pg2;
-                ks = ks1;
-                vs = vs1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ms.p_full[u]));
             }
             // ---- the segment's rows: sums over all keys, then O^T columns
             const uint32_t jl = j - 1;
-            mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
-            tc_fence_after();
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
+            for (int r = 0; r < RW; ++r) {
                 float v = l[r];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-                if (lane == (r & 31)) ms.part[warp][r] = v;
+                if (lane == r) ms.part[w4][rw0 + r] = v;
             }
-            sync_softmax();
+            mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
+            tc_fence_after();
+            named_barrier_sync(id, 128);
             const bool whole = s.t0 == 0 && s.t1 == s.nt;
-            const bool bad = ms.bad != 0;
+            const bool bad = ms.bad[qb] != 0;
             const bool dead = *g.abort != 0;
-            const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * RB;
+            const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * RB + rw0;
             const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
-            const float ov = ms.vref * (1.f / kOneP);
-            if (bad && tid == 0) {
+            const float ov = ms.vref[wg] * (1.f / kOneP);
+            if (bad && threadIdx.x == 0) {
                 atomicCAS(a.status + 1, 0, SITE_DEC8_BAD_PAGE);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
             }
-            if (tid < rows && !dead) {
-                const float sum = (ms.part[0][tid] + ms.part[1][tid]) + (ms.part[2][tid] + ms.part[3][tid]);
-                const float l2 = sum == 0.f ? -INFINITY : ms.mref[tid] + lg2(sum);  // base 2
-                if (!whole) a.part_l[prow + tid] = bad ? __uint_as_float(kBadPartial) : l2;
-                else if (!bad) a.lse[row0 + tid] = l2 * kLn2;
+            if (kk < rows && !dead) {
+                const int r = rw0 + kk;
+                const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
+                const float l2 = sum == 0.f ? -INFINITY : ms.mref[r] + lg2(sum);  // base 2
+                if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
+                else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
             }
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c) {
-                const int dd = c * 128 + tid;
+                const int dd = c * 128 + kk;
 #pragma unroll 1
-                for (int q = 0; q < RB / 8; ++q) {
+                for (int q = 0; q < RW; q += 8) {
                     float o0[8], o1[8], o2[8];
                     __syncwarp();
-                    const uint32_t at = tmem + lane_base + T::TM_O + c * T::NP + q * 24;
-                    tmem_ld8(at, o0);
-                    tmem_ld8(at + 8, o1);
-                    tmem_ld8(at + 16, o2);
-                    tmem_wait8(o0);
-                    tmem_wait8(o1);
-                    tmem_wait8(o2);
-                    if (dd >= a.d || dead || bad) continue;
+                    const uint32_t at = t_o + c * T::NP + q;
+                    tmem_ld(at, o0);
+                    tmem_ld(at + RW, o1);
+                    tmem_ld(at + 2 * RW, o2);
+                    tmem_wait(o0);
+                    tmem_wait(o1);
+                    tmem_wait(o2);
+                    if (dd < a.d && !dead && !bad) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = q * 8 + e;
-                        if (r >= rows) break;
-                        const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
-                        const float inv = sum == 0.f ? 0.f : ov / sum;
-                        const float o = fmaf(fmaf(o2[e], 0.0625f, o1[e]), 0.0625f, o0[e]) * inv;
-                        if (whole) a.o[(row0 + r) * a.d + dd] = __float2bfloat16(o);
-                        else a.part_o[(prow + r) * a.d + dd] = o;
+                        for (int e = 0; e < 8; ++e) {
+                            if (q + e < rows) {
+                                const int r = rw0 + q + e;
+                                const float sum =
+                                    (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
+                                const float inv = sum == 0.f ? 0.f : ov / sum;
+                                const float o = fmaf(fmaf(o2[e], 0.0625f, o1[e]), 0.0625f, o0[e]) * inv;
+                                if (whole) a.o[(row0 + q + e) * a.d + dd] = __float2bfloat16(o);
+                                else a.part_o[(prow + q + e) * a.d + dd] = o;
+                            }
+                        }
                     }
                 }
             }
             tc_fence_before();
-            sync_softmax();  // the state above is free for the next segment
-            if (tid == 0) mbar_arrive(bar(ms.q_empty[qb]));
+            named_barrier_sync(id, 128);  // the state above is free for the next segment
+            if (kk == 0) mbar_arrive(bar(ms.q_empty[qb]));
             ++seg;
         }
     }
@@ -808,76 +947,126 @@ __global__ void __launch_bounds__(kThreads, Dec8Tile<NCH, RB>::CTAS)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, T::TM_COLS);
     }
 }
 
-// Merge of the partial results of the items that were cut, one warp per query row:
-// L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  Rows of empty sequences are written here.
+// Merge of the partial results of the items that were cut: L = log2 sum 2^(L_s),
+// O = sum 2^(L_s - L) O_s.  A CTA has four query rows; its warps find one row's partials each,
+// then all of them take every fourth partial of every row (a long sequence alone in the
+// launch is cut into dozens) and add up through shared memory.  Bound by latency: two rounds
+// of loads.  Rows of empty sequences are written here.
+constexpr int kMergeRows = 4;
 template <int NCH, int RB>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kMergeRows)
     fa_decode8_merge_kernel(const __grid_constant__ Dec8Args a, int n_cta, long long n_rows) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= n_rows) return;
-    const int i = (int)(row % a.Nq);
-    const long long bh = row / a.Nq;
-    const int b = (int)(bh / a.H), h = (int)(bh % a.H), group = a.H / a.Hkv;
-    const int len = a.seq_lens[b];
-    const long long ipb = (long long)a.Hkv * a.row_blocks;
-    long long before;
-    const long long total = count_tiles(a, b, &before) * ipb;
-    griddep_wait();  // every partial result is written
-    if (!len_ok(a, len)) return;
-    __nv_bfloat16 *o = a.o + row * a.d;
-    if (len == 0) {
-        for (int c = lane; c < a.d; c += 32) o[c] = __float2bfloat16(0.f);
-        if (lane == 0) a.lse[row] = -INFINITY;
-        return;
-    }
-    const int r = (h % group) * a.Nq + i, nt = tiles_of(a, b);
-    const long long first =
-        before * ipb + ((long long)(h / group) * a.row_blocks + r / RB) * nt;
-    const int n = busy_ctas(total, n_cta);
-    const int c0 = cta_of(total, first, n), c1 = cta_of(total, first + nt - 1, n);
-    if (c0 == c1) return;  // written directly
-    auto prow = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * RB + r % RB; };
-    float m = -INFINITY;
-    bool bad = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float x = __ldcg(a.part_l + prow(c));
-        bad = bad || __float_as_uint(x) == kBadPartial;
-        m = fmaxf(m, x);
-    }
-    if (__any_sync(kFull, bad)) return;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    if (m == -INFINITY) m = 0.f;  // the row sees no key: every weight is 0
-    constexpr int E = NCH == 2 ? 8 : 4;
-    float acc[E], wsum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-        const int n = min(32, c1 - cb + 1);
-        const float w = lane < n ? ex2(__ldcg(a.part_l + prow(cb + lane)) - m) : 0.f;
-        for (int k = 0; k < n; ++k) {
-            const float wk = __shfl_sync(kFull, w, k);
-            const float *po = a.part_o + prow(cb + k) * a.d;
-            wsum += wk;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = lane + 32 * e;
-                if (c < a.d) acc[e] = fmaf(wk, __ldcg(po + c), acc[e]);
-            }
+    constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
+    __shared__ float s_acc[kMergeRows][kMergeRows][E * 32], s_sum[kMergeRows][kMergeRows], s_max[kMergeRows];
+    __shared__ int s_c0[kMergeRows], s_n[kMergeRows], s_r[kMergeRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = (long long)blockIdx.x * kMergeRows + warp;
+    int n = 0;  // partials of this warp's row
+    bool empty = false;
+    int c0 = 0, r = 0;
+    if (row < n_rows) {
+        const int i = (int)(row % a.Nq);
+        const long long bh = row / a.Nq;
+        const int b = (int)(bh / a.H), h = (int)(bh % a.H), group = a.H / a.Hkv;
+        const int len = a.seq_lens[b];
+        const long long ipb = (long long)a.Hkv * a.row_blocks;
+        long long before;
+        const long long total = count_tiles(a, b, &before) * ipb;
+        empty = len == 0;
+        if (len_ok(a, len) && !empty) {
+            r = (h % group) * a.Nq + i;
+            const int nt = tiles_of(a, b);
+            const long long first =
+                before * ipb + ((long long)(h / group) * a.row_blocks + r / RB) * nt;
+            const int busy = busy_ctas(total, n_cta);
+            c0 = cta_of(total, first, busy);
+            n = cta_of(total, first + nt - 1, busy) - c0 + 1;
+            if (n == 1) n = 0;  // written directly
         }
     }
+    griddep_wait();  // every partial result is written
+    if (empty) {
+        __nv_bfloat16 *o = a.o + row * a.d;
+        for (int c = lane; c < a.d; c += 32) o[c] = __float2bfloat16(0.f);
+        if (lane == 0) a.lse[row] = -INFINITY;
+    }
+    auto prow = [&](int k, int c_first, int rr) {
+        return ((size_t)(c_first + k) * 2 + (k == 0 ? 1 : 0)) * RB + rr % RB;
+    };
+    if (n) {
+        float m = -INFINITY;
+        bool bad = false;
+        for (int k = lane; k < n; k += 32) {
+            const float x = __ldcg(a.part_l + prow(k, c0, r));
+            bad = bad || __float_as_uint(x) == kBadPartial;
+            m = fmaxf(m, x);
+        }
+        m = warp_max(m);
+        if (__any_sync(kFull, bad)) n = 0;
+        if (lane == 0) s_max[warp] = m == -INFINITY ? 0.f : m;  // a row without keys: weights 0
+    }
+    if (lane == 0) {
+        s_c0[warp] = c0;
+        s_n[warp] = n;
+        s_r[warp] = r;
+    }
+    if (!__syncthreads_or(n)) return;
+#pragma unroll 1
+    for (int q = 0; q < kMergeRows; ++q) {
+        const int nq = s_n[q], cq = s_c0[q], rq = s_r[q];
+        if (nq == 0) continue;
+        const float m = s_max[q];
+        float acc[E], wsum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        constexpr int U = 4;  // partials in flight per warp
+        for (int k0 = warp; k0 < nq; k0 += kMergeRows * U) {
+            float w[U], x[U][E];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const int k = k0 + kMergeRows * v;
+                const bool in = k < nq;
+                const size_t pr = prow(in ? k : k0, cq, rq);
+                w[v] = in ? __ldcg(a.part_l + pr) : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[v][e] = in && lane + 32 * e < a.d ? __ldcg(a.part_o + pr * a.d + lane + 32 * e) : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const float wk = ex2(w[v] - m);
+                wsum += wk;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[v][e], acc[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_acc[q][warp][lane + 32 * e] = acc[e];
+        if (lane == 0) s_sum[q][warp] = wsum;
+    }
+    __syncthreads();
+    if (n == 0) return;
+    float wsum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int v = 0; v < kMergeRows; ++v) {
+        wsum += s_sum[warp][v];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += s_acc[warp][v][lane + 32 * e];
+    }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    __nv_bfloat16 *o = a.o + row * a.d;
 #pragma unroll
     for (int e = 0; e < E; ++e)
         if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
-    if (lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (m + lg2(wsum)) * kLn2;
+    if (lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (s_max[warp] + lg2(wsum)) * kLn2;
 }
 
 // CTAs of a launch: all that are resident, or the largest number of tiles there can be.
@@ -933,16 +1122,16 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
     auto kern = fa_decode8_kernel<NCH, RB>;
-    constexpr int kSmem = (int)(T::OFF_MISC + 4096 + 1024);
+    constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = dec8_ctas<NCH, RB>(p);
-    kern<<<n_cta, kThreads, kSmem, stream>>>(a);
+    kern<<<n_cta, T::THREADS, kSmem, stream>>>(a);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // a programmatic dependent: launched as the last CTAs start, it waits for the whole grid
     const long long rows = (long long)p.B * p.H * p.Nq;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows));
+    cfg.blockDim = dim3(32 * kMergeRows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -957,13 +1146,16 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
 // Calls f with the tile that serves R query rows per key/value head of dimension d.
 template <typename F>
 auto with_tile(int d, long long R, F f) {
+    using std::integral_constant;
     if (d == 256) {
-        if (R <= 8) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
-        return f(std::integral_constant<int, 2>(), std::integral_constant<int, 32>());
+        if (R <= 8) return f(integral_constant<int, 2>(), integral_constant<int, 8>());
+        if (R <= 16) return f(integral_constant<int, 2>(), integral_constant<int, 16>());
+        return f(integral_constant<int, 2>(), integral_constant<int, 32>());
     }
-    if (R <= 8) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
-    if (R <= 32) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>());
-    return f(std::integral_constant<int, 1>(), std::integral_constant<int, 64>());
+    if (R <= 8) return f(integral_constant<int, 1>(), integral_constant<int, 8>());
+    if (R <= 16) return f(integral_constant<int, 1>(), integral_constant<int, 16>());
+    if (R <= 32) return f(integral_constant<int, 1>(), integral_constant<int, 32>());
+    return f(integral_constant<int, 1>(), integral_constant<int, 64>());
 }
 
 }  // namespace
