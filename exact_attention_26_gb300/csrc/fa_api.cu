@@ -981,7 +981,16 @@ int check_decode8(int B, int H, int Hkv, int Nq, int d, int page_size, int max_p
     int rc = check_cache8(B, Hkv, d, page_size, max_pages, num_pages, scale_group);
     if (rc == FA_ERR_INVALID_ARG) return rc;
     const int rc2 = check_decode_sizes(B, H, Hkv, Nq, 1, d);
-    return rc2 != FA_OK ? rc2 : rc;
+    if (rc2 != FA_OK || rc != FA_OK) return rc2 != FA_OK ? rc2 : rc;
+    Decode8Params p{};
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    return decode8_max_tiles(p) < (1LL << 31) ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
 }  // namespace

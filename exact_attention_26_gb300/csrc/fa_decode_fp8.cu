@@ -13,13 +13,14 @@
 //   c1 + c2 / 16: e4m3 keeps 4 significant bits, and the remainder of rounding 8 bits to 4
 //   has 4.  The sum is exact down to 2^-14 of the row's largest element and off by at most
 //   2^-22 of it below.
-//   p, fp32, times its key's value scale, is rounded to f16's 11 bits and split exactly into
-//   c1 + c2 / 16 + c3 / 256: relative error 2^-11, and at most 2^-22 of the largest where the
-//   terms run into e4m3's smallest step.
+//   p, fp32, times its key's value scale, is rounded to f16 and split into three e5m2 terms:
+//   e5m2 is f16's upper byte, so the first two are byte selections and the remainders exact
+//   subtractions; the third is rounded to nearest.  Relative error 2^-9 (bf16's), and with
+//   p = 1 entering as 2^12 nothing is lost in e5m2's smallest step above 2^-29.
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
-// reference by 2^3 (then P would leave e4m3's range): the softmax warps vote once per tile,
+// reference by 2^3 (then P would leave e5m2's range): the softmax warps vote once per tile,
 // and only a tile that does pass takes the maximum and rescales O^T.  A thread's terms of one
 // key are contiguous in P (MN-major, like V), so they leave in 16-byte stores.
 //
@@ -46,7 +47,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kTile = 128;             // keys per tile: the M of S^T and the K of O^T
 constexpr float kUnseen = -3.0e38f;    // reference of a row that has seen no key yet
 constexpr float kMoveLog2 = 3.0f;      // the reference moves when a score passes it by 2^3 ...
-constexpr float kOneP = 32.0f;         // ... so that p = 1 enters as 32 and at most 256 < 448
+constexpr float kOneP = 4096.0f;       // ... so that p = 1 enters as 2^12 and at most 2^15
 constexpr uint32_t kBadPartial = 0x7fc0bad1u;  // L of a partial result of a rejected sequence
 constexpr int kScaleStages = 3;
 
@@ -91,8 +92,7 @@ struct Dec8Misc {
     uint32_t tmem;
     int abort;
     int bad[2];                     // per query buffer: the segment met a page out of range
-    long long g0, g1, g_b;          // this CTA's tiles; tiles before sequence b0
-    int b0;
+    int b, item, t, nt, left;       // where this CTA's tiles begin, and their number
     alignas(16) float k_scale[kScaleStages][kTile];
     alignas(16) float v_scale[kScaleStages][kTile];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
@@ -217,13 +217,38 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return h;
 }
 // (h - c) * 16 on f16 pairs: exact for the remainder of rounding h to c.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t remainder16(uint32_t h, uint32_t c) {
     uint32_t r;
-    asm("{\n\t.reg .b32 m, k;\n\tmov.b32 k, 0x4c004c00;\n\tsub.rn.f16x2 m, %1, %2;\n\t"
-        "mul.rn.f16x2 %0, m, k;\n\t}"
-        : "=r"(r)
-        : "r"(h), "r"(c));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(sub_f16x2(h, c)), "r"(0x4c004c00u));
     return r;
+}
+// e5m2 of two f16 values, to nearest even.
+__device__ __forceinline__ uint32_t e5m2x2_of(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+
+// The sum over the warp of eight values per lane: every lane gets that of value
+// (lane >> 2) & 7, with 9 shuffles: each exchange halves the values a lane keeps.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+    float x[4], y[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = (b4 ? v[i + 4] : v[i]) + __shfl_xor_sync(kFull, b4 ? v[i] : v[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        y[i] = (b3 ? x[i + 2] : x[i]) + __shfl_xor_sync(kFull, b3 ? x[i] : x[i + 2], 8);
+    float z = (b2 ? y[1] : y[0]) + __shfl_xor_sync(kFull, b2 ? y[0] : y[1], 4);
+    z += __shfl_xor_sync(kFull, z, 2);
+    z += __shfl_xor_sync(kFull, z, 1);
+    return z;
 }
 
 // (x0, x1) <- (x0, x1) * (a0, a1) - (c0, c1).
@@ -242,6 +267,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool co
 }
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -281,44 +310,34 @@ __device__ __forceinline__ int tiles_of(const Dec8Args &a, int b) {
     return len_ok(a, len) ? (int)(((long long)len + kTile - 1) / kTile) : 0;
 }
 
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {  // inclusive
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += y;
-    }
-    return v;
-}
-
-// Tiles of all sequences (of one warp's call): total, and those before sequence `upto`.
-__device__ __forceinline__ long long count_tiles(const Dec8Args &a, int upto, long long *before) {
+// Tiles (of one head and row block) of all sequences, and of those before `upto`; one warp.
+__device__ __forceinline__ int count_tiles(const Dec8Args &a, int upto, int *before) {
     const int lane = threadIdx.x & 31;
-    long long all = 0, pre = 0;
+    int all = 0, pre = 0;
     for (int b = lane; b < a.B; b += 32) {
-        const long long t = tiles_of(a, b);
+        const int t = tiles_of(a, b);
         all += t;
         if (b < upto) pre += t;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(kFull, all, o);
-        pre += __shfl_xor_sync(kFull, pre, o);
-    }
-    *before = pre;
-    return all;
+    *before = __reduce_add_sync(kFull, pre);
+    return __reduce_add_sync(kFull, all);
 }
 
-// CTA c of n takes tiles [total * c / n, total * (c + 1) / n), n at most the tiles there are,
-// so that every one of the n has some.
-__device__ __forceinline__ int busy_ctas(long long total, int n_cta) {
-    return (int)(total < n_cta ? total : n_cta);
-}
-__device__ __forceinline__ long long first_tile(long long total, int c, int n) {
-    return c < n ? total * c / n : total;
-}
-__device__ __forceinline__ int cta_of(long long total, long long g, int n) {
-    return (int)(((g + 1) * n - 1) / total);
-}
+// An even cut of `total` tiles over the n CTAs that get any: the first `more` of them take
+// one tile more than the others.
+struct Cut {
+    int n, each, more;
+    __device__ __forceinline__ Cut(int total, int n_cta) {
+        n = min(total, n_cta);
+        each = n ? total / n : 0;
+        more = total - each * n;
+    }
+    __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(int g) const {  // the CTA of tile g
+        const int big = more * (each + 1);
+        return g < big ? g / (each + 1) : more + (g - big) / each;
+    }
+};
 
 // A run of tiles of one item within this CTA's range.  Every role walks the same segments.
 struct Segment {
@@ -326,8 +345,7 @@ struct Segment {
     int t0, t1, nt;   // tiles [t0, t1) of the item's nt
 };
 struct Walk {
-    long long left;
-    int b, item, t, nt;
+    int left, b, item, t, nt;
     __device__ __forceinline__ bool next(const Dec8Args &a, Segment *s) {
         if (left <= 0) return false;
         while (t >= nt) {  // the next item that has tiles
@@ -340,15 +358,50 @@ struct Walk {
         }
         s->b = b;
         s->kvh = item / a.row_blocks;
-        s->rb = item % a.row_blocks;
+        s->rb = item - s->kvh * a.row_blocks;
         s->t0 = t;
-        s->t1 = (int)(left < nt - t ? t + left : nt);
+        s->t1 = min(nt, t + left);
         s->nt = nt;
         left -= s->t1 - t;
         t = s->t1;
         return true;
     }
 };
+
+// Where CTA c of n_cta begins; one warp.
+__device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta) {
+    const int lane = threadIdx.x & 31, ipb = a.Hkv * a.row_blocks;
+    Walk w{0, 0, 0, 0, 0};
+    // the first 32 sequences' tiles stay in a register: most batches are no larger
+    const int nt0 = lane < a.B ? tiles_of(a, lane) : 0;
+    int mine = nt0;
+    for (int b = lane + 32; b < a.B; b += 32) mine += tiles_of(a, b);
+    const Cut cut(__reduce_add_sync(kFull, mine) * ipb, n_cta);
+    if (c >= cut.n) return w;
+    int g = cut.first(c);
+    w.left = cut.first(c + 1) - g;
+    for (int b = 0; b < a.B; b += 32) {
+        const int nt = b == 0 ? nt0 : b + lane < a.B ? tiles_of(a, b + lane) : 0;
+        int incl = nt * ipb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const unsigned m = __ballot_sync(kFull, incl > g);
+        if (m) {
+            const int k = __ffs(m) - 1;
+            w.b = b + k;
+            w.nt = __shfl_sync(kFull, nt, k);
+            g -= __shfl_sync(kFull, incl, k) - w.nt * ipb;
+            w.item = g / w.nt;
+            w.t = g - w.item * w.nt;
+            break;
+        }
+        g -= __shfl_sync(kFull, incl, 31);
+    }
+    return w;
+}
 
 // ---------------------------------------------------------------- the kernel
 
@@ -376,7 +429,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             mbar_init(bar(ms.empty[s]), 1);
         }
         for (int u = 0; u < 2; ++u) {
-            mbar_init(bar(ms.q_full[u]), 32);
+            mbar_init(bar(ms.q_full[u]), 4 * NWG);
             mbar_init(bar(ms.q_empty[u]), 1 + NWG);  // the MMAs that read it, the warpgroups
             mbar_init(bar(ms.s_full[u]), 1);
             mbar_init(bar(ms.p_full[u]), 4 * NWG);   // one arrival per softmax warp
@@ -398,38 +451,59 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         tma_prefetch_desc(&a.tm_k);
         tma_prefetch_desc(&a.tm_v);
     }
-    if (warp == kAuxWarp) {
-        // this CTA's range of tiles, and the sequence it begins in
-        long long pre;
-        const long long ipb = (long long)a.Hkv * a.row_blocks;
-        const long long total = count_tiles(a, 0, &pre) * ipb;
-        const int n = busy_ctas(total, gridDim.x);
-        const long long g0 = first_tile(total, blockIdx.x, n);
-        const long long g1 = first_tile(total, blockIdx.x + 1, n);
-        long long run = 0;
-        for (int b = 0; b < a.B; b += 32) {
-            const long long mine = b + lane < a.B ? tiles_of(a, b + lane) * ipb : 0;
-            const long long incl = run + warp_scan(mine, lane);
-            const unsigned m = __ballot_sync(kFull, incl > g0);
-            if (m || b + 32 >= a.B) {
-                const int k = m ? __ffs(m) - 1 : 31;
-                if (lane == k) {
-                    ms.b0 = min(b + lane, a.B - 1);
-                    ms.g_b = incl - mine;
-                    ms.g0 = g0;
-                    ms.g1 = g1;
-                }
-                break;
-            }
-            run = __shfl_sync(kFull, incl, 31);
+    // The two warps that fetch page numbers find the CTA's first tile themselves and have its
+    // pages under way before the barrier; the others read the result.
+    Walk walk{0, 0, 0, 0, 0};
+    Segment s{};
+    bool some = false;      // s is the CTA's first segment
+    int pg[4], len = 0;     // page numbers of this lane's boxes or keys of a tile; s's length
+    const int *bt = nullptr;
+    const int per_tile = kTile / a.box;
+    auto open = [&] {
+        len = a.seq_lens[s.b];
+        bt = a.block_table + (size_t)s.b * a.max_pages;
+    };
+    // pages of boxes lane, lane + 32, ... of tile t (-1: no such box, or behind the last key)
+    auto look_boxes = [&](int t, int (&pg)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int bx = lane + 32 * i;
+            const long long key = (long long)t * kTile + (long long)bx * a.box;
+            pg[i] = -1;
+            if (bx < per_tile && t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
         }
-        if (blockIdx.x == 0) {
-            bool ok = true;
-            for (int b = lane; b < a.B; b += 32) ok = ok && len_ok(a, a.seq_lens[b]);
-            if (!__all_sync(kFull, ok) && lane == 0) {
-                atomicCAS(a.status + 1, 0, SITE_DEC8_BAD_LEN);
-                atomicExch(a.status, FA_ERR_BAD_INDEX);
-            }
+    };
+    // pages of keys lane, lane + 32, ... of tile t (0 behind the last key)
+    auto look_keys = [&](int t, int (&pg)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long key = (long long)t * kTile + lane + 32 * i;
+            pg[i] = 0;
+            if (t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
+        }
+    };
+    if (warp == kTmaWarp || warp == kAuxWarp) {
+        walk = start_walk(a, blockIdx.x, gridDim.x);
+        if (warp == kTmaWarp && lane == 0) {
+            ms.b = walk.b;
+            ms.item = walk.item;
+            ms.t = walk.t;
+            ms.nt = walk.nt;
+            ms.left = walk.left;
+        }
+        some = walk.next(a, &s);
+        if (some) {
+            open();
+            if (warp == kTmaWarp) look_boxes(s.t0, pg);
+            else look_keys(s.t0, pg);
+        }
+    }
+    if (warp == kMmaWarp && blockIdx.x == 0) {
+        bool ok = true;
+        for (int b = lane; b < a.B; b += 32) ok = ok && len_ok(a, a.seq_lens[b]);
+        if (!__all_sync(kFull, ok) && lane == 0) {
+            atomicCAS(a.status + 1, 0, SITE_DEC8_BAD_LEN);
+            atomicExch(a.status, FA_ERR_BAD_INDEX);
         }
     }
     tc_fence_before();
@@ -437,13 +511,80 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     tc_fence_after();
     const uint32_t tmem = ms.tmem;
     const Guard g{a.status, &ms.abort, a.limit_ns};
-    Walk walk;
-    walk.left = ms.g1 - ms.g0;
-    walk.b = ms.b0;
-    walk.nt = walk.left > 0 ? tiles_of(a, walk.b) : 0;
-    walk.item = walk.left > 0 ? (int)((ms.g0 - ms.g_b) / walk.nt) : 0;
-    walk.t = walk.left > 0 ? (int)((ms.g0 - ms.g_b) % walk.nt) : 0;
-    Segment s;
+    if (warp != kTmaWarp && warp != kAuxWarp) walk = Walk{ms.left, ms.b, ms.item, ms.t, ms.nt};
+
+    // Query terms of rows r, r + step, ... (N of them) of segment s into buffer qb, one warp.
+    // A row is scaled by the power of two that brings its largest magnitude into [128, 256);
+    // a row with a NaN or an infinity becomes NaN.
+    auto put_queries = [&](auto count, int qb, int len, int r_first, int step) {
+        constexpr int N = decltype(count)::value, W = NCH == 2 ? 4 : 2;
+        const int E = a.d == 96 ? 4 : a.d / 32;  // elements per lane
+        const bool on = lane * E < a.d;
+        const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
+        const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
+        uint32_t w[N][W];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int r = r_first + e * step;
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[e][i] = 0u;
+            if (r < rows && on) {
+                const __nv_bfloat16 *p = a.q + (row0 + r) * a.d + lane * E;
+                if constexpr (NCH == 2) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                    w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
+                } else if (E == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                    w[e][0] = x.x; w[e][1] = x.y;
+                } else {
+                    w[e][0] = *reinterpret_cast<const uint32_t *>(p);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int r = r_first + e * step;
+            uint32_t am = 0;
+#pragma unroll
+            for (int i = 0; i < W; ++i) am = max(am, max(w[e][i] & 0x7fffu, (w[e][i] >> 16) & 0x7fffu));
+            am = __reduce_max_sync(kFull, am);
+            const uint32_t ex = max((int)(am >> 7) - 7, 1);
+            const float inv = __uint_as_float((254u - ex) << 23);
+            uint32_t c1[W / 2], c2[W / 2];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                // 8 significant bits fit f16, and so do both remainders
+                uint32_t h = pack_f16(__uint_as_float(w[e][i] << 16) * inv,
+                                      __uint_as_float(w[e][i] & 0xffff0000u) * inv);
+                if (am >= 0x7f80u) h = 0x7fff7fffu;
+                const uint32_t c = e4m3x2_of(h);
+                const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
+                c1[i / 2] = i % 2 ? c1[i / 2] | c << 16 : c;
+                c2[i / 2] = i % 2 ? c2[i / 2] | d << 16 : d;
+            }
+            if (on) {
+                const int n1 = r / RW * (2 * RW) + r % RW;
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) {
+                    const int col = lane * E + 4 * i;  // byte of the row
+                    const uint32_t q0 = sQ + qb * T::Q_BYTES + (col >> 7) * T::Q_CHUNK;
+                    const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + RW, col & 127);
+                    if (NCH == 1 && E == 2) {
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a1), "h"((uint16_t)c1[i]) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a2), "h"((uint16_t)c2[i]) : "memory");
+                    } else {
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a1), "r"(c1[i]) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a2), "r"(c2[i]) : "memory");
+                    }
+                }
+            }
+            if (lane == 0) {
+                ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
+                ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
+            }
+        }
+    };
+    constexpr int kQueryRows = RB / (4 * NWG);  // rows per softmax warp
 
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA producer
@@ -451,26 +592,16 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         // power of two that divides the page size, so a box never straddles two pages); lane i
         // looks up and copies boxes i, i + 32, ...  Boxes behind the last key are not copied.
         // Page numbers are fetched one tile ahead and looked at only when they are used.
-        const int per_tile = kTile / a.box;
         uint32_t n = 0;  // ring slots used so far
         bool ok = true;
-        while (ok && walk.next(a, &s)) {
-            const int len = a.seq_lens[s.b];
-            const int *bt = a.block_table + (size_t)s.b * a.max_pages;
-            auto look = [&](int t, int (&pg)[4]) {  // pages of this lane's boxes of tile t
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int bx = lane + 32 * i;
-                    const long long key = (long long)t * kTile + (long long)bx * a.box;
-                    pg[i] = -1;
-                    if (bx < per_tile && t < s.t1 && key < len)
-                        pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
-                }
-            };
-            int pg[4], pg_next[4];
-            look(s.t0, pg);
+        int pg_next[4];
+        for (bool first = true; ok && some; first = false, some = walk.next(a, &s)) {
+            if (!first) {
+                open();
+                look_boxes(s.t0, pg);
+            }
             for (int t = s.t0; ok && t < s.t1; ++t) {
-                look(t + 1, pg_next);
+                look_boxes(t + 1, pg_next);
                 int mine = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mine += pg[i] >= 0 && pg[i] < a.num_pages ? 1 : 0;
@@ -516,7 +647,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescS = idesc_e4m3_f32(128, T::NS);
-        constexpr uint32_t kIdescO = idesc_e4m3_f32(128, T::NP) | (3u << 15);  // both MN-major
+        constexpr uint32_t kIdescO = idesc_e4m3_f32(128, T::NP) | (1u << 10) | (3u << 15);  // B e5m2; both MN-major
         const int ksteps = a.d / 32;
         Walk ahead = walk;   // segments of S, up to two tiles ahead of O
         Segment sa;
@@ -582,105 +713,31 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
     } else if (warp == kAuxWarp) {
         // ------------------------------------------- query terms, key and value scales
-        const int E = a.d == 96 ? 4 : a.d / 32;  // elements of a query row per lane
-        const bool on = lane * E < a.d;
+        // Query terms of the segments after the first (whose rows the softmax warps, idle then,
+        // share out), and for every tile the scales of its keys, in asynchronous copies.
         uint32_t seg = 0, j = 0;
         bool ok = true;
-        while (ok && walk.next(a, &s)) {
+        int pg_next[4];
+        for (; ok && some; ++seg, some = walk.next(a, &s)) {
             const int qb = seg & 1;
-            ok = seg < 2 || mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
-            if (!ok) break;
-            const int len = a.seq_lens[s.b];
-            const int *bt = a.block_table + (size_t)s.b * a.max_pages;
-            // lane i has keys i, i + 32, ... of a tile; pages are fetched one tile ahead
-            auto look = [&](int t, int (&pg)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long key = (long long)t * kTile + lane + 32 * i;
-                    pg[i] = 0;
-                    if (t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
-                }
-            };
-            int pg[4], pg_next[4];
-            look(s.t0, pg);
-            const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
-            const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
-            const uint32_t sq = sQ + qb * T::Q_BYTES;
+            if (seg >= 1) {
+                open();
+                look_keys(s.t0, pg);
+                if (seg >= 2)
+                    ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+                if (!ok) break;
+            }
             if (lane == 0) ms.bad[qb] = 0;
             __syncwarp();
+            if (seg >= 1) {
 #pragma unroll 1
-            for (int r8 = 0; r8 < RB; r8 += 8) {
-                uint32_t w[8][NCH == 2 ? 4 : 2];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    w[e][0] = w[e][1] = 0u;
-                    if constexpr (NCH == 2) w[e][2] = w[e][3] = 0u;
-                    if (r8 + e < rows && on) {
-                        const __nv_bfloat16 *p = a.q + (row0 + r8 + e) * a.d + lane * E;
-                        if constexpr (NCH == 2) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(p);
-                            w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
-                        } else if (E == 4) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-                            w[e][0] = x.x; w[e][1] = x.y;
-                        } else {
-                            w[e][0] = *reinterpret_cast<const uint32_t *>(p);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = r8 + e;
-                    uint32_t am = 0;
-#pragma unroll
-                    for (int i = 0; i < (NCH == 2 ? 4 : 2); ++i)
-                        am = max(am, max(w[e][i] & 0x7fffu, (w[e][i] >> 16) & 0x7fffu));
-                    am = __reduce_max_sync(kFull, am);
-                    // row scale 2^(e - 7) of the largest magnitude's exponent e; a row with a
-                    // NaN or an infinity becomes NaN
-                    const uint32_t ex = max((int)(am >> 7) - 7, 1);
-                    const float inv = __uint_as_float((254u - ex) << 23);
-                    const bool finite = am < 0x7f80u;
-#pragma unroll
-                    for (int i = 0; i < (NCH == 2 ? 4 : 2); i += 2) {
-                        // 8 significant bits fit f16, and so do both remainders
-                        uint32_t h[2], c1 = 0, c2 = 0;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t u = w[e][i + k];
-                            h[k] = pack_f16(__uint_as_float(u << 16) * inv,
-                                            __uint_as_float(u & 0xffff0000u) * inv);
-                            if (!finite) h[k] = 0x7fff7fffu;
-                            const uint32_t c = e4m3x2_of(h[k]);
-                            c1 |= c << (16 * k);
-                            c2 |= e4m3x2_of(remainder16(h[k], f16x2_of(c))) << (16 * k);
-                        }
-                        if (on) {
-                            const int col = lane * E + 2 * i;  // byte of the row
-                            const uint32_t q0 = sq + (col >> 7) * T::Q_CHUNK;
-                            const int n1 = r / RW * (2 * RW) + r % RW;
-                            const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + RW, col & 127);
-                            if (NCH == 1 && E == 2) {
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(a1), "h"((uint16_t)c1) : "memory");
-                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(a2), "h"((uint16_t)c2) : "memory");
-                            } else {
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(a1), "r"(c1) : "memory");
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(a2), "r"(c2) : "memory");
-                            }
-                        }
-                    }
-                    if (lane == e) {
-                        ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
-                        ms.limit[qb][r] = a.causal && r < rows
-                                              ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
-                    }
-                }
+                for (int r = 0; r < RB; r += 4) put_queries(std::integral_constant<int, 4>(), qb, len, r, 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(bar(ms.q_full[qb]), 4 * NWG);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(bar(ms.q_full[qb]));
-            ++seg;
             for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
-                look(t + 1, pg_next);
+                look_keys(t + 1, pg_next);
                 const int st = (int)(j % kScaleStages);
                 ok = j < kScaleStages || mbar_wait_warp(bar(ms.scale_empty[st]), ((j / kScaleStages) - 1) & 1,
                                                         g, SITE_DEC_EMPTY);
@@ -722,6 +779,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             const int len = a.seq_lens[s.b];
             const int r0 = s.rb * RB + rw0, rows = min(RW, a.R - r0);  // may be none
             const int full_keys = a.causal ? len - a.Nq + 1 : len;     // keys that every row sees
+            if (seg == 0) {
+                put_queries(std::integral_constant<int, kQueryRows>(), 0, len, warp, 4 * NWG);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
+            }
             if (kk < RW) ms.mref[rw0 + kk] = kUnseen;
             if (kk == 0) ms.vref[wg] = 0.f;
 #pragma unroll
@@ -767,11 +830,15 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                             if (key >= ms.limit[qb][rw0 + r]) x[r] = -INFINITY;
                     }
                 };
-                scores(std::true_type());
-                float top = x[0];
+                bool move = t == s.t0;  // the first tile always sets them
+                if (!move) {
+                    scores(std::true_type());
+                    float top = x[0];
 #pragma unroll
-                for (int r = 1; r < RW; ++r) top = fmaxf(top, x[r]);
-                if (vote_group(id, top > kMoveLog2 || vs > ms.vref[wg])) {
+                    for (int r = 1; r < RW; ++r) top = fmaxf(top, x[r]);
+                    move = vote_group(id, top > kMoveLog2 || vs > ms.vref[wg]);
+                }
+                if (move) {
                     // new references: the tile's maximum where it passes the old one by 2^3
                     scores(std::false_type());
 #pragma unroll
@@ -788,7 +855,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     float v_new = v_old;
                     if (vm > v_old)  // the power of two at or above, and kOneP / v_new stays finite
                         v_new = fmaxf(__uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u),
-                                      0x1p-120f);
+                                      0x1p-110f);
                     if (kk < RW) {
                         const int r = rw0 + kk;
                         const float m_old = ms.mref[r];
@@ -839,14 +906,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         h[k] = pack_f16(pa, pb);
                     }
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        const uint32_t ca = e4m3x2_of(h[0]), cb = e4m3x2_of(h[1]);
-                        term[e][r / 4] = ca | cb << 16;
-                        if (e < 2) {
-                            h[0] = remainder16(h[0], f16x2_of(ca));
-                            h[1] = remainder16(h[1], f16x2_of(cb));
-                        }
+                    for (int e = 0; e < 2; ++e) {  // the upper bytes, and what they leave
+                        term[e][r / 4] = __byte_perm(h[0], h[1], 0x7531);
+                        h[0] = sub_f16x2(h[0], h[0] & 0xff00ff00u);
+                        h[1] = sub_f16x2(h[1], h[1] & 0xff00ff00u);
                     }
+                    term[2][r / 4] = e5m2x2_of(h[0]) | e5m2x2_of(h[1]) << 16;
                 }
                 if (j >= 2)  // the P buffer's last reader
                     mbar_wait_warp(bar(ms.pv_done[u]), ((j >> 1) - 1) & 1, g, SITE_DEC_MMA);
@@ -881,37 +946,43 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             // ---- the segment's rows: sums over all keys, then O^T columns
             const uint32_t jl = j - 1;
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                float v = l[r];
+            for (int q = 0; q < RW; q += 8) {
+                float v[8];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-                if (lane == r) ms.part[w4][rw0 + r] = v;
+                for (int e = 0; e < 8; ++e) v[e] = l[q + e];
+                const float sum = warp_sum8(v, lane);
+                if ((lane & 3) == 0) ms.part[w4][rw0 + q + (lane >> 2)] = sum;
             }
-            mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
-            tc_fence_after();
             named_barrier_sync(id, 128);
             const bool whole = s.t0 == 0 && s.t1 == s.nt;
             const bool bad = ms.bad[qb] != 0;
             const bool dead = *g.abort != 0;
             const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * RB + rw0;
             const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
-            const float ov = ms.vref[wg] * (1.f / kOneP);
             if (bad && threadIdx.x == 0) {
                 atomicCAS(a.status + 1, 0, SITE_DEC8_BAD_PAGE);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
             }
-            if (kk < rows && !dead) {
+            if (kk < RW) {
                 const int r = rw0 + kk;
                 const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
                 const float l2 = sum == 0.f ? -INFINITY : ms.mref[r] + lg2(sum);  // base 2
-                if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
-                else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
+                ms.alpha[r] = sum == 0.f ? 0.f : ms.vref[wg] * (1.f / kOneP) / sum;
+                if (kk < rows && !dead) {
+                    if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
+                    else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
+                }
             }
+            mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
+            tc_fence_after();
+            named_barrier_sync(id, 128);
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c) {
                 const int dd = c * 128 + kk;
+                __nv_bfloat16 *o_out = a.o + row0 * a.d + dd;
+                float *p_out = a.part_o + prow * a.d + dd;
 #pragma unroll 1
-                for (int q = 0; q < RW; q += 8) {
+                for (int q = 0; q < RW && q < rows; q += 8) {
                     float o0[8], o1[8], o2[8];
                     __syncwarp();
                     const uint32_t at = t_o + c * T::NP + q;
@@ -925,13 +996,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             if (q + e < rows) {
-                                const int r = rw0 + q + e;
-                                const float sum =
-                                    (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
-                                const float inv = sum == 0.f ? 0.f : ov / sum;
-                                const float o = fmaf(fmaf(o2[e], 0.0625f, o1[e]), 0.0625f, o0[e]) * inv;
-                                if (whole) a.o[(row0 + q + e) * a.d + dd] = __float2bfloat16(o);
-                                else a.part_o[(prow + q + e) * a.d + dd] = o;
+                                const float o = (o0[e] + (o1[e] + o2[e])) * ms.alpha[rw0 + q + e];
+                                if (whole) o_out[(q + e) * a.d] = __float2bfloat16(o);
+                                else p_out[(q + e) * a.d] = o;
                             }
                         }
                     }
@@ -954,85 +1021,78 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 }
 
 // Merge of the partial results of the items that were cut: L = log2 sum 2^(L_s),
-// O = sum 2^(L_s - L) O_s.  A CTA has four query rows; its warps find one row's partials each,
-// then all of them take every fourth partial of every row (a long sequence alone in the
-// launch is cut into dozens) and add up through shared memory.  Bound by latency: two rounds
-// of loads.  Rows of empty sequences are written here.
-constexpr int kMergeRows = 4;
-template <int NCH, int RB>
-__global__ void __launch_bounds__(32 * kMergeRows)
+// O = sum 2^(L_s - L) O_s.  A CTA has ROWS query rows and WARPS warps; each row's partials are
+// shared out to all warps (a long sequence alone in the launch is cut into dozens), four loads
+// of each in flight, and the warps' sums meet in shared memory.  Bound by latency: one row per
+// CTA and eight warps to it where that fills no more than the GPU, else four rows per CTA,
+// most of which have nothing to merge.  Rows of empty sequences are written here.
+template <int NCH, int RB, int ROWS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
     fa_decode8_merge_kernel(const __grid_constant__ Dec8Args a, int n_cta, long long n_rows) {
     constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
-    __shared__ float s_acc[kMergeRows][kMergeRows][E * 32], s_sum[kMergeRows][kMergeRows], s_max[kMergeRows];
-    __shared__ int s_c0[kMergeRows], s_n[kMergeRows], s_r[kMergeRows];
+    static_assert(ROWS <= WARPS, "a warp finishes a row");
+    __shared__ float s_acc[ROWS][WARPS][E * 32], s_sum[ROWS][WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = (long long)blockIdx.x * kMergeRows + warp;
-    int n = 0;  // partials of this warp's row
-    bool empty = false;
-    int c0 = 0, r = 0;
-    if (row < n_rows) {
+    // every warp looks up every row of its CTA: the rows are few and the loads the same
+    int c0[ROWS], n[ROWS], rr[ROWS];
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        const long long row = (long long)blockIdx.x * ROWS + q;
+        c0[q] = n[q] = rr[q] = 0;
+        if (row >= n_rows) continue;
         const int i = (int)(row % a.Nq);
-        const long long bh = row / a.Nq;
-        const int b = (int)(bh / a.H), h = (int)(bh % a.H), group = a.H / a.Hkv;
+        const int bh = (int)(row / a.Nq);
+        const int b = bh / a.H, h = bh % a.H, group = a.H / a.Hkv;
         const int len = a.seq_lens[b];
-        const long long ipb = (long long)a.Hkv * a.row_blocks;
-        long long before;
-        const long long total = count_tiles(a, b, &before) * ipb;
-        empty = len == 0;
-        if (len_ok(a, len) && !empty) {
-            r = (h % group) * a.Nq + i;
+        int before;
+        const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
+        if (len == 0) {
+            n[q] = -1;
+        } else if (len_ok(a, len)) {
+            rr[q] = (h % group) * a.Nq + i;
             const int nt = tiles_of(a, b);
-            const long long first =
-                before * ipb + ((long long)(h / group) * a.row_blocks + r / RB) * nt;
-            const int busy = busy_ctas(total, n_cta);
-            c0 = cta_of(total, first, busy);
-            n = cta_of(total, first + nt - 1, busy) - c0 + 1;
-            if (n == 1) n = 0;  // written directly
+            const int first = before * a.Hkv * a.row_blocks + (h / group * a.row_blocks + rr[q] / RB) * nt;
+            c0[q] = cut.owner(first);
+            n[q] = cut.owner(first + nt - 1) - c0[q] + 1;
+            if (n[q] == 1) n[q] = 0;  // written directly
         }
+        any = any || n[q] != 0;
     }
     griddep_wait();  // every partial result is written
-    if (empty) {
-        __nv_bfloat16 *o = a.o + row * a.d;
-        for (int c = lane; c < a.d; c += 32) o[c] = __float2bfloat16(0.f);
-        if (lane == 0) a.lse[row] = -INFINITY;
-    }
-    auto prow = [&](int k, int c_first, int rr) {
-        return ((size_t)(c_first + k) * 2 + (k == 0 ? 1 : 0)) * RB + rr % RB;
-    };
-    if (n) {
+    if (!any) return;
+    float top[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+        top[q] = 0.f;
+        if (n[q] <= 0) continue;
+        auto prow = [&](int k) {
+            return ((size_t)(c0[q] + k) * 2 + (k == 0 ? 1 : 0)) * RB + rr[q] % RB;
+        };
         float m = -INFINITY;
         bool bad = false;
-        for (int k = lane; k < n; k += 32) {
-            const float x = __ldcg(a.part_l + prow(k, c0, r));
+        for (int k = lane; k < n[q]; k += 32) {
+            const float x = __ldcg(a.part_l + prow(k));
             bad = bad || __float_as_uint(x) == kBadPartial;
             m = fmaxf(m, x);
         }
         m = warp_max(m);
-        if (__any_sync(kFull, bad)) n = 0;
-        if (lane == 0) s_max[warp] = m == -INFINITY ? 0.f : m;  // a row without keys: weights 0
-    }
-    if (lane == 0) {
-        s_c0[warp] = c0;
-        s_n[warp] = n;
-        s_r[warp] = r;
-    }
-    if (!__syncthreads_or(n)) return;
-#pragma unroll 1
-    for (int q = 0; q < kMergeRows; ++q) {
-        const int nq = s_n[q], cq = s_c0[q], rq = s_r[q];
-        if (nq == 0) continue;
-        const float m = s_max[q];
+        top[q] = m == -INFINITY ? 0.f : m;  // a row without keys: weights 0
+        if (__any_sync(kFull, bad)) {
+            n[q] = 0;
+            continue;
+        }
         float acc[E], wsum = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         constexpr int U = 4;  // partials in flight per warp
-        for (int k0 = warp; k0 < nq; k0 += kMergeRows * U) {
+        for (int k0 = warp; k0 < n[q]; k0 += WARPS * U) {
             float w[U], x[U][E];
 #pragma unroll
             for (int v = 0; v < U; ++v) {
-                const int k = k0 + kMergeRows * v;
-                const bool in = k < nq;
-                const size_t pr = prow(in ? k : k0, cq, rq);
+                const int k = k0 + WARPS * v;
+                const bool in = k < n[q];
+                const size_t pr = prow(in ? k : k0);
                 w[v] = in ? __ldcg(a.part_l + pr) : -INFINITY;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
@@ -1040,7 +1100,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
             }
 #pragma unroll
             for (int v = 0; v < U; ++v) {
-                const float wk = ex2(w[v] - m);
+                const float wk = ex2(w[v] - top[q]);
                 wsum += wk;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[v][e], acc[e]);
@@ -1051,22 +1111,29 @@ __global__ void __launch_bounds__(32 * kMergeRows)
         if (lane == 0) s_sum[q][warp] = wsum;
     }
     __syncthreads();
-    if (n == 0) return;
-    float wsum = 0.f, acc[E];
+    if (warp >= ROWS) return;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int q = 0; q < ROWS; ++q) {
+        if (q != warp || n[q] == 0) continue;
+        const long long row = (long long)blockIdx.x * ROWS + q;
+        float wsum = 0.f, acc[E];
 #pragma unroll
-    for (int v = 0; v < kMergeRows; ++v) {
-        wsum += s_sum[warp][v];
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        if (n[q] > 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += s_acc[warp][v][lane + 32 * e];
+            for (int v = 0; v < WARPS; ++v) {
+                wsum += s_sum[q][v];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += s_acc[q][v][lane + 32 * e];
+            }
+        }
+        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+        __nv_bfloat16 *o = a.o + row * a.d;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
+        if (lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (top[q] + lg2(wsum)) * kLn2;
     }
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    __nv_bfloat16 *o = a.o + row * a.d;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
-    if (lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (s_max[warp] + lg2(wsum)) * kLn2;
 }
 
 // CTAs of a launch: all that are resident, or the largest number of tiles there can be.
@@ -1129,17 +1196,18 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // a programmatic dependent: launched as the last CTAs start, it waits for the whole grid
     const long long rows = (long long)p.B * p.H * p.Nq;
+    const bool few = rows <= 8LL * p.num_sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows));
-    cfg.blockDim = dim3(32 * kMergeRows);
+    cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 3) / 4));
+    cfg.blockDim = dim3(few ? 256 : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fa_decode8_merge_kernel<NCH, RB>, a, n_cta, rows) != cudaSuccess)
-        return FA_ERR_CUDA;
+    auto merge = few ? fa_decode8_merge_kernel<NCH, RB, 1, 8> : fa_decode8_merge_kernel<NCH, RB, 4, 4>;
+    if (cudaLaunchKernelEx(&cfg, merge, a, n_cta, rows) != cudaSuccess) return FA_ERR_CUDA;
     return FA_OK;
 }
 
@@ -1164,6 +1232,15 @@ int decode8_box_rows(int page_size) {
     int box = 1;
     while (box < kTile && page_size % (2 * box) == 0) box *= 2;
     return box;
+}
+
+long long decode8_max_tiles(const Decode8Params &p) {
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    return with_tile(p.d, R, [&](auto, auto rb) {
+        const long long nt = ((long long)p.page_size * p.max_pages + kTile - 1) / kTile;
+        const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
+        return items >= (1LL << 31) ? items : items * nt;
+    });
 }
 
 size_t decode8_workspace_bytes(const Decode8Params &p) {

@@ -229,6 +229,8 @@ struct Decode8Params {
     int num_sms;
 };
 int decode8_box_rows(int page_size);
+// Tiles of 128 keys of all items at the longest possible lengths; the kernels count in ints.
+long long decode8_max_tiles(const Decode8Params &p);
 size_t decode8_workspace_bytes(const Decode8Params &p);  // of its sizes and num_sms
 int launch_decode8(const Decode8Params &p, cudaStream_t stream);
 
