@@ -16,7 +16,7 @@
 //   p, fp32, times its key's value scale, is rounded to f16 and split into three e5m2 terms:
 //   e5m2 is f16's upper byte, so the first two are byte selections and the remainders exact
 //   subtractions; the third is rounded to nearest.  Relative error 2^-9 (bf16's), and with
-//   p = 1 entering as 2^12 nothing is lost in e5m2's smallest step above 2^-29.
+//   p = 1 entering as 2^12 at most 2^-25 of the largest is lost in e5m2's smallest step.
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
@@ -97,7 +97,7 @@ struct Dec8Misc {
     alignas(16) float v_scale[kScaleStages][kTile];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
     alignas(16) int limit[2][RB];        // keys the row sees
-    alignas(16) float mref[RB];          // reference of the row's scores, base 2
+    alignas(16) float nref[RB];          // minus the reference of the row's scores, base 2
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
     float vref[NWG];                // power of two that the value scales are taken relative to
@@ -251,12 +251,12 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
     return z;
 }
 
-// (x0, x1) <- (x0, x1) * (a0, a1) - (c0, c1).
-__device__ __forceinline__ void fms_f32x2(float &x0, float &x1, float a0, float a1, float c0, float c1) {
+// (x0, x1) <- (x0, x1) * (a0, a1) + (c0, c1).
+__device__ __forceinline__ void fma_pairs(float &x0, float &x1, float a0, float a1, float c0, float c1) {
     asm("{\n\t.reg .b64 x, a, c;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\t"
         "mov.b64 c, {%4, %5};\n\tfma.rn.f32x2 x, x, a, c;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(x0), "+f"(x1)
-        : "f"(a0), "f"(a1), "f"(-c0), "f"(-c1));
+        : "f"(a0), "f"(a1), "f"(c0), "f"(c1));
 }
 
 // 4-byte asynchronous copy global -> shared, or 4 zero bytes; the thread's earlier ones
@@ -467,19 +467,20 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     auto look_boxes = [&](int t, int (&pg)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int bx = lane + 32 * i;
-            const long long key = (long long)t * kTile + (long long)bx * a.box;
             pg[i] = -1;
-            if (bx < per_tile && t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
+            if (32 * i >= per_tile) continue;
+            const int bx = lane + 32 * i;
+            const uint32_t key = (uint32_t)t * kTile + (uint32_t)(bx * a.box);
+            if (bx < per_tile && t < s.t1 && key < (uint32_t)len) pg[i] = __ldg(bt + a.by_page.div(key));
         }
     };
     // pages of keys lane, lane + 32, ... of tile t (0 behind the last key)
     auto look_keys = [&](int t, int (&pg)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const long long key = (long long)t * kTile + lane + 32 * i;
+            const uint32_t key = (uint32_t)t * kTile + (uint32_t)(lane + 32 * i);
             pg[i] = 0;
-            if (t < s.t1 && key < len) pg[i] = __ldg(bt + a.by_page.div((uint32_t)key));
+            if (t < s.t1 && key < (uint32_t)len) pg[i] = __ldg(bt + a.by_page.div(key));
         }
     };
     if (warp == kTmaWarp || warp == kAuxWarp) {
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (pg[i] < 0 || pg[i] >= a.num_pages) continue;
+                        if (32 * i >= per_tile || pg[i] < 0 || pg[i] >= a.num_pages) continue;
                         const int row = (lane + 32 * i) * a.box;
                         const uint32_t key = (uint32_t)(t * kTile + row);
                         const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
             }
-            if (kk < RW) ms.mref[rw0 + kk] = kUnseen;
+            if (kk < RW) ms.nref[rw0 + kk] = -kUnseen;
             if (kk == 0) ms.vref[wg] = 0.f;
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
@@ -795,9 +796,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 const int u = j & 1;
                 const int key = t * kTile + kk;
                 const int st = (int)(j % kScaleStages);
-                mbar_wait_warp(bar(ms.scale_full[st]), (j / kScaleStages) & 1, g, SITE_DEC_FULL);
+                mbar_wait(bar(ms.scale_full[st]), (j / kScaleStages) & 1, g, SITE_DEC_FULL);
                 const float ks = ms.k_scale[st][kk], vs = ms.v_scale[st][kk];
-                mbar_wait_warp(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
+                mbar_wait(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
+                __syncwarp();
                 tc_fence_after();
                 const bool partly = (t + 1) * (long long)kTile > full_keys;  // some row sees less
                 // base-2 exponents of the rows' scores of this thread's key; with REF less the
@@ -816,13 +818,13 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         float f[4] = {rs.x, rs.y, rs.z, rs.w};
                         float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
                         if constexpr (decltype(ref)::value)
-                            m = *reinterpret_cast<const float4 *>(&ms.mref[rw0 + r]);
+                            m = *reinterpret_cast<const float4 *>(&ms.nref[rw0 + r]);
                         mul_f32x2(f[0], f[1], ks2);
                         mul_f32x2(f[2], f[3], ks2);
                         fma_f32x2(x[r], x[r + 1], k16, c1[r], c1[r + 1]);
                         fma_f32x2(x[r + 2], x[r + 3], k16, c1[r + 2], c1[r + 3]);
-                        fms_f32x2(x[r], x[r + 1], f[0], f[1], m.x, m.y);
-                        fms_f32x2(x[r + 2], x[r + 3], f[2], f[3], m.z, m.w);
+                        fma_pairs(x[r], x[r + 1], f[0], f[1], m.x, m.y);
+                        fma_pairs(x[r + 2], x[r + 3], f[2], f[3], m.z, m.w);
                     }
                     if (partly) {
 #pragma unroll
@@ -833,9 +835,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 bool move = t == s.t0;  // the first tile always sets them
                 if (!move) {
                     scores(std::true_type());
-                    float top = x[0];
+                    float top = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int r = 1; r < RW; ++r) top = fmaxf(top, x[r]);
+                    for (int r = 2; r < RW; r += 2) top = fmax3(top, x[r], x[r + 1]);
                     move = vote_group(id, top > kMoveLog2 || vs > ms.vref[wg]);
                 }
                 if (move) {
@@ -853,24 +855,25 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     const float vm = fmaxf(fmaxf(ms.vpart[wg][0], ms.vpart[wg][1]),
                                            fmaxf(ms.vpart[wg][2], ms.vpart[wg][3]));
                     float v_new = v_old;
-                    if (vm > v_old)  // the power of two at or above, and kOneP / v_new stays finite
-                        v_new = fmaxf(__uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u),
-                                      0x1p-110f);
+                    // a power of two 8 to 16 times the largest scale, so that it seldom moves
+                    // again (p's terms have the room), and kOneP / v_new stays finite
+                    if (vm > v_old)
+                        v_new = fmaxf(__uint_as_float(__float_as_uint(vm) & 0x7f800000u) * 16.f, 0x1p-110f);
                     if (kk < RW) {
                         const int r = rw0 + kk;
-                        const float m_old = ms.mref[r];
+                        const float m_old = -ms.nref[r];
                         const float m = fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]),
                                               fmaxf(ms.part[2][r], ms.part[3][r]));
                         const bool up = m > m_old + kMoveLog2;
                         ms.alpha[r] = up ? ex2(m_old - m) : 1.f;
-                        if (up) ms.mref[r] = m;
+                        if (up) ms.nref[r] = -m;
                     }
                     if (kk == 0) ms.vref[wg] = v_new;
                     named_barrier_sync(id, 128);
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
                         l[r] *= ms.alpha[rw0 + r];
-                        x[r] -= ms.mref[rw0 + r];
+                        x[r] += ms.nref[rw0 + r];
                     }
                     if (t > s.t0) {  // O^T to the new references, once PV of the tile before is done
                         const float fo = v_new > 0.f ? v_old / v_new : 1.f;
@@ -913,8 +916,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     }
                     term[2][r / 4] = e5m2x2_of(h[0]) | e5m2x2_of(h[1]) << 16;
                 }
-                if (j >= 2)  // the P buffer's last reader
-                    mbar_wait_warp(bar(ms.pv_done[u]), ((j >> 1) - 1) & 1, g, SITE_DEC_MMA);
+                // the buffer's last reader, PV of tile j - 2, was issued before S of this tile, whose
+                // commit covers all that was issued before it
                 const uint32_t p0 = sP + u * T::P_BYTES;
                 if constexpr (RW == 8) {
                     sts128(p_addr(p0, T::P_CHUNK, 0, kk), term[0][0], term[0][1], term[1][0], term[1][1]);
@@ -966,7 +969,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             if (kk < RW) {
                 const int r = rw0 + kk;
                 const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
-                const float l2 = sum == 0.f ? -INFINITY : ms.mref[r] + lg2(sum);  // base 2
+                const float l2 = sum == 0.f ? -INFINITY : lg2(sum) - ms.nref[r];  // base 2
                 ms.alpha[r] = sum == 0.f ? 0.f : ms.vref[wg] * (1.f / kOneP) / sum;
                 if (kk < rows && !dead) {
                     if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
