@@ -15,12 +15,12 @@
 //   2^-22 of it below.
 //   p, fp32, times its key's value scale, is rounded to f16 and split into three e5m2 terms:
 //   e5m2 is f16's upper byte, so the first two are byte selections and the remainders exact
-//   subtractions; the third is rounded to nearest.  Relative error 2^-9 (bf16's), and with
-//   p = 1 entering as 2^12 at most 2^-25 of the largest is lost in e5m2's smallest step.
+//   subtractions; the third is rounded to nearest.  Relative error 2^-9 (bf16's), and at most
+//   2^-22 of the row's largest where the terms run into e5m2's smallest step, 2^-16.
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
-// reference by 2^3 (then P would leave e5m2's range): the softmax warps vote once per tile,
+// reference by 2^6 (then P would leave e5m2's range): the softmax warps vote once per tile,
 // and only a tile that does pass takes the maximum and rescales O^T.  A thread's terms of one
 // key are contiguous in P (MN-major, like V), so they leave in 16-byte stores.
 //
@@ -46,8 +46,12 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kTile = 128;             // keys per tile: the M of S^T and the K of O^T
 constexpr float kUnseen = -3.0e38f;    // reference of a row that has seen no key yet
-constexpr float kMoveLog2 = 3.0f;      // the reference moves when a score passes it by 2^3 ...
-constexpr float kOneP = 4096.0f;       // ... so that p = 1 enters as 2^12 and at most 2^15
+// e5m2 reaches from 2^-16 to 57344, and p times the value scale is placed in it so that neither
+// reference moves often: the rows' references move when a score passes them by 2^6, the value
+// scales' (first 8 to 16 times the largest) when a scale passes it, and p = 2^6 at the reference
+// scale is 2^15.  A threshold of 2^3 moved in one of three tiles of the Nq4 Hkv4 d64 batch.
+constexpr float kMoveLog2 = 6.0f;
+constexpr float kOneP = 512.0f;        // p = 1 at the reference scale
 constexpr uint32_t kBadPartial = 0x7fc0bad1u;  // L of a partial result of a rejected sequence
 constexpr int kScaleStages = 3;
 
@@ -159,10 +163,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[16]) {
           "=f"(r[14]), "=f"(r[15])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
                  : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]),
+        "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+        : "memory");
 }
 // Wait for this thread's tcgen05.ld; the registers are tied to the wait.
 __device__ __forceinline__ void tmem_wait(float (&r)[8]) {
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     move = vote_group(id, top > kMoveLog2 || vs > ms.vref[wg]);
                 }
                 if (move) {
-                    // new references: the tile's maximum where it passes the old one by 2^3
+                    // new references: the tile's maximum where it passes the old one by 2^6
                     scores(std::false_type());
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -882,14 +894,14 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 #pragma unroll 1
                         for (int c = 0; c < NCH; ++c)
 #pragma unroll 1
-                            for (int n = 0; n < 3 * RW; n += 8) {
-                                float o[8];
+                            for (int n = 0; n < 3 * RW; n += RW) {
+                                float o[RW];
                                 const uint32_t at = t_o + c * T::NP + n;
                                 tmem_ld(at, o);
                                 tmem_wait(o);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] *= ms.alpha[rw0 + n % RW + e] * fo;
-                                tmem_st8(at, o);
+                                for (int e = 0; e < RW; ++e) o[e] *= ms.alpha[rw0 + e] * fo;
+                                tmem_st(at, o);
                             }
                         tmem_wait_st();
                     }

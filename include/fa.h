@@ -439,7 +439,7 @@ int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cac
  * their codes are, with one exception: among the last Nq keys of a causal call, a NaN code
  * of V reaches also the rows that do not see it.  A NaN or infinity in a query makes its row NaN.
  * Rounding: q's 8 significant bits are kept, probabilities enter the product with V with a
- * relative error of at most 2^-9 (absolute 2^-25 of the row's largest), sums are fp32.
+ * relative error of at most 2^-9 (absolute 2^-22 of the row's largest), sums are fp32.
  *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, and
  *            B * Hkv * ceil((H / Hkv) * Nq / 8) * ceil(page_size * max_pages_per_seq / 128)
  *            < 2^31 (FA_ERR_INVALID_ARG where it overflows).
