@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
@@ -38,6 +40,7 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_status_string", "f
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
 _LIB = None
+_NATIVE = None
 
 
 class FaError(RuntimeError):
@@ -118,6 +121,20 @@ def load() -> ctypes.CDLL:
         lib.fa_copy_pages.restype = _int
         _LIB = lib
     return _LIB
+
+
+def native():
+    """The CPython extension that makes the paged-cache calls on tensors (raises if it has
+    not been built)."""
+    global _NATIVE
+    if _NATIVE is None:
+        load()
+        if not os.path.exists(_build.EXT):
+            raise RuntimeError(f"{_build.EXT} is missing: build it first (__graft_entry__.build())")
+        loader = importlib.machinery.ExtensionFileLoader("_fa_torch", _build.EXT)
+        spec = importlib.util.spec_from_file_location("_fa_torch", _build.EXT, loader=loader)
+        _NATIVE = importlib.util.module_from_spec(spec)
+    return _NATIVE
 
 
 # ------------------------------------------------------------ raw C-ABI calls
@@ -725,6 +742,20 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
     return out, lse
 
 
+# The calls on a paged e4m3 cache are made many times per decode step on kernels of a few
+# microseconds, so the extension makes them: it answers with the outputs, with a status, or
+# with None when an argument is not as expected.  What follows it here names the argument
+# that is wrong (and serves the calls the extension leaves alone, tensor subclasses).
+
+def _raw(stream, t):
+    return None if stream is None else _stream(t, stream)
+
+
+def _ok(status, where):
+    if status != FA_OK:
+        raise FaError(status, where)
+
+
 def _cache8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, di):
     """Checks of a paged e4m3 cache and its table on device `di`; returns (B, num_pages, Hkv,
     page_size, d, max_pages, scale_group)."""
@@ -769,6 +800,10 @@ def append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     one new token each).  The cache is uint8 codes [num_pages, Hkv, page_size, d] and fp32
     scales [num_pages, Hkv, page_size / group] for k and for v, changed in place; seq_lens is
     not changed.  Returns None."""
+    r = native().append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                  cu_seqlens, _raw(stream, k))
+    if r is not None:
+        return _ok(r, "fa_append_paged_fp8")
     di = k_cache.get_device() if isinstance(k_cache, torch.Tensor) else -1
     B, num_pages, Hkv, page_size, d, max_pages, group = _cache8(k_cache, v_cache, k_scale, v_scale,
                                                                 block_table, seq_lens, di)
@@ -788,8 +823,7 @@ def append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                                  k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
                                  seq_lens.data_ptr(), cu, B, T, Hkv, d, page_size, max_pages,
                                  num_pages, group, ks, vs, _stream(k, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_append_paged_fp8")
+    _ok(rc, "fa_append_paged_fp8")
 
 
 def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, causal=False,
@@ -799,6 +833,12 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     group]; block_table int32 [B, max_pages]; seq_lens int32 [B], 0 allowed.  causal: the Nq
     queries are the sequence's last tokens, each sees the keys up to its own.  Rows that see
     no key get o = 0 and lse = -inf.  Returns (o, lse)."""
+    r = native().decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, causal,
+                                  scale, out, lse, workspace, _raw(stream, q))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_decode_paged_fp8")
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, Nq, d]")
@@ -830,8 +870,7 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
                                  seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
                                  d, page_size, max_pages, num_pages, group, causal, scale,
                                  workspace.data_ptr(), workspace.numel(), _stream(q, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_decode_paged_fp8")
+    _ok(rc, "fa_decode_paged_fp8")
     return out, lse
 
 
@@ -850,14 +889,18 @@ def _int32(shape, like):
 def free_pages(block_table, seq_lens, page_size, num_pages, stream=None):
     """The pages of a paged cache that no sequence uses: (pages int32 [num_pages], ascending,
     then -1; count int32 [1])."""
+    r = native().free_pages(block_table, seq_lens, page_size, num_pages, _raw(stream, block_table))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_free_pages")
     di, B, max_pages = _table(block_table, seq_lens)
     pages, count = _int32(max(int(num_pages), 0), block_table), _int32(1, block_table)
     with _device(di):
         rc = fa_free_pages(block_table.data_ptr(), seq_lens.data_ptr(), pages.data_ptr(),
                            count.data_ptr(), B, max_pages, int(page_size), int(num_pages),
                            _stream(block_table, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_free_pages")
+    _ok(rc, "fa_free_pages")
     return pages, count
 
 
@@ -866,6 +909,12 @@ def fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages, stre
     parents' full pages, and child i takes page fresh[i] (int32 [n]) for a copy of a last page
     that is not full.  Returns (rows int32 [n, max_pages], lens [n], src [n], dst [n]): the
     children's table rows and lengths, and the pages to pass to copy_pages (-1: none)."""
+    r = native().fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages,
+                            _raw(stream, block_table))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_fork_pages")
     di, B, max_pages = _table(block_table, seq_lens)
     _check("parents", parents, torch.int32, dev=di)
     if parents.dim() != 1:
@@ -878,8 +927,7 @@ def fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages, stre
                            fresh.data_ptr(), rows.data_ptr(), lens.data_ptr(), src.data_ptr(),
                            dst.data_ptr(), B, n, max_pages, int(page_size), int(num_pages),
                            _stream(block_table, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_fork_pages")
+    _ok(rc, "fa_fork_pages")
     return rows, lens, src, dst
 
 
@@ -887,6 +935,11 @@ def compact_pages(block_table, seq_lens, page_size, num_pages, stream=None):
     """Plan that packs the n pages in use into pages 0 .. n-1: (table int32 [B, max_pages] after
     the moves, src, dst int32 [max(1, num_pages // 2)] ending in -1, counts int32 [2] = n and
     the number of moves).  copy_pages(caches, src, dst, count=counts[1:]) makes the moves."""
+    r = native().compact_pages(block_table, seq_lens, page_size, num_pages, _raw(stream, block_table))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_compact_pages")
     di, B, max_pages = _table(block_table, seq_lens)
     cap = max(1, int(num_pages) // 2)
     table, src, dst, counts = (_int32(s, block_table) for s in ((B, max_pages), cap, cap, 2))
@@ -894,8 +947,7 @@ def compact_pages(block_table, seq_lens, page_size, num_pages, stream=None):
         rc = fa_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), table.data_ptr(),
                               src.data_ptr(), dst.data_ptr(), counts.data_ptr(), B, max_pages,
                               int(page_size), int(num_pages), _stream(block_table, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_compact_pages")
+    _ok(rc, "fa_compact_pages")
     return table, src, dst, counts
 
 
@@ -907,7 +959,10 @@ def copy_pages(caches, src, dst, count=None, stream=None):
     dimension num_pages: codes and scales, any number of layers up to 128 tensors) onto its page
     dst[i], for every pair of int32 [n] src, dst with src[i] != -1; with `count` (int32 [1]) only
     the first count pairs.  No page may be a destination twice, or destination and source."""
-    caches = list(caches)
+    caches = caches if isinstance(caches, list) else list(caches)
+    r = native().copy_pages(caches, src, dst, count, _raw(stream, src))
+    if r is not None:
+        return _ok(r, "fa_copy_pages")
     if not 1 <= len(caches) <= FA_MAX_COPY_CACHES:
         raise ValueError(f"caches must be 1 to {FA_MAX_COPY_CACHES} tensors")
     di = src.get_device() if isinstance(src, torch.Tensor) else -1
@@ -932,5 +987,4 @@ def copy_pages(caches, src, dst, count=None, stream=None):
         rc = fa_copy_pages(ptrs, sizes, len(caches), num_pages, src.data_ptr(), dst.data_ptr(),
                            src.shape[0], None if count is None else count.data_ptr(),
                            _stream(src, stream))
-    if rc != FA_OK:
-        raise FaError(rc, "fa_copy_pages")
+    _ok(rc, "fa_copy_pages")
