@@ -22,13 +22,15 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 //
 // A group's new codes need the group's largest magnitude first, so its rows are held in
 // registers between the maximum and the conversion and read once: 2 bytes in, 1 byte out
-// per element, bound by HBM.  A team of W warps owns one (group, head, key or value); warp
-// w of it takes rows w, w + W, ... (at most 16 of them), a lane E consecutive elements.
-// Teams are handed out by windows of `window` consecutive rows of the call: a team walks
-// the groups that begin in its window, which needs no list of the groups (their number is
-// only known on the device).  The host sets the window to about the rows a group gets, so a
+// per element, bound by HBM.  A team of W warps works on one (group, head, key or value) at a
+// time; warp w of it takes rows w, w + W, ... (at most 16 of them), a lane E consecutive
+// elements.  Teams are handed out by windows of `window` consecutive rows of the call: a team
+// walks the groups that begin in its window, which needs no list of the groups (their number
+// is only known on the device).  The host sets the window to about the rows a group gets, so a
 // window holds about one group whether the call stores prompts or one token per sequence.
-
+// Finding a group takes a chain of dependent loads (offsets, length, page).  A large call would
+// pay it in every wave of CTAs, so there a team does `jobs` heads of a group in turn, the rows of
+// the next under way while one is converted; a small call gives every head its own team.
 template <int D>
 struct RowLanes {
     static constexpr int E = (D == 96) ? 4 : D / 32;  // d = 96: 24 lanes of 4
@@ -103,6 +105,11 @@ __device__ __forceinline__ float least_scale(uint32_t amax) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
+// A scale that was there, rounded up to a power of two (what this kernel stores is one already).
+__device__ __forceinline__ float up_to_pow2(float s) {
+    return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
+}
+
 template <int D, int W>
 __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
     using L = RowLanes<D>;
@@ -113,15 +120,11 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
     const int team = warp / W, w = warp % W;
     const bool on = lane < L::LANES;
     // heads fastest: the CTAs that run together read whole rows of the call
-    const int job_ctas = (2 * p.Hkv + TEAMS - 1) / TEAMS;
-    const int job = (int)(blockIdx.x % job_ctas) * TEAMS + team;  // (head, key or value)
-    if (job >= 2 * p.Hkv) return;
-    const int h = job >> 1;
-    const bool is_v = job & 1;
-    const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(is_v ? p.v : p.k);
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    uint8_t *cache = is_v ? p.v_cache : p.k_cache;
-    float *scales = is_v ? p.v_scale : p.k_scale;
+    const int all_jobs = 2 * p.Hkv;  // job 2 h: keys of head h, 2 h + 1: values
+    const int per_cta = TEAMS * p.jobs, job_ctas = (all_jobs + per_cta - 1) / per_cta;
+    const int job0 = (int)(blockIdx.x % job_ctas) * per_cta + team;  // then every TEAMS-th
+    if (job0 >= all_jobs) return;
+    const bool reports = blockIdx.x % job_ctas == 0 && team == 0 && w == 0 && lane == 0;
     const int G = p.group, ps = p.page_size, groups = ps / G;
 
     int t = (int)(blockIdx.x / job_ctas) * p.window;
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             n = min(step, n - k * step);
         }
         b = lo;
-        if (blockIdx.x == 0 && job == 0 && w == 0) {
+        if (blockIdx.x == 0 && team == 0 && w == 0) {
             bool ok = true;  // the offsets, checked once per call
             for (int i = lane; i < p.B; i += 32) {
                 const int c0 = p.cu_seqlens[i], c1 = p.cu_seqlens[i + 1];
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
         const int start = p.seq_lens[b];
         const long long room = (long long)ps * p.max_pages;
         if (start < 0 || start + (long long)(c1 - c0) > room) {
-            if (job == 0 && w == 0 && lane == 0) flag_index(p.status, SITE_APPEND_BAD_SEQ);
+            if (reports) flag_index(p.status, SITE_APPEND_BAD_SEQ);
             t = c1;
             continue;
         }
@@ -179,77 +182,90 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             continue;
         }
         const int page = p.block_table[(size_t)b * p.max_pages + pos / ps];
+        const int g = pos % ps / G;
+        // the team's rows of one job; `next` is loaded while the one before is converted
+        auto load = [&](int job, uint32_t (&u)[kRowsPerWarp][L::WORDS]) {
+            const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(job & 1 ? p.v : p.k) +
+                                     (long long)t * (job & 1 ? p.v_stride : p.k_stride) +
+                                     (long long)(job >> 1) * D + lane * E;
+            const long long stride = job & 1 ? p.v_stride : p.k_stride;
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i) {
+                const int r = w + i * W;
+                if (r < cnt && on) {
+                    load_bf16<D>(x + r * stride, u[i]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < L::WORDS; ++e) u[i][e] = 0u;
+                }
+            }
+        };
+        uint32_t next[kRowsPerWarp][L::WORDS];
+        load(job0, next);
         if (page < 0 || page >= p.num_pages) {
-            if (job == 0 && w == 0 && lane == 0) flag_index(p.status, SITE_APPEND_BAD_PAGE);
+            if (reports) flag_index(p.status, SITE_APPEND_BAD_PAGE);
             t += cnt;
             continue;
         }
-        const size_t ph = (size_t)page * p.Hkv + h;
-        const int g = pos % ps / G;
-        float *sc = scales + ph * groups + g;
-        uint8_t *rows = cache + (ph * ps + (size_t)g * G) * D + lane * E;  // of the group
-
-        uint32_t u[kRowsPerWarp][L::WORDS];
-        uint32_t amax = 0;
+#pragma unroll 1
+        for (int job = job0; job < all_jobs && job < job0 + per_cta; job += TEAMS) {
+            const size_t ph = (size_t)page * p.Hkv + (job >> 1);
+            float *sc = (job & 1 ? p.v_scale : p.k_scale) + ph * groups + g;
+            uint8_t *rows = (job & 1 ? p.v_cache : p.k_cache) + (ph * ps + (size_t)g * G) * D + lane * E;
+            const float old = in_group ? *sc : 0.f;
+            uint32_t u[kRowsPerWarp][L::WORDS];
+            uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int r = w + i * W;
-            if (r < cnt && on) {
-                load_bf16<D>(x + (size_t)(t + r) * stride + (size_t)h * D + lane * E, u[i]);
-            } else {
+            for (int i = 0; i < kRowsPerWarp; ++i)
 #pragma unroll
-                for (int e = 0; e < L::WORDS; ++e) u[i][e] = 0u;
+                for (int e = 0; e < L::WORDS; ++e) {
+                    u[i][e] = next[i][e];
+                    amax = max(amax, amax_bits(u[i][e]));
+                }
+            if (job + TEAMS < all_jobs && job + TEAMS < job0 + per_cta) load(job + TEAMS, next);
+            amax = __reduce_max_sync(kFull, amax);
+            if constexpr (W > 1) {
+                if (lane == 0) s_amax[team][w] = amax;
+                named_barrier_sync(1 + team, 32 * W);
+#pragma unroll
+                for (int i = 0; i < W; ++i) amax = max(amax, s_amax[team][i]);
+                named_barrier_sync(1 + team, 32 * W);  // everyone has read before the next job's
             }
-        }
-        const float old = in_group ? *sc : 0.f;
+            const float s = fmaxf(least_scale(amax), up_to_pow2(old));
+            if (in_group && s > old) {  // the codes that were there, at the larger scale
+                const float ratio = old / s;
+                for (int r = w; r < in_group; r += W) {
+                    if (on) {
+                        uint32_t c[CW];
+                        load_codes<E>(rows + (size_t)r * D, c);
+                        float y[E];
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i)
+                        for (int e = 0; e < E; ++e) y[e] = e4m3_float(c[e / 4] >> (8 * (e % 4))) * ratio;
+                        encode<E>(y, c);
+                        store_codes<E>(rows + (size_t)r * D, c);
+                    }
+                }
+            }
+            const float inv = 1.f / s;  // exact, and so is f * inv
 #pragma unroll
-            for (int e = 0; e < L::WORDS; ++e) amax = max(amax, amax_bits(u[i][e]));
-        amax = __reduce_max_sync(kFull, amax);
-        if constexpr (W > 1) {
-            if (lane == 0) s_amax[team][w] = amax;
-            named_barrier_sync(1 + team, 32 * W);
-#pragma unroll
-            for (int i = 0; i < W; ++i) amax = max(amax, s_amax[team][i]);
-            named_barrier_sync(1 + team, 32 * W);  // everyone has read before the next group's
-        }
-        const float least = least_scale(amax);
-        const float s = fmaxf(least, old);
-        if (in_group && s > old) {  // the codes that were there, at the larger scale
-            const float ratio = old / s;
-            for (int r = w; r < in_group; r += W) {
-                if (on) {
-                    uint32_t c[CW];
-                    load_codes<E>(rows + (size_t)r * D, c);
+            for (int i = 0; i < kRowsPerWarp; ++i) {
+                const int r = w + i * W;
+                if (r < cnt && on) {
                     float y[E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) y[e] = e4m3_float(c[e / 4] >> (8 * (e % 4))) * ratio;
+                    for (int e = 0; e < E; ++e) {
+                        const uint32_t q = u[i][e / 2];
+                        const float f = __uint_as_float(e % 2 ? (q & 0xffff0000u) : (q << 16));
+                        // f * 0 is NaN where f is NaN or infinite, and adds nothing elsewhere
+                        y[e] = __fmaf_rn(f, 0.f, f * inv);
+                    }
+                    uint32_t c[CW];
                     encode<E>(y, c);
-                    store_codes<E>(rows + (size_t)r * D, c);
+                    store_codes<E>(rows + (size_t)(in_group + r) * D, c);
                 }
             }
+            if (w == 0 && lane == 0) *sc = s;
         }
-        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-        const float inv = 1.f / s;
-#pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int r = w + i * W;
-            if (r < cnt && on) {
-                float y[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const uint32_t q = u[i][e / 2];
-                    const float f = __uint_as_float(e % 2 ? (q & 0xffff0000u) : (q << 16));
-                    // f * 0 is NaN where f is NaN or infinite, and adds nothing elsewhere
-                    y[e] = __fmaf_rn(f, 0.f, pow2 ? f * inv : __fdiv_rn(f, s));
-                }
-                uint32_t c[CW];
-                encode<E>(y, c);
-                store_codes<E>(rows + (size_t)(in_group + r) * D, c);
-            }
-        }
-        if (w == 0 && lane == 0) *sc = s;
         t += cnt;
     }
 }
@@ -257,9 +273,15 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
 template <int D, int W>
 int launch_append_t(const AppendParams &p, cudaStream_t stream) {
     constexpr int TEAMS = kAppendThreads / 32 / W;
-    const long long ctas = (2LL * p.Hkv + TEAMS - 1) / TEAMS * ((p.T - 1LL) / p.window + 1);
+    const long long windows = (p.T - 1LL) / p.window + 1;
+    AppendParams q = p;
+    // one head per team while the teams fit the GPU at once (16 warps per SM), then 2 and 4
+    q.jobs = 1;
+    while (q.jobs < 4 && windows * 2 * p.Hkv * W > (long long)p.num_sms * 16 * q.jobs) q.jobs *= 2;
+    const long long per_cta = (long long)TEAMS * q.jobs;
+    const long long ctas = (2LL * p.Hkv + per_cta - 1) / per_cta * windows;
     if (ctas >= (1LL << 31)) return FA_ERR_INVALID_ARG;
-    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(p);
+    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(q);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -314,14 +336,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     Bitmap bm{cg::this_cluster(), plan_smem, plan_smem + per_cta, per_cta};
     const int rank = (int)bm.cluster.block_rank();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long entries = (long long)p.B * p.max_pages;
-    const long long first = (long long)rank * kPlanThreads + tid;
-    constexpr long long kStep = (long long)kPlanCtas * kPlanThreads;
+    const uint32_t entries = (uint32_t)p.B * (uint32_t)p.max_pages;  // below 2^31
+    const uint32_t first = (uint32_t)rank * kPlanThreads + tid;
+    constexpr uint32_t kStep = kPlanCtas * kPlanThreads;
 
     for (int i = tid; i < per_cta; i += kPlanThreads) bm.words[i] = 0u;
     bm.cluster.sync();
-    for (long long i = first; i < entries; i += kStep) {
-        const int b = (int)(i / p.max_pages), col = (int)(i % p.max_pages);
+    for (uint32_t i = first; i < entries; i += kStep) {
+        const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
         bool bad;
         const int need = used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad);
         if (bad && col == 0) flag_index(p.status, SITE_PAGES_BAD_LEN);
@@ -378,7 +400,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             if (page < p.num_pages && !((bits >> lane) & 1u))
                 p.pages[page - (int)bm.before[i] - __popc(bits & ((1u << lane) - 1u))] = page;
         }
-        for (long long i = n_free + first; i < p.num_pages; i += kStep) p.pages[i] = -1;
+        for (uint32_t i = n_free + first; i < (uint32_t)p.num_pages; i += kStep) p.pages[i] = -1;
         if (first == 0) p.counts[0] = n_free;
     } else {
         bool live;
@@ -392,15 +414,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             if (page < n_live && !in_use) p.dst[page - r] = page;
             if (page >= n_live && page < p.num_pages && in_use) p.src[r - below] = page;
         }
-        for (long long i = moves + first; i < p.cap; i += kStep) p.src[i] = p.dst[i] = -1;
+        for (uint32_t i = moves + first; i < (uint32_t)p.cap; i += kStep) p.src[i] = p.dst[i] = -1;
         if (first == 0) {
             p.counts[0] = n_live;
             p.counts[1] = moves;
         }
         __threadfence();
         bm.cluster.sync();  // dst is complete
-        for (long long i = first; i < entries; i += kStep) {
-            const int b = (int)(i / p.max_pages), col = (int)(i % p.max_pages);
+        for (uint32_t i = first; i < entries; i += kStep) {
+            const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
             bool bad;
             int page = p.block_table[i];
             if (page >= n_live && page < p.num_pages &&

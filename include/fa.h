@@ -401,9 +401,9 @@ size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int
  * changed).  Per group and head that gets new tokens:
  *   least = the smallest power of two s >= 2^-126 with |x| <= 448 s for the group's finite
  *           new elements x;
- *   scale = least in a group that held no token, else max(least, its scale so far), and
- *           where that is larger than before, the codes that were there are rounded again,
- *           e4m3(value(code) * old / new);
+ *   scale = least in a group that held no token, else max(least, its scale so far rounded up
+ *           to a power of two), and where that is larger than before, the codes that were
+ *           there are rounded again, e4m3(value(code) * old / new);
  *   code  = e4m3(x / scale), to nearest even; a NaN or infinite x is stored as NaN and has
  *           no part in the scale.
  * Powers of two make x / scale exact and leave the second rounding exact too for every

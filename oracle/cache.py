@@ -21,6 +21,11 @@ def least_scale(amax: float) -> float:
     return s
 
 
+def pow2_at_least(x: float) -> float:
+    """The smallest power of two >= x (0 for 0)."""
+    return 0.0 if x == 0 else float(2.0 ** np.ceil(np.log2(x)))
+
+
 def encode(x) -> np.ndarray:
     """e4m3 codes of x: nearest even; NaN and infinities become the NaN code."""
     x = np.asarray(x, dtype=np.float64)
@@ -46,7 +51,7 @@ def append(x, codes, scale, table, lens, cu):
                 s = least_scale(float(fin.max()) if fin.size else 0.0)
                 if j % size:
                     old = float(scale[page, h, g])
-                    s = max(s, old)
+                    s = max(s, pow2_at_least(old))
                     if s > old:
                         r = slice(g * size, j % ps)
                         codes[page, h, r] = encode(e4m3_value(codes[page, h, r]) * (old / s))

@@ -103,7 +103,7 @@ def test_append_rows_outside_every_sequence(fa):
 
 
 def test_append_grown_scale_of_foreign_groups(fa):
-    """A group whose scale is no power of two keeps it while the new tokens fit."""
+    """A group whose scale is no power of two gets one, its older codes rounded again."""
     def edit(kc, vc, ks, vs, table):
         ks[:], vs[:] = 0.3, 1e-3
     _run(fa, _rows(20, 2, 128, 4), 2, 128, 16, 16, [5, 3], [10, 10], edit=edit)
