@@ -91,11 +91,22 @@ __device__ __forceinline__ void encode(const float (&y)[E], uint32_t (&c)[(E + 3
     }
 }
 
-// The largest finite magnitude of a word's two bf16 values, as its 15 bits (bf16
-// magnitudes order like the integers of their bits; 0x7f80 and up are not finite).
-__device__ __forceinline__ uint32_t amax_bits(uint32_t u) {
+// bf16 magnitudes order like the integers of their 15 bits; 0x7f80 and up are not finite.
+constexpr uint32_t kNotFinite = 0x7f80u;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The larger magnitudes of two words' halves, as bits.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t u) {
+    return max_u16x2(m, u & 0x7fff7fffu);
+}
+// The same without what is not finite.
+__device__ __forceinline__ uint32_t max_finite_bits(uint32_t m, uint32_t u) {
     const uint32_t a = u & 0x7fffu, b = (u >> 16) & 0x7fffu;
-    return max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u);
+    return max_u16x2(m, (a < kNotFinite ? a : 0u) | (b < kNotFinite ? b : 0u) << 16);
 }
 
 // The least power of two s >= 2^-126 with amax <= 448 s: amax = m 2^e, 448 = 1.75 * 2^8,
@@ -133,18 +144,19 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
     if (p.cu_seqlens == nullptr) {
         b = t;
     } else {
-        // the last b with cu[b] <= t (0 if there is none), by steps of 32 pivots
-        int lo = 0, n = p.B;
+        // the last b with cu[b] <= t (0 if there is none) among every 32nd, by steps of 32
+        // pivots; the walk finds it among the 32 from there, which it holds in registers
+        int lo = 0, n = (p.B + 31) / 32;
         while (n > 1) {
             const int step = (n + 31) / 32;
             const int i = lane * step;
-            const bool le = i < n && p.cu_seqlens[lo + i] <= t;
+            const bool le = i < n && p.cu_seqlens[(lo + i) * 32] <= t;
             const unsigned m = __ballot_sync(kFull, le);
             const int k = m ? 31 - __clz(m) : 0;
             lo += k * step;
             n = min(step, n - k * step);
         }
-        b = lo;
+        b = lo * 32;
         if (blockIdx.x == 0 && team == 0 && w == 0) {
             bool ok = true;  // the offsets, checked once per call
             for (int i = lane; i < p.B; i += 32) {
@@ -154,10 +166,27 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             if (!__all_sync(kFull, ok) && lane == 0) flag_index(p.status, SITE_APPEND_BAD_SEQ);
         }
     }
+    // lane i holds the offsets and length of sequence held + i
+    int held = b, my_c0 = 0, my_c1 = 0, my_len = 0;
+    auto hold = [&] {
+        held = b;
+        const int i = b + lane;
+        if (i < p.B) {
+            my_c0 = p.cu_seqlens ? p.cu_seqlens[i] : i;
+            my_c1 = p.cu_seqlens ? p.cu_seqlens[i + 1] : i + 1;
+            my_len = p.seq_lens[i];
+        }
+    };
+    hold();
+    if (p.cu_seqlens) {
+        const unsigned m = __ballot_sync(kFull, b + lane < p.B && my_c0 <= t);
+        if (m) b += 31 - __clz(m);
+    }
     // Walk the groups that begin at rows t .. t_end - 1 (all values are uniform over the team).
     while (t < t_end && b < p.B) {
-        const int c0 = p.cu_seqlens ? p.cu_seqlens[b] : b;
-        const int c1 = p.cu_seqlens ? p.cu_seqlens[b + 1] : b + 1;
+        if (b - held >= 32) hold();
+        const int c0 = __shfl_sync(kFull, my_c0, b - held), c1 = __shfl_sync(kFull, my_c1, b - held);
+        const int start = __shfl_sync(kFull, my_len, b - held);
         if (t >= c1) {  // an empty sequence, or the end of this one
             ++b;
             continue;
@@ -167,7 +196,6 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             t = c0;
             continue;
         }
-        const int start = p.seq_lens[b];
         const long long room = (long long)ps * p.max_pages;
         if (start < 0 || start + (long long)(c1 - c0) > room) {
             if (reports) flag_index(p.status, SITE_APPEND_BAD_SEQ);
@@ -188,17 +216,29 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(job & 1 ? p.v : p.k) +
                                      (long long)t * (job & 1 ? p.v_stride : p.k_stride) +
                                      (long long)(job >> 1) * D + lane * E;
-            const long long stride = job & 1 ? p.v_stride : p.k_stride;
+            const long long step = (long long)W * (job & 1 ? p.v_stride : p.k_stride);
+            x += w * (job & 1 ? p.v_stride : p.k_stride);
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i) {
-                const int r = w + i * W;
-                if (r < cnt && on) {
-                    load_bf16<D>(x + r * stride, u[i]);
+            for (int i = 0; i < kRowsPerWarp; ++i, x += step) {
+                if (w + i * W < cnt && on) {
+                    load_bf16<D>(x, u[i]);
                 } else {
 #pragma unroll
                     for (int e = 0; e < L::WORDS; ++e) u[i][e] = 0u;
                 }
             }
+        };
+        // the team's larger of a value per warp
+        auto team_max = [&](uint32_t m) {
+            m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+            if constexpr (W > 1) {
+                if (lane == 0) s_amax[team][w] = m;
+                named_barrier_sync(1 + team, 32 * W);
+#pragma unroll
+                for (int i = 0; i < W; ++i) m = max(m, s_amax[team][i]);
+                named_barrier_sync(1 + team, 32 * W);  // everyone has read before it is written again
+            }
+            return m;
         };
         uint32_t next[kRowsPerWarp][L::WORDS];
         load(job0, next);
@@ -214,22 +254,24 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             uint8_t *rows = (job & 1 ? p.v_cache : p.k_cache) + (ph * ps + (size_t)g * G) * D + lane * E;
             const float old = in_group ? *sc : 0.f;
             uint32_t u[kRowsPerWarp][L::WORDS];
-            uint32_t amax = 0;
+            uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < kRowsPerWarp; ++i)
 #pragma unroll
                 for (int e = 0; e < L::WORDS; ++e) {
                     u[i][e] = next[i][e];
-                    amax = max(amax, amax_bits(u[i][e]));
+                    m = max_bits(m, u[i][e]);
                 }
             if (job + TEAMS < all_jobs && job + TEAMS < job0 + per_cta) load(job + TEAMS, next);
-            amax = __reduce_max_sync(kFull, amax);
-            if constexpr (W > 1) {
-                if (lane == 0) s_amax[team][w] = amax;
-                named_barrier_sync(1 + team, 32 * W);
+            uint32_t amax = team_max(m);
+            const bool odd = amax >= kNotFinite;
+            if (odd) {  // something is not finite: the largest of the rest
+                m = 0;
 #pragma unroll
-                for (int i = 0; i < W; ++i) amax = max(amax, s_amax[team][i]);
-                named_barrier_sync(1 + team, 32 * W);  // everyone has read before the next job's
+                for (int i = 0; i < kRowsPerWarp; ++i)
+#pragma unroll
+                    for (int e = 0; e < L::WORDS; ++e) m = max_finite_bits(m, u[i][e]);
+                amax = team_max(m);
             }
             const float s = fmaxf(least_scale(amax), up_to_pow2(old));
             if (in_group && s > old) {  // the codes that were there, at the larger scale
@@ -246,22 +288,27 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
                     }
                 }
             }
-            const float inv = 1.f / s;  // exact, and so is f * inv
+            const uint64_t inv = f32x2_splat(1.f / s);  // exact, and so are the products
+            uint8_t *out = rows + (size_t)(in_group + w) * D;
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i) {
-                const int r = w + i * W;
-                if (r < cnt && on) {
+            for (int i = 0; i < kRowsPerWarp; ++i, out += W * D) {
+                if (w + i * W < cnt && on) {
                     float y[E];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint32_t q = u[i][e / 2];
-                        const float f = __uint_as_float(e % 2 ? (q & 0xffff0000u) : (q << 16));
-                        // f * 0 is NaN where f is NaN or infinite, and adds nothing elsewhere
-                        y[e] = __fmaf_rn(f, 0.f, f * inv);
+                    for (int e = 0; e < E; e += 2) {
+                        y[e] = __uint_as_float(u[i][e / 2] << 16);
+                        y[e + 1] = __uint_as_float(u[i][e / 2] & 0xffff0000u);
+                        mul_f32x2(y[e], y[e + 1], inv);
                     }
                     uint32_t c[CW];
                     encode<E>(y, c);
-                    store_codes<E>(rows + (size_t)(in_group + r) * D, c);
+                    if (odd) {  // an infinity is stored as NaN, not as the largest number
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (!(fabsf(y[e]) < INFINITY))
+                                c[e / 4] = (c[e / 4] & ~(0xffu << (8 * (e % 4)))) | 0x7fu << (8 * (e % 4));
+                    }
+                    store_codes<E>(out, c);
                 }
             }
             if (w == 0 && lane == 0) *sc = s;
@@ -299,60 +346,80 @@ int launch_append_d(const AppendParams &p, cudaStream_t stream) {
 // of CTAs does the whole plan in one launch with the bitmap in its shared memory: mark the
 // pages of the table (atomics on the owner's words through distributed shared memory),
 // count the bits of the words before each word, then write the lists.  A launch that is
-// bound by latency: four cluster barriers and two passes over the table.
+// bound by latency: barriers and two passes over the table.  A small table is done sooner by
+// one CTA, whose barriers are local (kOneCta below).
 
-constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
 
+template <int CTAS>
 struct Bitmap {
     cg::cluster_group cluster;
     uint32_t *words, *before;  // this CTA's part: bits, and bits set before the word (globally)
     int per_cta;               // words per CTA
 
-    __device__ uint32_t *remote(uint32_t *base, int word) {
-        return cluster.map_shared_rank(base, word / per_cta) + word % per_cta;
+    __device__ void sync() {
+        if constexpr (CTAS > 1) cluster.sync();
+        else __syncthreads();
     }
-    __device__ void set(int page) { atomicOr(remote(words, page >> 5), 1u << (page & 31)); }
-    // pages in use below `page`, and whether it is in use itself
-    __device__ int rank(int page, bool *live) {
+    __device__ uint32_t *at(uint32_t *base, int word) {
+        if constexpr (CTAS == 1) return base + word;
+        else return cluster.map_shared_rank(base, word / per_cta) + word % per_cta;
+    }
+    __device__ void set(int page) { atomicOr(at(words, page >> 5), 1u << (page & 31)); }
+    // pages in use below `page`
+    __device__ int rank(int page) {
         const int w = page >> 5;
-        const uint32_t bits = *remote(words, w);
-        *live = (bits >> (page & 31)) & 1u;
-        return (int)*remote(before, w) + __popc(bits & ((1u << (page & 31)) - 1u));
+        return (int)*at(before, w) + __popc(*at(words, w) & ((1u << (page & 31)) - 1u));
     }
 };
 
+// Table entries (and four per word of the bitmap) up to which one CTA does the plan.
+constexpr long long kOneCta = 5000;
+
 // Entries of a table row that are in use.
 __device__ __forceinline__ int used_entries(int len, int page_size, int max_pages, bool *bad) {
-    const int need = len <= 0 ? 0 : (int)(((long long)len + page_size - 1) / page_size);
+    const int need = len <= 0 ? 0 : (int)((uint32_t)(len - 1) / (uint32_t)page_size) + 1;
     *bad = len < 0 || need > max_pages;
     return min(need, max_pages);
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    fa_pages_kernel(const PagesParams p, int per_cta) {
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanThreads) fa_pages_kernel(const PagesParams p, int per_cta) {
     extern __shared__ uint32_t plan_smem[];
     __shared__ int s_total, s_warp[kPlanThreads / 32];
-    Bitmap bm{cg::this_cluster(), plan_smem, plan_smem + per_cta, per_cta};
-    const int rank = (int)bm.cluster.block_rank();
+    Bitmap<CTAS> bm{cg::this_cluster(), plan_smem, plan_smem + per_cta, per_cta};
+    const int rank = CTAS > 1 ? (int)bm.cluster.block_rank() : 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t entries = (uint32_t)p.B * (uint32_t)p.max_pages;  // below 2^31
     const uint32_t first = (uint32_t)rank * kPlanThreads + tid;
-    constexpr uint32_t kStep = kPlanCtas * kPlanThreads;
+    constexpr uint32_t kStep = CTAS * kPlanThreads;
+    constexpr int U = 4;  // entries whose loads a thread has in flight
 
     for (int i = tid; i < per_cta; i += kPlanThreads) bm.words[i] = 0u;
-    bm.cluster.sync();
-    for (uint32_t i = first; i < entries; i += kStep) {
-        const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
-        bool bad;
-        const int need = used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad);
-        if (bad && col == 0) flag_index(p.status, SITE_PAGES_BAD_LEN);
-        if (col >= need) continue;
-        const int page = p.block_table[i];
-        if (page >= 0 && page < p.num_pages) bm.set(page);
-        else flag_index(p.status, SITE_PAGES_BAD_PAGE);
+    bm.sync();
+    for (uint32_t i0 = first; i0 < entries; i0 += U * kStep) {
+        int page[U];
+        bool used[U];
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            const uint32_t i = i0 + v * kStep;
+            used[v] = false;
+            page[v] = 0;
+            if (i >= entries) continue;
+            const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
+            bool bad;
+            used[v] = col < used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad);
+            if (bad && col == 0) flag_index(p.status, SITE_PAGES_BAD_LEN);
+            page[v] = p.block_table[i];
+        }
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            if (!used[v]) continue;
+            if (page[v] >= 0 && page[v] < p.num_pages) bm.set(page[v]);
+            else flag_index(p.status, SITE_PAGES_BAD_PAGE);
+        }
     }
-    bm.cluster.sync();
+    bm.sync();
 
     // bits before each word: a thread's run of words, then the CTA's threads, then the CTAs
     const int run = (per_cta + kPlanThreads - 1) / kPlanThreads;
@@ -377,20 +444,22 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         s_warp[lane] = v;
         if (lane == 31) s_total = v;
     }
-    __syncthreads();
+    bm.sync();
     int base = incl - mine + (warp > 0 ? s_warp[warp - 1] : 0);
-    bm.cluster.sync();
-    int n_live = 0;
-    for (int r = 0; r < kPlanCtas; ++r) {
-        const int tot = *bm.cluster.map_shared_rank(&s_total, r);
-        if (r < rank) base += tot;
-        n_live += tot;
+    int n_live = s_total;
+    if constexpr (CTAS > 1) {
+        n_live = 0;
+        for (int r = 0; r < CTAS; ++r) {
+            const int tot = *bm.cluster.map_shared_rank(&s_total, r);
+            if (r < rank) base += tot;
+            n_live += tot;
+        }
     }
     for (int i = w0; i < w1; ++i) {
         bm.before[i] = (uint32_t)base;
         base += __popc(bm.words[i]);
     }
-    bm.cluster.sync();
+    bm.sync();
 
     if (p.pages) {
         const int n_free = p.num_pages - n_live;
@@ -403,8 +472,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         for (uint32_t i = n_free + first; i < (uint32_t)p.num_pages; i += kStep) p.pages[i] = -1;
         if (first == 0) p.counts[0] = n_free;
     } else {
-        bool live;
-        const int below = n_live < p.num_pages ? bm.rank(n_live, &live) : n_live;
+        const int below = n_live < p.num_pages ? bm.rank(n_live) : n_live;
         const int moves = n_live - below;  // pages in use from n_live on = unused ones below it
         for (int i = warp; i < per_cta; i += kPlanThreads / 32) {
             const int page = (rank * per_cta + i) * 32 + lane;
@@ -419,21 +487,31 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             p.counts[0] = n_live;
             p.counts[1] = moves;
         }
-        __threadfence();
-        bm.cluster.sync();  // dst is complete
-        for (uint32_t i = first; i < entries; i += kStep) {
-            const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
-            bool bad;
-            int page = p.block_table[i];
-            if (page >= n_live && page < p.num_pages &&
-                col < used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad)) {
-                const int r = bm.rank(page, &live);
-                page = __ldcg(p.dst + (r - below));
+        bm.sync();  // dst is complete
+        for (uint32_t i0 = first; i0 < entries; i0 += U * kStep) {
+            int page[U];
+            bool moved[U];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const uint32_t i = i0 + v * kStep;
+                moved[v] = false;
+                page[v] = 0;
+                if (i >= entries) continue;
+                const int b = (int)(i / (uint32_t)p.max_pages), col = (int)(i - (uint32_t)b * p.max_pages);
+                bool bad;
+                page[v] = p.block_table[i];
+                moved[v] = col < used_entries(p.seq_lens[b], p.page_size, p.max_pages, &bad) &&
+                           page[v] >= n_live && page[v] < p.num_pages;
             }
-            p.new_table[i] = page;
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+                if (moved[v]) page[v] = __ldcg(p.dst + (bm.rank(page[v]) - below));
+#pragma unroll
+            for (int v = 0; v < U; ++v)
+                if (i0 + v * kStep < entries) p.new_table[i0 + v * kStep] = page[v];
         }
     }
-    bm.cluster.sync();  // nobody reads this CTA's words any more
+    if constexpr (CTAS > 1) bm.sync();  // nobody reads this CTA's words any more
 }
 
 // One CTA per child.
@@ -557,12 +635,24 @@ int launch_append(const AppendParams &p, cudaStream_t stream) {
 
 int launch_pages(const PagesParams &p, cudaStream_t stream) {
     const int words = (p.num_pages + 31) / 32;
-    const int per_cta = (words + kPlanCtas - 1) / kPlanCtas;
+    const bool one = (long long)p.B * p.max_pages + 4LL * words <= kOneCta;
+    const int ctas = one ? 1 : 8;
+    const int per_cta = (words + ctas - 1) / ctas;
+    auto kern = one ? fa_pages_kernel<1> : fa_pages_kernel<8>;
     const int smem = per_cta * 8;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(fa_pages_kernel), smem) != FA_OK)
-        return FA_ERR_CUDA;
-    fa_pages_kernel<<<kPlanCtas, kPlanThreads, smem, stream>>>(p, per_cta);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), smem) != FA_OK) return FA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, per_cta) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int launch_fork(const ForkParams &p, cudaStream_t stream) {
