@@ -969,7 +969,6 @@ extern "C" int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, 
     // rows per window: about what one group gets of this call (T / B rows per sequence)
     const int per_seq = T / B < 1 ? 1 : T / B;
     p.window = per_seq < scale_group ? per_seq : scale_group;
-    p.num_sms = dc->num_sms;
     p.status = dc->status;
     return launch_append(p, static_cast<cudaStream_t>(stream));
 }

@@ -3,6 +3,8 @@
 // the unused ones, forking sequences, compaction, copying).  The definitions are in fa.h.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -22,55 +24,26 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 //
 // A group's new codes need the group's largest magnitude first, so its rows are held in
 // registers between the maximum and the conversion and read once: 2 bytes in, 1 byte out
-// per element, bound by HBM.  A team of W warps works on one (group, head, key or value) at a
-// time; warp w of it takes rows w, w + W, ... (at most 16 of them), a lane E consecutive
-// elements.  Teams are handed out by windows of `window` consecutive rows of the call: a team
-// walks the groups that begin in its window, which needs no list of the groups (their number
-// is only known on the device).  The host sets the window to about the rows a group gets, so a
-// window holds about one group whether the call stores prompts or one token per sequence.
-// Finding a group takes a chain of dependent loads (offsets, length, page).  A large call would
-// pay it in every wave of CTAs, so there a team does `jobs` heads of a group in turn, the rows of
-// the next under way while one is converted; a small call gives every head its own team.
+// per element, bound by HBM.  A team of W warps owns one (group, head, key or value); a lane
+// holds eight consecutive elements of a row (16-byte loads, 8-byte stores), so a warp covers
+// one to four rows at a time and 16 in all.  Teams are handed out by windows of `window`
+// consecutive rows of the call: a team walks the groups that begin in its window, which needs
+// no list of the groups (their number is only known on the device).  The host sets the window
+// to about the rows a group gets, so a window holds about one group whether the call stores
+// prompts or one token per sequence.  Finding a group is a chain of dependent loads (offsets
+// and lengths, page), during which a warp holds no data: many resident warps hide it, which
+// the registers are kept few for.
+
 template <int D>
 struct RowLanes {
-    static constexpr int E = (D == 96) ? 4 : D / 32;  // d = 96: 24 lanes of 4
-    static constexpr int LANES = D / E;
-    static constexpr int WORDS = E / 2;  // 32-bit words of bf16 pairs per lane
+    static constexpr int E = 8;                // elements per lane
+    static constexpr int PER_ROW = D / E;      // lanes of a row
+    static constexpr int ROWS = 32 / PER_ROW;  // rows a warp covers at a time (d = 96: 2, 24 lanes)
+    static constexpr int STEPS = 16 / ROWS;    // to cover 16 rows
+    static_assert(16 % ROWS == 0, "whole steps");
 };
 
-constexpr int kRowsPerWarp = 16;
 constexpr int kAppendThreads = 256;
-
-template <int D>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, uint32_t (&u)[RowLanes<D>::WORDS]) {
-    if constexpr (RowLanes<D>::WORDS == 1) {
-        u[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (RowLanes<D>::WORDS == 2) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        u[0] = w.x; u[1] = w.y;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
-    }
-}
-
-// E e4m3 codes of a lane, in one access of E bytes.
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&c)[(E + 3) / 4]) {
-    if constexpr (E == 2) *reinterpret_cast<uint16_t *>(p) = (uint16_t)c[0];
-    else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(p) = c[0];
-    else *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
-}
-
-template <int E>
-__device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&c)[(E + 3) / 4]) {
-    if constexpr (E == 2) c[0] = *reinterpret_cast<const uint16_t *>(p);
-    else if constexpr (E == 4) c[0] = *reinterpret_cast<const uint32_t *>(p);
-    else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        c[0] = w.x; c[1] = w.y;
-    }
-}
 
 // Value of an e4m3 code (in the low byte): e4m3's exponent bias is 7 and bf16's 127, so the
 // code's bits moved to a bf16's places read as value * 2^-120 (subnormals too).
@@ -80,15 +53,8 @@ __device__ __forceinline__ float e4m3_float(uint32_t c) {
     return m == 0x7fu ? __uint_as_float(0x7fc00000u) : v;
 }
 
-template <int E>
-__device__ __forceinline__ void encode(const float (&y)[E], uint32_t (&c)[(E + 3) / 4]) {
-    if constexpr (E == 2) {
-        c[0] = pack_e4m3x4(y[0], y[1], 0.f, 0.f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i)
-            c[i] = pack_e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    }
+__device__ __forceinline__ uint2 encode8(const float (&y)[8]) {
+    return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
 // bf16 magnitudes order like the integers of their 15 bits; 0x7f80 and up are not finite.
@@ -122,20 +88,26 @@ __device__ __forceinline__ float up_to_pow2(float s) {
 }
 
 template <int D, int W>
-__global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) fa_append_kernel(const AppendParams p) {
     using L = RowLanes<D>;
-    constexpr int E = L::E, CW = (E + 3) / 4;
+    constexpr int STEPS = L::STEPS;
     constexpr int TEAMS = kAppendThreads / 32 / W;
     __shared__ uint32_t s_amax[TEAMS][W];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / W, w = warp % W;
-    const bool on = lane < L::LANES;
+    const bool on = lane < L::PER_ROW * L::ROWS;
+    const int sub = lane / L::PER_ROW, col = lane % L::PER_ROW * L::E;  // of the rows of a step
     // heads fastest: the CTAs that run together read whole rows of the call
-    const int all_jobs = 2 * p.Hkv;  // job 2 h: keys of head h, 2 h + 1: values
-    const int per_cta = TEAMS * p.jobs, job_ctas = (all_jobs + per_cta - 1) / per_cta;
-    const int job0 = (int)(blockIdx.x % job_ctas) * per_cta + team;  // then every TEAMS-th
-    if (job0 >= all_jobs) return;
-    const bool reports = blockIdx.x % job_ctas == 0 && team == 0 && w == 0 && lane == 0;
+    const int job_ctas = (2 * p.Hkv + TEAMS - 1) / TEAMS;
+    const int job = (int)(blockIdx.x % job_ctas) * TEAMS + team;  // 2 h: keys of head h, 2 h + 1: values
+    if (job >= 2 * p.Hkv) return;
+    const int h = job >> 1;
+    const __nv_bfloat16 *x =
+        reinterpret_cast<const __nv_bfloat16 *>(job & 1 ? p.v : p.k) + (size_t)h * D + col;
+    const long long stride = job & 1 ? p.v_stride : p.k_stride;
+    uint8_t *cache = (job & 1 ? p.v_cache : p.k_cache) + col;
+    float *scales = job & 1 ? p.v_scale : p.k_scale;
+    const bool reports = job == 0 && w == 0 && lane == 0;
     const int G = p.group, ps = p.page_size, groups = ps / G;
 
     int t = (int)(blockIdx.x / job_ctas) * p.window;
@@ -157,7 +129,7 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             n = min(step, n - k * step);
         }
         b = lo * 32;
-        if (blockIdx.x == 0 && team == 0 && w == 0) {
+        if (blockIdx.x == 0 && job == 0 && w == 0) {
             bool ok = true;  // the offsets, checked once per call
             for (int i = lane; i < p.B; i += 32) {
                 const int c0 = p.cu_seqlens[i], c1 = p.cu_seqlens[i + 1];
@@ -211,24 +183,23 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
         }
         const int page = p.block_table[(size_t)b * p.max_pages + pos / ps];
         const int g = pos % ps / G;
-        // the team's rows of one job; `next` is loaded while the one before is converted
-        auto load = [&](int job, uint32_t (&u)[kRowsPerWarp][L::WORDS]) {
-            const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(job & 1 ? p.v : p.k) +
-                                     (long long)t * (job & 1 ? p.v_stride : p.k_stride) +
-                                     (long long)(job >> 1) * D + lane * E;
-            const long long step = (long long)W * (job & 1 ? p.v_stride : p.k_stride);
-            x += w * (job & 1 ? p.v_stride : p.k_stride);
+        // step i: rows row(i) of the new ones, loaded while the page number is on its way
+        auto row = [&](int i) { return (i * W + w) * L::ROWS + sub; };
+        uint4 u[STEPS];
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i, x += step) {
-                if (w + i * W < cnt && on) {
-                    load_bf16<D>(x, u[i]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < L::WORDS; ++e) u[i][e] = 0u;
-                }
-            }
-        };
-        // the team's larger of a value per warp
+        for (int i = 0; i < STEPS; ++i)
+            u[i] = row(i) < cnt && on ? *reinterpret_cast<const uint4 *>(x + (t + row(i)) * stride)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+        if (page < 0 || page >= p.num_pages) {
+            if (reports) flag_index(p.status, SITE_APPEND_BAD_PAGE);
+            t += cnt;
+            continue;
+        }
+        const size_t ph = (size_t)page * p.Hkv + h;
+        float *sc = scales + ph * groups + g;
+        uint8_t *rows = cache + (ph * ps + (size_t)g * G) * D;  // of the group
+        const float old = in_group ? *sc : 0.f;
+        // the team's largest of a word's halves
         auto team_max = [&](uint32_t m) {
             m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
             if constexpr (W > 1) {
@@ -240,79 +211,66 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
             }
             return m;
         };
-        uint32_t next[kRowsPerWarp][L::WORDS];
-        load(job0, next);
-        if (page < 0 || page >= p.num_pages) {
-            if (reports) flag_index(p.status, SITE_APPEND_BAD_PAGE);
-            t += cnt;
-            continue;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            m = max_bits(max_bits(m, u[i].x), u[i].y);
+            m = max_bits(max_bits(m, u[i].z), u[i].w);
         }
-#pragma unroll 1
-        for (int job = job0; job < all_jobs && job < job0 + per_cta; job += TEAMS) {
-            const size_t ph = (size_t)page * p.Hkv + (job >> 1);
-            float *sc = (job & 1 ? p.v_scale : p.k_scale) + ph * groups + g;
-            uint8_t *rows = (job & 1 ? p.v_cache : p.k_cache) + (ph * ps + (size_t)g * G) * D + lane * E;
-            const float old = in_group ? *sc : 0.f;
-            uint32_t u[kRowsPerWarp][L::WORDS];
-            uint32_t m = 0;
+        uint32_t amax = team_max(m);
+        const bool odd = amax >= kNotFinite;
+        if (odd) {  // something is not finite: the largest of the rest
+            m = 0;
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i)
-#pragma unroll
-                for (int e = 0; e < L::WORDS; ++e) {
-                    u[i][e] = next[i][e];
-                    m = max_bits(m, u[i][e]);
-                }
-            if (job + TEAMS < all_jobs && job + TEAMS < job0 + per_cta) load(job + TEAMS, next);
-            uint32_t amax = team_max(m);
-            const bool odd = amax >= kNotFinite;
-            if (odd) {  // something is not finite: the largest of the rest
-                m = 0;
-#pragma unroll
-                for (int i = 0; i < kRowsPerWarp; ++i)
-#pragma unroll
-                    for (int e = 0; e < L::WORDS; ++e) m = max_finite_bits(m, u[i][e]);
-                amax = team_max(m);
+            for (int i = 0; i < STEPS; ++i) {
+                m = max_finite_bits(max_finite_bits(m, u[i].x), u[i].y);
+                m = max_finite_bits(max_finite_bits(m, u[i].z), u[i].w);
             }
-            const float s = fmaxf(least_scale(amax), up_to_pow2(old));
-            if (in_group && s > old) {  // the codes that were there, at the larger scale
-                const float ratio = old / s;
-                for (int r = w; r < in_group; r += W) {
-                    if (on) {
-                        uint32_t c[CW];
-                        load_codes<E>(rows + (size_t)r * D, c);
-                        float y[E];
-#pragma unroll
-                        for (int e = 0; e < E; ++e) y[e] = e4m3_float(c[e / 4] >> (8 * (e % 4))) * ratio;
-                        encode<E>(y, c);
-                        store_codes<E>(rows + (size_t)r * D, c);
-                    }
-                }
-            }
-            const uint64_t inv = f32x2_splat(1.f / s);  // exact, and so are the products
-            uint8_t *out = rows + (size_t)(in_group + w) * D;
-#pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i, out += W * D) {
-                if (w + i * W < cnt && on) {
-                    float y[E];
-#pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        y[e] = __uint_as_float(u[i][e / 2] << 16);
-                        y[e + 1] = __uint_as_float(u[i][e / 2] & 0xffff0000u);
-                        mul_f32x2(y[e], y[e + 1], inv);
-                    }
-                    uint32_t c[CW];
-                    encode<E>(y, c);
-                    if (odd) {  // an infinity is stored as NaN, not as the largest number
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (!(fabsf(y[e]) < INFINITY))
-                                c[e / 4] = (c[e / 4] & ~(0xffu << (8 * (e % 4)))) | 0x7fu << (8 * (e % 4));
-                    }
-                    store_codes<E>(out, c);
-                }
-            }
-            if (w == 0 && lane == 0) *sc = s;
+            amax = team_max(m);
         }
+        const float s = fmaxf(least_scale(amax), up_to_pow2(old));
+        if (in_group && s > old) {  // the codes that were there, at the larger scale
+            const float ratio = old / s;
+            for (int r = w * L::ROWS + sub; r < in_group; r += W * L::ROWS) {
+                if (on) {
+                    const uint2 c = *reinterpret_cast<const uint2 *>(rows + (size_t)r * D);
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = e4m3_float((e < 4 ? c.x : c.y) >> (8 * (e % 4))) * ratio;
+                    *reinterpret_cast<uint2 *>(rows + (size_t)r * D) = encode8(y);
+                }
+            }
+        }
+        const uint64_t inv = f32x2_splat(1.f / s);  // exact, and so are the products
+        uint8_t *out = rows + (size_t)in_group * D;
+        auto put = [&](auto fix) {
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                if (row(i) < cnt && on) {
+                    const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[2 * e] = __uint_as_float(v[e] << 16);
+                        y[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+                        mul_f32x2(y[2 * e], y[2 * e + 1], inv);
+                    }
+                    uint2 c = encode8(y);
+                    if constexpr (decltype(fix)::value) {  // an infinity is stored as NaN
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t &word = e < 4 ? c.x : c.y;
+                            const int at = 8 * (e % 4);
+                            if (!(fabsf(y[e]) < INFINITY)) word = (word & ~(0xffu << at)) | 0x7fu << at;
+                        }
+                    }
+                    *reinterpret_cast<uint2 *>(out + (size_t)row(i) * D) = c;
+                }
+            }
+        };
+        if (odd) put(std::true_type());
+        else put(std::false_type());
+        if (w == 0 && lane == 0) *sc = s;
         t += cnt;
     }
 }
@@ -320,15 +278,9 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
 template <int D, int W>
 int launch_append_t(const AppendParams &p, cudaStream_t stream) {
     constexpr int TEAMS = kAppendThreads / 32 / W;
-    const long long windows = (p.T - 1LL) / p.window + 1;
-    AppendParams q = p;
-    // one head per team while the teams fit the GPU at once (16 warps per SM), then 2 and 4
-    q.jobs = 1;
-    while (q.jobs < 4 && windows * 2 * p.Hkv * W > (long long)p.num_sms * 16 * q.jobs) q.jobs *= 2;
-    const long long per_cta = (long long)TEAMS * q.jobs;
-    const long long ctas = (2LL * p.Hkv + per_cta - 1) / per_cta * windows;
+    const long long ctas = (2LL * p.Hkv + TEAMS - 1) / TEAMS * ((p.T - 1LL) / p.window + 1);
     if (ctas >= (1LL << 31)) return FA_ERR_INVALID_ARG;
-    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(q);
+    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

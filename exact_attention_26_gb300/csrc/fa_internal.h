@@ -178,8 +178,6 @@ struct AppendParams {
     const int *cu_seqlens;           // [B+1], or null: one token each
     int B, T, Hkv, d, page_size, max_pages, num_pages, group;
     int window;                      // consecutive rows a team of warps looks after
-    int jobs;                        // heads (of keys or values) a team does; set by the launch
-    int num_sms;
     int *status;
 };
 int launch_append(const AppendParams &p, cudaStream_t stream);
