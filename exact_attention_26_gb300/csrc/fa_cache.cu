@@ -88,11 +88,13 @@ __device__ __forceinline__ float up_to_pow2(float s) {
 }
 
 template <int D, int W>
-__global__ void __launch_bounds__(kAppendThreads, 4) fa_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, D == 256 ? 2 : D == 96 ? 3 : 4) fa_append_kernel(const AppendParams p) {
     using L = RowLanes<D>;
     constexpr int STEPS = L::STEPS;
     constexpr int TEAMS = kAppendThreads / 32 / W;
     __shared__ uint32_t s_amax[TEAMS][W];
+    griddep_wait();
+    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / W, w = warp % W;
     const bool on = lane < L::PER_ROW * L::ROWS;
@@ -280,8 +282,7 @@ int launch_append_t(const AppendParams &p, cudaStream_t stream) {
     constexpr int TEAMS = kAppendThreads / 32 / W;
     const long long ctas = (2LL * p.Hkv + TEAMS - 1) / TEAMS * ((p.T - 1LL) / p.window + 1);
     if (ctas >= (1LL << 31)) return FA_ERR_INVALID_ARG;
-    fa_append_kernel<D, W><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_dependent(fa_append_kernel<D, W>, (unsigned)ctas, kAppendThreads, 0, stream, 1, p);
 }
 
 template <int D>
@@ -348,6 +349,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_pages_kernel(const PagesParam
     constexpr int U = 4;  // entries whose loads a thread has in flight
 
     for (int i = tid; i < per_cta; i += kPlanThreads) bm.words[i] = 0u;
+    griddep_wait();
+    griddep_launch_dependents();
     bm.sync();
     for (uint32_t i0 = first; i0 < entries; i0 += U * kStep) {
         int page[U];
@@ -468,6 +471,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_pages_kernel(const PagesParam
 
 // One CTA per child.
 __global__ void __launch_bounds__(128) fa_fork_kernel(const ForkParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
     const int i = blockIdx.x;
     const int parent = p.parents[i];
     const bool known = parent >= 0 && parent < p.B;
@@ -540,6 +545,8 @@ __device__ __forceinline__ void copy_unit(const uint8_t *s, uint8_t *d, int byte
 __global__ void __launch_bounds__(kCopyThreads) fa_copy_pages_kernel(const __grid_constant__ CopyParams p) {
     const int lane = threadIdx.x & 31;
     const int per_pair = p.first_unit[p.n_caches];
+    griddep_wait();
+    griddep_launch_dependents();
     int n = p.n_pairs;
     if (p.count) n = max(0, min(n, *p.count));
     const long long units = (long long)n * per_pair;
@@ -593,23 +600,11 @@ int launch_pages(const PagesParams &p, cudaStream_t stream) {
     auto kern = one ? fa_pages_kernel<1> : fa_pages_kernel<8>;
     const int smem = per_cta * 8;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), smem) != FA_OK) return FA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, per_cta) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_dependent(kern, (unsigned)ctas, kPlanThreads, (size_t)smem, stream, ctas, p, per_cta);
 }
 
 int launch_fork(const ForkParams &p, cudaStream_t stream) {
-    fa_fork_kernel<<<p.n, 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_dependent(fa_fork_kernel, (unsigned)p.n, 128, 0, stream, 1, p);
 }
 
 int launch_copy(CopyParams &p, cudaStream_t stream) {
@@ -624,8 +619,8 @@ int launch_copy(CopyParams &p, cudaStream_t stream) {
     const long long units = per_pair * p.n_pairs;
     const long long most = (long long)p.num_sms * (2048 / kCopyThreads);
     const long long ctas = (units + kWarps - 1) / kWarps;
-    fa_copy_pages_kernel<<<(unsigned)(ctas < most ? ctas : most), kCopyThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return launch_dependent(fa_copy_pages_kernel, (unsigned)(ctas < most ? ctas : most), kCopyThreads, 0,
+                            stream, 1, p);
 }
 
 }  // namespace fa

@@ -104,7 +104,6 @@ struct Dec8Misc {
     alignas(16) float nref[RB];          // minus the reference of the row's scores, base 2
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
-    float vref[NWG];                // power of two that the value scales are taken relative to
     float vpart[NWG][4];
 };
 
@@ -425,7 +424,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
     constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG;
     constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
-    griddep_launch_dependents();  // the merge kernel may launch while the tiles run
     extern __shared__ uint8_t dec8_smem[];
     const uint32_t raw = smem_u32(dec8_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -463,6 +461,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         tma_prefetch_desc(&a.tm_k);
         tma_prefetch_desc(&a.tm_v);
     }
+    // What the kernels before this one wrote is there from here on; the merge kernel may launch.
+    griddep_wait();
+    griddep_launch_dependents();
+
     // The two warps that fetch page numbers find the CTA's first tile themselves and have its
     // pages under way before the barrier; the others read the result.
     Walk walk{0, 0, 0, 0, 0};
@@ -799,7 +801,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
             }
             if (kk < RW) ms.nref[rw0 + kk] = -kUnseen;
-            if (kk == 0) ms.vref[wg] = 0.f;
+            float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
+            const int full_tiles = max(full_keys, 0) / kTile, len_tiles = len / kTile;  // wholly seen, held
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 mbar_wait(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 __syncwarp();
                 tc_fence_after();
-                const bool partly = (t + 1) * (long long)kTile > full_keys;  // some row sees less
+                const bool partly = t >= full_tiles;  // some row sees less
                 // base-2 exponents of the rows' scores of this thread's key; with REF less the
                 // references
                 float x[RW];
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     float top = fmaxf(x[0], x[1]);
 #pragma unroll
                     for (int r = 2; r < RW; r += 2) top = fmax3(top, x[r], x[r + 1]);
-                    move = vote_group(id, top > kMoveLog2 || vs > ms.vref[wg]);
+                    move = vote_group(id, top > kMoveLog2 || vs > vref);
                 }
                 if (move) {
                     // new references: the tile's maximum where it passes the old one by 2^6
@@ -862,15 +865,16 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     }
                     const float vm_warp = warp_max(vs);
                     if (lane == 0) ms.vpart[wg][w4] = vm_warp;
-                    const float v_old = ms.vref[wg];
+                    const float v_old = vref;
                     named_barrier_sync(id, 128);
                     const float vm = fmaxf(fmaxf(ms.vpart[wg][0], ms.vpart[wg][1]),
                                            fmaxf(ms.vpart[wg][2], ms.vpart[wg][3]));
-                    float v_new = v_old;
                     // a power of two 8 to 16 times the largest scale, so that it seldom moves
                     // again (p's terms have the room), and kOneP / v_new stays finite
-                    if (vm > v_old)
-                        v_new = fmaxf(__uint_as_float(__float_as_uint(vm) & 0x7f800000u) * 16.f, 0x1p-110f);
+                    if (vm > v_old) {
+                        vref = fmaxf(__uint_as_float(__float_as_uint(vm) & 0x7f800000u) * 16.f, 0x1p-110f);
+                        vmul = kOneP / vref;
+                    }
                     if (kk < RW) {
                         const int r = rw0 + kk;
                         const float m_old = -ms.nref[r];
@@ -880,7 +884,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         ms.alpha[r] = up ? ex2(m_old - m) : 1.f;
                         if (up) ms.nref[r] = -m;
                     }
-                    if (kk == 0) ms.vref[wg] = v_new;
                     named_barrier_sync(id, 128);
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -888,7 +891,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         x[r] += ms.nref[rw0 + r];
                     }
                     if (t > s.t0) {  // O^T to the new references, once PV of the tile before is done
-                        const float fo = v_new > 0.f ? v_old / v_new : 1.f;
+                        const float fo = vref > 0.f ? v_old / vref : 1.f;
                         mbar_wait_warp(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
@@ -906,9 +909,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         tmem_wait_st();
                     }
                 }
-                const float vref = ms.vref[wg];
-                const float fv = vref > 0.f ? vs * (kOneP / vref) : 0.f;
-                const uint64_t fv2 = f32x2_splat(fv);
+                const uint64_t fv2 = f32x2_splat(vs * vmul);
                 uint32_t term[3][RW / 4];
 #pragma unroll
                 for (int r = 0; r < RW; r += 4) {
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         sts128(p_addr(p0, T::P_CHUNK, 3 * wg + e, kk), term[e][0], term[e][1], term[e][2],
                                term[e][3]);
                 }
-                if (wg == 0 && (t + 1) * (long long)kTile > len) {
+                if (wg == 0 && t >= len_tiles) {
                     // rows of V behind the last key: whatever lies there, P is 0 and V must not be NaN
                     const uint32_t i = 2 * j + 1;
                     const int slot = (int)(i % ST);
@@ -982,7 +983,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 const int r = rw0 + kk;
                 const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
                 const float l2 = sum == 0.f ? -INFINITY : lg2(sum) - ms.nref[r];  // base 2
-                ms.alpha[r] = sum == 0.f ? 0.f : ms.vref[wg] * (1.f / kOneP) / sum;
+                ms.alpha[r] = sum == 0.f ? 0.f : vref * (1.f / kOneP) / sum;
                 if (kk < rows && !dead) {
                     if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
                     else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
@@ -1207,23 +1208,13 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = dec8_ctas<NCH, RB>(p);
-    kern<<<n_cta, T::THREADS, kSmem, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    // a programmatic dependent: launched as the last CTAs start, it waits for the whole grid
+    if (launch_dependent(kern, (unsigned)n_cta, T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     const long long rows = (long long)p.B * p.H * p.Nq;
-    const bool few = rows <= 8LL * p.num_sms;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 3) / 4));
-    cfg.blockDim = dim3(few ? 256 : 128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    auto merge = few ? fa_decode8_merge_kernel<NCH, RB, 1, 8> : fa_decode8_merge_kernel<NCH, RB, 4, 4>;
-    if (cudaLaunchKernelEx(&cfg, merge, a, n_cta, rows) != cudaSuccess) return FA_ERR_CUDA;
-    return FA_OK;
+    if (rows <= 8LL * p.num_sms)
+        return launch_dependent(fa_decode8_merge_kernel<NCH, RB, 1, 8>, (unsigned)rows, 256, 0, stream, 1, a,
+                                n_cta, rows);
+    return launch_dependent(fa_decode8_merge_kernel<NCH, RB, 4, 4>, (unsigned)((rows + 3) / 4), 128, 0, stream,
+                            1, a, n_cta, rows);
 }
 
 // Calls f with the tile that serves R query rows per key/value head of dimension d.

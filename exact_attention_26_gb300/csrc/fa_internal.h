@@ -242,6 +242,29 @@ constexpr int kMaxCachedDevices = 64;
 // later launches skip the driver call.  FA_OK or FA_ERR_CUDA.
 int ensure_smem_attr(const void *kernel, int bytes);
 
+// Launch as a programmatic dependent of the stream's previous kernel: the CTAs may start (and
+// set up what needs no memory of others) while that kernel ends, and wait for its results with
+// griddepcontrol.wait.  Kernels launched this way make that wait before they read or write
+// global memory, and let their own dependents start after it, so a chain of them stays ordered.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                     cudaStream_t stream, int cluster, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 // Registers per thread a kernel is launched with (cached per kernel), or -1.
 int kernel_num_regs(const void *kernel);
 
