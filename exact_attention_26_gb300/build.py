@@ -51,7 +51,7 @@ def _torch_flags():
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
                 "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
                 "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_inc]
-    link = ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    link = ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-Wl,-rpath,{lib}"]
     return compile_, link
 
 

@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -43,9 +43,25 @@ bool shaped(const Tensor &t, std::initializer_list<int64_t> sizes) {
 bool is_int(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 Tensor make(std::initializer_list<int64_t> sizes, at::ScalarType type, int device) {
-    return at::empty(at::IntArrayRef(sizes),
-                     at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)device)));
+    return Tensor(at::detail::empty_cuda(at::IntArrayRef(sizes), type,
+                                         c10::Device(c10::kCUDA, (c10::DeviceIndex)device), std::nullopt));
 }
+
+// int32 outputs of one call as parts of one allocation (each allocation is most of a
+// microsecond): a buffer, and tensors over its elements in turn.
+struct Parts {
+    Tensor buffer;
+    int64_t used = 0;
+    Parts(int64_t elements, int device) : buffer(make({elements}, at::kInt, device)) {}
+    Tensor take(std::initializer_list<int64_t> sizes) {
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(),
+                                                            buffer.dtype());
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(sizes));
+        t.unsafeGetTensorImpl()->set_storage_offset(used);
+        used += t.numel();
+        return t;
+    }
+};
 
 PyObject *declined() { Py_RETURN_NONE; }
 
@@ -243,7 +259,8 @@ PyObject *free_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *stream;
     if (!stream_of(a[4], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
-    Tensor pages = make({t.num_pages}, at::kInt, t.device), count = make({1}, at::kInt, t.device);
+    Parts parts((int64_t)t.num_pages + 1, t.device);
+    const Tensor pages = parts.take({t.num_pages}), count = parts.take({1});
     const int rc = fa_free_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(pages), ptr<int>(count), t.B,
                                  t.max_pages, t.page_size, t.num_pages, stream);
     return rc != FA_OK ? PyLong_FromLong(rc) : results({pages, count});
@@ -263,8 +280,9 @@ PyObject *fork_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!stream_of(a[6], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
     const int64_t m = parents->size(0);
-    Tensor rows = make({m, t.max_pages}, at::kInt, t.device), lens = make({m}, at::kInt, t.device);
-    Tensor src = make({m}, at::kInt, t.device), dst = make({m}, at::kInt, t.device);
+    Parts parts(m * t.max_pages + 3 * m, t.device);
+    const Tensor rows = parts.take({m, t.max_pages}), lens = parts.take({m});
+    const Tensor src = parts.take({m}), dst = parts.take({m});
     const int rc = fa_fork_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(*parents), ptr<int>(*fresh),
                                  ptr<int>(rows), ptr<int>(lens), ptr<int>(src), ptr<int>(dst), t.B, (int)m,
                                  t.max_pages, t.page_size, t.num_pages, stream);
@@ -281,8 +299,9 @@ PyObject *compact_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!stream_of(a[4], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
     const int64_t cap = t.num_pages / 2 > 1 ? t.num_pages / 2 : 1;
-    Tensor table = make({t.B, t.max_pages}, at::kInt, t.device), src = make({cap}, at::kInt, t.device);
-    Tensor dst = make({cap}, at::kInt, t.device), counts = make({2}, at::kInt, t.device);
+    Parts parts((int64_t)t.B * t.max_pages + 2 * cap + 2, t.device);
+    const Tensor table = parts.take({t.B, t.max_pages}), src = parts.take({cap});
+    const Tensor dst = parts.take({cap}), counts = parts.take({2});
     const int rc = fa_compact_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(table), ptr<int>(src),
                                     ptr<int>(dst), ptr<int>(counts), t.B, t.max_pages, t.page_size,
                                     t.num_pages, stream);
