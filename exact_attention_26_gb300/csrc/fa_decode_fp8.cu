@@ -74,7 +74,10 @@ struct Dec8Tile {
     static constexpr uint32_t FIXED = 2 * Q_BYTES + 2 * P_BYTES + MISC + 1024;
     static constexpr uint32_t BUDGET = (CTAS == 2 ? 113u : 226u) * 1024u;
     static constexpr int FIT = (int)((BUDGET - FIXED) / SLOT);
-    static constexpr int STAGES = FIT > 10 ? 10 : FIT;
+    // five where two CTAs share an SM: that keeps the HBM busy (6: 322 us, 5: 316 us, 4: 327 us
+    // for B8 H32 Nk32768 d128) and leaves the merge kernel's CTAs room to start early
+    static constexpr int MOST = CTAS == 2 ? 5 : 10;
+    static constexpr int STAGES = FIT > MOST ? MOST : FIT;
     static constexpr uint32_t OFF_Q = STAGES * SLOT;
     static constexpr uint32_t OFF_P = OFF_Q + 2 * Q_BYTES;
     static constexpr uint32_t OFF_MISC = OFF_P + 2 * P_BYTES;
@@ -97,7 +100,7 @@ struct Dec8Misc {
     int abort;
     int bad[2];                     // per query buffer: the segment met a page out of range
     int b, item, t, nt, left;       // where this CTA's tiles begin, and their number
-    alignas(16) float k_scale[kScaleStages][kTile];
+    alignas(16) float k_scale[kScaleStages][kTile];  // of keys 0, 2^run, ... of a tile
     alignas(16) float v_scale[kScaleStages][kTile];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
     alignas(16) int limit[2][RB];        // keys the row sees
@@ -138,6 +141,7 @@ struct Dec8Args {
     int B, H, Hkv, Nq, d, page_size, max_pages, num_pages, groups;
     int R, row_blocks;              // query rows per key/value head, blocks of RB of them
     int box;                        // rows per TMA box
+    int run;                        // log2 of the keys that one entry of the scales stands for
     int causal;
     float scale_log2;
     int *status;
@@ -470,32 +474,22 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     Walk walk{0, 0, 0, 0, 0};
     Segment s{};
     bool some = false;      // s is the CTA's first segment
-    int pg[4], len = 0;     // page numbers of this lane's boxes or keys of a tile; s's length
+    int len = 0;            // s's length and table row
     const int *bt = nullptr;
-    const int per_tile = kTile / a.box;
+    const int boxes = kTile / a.box, entries = kTile >> a.run;  // of a tile
     auto open = [&] {
         len = a.seq_lens[s.b];
         bt = a.block_table + (size_t)s.b * a.max_pages;
     };
-    // pages of boxes lane, lane + 32, ... of tile t (-1: no such box, or behind the last key)
-    auto look_boxes = [&](int t, int (&pg)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            pg[i] = -1;
-            if (32 * i >= per_tile) continue;
-            const int bx = lane + 32 * i;
-            const uint32_t key = (uint32_t)t * kTile + (uint32_t)(bx * a.box);
-            if (bx < per_tile && t < s.t1 && key < (uint32_t)len) pg[i] = __ldg(bt + a.by_page.div(key));
-        }
+    // page of the key that is `at` keys into tile t (-1 behind the last key or past this segment)
+    auto page_at = [&](int t, int at) {
+        const uint32_t key = (uint32_t)t * kTile + (uint32_t)at;
+        return t < s.t1 && key < (uint32_t)len ? __ldg(bt + a.by_page.div(key)) : -1;
     };
-    // pages of keys lane, lane + 32, ... of tile t (0 behind the last key)
-    auto look_keys = [&](int t, int (&pg)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t key = (uint32_t)t * kTile + (uint32_t)(lane + 32 * i);
-            pg[i] = 0;
-            if (t < s.t1 && key < (uint32_t)len) pg[i] = __ldg(bt + a.by_page.div(key));
-        }
+    int pg = -1;            // of this lane's first box, or scale entry, of a tile
+    auto first_page = [&](int t) {
+        if (warp == kTmaWarp) return lane < boxes ? page_at(t, lane * a.box) : -1;
+        return page_at(t, lane << a.run);
     };
     if (warp == kTmaWarp || warp == kAuxWarp) {
         walk = start_walk(a, blockIdx.x, gridDim.x);
@@ -509,8 +503,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         some = walk.next(a, &s);
         if (some) {
             open();
-            if (warp == kTmaWarp) look_boxes(s.t0, pg);
-            else look_keys(s.t0, pg);
+            pg = first_page(s.t0);
         }
     }
     if (warp == kMmaWarp && blockIdx.x == 0) {
@@ -605,51 +598,53 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         // ------------------------------------------------------------ TMA producer
         // The whole warp runs the loop.  A tile is a run of boxes of `box` rows (the largest
         // power of two that divides the page size, so a box never straddles two pages); lane i
-        // looks up and copies boxes i, i + 32, ...  Boxes behind the last key are not copied.
-        // Page numbers are fetched one tile ahead and looked at only when they are used.
+        // looks up and copies box i (and i + 32, ... of pages that allow only tiny boxes).  Boxes
+        // behind the last key are not copied.  Page numbers are fetched one tile ahead and looked
+        // at only when they are used.
         uint32_t n = 0;  // ring slots used so far
         bool ok = true;
-        int pg_next[4];
         for (bool first = true; ok && some; first = false, some = walk.next(a, &s)) {
             if (!first) {
                 open();
-                look_boxes(s.t0, pg);
+                pg = first_page(s.t0);
             }
+#pragma unroll 1
             for (int t = s.t0; ok && t < s.t1; ++t) {
-                look_boxes(t + 1, pg_next);
+                const int pg_next = first_page(t + 1);
+                auto page_of = [&](int i) { return i < 32 ? pg : page_at(t, i * a.box); };
+                auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
                 int mine = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mine += pg[i] >= 0 && pg[i] < a.num_pages ? 1 : 0;
+#pragma unroll 1
+                for (int i = lane; i < boxes; i += 32) mine += valid(page_of(i)) ? 1 : 0;
                 const uint32_t bytes =
                     (uint32_t)__reduce_add_sync(kFull, mine) * (uint32_t)a.box * 128u * NCH;
-#pragma unroll
-                for (int kv = 0; kv < 2 && ok; ++kv) {
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int slot = (int)(n % ST);
                     ok = n < (uint32_t)ST ||
                          mbar_wait_warp(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
                     if (!ok) break;
                     const uint32_t fb = bar(ms.full[slot]);
+                    const CUtensorMap *map = kv ? &a.tm_v : &a.tm_k;
                     if (lane == 0) {
                         if (bytes) mbar_arrive_expect_tx(fb, bytes);
                         else mbar_arrive(fb);
                     }
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (32 * i >= per_tile || pg[i] < 0 || pg[i] >= a.num_pages) continue;
-                        const int row = (lane + 32 * i) * a.box;
+#pragma unroll 1
+                    for (int i = lane; i < boxes; i += 32) {
+                        const int page = page_of(i), row = i * a.box;
+                        if (!valid(page)) continue;
                         const uint32_t key = (uint32_t)(t * kTile + row);
                         const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
                         const uint32_t dst = base + slot * T::SLOT + row * 128;
 #pragma unroll
                         for (int c = 0; c < NCH; ++c)
-                            tma_load_3d(dst + c * T::CHUNK, kv ? &a.tm_v : &a.tm_k, fb, c * 128, y,
-                                        pg[i] * a.Hkv + s.kvh);
+                            tma_load_3d(dst + c * T::CHUNK, map, fb, c * 128, y, page * a.Hkv + s.kvh);
                     }
-                    ++n;
+                    __syncwarp();
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) pg[i] = pg_next[i];
+                pg = pg_next;
             }
         }
         if (*g.abort) {
@@ -732,12 +727,11 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         // share out), and for every tile the scales of its keys, in asynchronous copies.
         uint32_t seg = 0, j = 0;
         bool ok = true;
-        int pg_next[4];
         for (; ok && some; ++seg, some = walk.next(a, &s)) {
             const int qb = seg & 1;
             if (seg >= 1) {
                 open();
-                look_keys(s.t0, pg);
+                pg = first_page(s.t0);
                 if (seg >= 2)
                     ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
                 if (!ok) break;
@@ -752,27 +746,28 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 if (lane == 0) mbar_arrive_n(bar(ms.q_full[qb]), 4 * NWG);
             }
             for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
-                look_keys(t + 1, pg_next);
+                const int pg_next = first_page(t + 1);
                 const int st = (int)(j % kScaleStages);
                 ok = j < kScaleStages || mbar_wait_warp(bar(ms.scale_empty[st]), ((j / kScaleStages) - 1) & 1,
                                                         g, SITE_DEC_EMPTY);
                 if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int kk = lane + 32 * i;
-                    const uint32_t key = (uint32_t)(t * kTile + kk);
-                    const bool valid = pg[i] >= 0 && pg[i] < a.num_pages;
-                    const bool copy = (int)key < len && valid;  // keys not there: scale 0
-                    if (!valid) ms.bad[qb] = 1;
+#pragma unroll 1
+                for (int i = lane; i < entries; i += 32) {
+                    const int at = i << a.run;
+                    const int page = i < 32 ? pg : page_at(t, at);
+                    const uint32_t key = (uint32_t)(t * kTile + at);
+                    const bool here = key < (uint32_t)len, valid = page >= 0 && page < a.num_pages;
+                    if (here && !valid) ms.bad[qb] = 1;
+                    const bool copy = here && valid;  // keys not there: scale 0
                     const uint32_t row = key - a.by_page.div(key) * (uint32_t)a.page_size;
-                    const size_t at = copy ? ((size_t)pg[i] * a.Hkv + s.kvh) * a.groups + a.by_group.div(row) : 0;
-                    cp_async4(smem_u32(&ms.k_scale[st][kk]), a.k_scale + at, copy);
-                    cp_async4(smem_u32(&ms.v_scale[st][kk]), a.v_scale + at, copy);
+                    const size_t from = copy ? ((size_t)page * a.Hkv + s.kvh) * a.groups + a.by_group.div(row) : 0;
+                    cp_async4(smem_u32(&ms.k_scale[st][i]), a.k_scale + from, copy);
+                    cp_async4(smem_u32(&ms.v_scale[st][i]), a.v_scale + from, copy);
                 }
+                __syncwarp();
                 cp_async_arrive(bar(ms.scale_full[st]));
                 mbar_arrive(bar(ms.scale_full[st]));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) pg[i] = pg_next[i];
+                pg = pg_next;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -812,7 +807,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 const int key = t * kTile + kk;
                 const int st = (int)(j % kScaleStages);
                 mbar_wait(bar(ms.scale_full[st]), (j / kScaleStages) & 1, g, SITE_DEC_FULL);
-                const float ks = ms.k_scale[st][kk], vs = ms.v_scale[st][kk];
+                float ks = ms.k_scale[st][kk >> a.run], vs = ms.v_scale[st][kk >> a.run];
                 mbar_wait(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 __syncwarp();
                 tc_fence_after();
@@ -1038,16 +1033,17 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 
 // Merge of the partial results of the items that were cut: L = log2 sum 2^(L_s),
 // O = sum 2^(L_s - L) O_s.  A CTA has ROWS query rows and WARPS warps; each row's partials are
-// shared out to all warps (a long sequence alone in the launch is cut into dozens), four loads
-// of each in flight, and the warps' sums meet in shared memory.  Bound by latency: one row per
-// CTA and eight warps to it where that fills no more than the GPU, else four rows per CTA,
-// most of which have nothing to merge.  Rows of empty sequences are written here.
+// shared out to all warps (a long sequence alone in the launch is cut into dozens), four of
+// them with their L in flight at a time, and the warps' running results meet in shared memory.
+// Bound by latency, one round of loads for up to 4 WARPS partials: one row per CTA and eight
+// warps to it where that fills no more than the GPU, else four rows per CTA, most of which have
+// nothing to merge.  Rows of empty sequences are written here.
 template <int NCH, int RB, int ROWS, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS)
     fa_decode8_merge_kernel(const __grid_constant__ Dec8Args a, int n_cta, long long n_rows) {
     constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
     static_assert(ROWS <= WARPS, "a warp finishes a row");
-    __shared__ float s_acc[ROWS][WARPS][E * 32], s_sum[ROWS][WARPS];
+    __shared__ float s_acc[ROWS][WARPS][E * 32], s_sum[ROWS][WARPS], s_max[ROWS][WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // every warp looks up every row of its CTA: the rows are few and the loads the same
     int c0[ROWS], n[ROWS], rr[ROWS];
@@ -1076,29 +1072,12 @@ __global__ void __launch_bounds__(32 * WARPS)
         any = any || n[q] != 0;
     }
     griddep_wait();  // every partial result is written
+    griddep_launch_dependents();
     if (!any) return;
-    float top[ROWS];
+    bool bad = false;
 #pragma unroll
     for (int q = 0; q < ROWS; ++q) {
-        top[q] = 0.f;
-        if (n[q] <= 0) continue;
-        auto prow = [&](int k) {
-            return ((size_t)(c0[q] + k) * 2 + (k == 0 ? 1 : 0)) * RB + rr[q] % RB;
-        };
-        float m = -INFINITY;
-        bool bad = false;
-        for (int k = lane; k < n[q]; k += 32) {
-            const float x = __ldcg(a.part_l + prow(k));
-            bad = bad || __float_as_uint(x) == kBadPartial;
-            m = fmaxf(m, x);
-        }
-        m = warp_max(m);
-        top[q] = m == -INFINITY ? 0.f : m;  // a row without keys: weights 0
-        if (__any_sync(kFull, bad)) {
-            n[q] = 0;
-            continue;
-        }
-        float acc[E], wsum = 0.f;
+        float m = kUnseen, sum = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         constexpr int U = 4;  // partials in flight per warp
@@ -1108,23 +1087,39 @@ __global__ void __launch_bounds__(32 * WARPS)
             for (int v = 0; v < U; ++v) {
                 const int k = k0 + WARPS * v;
                 const bool in = k < n[q];
-                const size_t pr = prow(in ? k : k0);
+                const size_t pr =
+                    ((size_t)(c0[q] + (in ? k : k0)) * 2 + ((in ? k : k0) == 0 ? 1 : 0)) * RB + rr[q] % RB;
                 w[v] = in ? __ldcg(a.part_l + pr) : -INFINITY;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     x[v][e] = in && lane + 32 * e < a.d ? __ldcg(a.part_o + pr * a.d + lane + 32 * e) : 0.f;
             }
+            float top = m;
 #pragma unroll
             for (int v = 0; v < U; ++v) {
-                const float wk = ex2(w[v] - top[q]);
-                wsum += wk;
+                bad = bad || __float_as_uint(w[v]) == kBadPartial;
+                top = fmaxf(top, w[v]);
+            }
+            const float f = ex2(m - top);
+            sum *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const float wk = ex2(w[v] - top);
+                sum += wk;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[v][e], acc[e]);
             }
+            m = top;
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) s_acc[q][warp][lane + 32 * e] = acc[e];
-        if (lane == 0) s_sum[q][warp] = wsum;
+        if (lane == 0) {
+            s_sum[q][warp] = sum;
+            s_max[q][warp] = bad ? INFINITY : m;
+        }
+        bad = false;
     }
     __syncthreads();
     if (warp >= ROWS) return;
@@ -1132,23 +1127,25 @@ __global__ void __launch_bounds__(32 * WARPS)
     for (int q = 0; q < ROWS; ++q) {
         if (q != warp || n[q] == 0) continue;
         const long long row = (long long)blockIdx.x * ROWS + q;
-        float wsum = 0.f, acc[E];
+        float m = kUnseen, sum = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (n[q] > 0) {
 #pragma unroll
-            for (int v = 0; v < WARPS; ++v) {
-                wsum += s_sum[q][v];
+        for (int v = 0; v < WARPS; ++v) m = fmaxf(m, s_max[q][v]);
+        if (m == INFINITY) continue;  // the sequence was rejected: nothing is written
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += s_acc[q][v][lane + 32 * e];
-            }
+        for (int v = 0; v < WARPS; ++v) {
+            const float f = ex2(s_max[q][v] - m);
+            sum = fmaf(s_sum[q][v], f, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[q][v][lane + 32 * e], f, acc[e]);
         }
-        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         __nv_bfloat16 *o = a.o + row * a.d;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
-        if (lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (top[q] + lg2(wsum)) * kLn2;
+        if (lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
     }
 }
 
@@ -1200,6 +1197,7 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.R = p.H / p.Hkv * p.Nq;
     a.row_blocks = (a.R + RB - 1) / RB;
     a.box = decode8_box_rows(p.page_size);
+    a.run = p.group % 4 == 0 ? 2 : 0;  // four keys of a tile share a page and a group, or none do
     a.causal = p.causal;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
