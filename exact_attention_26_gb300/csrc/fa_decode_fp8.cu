@@ -342,6 +342,7 @@ __device__ __forceinline__ int count_tiles(const Dec8Args &a, int upto, int *bef
 // one tile more than the others.
 struct Cut {
     int n, each, more;
+    Cut() = default;
     __device__ __forceinline__ Cut(int total, int n_cta) {
         n = min(total, n_cta);
         each = n ? total / n : 0;
@@ -383,8 +384,8 @@ struct Walk {
     }
 };
 
-// Where CTA c of n_cta begins; one warp.
-__device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta) {
+// Where CTA c of n_cta begins, and the cut; one warp.
+__device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta, Cut *the_cut) {
     const int lane = threadIdx.x & 31, ipb = a.Hkv * a.row_blocks;
     Walk w{0, 0, 0, 0, 0};
     // the first 32 sequences' tiles stay in a register: most batches are no larger
@@ -392,6 +393,7 @@ __device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta) 
     int mine = nt0;
     for (int b = lane + 32; b < a.B; b += 32) mine += tiles_of(a, b);
     const Cut cut(__reduce_add_sync(kFull, mine) * ipb, n_cta);
+    *the_cut = cut;
     if (c >= cut.n) return w;
     int g = cut.first(c);
     w.left = cut.first(c + 1) - g;
@@ -492,7 +494,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         return page_at(t, lane << a.run);
     };
     if (warp == kTmaWarp || warp == kAuxWarp) {
-        walk = start_walk(a, blockIdx.x, gridDim.x);
+        Cut cut;
+        walk = start_walk(a, blockIdx.x, gridDim.x, &cut);
         if (warp == kTmaWarp && lane == 0) {
             ms.b = walk.b;
             ms.item = walk.item;
@@ -1032,121 +1035,163 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 }
 
 // Merge of the partial results of the items that were cut: L = log2 sum 2^(L_s),
-// O = sum 2^(L_s - L) O_s.  A CTA has ROWS query rows and WARPS warps; each row's partials are
-// shared out to all warps (a long sequence alone in the launch is cut into dozens), four of
-// them with their L in flight at a time, and the warps' running results meet in shared memory.
-// Bound by latency, one round of loads for up to 4 WARPS partials: one row per CTA and eight
-// warps to it where that fills no more than the GPU, else four rows per CTA, most of which have
-// nothing to merge.  Rows of empty sequences are written here.
-template <int NCH, int RB, int ROWS, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS)
-    fa_decode8_merge_kernel(const __grid_constant__ Dec8Args a, int n_cta, long long n_rows) {
-    constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
-    static_assert(ROWS <= WARPS, "a warp finishes a row");
-    __shared__ float s_acc[ROWS][WARPS][E * 32], s_sum[ROWS][WARPS], s_max[ROWS][WARPS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // every warp looks up every row of its CTA: the rows are few and the loads the same
-    int c0[ROWS], n[ROWS], rr[ROWS];
-    bool any = false;
+// O = sum 2^(L_s - L) O_s.  Both kernels below are bound by latency: find the partials before
+// waiting for the attention kernel, then one or two rounds of loads.
+
+// The running result of one warp over partials first, first + step, ... of a row's n: reference,
+// sum and output columns lane, lane + 32, ...; U partials with their L in flight at a time.
+template <int E, int U, typename Row>
+__device__ __forceinline__ void merge_part(const Dec8Args &a, Row prow, int first, int step, int n, float &m,
+                                           float &sum, float (&acc)[E], bool &bad) {
+    const int lane = threadIdx.x & 31;
+    m = kUnseen;
+    sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        const long long row = (long long)blockIdx.x * ROWS + q;
-        c0[q] = n[q] = rr[q] = 0;
-        if (row >= n_rows) continue;
-        const int i = (int)(row % a.Nq);
-        const int bh = (int)(row / a.Nq);
-        const int b = bh / a.H, h = bh % a.H, group = a.H / a.Hkv;
-        const int len = a.seq_lens[b];
-        int before;
-        const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
-        if (len == 0) {
-            n[q] = -1;
-        } else if (len_ok(a, len)) {
-            rr[q] = (h % group) * a.Nq + i;
-            const int nt = tiles_of(a, b);
-            const int first = before * a.Hkv * a.row_blocks + (h / group * a.row_blocks + rr[q] / RB) * nt;
-            c0[q] = cut.owner(first);
-            n[q] = cut.owner(first + nt - 1) - c0[q] + 1;
-            if (n[q] == 1) n[q] = 0;  // written directly
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = first; k0 < n; k0 += step * U) {
+        float w[U], x[U][E];
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            const int k = k0 + step * v;
+            const bool in = k < n;
+            const size_t pr = prow(in ? k : k0);
+            w[v] = in ? __ldcg(a.part_l + pr) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[v][e] = in && lane + 32 * e < a.d ? __ldcg(a.part_o + pr * a.d + lane + 32 * e) : 0.f;
         }
-        any = any || n[q] != 0;
+        float top = m;
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            bad = bad || __float_as_uint(w[v]) == kBadPartial;
+            top = fmaxf(top, w[v]);
+        }
+        const float f = ex2(m - top);
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+            const float wk = ex2(w[v] - top);
+            sum += wk;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[v][e], acc[e]);
+        }
+        m = top;
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void merge_out(const Dec8Args &a, long long row, float m, float sum,
+                                          const float (&acc)[E]) {
+    const int lane = threadIdx.x & 31;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16 *o = a.o + row * a.d;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
+    if (lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+}
+
+// A few rows: a CTA of eight warps for each, which may have dozens of partials (a long sequence
+// alone in the launch); the warps' running results meet in shared memory.
+constexpr int kRowWarps = 8;
+template <int NCH, int RB>
+__global__ void __launch_bounds__(32 * kRowWarps)
+    fa_decode8_merge_row_kernel(const __grid_constant__ Dec8Args a, int n_cta) {
+    constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
+    __shared__ float s_acc[kRowWarps][E * 32], s_sum[kRowWarps], s_max[kRowWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, i = row % a.Nq, bh = row / a.Nq;
+    const int b = bh / a.H, h = bh % a.H, group = a.H / a.Hkv;
+    const int len = a.seq_lens[b], nt = tiles_of(a, b), r = (h % group) * a.Nq + i;
+    int before, c0 = 0, n = 0;
+    const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
+    if (nt > 0) {
+        const int first = before * a.Hkv * a.row_blocks + (h / group * a.row_blocks + r / RB) * nt;
+        c0 = cut.owner(first);
+        n = cut.owner(first + nt - 1) - c0 + 1;
     }
     griddep_wait();  // every partial result is written
     griddep_launch_dependents();
-    if (!any) return;
+    if (n <= 1 && len != 0) return;  // written directly, or a rejected sequence
     bool bad = false;
+    float m, sum, acc[E];
+    merge_part<E, 4>(
+        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r % RB; }, warp, kRowWarps, n, m,
+        sum, acc, bad);
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        float m = kUnseen, sum = 0.f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        constexpr int U = 4;  // partials in flight per warp
-        for (int k0 = warp; k0 < n[q]; k0 += WARPS * U) {
-            float w[U], x[U][E];
-#pragma unroll
-            for (int v = 0; v < U; ++v) {
-                const int k = k0 + WARPS * v;
-                const bool in = k < n[q];
-                const size_t pr =
-                    ((size_t)(c0[q] + (in ? k : k0)) * 2 + ((in ? k : k0) == 0 ? 1 : 0)) * RB + rr[q] % RB;
-                w[v] = in ? __ldcg(a.part_l + pr) : -INFINITY;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    x[v][e] = in && lane + 32 * e < a.d ? __ldcg(a.part_o + pr * a.d + lane + 32 * e) : 0.f;
-            }
-            float top = m;
-#pragma unroll
-            for (int v = 0; v < U; ++v) {
-                bad = bad || __float_as_uint(w[v]) == kBadPartial;
-                top = fmaxf(top, w[v]);
-            }
-            const float f = ex2(m - top);
-            sum *= f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-            for (int v = 0; v < U; ++v) {
-                const float wk = ex2(w[v] - top);
-                sum += wk;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, x[v][e], acc[e]);
-            }
-            m = top;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) s_acc[q][warp][lane + 32 * e] = acc[e];
-        if (lane == 0) {
-            s_sum[q][warp] = sum;
-            s_max[q][warp] = bad ? INFINITY : m;
-        }
-        bad = false;
+    for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_max[warp] = bad ? INFINITY : m;
     }
     __syncthreads();
-    if (warp >= ROWS) return;
+    if (warp > 0) return;
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        if (q != warp || n[q] == 0) continue;
-        const long long row = (long long)blockIdx.x * ROWS + q;
-        float m = kUnseen, sum = 0.f, acc[E];
+    for (int v = 0; v < kRowWarps; ++v) m = fmaxf(m, s_max[v]);
+    if (m == INFINITY) return;  // the sequence was rejected: nothing is written
+    sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int v = 0; v < WARPS; ++v) m = fmaxf(m, s_max[q][v]);
-        if (m == INFINITY) continue;  // the sequence was rejected: nothing is written
+    for (int v = 0; v < kRowWarps; ++v) {
+        const float f = ex2(s_max[v] - m);
+        sum = fmaf(s_sum[v], f, sum);
 #pragma unroll
-        for (int v = 0; v < WARPS; ++v) {
-            const float f = ex2(s_max[q][v] - m);
-            sum = fmaf(s_sum[q][v], f, sum);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[q][v][lane + 32 * e], f, acc[e]);
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        __nv_bfloat16 *o = a.o + row * a.d;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (lane + 32 * e < a.d) o[lane + 32 * e] = __float2bfloat16(acc[e] * inv);
-        if (lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[v][lane + 32 * e], f, acc[e]);
     }
+    merge_out(a, row, m, sum, acc);  // an empty sequence: sum 0
+}
+
+// Many rows, most of which were not cut.  Every cut lies where one of the attention kernel's
+// CTAs begins, so there is a CTA here for each of those (times blocks of eight rows): it merges
+// the item that its counterpart begins in the middle of, if no counterpart before it does, one
+// warp per row.  (Batch of 128 with 4096 rows and 300 cuts: 6 us less than a warp for every row.)
+constexpr int kCutRows = 8;
+template <int NCH, int RB>
+__global__ void __launch_bounds__(32 * kCutRows)
+    fa_decode8_merge_cut_kernel(const __grid_constant__ Dec8Args a, int n_cta) {
+    constexpr int E = NCH == 2 ? 8 : 4;
+    __shared__ int s_b, s_item, s_n;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x;  // the CTA whose beginning this is
+    if (warp == 0) {
+        Cut cut;
+        const Walk w = start_walk(a, c, n_cta, &cut);
+        int n = 0;
+        if (c > 0 && w.left > 0 && w.t > 0) {
+            const int first = cut.first(c) - w.t;  // the item's first tile
+            if (cut.owner(first) == c - 1) n = cut.owner(first + w.nt - 1) - (c - 1) + 1;
+        }
+        if (lane == 0) {
+            s_b = w.b;
+            s_item = w.item;
+            s_n = n;
+        }
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    if (blockIdx.y == 0) {
+        for (int b = c; b < a.B; b += gridDim.x) {
+            if (a.seq_lens[b] != 0) continue;
+            const long long row0 = (long long)b * a.H * a.Nq, rows = (long long)a.H * a.Nq;
+            for (long long i = threadIdx.x; i < rows * a.d; i += blockDim.x)
+                a.o[row0 * a.d + i] = __float2bfloat16(0.f);
+            for (long long i = threadIdx.x; i < rows; i += blockDim.x) a.lse[row0 + i] = -INFINITY;
+        }
+    }
+    const int n = s_n, kvh = s_item / a.row_blocks, rb = s_item - kvh * a.row_blocks;
+    const int r = blockIdx.y * kCutRows + warp;  // row of the block of RB
+    if (n == 0 || r >= RB || rb * RB + r >= a.R) return;
+    bool bad = false;
+    float m, sum, acc[E];
+    merge_part<E, 4>(
+        a, [&](int k) { return ((size_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, 0, 1, n, m, sum, acc, bad);
+    if (bad) return;
+    const long long row = ((long long)s_b * a.H + (long long)kvh * (a.H / a.Hkv)) * a.Nq + rb * RB + r;
+    merge_out(a, row, m, sum, acc);
 }
 
 // CTAs of a launch: all that are resident, or the largest number of tiles there can be.
@@ -1206,13 +1251,15 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = dec8_ctas<NCH, RB>(p);
-    if (launch_dependent(kern, (unsigned)n_cta, T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
+    if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     const long long rows = (long long)p.B * p.H * p.Nq;
-    if (rows <= 8LL * p.num_sms)
-        return launch_dependent(fa_decode8_merge_kernel<NCH, RB, 1, 8>, (unsigned)rows, 256, 0, stream, 1, a,
-                                n_cta, rows);
-    return launch_dependent(fa_decode8_merge_kernel<NCH, RB, 4, 4>, (unsigned)((rows + 3) / 4), 128, 0, stream,
-                            1, a, n_cta, rows);
+    if (rows <= 8LL * p.num_sms)  // as many CTAs as are resident
+        return launch_dependent(fa_decode8_merge_row_kernel<NCH, RB>, dim3((unsigned)rows), 32 * kRowWarps, 0,
+                                stream, 1, a, n_cta);
+    const int block = a.R < RB ? a.R : RB;
+    return launch_dependent(fa_decode8_merge_cut_kernel<NCH, RB>,
+                            dim3((unsigned)n_cta, (unsigned)((block + kCutRows - 1) / kCutRows)), 32 * kCutRows, 0,
+                            stream, 1, a, n_cta);
 }
 
 // Calls f with the tile that serves R query rows per key/value head of dimension d.

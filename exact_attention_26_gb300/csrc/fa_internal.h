@@ -247,10 +247,10 @@ int ensure_smem_attr(const void *kernel, int bytes);
 // griddepcontrol.wait.  Kernels launched this way make that wait before they read or write
 // global memory, and let their own dependents start after it, so a chain of them stays ordered.
 template <typename... P, typename... A>
-int launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+int launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
                      cudaStream_t stream, int cluster, A &&...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
