@@ -524,78 +524,90 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     const Guard g{a.status, &ms.abort, a.limit_ns};
     if (warp != kTmaWarp && warp != kAuxWarp) walk = Walk{ms.left, ms.b, ms.item, ms.t, ms.nt};
 
-    // Query terms of rows r, r + step, ... (N of them) of segment s into buffer qb, one warp.
-    // A row is scaled by the power of two that brings its largest magnitude into [128, 256);
-    // a row with a NaN or an infinity becomes NaN.
-    auto put_queries = [&](auto count, int qb, int len, int r_first, int step) {
-        constexpr int N = decltype(count)::value, W = NCH == 2 ? 4 : 2;
+    // Query terms of rows r, r + step, ... below RB of segment s into buffer qb, one warp.  A row
+    // is scaled by the power of two that brings its largest magnitude into [128, 256); a row
+    // with a NaN or an infinity becomes NaN.  N rows at a time, the next ones' loads under way:
+    // one for the softmax warps, whose first segment waits for them (unrolled, code that runs
+    // once takes longer to fetch than to execute), four for the helper warp, which must be done
+    // with all RB rows while the segment before is at its last tiles.
+    auto put_queries = [&](auto at_once, int qb, int len, int r_first, int step) {
+        constexpr int N = decltype(at_once)::value, W = NCH == 2 ? 4 : 2;
         const int E = a.d == 96 ? 4 : a.d / 32;  // elements per lane
         const bool on = lane * E < a.d;
         const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
-        const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
-        uint32_t w[N][W];
+        const __nv_bfloat16 *src =
+            a.q + (((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0) * a.d + lane * E;
+        auto load = [&](int r, uint32_t (&w)[W]) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int r = r_first + e * step;
+            for (int i = 0; i < W; ++i) w[i] = 0u;
+            if (r >= rows || !on) return;
+            const __nv_bfloat16 *p = src + (long long)r * a.d;
+            if constexpr (NCH == 2) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            } else if (E == 4) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                w[0] = x.x; w[1] = x.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+        };
+        uint32_t rows_w[N][W], next[N][W];
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[e][i] = 0u;
-            if (r < rows && on) {
-                const __nv_bfloat16 *p = a.q + (row0 + r) * a.d + lane * E;
-                if constexpr (NCH == 2) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-                    w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
-                } else if (E == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-                    w[e][0] = x.x; w[e][1] = x.y;
-                } else {
-                    w[e][0] = *reinterpret_cast<const uint32_t *>(p);
+        for (int e = 0; e < N; ++e) load(r_first + e * step, rows_w[e]);
+#pragma unroll 1
+        for (int rn = r_first; rn < RB; rn += N * step) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) load(rn + (N + e) * step, next[e]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int r = rn + e * step;
+                const uint32_t (&w)[W] = rows_w[e];
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < W; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                am = __reduce_max_sync(kFull, am);
+                const uint32_t ex = max((int)(am >> 7) - 7, 1);
+                const float inv = __uint_as_float((254u - ex) << 23);
+                uint32_t c1[W / 2], c2[W / 2];
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    // 8 significant bits fit f16, and so do both remainders
+                    uint32_t h = pack_f16(__uint_as_float(w[i] << 16) * inv,
+                                          __uint_as_float(w[i] & 0xffff0000u) * inv);
+                    if (am >= 0x7f80u) h = 0x7fff7fffu;
+                    const uint32_t c = e4m3x2_of(h);
+                    const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
+                    c1[i / 2] = i % 2 ? c1[i / 2] | c << 16 : c;
+                    c2[i / 2] = i % 2 ? c2[i / 2] | d << 16 : d;
                 }
-            }
-        }
+                if (on) {
+                    const int n1 = r / RW * (2 * RW) + r % RW;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int r = r_first + e * step;
-            uint32_t am = 0;
-#pragma unroll
-            for (int i = 0; i < W; ++i) am = max(am, max(w[e][i] & 0x7fffu, (w[e][i] >> 16) & 0x7fffu));
-            am = __reduce_max_sync(kFull, am);
-            const uint32_t ex = max((int)(am >> 7) - 7, 1);
-            const float inv = __uint_as_float((254u - ex) << 23);
-            uint32_t c1[W / 2], c2[W / 2];
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                // 8 significant bits fit f16, and so do both remainders
-                uint32_t h = pack_f16(__uint_as_float(w[e][i] << 16) * inv,
-                                      __uint_as_float(w[e][i] & 0xffff0000u) * inv);
-                if (am >= 0x7f80u) h = 0x7fff7fffu;
-                const uint32_t c = e4m3x2_of(h);
-                const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
-                c1[i / 2] = i % 2 ? c1[i / 2] | c << 16 : c;
-                c2[i / 2] = i % 2 ? c2[i / 2] | d << 16 : d;
-            }
-            if (on) {
-                const int n1 = r / RW * (2 * RW) + r % RW;
-#pragma unroll
-                for (int i = 0; i < W / 2; ++i) {
-                    const int col = lane * E + 4 * i;  // byte of the row
-                    const uint32_t q0 = sQ + qb * T::Q_BYTES + (col >> 7) * T::Q_CHUNK;
-                    const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + RW, col & 127);
-                    if (NCH == 1 && E == 2) {
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a1), "h"((uint16_t)c1[i]) : "memory");
-                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a2), "h"((uint16_t)c2[i]) : "memory");
-                    } else {
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a1), "r"(c1[i]) : "memory");
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a2), "r"(c2[i]) : "memory");
+                    for (int i = 0; i < W / 2; ++i) {
+                        const int col = lane * E + 4 * i;  // byte of the row
+                        const uint32_t q0 = sQ + qb * T::Q_BYTES + (col >> 7) * T::Q_CHUNK;
+                        const uint32_t a1 = swizzled(q0, n1, col & 127), a2 = swizzled(q0, n1 + RW, col & 127);
+                        if (NCH == 1 && E == 2) {
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a1), "h"((uint16_t)c1[i]) : "memory");
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a2), "h"((uint16_t)c2[i]) : "memory");
+                        } else {
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a1), "r"(c1[i]) : "memory");
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(a2), "r"(c2[i]) : "memory");
+                        }
                     }
                 }
+                if (lane == 0) {
+                    ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
+                    ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
+                }
             }
-            if (lane == 0) {
-                ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
-                ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
-            }
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+#pragma unroll
+                for (int i = 0; i < W; ++i) rows_w[e][i] = next[e][i];
         }
     };
-    constexpr int kQueryRows = RB / (4 * NWG);  // rows per softmax warp
 
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA producer
@@ -742,8 +754,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             if (lane == 0) ms.bad[qb] = 0;
             __syncwarp();
             if (seg >= 1) {
-#pragma unroll 1
-                for (int r = 0; r < RB; r += 4) put_queries(std::integral_constant<int, 4>(), qb, len, r, 1);
+                put_queries(std::integral_constant<int, 4>(), qb, len, 0, 1);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(bar(ms.q_full[qb]), 4 * NWG);
@@ -793,7 +804,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             const int r0 = s.rb * RB + rw0, rows = min(RW, a.R - r0);  // may be none
             const int full_keys = a.causal ? len - a.Nq + 1 : len;     // keys that every row sees
             if (seg == 0) {
-                put_queries(std::integral_constant<int, kQueryRows>(), 0, len, warp, 4 * NWG);
+                put_queries(std::integral_constant<int, 1>(), 0, len, warp, 4 * NWG);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
@@ -993,8 +1004,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c) {
                 const int dd = c * 128 + kk;
-                __nv_bfloat16 *o_out = a.o + row0 * a.d + dd;
-                float *p_out = a.part_o + prow * a.d + dd;
 #pragma unroll 1
                 for (int q = 0; q < RW && q < rows; q += 8) {
                     float o0[8], o1[8], o2[8];
@@ -1006,15 +1015,22 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     tmem_wait(o0);
                     tmem_wait(o1);
                     tmem_wait(o2);
-                    if (dd < a.d && !dead && !bad) {
+                    const float4 f0 = *reinterpret_cast<const float4 *>(&ms.alpha[rw0 + q]);
+                    const float4 f1 = *reinterpret_cast<const float4 *>(&ms.alpha[rw0 + q + 4]);
+                    const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (q + e < rows) {
-                                const float o = (o0[e] + (o1[e] + o2[e])) * ms.alpha[rw0 + q + e];
-                                if (whole) o_out[(q + e) * a.d] = __float2bfloat16(o);
-                                else p_out[(q + e) * a.d] = o;
-                            }
-                        }
+                    for (int e = 0; e < 8; ++e) o0[e] = (o0[e] + (o1[e] + o2[e])) * f[e];
+                    const int here = dd < a.d && !dead && !bad ? rows - q : 0;
+                    if (whole) {
+                        __nv_bfloat16 *out = a.o + (row0 + q) * a.d + dd;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < here) out[e * a.d] = __float2bfloat16(o0[e]);
+                    } else {
+                        float *out = a.part_o + (prow + q) * a.d + dd;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < here) out[e * a.d] = o0[e];
                     }
                 }
             }
