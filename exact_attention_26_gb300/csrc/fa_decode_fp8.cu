@@ -70,7 +70,7 @@ struct Dec8Tile {
     static constexpr uint32_t Q_BYTES = NCH * Q_CHUNK;   // of one of two buffers
     static constexpr uint32_t P_CHUNK = kTile * 32;      // 32 columns of every key
     static constexpr uint32_t P_BYTES = (NP + 31) / 32 * P_CHUNK;  // of one of two buffers
-    static constexpr uint32_t MISC = RB <= 16 ? 4096 : 8192;
+    static constexpr uint32_t MISC = 8192;
     static constexpr uint32_t FIXED = 2 * Q_BYTES + 2 * P_BYTES + MISC + 1024;
     static constexpr uint32_t BUDGET = (CTAS == 2 ? 113u : 226u) * 1024u;
     static constexpr int FIT = (int)((BUDGET - FIXED) / SLOT);
@@ -91,7 +91,7 @@ struct Dec8Tile {
 };
 
 // Small per-CTA state behind the buffers.
-template <int RB, int STAGES, int NWG>
+template <int NCH, int RB, int STAGES, int NWG>
 struct Dec8Misc {
     unsigned long long full[STAGES], empty[STAGES];
     unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], done;
@@ -108,6 +108,10 @@ struct Dec8Misc {
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
     float vpart[NWG][4];
+    // causal calls: columns of O that a NaN code of V makes NaN in a row, where not every row
+    // sees its key (elsewhere the product does it), as bits; and whether there are any
+    uint32_t nan_cols[RB][NCH * 4];
+    int nan_any;
 };
 
 struct FastDiv {  // n / d for 0 <= n < 2^31
@@ -426,7 +430,7 @@ template <int NCH, int RB>
 __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>::CTAS)
     fa_decode8_kernel(const __grid_constant__ Dec8Args a) {
     using T = Dec8Tile<NCH, RB>;
-    using Misc = Dec8Misc<RB, T::STAGES, T::NWG>;
+    using Misc = Dec8Misc<NCH, RB, T::STAGES, T::NWG>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
     constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG;
     constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
@@ -810,8 +814,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
             }
             if (kk < RW) ms.nref[rw0 + kk] = -kUnseen;
+            if (a.causal && wg == 0) {
+                for (int i = kk; i < RB * NCH * 4; i += 128) ms.nan_cols[i / (NCH * 4)][i % (NCH * 4)] = 0u;
+                if (kk == 0) ms.nan_any = 0;
+            }
             float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
-            const int full_tiles = max(full_keys, 0) / kTile, len_tiles = len / kTile;  // wholly seen, held
+            const int full_tiles = max(full_keys, 0) / kTile;  // seen by every row
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
@@ -950,17 +958,40 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         sts128(p_addr(p0, T::P_CHUNK, 3 * wg + e, kk), term[e][0], term[e][1], term[e][2],
                                term[e][3]);
                 }
-                if (wg == 0 && t >= len_tiles) {
-                    // rows of V behind the last key: whatever lies there, P is 0 and V must not be NaN
+                if (wg == 0 && partly) {
+                    // P is 0 where a row does not see the key, but 0 times a NaN of V would not be:
+                    // rows of V behind the last key, whatever lies there, become 0; so do the NaN
+                    // codes of keys that some rows see and others do not, and the rows that
+                    // do are noted
                     const uint32_t i = 2 * j + 1;
                     const int slot = (int)(i % ST);
                     mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                    const uint32_t v0 = base + slot * T::SLOT + kk * 128;
                     if (key >= len) {
 #pragma unroll
-                        for (int c = 0; c < NCH; ++c)
+                        for (int e = 0; e < NCH * 8; ++e)
+                            sts128(v0 + (e >> 3) * T::CHUNK + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                    } else if (key >= full_keys) {
+#pragma unroll 1
+                        for (int e = 0; e < NCH * 8; ++e) {
+                            uint4 *v = reinterpret_cast<uint4 *>(gbase + slot * T::SLOT + (e >> 3) * T::CHUNK +
+                                                                 kk * 128 + (((e & 7) ^ (kk & 7)) << 4));
+                            uint4 w = *v;
+                            uint32_t *x4 = &w.x, bits = 0;  // of the 16 columns from 16 e on
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                sts128(base + slot * T::SLOT + c * T::CHUNK + kk * 128 + e * 16, 0u, 0u, 0u, 0u);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t nan = ((x4[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                x4[c] &= ~((nan >> 7) * 255u);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) bits |= (nan >> (8 * k + 7) & 1u) << (4 * c + k);
+                            }
+                            if (bits == 0) continue;
+                            *v = w;
+                            ms.nan_any = 1;
+                            for (int r = 0; r < RB; ++r)
+                                if (key < ms.limit[qb][r])
+                                    atomicOr(&ms.nan_cols[r][e >> 1], bits << (16 * (e & 1)));
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -1020,6 +1051,11 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o0[e] = (o0[e] + (o1[e] + o2[e])) * f[e];
+                    if (a.causal && ms.nan_any) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (ms.nan_cols[rw0 + q + e][dd >> 5] >> (dd & 31) & 1u) o0[e] = NAN;
+                    }
                     const int here = dd < a.d && !dead && !bad ? rows - q : 0;
                     if (whole) {
                         __nv_bfloat16 *out = a.o + (row0 + q) * a.d + dd;

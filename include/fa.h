@@ -436,8 +436,8 @@ int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cac
  *            sees keys 0 .. seq_lens[b] - Nq + i.
  * A row that sees no key (an empty sequence, or a causal query before its first token)
  * gets O = 0 and L = -infinity.  Keys a row does not see have no influence on it, whatever
- * their codes are, with one exception: among the last Nq keys of a causal call, a NaN code
- * of V reaches also the rows that do not see it.  A NaN or infinity in a query makes its row NaN.
+ * their codes are.  A NaN code of K that a row sees makes the row NaN, one of V its column of
+ * the row, a NaN or infinity in a query its row.
  * Rounding: q's 8 significant bits are kept, probabilities enter the product with V with a
  * relative error of at most 2^-9 (absolute 2^-22 of the row's largest), sums are fp32.
  *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, and

@@ -156,6 +156,29 @@ def test_nan_and_infinities_stay_in_their_rows(fa):
     assert fa.fa_device_status(None) == 0
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("H,Hkv,Nq", [(2, 2, 3), (4, 1, 4), (8, 2, 7), (8, 1, 8)])
+def test_causal_rows_are_free_of_later_tokens_nans(fa, d, H, Hkv, Nq):
+    """NaN codes in K and V of the last Nq tokens: rows before them stay finite."""
+    for n in (Nq, 127, 128, 130, 300):
+        prob = list(_problem(2, H, Hkv, Nq, d, 16, 16, [n, 40], seed=n + d))
+        table = prob[5]
+        hits = [(n - 1, 0, 3), (n - 2, Hkv - 1, d - 1), (n - 2, 0, 0), (n - Nq, 0, d // 2)]
+        for key, h, col in hits[:3] if n % 2 else hits:
+            prob[2][int(table[0, key // 16]), h, key % 16, col] = 0x7F if col % 2 else 0xFF
+        prob[1][int(table[1, 39 // 16]), 0, 39 % 16, 1] = 0x7F  # the last key of sequence 1
+        o, lse = fa.decode_paged_fp8(*[t.to(DEV) for t in prob], causal=True)
+        ref = oracle_decode(*prob, True, d ** -0.5)
+        o, lse = o.float().cpu().numpy(), lse.cpu().numpy()
+        assert np.array_equal(np.isnan(o), np.isnan(ref[0])), n
+        assert np.array_equal(np.isnan(lse), np.isnan(ref[1])), n
+        clean = [np.where(np.isnan(x), 0, x) for x in (o, ref[0], *ref[2][:2])]
+        rows = ~np.isnan(ref[1])
+        check_decode(clean[0][rows], lse[rows], (clean[1][rows], ref[1][rows],
+                                                 (clean[2][rows], clean[3][rows], ref[2][2][rows])))
+    assert fa.fa_device_status(None) == 0
+
+
 def test_shared_pages_and_repeated_entries(fa):
     prob = list(_problem(4, 4, 2, 1, 128, 16, 16, [100, 160, 33, 64], seed=11))
     prob[5][1, :6] = prob[5][0, :6]
