@@ -99,7 +99,6 @@ struct Dec8Misc {
     uint32_t tmem;
     int abort;
     int bad[2];                     // per query buffer: the segment met a page out of range
-    int b, item, t, nt, left;       // where this CTA's tiles begin, and their number
     alignas(16) float k_scale[kScaleStages][kTile];  // of keys 0, 2^run, ... of a tile
     alignas(16) float v_scale[kScaleStages][kTile];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
@@ -471,13 +470,20 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         tma_prefetch_desc(&a.tm_k);
         tma_prefetch_desc(&a.tm_v);
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    const Guard g{a.status, &ms.abort, a.limit_ns};
+
     // What the kernels before this one wrote is there from here on; the merge kernel may launch.
     griddep_wait();
     griddep_launch_dependents();
 
-    // The two warps that fetch page numbers find the CTA's first tile themselves and have its
-    // pages under way before the barrier; the others read the result.
-    Walk walk{0, 0, 0, 0, 0};
+    // Every warp finds the CTA's first tile for itself (none waits for another's answer), and the
+    // two that fetch page numbers the first of those.
+    Cut cut;
+    Walk walk = start_walk(a, blockIdx.x, gridDim.x, &cut);
     Segment s{};
     bool some = false;      // s is the CTA's first segment
     int len = 0;            // s's length and table row
@@ -498,15 +504,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         return page_at(t, lane << a.run);
     };
     if (warp == kTmaWarp || warp == kAuxWarp) {
-        Cut cut;
-        walk = start_walk(a, blockIdx.x, gridDim.x, &cut);
-        if (warp == kTmaWarp && lane == 0) {
-            ms.b = walk.b;
-            ms.item = walk.item;
-            ms.t = walk.t;
-            ms.nt = walk.nt;
-            ms.left = walk.left;
-        }
         some = walk.next(a, &s);
         if (some) {
             open();
@@ -521,13 +518,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             atomicExch(a.status, FA_ERR_BAD_INDEX);
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = ms.tmem;
-    const Guard g{a.status, &ms.abort, a.limit_ns};
-    if (warp != kTmaWarp && warp != kAuxWarp) walk = Walk{ms.left, ms.b, ms.item, ms.t, ms.nt};
-
     // Query terms of rows r, r + step, ... below RB of segment s into buffer qb, one warp.  A row
     // is scaled by the power of two that brings its largest magnitude into [128, 256); a row
     // with a NaN or an infinity becomes NaN.  N rows at a time, the next ones' loads under way:
