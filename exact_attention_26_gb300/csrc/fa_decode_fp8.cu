@@ -1143,25 +1143,34 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     fa_decode8_merge_row_kernel(const __grid_constant__ Dec8Args a, int n_cta) {
     constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
     __shared__ float s_acc[kRowWarps][E * 32], s_sum[kRowWarps], s_max[kRowWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x, i = row % a.Nq, bh = row / a.Nq;
-    const int b = bh / a.H, h = bh % a.H, group = a.H / a.Hkv;
-    const int len = a.seq_lens[b], nt = tiles_of(a, b), r = (h % group) * a.Nq + i;
-    int before, c0 = 0, n = 0;
-    const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
-    if (nt > 0) {
-        const int first = before * a.Hkv * a.row_blocks + (h / group * a.row_blocks + r / RB) * nt;
-        c0 = cut.owner(first);
-        n = cut.owner(first + nt - 1) - c0 + 1;
+    __shared__ int s_row, s_c0, s_n;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
+    if (warp == 0) {
+        const int i = row % a.Nq, bh = row / a.Nq, b = bh / a.H, h = bh - b * a.H, group = a.H / a.Hkv;
+        const int nt = tiles_of(a, b), kvh = h / group, r = (h - kvh * group) * a.Nq + i;
+        int before, c0 = 0, n = 0;
+        const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
+        if (nt > 0) {
+            const int first = before * a.Hkv * a.row_blocks + (kvh * a.row_blocks + r / RB) * nt;
+            c0 = cut.owner(first);
+            n = cut.owner(first + nt - 1) - c0 + 1;
+        }
+        if (lane == 0) {
+            s_row = r % RB;
+            s_c0 = c0;
+            s_n = n > 1 || a.seq_lens[b] == 0 ? n : -1;  // -1: written directly, or rejected
+        }
     }
     griddep_wait();  // every partial result is written
     griddep_launch_dependents();
-    if (n <= 1 && len != 0) return;  // written directly, or a rejected sequence
+    __syncthreads();
+    const int r = s_row, c0 = s_c0, n = s_n;
+    if (n < 0) return;
     bool bad = false;
     float m, sum, acc[E];
     merge_part<E, 4>(
-        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r % RB; }, warp, kRowWarps, n, m,
-        sum, acc, bad);
+        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, warp, kRowWarps, n, m, sum,
+        acc, bad);
 #pragma unroll
     for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
     if (lane == 0) {
