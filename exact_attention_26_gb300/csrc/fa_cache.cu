@@ -32,7 +32,10 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 // to about the rows a group gets, so a window holds about one group whether the call stores
 // prompts or one token per sequence.  Finding a group is a chain of dependent loads (offsets
 // and lengths, page), during which a warp holds no data: many resident warps hide it, which
-// the registers are kept few for.
+// the registers are kept few for.  Measured (GB300, graph replay, Hkv8 d128): 14083 tokens of
+// seven prompts 18.9 us, 4.5 TB/s of 3 bytes per element (a wave of CTAs is latency for its
+// first half; eight rows per warp and more warps 23 us, two heads per warp with the next
+// one's rows under way 27 us); one token each for 128 sequences 3.4 us, latency.
 
 template <int D>
 struct RowLanes {
@@ -300,7 +303,9 @@ int launch_append_d(const AppendParams &p, cudaStream_t stream) {
 // pages of the table (atomics on the owner's words through distributed shared memory),
 // count the bits of the words before each word, then write the lists.  A launch that is
 // bound by latency: barriers and two passes over the table.  A small table is done sooner by
-// one CTA, whose barriers are local (kOneCta below).
+// one CTA, whose barriers are local (kOneCta below).  Measured (graph replay): the compaction
+// plan of 12 x 20 entries and 300 pages 3.8 us (one CTA; 7.1 us as a cluster), of 192 x 63 and
+// 23000 pages 11.3 us (cluster; 18.7 us in one CTA), against 200 us of copies.
 
 constexpr int kPlanThreads = 1024;
 
@@ -521,6 +526,8 @@ __global__ void __launch_bounds__(128) fa_fork_kernel(const ForkParams p) {
 // units of 4 KB, one warp each (8 independent 16-byte loads per lane in flight); the small
 // pages of the scales are units of their own.  Warps stride over the units, so one launch of
 // resident CTAs serves any number of pairs, with their number on the device if it must be.
+// Measured (GB300): 2500 pages of 4 layers, 1.3 GB of traffic, 200 us, 6.5 TB/s; 128 pages of
+// 8 layers, 0.26 GB, 39 us, 6.8 TB/s.
 
 constexpr int kCopyUnit = 4096;
 constexpr int kCopyThreads = 256;
