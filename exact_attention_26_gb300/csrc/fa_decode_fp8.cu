@@ -44,7 +44,7 @@
 //   B8 H32 Hkv4 Nq4 d64        46 us      1.8 TB/s       32 rows per head: the softmax warps'
 //                                                        chain, 2.2k clocks per tile of 128 keys
 //   B1 H32 Hkv8 1000 keys       6.4 us                   latency of two launches
-// Per tile of 128 keys the chain of a softmax warp takes 0.5k clocks (8 rows) to 0.8k (16 rows)
+// Per tile of 128 keys the chain of a softmax warp takes 0.7k clocks (8 rows) to 0.9k (16 rows)
 // against 1.3k clocks in which its bytes arrive at d = 128, one of two CTAs on the SM.  At
 // d = 64 a row is half a swizzle span and TMA's rows, not its bytes, are the limit (31 keys per
 // ns, 4 TB/s).  Code that runs once per item is kept small: fetching it cold costs more than
@@ -64,7 +64,7 @@ constexpr float kUnseen = -3.0e38f;    // reference of a row that has seen no ke
 // e5m2 reaches from 2^-16 to 57344, and p times the value scale is placed in it so that neither
 // reference moves often: the rows' references move when a score passes them by 2^6, the value
 // scales' (first 8 to 16 times the largest) when a scale passes it, and p = 2^6 at the reference
-// scale is 2^15.  A threshold of 2^3 moved in one of three tiles of the Nq4 Hkv4 d64 batch.
+// scale is 2^15.  The wider the threshold, the fewer tiles rescale.
 constexpr float kMoveLog2 = 6.0f;
 constexpr float kOneP = 512.0f;        // p = 1 at the reference scale
 constexpr uint32_t kBadPartial = 0x7fc0bad1u;  // L of a partial result of a rejected sequence
