@@ -1055,14 +1055,13 @@ extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const voi
     p.status = dc->status;
     p.num_sms = dc->num_sms;
     if (workspace_bytes < decode8_workspace_bytes(p)) return FA_ERR_WORKSPACE;
-    // every head's rows of a page as one plane; boxes as wide as a swizzle span, columns from d
-    // on read as zeros
-    const uint64_t planes = (uint64_t)num_pages * Hkv, pitch = (uint64_t)d, plane = pitch * page_size;
-    const uint32_t box = (uint32_t)decode8_box_rows(page_size);
-    if ((rc = make_u8_map(&p.tm_k, k_cache, d, page_size, planes, pitch, plane, 128, box)) != FA_OK)
-        return rc;
-    if ((rc = make_u8_map(&p.tm_v, v_cache, d, page_size, planes, pitch, plane, 128, box)) != FA_OK)
-        return rc;
+    // every head's rows of a page as one plane, one or two keys to a row; boxes as wide as a
+    // swizzle span, columns from d on read as zeros
+    const int pack = decode8_pack(p), cols = d * pack, rows = page_size / pack;
+    const uint64_t planes = (uint64_t)num_pages * Hkv, pitch = (uint64_t)cols, plane = pitch * rows;
+    const uint32_t box = (uint32_t)decode8_box_rows(rows);
+    if ((rc = make_u8_map(&p.tm_k, k_cache, cols, rows, planes, pitch, plane, 128, box)) != FA_OK) return rc;
+    if ((rc = make_u8_map(&p.tm_v, v_cache, cols, rows, planes, pitch, plane, 128, box)) != FA_OK) return rc;
     return launch_decode8(p, static_cast<cudaStream_t>(stream));
 }
 

@@ -15,9 +15,10 @@
 //   2^-22 of it below.
 //   p, fp32, times its key's value scale, is rounded to f16 and split into three e5m2 terms:
 //   e5m2 is f16's upper byte, so the first two are byte selections and the remainders exact
-//   subtractions; the third is rounded to nearest.  Relative error at most 2^-9 + 2^-11 (a
-//   rounding to bf16 would be off by 2^-8), and 2^-22 of the row's largest where the terms run
-//   into e5m2's smallest step, 2^-16.
+//   subtractions; the third, of 2^5 times what they leave (less than 2^-5 of p), is rounded to
+//   nearest.  Relative error at most 2^-9 + 2^-11 (a rounding to bf16 would be off by 2^-8);
+//   where the first two run into e5m2's smallest step, 2^-16, they leave up to that, of which the
+//   third is off by 2^-20: 2^-24 of the row's largest p times the largest scale.
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
@@ -59,7 +60,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kTile = 128;             // keys per tile: the M of S^T and the K of O^T
+constexpr int kTile = 128;             // keys per step: the M of S^T and the K of O^T
 constexpr float kUnseen = -3.0e38f;    // reference of a row that has seen no key yet
 // e5m2 reaches from 2^-16 to 57344, and p times the value scale is placed in it so that neither
 // reference moves often: the rows' references move when a score passes them by 2^6, the value
@@ -71,7 +72,12 @@ constexpr uint32_t kBadPartial = 0x7fc0bad1u;  // L of a partial result of a rej
 constexpr int kScaleStages = 3;
 
 // NCH: 128-byte chunks of a row (d <= 128: 1, d = 256: 2).  RB: query rows per CTA.
-template <int NCH, int RB>
+// PACK: keys per 128-byte row of a tile.  With two (d = 64, even pages) TMA copies rows twice as
+// long, half as many; a tile holds 256 keys and is worked on in two steps, of the even keys and
+// of the odd ones.  K's halves are chosen by the column that S^T's products begin at; the
+// products with V take whole rows, so each step has columns of O^T of its own, of which the
+// lanes of its half are O and the others are not read, and the halves meet in the epilogue.
+template <int NCH, int RB, int PACK>
 struct Dec8Tile {
     static constexpr int RW = RB < 16 ? RB : 16;         // rows of a softmax warpgroup
     static constexpr int NWG = RB / RW;
@@ -79,6 +85,7 @@ struct Dec8Tile {
     static constexpr int NP = (3 * RB + 15) / 16 * 16;   // columns of O^T: three terms of p
     static constexpr int CTAS = (NCH == 1 && RB <= 32) ? 2 : 1;  // resident per SM
     static constexpr int THREADS = 32 * (4 * NWG + 3);
+    static constexpr int TK = PACK * kTile;              // keys of a tile
     static constexpr uint32_t CHUNK = kTile * 128;
     static constexpr uint32_t SLOT = NCH * CHUNK;
     static constexpr uint32_t Q_CHUNK = NS * 128;
@@ -98,15 +105,18 @@ struct Dec8Tile {
     static constexpr uint32_t OFF_MISC = OFF_P + 2 * P_BYTES;
     static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
     static constexpr uint32_t TM_O = 2 * NS;             // after two S slots
-    static constexpr uint32_t TM_USED = TM_O + NCH * NP;
+    static constexpr uint32_t TM_USED = TM_O + NCH * PACK * NP;
     static constexpr uint32_t TM_COLS = TM_USED <= 64 ? 64 : TM_USED <= 128 ? 128 : TM_USED <= 256 ? 256 : 512;
+    static_assert(NCH == 1 || PACK == 1, "only half rows are packed");
+    static_assert(PACK == 1 || (NWG == 1 && P_BYTES >= RB * 64 * sizeof(float)),
+                  "room for the halves of O to meet in a buffer of P");
     static_assert(STAGES >= 4, "two tiles in the ring");
     static_assert(TM_USED <= 512 && CTAS * TM_COLS <= 512, "tensor memory budget");
     static_assert(Q_CHUNK % 1024 == 0 && P_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 };
 
 // Small per-CTA state behind the buffers.
-template <int NCH, int RB, int STAGES, int NWG>
+template <int NCH, int RB, int STAGES, int NWG, int TK>
 struct Dec8Misc {
     unsigned long long full[STAGES], empty[STAGES];
     unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], done;
@@ -114,8 +124,8 @@ struct Dec8Misc {
     uint32_t tmem;
     int abort;
     int bad[2];                     // per query buffer: the segment met a page out of range
-    alignas(16) float k_scale[kScaleStages][kTile];  // of keys 0, 2^run, ... of a tile
-    alignas(16) float v_scale[kScaleStages][kTile];
+    alignas(16) float k_scale[kScaleStages][TK];  // of keys 0, 2^run, ... of a tile
+    alignas(16) float v_scale[kScaleStages][TK];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
     alignas(16) int limit[2][RB];        // keys the row sees
     alignas(16) float nref[RB];          // minus the reference of the row's scores, base 2
@@ -148,7 +158,8 @@ FastDiv fast_div(uint32_t d) {
 }
 
 struct Dec8Args {
-    CUtensorMap tm_k, tm_v;         // bytes (d, page_size, num_pages * Hkv), boxes 128 x box x 1
+    CUtensorMap tm_k, tm_v;         // bytes (d, page_size, num_pages * Hkv), boxes 128 x box x 1;
+                                    // packed (2 d, page_size / 2, num_pages * Hkv)
     const __nv_bfloat16 *q;
     const float *k_scale, *v_scale;
     const int *block_table, *seq_lens;
@@ -158,7 +169,8 @@ struct Dec8Args {
     FastDiv by_page, by_group;
     int B, H, Hkv, Nq, d, page_size, max_pages, num_pages, groups;
     int R, row_blocks;              // query rows per key/value head, blocks of RB of them
-    int box;                        // rows per TMA box
+    int box;                        // 128-byte rows per TMA box
+    int tile_log2;                  // log2 of the keys per tile
     int run;                        // log2 of the keys that one entry of the scales stands for
     int causal;
     float scale_log2;
@@ -260,6 +272,11 @@ __device__ __forceinline__ uint32_t remainder16(uint32_t h, uint32_t c) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(sub_f16x2(h, c)), "r"(0x4c004c00u));
     return r;
 }
+__device__ __forceinline__ uint32_t times32(uint32_t h) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x50005000u));
+    return r;
+}
 // e5m2 of two f16 values, to nearest even.
 __device__ __forceinline__ uint32_t e5m2x2_of(uint32_t h) {
     uint16_t r;
@@ -340,7 +357,7 @@ __device__ __forceinline__ bool len_ok(const Dec8Args &a, int len) {
 // Tiles of one (head, row block) item of sequence b.
 __device__ __forceinline__ int tiles_of(const Dec8Args &a, int b) {
     const int len = a.seq_lens[b];
-    return len_ok(a, len) ? (int)(((long long)len + kTile - 1) / kTile) : 0;
+    return len_ok(a, len) ? (int)(((long long)len + (1 << a.tile_log2) - 1) >> a.tile_log2) : 0;
 }
 
 // Tiles (of one head and row block) of all sequences, and of those before `upto`; one warp.
@@ -440,13 +457,13 @@ __device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta, 
 
 // ---------------------------------------------------------------- the kernel
 
-template <int NCH, int RB>
-__global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>::CTAS)
+template <int NCH, int RB, int PACK>
+__global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH, RB, PACK>::CTAS)
     fa_decode8_kernel(const __grid_constant__ Dec8Args a) {
-    using T = Dec8Tile<NCH, RB>;
-    using Misc = Dec8Misc<NCH, RB, T::STAGES, T::NWG>;
+    using T = Dec8Tile<NCH, RB, PACK>;
+    using Misc = Dec8Misc<NCH, RB, T::STAGES, T::NWG, T::TK>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
-    constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG;
+    constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG, TK = T::TK;
     constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
     extern __shared__ uint8_t dec8_smem[];
     const uint32_t raw = smem_u32(dec8_smem);
@@ -503,19 +520,19 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     bool some = false;      // s is the CTA's first segment
     int len = 0;            // s's length and table row
     const int *bt = nullptr;
-    const int boxes = kTile / a.box, entries = kTile >> a.run;  // of a tile
+    const int boxes = kTile / a.box, entries = TK >> a.run;  // of a tile
     auto open = [&] {
         len = a.seq_lens[s.b];
         bt = a.block_table + (size_t)s.b * a.max_pages;
     };
     // page of the key that is `at` keys into tile t (-1 behind the last key or past this segment)
     auto page_at = [&](int t, int at) {
-        const uint32_t key = (uint32_t)t * kTile + (uint32_t)at;
+        const uint32_t key = (uint32_t)t * TK + (uint32_t)at;
         return t < s.t1 && key < (uint32_t)len ? __ldg(bt + a.by_page.div(key)) : -1;
     };
     int pg = -1;            // of this lane's first box, or scale entry, of a tile
     auto first_page = [&](int t) {
-        if (warp == kTmaWarp) return lane < boxes ? page_at(t, lane * a.box) : -1;
+        if (warp == kTmaWarp) return lane < boxes ? page_at(t, lane * a.box * PACK) : -1;
         return page_at(t, lane << a.run);
     };
     if (warp == kTmaWarp || warp == kAuxWarp) {
@@ -621,7 +638,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA producer
         // The whole warp runs the loop.  A tile is a run of boxes of `box` rows (the largest
-        // power of two that divides the page size, so a box never straddles two pages); lane i
+        // power of two that divides a page's rows, so a box never straddles two pages); lane i
         // looks up and copies box i (and i + 32, ... of pages that allow only tiny boxes).  Boxes
         // behind the last key are not copied.  Page numbers are fetched one tile ahead and looked
         // at only when they are used.
@@ -635,7 +652,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
 #pragma unroll 1
             for (int t = s.t0; ok && t < s.t1; ++t) {
                 const int pg_next = first_page(t + 1);
-                auto page_of = [&](int i) { return i < 32 ? pg : page_at(t, i * a.box); };
+                auto page_of = [&](int i) { return i < 32 ? pg : page_at(t, i * a.box * PACK); };
                 auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
                 int mine = 0;
 #pragma unroll 1
@@ -659,8 +676,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     for (int i = lane; i < boxes; i += 32) {
                         const int page = page_of(i), row = i * a.box;
                         if (!valid(page)) continue;
-                        const uint32_t key = (uint32_t)(t * kTile + row);
-                        const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
+                        const uint32_t key = (uint32_t)(t * TK + row * PACK);
+                        const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size) / PACK;
                         const uint32_t dst = base + slot * T::SLOT + row * 128;
 #pragma unroll
                         for (int c = 0; c < NCH; ++c)
@@ -683,29 +700,30 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         constexpr uint32_t kIdescS = idesc_e4m3_f32(128, T::NS);
         constexpr uint32_t kIdescO = idesc_e4m3_f32(128, T::NP) | (1u << 10) | (3u << 15);  // B e5m2; both MN-major
         const int ksteps = a.d / 32;
-        Walk ahead = walk;   // segments of S, up to two tiles ahead of O
+        Walk ahead = walk;   // segments of S, up to two steps ahead of O
         Segment sa;
         bool more = ahead.next(a, &sa);
         int ta = more ? sa.t0 : 0;
-        uint32_t js = 0, seg = 0;  // tiles whose S is issued; segments begun
+        uint32_t js = 0, seg = 0;  // steps whose S is issued; segments begun
         bool ok = true;
         auto issue_s = [&]() {
-            const int u = js & 1, qb = seg & 1;
-            const uint32_t i = 2 * js;
+            const int u = js & 1, qb = seg & 1, half = (int)(js % PACK);
+            const uint32_t i = 2 * (js / PACK);
             const int slot = (int)(i % ST);
             if (ta == sa.t0) ok = ok && mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
             ok = ok && mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
             if (!ok) return;
             tc_fence_after();
-            const uint64_t dk = sdesc_sw128(base + slot * T::SLOT, 16, 1024);
+            const uint64_t dk = desc_add(sdesc_sw128(base + slot * T::SLOT, 16, 1024), half * 64);
             const uint64_t dq = sdesc_sw128(sQ + qb * T::Q_BYTES, 16, 1024);
             for (int ks = 0; ks < ksteps; ++ks)
                 mma_ss_elect_f8(tmem + u * T::NS, desc_add(dk, (ks >> 2) * T::CHUNK + (ks & 3) * 32),
                                 desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32), kIdescS,
                                 ks > 0 ? 1u : 0u);
             tc_commit_elect(bar(ms.s_full[u]));
-            tc_commit_elect(bar(ms.empty[slot]));
             ++js;
+            if (half + 1 < PACK) return;
+            tc_commit_elect(bar(ms.empty[slot]));
             if (++ta == sa.t1) {
                 tc_commit_elect(bar(ms.q_empty[qb]));
                 ++seg;
@@ -717,13 +735,13 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         if (more && ok) issue_s();
         uint32_t j = 0;
         while (ok && walk.next(a, &s)) {
-            for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
-                const int u = j & 1;
-                const uint32_t i = 2 * j + 1;
+            for (int t = s.t0; ok && t < s.t1; t += (int)(++j % PACK == 0)) {
+                const int u = j & 1, half = (int)(j % PACK);
+                const uint32_t jt = j / PACK, i = 2 * jt + 1;
                 const int slot = (int)(i % ST);
                 ok = mbar_wait_warp(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 // every softmax warp has read the tile's scales
-                if (lane == 0) mbar_arrive(bar(ms.scale_empty[j % kScaleStages]));
+                if (half + 1 == PACK && lane == 0) mbar_arrive(bar(ms.scale_empty[jt % kScaleStages]));
                 ok = ok && mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
                 if (!ok) break;
                 tc_fence_after();
@@ -733,10 +751,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
                     for (int ks = 0; ks < kTile / 32; ++ks)
-                        mma_ss_elect_f8(tmem + T::TM_O + c * T::NP, desc_add(dv, c * T::CHUNK + ks * 4096),
+                        mma_ss_elect_f8(tmem + T::TM_O + (c + half) * T::NP, desc_add(dv, c * T::CHUNK + ks * 4096),
                                         desc_add(dp, ks * 1024), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                 tc_commit_elect(bar(ms.pv_done[u]));
-                tc_commit_elect(bar(ms.empty[slot]));
+                if (half + 1 == PACK) tc_commit_elect(bar(ms.empty[slot]));
                 if (more) issue_s();
             }
         }
@@ -778,7 +796,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 for (int i = lane; i < entries; i += 32) {
                     const int at = i << a.run;
                     const int page = i < 32 ? pg : page_at(t, at);
-                    const uint32_t key = (uint32_t)(t * kTile + at);
+                    const uint32_t key = (uint32_t)(t * TK + at);
                     const bool here = key < (uint32_t)len, valid = page >= 0 && page < a.num_pages;
                     if (here && !valid) ms.bad[qb] = 1;
                     const bool copy = here && valid;  // keys not there: scale 0
@@ -799,7 +817,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
         // Every warp runs every step even after a wait has given up (waits then return at
         // once), so that none is left behind at a barrier.
         const int wg = warp >> 2, w4 = warp & 3;
-        const int kk = threadIdx.x & 127;  // key of the tile; lane of O^T (head dimension)
+        const int kk = threadIdx.x & 127;  // key of the step; lane of O^T (head dimension)
         const int rw0 = wg * RW;           // this warpgroup's rows of the CTA's
         const int id = 1 + wg;             // its named barrier
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
@@ -824,17 +842,19 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 if (kk == 0) ms.nan_any = 0;
             }
             float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
-            const int full_tiles = max(full_keys, 0) / kTile;  // seen by every row
+            const int full_tiles = max(full_keys, 0) / TK;  // seen by every row
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
             named_barrier_sync(id, 128);
-            for (int t = s.t0; t < s.t1; ++t, ++j) {
-                const int u = j & 1;
-                const int key = t * kTile + kk;
-                const int st = (int)(j % kScaleStages);
-                mbar_wait(bar(ms.scale_full[st]), (j / kScaleStages) & 1, g, SITE_DEC_FULL);
-                float ks = ms.k_scale[st][kk >> a.run], vs = ms.v_scale[st][kk >> a.run];
+            for (int t = s.t0; t < s.t1; t += (int)(++j % PACK == 0)) {
+                const int u = j & 1, half = (int)(j % PACK);
+                const uint32_t jt = j / PACK;
+                const int at = kk * PACK + half, key = t * TK + at;
+                const int st = (int)(jt % kScaleStages);
+                const bool first = t == s.t0 && half == 0;
+                mbar_wait(bar(ms.scale_full[st]), (jt / kScaleStages) & 1, g, SITE_DEC_FULL);
+                float ks = ms.k_scale[st][at >> a.run], vs = ms.v_scale[st][at >> a.run];
                 mbar_wait(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 __syncwarp();
                 tc_fence_after();
@@ -869,7 +889,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                             if (key >= ms.limit[qb][rw0 + r]) x[r] = -INFINITY;
                     }
                 };
-                bool move = t == s.t0;  // the first tile always sets them
+                bool move = first;  // which always sets them
                 if (!move) {
                     scores(std::true_type());
                     float top = fmaxf(x[0], x[1]);
@@ -878,7 +898,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     move = vote_group(id, top > kMoveLog2 || vs > vref);
                 }
                 if (move) {
-                    // new references: the tile's maximum where it passes the old one by 2^6
+                    // new references: the step's maximum where it passes the old one by 2^6
                     scores(std::false_type());
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -912,12 +932,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         l[r] *= ms.alpha[rw0 + r];
                         x[r] += ms.nref[rw0 + r];
                     }
-                    if (t > s.t0) {  // O^T to the new references, once PV of the tile before is done
+                    if (!first) {  // O^T to the new references, once PV of the step before is done
                         const float fo = vref > 0.f ? v_old / vref : 1.f;
                         mbar_wait_warp(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < NCH; ++c)
+                        for (int c = 0; c < NCH * PACK; ++c)
 #pragma unroll 1
                             for (int n = 0; n < 3 * RW; n += RW) {
                                 float o[RW];
@@ -949,9 +969,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                         h[0] = sub_f16x2(h[0], h[0] & 0xff00ff00u);
                         h[1] = sub_f16x2(h[1], h[1] & 0xff00ff00u);
                     }
-                    term[2][r / 4] = e5m2x2_of(h[0]) | e5m2x2_of(h[1]) << 16;
+                    term[2][r / 4] = e5m2x2_of(times32(h[0])) | e5m2x2_of(times32(h[1])) << 16;
                 }
-                // the buffer's last reader, PV of tile j - 2, was issued before S of this tile, whose
+                // the buffer's last reader, PV of step j - 2, was issued before S of this step, whose
                 // commit covers all that was issued before it
                 const uint32_t p0 = sP + u * T::P_BYTES;
                 if constexpr (RW == 8) {
@@ -968,19 +988,21 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     // rows of V behind the last key, whatever lies there, become 0; so do the NaN
                     // codes of keys that some rows see and others do not, and the rows that
                     // do are noted
-                    const uint32_t i = 2 * j + 1;
+                    const uint32_t i = 2 * jt + 1;
                     const int slot = (int)(i % ST);
                     mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
                     const uint32_t v0 = base + slot * T::SLOT + kk * 128;
+                    constexpr int kGroups = NCH * 8 / PACK;  // of 16 columns
+                    auto group = [&](int e) { return ((e & 7) + half * kGroups ^ (kk & 7)) << 4; };
                     if (key >= len) {
 #pragma unroll
-                        for (int e = 0; e < NCH * 8; ++e)
-                            sts128(v0 + (e >> 3) * T::CHUNK + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                        for (int e = 0; e < kGroups; ++e)
+                            sts128(v0 + (e >> 3) * T::CHUNK + group(e), 0u, 0u, 0u, 0u);
                     } else if (key >= full_keys) {
 #pragma unroll 1
-                        for (int e = 0; e < NCH * 8; ++e) {
+                        for (int e = 0; e < kGroups; ++e) {
                             uint4 *v = reinterpret_cast<uint4 *>(gbase + slot * T::SLOT + (e >> 3) * T::CHUNK +
-                                                                 kk * 128 + (((e & 7) ^ (kk & 7)) << 4));
+                                                                 kk * 128 + group(e));
                             uint4 w = *v;
                             uint32_t *x4 = &w.x, bits = 0;  // of the 16 columns from 16 e on
 #pragma unroll
@@ -1037,6 +1059,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
             mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
             tc_fence_after();
             named_barrier_sync(id, 128);
+            const int upper = PACK == 2 ? w4 >> 1 : 0;  // lanes of the odd keys' half
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c) {
                 const int dd = c * 128 + kk;
@@ -1044,7 +1067,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                 for (int q = 0; q < RW && q < rows; q += 8) {
                     float o0[8], o1[8], o2[8];
                     __syncwarp();
-                    const uint32_t at = t_o + c * T::NP + q;
+                    const uint32_t at = t_o + (c + upper) * T::NP + q;
                     tmem_ld(at, o0);
                     tmem_ld(at + RW, o1);
                     tmem_ld(at + 2 * RW, o2);
@@ -1055,7 +1078,19 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB>::THREADS, Dec8Tile<NCH, RB>:
                     const float4 f1 = *reinterpret_cast<const float4 *>(&ms.alpha[rw0 + q + 4]);
                     const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o0[e] = (o0[e] + (o1[e] + o2[e])) * f[e];
+                    for (int e = 0; e < 8; ++e) o0[e] += fmaf(o2[e], 0x1p-5f, o1[e]);
+                    if constexpr (PACK == 2) {  // the odd keys' part, through a buffer of P, idle now
+                        float *part = reinterpret_cast<float *>(gbase + T::OFF_P) + q * 64 + (kk & 63);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (upper) part[e * 64] = o0[e];
+                        named_barrier_sync(id, 128);
+                        if (upper) continue;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o0[e] += part[e * 64];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o0[e] *= f[e];
                     if (a.causal && ms.nan_any) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -1261,25 +1296,26 @@ __global__ void __launch_bounds__(32 * kCutRows)
 }
 
 // CTAs of a launch: all that are resident, or the largest number of tiles there can be.
-template <int NCH, int RB>
+template <int NCH, int RB, int PACK>
 int dec8_ctas(const Decode8Params &p) {
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
-    const long long nt = ((long long)p.page_size * p.max_pages + kTile - 1) / kTile;
+    const int tk = Dec8Tile<NCH, RB, PACK>::TK;
+    const long long nt = ((long long)p.page_size * p.max_pages + tk - 1) / tk;
     const long long items = (long long)p.B * p.Hkv * ((R + RB - 1) / RB);
-    const long long most = (long long)p.num_sms * Dec8Tile<NCH, RB>::CTAS;
+    const long long most = (long long)p.num_sms * Dec8Tile<NCH, RB, PACK>::CTAS;
     return (int)(items >= most || items * nt >= most ? most : items * nt);
 }
 
-template <int NCH, int RB>
+template <int NCH, int RB, int PACK>
 size_t dec8_bytes(const Decode8Params &p, size_t *l_offset) {
-    const size_t rows = (size_t)dec8_ctas<NCH, RB>(p) * 2 * RB;
+    const size_t rows = (size_t)dec8_ctas<NCH, RB, PACK>(p) * 2 * RB;
     *l_offset = rows * p.d * sizeof(float);  // a multiple of 16
     return *l_offset + rows * sizeof(float);
 }
 
-template <int NCH, int RB>
+template <int NCH, int RB, int PACK>
 int launch_t(const Decode8Params &p, cudaStream_t stream) {
-    using T = Dec8Tile<NCH, RB>;
+    using T = Dec8Tile<NCH, RB, PACK>;
     Dec8Args a{};
     a.tm_k = p.tm_k;
     a.tm_v = p.tm_v;
@@ -1291,7 +1327,7 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.lse = p.lse;
     size_t l_offset;
-    dec8_bytes<NCH, RB>(p, &l_offset);
+    dec8_bytes<NCH, RB, PACK>(p, &l_offset);
     a.part_o = static_cast<float *>(p.workspace);
     a.part_l = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + l_offset);
     a.by_page = fast_div((uint32_t)p.page_size);
@@ -1307,16 +1343,17 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.groups = p.page_size / p.group;
     a.R = p.H / p.Hkv * p.Nq;
     a.row_blocks = (a.R + RB - 1) / RB;
-    a.box = decode8_box_rows(p.page_size);
+    a.box = decode8_box_rows(p.page_size / PACK);
+    a.tile_log2 = PACK == 2 ? 8 : 7;
     a.run = p.group % 4 == 0 ? 2 : 0;  // four keys of a tile share a page and a group, or none do
     a.causal = p.causal;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
-    auto kern = fa_decode8_kernel<NCH, RB>;
+    auto kern = fa_decode8_kernel<NCH, RB, PACK>;
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
-    const int n_cta = dec8_ctas<NCH, RB>(p);
+    const int n_cta = dec8_ctas<NCH, RB, PACK>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     const long long rows = (long long)p.B * p.H * p.Nq;
     if (rows <= 8LL * p.num_sms)  // as many CTAs as are resident
@@ -1328,32 +1365,50 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
                             stream, 1, a, n_cta);
 }
 
-// Calls f with the tile that serves R query rows per key/value head of dimension d.
+// Two keys to a row of a tile where a row is half of one and up to 16 query rows leave the
+// time to copies.  (A key's number plus a tile's stays below 2^31.)
+bool packs(int d, long long R, int page_size, int max_pages) {
+    return d == 64 && R <= 16 && page_size % 2 == 0 && (long long)page_size * max_pages < (1LL << 31) - 256;
+}
+
+// Calls f with the tile that serves the call's query rows per key/value head: the constants
+// NCH, RB and PACK.
 template <typename F>
-auto with_tile(int d, long long R, F f) {
+auto with_tile(const Decode8Params &p, F f) {
     using std::integral_constant;
-    if (d == 256) {
-        if (R <= 8) return f(integral_constant<int, 2>(), integral_constant<int, 8>());
-        if (R <= 16) return f(integral_constant<int, 2>(), integral_constant<int, 16>());
-        return f(integral_constant<int, 2>(), integral_constant<int, 32>());
+    using One = integral_constant<int, 1>;
+    using Two = integral_constant<int, 2>;
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    if (p.d == 256) {
+        if (R <= 8) return f(Two(), integral_constant<int, 8>(), One());
+        if (R <= 16) return f(Two(), integral_constant<int, 16>(), One());
+        return f(Two(), integral_constant<int, 32>(), One());
     }
-    if (R <= 8) return f(integral_constant<int, 1>(), integral_constant<int, 8>());
-    if (R <= 16) return f(integral_constant<int, 1>(), integral_constant<int, 16>());
-    if (R <= 32) return f(integral_constant<int, 1>(), integral_constant<int, 32>());
-    return f(integral_constant<int, 1>(), integral_constant<int, 64>());
+    if (packs(p.d, R, p.page_size, p.max_pages)) {
+        if (R <= 8) return f(One(), integral_constant<int, 8>(), Two());
+        return f(One(), integral_constant<int, 16>(), Two());
+    }
+    if (R <= 8) return f(One(), integral_constant<int, 8>(), One());
+    if (R <= 16) return f(One(), integral_constant<int, 16>(), One());
+    if (R <= 32) return f(One(), integral_constant<int, 32>(), One());
+    return f(One(), integral_constant<int, 64>(), One());
 }
 
 }  // namespace
 
-int decode8_box_rows(int page_size) {
+int decode8_pack(const Decode8Params &p) {
+    return with_tile(p, [](auto, auto, auto pack) { return (int)pack; });
+}
+
+int decode8_box_rows(int rows) {
     int box = 1;
-    while (box < kTile && page_size % (2 * box) == 0) box *= 2;
+    while (box < kTile && rows % (2 * box) == 0) box *= 2;
     return box;
 }
 
 long long decode8_max_tiles(const Decode8Params &p) {
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
-    return with_tile(p.d, R, [&](auto, auto rb) {
+    return with_tile(p, [&](auto, auto rb, auto) {
         const long long nt = ((long long)p.page_size * p.max_pages + kTile - 1) / kTile;
         const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
         return items >= (1LL << 31) ? items : items * nt;
@@ -1361,15 +1416,15 @@ long long decode8_max_tiles(const Decode8Params &p) {
 }
 
 size_t decode8_workspace_bytes(const Decode8Params &p) {
-    return with_tile(p.d, (long long)(p.H / p.Hkv) * p.Nq, [&](auto nch, auto rb) {
+    return with_tile(p, [&](auto nch, auto rb, auto pack) {
         size_t l_offset;
-        return dec8_bytes<decltype(nch)::value, decltype(rb)::value>(p, &l_offset);
+        return dec8_bytes<decltype(nch)::value, decltype(rb)::value, decltype(pack)::value>(p, &l_offset);
     });
 }
 
 int launch_decode8(const Decode8Params &p, cudaStream_t stream) {
-    return with_tile(p.d, (long long)(p.H / p.Hkv) * p.Nq, [&](auto nch, auto rb) {
-        return launch_t<decltype(nch)::value, decltype(rb)::value>(p, stream);
+    return with_tile(p, [&](auto nch, auto rb, auto pack) {
+        return launch_t<decltype(nch)::value, decltype(rb)::value, decltype(pack)::value>(p, stream);
     });
 }
 

@@ -215,8 +215,8 @@ int launch_copy(CopyParams &p, cudaStream_t stream);  // fills first_unit
 
 // Attention over the paged e4m3 cache.
 struct Decode8Params {
-    CUtensorMap tm_k, tm_v;          // bytes (d, page_size, num_pages * Hkv), boxes of 128 x
-                                     // decode8_box_rows(page_size) x 1
+    CUtensorMap tm_k, tm_v;          // bytes (pack * d, rows = page_size / pack, num_pages * Hkv)
+                                     // with pack = decode8_pack, boxes 128 x decode8_box_rows(rows) x 1
     const void *q;                   // bf16 [B][H][Nq][d]
     const float *k_scale, *v_scale;  // [num_pages][Hkv][page_size / group]
     const int *block_table, *seq_lens;
@@ -228,7 +228,8 @@ struct Decode8Params {
     int *status;
     int num_sms;
 };
-int decode8_box_rows(int page_size);
+int decode8_pack(const Decode8Params &p);  // keys per row of the tensor maps, of the sizes
+int decode8_box_rows(int rows);
 // Tiles of 128 keys of all items at the longest possible lengths; the kernels count in ints.
 long long decode8_max_tiles(const Decode8Params &p);
 size_t decode8_workspace_bytes(const Decode8Params &p);  // of its sizes and num_sms

@@ -72,8 +72,8 @@ def gather(codes, scale, table_row, n, h):
 
 def decode(q, k_codes, v_codes, k_scale, v_scale, table, lens, causal, scale):
     """(o, lse, terms): float64 attention of q [B, H, Nq, d]; terms holds per row what error
-    bounds need: sum_j p_j |v_j| per column, sum_j |v_j| p_max, and the largest over the seen
-    keys of scale * sum_c |q_c k_c|."""
+    bounds need: sum_j p_j |v_j| per column, sum_j |code of v_j| times p_max and the largest value
+    scale of the head's n tokens, and the largest over the seen keys of scale * sum_c |q_c k_c|."""
     B, H, Nq, d = q.shape
     Hkv = k_codes.shape[1]
     o = np.zeros((B, H, Nq, d))
@@ -85,6 +85,10 @@ def decode(q, k_codes, v_codes, k_scale, v_scale, table, lens, causal, scale):
             kvh = h // (H // Hkv)
             k = gather(k_codes, k_scale, table[b], n, kvh)
             v = gather(v_codes, v_scale, table[b], n, kvh)
+            codes = np.abs(gather(v_codes, np.ones_like(v_scale), table[b], n, kvh))
+            ps, groups = v_codes.shape[2], v_scale.shape[2]
+            at = np.arange(n)
+            largest = v_scale[table[b][at // ps], kvh, at % ps // (ps // groups)].max(initial=0.0)
             for i in range(Nq):
                 end = max(0, min(n, n - Nq + 1 + i)) if causal else n
                 if end == 0:
@@ -96,7 +100,7 @@ def decode(q, k_codes, v_codes, k_scale, v_scale, table, lens, causal, scale):
                 p /= p.sum()
                 o[b, h, i] = p @ v[:end]
                 pv[b, h, i] = p @ np.abs(v[:end])
-                vmax[b, h, i] = p.max() * np.abs(v[:end]).sum(0)
+                vmax[b, h, i] = p.max() * float(largest) * codes[:end].sum(0)
                 qk[b, h, i] = scale * (np.abs(k[:end]) @ np.abs(q[b, h, i])).max()
     return o, lse, (pv, vmax, qk)
 

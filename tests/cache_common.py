@@ -41,11 +41,14 @@ def check_decode(o, lse, ref, what=""):
     The bound, from where the operation may round (u32 = 2^-24; half a bf16 step is 2^-8 of the
     value): a score is a sum of d products in fp32, whose error is allowed 16 u32 of the sum of
     its magnitudes (2^-20), and shifts L by at most that and every p by twice that relatively; p
-    enters the product with V with a relative error of 2^-9 + 2^-11 (rounded to f16's 11 bits, half
-    a step of which is 2^-11, then kept as three e5m2 numbers of 3 bits: the first two truncated,
-    which leaves less than 2^-5, the third rounded to half of its step, 2^-9) and an absolute one
-    of 2^-22 of the row's largest; the sums over keys and L itself are fp32 (2^-16 relative for up to 2^8
-    accumulation steps of u32); O is rounded to bf16."""
+    times its value scale is rounded to f16's 11 bits (2^-11 relative, or half of its smallest
+    step, 2^-25) and kept as three e5m2 numbers of 3 bits, the first two truncated, which leaves
+    less than 2^-5 of the value, or e5m2's smallest step 2^-16; the third, of 2^5 times that, is
+    rounded to half a step of 3 bits: 2^-9 relative, or 2^-20.  Here 2^9 stands for a reference
+    that is at most the row's largest p times 16 times the head's largest value scale, so the
+    absolute error of p times the scale is at most (2^-20 + 2^-25) 2^-9 2^4 < 2^-24 of those two's
+    product, and it meets each code once; the sums over keys and L itself are fp32 (2^-16
+    relative for up to 2^8 accumulation steps of u32); O is rounded to bf16."""
     ro, rl, (pv, vmax, qk) = ref
     o, lse = np.asarray(o, dtype=np.float64), np.asarray(lse, dtype=np.float64)
     es = 2.0 ** -20 * qk
@@ -56,7 +59,7 @@ def check_decode(o, lse, ref, what=""):
     el = np.where(empty, 0, np.abs(np.where(empty, 0, lse) - np.where(empty, 0, rl)))
     assert np.all(el <= bl), f"{what}: L off by {el.max():.3e}, worst ratio {(el / bl).max():.2f}"
     bo = (2.0 ** -8 * np.abs(ro) + (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -16 + 2 * es[..., None]) * pv * (1 + 2.0 ** -8)
-          + 2.0 ** -22 * vmax + 1e-30)
+          + 2.0 ** -24 * vmax + 1e-30)
     eo = np.abs(o - ro)
     assert np.all(eo <= bo), f"{what}: O off by {eo.max():.3e}, worst ratio {(eo / bo).max():.2f}"
     return float((eo / bo).max()), float((el / bl).max())

@@ -88,6 +88,21 @@ def test_long_sequences_are_cut_and_merged(fa, B, H, Hkv, Nq, d, lens):
     _check(fa, _problem(B, H, Hkv, Nq, d, 64, 32, lens, seed=d), causal=Nq > 1)
 
 
+@pytest.mark.parametrize("ps,group", [(2, 1), (2, 2), (6, 3), (7, 7), (16, 8), (64, 32), (512, 128)])
+@pytest.mark.parametrize("H,Hkv,Nq", [(2, 2, 1), (4, 2, 4), (4, 1, 4)])
+def test_keys_of_half_a_row(fa, ps, group, H, Hkv, Nq):
+    """d = 64, where two keys share a row of a tile: sequences that end in either half of one, on
+    both sides of a tile of 128 and of 256 keys."""
+    lens = [1, 2, 127, 128, 129, 255, 256, 257, 258, 511, 512, 513, 1000, 0, 3001]
+    _check(fa, _problem(len(lens), H, Hkv, Nq, 64, ps, group, lens, seed=ps), causal=Nq > 1)
+
+
+def test_a_chunk_of_many_queries(fa):
+    """A causal chunk of 300 new tokens behind, and as all of, a sequence."""
+    for d in (64, 128, 256):
+        _check(fa, _problem(3, 4, 2, 300, d, 16, 16, [300, 1111, 299], seed=d), causal=True)
+
+
 def test_many_sequences(fa):
     lens = [(b * 131) % 300 for b in range(400)]
     _check(fa, _problem(400, 2, 1, 1, 64, 16, 16, lens, seed=1))
