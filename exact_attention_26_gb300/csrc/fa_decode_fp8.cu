@@ -1365,10 +1365,22 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
                             stream, 1, a, n_cta);
 }
 
-// Two keys to a row of a tile where a row is half of one and up to 16 query rows leave the
-// time to copies.  (A key's number plus a tile's stays below 2^31.)
-bool packs(int d, long long R, int page_size, int max_pages) {
-    return d == 64 && R <= 16 && page_size % 2 == 0 && (long long)page_size * max_pages < (1LL << 31) - 256;
+// Tiles of 128 keys of all items in blocks of rb rows at the longest possible lengths.
+long long most_tiles(const Decode8Params &p, int rb) {
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    const long long nt = ((long long)p.page_size * p.max_pages + kTile - 1) / kTile;
+    const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
+    return items >= (1LL << 31) ? items : items * nt;
+}
+
+// Two keys to a row of a tile where a key is half of one, up to 16 query rows leave the time
+// to copies, and every CTA may get more than two tiles of 128 keys; with less work, a finer cut
+// is worth more.  (Hkv8 d64 R4, one key and two: B1 1000 keys 6.4 and 7.2 us, 16000 keys 11.9
+// and 12.0 us; B32 of 1..1000 keys 20.7 and 17.1 us; B32 H16 of 30000 keys 238 and 170 us.  A
+// key's number plus a tile's stays below 2^31.)
+bool packs(const Decode8Params &p) {
+    return p.d == 64 && (long long)(p.H / p.Hkv) * p.Nq <= 16 && p.page_size % 2 == 0 &&
+           (long long)p.page_size * p.max_pages < (1LL << 31) - 256 && most_tiles(p, 16) > 4LL * p.num_sms;
 }
 
 // Calls f with the tile that serves the call's query rows per key/value head: the constants
@@ -1384,7 +1396,7 @@ auto with_tile(const Decode8Params &p, F f) {
         if (R <= 16) return f(Two(), integral_constant<int, 16>(), One());
         return f(Two(), integral_constant<int, 32>(), One());
     }
-    if (packs(p.d, R, p.page_size, p.max_pages)) {
+    if (packs(p)) {
         if (R <= 8) return f(One(), integral_constant<int, 8>(), Two());
         return f(One(), integral_constant<int, 16>(), Two());
     }
@@ -1407,12 +1419,7 @@ int decode8_box_rows(int rows) {
 }
 
 long long decode8_max_tiles(const Decode8Params &p) {
-    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
-    return with_tile(p, [&](auto, auto rb, auto) {
-        const long long nt = ((long long)p.page_size * p.max_pages + kTile - 1) / kTile;
-        const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
-        return items >= (1LL << 31) ? items : items * nt;
-    });
+    return with_tile(p, [&](auto, auto rb, auto) { return most_tiles(p, rb); });
 }
 
 size_t decode8_workspace_bytes(const Decode8Params &p) {

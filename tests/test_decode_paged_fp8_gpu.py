@@ -18,11 +18,13 @@ def fa():
     return load_fa()
 
 
-def _problem(B, H, Hkv, Nq, d, ps, group, lens, seed=0, spread=1.0, extra=2, qmul=1.0):
+def _problem(B, H, Hkv, Nq, d, ps, group, lens, seed=0, spread=1.0, extra=2, qmul=1.0,
+             room=1):
     """(q, kc, vc, ks, vs, table, lens) on the CPU; rows behind the last token and whole unused
-    pages hold NaN codes, their scales are NaN too, unused table entries point nowhere."""
+    pages hold NaN codes, their scales are NaN too, unused table entries point nowhere.  The table
+    has room for at least `room` tokens per sequence (longer sequences may be cut differently)."""
     num = sum(-(-n // ps) for n in lens) + extra
-    width = max(1, max(-(-n // ps) for n in lens)) + 1
+    width = max(-(-room // ps), max(-(-n // ps) for n in lens)) + 1
     table = make_table(lens, ps, width, num, seed, unused=1 << 30)
     kc, ks = make_cache(num, Hkv, ps, d, group, seed + 1, spread)
     vc, vs = make_cache(num, Hkv, ps, d, group, seed + 2, spread)
@@ -94,7 +96,8 @@ def test_keys_of_half_a_row(fa, ps, group, H, Hkv, Nq):
     """d = 64, where two keys share a row of a tile: sequences that end in either half of one, on
     both sides of a tile of 128 and of 256 keys."""
     lens = [1, 2, 127, 128, 129, 255, 256, 257, 258, 511, 512, 513, 1000, 0, 3001]
-    _check(fa, _problem(len(lens), H, Hkv, Nq, 64, ps, group, lens, seed=ps), causal=Nq > 1)
+    for room in (1, 150000):
+        _check(fa, _problem(len(lens), H, Hkv, Nq, 64, ps, group, lens, seed=ps, room=room), causal=Nq > 1)
 
 
 def test_a_chunk_of_many_queries(fa):
@@ -171,12 +174,12 @@ def test_nan_and_infinities_stay_in_their_rows(fa):
     assert fa.fa_device_status(None) == 0
 
 
-@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("d,room", [(64, 1), (64, 150000), (96, 1), (128, 1), (256, 1)])
 @pytest.mark.parametrize("H,Hkv,Nq", [(2, 2, 3), (4, 1, 4), (8, 2, 7), (8, 1, 8)])
-def test_causal_rows_are_free_of_later_tokens_nans(fa, d, H, Hkv, Nq):
+def test_causal_rows_are_free_of_later_tokens_nans(fa, d, room, H, Hkv, Nq):
     """NaN codes in K and V of the last Nq tokens: rows before them stay finite."""
-    for n in (Nq, 127, 128, 130, 300):
-        prob = list(_problem(2, H, Hkv, Nq, d, 16, 16, [n, 40], seed=n + d))
+    for n in (Nq, 127, 128, 130, 255, 256, 300):
+        prob = list(_problem(2, H, Hkv, Nq, d, 16, 16, [n, 40], seed=n + d, room=room))
         table = prob[5]
         hits = [(n - 1, 0, 3), (n - 2, Hkv - 1, d - 1), (n - 2, 0, 0), (n - Nq, 0, d // 2)]
         for key, h, col in hits[:3] if n % 2 else hits:
@@ -192,6 +195,27 @@ def test_causal_rows_are_free_of_later_tokens_nans(fa, d, H, Hkv, Nq):
         check_decode(clean[0][rows], lse[rows], (clean[1][rows], ref[1][rows],
                                                  (clean[2][rows], clean[3][rows], ref[2][2][rows])))
     assert fa.fa_device_status(None) == 0
+
+
+@pytest.mark.parametrize("room", [1, 150000])
+def test_captured_calls_of_half_rows_follow_the_lengths(fa, room):
+    prob = _problem(4, 8, 2, 2, 64, 16, 8, [3000, 1000, 500, 64], seed=21, room=room)
+    dev = [t.to(DEV) for t in prob]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = fa.decode_paged_fp8(*dev, causal=True)
+    for lens in ([3000, 1000, 500, 64], [1, 0, 500, 63], [0, 0, 0, 0], [257, 998, 129, 1]):
+        dev[6].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = oracle_decode(*prob[:6], torch.tensor(lens), True, 0.125)
+        check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), ref, str(lens))
+    dev[5][1, 30] = -5
+    dev[6].copy_(torch.tensor([3000, 1000, 500, 64], dtype=torch.int32))
+    o.fill_(3.0)
+    g.replay()
+    assert fa.fa_device_status(None) == 7
+    assert bool((o[1] == 3.0).all()) and not bool((o[[0, 2, 3]] == 3.0).all())
 
 
 def test_shared_pages_and_repeated_entries(fa):
