@@ -33,7 +33,7 @@
 // ends in), which a second kernel merges by log-sum-exp.
 //
 // Warps: one or more softmax warpgroups of up to 16 rows each (they also write the results),
-// then MMA issue and tensor memory, TMA, and one that prepares query terms and key scales.
+// then one each for MMA issue and tensor memory, TMA, key and value scales, and query terms.
 // Per CTA: a ring of 16 KB slots (K_0 V_0 K_1 V_1 ...; 32 KB at d = 256) that runs across
 // items, two S slots, two P buffers, two query buffers, three tiles of scales.
 //
@@ -84,7 +84,7 @@ struct Dec8Tile {
     static constexpr int NS = 2 * RB;                    // columns of S^T: two terms of q
     static constexpr int NP = (3 * RB + 15) / 16 * 16;   // columns of O^T: three terms of p
     static constexpr int CTAS = (NCH == 1 && RB <= 32) ? 2 : 1;  // resident per SM
-    static constexpr int THREADS = 32 * (4 * NWG + 3);
+    static constexpr int THREADS = 32 * (4 * NWG + 4);
     static constexpr int TK = PACK * kTile;              // keys of a tile
     static constexpr uint32_t CHUNK = kTile * 128;
     static constexpr uint32_t SLOT = NCH * CHUNK;
@@ -128,6 +128,7 @@ struct Dec8Misc {
     alignas(16) float v_scale[kScaleStages][TK];
     alignas(16) float row_scale[2][RB];  // per query buffer: score -> base-2 exponent, before the key's scale
     alignas(16) int limit[2][RB];        // keys the row sees
+    int len[2];                          // per query buffer: the sequence's length
     alignas(16) float nref[RB];          // minus the reference of the row's scores, base 2
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
@@ -171,6 +172,7 @@ struct Dec8Args {
     int R, row_blocks;              // query rows per key/value head, blocks of RB of them
     int box;                        // 128-byte rows per TMA box
     int tile_log2;                  // log2 of the keys per tile
+    int start;                      // tiles that an item's start counts as in the cut, up to 3
     int run;                        // log2 of the keys that one entry of the scales stands for
     int causal;
     float scale_log2;
@@ -238,11 +240,24 @@ __device__ __forceinline__ bool vote_group(int id, bool yes) {
     return r != 0;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 __device__ __forceinline__ float warp_max(float x) {  // NaN is passed over
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// 1 / x to 2^-23 (x normal), which O's rounding to bf16 hides, without a divide's code.
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// 1 / x of a power of two, 2^-126 to 2^126: exponents e and -e.
+__device__ __forceinline__ float inverse2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // e4m3 of two f16 values (16 bits), and back, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_of(uint32_t h) {
@@ -354,27 +369,40 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t base, int n, int x) {
 __device__ __forceinline__ bool len_ok(const Dec8Args &a, int len) {
     return len >= 0 && (long long)len <= (long long)a.page_size * a.max_pages;
 }
-// Tiles of one (head, row block) item of sequence b.
-__device__ __forceinline__ int tiles_of(const Dec8Args &a, int b) {
-    const int len = a.seq_lens[b];
+// Tiles of one (head, row block) item of a sequence.
+__device__ __forceinline__ int tiles_of_len(const Dec8Args &a, int len) {
     return len_ok(a, len) ? (int)(((long long)len + (1 << a.tile_log2) - 1) >> a.tile_log2) : 0;
 }
+__device__ __forceinline__ int tiles_of(const Dec8Args &a, int b) { return tiles_of_len(a, a.seq_lens[b]); }
 
-// Tiles (of one head and row block) of all sequences, and of those before `upto`; one warp.
-__device__ __forceinline__ int count_tiles(const Dec8Args &a, int upto, int *before) {
-    const int lane = threadIdx.x & 31;
-    int all = 0, pre = 0;
-    for (int b = lane; b < a.B; b += 32) {
-        const int t = tiles_of(a, b);
-        all += t;
-        if (b < upto) pre += t;
-    }
-    *before = __reduce_add_sync(kFull, pre);
-    return __reduce_add_sync(kFull, all);
+// The cut is even in tiles and item starts: an item that begins inside a CTA's range costs it
+// the results of the one before and a new set of queries, and counts as a.start tiles.  With few
+// tiles per CTA the finest cut is better.
+// (Positions below count both: item i's tile t is at its base + start + t.)
+__device__ __forceinline__ int start_of(const Dec8Args &a, int tiles, int n_cta) {
+    return tiles >= 4 * n_cta && tiles < (1 << 29) ? a.start : 0;
 }
 
-// An even cut of `total` tiles over the n CTAs that get any: the first `more` of them take
-// one tile more than the others.
+// Tiles (of one head and row block) and non-empty sequences, of all and of those before `upto`;
+// one warp.
+struct Count {
+    int tiles, full, tiles_before, full_before;
+};
+__device__ __forceinline__ Count count_tiles(const Dec8Args &a, int upto) {
+    const int lane = threadIdx.x & 31;
+    Count c{};
+    for (int b = lane; b < a.B; b += 32) {
+        const int t = tiles_of(a, b);
+        c.tiles += t;
+        c.full += t > 0;
+        if (b < upto) c.tiles_before += t, c.full_before += t > 0;
+    }
+    return Count{__reduce_add_sync(kFull, c.tiles), __reduce_add_sync(kFull, c.full),
+                 __reduce_add_sync(kFull, c.tiles_before), __reduce_add_sync(kFull, c.full_before)};
+}
+
+// An even cut of `total` positions over the n CTAs that get any: the first `more` of them take
+// one more than the others.
 struct Cut {
     int n, each, more;
     Cut() = default;
@@ -384,7 +412,7 @@ struct Cut {
         more = total - each * n;
     }
     __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
-    __device__ __forceinline__ int owner(int g) const {  // the CTA of tile g
+    __device__ __forceinline__ int owner(int g) const {  // the CTA of position g
         const int big = more * (each + 1);
         return g < big ? g / (each + 1) : more + (g - big) / each;
     }
@@ -396,45 +424,61 @@ struct Segment {
     int t0, t1, nt;   // tiles [t0, t1) of the item's nt
 };
 struct Walk {
-    int left, b, item, t, nt;
+    int left, b, item, at, nt, start;  // positions left, and the next one's place in its item
+    int len_next;  // of sequence b + 1, under way while b is worked on
+    __device__ __forceinline__ int tile() const { return max(at - start, 0); }
     __device__ __forceinline__ bool next(const Dec8Args &a, Segment *s) {
-        if (left <= 0) return false;
-        while (t >= nt) {  // the next item that has tiles
-            t = 0;
-            if (++item >= a.Hkv * a.row_blocks || nt == 0) {
-                item = 0;
-                if (++b >= a.B) return false;  // not reached: `left` ends first
-                nt = tiles_of(a, b);
+        while (left > 0) {
+            if (nt == 0 || at >= start + nt) {  // the next item
+                at = 0;
+                if (++item >= a.Hkv * a.row_blocks || nt == 0) {
+                    item = 0;
+                    if (++b >= a.B) return false;  // not reached: `left` ends first
+                    nt = tiles_of_len(a, len_next);
+                    if (b + 1 < a.B) len_next = a.seq_lens[b + 1];
+                }
+                if (nt == 0) continue;
             }
+            const int end = min(start + nt, at + left);
+            s->t0 = tile();
+            left -= end - at;
+            at = end;
+            s->t1 = tile();
+            if (s->t1 == s->t0) continue;  // the range ends in the item's start
+            s->b = b;
+            s->kvh = a.row_blocks == 1 ? item : item / a.row_blocks;
+            s->rb = item - s->kvh * a.row_blocks;
+            s->nt = nt;
+            return true;
         }
-        s->b = b;
-        s->kvh = item / a.row_blocks;
-        s->rb = item - s->kvh * a.row_blocks;
-        s->t0 = t;
-        s->t1 = min(nt, t + left);
-        s->nt = nt;
-        left -= s->t1 - t;
-        t = s->t1;
-        return true;
+        return false;
     }
 };
 
 // Where CTA c of n_cta begins, and the cut; one warp.
 __device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta, Cut *the_cut) {
     const int lane = threadIdx.x & 31, ipb = a.Hkv * a.row_blocks;
-    Walk w{0, 0, 0, 0, 0};
+    Walk w{};
     // the first 32 sequences' tiles stay in a register: most batches are no larger
     const int nt0 = lane < a.B ? tiles_of(a, lane) : 0;
-    int mine = nt0;
-    for (int b = lane + 32; b < a.B; b += 32) mine += tiles_of(a, b);
-    const Cut cut(__reduce_add_sync(kFull, mine) * ipb, n_cta);
+    int mine = nt0, full = nt0 > 0;
+    for (int b = lane + 32; b < a.B; b += 32) {
+        const int nt = tiles_of(a, b);
+        mine += nt;
+        full += nt > 0;
+    }
+    mine = __reduce_add_sync(kFull, mine) * ipb;
+    full = __reduce_add_sync(kFull, full) * ipb;
+    w.start = start_of(a, mine, n_cta);
+    const Cut cut(mine + w.start * full, n_cta);
     *the_cut = cut;
     if (c >= cut.n) return w;
     int g = cut.first(c);
     w.left = cut.first(c + 1) - g;
     for (int b = 0; b < a.B; b += 32) {
         const int nt = b == 0 ? nt0 : b + lane < a.B ? tiles_of(a, b + lane) : 0;
-        int incl = nt * ipb;
+        const int size = (nt > 0 ? nt + w.start : 0) * ipb;
+        int incl = size;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(kFull, incl, o);
@@ -445,9 +489,10 @@ __device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta, 
             const int k = __ffs(m) - 1;
             w.b = b + k;
             w.nt = __shfl_sync(kFull, nt, k);
-            g -= __shfl_sync(kFull, incl, k) - w.nt * ipb;
-            w.item = g / w.nt;
-            w.t = g - w.item * w.nt;
+            g -= __shfl_sync(kFull, incl - size, k);
+            w.item = g / (w.nt + w.start);
+            w.at = g - w.item * (w.nt + w.start);
+            if (w.b + 1 < a.B) w.len_next = a.seq_lens[w.b + 1];
             break;
         }
         g -= __shfl_sync(kFull, incl, 31);
@@ -464,7 +509,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
     using Misc = Dec8Misc<NCH, RB, T::STAGES, T::NWG, T::TK>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
     constexpr int ST = T::STAGES, RW = T::RW, NWG = T::NWG, TK = T::TK;
-    constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
+    constexpr int kMmaWarp = 4 * NWG, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2, kQueryWarp = kMmaWarp + 3;
     extern __shared__ uint8_t dec8_smem[];
     const uint32_t raw = smem_u32(dec8_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -535,9 +580,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         if (warp == kTmaWarp) return lane < boxes ? page_at(t, lane * a.box * PACK) : -1;
         return page_at(t, lane << a.run);
     };
-    if (warp == kTmaWarp || warp == kAuxWarp) {
+    if (warp == kTmaWarp || warp == kAuxWarp || warp == kQueryWarp) {
         some = walk.next(a, &s);
-        if (some) {
+        if (some && warp != kQueryWarp) {
             open();
             pg = first_page(s.t0);
         }
@@ -554,15 +599,14 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
     // is scaled by the power of two that brings its largest magnitude into [128, 256); a row
     // with a NaN or an infinity becomes NaN.  N rows at a time, the next ones' loads under way:
     // one for the softmax warps, whose first segment waits for them (unrolled, code that runs
-    // once takes longer to fetch than to execute), four for the helper warp, which must be done
-    // with all RB rows while the segment before is at its last tiles.
-    auto put_queries = [&](auto at_once, int qb, int len, int r_first, int step) {
+    // once takes longer to fetch than to execute), four for the query warp, alone with all RB.
+    auto put_queries = [&](auto at_once, int qb, int r_first, int step) {
         constexpr int N = decltype(at_once)::value, W = NCH == 2 ? 4 : 2;
         const int E = a.d == 96 ? 4 : a.d / 32;  // elements per lane
         const bool on = lane * E < a.d;
         const int r0 = s.rb * RB, rows = min(RB, a.R - r0);
         const __nv_bfloat16 *src =
-            a.q + (((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0) * a.d + lane * E;
+            a.q + (((long long)s.b * a.Hkv + s.kvh) * a.R + r0) * a.d + lane * E;
         auto load = [&](int r, uint32_t (&w)[W]) {
 #pragma unroll
             for (int i = 0; i < W; ++i) w[i] = 0u;
@@ -578,6 +622,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 w[0] = *reinterpret_cast<const uint32_t *>(p);
             }
         };
+        const int len = a.seq_lens[s.b];
+        for (int r = r_first + lane * step; r < rows; r += 32 * step)  // all rows at once into L2
+            for (int x = 0; x < a.d; x += 64) prefetch_l2(src + (long long)r * a.d - lane * E + x);
         uint32_t rows_w[N][W], next[N][W];
 #pragma unroll
         for (int e = 0; e < N; ++e) load(r_first + e * step, rows_w[e]);
@@ -589,23 +636,28 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             for (int e = 0; e < N; ++e) {
                 const int r = rn + e * step;
                 const uint32_t (&w)[W] = rows_w[e];
-                uint32_t am = 0;
+                uint32_t c1[W / 2], c2[W / 2], ex = 1;
 #pragma unroll
-                for (int i = 0; i < W; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-                am = __reduce_max_sync(kFull, am);
-                const uint32_t ex = max((int)(am >> 7) - 7, 1);
-                const float inv = __uint_as_float((254u - ex) << 23);
-                uint32_t c1[W / 2], c2[W / 2];
+                for (int i = 0; i < W / 2; ++i) c1[i] = c2[i] = 0u;
+                if (r < rows) {
+                    uint32_t am = 0;
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    // 8 significant bits fit f16, and so do both remainders
-                    uint32_t h = pack_f16(__uint_as_float(w[i] << 16) * inv,
-                                          __uint_as_float(w[i] & 0xffff0000u) * inv);
-                    if (am >= 0x7f80u) h = 0x7fff7fffu;
-                    const uint32_t c = e4m3x2_of(h);
-                    const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
-                    c1[i / 2] = i % 2 ? c1[i / 2] | c << 16 : c;
-                    c2[i / 2] = i % 2 ? c2[i / 2] | d << 16 : d;
+                    for (int i = 0; i < W; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                    am = __reduce_max_sync(kFull, am);
+                    ex = max((int)(am >> 7) - 7, 1);
+                    const float inv = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        if (i % 2 && E == 2) continue;
+                        // 8 significant bits fit f16, and so do both remainders
+                        uint32_t h = pack_f16(__uint_as_float(w[i] << 16) * inv,
+                                              __uint_as_float(w[i] & 0xffff0000u) * inv);
+                        if (am >= 0x7f80u) h = 0x7fff7fffu;
+                        const uint32_t c = e4m3x2_of(h);
+                        const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
+                        c1[i / 2] |= c << (16 * (i % 2));
+                        c2[i / 2] |= d << (16 * (i % 2));
+                    }
                 }
                 if (on) {
                     const int n1 = r / RW * (2 * RW) + r % RW;
@@ -623,15 +675,17 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         }
                     }
                 }
-                if (lane == 0) {
-                    ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
-                    ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
-                }
+                if (lane == 0) ms.row_scale[qb][r] = __uint_as_float(ex << 23) * a.scale_log2;
             }
 #pragma unroll
             for (int e = 0; e < N; ++e)
 #pragma unroll
                 for (int i = 0; i < W; ++i) rows_w[e][i] = next[e][i];
+        }
+        if (r_first == 0) {
+            for (int r = lane; r < RB; r += 32)
+                ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
+            if (lane == 0) ms.len[qb] = len;
         }
     };
 
@@ -764,9 +818,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         const Guard g2{a.status, &never, kWaitLimitNs};
         mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
     } else if (warp == kAuxWarp) {
-        // ------------------------------------------- query terms, key and value scales
-        // Query terms of the segments after the first (whose rows the softmax warps, idle then,
-        // share out), and for every tile the scales of its keys, in asynchronous copies.
+        // ------------------------------------------------------ key and value scales
         uint32_t seg = 0, j = 0;
         bool ok = true;
         for (; ok && some; ++seg, some = walk.next(a, &s)) {
@@ -774,18 +826,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             if (seg >= 1) {
                 open();
                 pg = first_page(s.t0);
-                if (seg >= 2)
+                if (seg >= 2)  // `bad` of the segment before the last has been read
                     ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
                 if (!ok) break;
             }
             if (lane == 0) ms.bad[qb] = 0;
             __syncwarp();
-            if (seg >= 1) {
-                put_queries(std::integral_constant<int, 4>(), qb, len, 0, 1);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_n(bar(ms.q_full[qb]), 4 * NWG);
-            }
             for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
                 const int pg_next = first_page(t + 1);
                 const int st = (int)(j % kScaleStages);
@@ -812,6 +858,22 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == kQueryWarp) {
+        // ------------------------------------------------------ query terms
+        // Of the segments after the first, whose rows the softmax warps, idle then, share out: a
+        // warp of its own, because one warp takes longer for 32 rows than a tile takes (B8 H32
+        // Hkv4 Nq4 d64, by the warp of the scales between two segments: XX us).
+        bool ok = true;
+        if (some) some = walk.next(a, &s);
+        for (uint32_t seg = 1; some; ++seg, some = walk.next(a, &s)) {
+            const int qb = seg & 1;
+            if (seg >= 2) ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+            if (!ok) break;
+            put_queries(std::integral_constant<int, 4>(), qb, 0, 1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(bar(ms.q_full[qb]), 4 * NWG);
+        }
     } else {
         // ------------------------------------------------------------ softmax, epilogue
         // Every warp runs every step even after a wait has given up (waits then return at
@@ -827,11 +889,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         float l[RW];
         while (walk.next(a, &s)) {
             const int qb = seg & 1;
-            const int len = a.seq_lens[s.b];
             const int r0 = s.rb * RB + rw0, rows = min(RW, a.R - r0);  // may be none
-            const int full_keys = a.causal ? len - a.Nq + 1 : len;     // keys that every row sees
             if (seg == 0) {
-                put_queries(std::integral_constant<int, 1>(), 0, len, warp, 4 * NWG);
+                put_queries(std::integral_constant<int, 1>(), 0, warp, 4 * NWG);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
@@ -842,11 +902,13 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 if (kk == 0) ms.nan_any = 0;
             }
             float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
-            const int full_tiles = max(full_keys, 0) / TK;  // seen by every row
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
             named_barrier_sync(id, 128);
+            const int len = ms.len[qb];
+            const int full_keys = a.causal ? len - a.Nq + 1 : len;  // keys that every row sees
+            const int full_tiles = max(full_keys, 0) / TK;          // of those only
             for (int t = s.t0; t < s.t1; t += (int)(++j % PACK == 0)) {
                 const int u = j & 1, half = (int)(j % PACK);
                 const uint32_t jt = j / PACK;
@@ -915,7 +977,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     // again (p's terms have the room), and kOneP / v_new stays finite
                     if (vm > v_old) {
                         vref = fmaxf(__uint_as_float(__float_as_uint(vm) & 0x7f800000u) * 16.f, 0x1p-110f);
-                        vmul = kOneP / vref;
+                        vmul = kOneP * inverse2(vref);
                     }
                     if (kk < RW) {
                         const int r = rw0 + kk;
@@ -933,7 +995,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         x[r] += ms.nref[rw0 + r];
                     }
                     if (!first) {  // O^T to the new references, once PV of the step before is done
-                        const float fo = vref > 0.f ? v_old / vref : 1.f;
+                        const float fo = vref > 0.f ? v_old * inverse2(vref) : 1.f;
                         mbar_wait_warp(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
@@ -999,25 +1061,30 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         for (int e = 0; e < kGroups; ++e)
                             sts128(v0 + (e >> 3) * T::CHUNK + group(e), 0u, 0u, 0u, 0u);
                     } else if (key >= full_keys) {
-#pragma unroll 1
+                        auto codes = [&](int e) {
+                            return reinterpret_cast<uint4 *>(gbase + slot * T::SLOT + (e >> 3) * T::CHUNK + kk * 128 +
+                                                             group(e));
+                        };
+                        // a NaN code is 7f or ff: adding 1 to its low 7 bits sets the eighth
+                        auto nan_of = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+                        uint32_t any = 0;
+#pragma unroll 4
                         for (int e = 0; e < kGroups; ++e) {
-                            uint4 *v = reinterpret_cast<uint4 *>(gbase + slot * T::SLOT + (e >> 3) * T::CHUNK +
-                                                                 kk * 128 + group(e));
-                            uint4 w = *v;
-                            uint32_t *x4 = &w.x, bits = 0;  // of the 16 columns from 16 e on
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t nan = ((x4[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                                x4[c] &= ~((nan >> 7) * 255u);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) bits |= (nan >> (8 * k + 7) & 1u) << (4 * c + k);
+                            const uint4 w = *codes(e);
+                            any |= nan_of(w.x) | nan_of(w.y) | nan_of(w.z) | nan_of(w.w);
+                        }
+                        if (any) {
+#pragma unroll 1
+                            for (int e = 0; e < kGroups * 4; ++e) {  // four columns at a time
+                                uint32_t *x = reinterpret_cast<uint32_t *>(codes(e >> 2)) + (e & 3);
+                                const uint32_t nan = nan_of(*x);
+                                if (nan == 0) continue;
+                                *x &= ~((nan >> 7) * 255u);
+                                ms.nan_any = 1;
+                                const uint32_t bits = (nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u);
+                                for (int r = 0; r < RB; ++r)
+                                    if (key < ms.limit[qb][r]) atomicOr(&ms.nan_cols[r][e >> 3], bits << (4 * (e & 7)));
                             }
-                            if (bits == 0) continue;
-                            *v = w;
-                            ms.nan_any = 1;
-                            for (int r = 0; r < RB; ++r)
-                                if (key < ms.limit[qb][r])
-                                    atomicOr(&ms.nan_cols[r][e >> 1], bits << (16 * (e & 1)));
                         }
                     }
                 }
@@ -1041,7 +1108,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             const bool bad = ms.bad[qb] != 0;
             const bool dead = *g.abort != 0;
             const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * RB + rw0;
-            const long long row0 = ((long long)s.b * a.H + (long long)s.kvh * (a.H / a.Hkv)) * a.Nq + r0;
+            const long long row0 = ((long long)s.b * a.Hkv + s.kvh) * a.R + r0;
             if (bad && threadIdx.x == 0) {
                 atomicCAS(a.status + 1, 0, SITE_DEC8_BAD_PAGE);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
@@ -1050,7 +1117,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 const int r = rw0 + kk;
                 const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
                 const float l2 = sum == 0.f ? -INFINITY : lg2(sum) - ms.nref[r];  // base 2
-                ms.alpha[r] = sum == 0.f ? 0.f : vref * (1.f / kOneP) / sum;
+                ms.alpha[r] = sum == 0.f ? 0.f : vref * (1.f / kOneP) * reciprocal(sum);
                 if (kk < rows && !dead) {
                     if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
                     else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
@@ -1177,7 +1244,7 @@ template <int E>
 __device__ __forceinline__ void merge_out(const Dec8Args &a, long long row, float m, float sum,
                                           const float (&acc)[E]) {
     const int lane = threadIdx.x & 31;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : reciprocal(sum);
     __nv_bfloat16 *o = a.o + row * a.d;
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -1198,10 +1265,14 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     if (warp == 0) {
         const int i = row % a.Nq, bh = row / a.Nq, b = bh / a.H, h = bh - b * a.H, group = a.H / a.Hkv;
         const int nt = tiles_of(a, b), kvh = h / group, r = (h - kvh * group) * a.Nq + i;
-        int before, c0 = 0, n = 0;
-        const Cut cut(count_tiles(a, b, &before) * a.Hkv * a.row_blocks, n_cta);
+        const int ipb = a.Hkv * a.row_blocks;
+        int c0 = 0, n = 0;
+        const Count count = count_tiles(a, b);
+        const int start = start_of(a, count.tiles * ipb, n_cta);
+        const Cut cut((count.tiles + start * count.full) * ipb, n_cta);
         if (nt > 0) {
-            const int first = before * a.Hkv * a.row_blocks + (kvh * a.row_blocks + r / RB) * nt;
+            const int first = (count.tiles_before + start * count.full_before) * ipb +
+                              (kvh * a.row_blocks + r / RB) * (nt + start) + start;
             c0 = cut.owner(first);
             n = cut.owner(first + nt - 1) - c0 + 1;
         }
@@ -1261,8 +1332,8 @@ __global__ void __launch_bounds__(32 * kCutRows)
         Cut cut;
         const Walk w = start_walk(a, c, n_cta, &cut);
         int n = 0;
-        if (c > 0 && w.left > 0 && w.t > 0) {
-            const int first = cut.first(c) - w.t;  // the item's first tile
+        if (c > 0 && w.left > 0 && w.tile() > 0) {
+            const int first = cut.first(c) - w.tile();  // the item's first tile
             if (cut.owner(first) == c - 1) n = cut.owner(first + w.nt - 1) - (c - 1) + 1;
         }
         if (lane == 0) {
@@ -1291,7 +1362,7 @@ __global__ void __launch_bounds__(32 * kCutRows)
     merge_part<E, 4>(
         a, [&](int k) { return ((size_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, 0, 1, n, m, sum, acc, bad);
     if (bad) return;
-    const long long row = ((long long)s_b * a.H + (long long)kvh * (a.H / a.Hkv)) * a.Nq + rb * RB + r;
+    const long long row = ((long long)s_b * a.Hkv + kvh) * a.R + rb * RB + r;
     merge_out(a, row, m, sum, acc);
 }
 
@@ -1345,6 +1416,11 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.row_blocks = (a.R + RB - 1) / RB;
     a.box = decode8_box_rows(p.page_size / PACK);
     a.tile_log2 = PACK == 2 ? 8 : 7;
+    // With up to 8 rows the copies are the limit and another CTA of the SM uses the time (B32
+    // H32 Hkv8 of 1..8192 keys 51.0 us counted as 0, 51.8 as 3); with more, 3 is best (0, 2, 3, 4
+    // of B8 Hkv4 19000 keys d64: R = 16 25.1, 23.8, 24.0, 24.4; R = 32 40.5, 39.6, 38.7, 38.6;
+    // R = 64 61.2, 63.2, 55.9, 60.6).
+    a.start = RB > 8 ? 3 : 0;
     a.run = p.group % 4 == 0 ? 2 : 0;  // four keys of a tile share a page and a group, or none do
     a.causal = p.causal;
     a.scale_log2 = p.scale_log2;
