@@ -38,18 +38,20 @@
 // items, two S slots, two P buffers, two query buffers, three tiles of scales.
 //
 // Measured (GB300, graph replay, caches larger than L2, d = 128 and one query unless stated):
-//   B8 H32 Hkv32 32768 keys   316-328 us  6.6-6.8 TB/s   HBM
+//   B8 H32 Hkv32 32768 keys   320-327 us  6.6-6.7 TB/s   HBM
 //   B1 H32 Hkv8 131072 keys    48 us      5.6 TB/s       37 us of stream; the rest is launch,
 //                                                        first tile, partials and merge
-//   B32 H32 Hkv8 1..8192 keys  52 us      5.2 TB/s       the same, twice an item per CTA
-//   B8 H32 Hkv4 Nq4 d64        46 us      1.8 TB/s       32 rows per head: the softmax warps'
-//                                                        chain, 2.2k clocks per tile of 128 keys
+//   B32 H32 Hkv8 1..8192 keys  50-51 us   5.4 TB/s       the same, twice an item per CTA
+//   B32 H16 Hkv8 30000 d64    170 us      5.8 TB/s       two keys to a row of a tile
+//   B8 H32 Hkv4 Nq4 d64        40 us      2.0 TB/s       32 rows per head: 16 tiles of 1.3 us per
+//                                                        CTA in the softmax warps, whose ~400
+//                                                        instructions per tile share an SM's four
+//                                                        schedulers 16 ways; then as above
 //   B1 H32 Hkv8 1000 keys       6.4 us                   latency of two launches
-// Per tile of 128 keys the chain of a softmax warp takes 0.7k clocks (8 rows) to 0.9k (16 rows)
-// against 1.3k clocks in which its bytes arrive at d = 128, one of two CTAs on the SM.  At
-// d = 64 a row is half a swizzle span and TMA's rows, not its bytes, are the limit (31 keys per
-// ns, 4 TB/s).  Code that runs once per item is kept small: fetching it cold costs more than
-// running it (unrolled copy and scale loops: 54 -> 60 us for the ragged batch).
+// Alone, the chain of a softmax warp takes 0.7k clocks (8 rows) to 0.9k (16 rows) per tile of 128
+// keys, against 1.3k clocks in which its bytes arrive at d = 128 for one of two CTAs on the SM.
+// Code that runs once per item is kept small: fetching it cold costs more than running it
+// (unrolled copy and scale loops: 54 -> 60 us for the ragged batch).
 #include <type_traits>
 
 #include "fa_internal.h"
@@ -861,8 +863,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
     } else if (warp == kQueryWarp) {
         // ------------------------------------------------------ query terms
         // Of the segments after the first, whose rows the softmax warps, idle then, share out: a
-        // warp of its own, because one warp takes longer for 32 rows than a tile takes (B8 H32
-        // Hkv4 Nq4 d64, by the warp of the scales between two segments: XX us).
+        // warp of its own, because 32 rows take one warp longer than several tiles take the others
+        // (B8 H32 Hkv4 Nq4 d64: 41.7 us, and 44.6 us when the warp of the scales did it between
+        // two items).
         bool ok = true;
         if (some) some = walk.next(a, &s);
         for (uint32_t seg = 1; some; ++seg, some = walk.next(a, &s)) {

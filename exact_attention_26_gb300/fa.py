@@ -830,9 +830,9 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
                      scale=None, out=None, lse=None, workspace=None, stream=None):
     """Decode against a paged e4m3 cache: q bf16 CUDA [B,H,Nq,d]; k_cache, v_cache uint8 codes
     [num_pages, Hkv, page_size, d] (Hkv divides H) with scales fp32 [num_pages, Hkv, page_size /
-    group]; block_table int32 [B, max_pages]; seq_lens int32 [B], 0 allowed.  causal: the Nq
-    queries are the sequence's last tokens, each sees the keys up to its own.  Rows that see
-    no key get o = 0 and lse = -inf.  Returns (o, lse)."""
+    group], >= 0 and at most 2^120; block_table int32 [B, max_pages]; seq_lens int32 [B], 0
+    allowed.  causal: the Nq queries are the sequence's last tokens, each sees the keys up to its
+    own.  Rows that see no key get o = 0 and lse = -inf.  Returns (o, lse)."""
     r = native().decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, causal,
                                   scale, out, lse, workspace, _raw(stream, q))
     if r.__class__ is tuple:

@@ -387,8 +387,8 @@ size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int
  * and a scale for every group of scale_group consecutive tokens of a page and head:
  *   k_cache, v_cache : uint8 e4m3 [num_pages][Hkv][page_size][d].
  *   k_scale, v_scale : fp32 [num_pages][Hkv][page_size / scale_group]; the value of a
- *                      code is value(code) * scale of its group.  Scales are finite and
- *                      >= 0.
+ *                      code is value(code) * scale of its group.  Scales are >= 0 and at
+ *                      most 2^120, which storing never exceeds.
  *   block_table      : int32 [B][max_pages_per_seq]; seq_lens int32 [B] (device memory).
  *   d                : 64, 96, 128 or 256 (FA_ERR_UNSUPPORTED otherwise).
  *   scale_group      : divides page_size; page_size * max_pages_per_seq <= 2^31 - 128,

@@ -145,6 +145,16 @@ def test_value_scales_over_many_binades(fa):
     _check(fa, _problem(2, 4, 2, 1, 128, 16, 8, [900, 333], seed=8, spread=3.0))
 
 
+@pytest.mark.parametrize("exponent", [120, 100, -100, -126])
+def test_extreme_value_scales(fa, exponent):
+    prob = list(_problem(2, 4, 2, 1, 128, 16, 16, [700, 140], seed=19))
+    prob[2] &= 0xBF  # codes below 2, so that the outputs fit
+    prob[4] = torch.full_like(prob[4], 2.0 ** exponent)
+    _check(fa, prob)
+    prob[4][:, :, 0] *= torch.exp2(-torch.randint(0, 40, prob[4].shape[:2]).float())
+    _check(fa, prob)
+
+
 def test_groups_of_zero_scale(fa):
     prob = _problem(2, 4, 2, 1, 128, 16, 16, [300, 140], seed=9)
     for b, n in ((0, 300), (1, 140)):
