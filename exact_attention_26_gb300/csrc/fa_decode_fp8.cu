@@ -87,6 +87,9 @@ struct Dec8Tile {
     static constexpr int NP = (3 * RB + 15) / 16 * 16;   // columns of O^T: three terms of p
     static constexpr int CTAS = (NCH == 1 && RB <= 32) ? 2 : 1;  // resident per SM
     static constexpr int THREADS = 32 * (4 * NWG + 4);
+    // A wait that calls a function costs the registers that calls clobber.  Where registers are
+    // short, waits are inlined (B8 H32 Hkv4 Nq4 19000 keys d128: 46.5 -> 42.3 us).
+    static constexpr bool INLINE_WAITS = NCH == 1 && RB >= 32;
     static constexpr int TK = PACK * kTile;              // keys of a tile
     static constexpr uint32_t CHUNK = kTile * 128;
     static constexpr uint32_t SLOT = NCH * CHUNK;
@@ -334,6 +337,18 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool co
 }
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Has the phase of this parity completed?  Does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
@@ -719,7 +734,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int slot = (int)(n % ST);
                     ok = n < (uint32_t)ST ||
-                         mbar_wait_warp(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
+                         mbar_wait_warp<T::INLINE_WAITS>(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
                     if (!ok) break;
                     const uint32_t fb = bar(ms.full[slot]);
                     const CUtensorMap *map = kv ? &a.tm_v : &a.tm_k;
@@ -749,7 +764,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             volatile int never = 0;
             const Guard g2{a.status, &never, kWaitLimitNs};
             for (uint32_t i = n > (uint32_t)ST ? n - ST : 0; i < n; ++i)
-                mbar_wait_warp(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
+                mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
@@ -766,8 +781,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             const int u = js & 1, qb = seg & 1, half = (int)(js % PACK);
             const uint32_t i = 2 * (js / PACK);
             const int slot = (int)(i % ST);
-            if (ta == sa.t0) ok = ok && mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
-            ok = ok && mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+            if (ta == sa.t0) ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
+            ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
             if (!ok) return;
             tc_fence_after();
             const uint64_t dk = desc_add(sdesc_sw128(base + slot * T::SLOT, 16, 1024), half * 64);
@@ -787,18 +802,23 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 ta = more ? sa.t0 : 0;
             }
         };
-        if (more) issue_s();
-        if (more && ok) issue_s();
+        // S of a segment whose queries are not there yet is not waited for while O of the tiles
+        // before it can be issued.  (B75 Hkv16 R = 16 d256, one tile per item: 61 -> 50 us.)
+        auto ready = [&]() {
+            return (ta != sa.t0 || __all_sync(kFull, mbar_test(bar(ms.q_full[seg & 1]), (seg >> 1) & 1)));
+        };
         uint32_t j = 0;
         while (ok && walk.next(a, &s)) {
             for (int t = s.t0; ok && t < s.t1; t += (int)(++j % PACK == 0)) {
                 const int u = j & 1, half = (int)(j % PACK);
                 const uint32_t jt = j / PACK, i = 2 * jt + 1;
                 const int slot = (int)(i % ST);
-                ok = mbar_wait_warp(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
+#pragma unroll 1
+                while (ok && more && (js == j || (js == j + 1 && ready()))) issue_s();
+                ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 // every softmax warp has read the tile's scales
                 if (half + 1 == PACK && lane == 0) mbar_arrive(bar(ms.scale_empty[jt % kScaleStages]));
-                ok = ok && mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t dv = sdesc_sw128(base + slot * T::SLOT, T::CHUNK, 1024);
@@ -811,14 +831,13 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                                         desc_add(dp, ks * 1024), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                 tc_commit_elect(bar(ms.pv_done[u]));
                 if (half + 1 == PACK) tc_commit_elect(bar(ms.empty[slot]));
-                if (more) issue_s();
             }
         }
         // fires once every MMA issued above has completed (normal or aborted run)
         tc_commit_elect(bar(ms.done));
         volatile int never = 0;
         const Guard g2{a.status, &never, kWaitLimitNs};
-        mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
+        mbar_wait_warp<T::INLINE_WAITS>(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
     } else if (warp == kAuxWarp) {
         // ------------------------------------------------------ key and value scales
         uint32_t seg = 0, j = 0;
@@ -829,7 +848,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 open();
                 pg = first_page(s.t0);
                 if (seg >= 2)  // `bad` of the segment before the last has been read
-                    ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+                    ok = mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
                 if (!ok) break;
             }
             if (lane == 0) ms.bad[qb] = 0;
@@ -837,7 +856,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             for (int t = s.t0; ok && t < s.t1; ++t, ++j) {
                 const int pg_next = first_page(t + 1);
                 const int st = (int)(j % kScaleStages);
-                ok = j < kScaleStages || mbar_wait_warp(bar(ms.scale_empty[st]), ((j / kScaleStages) - 1) & 1,
+                ok = j < kScaleStages || mbar_wait_warp<T::INLINE_WAITS>(bar(ms.scale_empty[st]), ((j / kScaleStages) - 1) & 1,
                                                         g, SITE_DEC_EMPTY);
                 if (!ok) break;
 #pragma unroll 1
@@ -870,7 +889,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         if (some) some = walk.next(a, &s);
         for (uint32_t seg = 1; some; ++seg, some = walk.next(a, &s)) {
             const int qb = seg & 1;
-            if (seg >= 2) ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+            if (seg >= 2) ok = mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_empty[qb]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
             if (!ok) break;
             put_queries(std::integral_constant<int, 4>(), qb, 0, 1);
             fence_proxy_async_smem();
@@ -907,7 +926,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
-            mbar_wait_warp(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
+            mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
             named_barrier_sync(id, 128);
             const int len = ms.len[qb];
             const int full_keys = a.causal ? len - a.Nq + 1 : len;  // keys that every row sees
@@ -918,9 +937,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 const int at = kk * PACK + half, key = t * TK + at;
                 const int st = (int)(jt % kScaleStages);
                 const bool first = t == s.t0 && half == 0;
-                mbar_wait(bar(ms.scale_full[st]), (jt / kScaleStages) & 1, g, SITE_DEC_FULL);
+                mbar_wait<T::INLINE_WAITS>(bar(ms.scale_full[st]), (jt / kScaleStages) & 1, g, SITE_DEC_FULL);
                 float ks = ms.k_scale[st][at >> a.run], vs = ms.v_scale[st][at >> a.run];
-                mbar_wait(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
+                mbar_wait<T::INLINE_WAITS>(bar(ms.s_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 __syncwarp();
                 tc_fence_after();
                 const bool partly = t >= full_tiles;  // some row sees less
@@ -999,7 +1018,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     }
                     if (!first) {  // O^T to the new references, once PV of the step before is done
                         const float fo = vref > 0.f ? v_old * inverse2(vref) : 1.f;
-                        mbar_wait_warp(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
+                        mbar_wait_warp<T::INLINE_WAITS>(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < NCH * PACK; ++c)
@@ -1055,7 +1074,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     // do are noted
                     const uint32_t i = 2 * jt + 1;
                     const int slot = (int)(i % ST);
-                    mbar_wait_warp(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                    mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
                     const uint32_t v0 = base + slot * T::SLOT + kk * 128;
                     constexpr int kGroups = NCH * 8 / PACK;  // of 16 columns
                     auto group = [&](int e) { return ((e & 7) + half * kGroups ^ (kk & 7)) << 4; };
@@ -1126,7 +1145,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     else if (!bad) a.lse[row0 + kk] = l2 * kLn2;
                 }
             }
-            mbar_wait_warp(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
+            mbar_wait_warp<T::INLINE_WAITS>(bar(ms.pv_done[jl & 1]), (jl >> 1) & 1, g, SITE_DEC_MMA);
             tc_fence_after();
             named_barrier_sync(id, 128);
             const int upper = PACK == 2 ? w4 >> 1 : 0;  // lanes of the odd keys' half
