@@ -777,24 +777,39 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         int ta = more ? sa.t0 : 0;
         uint32_t js = 0, seg = 0;  // steps whose S is issued; segments begun
         bool ok = true;
+        // a ring slot of K or V and the parity of its round, two slots further with every tile
+        struct Slot {
+            int at;
+            uint32_t round;
+            __device__ __forceinline__ void advance() {
+                at += 2;
+                if (at >= ST) at -= ST, round ^= 1;
+            }
+        };
+        Slot k_slot{0, 0}, v_slot{1, 0};
+        const uint64_t d_ring = sdesc_sw128(base, 16, 1024), d_q = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t d_v = sdesc_sw128(base, T::CHUNK, 1024), d_p = sdesc_sw32(sP, T::P_CHUNK, 256);
         auto issue_s = [&]() {
             const int u = js & 1, qb = seg & 1, half = (int)(js % PACK);
-            const uint32_t i = 2 * (js / PACK);
-            const int slot = (int)(i % ST);
-            if (ta == sa.t0) ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
-            ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+            if (ta == sa.t0)
+                ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
+            if (half == 0)
+                ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
             if (!ok) return;
             tc_fence_after();
-            const uint64_t dk = desc_add(sdesc_sw128(base + slot * T::SLOT, 16, 1024), half * 64);
-            const uint64_t dq = sdesc_sw128(sQ + qb * T::Q_BYTES, 16, 1024);
-            for (int ks = 0; ks < ksteps; ++ks)
-                mma_ss_elect_f8(tmem + u * T::NS, desc_add(dk, (ks >> 2) * T::CHUNK + (ks & 3) * 32),
-                                desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32), kIdescS,
-                                ks > 0 ? 1u : 0u);
+            const uint64_t dk = desc_add(d_ring, k_slot.at * T::SLOT + half * 64);
+            const uint64_t dq = desc_add(d_q, qb * T::Q_BYTES);
+#pragma unroll
+            for (int ks = 0; ks < NCH * 4 / PACK; ++ks)
+                if (PACK == 2 || NCH == 2 || ks < ksteps)
+                    mma_ss_elect_f8(tmem + u * T::NS, desc_add(dk, (ks >> 2) * T::CHUNK + (ks & 3) * 32),
+                                    desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32), kIdescS,
+                                    ks > 0 ? 1u : 0u);
             tc_commit_elect(bar(ms.s_full[u]));
             ++js;
             if (half + 1 < PACK) return;
-            tc_commit_elect(bar(ms.empty[slot]));
+            tc_commit_elect(bar(ms.empty[k_slot.at]));
+            k_slot.advance();
             if (++ta == sa.t1) {
                 tc_commit_elect(bar(ms.q_empty[qb]));
                 ++seg;
@@ -811,18 +826,16 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         while (ok && walk.next(a, &s)) {
             for (int t = s.t0; ok && t < s.t1; t += (int)(++j % PACK == 0)) {
                 const int u = j & 1, half = (int)(j % PACK);
-                const uint32_t jt = j / PACK, i = 2 * jt + 1;
-                const int slot = (int)(i % ST);
 #pragma unroll 1
                 while (ok && more && (js == j || (js == j + 1 && ready()))) issue_s();
                 ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.p_full[u]), (j >> 1) & 1, g, SITE_DEC_MMA);
                 // every softmax warp has read the tile's scales
-                if (half + 1 == PACK && lane == 0) mbar_arrive(bar(ms.scale_empty[jt % kScaleStages]));
-                ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                if (half + 1 == PACK && lane == 0) mbar_arrive(bar(ms.scale_empty[j / PACK % kScaleStages]));
+                if (half == 0)
+                    ok = ok && mbar_wait_warp<T::INLINE_WAITS>(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t dv = sdesc_sw128(base + slot * T::SLOT, T::CHUNK, 1024);
-                const uint64_t dp = sdesc_sw32(sP + u * T::P_BYTES, T::P_CHUNK, 256);
+                const uint64_t dv = desc_add(d_v, v_slot.at * T::SLOT), dp = desc_add(d_p, u * T::P_BYTES);
 #pragma unroll
                 for (int c = 0; c < NCH; ++c)
 #pragma unroll
@@ -830,7 +843,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         mma_ss_elect_f8(tmem + T::TM_O + (c + half) * T::NP, desc_add(dv, c * T::CHUNK + ks * 4096),
                                         desc_add(dp, ks * 1024), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                 tc_commit_elect(bar(ms.pv_done[u]));
-                if (half + 1 == PACK) tc_commit_elect(bar(ms.empty[slot]));
+                if (half + 1 == PACK) {
+                    tc_commit_elect(bar(ms.empty[v_slot.at]));
+                    v_slot.advance();
+                }
             }
         }
         // fires once every MMA issued above has completed (normal or aborted run)
