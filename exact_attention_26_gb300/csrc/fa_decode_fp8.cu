@@ -1290,14 +1290,51 @@ __device__ __forceinline__ void merge_out(const Dec8Args &a, long long row, floa
     if (lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
 }
 
-// A few rows: a CTA of eight warps for each, which may have dozens of partials (a long sequence
-// alone in the launch); the warps' running results meet in shared memory.
+// One row by the CTA's eight warps: row r of its block, whose n partials the attention kernel's
+// CTAs from c0 on left (n == 0: an empty sequence).  The warps' running results meet in `sh`.
 constexpr int kRowWarps = 8;
+template <int E>
+struct RowShared {
+    float acc[kRowWarps][E * 32], sum[kRowWarps], max[kRowWarps];
+};
+template <int E, int RB>
+__device__ __forceinline__ void merge_row(const Dec8Args &a, RowShared<E> &sh, int c0, int r, int n, long long row) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool bad = false;
+    float m, sum, acc[E];
+    merge_part<E, 4>(
+        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, warp, kRowWarps, n, m, sum,
+        acc, bad);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh.acc[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) {
+        sh.sum[warp] = sum;
+        sh.max[warp] = bad ? INFINITY : m;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int v = 0; v < kRowWarps; ++v) m = fmaxf(m, sh.max[v]);
+    if (m == INFINITY) return;  // the sequence was rejected: nothing is written
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int v = 0; v < kRowWarps; ++v) {
+        const float f = ex2(sh.max[v] - m);
+        sum = fmaf(sh.sum[v], f, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(sh.acc[v][lane + 32 * e], f, acc[e]);
+    }
+    merge_out(a, row, m, sum, acc);  // an empty sequence: sum 0
+}
+
+// A CTA for each row, which may have dozens of partials (a long sequence alone in the launch).
 template <int NCH, int RB>
 __global__ void __launch_bounds__(32 * kRowWarps)
     fa_decode8_merge_row_kernel(const __grid_constant__ Dec8Args a, int n_cta) {
     constexpr int E = NCH == 2 ? 8 : 4;  // columns lane, lane + 32, ... of a row
-    __shared__ float s_acc[kRowWarps][E * 32], s_sum[kRowWarps], s_max[kRowWarps];
+    __shared__ RowShared<E> sh;
     __shared__ int s_row, s_c0, s_n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
     if (warp == 0) {
@@ -1323,60 +1360,36 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     griddep_wait();  // every partial result is written
     griddep_launch_dependents();
     __syncthreads();
-    const int r = s_row, c0 = s_c0, n = s_n;
-    if (n < 0) return;
-    bool bad = false;
-    float m, sum, acc[E];
-    merge_part<E, 4>(
-        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, warp, kRowWarps, n, m, sum,
-        acc, bad);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
-    if (lane == 0) {
-        s_sum[warp] = sum;
-        s_max[warp] = bad ? INFINITY : m;
-    }
-    __syncthreads();
-    if (warp > 0) return;
-#pragma unroll
-    for (int v = 0; v < kRowWarps; ++v) m = fmaxf(m, s_max[v]);
-    if (m == INFINITY) return;  // the sequence was rejected: nothing is written
-    sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int v = 0; v < kRowWarps; ++v) {
-        const float f = ex2(s_max[v] - m);
-        sum = fmaf(s_sum[v], f, sum);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[v][lane + 32 * e], f, acc[e]);
-    }
-    merge_out(a, row, m, sum, acc);  // an empty sequence: sum 0
+    if (s_n >= 0) merge_row<E, RB>(a, sh, s_c0, s_row, s_n, row);
 }
 
 // Many rows, most of which were not cut.  Every cut lies where one of the attention kernel's
-// CTAs begins, so there is a CTA here for each of those (times blocks of eight rows): it merges
-// the item that its counterpart begins in the middle of, if no counterpart before it does, one
-// warp per row.  (Batch of 128 with 4096 rows and 300 cuts: 6 us less than a warp for every row.)
-constexpr int kCutRows = 8;
+// CTAs begins, so there is a CTA here for each of those (times blocks of eight rows).  The first
+// cut of an item merges it, one warp per row; in an item of many cuts (a long sequence among
+// short ones) each takes some of the rows, with all of its warps.
+constexpr int kCutRows = 8, kManyCuts = 16;
+static_assert(kCutRows == kRowWarps, "the same CTA does both");
 template <int NCH, int RB>
 __global__ void __launch_bounds__(32 * kCutRows)
     fa_decode8_merge_cut_kernel(const __grid_constant__ Dec8Args a, int n_cta) {
     constexpr int E = NCH == 2 ? 8 : 4;
-    __shared__ int s_b, s_item, s_n;
+    __shared__ RowShared<E> sh;
+    __shared__ int s_b, s_item, s_c0, s_n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x;  // the CTA whose beginning this is
     if (warp == 0) {
         Cut cut;
         const Walk w = start_walk(a, c, n_cta, &cut);
-        int n = 0;
+        int c0 = 0, n = 0;
         if (c > 0 && w.left > 0 && w.tile() > 0) {
             const int first = cut.first(c) - w.tile();  // the item's first tile
-            if (cut.owner(first) == c - 1) n = cut.owner(first + w.nt - 1) - (c - 1) + 1;
+            c0 = cut.owner(first);
+            n = cut.owner(first + w.nt - 1) - c0 + 1;
         }
         if (lane == 0) {
             s_b = w.b;
             s_item = w.item;
+            s_c0 = c0;
             s_n = n;
         }
     }
@@ -1392,16 +1405,23 @@ __global__ void __launch_bounds__(32 * kCutRows)
             for (long long i = threadIdx.x; i < rows; i += blockDim.x) a.lse[row0 + i] = -INFINITY;
         }
     }
-    const int n = s_n, kvh = s_item / a.row_blocks, rb = s_item - kvh * a.row_blocks;
-    const int r = blockIdx.y * kCutRows + warp;  // row of the block of RB
-    if (n == 0 || r >= RB || rb * RB + r >= a.R) return;
-    bool bad = false;
-    float m, sum, acc[E];
-    merge_part<E, 4>(
-        a, [&](int k) { return ((size_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, 0, 1, n, m, sum, acc, bad);
-    if (bad) return;
-    const long long row = ((long long)s_b * a.Hkv + kvh) * a.R + rb * RB + r;
-    merge_out(a, row, m, sum, acc);
+    const int n = s_n, c0 = s_c0, nth = c - c0 - 1;  // the item's nth cut, from 0
+    const int kvh = a.row_blocks == 1 ? s_item : s_item / a.row_blocks, rb = s_item - kvh * a.row_blocks;
+    const int r0 = blockIdx.y * kCutRows, rows = min(min(kCutRows, RB - r0), a.R - rb * RB - r0);
+    const long long row0 = ((long long)s_b * a.Hkv + kvh) * a.R + rb * RB + r0;
+    if (n > kManyCuts) {
+        for (int i = nth; i < rows; i += n - 1) {
+            merge_row<E, RB>(a, sh, c0, r0 + i, n, row0 + i);
+            __syncthreads();
+        }
+    } else if (n > 0 && nth == 0 && warp < rows) {
+        bool bad = false;
+        float m, sum, acc[E];
+        merge_part<E, 4>(
+            a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r0 + warp; }, 0, 1, n, m, sum,
+            acc, bad);
+        if (!bad) merge_out(a, row0 + warp, m, sum, acc);
+    }
 }
 
 // CTAs of a launch: all that are resident, or the largest number of tiles there can be.
@@ -1469,14 +1489,15 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = dec8_ctas<NCH, RB, PACK>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
+    // the merge that has fewer CTAs (B32 H32 Hkv8, 1024 rows against 304 cuts: 50.7 us by rows,
+    // 49.3 by cuts; B8 H32 Hkv4 Nq4, 1024 against 1216: 39.0 by rows, 39.9 by cuts)
     const long long rows = (long long)p.B * p.H * p.Nq;
-    if (rows <= 8LL * p.num_sms)  // as many CTAs as are resident
+    const int blocks = ((a.R < RB ? a.R : RB) + kCutRows - 1) / kCutRows;
+    if (rows <= (long long)n_cta * blocks)
         return launch_dependent(fa_decode8_merge_row_kernel<NCH, RB>, dim3((unsigned)rows), 32 * kRowWarps, 0,
                                 stream, 1, a, n_cta);
-    const int block = a.R < RB ? a.R : RB;
-    return launch_dependent(fa_decode8_merge_cut_kernel<NCH, RB>,
-                            dim3((unsigned)n_cta, (unsigned)((block + kCutRows - 1) / kCutRows)), 32 * kCutRows, 0,
-                            stream, 1, a, n_cta);
+    return launch_dependent(fa_decode8_merge_cut_kernel<NCH, RB>, dim3((unsigned)n_cta, (unsigned)blocks),
+                            32 * kCutRows, 0, stream, 1, a, n_cta);
 }
 
 // Tiles of 128 keys of all items in blocks of rb rows at the longest possible lengths.

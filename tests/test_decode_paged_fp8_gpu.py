@@ -111,6 +111,26 @@ def test_many_sequences(fa):
     _check(fa, _problem(400, 2, 1, 1, 64, 16, 16, lens, seed=1))
 
 
+@pytest.mark.parametrize("H,Hkv,Nq,d", [(8, 2, 1, 128), (8, 1, 2, 64), (32, 1, 1, 256)])
+def test_a_long_sequence_among_many_short_ones(fa, H, Hkv, Nq, d):
+    """Hundreds of CTAs share the long sequence, and its partial results meet; then a bad page of
+    it, which leaves it alone and no other."""
+    lens = [(b * 17) % 40 for b in range(110)]
+    lens[40], lens[77] = 50000, 3000
+    prob = _problem(len(lens), H, Hkv, Nq, d, 64, 32, lens, seed=d)
+    _check(fa, prob, causal=Nq > 1)
+    dev = [t.to(DEV) for t in prob]
+    dev[5][40, 300] = -1
+    out = torch.full(prob[0].shape, 3.0, dtype=torch.bfloat16, device=DEV)
+    again, _ = fa.decode_paged_fp8(*dev, causal=Nq > 1)
+    assert fa.fa_device_status(None) == 7
+    fa.decode_paged_fp8(*dev, causal=Nq > 1, out=out)
+    assert fa.fa_device_status(None) == 7
+    keep = torch.ones(len(lens), dtype=torch.bool)
+    keep[40] = False
+    assert torch.equal(out[keep.to(DEV)], again[keep.to(DEV)]) and bool((out[40] == 3.0).all())
+
+
 def test_all_sequences_empty(fa):
     o, lse = _check(fa, _problem(3, 4, 2, 1, 128, 16, 16, [0, 0, 0]))
     assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
