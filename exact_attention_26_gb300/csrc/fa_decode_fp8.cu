@@ -38,15 +38,15 @@
 // items, two S slots, two P buffers, two query buffers, three tiles of scales.
 //
 // Measured (GB300, graph replay, caches larger than L2, d = 128 and one query unless stated):
-//   B8 H32 Hkv32 32768 keys   320-327 us  6.6-6.7 TB/s   HBM
+//   B8 H32 Hkv32 32768 keys   320-325 us  6.6-6.7 TB/s   HBM
 //   B1 H32 Hkv8 131072 keys    48 us      5.6 TB/s       37 us of stream; the rest is launch,
 //                                                        first tile, partials and merge
-//   B32 H32 Hkv8 1..8192 keys  50-51 us   5.4 TB/s       the same, twice an item per CTA
-//   B32 H16 Hkv8 30000 d64    170 us      5.8 TB/s       two keys to a row of a tile
-//   B8 H32 Hkv4 Nq4 d64        40 us      2.0 TB/s       32 rows per head: 16 tiles of 1.3 us per
-//                                                        CTA in the softmax warps, whose ~400
-//                                                        instructions per tile share an SM's four
-//                                                        schedulers 16 ways; then as above
+//   B32 H32 Hkv8 1..8192 keys  49 us      5.6 TB/s       the same, twice an item per CTA
+//   B32 H16 Hkv8 30000 d64    165 us      6.0 TB/s       two keys to a row of a tile
+//   B8 H32 Hkv4 Nq4 d64        39 us      2.1 TB/s       32 rows per head: 16 tiles of 1.2 us per
+//                                                        CTA, the issue slots of softmax and
+//                                                        producer warps (54% over the launch) and
+//                                                        TMA's rows; then as above
 //   B1 H32 Hkv8 1000 keys       6.4 us                   latency of two launches
 // Alone, the chain of a softmax warp takes 0.7k clocks (8 rows) to 0.9k (16 rows) per tile of 128
 // keys, against 1.3k clocks in which its bytes arrive at d = 128 for one of two CTAs on the SM.
@@ -1474,11 +1474,11 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.row_blocks = (a.R + RB - 1) / RB;
     a.box = decode8_box_rows(p.page_size / PACK);
     a.tile_log2 = PACK == 2 ? 8 : 7;
-    // With up to 8 rows the copies are the limit and another CTA of the SM uses the time (B32
-    // H32 Hkv8 of 1..8192 keys 51.0 us counted as 0, 51.8 as 3); with more, 3 is best (0, 2, 3, 4
-    // of B8 Hkv4 19000 keys d64: R = 16 25.1, 23.8, 24.0, 24.4; R = 32 40.5, 39.6, 38.7, 38.6;
-    // R = 64 61.2, 63.2, 55.9, 60.6).
-    a.start = RB > 8 ? 3 : 0;
+    // Measured, counted as 0, 1, 2 (and 3) tiles: one sequence of 131072 keys among 199 of 20, H32
+    // Hkv8, 94, 74, 62 us; B256 of 1..600 keys 70.6, 66.0, 65.0; B32 of 1..8192 keys 49.0, 49.3,
+    // 49.2 (0.8 more with 3).  With more rows a start costs more (0, 2, 3, 4 of B8 Hkv4 19000 keys
+    // d64: R = 16 25.1, 23.8, 24.0, 24.4; R = 32 40.5, 39.6, 38.7, 38.6; R = 64 61.2, 63.2, 55.9, 60.6).
+    a.start = RB > 8 ? 3 : 2;
     a.run = p.group % 4 == 0 ? 2 : 0;  // four keys of a tile share a page and a group, or none do
     a.causal = p.causal;
     a.scale_log2 = p.scale_log2;
