@@ -138,10 +138,12 @@ struct Dec8Misc {
     alignas(16) float alpha[RB];         // old reference to new, as a factor
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
     float vpart[NWG][4];
-    // causal calls: columns of O that a NaN code of V makes NaN in a row, where not every row
-    // sees its key (elsewhere the product does it), as bits; and whether there are any
-    uint32_t nan_cols[RB][NCH * 4];
-    int nan_any;
+    // causal calls, per query buffer: columns of O that a NaN code of V makes NaN in a row, where
+    // not every row sees its key (elsewhere the product does it), as bits; and whether there are
+    // any.  One warpgroup marks them for all, and may be a segment ahead of the others' epilogues,
+    // so they are cleared with the buffer's queries, which waits for every warpgroup.
+    uint32_t nan_cols[2][RB][NCH * 4];
+    int nan_any[2];
 };
 
 struct FastDiv {  // n / d for 0 <= n < 2^31
@@ -702,7 +704,12 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         if (r_first == 0) {
             for (int r = lane; r < RB; r += 32)
                 ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
-            if (lane == 0) ms.len[qb] = len;
+            if (a.causal)
+                for (int i = lane; i < RB * NCH * 4; i += 32) ms.nan_cols[qb][i / (NCH * 4)][i % (NCH * 4)] = 0u;
+            if (lane == 0) {
+                ms.len[qb] = len;
+                ms.nan_any[qb] = 0;
+            }
         }
     };
 
@@ -935,10 +942,6 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
             }
             if (kk < RW) ms.nref[rw0 + kk] = -kUnseen;
-            if (a.causal && wg == 0) {
-                for (int i = kk; i < RB * NCH * 4; i += 128) ms.nan_cols[i / (NCH * 4)][i % (NCH * 4)] = 0u;
-                if (kk == 0) ms.nan_any = 0;
-            }
             float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
@@ -1118,10 +1121,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                                 const uint32_t nan = nan_of(*x);
                                 if (nan == 0) continue;
                                 *x &= ~((nan >> 7) * 255u);
-                                ms.nan_any = 1;
+                                ms.nan_any[qb] = 1;
                                 const uint32_t bits = (nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u);
                                 for (int r = 0; r < RB; ++r)
-                                    if (key < ms.limit[qb][r]) atomicOr(&ms.nan_cols[r][e >> 3], bits << (4 * (e & 7)));
+                                    if (key < ms.limit[qb][r]) atomicOr(&ms.nan_cols[qb][r][e >> 3], bits << (4 * (e & 7)));
                             }
                         }
                     }
@@ -1196,10 +1199,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o0[e] *= f[e];
-                    if (a.causal && ms.nan_any) {
+                    if (a.causal && ms.nan_any[qb]) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (ms.nan_cols[rw0 + q + e][dd >> 5] >> (dd & 31) & 1u) o0[e] = NAN;
+                            if (ms.nan_cols[qb][rw0 + q + e][dd >> 5] >> (dd & 31) & 1u) o0[e] = NAN;
                     }
                     const int here = dd < a.d && !dead && !bad ? rows - q : 0;
                     if (whole) {

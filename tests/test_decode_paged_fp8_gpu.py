@@ -227,6 +227,38 @@ def test_causal_rows_are_free_of_later_tokens_nans(fa, d, room, H, Hkv, Nq):
     assert fa.fa_device_status(None) == 0
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("H,Hkv,Nq", [(4, 1, 5), (7, 1, 7), (2, 1, 3)])
+def test_nan_values_of_many_items_stay_in_their_rows(fa, d, H, Hkv, Nq):
+    """20, 49 and 6 rows per head and several items per CTA, whose row warpgroups may be an item
+    apart: NaN codes of V among the last Nq tokens of every third sequence and of no other."""
+    g = torch.Generator().manual_seed(d + H)
+    lens = torch.randint(Nq, 300, (1500,), generator=g).tolist()
+    prob = list(_problem(len(lens), H, Hkv, Nq, d, 16, 16, lens, seed=d))
+    expect = np.zeros((len(lens), H, Nq, d), dtype=bool)
+    for b in range(0, len(lens), 3):
+        for back, col in ((1, b % d), (2, (7 * b + 3) % d), (Nq, (5 * b) % d)):
+            key = lens[b] - back
+            prob[2][int(prob[5][b, key // 16]), 0, key % 16, col] = 0x7F if col % 2 else 0xFF
+            expect[b, :, Nq - back:, col] = True
+    dev = [t.to(DEV) for t in prob]
+    first = None
+    for _ in range(20):
+        o, lse = fa.decode_paged_fp8(*dev, causal=True)
+        if first is None:
+            first = (o, lse)
+            assert np.array_equal(torch.isnan(o).cpu().numpy(), expect)
+            assert not bool(torch.isnan(lse).any())
+        assert torch.equal(torch.nan_to_num(o), torch.nan_to_num(first[0])) and torch.equal(lse, first[1])
+        assert torch.equal(torch.isnan(o), torch.isnan(first[0]))
+    assert fa.fa_device_status(None) == 0
+    some = list(range(0, 60)) + list(range(len(lens) - 30, len(lens)))
+    ref = oracle_decode(prob[0][some], *prob[1:5], prob[5][some], prob[6][some], True, d ** -0.5)
+    o, lse = first[0][some].float().cpu().numpy(), first[1][some].cpu().numpy()
+    clean = [np.where(expect[some], 0, x) for x in (o, ref[0], *ref[2][:2])]
+    check_decode(clean[0], lse, (clean[1], ref[1], (clean[2], clean[3], ref[2][2])))
+
+
 @pytest.mark.parametrize("room", [1, 150000])
 def test_captured_calls_of_half_rows_follow_the_lengths(fa, room):
     prob = _problem(4, 8, 2, 2, 64, 16, 8, [3000, 1000, 500, 64], seed=21, room=room)
