@@ -122,13 +122,14 @@ __global__ void __launch_bounds__(kAppendThreads, D == 256 ? 2 : D == 96 ? 3 : 4
         b = t;
     } else {
         // the last b with cu[b] <= t (0 if there is none) among every 32nd, by steps of 32
-        // pivots; the walk finds it among the 32 from there, which it holds in registers
+        // pivots; the walk finds it among the 32 from there, which it holds in registers.  An
+        // offset outside 0 .. T never counts, so the walk may begin early but not late.
         int lo = 0, n = (p.B + 31) / 32;
         while (n > 1) {
             const int step = (n + 31) / 32;
             const int i = lane * step;
-            const bool le = i < n && p.cu_seqlens[(lo + i) * 32] <= t;
-            const unsigned m = __ballot_sync(kFull, le);
+            const int c = i < n ? p.cu_seqlens[(lo + i) * 32] : -1;
+            const unsigned m = __ballot_sync(kFull, c >= 0 && c <= t);
             const int k = m ? 31 - __clz(m) : 0;
             lo += k * step;
             n = min(step, n - k * step);
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads, D == 256 ? 2 : D == 96 ? 3 : 4
     };
     hold();
     if (p.cu_seqlens) {
-        const unsigned m = __ballot_sync(kFull, b + lane < p.B && my_c0 <= t);
+        const unsigned m = __ballot_sync(kFull, b + lane < p.B && my_c0 >= 0 && my_c0 <= t);
         if (m) b += 31 - __clz(m);
     }
     // Walk the groups that begin at rows t .. t_end - 1 (all values are uniform over the team).
@@ -164,11 +165,11 @@ __global__ void __launch_bounds__(kAppendThreads, D == 256 ? 2 : D == 96 ? 3 : 4
         if (b - held >= 32) hold();
         const int c0 = __shfl_sync(kFull, my_c0, b - held), c1 = __shfl_sync(kFull, my_c1, b - held);
         const int start = __shfl_sync(kFull, my_len, b - held);
-        if (t >= c1) {  // an empty sequence, or the end of this one
+        // an empty sequence, the end of this one, or one with a bad offset
+        if (t >= c1 || c0 < 0 || c0 > c1 || c1 > p.T) {
             ++b;
             continue;
         }
-        if (c0 < 0 || c1 > p.T) break;
         if (t < c0) {  // rows before the first sequence
             t = c0;
             continue;

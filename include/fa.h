@@ -416,8 +416,10 @@ size_t fa_decode_paged_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int
  *                new token each (T = B).  Rows from cu[B] on belong to no sequence.
  *   scale_group: at most 128 here.
  * Two sequences of a call must not append to one page (copy a shared page first:
- * fa_fork_pages).  A sequence with a bad offset or length, and a group whose page is out
- * of range, is skipped and recorded as FA_ERR_BAD_INDEX (fa_device_status).
+ * fa_fork_pages).  A sequence whose offsets are not 0 <= cu[b] <= cu[b+1] <= T or whose length
+ * is bad, and a group whose page is out of range, is skipped and recorded as FA_ERR_BAD_INDEX
+ * (fa_device_status); the others are stored.  (Only where offsets within 0 .. T descend, so that
+ * sequences on both sides claim the same rows, may those be stored in part.)
  */
 int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cache,
                         float *k_scale, float *v_scale, const int *block_table,

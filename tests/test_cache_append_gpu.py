@@ -169,3 +169,38 @@ def test_append_on_another_stream_and_captured(fa):
                            [3 + step, 15 + step], [0, 1, 2])
         assert np.array_equal(t[0].cpu().numpy(), rc) and np.array_equal(t[2].cpu().numpy(), rs)
     assert fa.fa_device_status(None) == 0
+
+
+def _bad_offset_cases():
+    """(offsets, sequences stored, rows): offsets outside 0 .. T among good ones."""
+    yield [-3, 4, 8], [1], 12
+    yield [0, 4, 99, 8, 12], [0, 3], 12
+    yield [2, -1, 5, 12], [2], 12
+    yield [0, 13, 4, 12], [2], 12
+    yield [0, 3, 7, 13], [0, 1], 12
+    cu = list(range(0, 303, 3))
+    for at in (0, 1, 31, 32, 50, 64, 96, 99, 100):  # the search for a row's sequence meets it or not
+        for wild in (-1, 1 << 30):
+            yield cu[:at] + [wild] + cu[at + 1:], [b for b in range(100) if b not in (at - 1, at)], 300
+
+
+@pytest.mark.parametrize("cu,good,T", list(_bad_offset_cases()))
+@pytest.mark.parametrize("ps,group,old", [(8, 4, 0), (16, 16, 5), (6, 1, 3)])
+def test_append_bad_offsets_skip_their_sequences_only(fa, cu, good, T, ps, group, old):
+    B, Hkv, d = len(cu) - 1, 2, 64
+    x = _rows(T, Hkv, d, 31)
+    table = make_table([old + 20] * B, ps, -(-(old + 20) // ps), B * (-(-(old + 20) // ps)) + 2, 32)
+    caches = [make_cache(int(table.max()) + 2, Hkv, ps, d, group, seed, pow2=True) for seed in (33, 34)]
+    (kc, ks), (vc, vs) = caches
+    dev = [t.to(DEV) for t in (kc, vc, ks, vs)]
+    xd = x.to(DEV)
+    fa.append_paged_fp8(xd[:, :Hkv], xd[:, Hkv:], *dev, table.to(DEV),
+                        torch.full((B,), old, dtype=torch.int32, device=DEV),
+                        cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+    assert fa.fa_device_status(None) == 7
+    for i, (codes, scale) in enumerate(caches):
+        rc, rs = codes.numpy(), scale.numpy()
+        for b in good:
+            rc, rs = oc.append(x[cu[b]:cu[b + 1], i * Hkv:(i + 1) * Hkv].double().numpy(), rc, rs,
+                               table[b:b + 1].numpy(), [old], [0, cu[b + 1] - cu[b]])
+        assert np.array_equal(dev[i].cpu().numpy(), rc) and np.array_equal(dev[i + 2].cpu().numpy(), rs)
