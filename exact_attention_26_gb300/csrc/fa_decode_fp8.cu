@@ -10,9 +10,10 @@
 //   O^T (d x rows)        += V^T (V is keys x d: MN-major) P^T
 // The other operand is made of e4m3 terms that carry the precision:
 //   q, bf16 with 8 significant bits, scaled per row by a power of two into [128, 256), is
-//   c1 + c2 / 16: e4m3 keeps 4 significant bits, and the remainder of rounding 8 bits to 4
-//   has 4.  The sum is exact down to 2^-14 of the row's largest element and off by at most
-//   2^-22 of it below.
+//   c1 + c2 / 32: e4m3 keeps 4 significant bits, and the remainder of rounding 8 bits to 4
+//   has 4 and is at most 8, so 32 times it is in range.  c2 / 32 has steps of 2^-14: the sum is
+//   exact from 2^-7 up, which is 2^-14 of the row's largest element or less, and off by at most
+//   2^-15 below, 2^-22 of the largest or less.
 //   p, fp32, times its key's value scale, is rounded to f16 and split into three e5m2 terms:
 //   e5m2 is f16's upper byte, so the first two are byte selections and the remainders exact
 //   subtractions; the third, of 2^5 times what they leave (less than 2^-5 of p), is rounded to
@@ -283,15 +284,10 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
     return h;
 }
-// (h - c) * 16 on f16 pairs: exact for the remainder of rounding h to c.
+// h * 32 and (h - c) * 32 on f16 pairs: exact for the remainder of rounding h to c.
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t remainder16(uint32_t h, uint32_t c) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(sub_f16x2(h, c)), "r"(0x4c004c00u));
     return r;
 }
 __device__ __forceinline__ uint32_t times32(uint32_t h) {
@@ -299,6 +295,7 @@ __device__ __forceinline__ uint32_t times32(uint32_t h) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x50005000u));
     return r;
 }
+__device__ __forceinline__ uint32_t remainder32(uint32_t h, uint32_t c) { return times32(sub_f16x2(h, c)); }
 // e5m2 of two f16 values, to nearest even.
 __device__ __forceinline__ uint32_t e5m2x2_of(uint32_t h) {
     uint16_t r;
@@ -673,7 +670,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                                               __uint_as_float(w[i] & 0xffff0000u) * inv);
                         if (am >= 0x7f80u) h = 0x7fff7fffu;
                         const uint32_t c = e4m3x2_of(h);
-                        const uint32_t d = e4m3x2_of(remainder16(h, f16x2_of(c)));
+                        const uint32_t d = e4m3x2_of(remainder32(h, f16x2_of(c)));
                         c1[i / 2] |= c << (16 * (i % 2));
                         c2[i / 2] |= d << (16 * (i % 2));
                     }
@@ -971,7 +968,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     tmem_ld(t_s + u * T::NS + RW, x);
                     tmem_wait(c1);
                     tmem_wait(x);
-                    const uint64_t k16 = f32x2_splat(0.0625f), ks2 = f32x2_splat(ks);
+                    const uint64_t k32 = f32x2_splat(1.f / 32.f), ks2 = f32x2_splat(ks);
 #pragma unroll
                     for (int r = 0; r < RW; r += 4) {
                         const float4 rs = *reinterpret_cast<const float4 *>(&ms.row_scale[qb][rw0 + r]);
@@ -981,8 +978,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                             m = *reinterpret_cast<const float4 *>(&ms.nref[rw0 + r]);
                         mul_f32x2(f[0], f[1], ks2);
                         mul_f32x2(f[2], f[3], ks2);
-                        fma_f32x2(x[r], x[r + 1], k16, c1[r], c1[r + 1]);
-                        fma_f32x2(x[r + 2], x[r + 3], k16, c1[r + 2], c1[r + 3]);
+                        fma_f32x2(x[r], x[r + 1], k32, c1[r], c1[r + 1]);
+                        fma_f32x2(x[r + 2], x[r + 3], k32, c1[r + 2], c1[r + 3]);
                         fma_pairs(x[r], x[r + 1], f[0], f[1], m.x, m.y);
                         fma_pairs(x[r + 2], x[r + 3], f[2], f[3], m.z, m.w);
                     }

@@ -440,8 +440,9 @@ int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cac
  * gets O = 0 and L = -infinity.  Keys a row does not see have no influence on it, whatever
  * their codes are.  A NaN code of K that a row sees makes the row NaN, one of V its column of
  * the row, a NaN or infinity in a query its row.
- * Rounding: q's 8 significant bits are kept, probabilities times value scales enter the
- * product with the codes of V with a relative error of at most 2^-9 + 2^-11 (absolute 2^-24 of
+ * Rounding: q's 8 significant bits are kept in elements of at least 2^-14 of the row's largest
+ * magnitude, smaller ones are off by at most 2^-22 (1 + 2^-10) of it; probabilities times value
+ * scales enter the product with the codes of V with a relative error of at most 2^-9 + 2^-11 (absolute 2^-24 of
  * the row's largest probability times the sequence's largest value scale), sums are fp32.
  *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, and
  *            B * Hkv * ceil((H / Hkv) * Nq / 8) * ceil(page_size * max_pages_per_seq / 128)

@@ -148,6 +148,34 @@ def test_queries_over_many_binades(fa):
     _check(fa, prob, scale=0.3)
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("exponent", [-2, -6, -7, -8, -9, -12, -16])
+def test_small_elements_beside_a_large_one_of_a_query(fa, d, exponent):
+    """The row's largest element, 2^7, meets keys of zero, and the rest, all near 2^exponent and of
+    one sign with its keys, make up the score, which is L for a single key.  q is kept exactly down
+    to 2^-14 of the largest element; below, an element x is off by at most 2^-15 where the largest
+    is 2^7, and by f16's half step below 2^-14, 2^-25, with it: 2^-22 (1 + 2^-10) of the largest."""
+    H = 8
+    g = torch.Generator().manual_seed(d - exponent)
+    mantissa = 1 + torch.randint(0, 128, (1, H, 1, d), generator=g) / 128
+    mantissa[0, 0], mantissa[0, 1] = 1 + 1 / 128, 1 + 127 / 128
+    sign = torch.where(torch.rand(d, generator=g) < 0.5, -1.0, 1.0)
+    q = (mantissa * 2.0 ** exponent * sign).to(torch.bfloat16)
+    assert torch.equal(q.float(), mantissa * 2.0 ** exponent * sign)
+    q[..., d // 2] = 128.0
+    kc = torch.where(sign > 0, 0x38, 0xB8).to(torch.uint8).expand(1, 1, 16, d).contiguous()  # 1.0
+    kc[..., d // 2] = 0
+    vc, vs = make_cache(1, 1, 16, d, 16, 5)
+    ks = torch.full((1, 1, 1), 2.0 ** (-exponent - 6))
+    prob = [q, kc, vc, ks, vs, torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32)]
+    _, lse = fa.decode_paged_fp8(*[t.to(DEV) for t in prob], scale=1.0)
+    ref = oracle_decode(*prob, False, 1.0)
+    off = 0.0 if exponent >= -7 else 2.0 ** -22 * (1 + 2.0 ** -10) * 128 * (d - 1) * float(ks)
+    bound = off + 2.0 ** -20 * ref[2][2] + 2.0 ** -20 * (1 + np.abs(ref[1]))
+    err = np.abs(lse.cpu().double().numpy() - ref[1])
+    assert np.all(err <= bound), f"L off by {err.max():.3e}, bound {bound[err > bound].min():.3e}"
+
+
 def test_a_sink_token_and_many_small_weights(fa):
     """One key takes nearly all of the weight and has a small value; thousands of weights near
     2^-12 of the largest make up the rest of the output."""
