@@ -12,13 +12,14 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
-#include <vector>
+#include <optional>
 
 #include "fa.h"
 
@@ -65,15 +66,38 @@ struct Parts {
 
 PyObject *declined() { Py_RETURN_NONE; }
 
-// The raw stream of argument `o` (None: the device's current stream; else an integer).
-bool stream_of(PyObject *o, int device, void **out) {
-    if (o == Py_None) {
-        *out = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
+// The stream of a call on `device`: argument `o`, None for the device's current stream or the
+// handle of another, which is current while this lives.  So what the call allocates belongs to
+// the stream that its kernels run on, and scratch that is released on return is handed out
+// again only behind them.
+class CallStream {
+   public:
+    void *raw = nullptr;
+
+    bool read(PyObject *o, int device) {
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device);
+        raw = current.stream();
+        if (o == Py_None) return true;
+        raw = PyLong_AsVoidPtr(o);
+        if (PyErr_Occurred()) return false;
+        if (raw != current.stream()) {
+            caller_ = current;
+            guard_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw),
+                                                            (c10::DeviceIndex)device));
+        }
         return true;
     }
-    *out = PyLong_AsVoidPtr(o);
-    return !PyErr_Occurred();
-}
+
+    // `t`, allocated by the call, goes to a caller who works on another stream: its memory is
+    // kept, once released, until what that stream holds by then is done too.
+    void hand_out(const Tensor &t) const {
+        if (caller_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *caller_);
+    }
+
+   private:
+    std::optional<c10::cuda::CUDAStream> caller_;
+    std::optional<c10::cuda::CUDAStreamGuard> guard_;
+};
 
 template <typename T>
 T *ptr(const Tensor &t) {
@@ -133,9 +157,13 @@ PyObject *decode_paged_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         scale = PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) return nullptr;
     }
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[12], device)) return nullptr;
     Tensor out, lse, ws;
     if (a[9] == Py_None) {
         out = make({B, H, Nq, c.d}, at::kBFloat16, device);
+        stream.hand_out(out);
     } else {
         const Tensor *t = tensor(a[9], at::kBFloat16, 4);
         if (!on(t, device) || !t->sizes().equals(q->sizes())) return declined();
@@ -143,12 +171,12 @@ PyObject *decode_paged_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (a[10] == Py_None) {
         lse = make({B, H, Nq}, at::kFloat, device);
+        stream.hand_out(lse);
     } else {
         const Tensor *t = tensor(a[10], at::kFloat, 3);
         if (!on(t, device) || !shaped(*t, {B, H, Nq})) return declined();
         lse = *t;
     }
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     if (a[11] == Py_None) {
         const size_t need = fa_decode_paged_fp8_workspace_bytes((int)B, (int)H, c.Hkv, (int)Nq, c.d,
                                                                 c.page_size, c.max_pages);
@@ -159,13 +187,11 @@ PyObject *decode_paged_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return declined();
         ws = *t;
     }
-    void *stream;
-    if (!stream_of(a[12], device, &stream)) return nullptr;
     const int rc = fa_decode_paged_fp8(
         q->data_ptr(), c.kc->data_ptr(), c.vc->data_ptr(), ptr<float>(*c.ks), ptr<float>(*c.vs),
         ptr<int>(*c.bt), ptr<int>(*c.lens), out.data_ptr(), ptr<float>(lse), (int)B, (int)H, c.Hkv, (int)Nq,
         c.d, c.page_size, c.max_pages, c.num_pages, c.group, causal, (float)scale, ws.data_ptr(),
-        (size_t)ws.numel(), stream);
+        (size_t)ws.numel(), stream.raw);
     if (rc != FA_OK) return PyLong_FromLong(rc);
     PyObject *po = a[9] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[9]);
     PyObject *pl = a[10] == Py_None ? THPVariable_Wrap(lse) : Py_NewRef(a[10]);
@@ -205,13 +231,13 @@ PyObject *append_paged_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else if (k.size(0) != c.B) {
         return declined();
     }
-    void *stream;
-    if (!stream_of(a[9], device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[9], device)) return nullptr;
     return PyLong_FromLong(fa_append_paged_fp8(
         k.data_ptr(), v.data_ptr(), c.kc->data_ptr(), c.vc->data_ptr(), ptr<float>(*c.ks), ptr<float>(*c.vs),
         ptr<int>(*c.bt), ptr<int>(*c.lens), cu, c.B, (int)k.size(0), c.Hkv, c.d, c.page_size, c.max_pages,
-        c.num_pages, c.group, ks, vs, stream));
+        c.num_pages, c.group, ks, vs, stream.raw));
     END_HANDLE_TH_ERRORS
 }
 
@@ -256,13 +282,14 @@ PyObject *free_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Table t;
     if (n != 5 || !t.read(a[0], a[1], a[2], a[3])) return declined();
-    void *stream;
-    if (!stream_of(a[4], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
+    CallStream stream;
+    if (!stream.read(a[4], t.device)) return nullptr;
     Parts parts((int64_t)t.num_pages + 1, t.device);
+    stream.hand_out(parts.buffer);
     const Tensor pages = parts.take({t.num_pages}), count = parts.take({1});
     const int rc = fa_free_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(pages), ptr<int>(count), t.B,
-                                 t.max_pages, t.page_size, t.num_pages, stream);
+                                 t.max_pages, t.page_size, t.num_pages, stream.raw);
     return rc != FA_OK ? PyLong_FromLong(rc) : results({pages, count});
     END_HANDLE_TH_ERRORS
 }
@@ -276,16 +303,17 @@ PyObject *fork_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!on(parents, t.device) || !on(fresh, t.device) || fresh->size(0) != parents->size(0) ||
         !is_int(parents->size(0)))
         return declined();
-    void *stream;
-    if (!stream_of(a[6], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
+    CallStream stream;
+    if (!stream.read(a[6], t.device)) return nullptr;
     const int64_t m = parents->size(0);
     Parts parts(m * t.max_pages + 3 * m, t.device);
+    stream.hand_out(parts.buffer);
     const Tensor rows = parts.take({m, t.max_pages}), lens = parts.take({m});
     const Tensor src = parts.take({m}), dst = parts.take({m});
     const int rc = fa_fork_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(*parents), ptr<int>(*fresh),
                                  ptr<int>(rows), ptr<int>(lens), ptr<int>(src), ptr<int>(dst), t.B, (int)m,
-                                 t.max_pages, t.page_size, t.num_pages, stream);
+                                 t.max_pages, t.page_size, t.num_pages, stream.raw);
     return rc != FA_OK ? PyLong_FromLong(rc) : results({rows, lens, src, dst});
     END_HANDLE_TH_ERRORS
 }
@@ -295,16 +323,17 @@ PyObject *compact_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Table t;
     if (n != 5 || !t.read(a[0], a[1], a[2], a[3])) return declined();
-    void *stream;
-    if (!stream_of(a[4], t.device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)t.device);
+    CallStream stream;
+    if (!stream.read(a[4], t.device)) return nullptr;
     const int64_t cap = t.num_pages / 2 > 1 ? t.num_pages / 2 : 1;
     Parts parts((int64_t)t.B * t.max_pages + 2 * cap + 2, t.device);
+    stream.hand_out(parts.buffer);
     const Tensor table = parts.take({t.B, t.max_pages}), src = parts.take({cap});
     const Tensor dst = parts.take({cap}), counts = parts.take({2});
     const int rc = fa_compact_pages(ptr<int>(*t.bt), ptr<int>(*t.lens), ptr<int>(table), ptr<int>(src),
                                     ptr<int>(dst), ptr<int>(counts), t.B, t.max_pages, t.page_size,
-                                    t.num_pages, stream);
+                                    t.num_pages, stream.raw);
     return rc != FA_OK ? PyLong_FromLong(rc) : results({table, src, dst, counts});
     END_HANDLE_TH_ERRORS
 }
@@ -338,11 +367,11 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
         caches[i] = t.data_ptr();
         bytes[i] = t.nbytes() / (size_t)num_pages;
     }
-    void *stream;
-    if (!stream_of(a[4], device, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[4], device)) return nullptr;
     return PyLong_FromLong(fa_copy_pages(caches, bytes, (int)m, (int)num_pages, ptr<int>(*src), ptr<int>(*dst),
-                                         (int)src->size(0), count, stream));
+                                         (int)src->size(0), count, stream.raw));
     END_HANDLE_TH_ERRORS
 }
 

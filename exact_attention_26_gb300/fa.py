@@ -418,6 +418,24 @@ def _stream(t, stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _under(stream, t, fn, *args):
+    """fn(*args), a call on GPU tensors like `t`, with `stream` (a torch stream or a handle) as
+    the current one: what the call allocates belongs to the stream that its kernels run on, so
+    scratch that is released on return is handed out again only behind them.  Results it made
+    are marked as in use on the caller's stream too."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return fn(*args)  # which refuses it
+    caller = torch.cuda.current_stream(t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), t.device)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    for r in result:
+        if not any(r is a for a in args):
+            r.record_stream(caller)
+    return result
+
+
 _SAME_DEVICE = contextlib.nullcontext()
 
 
@@ -839,6 +857,9 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
         return r
     if r is not None:
         raise FaError(r, "fa_decode_paged_fp8")
+    if stream is not None:
+        return _under(stream, q, decode_paged_fp8, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                      seq_lens, causal, scale, out, lse, workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, Nq, d]")
@@ -869,7 +890,7 @@ def decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
                                  k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
                                  seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
                                  d, page_size, max_pages, num_pages, group, causal, scale,
-                                 workspace.data_ptr(), workspace.numel(), _stream(q, stream))
+                                 workspace.data_ptr(), workspace.numel(), _stream(q, None))
     _ok(rc, "fa_decode_paged_fp8")
     return out, lse
 
@@ -894,12 +915,14 @@ def free_pages(block_table, seq_lens, page_size, num_pages, stream=None):
         return r
     if r is not None:
         raise FaError(r, "fa_free_pages")
+    if stream is not None:
+        return _under(stream, block_table, free_pages, block_table, seq_lens, page_size, num_pages)
     di, B, max_pages = _table(block_table, seq_lens)
     pages, count = _int32(max(int(num_pages), 0), block_table), _int32(1, block_table)
     with _device(di):
         rc = fa_free_pages(block_table.data_ptr(), seq_lens.data_ptr(), pages.data_ptr(),
                            count.data_ptr(), B, max_pages, int(page_size), int(num_pages),
-                           _stream(block_table, stream))
+                           _stream(block_table, None))
     _ok(rc, "fa_free_pages")
     return pages, count
 
@@ -915,6 +938,9 @@ def fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages, stre
         return r
     if r is not None:
         raise FaError(r, "fa_fork_pages")
+    if stream is not None:
+        return _under(stream, block_table, fork_pages, block_table, seq_lens, parents, fresh, page_size,
+                      num_pages)
     di, B, max_pages = _table(block_table, seq_lens)
     _check("parents", parents, torch.int32, dev=di)
     if parents.dim() != 1:
@@ -926,7 +952,7 @@ def fork_pages(block_table, seq_lens, parents, fresh, page_size, num_pages, stre
         rc = fa_fork_pages(block_table.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
                            fresh.data_ptr(), rows.data_ptr(), lens.data_ptr(), src.data_ptr(),
                            dst.data_ptr(), B, n, max_pages, int(page_size), int(num_pages),
-                           _stream(block_table, stream))
+                           _stream(block_table, None))
     _ok(rc, "fa_fork_pages")
     return rows, lens, src, dst
 
@@ -940,13 +966,15 @@ def compact_pages(block_table, seq_lens, page_size, num_pages, stream=None):
         return r
     if r is not None:
         raise FaError(r, "fa_compact_pages")
+    if stream is not None:
+        return _under(stream, block_table, compact_pages, block_table, seq_lens, page_size, num_pages)
     di, B, max_pages = _table(block_table, seq_lens)
     cap = max(1, int(num_pages) // 2)
     table, src, dst, counts = (_int32(s, block_table) for s in ((B, max_pages), cap, cap, 2))
     with _device(di):
         rc = fa_compact_pages(block_table.data_ptr(), seq_lens.data_ptr(), table.data_ptr(),
                               src.data_ptr(), dst.data_ptr(), counts.data_ptr(), B, max_pages,
-                              int(page_size), int(num_pages), _stream(block_table, stream))
+                              int(page_size), int(num_pages), _stream(block_table, None))
     _ok(rc, "fa_compact_pages")
     return table, src, dst, counts
 
