@@ -480,6 +480,9 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
     CTAs and merged (fa_fwd_ws): kv_chunk = 0 lets the library decide, > 0 asks for
     chunks of about that many keys; the workspace that needs is allocated here
     unless given."""
+    if stream is not None:
+        return _under(stream, q, forward, q, k, v, causal, scale, out, lse, None, kv_chunk,
+                      workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, N, d]")
@@ -497,7 +500,7 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
         need = _memo(fa_fwd_workspace_bytes, B, H, N, d, causal, int(kv_chunk))
         if need == 0:
             rc = fa_fwd_gqa(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                            lse.data_ptr(), B, H, Hkv, N, d, causal, scale, _stream(q, stream))
+                            lse.data_ptr(), B, H, Hkv, N, d, causal, scale, _stream(q, None))
             where = "fa_fwd_gqa"
         else:
             if workspace is None:
@@ -505,7 +508,7 @@ def forward(q, k, v, causal=False, scale=None, out=None, lse=None, stream=None, 
             _check("workspace", workspace, torch.uint8, dev=q.device)
             rc = fa_fwd_ws(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                            lse.data_ptr(), B, H, Hkv, N, d, causal, scale, int(kv_chunk),
-                           workspace.data_ptr(), workspace.numel(), _stream(q, stream))
+                           workspace.data_ptr(), workspace.numel(), _stream(q, None))
             where = "fa_fwd_ws"
     if rc != FA_OK:
         raise FaError(rc, where)
@@ -517,6 +520,9 @@ def backward(q, k, v, o, lse, do, causal=False, scale=None, dq=None, dk=None, dv
     """dQ, dK, dV (fp32) of attention(q, k, v) given dO; o and lse from forward().
     With fewer key/value heads (k, v [B,Hkv,N,d]) dK, dV are [B,Hkv,N,d] sums over
     each head's query group."""
+    if stream is not None:
+        return _under(stream, q, backward, q, k, v, o, lse, do, causal, scale, dq, dk, dv,
+                      workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, N, d]")
@@ -540,7 +546,7 @@ def backward(q, k, v, o, lse, do, causal=False, scale=None, dq=None, dk=None, dv
         rc = fa_bwd_gqa(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                         do.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
                         grads[2].data_ptr(), B, H, Hkv, N, d, causal, scale, workspace.data_ptr(),
-                        workspace.numel(), _stream(q, stream))
+                        workspace.numel(), _stream(q, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_gqa")
     return tuple(grads)
@@ -550,6 +556,8 @@ def decode(q, k, v, scale=None, num_splits=0, out=None, lse=None, workspace=None
     """Decode attention: q bf16 CUDA [B,H,Nq,d] against the cache k, v [B,Hkv,Nk,d]
     (Hkv divides H; no mask), the key range split over CTAs and merged by LSE.
     Returns (o, lse)."""
+    if stream is not None:
+        return _under(stream, q, decode, q, k, v, scale, num_splits, out, lse, workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, Nq, d]")
@@ -576,7 +584,7 @@ def decode(q, k, v, scale=None, num_splits=0, out=None, lse=None, workspace=None
         ws_ptr = workspace.data_ptr() if workspace is not None else None
         ws_len = workspace.numel() if workspace is not None else 0
         rc = fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                       B, H, Hkv, Nq, Nk, d, scale, num_splits, ws_ptr, ws_len, _stream(q, stream))
+                       B, H, Hkv, Nq, Nk, d, scale, num_splits, ws_ptr, ws_len, _stream(q, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_decode")
     return out, lse
@@ -587,6 +595,9 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, num_spl
     """Decode against a paged cache: q bf16 [B,H,Nq,d]; k_cache, v_cache bf16
     [num_pages, Hkv, page_size, d] (Hkv divides H); block_table int32 [B, max_pages];
     seq_lens int32 [B] (all CUDA).  Returns (o, lse)."""
+    if stream is not None:
+        return _under(stream, q, decode_paged, q, k_cache, v_cache, block_table, seq_lens, scale,
+                      num_splits, out, lse, workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 4:
         raise ValueError("q must be [B, H, Nq, d]")
@@ -619,7 +630,7 @@ def decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale=None, num_spl
         rc = fa_decode_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                              block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                              lse.data_ptr(), B, H, Hkv, Nq, d, page_size, max_pages, num_pages,
-                             scale, num_splits, ws_ptr, ws_len, _stream(q, stream))
+                             scale, num_splits, ws_ptr, ws_len, _stream(q, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_decode_paged")
     return out, lse
@@ -630,6 +641,9 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, scale=None, ou
     """Packed variable-length forward: q bf16 CUDA [T,H,d], k/v [T,Hkv,d], cu_seqlens
     int32 CUDA [B+1] (sequence b = tokens cu[b]..cu[b+1]-1, each <= max_seqlen).
     Returns (o [T,H,d], lse [H,T])."""
+    if stream is not None:
+        return _under(stream, q, forward_varlen, q, k, v, cu_seqlens, max_seqlen, causal, scale,
+                      out, lse)
     _check("q", q, torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [T, H, d]")
@@ -653,7 +667,7 @@ def forward_varlen(q, k, v, cu_seqlens, max_seqlen, causal=False, scale=None, ou
     with torch.cuda.device(q.device):
         rc = fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                            cu_seqlens.data_ptr(), B, H, Hkv, T, int(max_seqlen), d, causal, scale,
-                           _stream(q, stream))
+                           _stream(q, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_varlen")
     return out, lse
@@ -663,6 +677,9 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causal=False, s
                     dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradients of forward_varlen: q/o/do bf16 [T,H,d], k/v [T,Hkv,d], lse [H,T].
     Returns (dq [T,H,d], dk [T,Hkv,d], dv [T,Hkv,d]) fp32."""
+    if stream is not None:
+        return _under(stream, q, backward_varlen, q, k, v, o, lse, do, cu_seqlens, max_seqlen,
+                      causal, scale, dq, dk, dv, workspace)
     _check("q", q, torch.bfloat16)
     if q.dim() != 3:
         raise ValueError("q must be [T, H, d]")
@@ -693,7 +710,7 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causal=False, s
                            do.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
                            grads[2].data_ptr(), cu_seqlens.data_ptr(), B, H, Hkv, T,
                            int(max_seqlen), d, causal, scale, workspace.data_ptr(),
-                           workspace.numel(), _stream(q, stream))
+                           workspace.numel(), _stream(q, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd_varlen")
     return tuple(grads)
@@ -702,6 +719,8 @@ def backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causal=False, s
 def quantize_fp8(x, block_rows=128, signs=None, transpose=False, workspace=None, stream=None):
     """e4m3 block quantisation of x bf16 CUDA [..., N, d] (heads flattened).
     Returns (codes uint8 [..., N, d] or [..., d, Np], descale fp32 [..., n_blocks])."""
+    if stream is not None:
+        return _under(stream, x, quantize_fp8, x, block_rows, signs, transpose, workspace)
     _check("x", x, torch.bfloat16)
     if x.dim() < 2:
         raise ValueError("x must be [..., N, d]")
@@ -720,7 +739,7 @@ def quantize_fp8(x, block_rows=128, signs=None, transpose=False, workspace=None,
     with torch.cuda.device(x.device):
         rc = fa_quantize_fp8(x.data_ptr(), codes.data_ptr(), descale.data_ptr(), BH, N, d,
                              int(block_rows), None if signs is None else signs.data_ptr(),
-                             transpose, workspace.data_ptr(), workspace.numel(), _stream(x, stream))
+                             transpose, workspace.data_ptr(), workspace.numel(), _stream(x, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_quantize_fp8")
     return codes, descale
@@ -730,6 +749,9 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
                 lse=None, stream=None):
     """Attention on e4m3 inputs: q8 uint8 CUDA [B,H,N,d], k8 [B,Hkv,N,d], vt8 [B,Hkv,d,Np],
     q/k descales [B,H|Hkv,ceil(N/128)], v descale [B,Hkv,1].  Returns (o bf16, lse fp32)."""
+    if stream is not None:
+        return _under(stream, q8, forward_fp8, q8, k8, vt8, q_descale, k_descale, v_descale, causal,
+                      scale, out, lse)
     _check("q8", q8, torch.uint8)
     if q8.dim() != 4:
         raise ValueError("q8 must be [B, H, N, d]")
@@ -754,7 +776,7 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
     with torch.cuda.device(q8.device):
         rc = fa_fwd_fp8(q8.data_ptr(), k8.data_ptr(), vt8.data_ptr(), q_descale.data_ptr(),
                         k_descale.data_ptr(), v_descale.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                        B, H, Hkv, N, d, causal, scale, _stream(q8, stream))
+                        B, H, Hkv, N, d, causal, scale, _stream(q8, None))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_fp8")
     return out, lse

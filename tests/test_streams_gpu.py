@@ -33,17 +33,52 @@ def _paged(fa):
     }
 
 
+def _dense(fa):
+    """name -> a call on tensors that are not a paged e4m3 cache, taking the stream."""
+    g = torch.Generator().manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g).to(torch.bfloat16).to(DEV)
+
+    q, k, v, do = (rand(1, 2, 2048, 128) for _ in range(4))
+    o, lse = fa.forward(q, k, v, causal=True)
+    q1, kc, vc = rand(2, 4, 1, 128), rand(2, 4, 6000, 128), rand(2, 4, 6000, 128)
+    pages = (rand(400, 2, 16, 128), rand(400, 2, 16, 128))
+    table = torch.randperm(400, generator=g).to(torch.int32).reshape(2, 200).to(DEV)
+    lens = torch.tensor([3100, 77], dtype=torch.int32, device=DEV)
+    tq, tk, tv, tdo = (rand(700, 4, 64) for _ in range(4))
+    cu = torch.tensor([0, 300, 700], dtype=torch.int32, device=DEV)
+    to, tl = fa.forward_varlen(tq, tk, tv, cu, 400, causal=True)
+    x8 = [fa.quantize_fp8(t) for t in (q, k)] + [fa.quantize_fp8(v, 0, transpose=True)]
+    torch.cuda.synchronize()
+    return {
+        "forward": lambda s: fa.forward(q, k, v, causal=True, stream=s),
+        "forward with cut key ranges": lambda s: fa.forward(q, k, v, causal=True, stream=s, kv_chunk=512),
+        "backward": lambda s: fa.backward(q, k, v, o, lse, do, causal=True, stream=s)[1:],  # dQ: atomic sums
+        "decode": lambda s: fa.decode(q1, kc, vc, num_splits=8, stream=s),
+        "decode_paged": lambda s: fa.decode_paged(q1, *pages, table, lens, num_splits=8, stream=s),
+        "forward_varlen": lambda s: fa.forward_varlen(tq, tk, tv, cu, 400, causal=True, stream=s),
+        "backward_varlen": lambda s: fa.backward_varlen(tq, tk, tv, to, tl, tdo, cu, 400, causal=True,
+                                                        stream=s)[1:],
+        "quantize_fp8": lambda s: fa.quantize_fp8(q, stream=s),
+        "forward_fp8": lambda s: fa.forward_fp8(*(t[0] for t in x8), *(t[1] for t in x8), causal=True,
+                                                stream=s),
+    }
+
+
+DENSE = ["forward", "forward with cut key ranges", "backward", "decode", "decode_paged", "forward_varlen",
+         "backward_varlen", "quantize_fp8", "forward_fp8"]
 PAGED = ["decode_paged_fp8", "decode_paged_fp8 of a tensor subclass", "free_pages", "fork_pages",
          "compact_pages"]
 
 
 @pytest.fixture(scope="module")
 def calls(fa):
-    return _paged(fa)
+    return {**_paged(fa), **_dense(fa)}
 
 
 @pytest.mark.parametrize("handle", [False, True])
-@pytest.mark.parametrize("name", PAGED)
+@pytest.mark.parametrize("name", PAGED + DENSE)
 def test_allocations_belong_to_the_given_stream(fa, calls, name, handle):
     s = torch.cuda.Stream()
     call = calls[name]
@@ -61,7 +96,7 @@ def test_allocations_belong_to_the_given_stream(fa, calls, name, handle):
     assert all(torch.equal(a, b) for a, b in zip(expect, got))
 
 
-@pytest.mark.parametrize("name", PAGED)
+@pytest.mark.parametrize("name", PAGED + DENSE)
 def test_the_current_stream_goes_on_meanwhile(fa, calls, name):
     """Calls on one stream while the current one allocates and writes memory of all sizes."""
     s = torch.cuda.Stream()
@@ -78,7 +113,7 @@ def test_the_current_stream_goes_on_meanwhile(fa, calls, name):
         assert all(torch.equal(a, b) for a, b in zip(expect, g))
 
 
-@pytest.mark.parametrize("name", PAGED)
+@pytest.mark.parametrize("name", PAGED + DENSE)
 def test_results_outlive_their_release_while_the_caller_reads_them(fa, calls, name):
     """Results released while the current stream has not read them yet: the next calls on the
     other stream must not be given their memory."""
