@@ -19,7 +19,8 @@
 //   subtractions; the third, of 2^5 times what they leave (less than 2^-5 of p), is rounded to
 //   nearest.  Relative error at most 2^-9 + 2^-11 (a rounding to bf16 would be off by 2^-8);
 //   where the first two run into e5m2's smallest step, 2^-16, they leave up to that, of which the
-//   third is off by 2^-20: 2^-24 of the row's largest p times the largest scale.
+//   third is off by 2^-20: 2^-24 of the row's largest p times the largest scale it sees (or 2^-84
+//   of any).
 // Every term is a column of N of its own; the columns are put together in fp32 after the
 // product.  A thread owns one key of S^T, so the key scales, the mask, exp2 and the row sums
 // are per-thread work, and the row maximum is needed only when a score passes the row's
@@ -98,7 +99,7 @@ struct Dec8Tile {
     static constexpr uint32_t Q_BYTES = NCH * Q_CHUNK;   // of one of two buffers
     static constexpr uint32_t P_CHUNK = kTile * 32;      // 32 columns of every key
     static constexpr uint32_t P_BYTES = (NP + 31) / 32 * P_CHUNK;  // of one of two buffers
-    static constexpr uint32_t MISC = 8192;
+    static constexpr uint32_t MISC = RB > 32 ? 9216 : 8192;
     static constexpr uint32_t FIXED = 2 * Q_BYTES + 2 * P_BYTES + MISC + 1024;
     static constexpr uint32_t BUDGET = (CTAS == 2 ? 113u : 226u) * 1024u;
     static constexpr int FIT = (int)((BUDGET - FIXED) / SLOT);
@@ -137,6 +138,9 @@ struct Dec8Misc {
     int len[2];                          // per query buffer: the sequence's length
     alignas(16) float nref[RB];          // minus the reference of the row's scores, base 2
     alignas(16) float alpha[RB];         // old reference to new, as a factor
+    // causal calls: log2 of what a row's terms of p are divided by, to make room for value scales
+    // above the common reference, and the row's factor of O^T when that or the reference moves
+    alignas(16) float room[RB], alpha_o[RB];
     alignas(16) float part[4][RB];       // per-warp maxima, then sums
     float vpart[NWG][4];
     // causal calls, per query buffer: columns of O that a NaN code of V makes NaN in a row, where
@@ -939,7 +943,10 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 if (lane == 0) mbar_arrive(bar(ms.q_full[0]));
             }
             if (kk < RW) ms.nref[rw0 + kk] = -kUnseen;
-            float vref = 0.f, vmul = 0.f;  // power of two the value scales are taken relative to, kOneP / vref
+            // kOneP / vref (0: none yet), vref the power of two that value scales are taken relative
+            // to; and what a scale may not pass, vref, or -1 where some row's terms are divided
+            float vmul = 0.f, vmax = 0.f;
+            auto vref_of = [&] { return vmul > 0.f ? kOneP * inverse2(vmul) : 0.f; };
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
@@ -995,19 +1002,27 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     float top = fmaxf(x[0], x[1]);
 #pragma unroll
                     for (int r = 2; r < RW; r += 2) top = fmax3(top, x[r], x[r + 1]);
-                    move = vote_group(id, top > kMoveLog2 || vs > vref);
+                    move = vote_group(id, top > kMoveLog2 || vs > vmax);
                 }
                 if (move) {
                     // new references: the step's maximum where it passes the old one by 2^6
                     scores(std::false_type());
+                    // Where not every row sees the key, its value scale must not push the others'
+                    // terms out of e5m2's range: it counts for the common reference as 2^-60 of
+                    // itself, and where it is above that still, the rows that see the key divide
+                    // their terms.  Then every step up to the item's end comes here.
+                    const bool uneven = a.causal && partly, some_see = uneven && key >= full_keys;
+                    const float vs_all = some_see && vs > 0.f ? fmaxf(vs * 0x1p-60f, 0x1p-126f) : vs;
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
                         const float m = warp_max(x[r]);
                         if (lane == r) ms.part[w4][rw0 + r] = m;
                     }
-                    const float vm_warp = warp_max(vs);
+                    const float vm_warp = warp_max(vs_all);
                     if (lane == 0) ms.vpart[wg][w4] = vm_warp;
-                    const float v_old = vref;
+                    const bool roomy = vmax < 0.f;
+                    const float v_old = vref_of();
+                    float vref = v_old;
                     named_barrier_sync(id, 128);
                     const float vm = fmaxf(fmaxf(ms.vpart[wg][0], ms.vpart[wg][1]),
                                            fmaxf(ms.vpart[wg][2], ms.vpart[wg][3]));
@@ -1017,14 +1032,43 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         vref = fmaxf(__uint_as_float(__float_as_uint(vm) & 0x7f800000u) * 16.f, 0x1p-110f);
                         vmul = kOneP * inverse2(vref);
                     }
+                    vmax = vref;
+                    auto row_max = [&](int r) {
+                        return fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]), fmaxf(ms.part[2][r], ms.part[3][r]));
+                    };
+                    float down = 0.f;  // log2 of alpha
                     if (kk < RW) {
                         const int r = rw0 + kk;
                         const float m_old = -ms.nref[r];
-                        const float m = fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]),
-                                              fmaxf(ms.part[2][r], ms.part[3][r]));
+                        const float m = row_max(r);
                         const bool up = m > m_old + kMoveLog2;
-                        ms.alpha[r] = up ? ex2(m_old - m) : 1.f;
+                        if (up) down = m_old - m;
+                        ms.alpha[r] = up ? ex2(down) : 1.f;
                         if (up) ms.nref[r] = -m;
+                    }
+                    if (__builtin_expect(uneven, 0)) {  // the same of p times the value scale
+                        named_barrier_sync(id, 128);
+                        const float lift =  // log2 of the scale over the reference, rounded up
+                            some_see && vs > vref ? (float)((int)(__float_as_uint(vs) >> 23) -
+                                                            (int)(__float_as_uint(vref) >> 23) + 1)
+                                                  : 0.f;
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) {
+                            const float m = warp_max(x[r] + lift);
+                            if (lane == r) ms.part[w4][rw0 + r] = m;
+                        }
+                        named_barrier_sync(id, 128);
+                        if (kk < RW) {
+                            const int r = rw0 + kk;
+                            const float old = roomy ? ms.room[r] : 0.f;
+                            const float v_up = roomy ? (float)((int)(__float_as_uint(vref) >> 23) -
+                                                               (int)(__float_as_uint(v_old) >> 23))
+                                                     : 0.f;
+                            const float left = fmaxf(old + down - v_up, 0.f), need = row_max(r) + ms.nref[r];
+                            const float room = ceilf(need > left + kMoveLog2 ? need : left);
+                            ms.alpha_o[r] = ex2(down + old - room);
+                            ms.room[r] = room;
+                        }
                     }
                     named_barrier_sync(id, 128);
 #pragma unroll
@@ -1032,8 +1076,22 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         l[r] *= ms.alpha[rw0 + r];
                         x[r] += ms.nref[rw0 + r];
                     }
+                    if (__builtin_expect(uneven, 0)) {
+#pragma unroll
+                        for (int r = 0; r < RW; ++r)
+                            if (ms.room[rw0 + r] > 0.f) vmax = -1.f;
+                        if (vmax < 0.f) {
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) {  // the sum keeps p itself
+                                const float p = ex2(x[r]);
+                                x[r] -= ms.room[rw0 + r];
+                                l[r] += p - ex2(x[r]);
+                            }
+                        }
+                    }
                     if (!first) {  // O^T to the new references, once PV of the step before is done
                         const float fo = vref > 0.f ? v_old * inverse2(vref) : 1.f;
+                        const float *alpha = uneven ? ms.alpha_o : ms.alpha;
                         mbar_wait_warp<T::INLINE_WAITS>(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
@@ -1045,7 +1103,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                                 tmem_ld(at, o);
                                 tmem_wait(o);
 #pragma unroll
-                                for (int e = 0; e < RW; ++e) o[e] *= ms.alpha[rw0 + e] * fo;
+                                for (int e = 0; e < RW; ++e) o[e] *= alpha[rw0 + e] * fo;
                                 tmem_st(at, o);
                             }
                         tmem_wait_st();
@@ -1155,7 +1213,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 const int r = rw0 + kk;
                 const float sum = (ms.part[0][r] + ms.part[1][r]) + (ms.part[2][r] + ms.part[3][r]);
                 const float l2 = sum == 0.f ? -INFINITY : lg2(sum) - ms.nref[r];  // base 2
-                ms.alpha[r] = sum == 0.f ? 0.f : vref * (1.f / kOneP) * reciprocal(sum);
+                ms.alpha[r] = sum == 0.f ? 0.f : vref_of() * (1.f / kOneP) * reciprocal(sum);
+                if (vmax < 0.f) ms.alpha[r] *= ex2(ms.room[r]);
                 if (kk < rows && !dead) {
                     if (!whole) a.part_l[prow + kk] = bad ? __uint_as_float(kBadPartial) : l2;
                     else if (!bad) a.lse[row0 + kk] = l2 * kLn2;

@@ -438,12 +438,14 @@ int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cac
  *            sees keys 0 .. seq_lens[b] - Nq + i.
  * A row that sees no key (an empty sequence, or a causal query before its first token)
  * gets O = 0 and L = -infinity.  Keys a row does not see have no influence on it, whatever
- * their codes are.  A NaN code of K that a row sees makes the row NaN, one of V its column of
+ * their codes are (a value scale of theirs 2^60 times what the row sees costs it precision, see
+ * below).  A NaN code of K that a row sees makes the row NaN, one of V its column of
  * the row, a NaN or infinity in a query its row.
  * Rounding: q's 8 significant bits are kept in elements of at least 2^-14 of the row's largest
  * magnitude, smaller ones are off by at most 2^-22 (1 + 2^-10) of it; probabilities times value
- * scales enter the product with the codes of V with a relative error of at most 2^-9 + 2^-11 (absolute 2^-24 of
- * the row's largest probability times the sequence's largest value scale), sums are fp32.
+ * scales enter the product with the codes of V with a relative error of at most 2^-9 + 2^-11, or
+ * an absolute one of 2^-24 of the row's largest probability times the largest value scale among
+ * the keys it sees (2^-84 of any of the sequence's); sums are fp32.
  *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, and
  *            B * Hkv * ceil((H / Hkv) * Nq / 8) * ceil(page_size * max_pages_per_seq / 128)
  *            < 2^31 (FA_ERR_INVALID_ARG where it overflows).

@@ -203,6 +203,43 @@ def test_extreme_value_scales(fa, exponent):
     _check(fa, prob)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,Hkv,Nq,room", [(2, 2, 4, 1), (4, 2, 7, 1), (2, 2, 7, 150000), (4, 1, 8, 1), (8, 1, 8, 1)])
+@pytest.mark.parametrize("grow", [-40, 12, 25, 45])
+def test_value_scales_of_later_tokens_stay_out_of_a_row(fa, d, H, Hkv, Nq, room, grow):
+    """Value scales that grow from one new token to the next, to 2^grow and more times the cached
+    ones': every row is as exact as if the tokens behind it were not there."""
+    lens = [300, 2, Nq, 127 + Nq, 128, 0, 512 + Nq // 2]
+    prob = list(_problem(len(lens), H, Hkv, Nq, d, 16, 1, lens, seed=d + Nq, room=room))
+    for b, n in enumerate(lens):
+        for j in range(max(0, n - Nq), n):
+            prob[4][int(prob[5][b, j // 16]), :, j % 16] *= 2.0 ** (grow * (j - n + Nq) / (Nq - 1))
+    o, lse = fa.decode_paged_fp8(*[t.to(DEV) for t in prob], causal=True)
+    rows = [oracle_decode(prob[0][:, :, i:i + 1], *prob[1:6], (prob[6] - Nq + 1 + i).clamp(min=0), False,
+                          d ** -0.5) for i in range(Nq)]
+    ref = [np.concatenate([r[k] for r in rows], 2) for k in (0, 1)]
+    terms = tuple(np.concatenate([r[2][k] for r in rows], 2) for k in range(3))
+    check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), (*ref, terms))
+    assert fa.fa_device_status(None) == 0
+
+
+@pytest.mark.parametrize("exponent", [-126, -100, 90, 120])
+def test_last_tokens_of_an_extreme_value_scale(fa, exponent):
+    prob = list(_problem(2, 4, 2, 4, 128, 16, 16, [145, 40], seed=22))
+    prob[2] &= 0xBF  # codes below 2, so that the outputs fit
+    prob[4][int(prob[5][0, 9])] = 2.0 ** exponent  # token 144, alone in its group
+    _check(fa, prob, causal=True)
+    prob = list(_problem(3, 4, 2, 4, 128, 16, 16, [4, 3, 1], seed=23))  # no key that all rows see
+    prob[2] &= 0xBF
+    prob[4] = torch.full_like(prob[4], 2.0 ** exponent)
+    o, lse = _check(fa, prob, causal=True)
+    assert float(o[0, :, 3].float().abs().max()) > 0
+    if exponent == -100:  # normal in bf16: as outputs near 1, to which the bound's last term is nothing
+        ro, rl, (pv, vmax, qk) = oracle_decode(*prob, True, 128 ** -0.5)
+        f = 2.0 ** 100
+        check_decode(o.double().cpu().numpy() * f, lse.cpu().numpy(), (ro * f, rl, (pv * f, vmax * f, qk)))
+
+
 def test_groups_of_zero_scale(fa):
     prob = _problem(2, 4, 2, 1, 128, 16, 16, [300, 140], seed=9)
     for b, n in ((0, 300), (1, 140)):
