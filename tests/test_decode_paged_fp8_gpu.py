@@ -240,6 +240,22 @@ def test_last_tokens_of_an_extreme_value_scale(fa, exponent):
         check_decode(o.double().cpu().numpy() * f, lse.cpu().numpy(), (ro * f, rl, (pv * f, vmax * f, qk)))
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("H,Hkv,Nq,causal", [(4, 1, 5, True), (24, 1, 1, False), (32, 2, 2, True), (16, 1, 4, False),
+                                             (33, 1, 2, True)])
+def test_many_items_of_many_rows(fa, d, H, Hkv, Nq, causal):
+    """17 to 66 rows per head and several items per CTA, some of them cut: two and four row
+    warpgroups, two row blocks, the queries of the next item prepared ahead."""
+    lens = [(b * 37) % 280 for b in range(260)]
+    lens[9], lens[100], lens[101], lens[259] = 5000, 12000, 0, 900
+    prob = _problem(len(lens), H, Hkv, Nq, d, 32, 16, lens, seed=d + H)
+    o, lse = fa.decode_paged_fp8(*[t.to(DEV) for t in prob], causal=causal)
+    assert fa.fa_device_status(None) == 0
+    some = [9, 100, 101, 259, *range(0, 260, 7)]
+    ref = oracle_decode(prob[0][some], *prob[1:5], prob[5][some], prob[6][some], causal, d ** -0.5)
+    check_decode(o[some].float().cpu().numpy(), lse[some].cpu().numpy(), ref)
+
+
 def test_groups_of_zero_scale(fa):
     prob = _problem(2, 4, 2, 1, 128, 16, 16, [300, 140], seed=9)
     for b, n in ((0, 300), (1, 140)):
