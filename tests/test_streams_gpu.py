@@ -147,3 +147,27 @@ def test_given_the_current_stream_or_the_default_one(fa, calls):
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(expect, g))
     assert fa.fa_device_status(None) == 0
+
+
+@pytest.mark.parametrize("name", PAGED + ["forward with cut key ranges", "decode", "backward_varlen"])
+def test_captured_on_a_side_stream(fa, calls, name):
+    """A capture whose calls run on a stream that forks from the capturing one and joins it."""
+    call = calls[name]
+    expect = call(None)
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+        del got
+    for _ in range(3):
+        for c in copies:
+            c.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(expect, copies))
+    assert fa.fa_device_status(None) == 0
