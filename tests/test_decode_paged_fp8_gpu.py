@@ -453,6 +453,57 @@ def test_pages_beyond_four_gigabytes(fa):
     check_decode(o.float().cpu().numpy(), lse.cpu().numpy(), oracle_decode(*prob, False, d ** -0.5))
 
 
+@pytest.mark.parametrize("B,Hkv,group", [(3, 1, 2), (64, 2, 4)])
+def test_calls_that_follow_one_another_at_once(fa, B, Hkv, group):
+    """Store, attention, page copy and attention with no other kernel between them, so that each
+    may start while the one before it ends: the bits of calls that wait for one another, eager and
+    replayed.  Magnitudes grow, so that scales beside each other change from step to step."""
+    H, d, ps, num, steps = 4 * Hkv, 128, 16, 8 * B, 60
+    g = torch.Generator().manual_seed(24)
+    table = torch.randperm(4 * B, generator=g).to(torch.int32).reshape(B, 4).to(DEV)
+    lens = [torch.full((B,), n, dtype=torch.int32, device=DEV) + (torch.arange(B, device=DEV) % 3).int()
+            for n in range(steps + 1)]
+    x = torch.randn((steps, B, 2 * Hkv, d), generator=g) * torch.exp2(torch.arange(steps) // 3 % 7)[:, None, None, None]
+    x, q = x.to(torch.bfloat16).to(DEV), torch.randn((B, H, 1, d), generator=g).to(torch.bfloat16).to(DEV)
+    src, dst = (torch.arange(4 * B, dtype=torch.int32, device=DEV) + k * 4 * B for k in (0, 1))
+    later = table + 4 * B
+
+    def caches():
+        return [torch.zeros((num, Hkv, ps, d), dtype=torch.uint8, device=DEV) for _ in "kv"] + \
+               [torch.zeros((num, Hkv, ps // group), device=DEV) for _ in "kv"]
+
+    def run(c, wait):
+        out = []
+        for i in range(steps):
+            fa.append_paged_fp8(x[i, :, :Hkv], x[i, :, Hkv:], *c, table, lens[i])
+            wait()
+            out += fa.decode_paged_fp8(q, *c, table, lens[i + 1])
+            wait()
+            fa.copy_pages(c, src, dst)
+            wait()
+            out += fa.decode_paged_fp8(q, *c, later, lens[i + 1])
+            wait()
+        return out
+
+    expect = run(caches(), torch.cuda.synchronize)
+    for a, b in zip(expect[0::4] + expect[1::4], expect[2::4] + expect[3::4]):
+        assert torch.equal(a, b)  # the copies
+    for _ in range(3):
+        got = run(caches(), lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(expect, got))
+    c = caches()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(c, lambda: None)
+    for _ in range(3):
+        for t in c:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(expect, got))
+    assert fa.fa_device_status(None) == 0
+
+
 def test_a_serving_loop(fa):
     """Prefill, decode steps, a fork, more steps, a release with compaction, more steps: the
     cache as the oracle keeps it, and attention over it, at every step."""
