@@ -186,7 +186,6 @@ struct Dec8Args {
     int tile_log2;                  // log2 of the keys per tile
     int start;                      // tiles that an item's start counts as in the cut, up to 3
     int run;                        // log2 of the keys that one entry of the scales stands for
-    int causal;
     float scale_log2;
     int *status;
     unsigned long long limit_ns;
@@ -522,7 +521,10 @@ __device__ __forceinline__ Walk start_walk(const Dec8Args &a, int c, int n_cta, 
 
 // ---------------------------------------------------------------- the kernel
 
-template <int NCH, int RB, int PACK>
+// CAUSAL: rows of one item see different numbers of keys.  A kernel of its own, because what that
+// needs (marks of NaN values, room for value scales) lies in code that runs once per item, where
+// its size alone costs time (B256 of 1..600 keys, one query: 60 us without it, 68 us with).
+template <int NCH, int RB, int PACK, bool CAUSAL>
 __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH, RB, PACK>::CTAS)
     fa_decode8_kernel(const __grid_constant__ Dec8Args a) {
     using T = Dec8Tile<NCH, RB, PACK>;
@@ -704,8 +706,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
         }
         if (r_first == 0) {
             for (int r = lane; r < RB; r += 32)
-                ms.limit[qb][r] = a.causal && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
-            if (a.causal)
+                ms.limit[qb][r] = CAUSAL && r < rows ? min(len, len - a.Nq + 1 + (r0 + r) % a.Nq) : len;
+            if (CAUSAL)
                 for (int i = lane; i < RB * NCH * 4; i += 32) ms.nan_cols[qb][i / (NCH * 4)][i % (NCH * 4)] = 0u;
             if (lane == 0) {
                 ms.len[qb] = len;
@@ -952,7 +954,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
             named_barrier_sync(id, 128);
             const int len = ms.len[qb];
-            const int full_keys = a.causal ? len - a.Nq + 1 : len;  // keys that every row sees
+            const int full_keys = CAUSAL ? len - a.Nq + 1 : len;  // keys that every row sees
             const int full_tiles = max(full_keys, 0) / TK;          // of those only
             for (int t = s.t0; t < s.t1; t += (int)(++j % PACK == 0)) {
                 const int u = j & 1, half = (int)(j % PACK);
@@ -1011,7 +1013,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     // terms out of e5m2's range: it counts for the common reference as 2^-60 of
                     // itself, and where it is above that still, the rows that see the key divide
                     // their terms.  Then every step up to the item's end comes here.
-                    const bool uneven = a.causal && partly, some_see = uneven && key >= full_keys;
+                    const bool uneven = CAUSAL && partly, some_see = uneven && key >= full_keys;
                     const float vs_all = some_see && vs > 0.f ? fmaxf(vs * 0x1p-60f, 0x1p-126f) : vs;
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -1255,7 +1257,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o0[e] *= f[e];
-                    if (a.causal && ms.nan_any[qb]) {
+                    if (CAUSAL && ms.nan_any[qb]) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             if (ms.nan_cols[qb][rw0 + q + e][dd >> 5] >> (dd & 31) & 1u) o0[e] = NAN;
@@ -1539,11 +1541,12 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     // d64: R = 16 25.1, 23.8, 24.0, 24.4; R = 32 40.5, 39.6, 38.7, 38.6; R = 64 61.2, 63.2, 55.9, 60.6).
     a.start = RB > 8 ? 3 : 2;
     a.run = p.group % 4 == 0 ? 2 : 0;  // four keys of a tile share a page and a group, or none do
-    a.causal = p.causal;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
-    auto kern = fa_decode8_kernel<NCH, RB, PACK>;
+    // a single query is the last token: it sees every key with either mask
+    auto kern = p.causal && p.Nq > 1 ? fa_decode8_kernel<NCH, RB, PACK, true>
+                                     : fa_decode8_kernel<NCH, RB, PACK, false>;
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = dec8_ctas<NCH, RB, PACK>(p);
