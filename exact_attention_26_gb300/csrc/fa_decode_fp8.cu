@@ -948,7 +948,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
             // kOneP / vref (0: none yet), vref the power of two that value scales are taken relative
             // to; and what a scale may not pass, vref, or -1 where some row's terms are divided
             float vmul = 0.f, vmax = 0.f;
-            auto vref_of = [&] { return vmul > 0.f ? kOneP * inverse2(vmul) : 0.f; };
+            auto vref_of = [&] { return !CAUSAL ? vmax : vmul > 0.f ? kOneP * inverse2(vmul) : 0.f; };
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             mbar_wait_warp<T::INLINE_WAITS>(bar(ms.q_full[qb]), (seg >> 1) & 1, g, SITE_DEC_MMA);
