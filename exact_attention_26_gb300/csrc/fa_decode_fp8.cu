@@ -44,12 +44,12 @@
 //   B1 H32 Hkv8 131072 keys    48 us      5.6 TB/s       37 us of stream; the rest is launch,
 //                                                        first tile, partials and merge
 //   B32 H32 Hkv8 1..8192 keys  49 us      5.6 TB/s       the same, twice an item per CTA
-//   B32 H16 Hkv8 30000 d64    165 us      6.0 TB/s       two keys to a row of a tile
-//   B8 H32 Hkv4 Nq4 d64        39 us      2.1 TB/s       32 rows per head: 16 tiles of 1.2 us per
-//                                                        CTA, the issue slots of softmax and
-//                                                        producer warps (54% over the launch) and
-//                                                        TMA's rows; then as above
-//   B1 H32 Hkv8 1000 keys       6.4 us                   latency of two launches
+//   B32 H16 Hkv8 30000 d64    166 us      6.0 TB/s       two keys to a row of a tile (pages of 32)
+//   B8 H32 Hkv4 Nq4 d64        38 us      2.1 TB/s       32 rows per head: 16 tiles of 1.2 us per
+//                                                        CTA; fixed work per step of 128 keys and
+//                                                        16 scores a thread, and TMA's half rows
+//                                                        (issue slots 53% busy); then as above
+//   B1 H32 Hkv8 1000 keys       6.5 us                   latency of two launches
 // Alone, the chain of a softmax warp takes 0.7k clocks (8 rows) to 0.9k (16 rows) per tile of 128
 // keys, against 1.3k clocks in which its bytes arrive at d = 128 for one of two CTAs on the SM.
 // Code that runs once per item is kept small: fetching it cold costs more than running it
@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
     const uint32_t tmem = ms.tmem;
     const Guard g{a.status, &ms.abort, a.limit_ns};
 
-    // What the kernels before this one wrote is there from here on; the merge kernel may launch.
+    // What the kernels before this one wrote is there from here on; the merge kernel may launch,
+    // not earlier: it reads seq_lens without a wait of its own.
     griddep_wait();
     griddep_launch_dependents();
 
@@ -1294,7 +1295,9 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
 
 // Merge of the partial results of the items that were cut: L = log2 sum 2^(L_s),
 // O = sum 2^(L_s - L) O_s.  Both kernels below are bound by latency: find the partials before
-// waiting for the attention kernel, then one or two rounds of loads.
+// waiting for the attention kernel, then one or two rounds of loads.  (What they read before that
+// wait is seq_lens only, written by nothing later than the kernels before the attention kernel,
+// which has waited for those before it lets a merge start.)
 
 // The running result of one warp over partials first, first + step, ... of a row's n: reference,
 // sum and output columns lane, lane + 32, ...; U partials with their L in flight at a time.
@@ -1535,7 +1538,8 @@ int launch_t(const Decode8Params &p, cudaStream_t stream) {
     a.row_blocks = (a.R + RB - 1) / RB;
     a.box = decode8_box_rows(p.page_size / PACK);
     a.tile_log2 = PACK == 2 ? 8 : 7;
-    // Measured, counted as 0, 1, 2 (and 3) tiles: one sequence of 131072 keys among 199 of 20, H32
+    // Measured, counted as 0, 1, 2 (and 3) tiles, in an earlier state whose calls of many short
+    // sequences took 8% longer: one sequence of 131072 keys among 199 of 20, H32
     // Hkv8, 94, 74, 62 us; B256 of 1..600 keys 70.6, 66.0, 65.0; B32 of 1..8192 keys 49.0, 49.3,
     // 49.2 (0.8 more with 3).  With more rows a start costs more (0, 2, 3, 4 of B8 Hkv4 19000 keys
     // d64: R = 16 25.1, 23.8, 24.0, 24.4; R = 32 40.5, 39.6, 38.7, 38.6; R = 64 61.2, 63.2, 55.9, 60.6).

@@ -246,7 +246,10 @@ int ensure_smem_attr(const void *kernel, int bytes);
 // Launch as a programmatic dependent of the stream's previous kernel: the CTAs may start (and
 // set up what needs no memory of others) while that kernel ends, and wait for its results with
 // griddepcontrol.wait.  Kernels launched this way make that wait before they read or write
-// global memory, and let their own dependents start after it, so a chain of them stays ordered.
+// global memory, and let their own dependents start only after it, so a chain of them stays
+// ordered: where one runs, all that the stream held before its predecessor is done.  Only for that
+// reason may the merges of the paged e4m3 decode read seq_lens before their wait (the attention
+// kernel that they follow does not write them, and what did is done).
 template <typename... P, typename... A>
 int launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
                      cudaStream_t stream, int cluster, A &&...args) {

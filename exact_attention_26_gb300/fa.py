@@ -785,7 +785,8 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
 # The calls on a paged e4m3 cache are made many times per decode step on kernels of a few
 # microseconds, so the extension makes them: it answers with the outputs, with a status, or
 # with None when an argument is not as expected.  What follows it here names the argument
-# that is wrong (and serves the calls the extension leaves alone, tensor subclasses).
+# that is wrong (and serves the calls the extension leaves alone, tensor subclasses).  The int32
+# outputs of one call of the extension are parts of one allocation, which any of them keeps.
 
 def _raw(stream, t):
     return None if stream is None else _stream(t, stream)
@@ -838,8 +839,8 @@ def append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     holds: k, v bf16 CUDA [T, Hkv, d] (rows contiguous, any row stride that is a multiple of
     8), rows cu_seqlens[b] .. cu_seqlens[b+1]-1 belonging to sequence b (int32 [B+1]; None:
     one new token each).  The cache is uint8 codes [num_pages, Hkv, page_size, d] and fp32
-    scales [num_pages, Hkv, page_size / group] for k and for v, changed in place; seq_lens is
-    not changed.  Returns None."""
+    scales [num_pages, Hkv, page_size / group], group at most 128, for k and for v, changed in
+    place; seq_lens is not changed.  Returns None."""
     r = native().append_paged_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                   cu_seqlens, _raw(stream, k))
     if r is not None:

@@ -449,7 +449,7 @@ int fa_append_paged_fp8(const void *k, const void *v, void *k_cache, void *v_cac
  *   B, H, Nq >= 1, Hkv divides H, (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, and
  *            B * Hkv * ceil((H / Hkv) * Nq / 8) * ceil(page_size * max_pages_per_seq / 128)
  *            < 2^31 (FA_ERR_INVALID_ARG where it overflows).
- *   scale  : finite and > 0.
+ *   scale  : finite and > 0.  o and lse overlap none of the inputs.
  *   workspace : device buffer of fa_decode_paged_fp8_workspace_bytes(...) bytes, 16-byte
  *            aligned, contents on entry irrelevant; calls that share one must not overlap.
  * The work is cut evenly over the SMs on the device, from seq_lens: a captured call replays
@@ -476,7 +476,7 @@ int fa_decode_paged_fp8(const void *q, const void *k_cache, const void *v_cache,
  * fa_free_pages lists the pages no sequence uses: pages [num_pages] gets them in ascending
  * order, then -1; count [1] their number.
  *
- * fa_fork_pages lets n new sequences continue from copies of sequences parents[i] (rows of
+ * fa_fork_pages lets n >= 1 new sequences continue from copies of sequences parents[i] (rows of
  * the table, the same one any number of times): rows [n][max_pages_per_seq] and lens [n]
  * are the children's, sharing the parent's full pages; a last page that is not full is
  * replaced by page fresh[i] and appears as the pair src[i] = parent's page, dst[i] =
@@ -504,7 +504,7 @@ int fa_compact_pages(const int *block_table, const int *seq_lens, int *new_table
  *   caches     : HOST array of n_caches device pointers (1 .. FA_MAX_COPY_CACHES), buffer c
  *                holding num_pages pages of page_bytes[c] >= 1 bytes (host array), any
  *                alignment (16-byte aligned pages are copied fastest).
- *   src, dst   : int32 [n_pairs], device memory; a pair with src[i] = -1 is passed over.
+ *   src, dst   : int32 [n_pairs], n_pairs >= 1, device memory; a pair with src[i] = -1 is passed over.
  *                No page may be a destination twice, or a destination and a source.
  *   count      : NULL, or device int32 [1]: only the first min(*count, n_pairs) pairs.
  * Pages out of range are skipped and recorded as FA_ERR_BAD_INDEX.
