@@ -415,7 +415,15 @@ def _stream(t, stream):
         if _raw_stream is not None:
             return _raw_stream(t.get_device())
         return torch.cuda.current_stream(t.device).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    _same_device(t, stream)
+    return stream.cuda_stream
+
+
+def _same_device(t, stream):
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device_index != t.get_device():
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on {t.device}")
 
 
 def _under(stream, t, fn, *args):
@@ -425,9 +433,10 @@ def _under(stream, t, fn, *args):
     are marked as in use on the caller's stream too."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return fn(*args)  # which refuses it
-    caller = torch.cuda.current_stream(t.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), t.device)
+    _same_device(t, stream)
+    caller = torch.cuda.current_stream(t.device)
     with torch.cuda.stream(stream):
         result = fn(*args)
     for r in result:

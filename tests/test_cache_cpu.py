@@ -241,3 +241,26 @@ def test_page_wrappers_reject(fa):  # noqa: F811
         fa.copy_pages([cache, x((8, 2, 16), torch.uint8, 1)], x((2,)), x((2,)))
     with pytest.raises(ValueError, match="contiguous"):
         fa.copy_pages([_on(torch.zeros((8, 4, 2)).transpose(1, 2), 0)], x((2,)), x((2,)))
+
+
+class _OtherStream:
+    """Stands for a torch stream of GPU 1."""
+    device_index, cuda_stream = 1, 0x1000
+
+
+def test_streams_of_another_device_are_refused(fa, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "Stream", _OtherStream)
+    q = _on(torch.zeros((3, 4, 1, 64), dtype=torch.bfloat16), 0)
+    a, i32 = _cache_args(), _on(torch.zeros(2, dtype=torch.int32), 0)
+    kv = _on(torch.zeros((3, 2, 64), dtype=torch.bfloat16), 0)
+    s = _OtherStream()
+    calls = [lambda: fa.decode_paged_fp8(q, **a, stream=s), lambda: fa.append_paged_fp8(kv, kv, **a, stream=s),
+             lambda: fa.free_pages(a["block_table"], a["seq_lens"], 16, 9, stream=s),
+             lambda: fa.compact_pages(a["block_table"], a["seq_lens"], 16, 9, stream=s),
+             lambda: fa.fork_pages(a["block_table"], a["seq_lens"], i32, i32, 16, 9, stream=s),
+             lambda: fa.copy_pages([a["k_cache"]], i32, i32, stream=s),
+             lambda: fa.forward(q, q, q, stream=s), lambda: fa.backward(q, q, q, q, q, q, stream=s),
+             lambda: fa.decode(q, q, q, stream=s), lambda: fa.quantize_fp8(q, stream=s)]
+    for call in calls:
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
