@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     // terms out of e5m2's range: it counts for the common reference as 2^-60 of
                     // itself, and where it is above that still, the rows that see the key divide
                     // their terms.  Then every step up to the item's end comes here.
-                    const bool uneven = CAUSAL && partly, some_see = uneven && key >= full_keys;
+                    const bool some_see = CAUSAL && partly && key >= full_keys;
                     const float vs_all = some_see && vs > 0.f ? fmaxf(vs * 0x1p-60f, 0x1p-126f) : vs;
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
@@ -1036,65 +1036,52 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                         vmul = kOneP * inverse2(vref);
                     }
                     vmax = vref;
-                    auto row_max = [&](int r) {
-                        return fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]), fmaxf(ms.part[2][r], ms.part[3][r]));
-                    };
-                    float down = 0.f;  // log2 of alpha
+                    float room = 0.f;
                     if (kk < RW) {
                         const int r = rw0 + kk;
                         const float m_old = -ms.nref[r];
-                        const float m = row_max(r);
+                        const float m = fmaxf(fmaxf(ms.part[0][r], ms.part[1][r]),
+                                              fmaxf(ms.part[2][r], ms.part[3][r]));
                         const bool up = m > m_old + kMoveLog2;
-                        if (up) down = m_old - m;
-                        ms.alpha[r] = up ? ex2(down) : 1.f;
+                        const float down = up ? m_old - m : 0.f;  // log2 of alpha
+                        ms.alpha[r] = ex2(down);
                         if (up) ms.nref[r] = -m;
-                    }
-                    if (__builtin_expect(uneven, 0)) {  // the same of p times the value scale
-                        named_barrier_sync(id, 128);
-                        const float lift =  // log2 of the scale over the reference, rounded up
-                            some_see && vs > vref ? (float)((int)(__float_as_uint(vs) >> 23) -
-                                                            (int)(__float_as_uint(vref) >> 23) + 1)
-                                                  : 0.f;
-#pragma unroll
-                        for (int r = 0; r < RW; ++r) {
-                            const float m = warp_max(x[r] + lift);
-                            if (lane == r) ms.part[w4][rw0 + r] = m;
-                        }
-                        named_barrier_sync(id, 128);
-                        if (kk < RW) {
-                            const int r = rw0 + kk;
+                        if (CAUSAL && partly) {
+                            // what the row's terms are divided by: the largest scale among the keys
+                            // of the tile that it sees and others do not, over the reference, or
+                            // what earlier ones leave of it
+                            const int from = max(full_keys - t * TK, 0), to = min(ms.limit[qb][r] - t * TK, TK);
+                            float top = 0.f;
+                            if (from < to)
+                                for (int i = from >> a.run; i <= (to - 1) >> a.run; ++i) top = fmaxf(top, ms.v_scale[st][i]);
+                            auto log_over = [](float x, float y) {  // of powers of two
+                                return (float)((int)(__float_as_uint(x) >> 23) - (int)(__float_as_uint(y) >> 23));
+                            };
                             const float old = roomy ? ms.room[r] : 0.f;
-                            const float v_up = roomy ? (float)((int)(__float_as_uint(vref) >> 23) -
-                                                               (int)(__float_as_uint(v_old) >> 23))
-                                                     : 0.f;
-                            const float left = fmaxf(old + down - v_up, 0.f), need = row_max(r) + ms.nref[r];
-                            const float room = ceilf(need > left + kMoveLog2 ? need : left);
+                            const float left = roomy ? old + down - log_over(vref, v_old) : 0.f;
+                            room = fmaxf(ceilf(left), top > vref ? log_over(top, vref) + 1.f : 0.f);
                             ms.alpha_o[r] = ex2(down + old - room);
                             ms.room[r] = room;
                         }
                     }
-                    named_barrier_sync(id, 128);
+                    const bool divide = vote_group(id, room > 0.f);
 #pragma unroll
                     for (int r = 0; r < RW; ++r) {
                         l[r] *= ms.alpha[rw0 + r];
                         x[r] += ms.nref[rw0 + r];
                     }
-                    if (__builtin_expect(uneven, 0)) {
+                    if (CAUSAL && divide) {
+                        vmax = -1.f;
 #pragma unroll
-                        for (int r = 0; r < RW; ++r)
-                            if (ms.room[rw0 + r] > 0.f) vmax = -1.f;
-                        if (vmax < 0.f) {
-#pragma unroll
-                            for (int r = 0; r < RW; ++r) {  // the sum keeps p itself
-                                const float p = ex2(x[r]);
-                                x[r] -= ms.room[rw0 + r];
-                                l[r] += p - ex2(x[r]);
-                            }
+                        for (int r = 0; r < RW; ++r) {  // the sum keeps p itself
+                            const float p = ex2(x[r]);
+                            x[r] -= ms.room[rw0 + r];
+                            l[r] += p - ex2(x[r]);
                         }
                     }
                     if (!first) {  // O^T to the new references, once PV of the step before is done
                         const float fo = vref > 0.f ? v_old * inverse2(vref) : 1.f;
-                        const float *alpha = uneven ? ms.alpha_o : ms.alpha;
+                        const float *alpha = CAUSAL && partly ? ms.alpha_o : ms.alpha;
                         mbar_wait_warp<T::INLINE_WAITS>(bar(ms.pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, g, SITE_DEC_MMA);
                         tc_fence_after();
 #pragma unroll 1
