@@ -1009,6 +1009,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 }
                 if (move) {
                     // new references: the step's maximum where it passes the old one by 2^6
+                    __syncwarp();  // a vote's barrier does not bring a warp's lanes together
                     scores(std::false_type());
                     // Where not every row sees the key, its value scale must not push the others'
                     // terms out of e5m2's range: it counts for the common reference as 2^-60 of
@@ -1026,6 +1027,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                     const bool roomy = vmax < 0.f;
                     const float v_old = vref_of();
                     float vref = v_old;
+                    __syncwarp();
                     named_barrier_sync(id, 128);
                     const float vm = fmaxf(fmaxf(ms.vpart[wg][0], ms.vpart[wg][1]),
                                            fmaxf(ms.vpart[wg][2], ms.vpart[wg][3]));
@@ -1189,6 +1191,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 const float sum = warp_sum8(v, lane);
                 if ((lane & 3) == 0) ms.part[w4][rw0 + q + (lane >> 2)] = sum;
             }
+            __syncwarp();
             named_barrier_sync(id, 128);
             const bool whole = s.t0 == 0 && s.t1 == s.nt;
             const bool bad = ms.bad[qb] != 0;
@@ -1265,6 +1268,7 @@ __global__ void __launch_bounds__(Dec8Tile<NCH, RB, PACK>::THREADS, Dec8Tile<NCH
                 }
             }
             tc_fence_before();
+            __syncwarp();
             named_barrier_sync(id, 128);  // the state above is free for the next segment
             if (kk == 0) mbar_arrive(bar(ms.q_empty[qb]));
             ++seg;
