@@ -75,11 +75,12 @@ def draw(rng):
         Hkv = rng.choice((1, 2, 4, 5, 8, 16))
         G = rng.choice((1, 2, 3, 4, 6, 8))
         B, Nt = _log_int(rng, 1, 64), _log_int(rng, 1, 128)
-        Nq = rng.choice((Nt, Nt, rng.randint(1, Nt)))
+        chain = rng.random() < 0.2
+        Nq = Nt if chain else rng.choice((Nt, Nt, rng.randint(1, Nt)))
         most = min(300_000_000 // (B * Hkv * d), 50_000_000_000 // (B * Hkv * G * Nq * d))
         hi = _log_int(rng, 20, max(21, min(100000, most)))
         return dict(op=op, B=B, H=Hkv * G, Hkv=Hkv, Nt=Nt, Nq=Nq, d=d, page=page,
-                    lo=rng.choice((0, hi // 3 + 1, hi)), hi=hi, chain=rng.random() < 0.2,
+                    lo=rng.choice((0, hi // 3 + 1, hi)), hi=hi, chain=chain,
                     ragged=rng.random() < 0.5)
     if op == "verify":
         V = _log_int(rng, 1000, 160000)
