@@ -1068,6 +1068,92 @@ extern "C" int fa_decode_paged_fp8(const void *q, const void *k_cache, const voi
 namespace fa {
 namespace {
 
+int check_tree(int B, int H, int Hkv, int Nq, int Nt, int d, int page_size, int max_pages,
+               int num_pages) {
+    int rc = check_paged_sizes(B, H, Hkv, Nq, d, page_size, max_pages, num_pages);
+    if (rc != FA_OK) return rc;
+    if (Nt < Nq || (long long)page_size * max_pages >= (1LL << 31) - 1024 ||
+        (long long)num_pages * Hkv >= (1LL << 31) || (long long)B * Nt >= (1LL << 31))
+        return FA_ERR_INVALID_ARG;
+    if (Nt > FA_MAX_TREE_NODES) return FA_ERR_UNSUPPORTED;
+    TreeParams p{};
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.Nt = Nt;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    return tree_max_tiles(p) < (1LL << 31) ? FA_OK : FA_ERR_INVALID_ARG;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" size_t fa_decode_paged_tree_workspace_bytes(int B, int H, int Hkv, int Nq, int Nt, int d,
+                                                       int page_size, int max_pages_per_seq) {
+    if (check_tree(B, H, Hkv, Nq, Nt, d, page_size, max_pages_per_seq, 1) != FA_OK) return 0;
+    DeviceCache *dc = nullptr;
+    if (current_device(&dc) != FA_OK) return 0;
+    TreeParams p{};
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.Nt = Nt;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_sms = dc->num_sms;
+    return tree_workspace_bytes(p);
+}
+
+extern "C" int fa_decode_paged_tree(const void *q, const void *k_cache, const void *v_cache,
+                                    const int *block_table, const int *seq_lens, const int *parents,
+                                    void *o, float *lse, int B, int H, int Hkv, int Nq, int Nt, int d,
+                                    int page_size, int max_pages_per_seq, int num_pages, float scale,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
+    int rc = check_tree(B, H, Hkv, Nq, Nt, d, page_size, max_pages_per_seq, num_pages);
+    if (rc != FA_OK) return rc;
+    if ((rc = check_scale(scale)) != FA_OK) return rc;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(lse) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(parents) || !aligned16(workspace))
+        return FA_ERR_MISALIGNED;
+    if (!workspace) return FA_ERR_WORKSPACE;
+    DeviceCache *dc = nullptr;
+    if ((rc = current_device(&dc)) != FA_OK) return rc;
+    TreeParams p{};
+    p.v_cache = v_cache;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.parents = parents;
+    p.o = o;
+    p.lse = lse;
+    p.workspace = workspace;
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.Nt = Nt;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.scale_log2 = scale * kLog2e;
+    p.status = dc->status;
+    p.num_sms = dc->num_sms;
+    if (workspace_bytes < tree_workspace_bytes(p)) return FA_ERR_WORKSPACE;
+    if ((rc = make_bhnd_map(&p.tm_q, q, 1, B * H * Nq, d, tree_query_box(p))) != FA_OK) return rc;
+    if ((rc = make_bhnd_map(&p.tm_k, k_cache, num_pages * Hkv, page_size, d, tree_box_rows(p))) != FA_OK) return rc;
+    if ((rc = make_bhnd_map(&p.tm_v, v_cache, num_pages * Hkv, page_size, d, tree_box_rows(p))) != FA_OK) return rc;
+    return launch_tree(p, static_cast<cudaStream_t>(stream));
+}
+
+namespace fa {
+namespace {
+
 int check_pages(int B, int max_pages, int page_size, int num_pages) {
     if (B < 1 || max_pages < 1 || page_size < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
     if ((long long)B * max_pages >= (1LL << 31) || (long long)page_size * max_pages >= (1LL << 31))

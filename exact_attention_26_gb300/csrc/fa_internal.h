@@ -48,6 +48,9 @@ enum WaitSite : int {
     SITE_COPY_BAD_PAGE = 35,
     SITE_DEC8_BAD_LEN = 36,
     SITE_DEC8_BAD_PAGE = 37,
+    SITE_TREE_BAD_LEN = 38,
+    SITE_TREE_BAD_PAGE = 39,
+    SITE_TREE_BAD_PARENT = 40,
 };
 
 // Default limit of one in-kernel wait.
@@ -234,6 +237,28 @@ int decode8_box_rows(int rows);
 long long decode8_max_tiles(const Decode8Params &p);
 size_t decode8_workspace_bytes(const Decode8Params &p);  // of its sizes and num_sms
 int launch_decode8(const Decode8Params &p, cudaStream_t stream);
+
+// Attention of drafted tokens over the paged bf16 cache.
+struct TreeParams {
+    CUtensorMap tm_q, tm_k, tm_v;    // q as one plane of B * H * Nq rows, boxes of tree_query_box rows;
+                                     // k, v as num_pages * Hkv planes, boxes of tree_box_rows rows
+    const void *v_cache;
+    const int *block_table, *seq_lens;
+    const int *parents;              // [B][Nt], or null: a chain
+    void *o;                         // bf16 [B][H][Nq][d]
+    float *lse;                      // [B][H][Nq]
+    void *workspace;
+    int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
+    float scale_log2;
+    int *status;
+    int num_sms;
+};
+int tree_box_rows(const TreeParams &p);
+int tree_query_box(const TreeParams &p);
+// Tiles of all items at the longest possible lengths; the kernels count in ints.
+long long tree_max_tiles(const TreeParams &p);
+size_t tree_workspace_bytes(const TreeParams &p);  // of its sizes and num_sms
+int launch_tree(const TreeParams &p, cudaStream_t stream);
 
 // Devices the per-device caches of the host code cover (ordinals 0..63).
 constexpr int kMaxCachedDevices = 64;

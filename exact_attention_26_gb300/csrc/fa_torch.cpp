@@ -202,6 +202,100 @@ PyObject *decode_paged_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A paged bf16 cache and its table.
+struct Cache16 {
+    const Tensor *kc, *vc, *bt, *lens;
+    int B, num_pages, Hkv, page_size, d, max_pages;
+
+    bool read(PyObject *const *a, int device) {
+        kc = tensor(a[0], at::kBFloat16, 4);
+        vc = tensor(a[1], at::kBFloat16, 4);
+        bt = tensor(a[2], at::kInt, 2);
+        lens = tensor(a[3], at::kInt, 1);
+        if (!on(kc, device) || !on(vc, device) || !on(bt, device) || !on(lens, device)) return false;
+        for (int64_t s : kc->sizes())
+            if (s < 1 || !is_int(s)) return false;
+        if (!vc->sizes().equals(kc->sizes())) return false;
+        if (!is_int(bt->size(0)) || !is_int(bt->size(1)) || bt->size(1) < 1 || lens->size(0) != bt->size(0))
+            return false;
+        num_pages = (int)kc->size(0);
+        Hkv = (int)kc->size(1);
+        page_size = (int)kc->size(2);
+        d = (int)kc->size(3);
+        B = (int)bt->size(0);
+        max_pages = (int)bt->size(1);
+        return true;
+    }
+};
+
+// q, k_cache, v_cache, block_table, seq_lens, parents, scale, out, lse, workspace, stream
+PyObject *decode_paged_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 11) return declined();
+    const Tensor *q = tensor(a[0], at::kBFloat16, 4);
+    if (!q) return declined();
+    const int device = q->get_device();
+    Cache16 c;
+    if (!c.read(a + 1, device)) return declined();
+    const int64_t B = q->size(0), H = q->size(1), Nq = q->size(2);
+    if (B != c.B || q->size(3) != c.d || H % c.Hkv || !is_int(H) || !is_int(Nq)) return declined();
+    const int *parents = nullptr;
+    int64_t Nt = Nq;
+    if (a[5] != Py_None) {
+        const Tensor *t = tensor(a[5], at::kInt, 2);
+        if (!on(t, device) || t->size(0) != B || t->size(1) < Nq || !is_int(t->size(1))) return declined();
+        parents = ptr<int>(*t);
+        Nt = t->size(1);
+    }
+    double scale = 1.0 / std::sqrt((double)c.d);
+    if (a[6] != Py_None) {
+        scale = PyFloat_AsDouble(a[6]);
+        if (PyErr_Occurred()) return nullptr;
+    }
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[10], device)) return nullptr;
+    Tensor out, lse, ws;
+    if (a[7] == Py_None) {
+        out = make({B, H, Nq, c.d}, at::kBFloat16, device);
+        stream.hand_out(out);
+    } else {
+        const Tensor *t = tensor(a[7], at::kBFloat16, 4);
+        if (!on(t, device) || !t->sizes().equals(q->sizes())) return declined();
+        out = *t;
+    }
+    if (a[8] == Py_None) {
+        lse = make({B, H, Nq}, at::kFloat, device);
+        stream.hand_out(lse);
+    } else {
+        const Tensor *t = tensor(a[8], at::kFloat, 3);
+        if (!on(t, device) || !shaped(*t, {B, H, Nq})) return declined();
+        lse = *t;
+    }
+    if (a[9] == Py_None) {
+        const size_t need = fa_decode_paged_tree_workspace_bytes((int)B, (int)H, c.Hkv, (int)Nq, (int)Nt, c.d,
+                                                                 c.page_size, c.max_pages);
+        ws = make({(int64_t)need}, at::kByte, device);
+    } else {
+        const Tensor *t = THPVariable_CheckExact(a[9]) ? &THPVariable_Unpack(a[9]) : nullptr;
+        if (!t || !t->is_cuda() || t->scalar_type() != at::kByte || !t->is_contiguous() || !on(t, device))
+            return declined();
+        ws = *t;
+    }
+    const int rc = fa_decode_paged_tree(q->data_ptr(), c.kc->data_ptr(), c.vc->data_ptr(), ptr<int>(*c.bt),
+                                        ptr<int>(*c.lens), parents, out.data_ptr(), ptr<float>(lse), (int)B, (int)H,
+                                        c.Hkv, (int)Nq, (int)Nt, c.d, c.page_size, c.max_pages, c.num_pages,
+                                        (float)scale, ws.data_ptr(), (size_t)ws.numel(), stream.raw);
+    if (rc != FA_OK) return PyLong_FromLong(rc);
+    PyObject *po = a[7] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[7]);
+    PyObject *pl = a[8] == Py_None ? THPVariable_Wrap(lse) : Py_NewRef(a[8]);
+    PyObject *r = po && pl ? PyTuple_Pack(2, po, pl) : nullptr;
+    Py_XDECREF(po);
+    Py_XDECREF(pl);
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
 // New rows [T, Hkv, d] at any row stride; -1 if they are not that.
 long long row_stride(const Tensor &t, const Cache &c) {
     if (!t.is_cuda() || t.scalar_type() != at::kBFloat16 || t.dim() != 3 || t.size(0) < 1 || !is_int(t.size(0)) ||
@@ -376,7 +470,7 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define FN(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {FN(decode_paged_fp8), FN(append_paged_fp8), FN(free_pages), FN(fork_pages),
+PyMethodDef kMethods[] = {FN(decode_paged_fp8), FN(decode_paged_tree), FN(append_paged_fp8), FN(free_pages), FN(fork_pages),
                           FN(compact_pages), FN(copy_pages), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr,
                        nullptr};

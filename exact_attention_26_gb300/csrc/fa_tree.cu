@@ -1,0 +1,777 @@
+// Attention of drafted tokens against a paged bf16 cache (fa_decode_paged_tree; definition in
+// fa.h): every query sees its sequence's cached tokens, itself and its ancestors in the tree.
+//
+// The R = (H / Hkv) * Nq query rows of a key/value head are the M of the products, 128 rows to a
+// block, one or two blocks per CTA that share each tile of keys on its way through shared memory:
+//   S (128 rows x BK keys) = Q K^T        both from shared memory
+//   O (128 rows x d)      += P V          P, bf16, from tensor memory over S's own columns
+// A thread owns one row, so the running maximum and sum of the softmax are per-thread work without
+// exchange, and so is the mask: a tile of keys behind the cached ones is looked up in the row's
+// bits of the nodes that it sees (a tile before them is not masked at all).  The reference of a
+// row's exponents moves only when a score passes it by 2^8; then the thread rescales its row of O.
+// P is rounded to bf16 (2^-8 at most of each term, the sum of the row is taken before that): V is
+// bf16, the product takes both of one type, and O is rounded to bf16 at the end all the same.
+//
+// Work is cut over the CTAs as fa_cut.cuh describes.  Warps: one softmax warpgroup per block of
+// rows (they also write the results), then one each for MMA issue and tensor memory, for the TMA
+// copies of K and V, and for the queries and the trees.  Per CTA: a ring of K_0 V_0 K_1 V_1 ...,
+// two S slots, one or two query buffers.  A *unit* is one block's work on one tile; units take the
+// S slots in turn.
+#include <type_traits>
+
+#include "fa_cut.cuh"
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kMoveLog2 = 8.0f;
+constexpr int kMaxNodes = FA_MAX_TREE_NODES, kNodeWords = kMaxNodes / 32;
+
+template <int D, int NB>
+struct TreeTile {
+    static constexpr int DP = (D + 63) / 64 * 64;       // row width in shared memory
+    static constexpr int NCH = DP / 64;                 // 128-byte swizzle spans per row
+    static constexpr int BK = D == 256 ? 64 : 128;      // keys per tile
+    static constexpr int RB = 128 * NB;                 // query rows per item
+    static constexpr int THREADS = 32 * (4 * NB + 3);
+    static constexpr uint32_t CHUNK = BK * 128;
+    static constexpr uint32_t SLOT = NCH * CHUNK;
+    static constexpr uint32_t Q_CHUNK = 128 * 128;
+    static constexpr uint32_t Q_BLOCK = NCH * Q_CHUNK;
+    static constexpr uint32_t Q_BYTES = NB * Q_BLOCK;
+    static constexpr int QBUF = Q_BYTES <= 32 * 1024 ? 2 : 1;
+    static constexpr uint32_t MISC = 20 * 1024;
+    static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - MISC - 1024) / SLOT) / 2 * 2;
+    static constexpr int STAGES = FIT > 8 ? 8 : FIT;    // 128 KB of keys and values
+    static constexpr uint32_t OFF_Q = STAGES * SLOT;
+    static constexpr uint32_t OFF_MISC = OFF_Q + QBUF * Q_BYTES;
+    static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
+    static constexpr uint32_t TM_O = 2 * BK;
+    static constexpr uint32_t TM_USED = TM_O + NB * DP;
+    static constexpr uint32_t TM_COLS = TM_USED <= 256 ? 256 : 512;
+    static_assert(STAGES >= 4, "two tiles in the ring");
+    static_assert(TM_USED <= 512, "tensor memory budget");
+    static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+
+template <int STAGES, int NB>
+struct TreeMisc {
+    unsigned long long full[STAGES], empty[STAGES];
+    // per block of rows, by its own units in turn: S is there, P is there (of two), O is there
+    unsigned long long s_full[NB][2], p_full[NB][2], pv_done[NB];
+    unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done;
+    uint32_t tmem;
+    int abort;
+    // per segment of this CTA's work, in turn:
+    int bad_page[2], bad_tree[2];         // a page or a parent out of range
+    int special_any[2];
+    uint32_t special[2][kNodeWords];      // nodes whose values have infinities or NaN
+    uint32_t sees[2][kMaxNodes][kNodeWords];  // the nodes that a node sees, as bits
+};
+
+struct TreeArgs {
+    CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; (d, page_size, num_pages *
+                                    // Hkv), boxes 64 x box x 1
+    const __nv_bfloat16 *v_cache;
+    const int *block_table, *seq_lens, *parents;
+    __nv_bfloat16 *o;
+    float *lse;
+    float *part_o, *part_l;         // [CTA][2][RB][d], [CTA][2][RB]
+    FastDiv by_page;
+    int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
+    int R, row_blocks;              // query rows per key/value head, items of RB of them
+    int box, box_q;                 // rows of a TMA box
+    int tile_log2;
+    int start;
+    float scale_log2;
+    int *status;
+    unsigned long long limit_ns;
+};
+
+__device__ __forceinline__ bool len_ok(const TreeArgs &a, int len) {
+    return len >= 0 && (long long)len <= (long long)a.page_size * a.max_pages;
+}
+__device__ __forceinline__ int tiles_of_len(const TreeArgs &a, int len) {
+    return len_ok(a, len) ? (len + a.Nt + (1 << a.tile_log2) - 1) >> a.tile_log2 : 0;
+}
+// A sequence always has its nodes' tiles, so attention writes its rows.
+__device__ __forceinline__ bool empty_len(const TreeArgs &, int) { return false; }
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Of a pair of bf16 values, the bits of those that are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+    const uint32_t lo = (x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+    const uint32_t hi = (x & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+    return lo | hi;
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
+    fa_tree_kernel(const __grid_constant__ TreeArgs a) {
+    using T = TreeTile<D, NB>;
+    constexpr int ST = T::STAGES, BK = T::BK, NCH = T::NCH, QBUF = T::QBUF;
+    using Misc = TreeMisc<ST, NB>;
+    static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
+    constexpr int kMmaWarp = 4 * NB, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
+    extern __shared__ uint8_t tree_smem[];
+    const uint32_t raw = smem_u32(tree_smem);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = tree_smem + (base - raw);
+    Misc &ms = *reinterpret_cast<Misc *>(gbase + T::OFF_MISC);
+    auto bar = [](unsigned long long &b) { return smem_u32(&b); };
+    const uint32_t sQ = base + T::OFF_Q;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(bar(ms.full[s]), 1);
+            mbar_init(bar(ms.empty[s]), 1);
+        }
+        for (int u = 0; u < 2; ++u) {
+            for (int k = 0; k < NB; ++k) {
+                mbar_init(bar(ms.s_full[k][u]), 1);
+                mbar_init(bar(ms.p_full[k][u]), 4);  // one arrival per softmax warp
+            }
+            mbar_init(bar(ms.q_full[u]), 1);
+            mbar_init(bar(ms.q_empty[u]), 1);
+            mbar_init(bar(ms.info_full[u]), 1);
+            mbar_init(bar(ms.info_empty[u]), 4 * NB);
+        }
+        for (int k = 0; k < NB; ++k) mbar_init(bar(ms.pv_done[k]), 1);
+        mbar_init(bar(ms.done), 1);
+        ms.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&ms.tmem), T::TM_COLS);
+        tmem_relinquish();
+    }
+    if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_desc(&a.tm_q);
+        tma_prefetch_desc(&a.tm_k);
+        tma_prefetch_desc(&a.tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    const Guard g{a.status, &ms.abort, a.limit_ns};
+
+    // What the kernels before this one wrote is there from here on.
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Every warp finds the CTA's first tile for itself.
+    Cut cut;
+    Walk walk = start_walk(a, blockIdx.x, gridDim.x, &cut);
+    Segment s{};
+    auto rows_of = [&](const Segment &x) { return min(T::RB, a.R - x.rb * T::RB); };
+    auto blocks_of = [&](const Segment &x) { return NB == 1 ? 1 : (rows_of(x) + 127) / 128; };
+
+    if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ K and V
+        // A tile is a run of boxes of `box` rows (the largest power of two that divides a page's
+        // rows, so a box never straddles two pages); lane i looks up and copies box i (and i +
+        // 32, ... of pages that allow only tiny boxes).  Boxes behind the last node are not copied.
+        uint32_t n = 0, seg = 0;  // ring slots used so far; segments begun
+        bool ok = true;
+        const int boxes = BK / a.box;
+        for (; ok && walk.next(a, &s); ++seg) {
+            const int ib = seg & 1, len = a.seq_lens[s.b], keys = len + a.Nt;
+            const int *bt = a.block_table + (size_t)s.b * a.max_pages;
+            // page of the key that is `at` keys into tile t, -1 where there is none
+            auto page_at = [&](int t, int at) {
+                const int key = t * BK + at;
+                if (t >= s.t1 || key >= keys) return -1;
+                const uint32_t i = a.by_page.div((uint32_t)key);
+                return i < (uint32_t)a.max_pages ? __ldg(bt + i) : -1;
+            };
+            auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
+            int pg = lane < boxes ? page_at(s.t0, lane * a.box) : -1;
+            if (seg >= 2)  // `bad_page` of the segment before the last has been read
+                ok = mbar_wait_warp(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+            if (!ok) break;
+            if (lane == 0) ms.bad_page[ib] = 0;
+            __syncwarp();
+#pragma unroll 1
+            for (int t = s.t0; ok && t < s.t1; ++t) {
+                const int pg_next = lane < boxes ? page_at(t + 1, lane * a.box) : -1;
+                auto page_of = [&](int i) { return i < 32 ? pg : page_at(t, i * a.box); };
+                int mine = 0;
+#pragma unroll 1
+                for (int i = lane; i < boxes; i += 32) {
+                    const int key = t * BK + i * a.box;
+                    if (valid(page_of(i))) {
+                        ++mine;
+                    } else if (key < keys) {  // wrong if it holds a token: places without a node do not
+                        bool token = key < len || !a.parents;
+                        for (int j = key - len; !token && j < min(key - len + a.box, a.Nt); ++j)
+                            token = a.parents[(size_t)s.b * a.Nt + j] >= -1;
+                        if (token) ms.bad_page[ib] = 1;
+                    }
+                }
+                const uint32_t bytes = (uint32_t)__reduce_add_sync(kFull, mine) * (uint32_t)a.box * 128u * NCH;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int slot = (int)(n % ST);
+                    ok = n < (uint32_t)ST ||
+                         mbar_wait_warp(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
+                    if (!ok) break;
+                    const uint32_t fb = bar(ms.full[slot]);
+                    const CUtensorMap *map = kv ? &a.tm_v : &a.tm_k;
+                    if (lane == 0) {
+                        if (bytes) mbar_arrive_expect_tx(fb, bytes);
+                        else mbar_arrive(fb);
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = lane; i < boxes; i += 32) {
+                        const int page = page_of(i), row = i * a.box;
+                        if (!valid(page)) continue;
+                        const uint32_t key = (uint32_t)(t * BK + row);
+                        const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
+                        const uint32_t dst = base + slot * T::SLOT + row * 128;
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_3d(dst + c * T::CHUNK, map, fb, c * 64, y, page * a.Hkv + s.kvh);
+                    }
+                    __syncwarp();
+                }
+                pg = pg_next;
+            }
+        }
+        if (*g.abort) {
+            // let every copy still in flight land before the CTA exits
+            volatile int never = 0;
+            const Guard g2{a.status, &never, kWaitLimitNs};
+            for (uint32_t i = n > (uint32_t)ST ? n - ST : 0; i < n; ++i)
+                mbar_wait_warp(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        if (blockIdx.x == 0) {
+            bool ok = true;
+            for (int b = lane; b < a.B; b += 32) ok = ok && len_ok(a, a.seq_lens[b]);
+            if (!__all_sync(kFull, ok) && lane == 0) {
+                atomicCAS(a.status + 1, 0, SITE_TREE_BAD_LEN);
+                atomicExch(a.status, FA_ERR_BAD_INDEX);
+            }
+        }
+        constexpr uint32_t kIdescS = idesc_bf16_f32(128, BK, false, false);
+        constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+        Walk ahead = walk;   // segments of S, up to two units ahead of O
+        Segment sa{};
+        bool more = ahead.next(a, &sa);
+        int ta = sa.t0, ba = 0, nba = more ? blocks_of(sa) : 0;
+        uint32_t js = 0, jp = 0, seg = 0;              // units whose S, O is issued; segments of S begun
+        uint32_t cs[NB] = {}, cp[NB] = {};             // the same per block
+        bool ok = true;
+        struct Slot {  // a ring slot of K or V and the parity of its round
+            int at;
+            uint32_t round;
+            __device__ __forceinline__ void advance() {
+                at += 2;
+                if (at >= ST) at -= ST, round ^= 1;
+            }
+        };
+        Slot k_slot{0, 0}, v_slot{1, 0};
+        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
+        const uint64_t d_v = sdesc_sw128(base, T::CHUNK, 1024);
+        auto issue_s = [&]() {
+            const int qb = (int)(seg % QBUF);
+            if (ta == sa.t0 && ba == 0)
+                ok = mbar_wait_warp(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
+            if (ok && ba == 0)
+                ok = mbar_wait_warp(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t dq = desc_add(d_q, qb * T::Q_BYTES + ba * T::Q_BLOCK);
+            const uint64_t dk = desc_add(d_k, k_slot.at * T::SLOT);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss_elect(tmem + (js & 1) * BK, desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32),
+                             desc_add(dk, (ks >> 2) * T::CHUNK + (ks & 3) * 32), kIdescS, ks > 0 ? 1u : 0u);
+            const uint32_t m = NB == 2 && ba == 1 ? cs[NB - 1]++ : cs[0]++;
+            tc_commit_elect(bar(ms.s_full[ba][m & 1]));
+            ++js;
+            if (++ba < nba) return;
+            ba = 0;
+            tc_commit_elect(bar(ms.empty[k_slot.at]));
+            k_slot.advance();
+            if (++ta == sa.t1) {
+                tc_commit_elect(bar(ms.q_empty[qb]));
+                ++seg;
+                more = ahead.next(a, &sa);
+                ta = sa.t0;
+                nba = blocks_of(sa);
+            }
+        };
+        // S of what has not arrived is not waited for while the O before it can be issued
+        auto ready = [&]() {
+            bool r = ba > 0 || mbar_test(bar(ms.full[k_slot.at]), k_slot.round);
+            if (ta == sa.t0 && ba == 0) r = r && mbar_test(bar(ms.q_full[seg % QBUF]), (seg / QBUF) & 1);
+            return __all_sync(kFull, r);
+        };
+        while (ok && walk.next(a, &s)) {
+            const int nb = blocks_of(s);
+            for (int t = s.t0; ok && t < s.t1; ++t)
+                for (int blk = 0; ok && blk < nb; ++blk, ++jp) {
+#pragma unroll 1
+                    while (ok && more && (js == jp || (js == jp + 1 && ready()))) issue_s();
+                    const uint32_t m = NB == 2 && blk == 1 ? cp[NB - 1]++ : cp[0]++;
+                    ok = ok && mbar_wait_warp(bar(ms.p_full[blk][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+                    if (ok && blk == 0)
+                        ok = mbar_wait_warp(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dv = desc_add(d_v, v_slot.at * T::SLOT);
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ++ks)
+                        mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks * 8,
+                                     desc_add(dv, ks * 2048), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
+                    tc_commit_elect(bar(ms.pv_done[blk]));
+                    if (blk + 1 == nb) {
+                        tc_commit_elect(bar(ms.empty[v_slot.at]));
+                        v_slot.advance();
+                    }
+                }
+        }
+        // fires once every MMA issued above has completed (normal or aborted run)
+        tc_commit_elect(bar(ms.done));
+        volatile int never = 0;
+        const Guard g2{a.status, &never, kWaitLimitNs};
+        mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
+    } else if (warp == kAuxWarp) {
+        // ------------------------------------------------------ queries and trees
+        uint32_t seg = 0, q_sent = 0;
+        bool ok = true;
+        // the segment's query rows; rows behind them in the last box are other heads', or zeros
+        // past the tensor, and what they give is dropped
+        auto put_queries = [&]() {
+            const int qb = (int)(seg % QBUF), nb = blocks_of(s);
+            if (seg >= (uint32_t)QBUF)
+                ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg / QBUF) - 1) & 1, g, SITE_DEC_EMPTY);
+            if (!ok) return;
+            if (lane == 0) {
+                const uint32_t fb = bar(ms.q_full[qb]);
+                mbar_arrive_expect_tx(fb, (uint32_t)(nb * NCH * a.box_q) * 128u);
+                const int row0 = (int)(((long long)s.b * a.Hkv + s.kvh) * a.R + (long long)s.rb * T::RB);
+                for (int k = 0; k < nb; ++k)
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(sQ + qb * T::Q_BYTES + k * T::Q_BLOCK + c * T::Q_CHUNK, &a.tm_q, fb, c * 64,
+                                    row0 + 128 * k, 0);
+            }
+            __syncwarp();
+            ++q_sent;
+        };
+        for (; ok && walk.next(a, &s); ++seg) {
+            const int ib = seg & 1;
+            const bool first = QBUF == 2 || seg == 0;
+            if (first) put_queries();
+            if (ok && seg >= 2)
+                ok = mbar_wait_warp(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+            if (!ok) break;
+            if (lane < kNodeWords) ms.special[ib][lane] = 0;
+            bool bad = false;
+            if (a.parents) {
+                const int *parents = a.parents + (size_t)s.b * a.Nt;
+                int p[kNodeWords];
+#pragma unroll
+                for (int k = 0; k < kNodeWords; ++k) {
+                    const int j = 32 * k + lane;
+                    p[k] = j < a.Nt ? parents[j] : -2;
+                    if (p[k] >= j || (p[k] >= 0 && parents[p[k]] < -1)) {
+                        bad = true;
+                        p[k] = -1;
+                    }
+                }
+                bad = __any_sync(kFull, bad);
+                // node by node in order: what the parent sees, and itself; lane w has word w
+#pragma unroll
+                for (int k = 0; k < kNodeWords; ++k) {
+                    const int n = min(32, a.Nt - 32 * k);
+                    for (int i = 0; i < n; ++i) {
+                        const int up = __shfl_sync(kFull, p[k], i);
+                        if (lane < kNodeWords) {
+                            uint32_t w = up >= 0 ? ms.sees[ib][up][lane] : 0u;
+                            if (lane == k && up >= -1) w |= 1u << i;
+                            ms.sees[ib][32 * k + i][lane] = w;
+                        }
+                    }
+                }
+            }
+            if (lane == 0) {
+                ms.bad_tree[ib] = bad;
+                ms.special_any[ib] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ms.info_full[ib]));
+            if (!first) put_queries();
+        }
+        if (*g.abort) {
+            volatile int never = 0;
+            const Guard g2{a.status, &never, kWaitLimitNs};
+            for (uint32_t i = q_sent > (uint32_t)QBUF ? q_sent - QBUF : 0; i < q_sent; ++i)
+                mbar_wait_warp(bar(ms.q_full[i % QBUF]), (i / QBUF) & 1, g2, SITE_DEC_DRAIN);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax, results
+        // Every warp runs every step even after a wait has given up (waits then return soon).
+        const int wg = warp >> 2, w4 = warp & 3;
+        const int kk = threadIdx.x & 127;  // row of the block; lane of S and O; key of a tile's V
+        const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+        const uint32_t t_o = tmem + lane_base + T::TM_O + wg * T::DP;
+        const float c_s = a.scale_log2;
+        uint32_t seg = 0, m = 0, tiles = 0, units = 0;  // this block's units; the CTA's tiles and units
+        while (walk.next(a, &s)) {
+            const int ib = seg & 1, len = a.seq_lens[s.b], nb = blocks_of(s);
+            const int r0 = s.rb * T::RB + wg * 128, rows = min(128, a.R - r0);  // may be none
+            const bool mine = w4 * 32 < rows;                                   // this warp has rows
+            const int node = a.Nt - a.Nq + (r0 + kk) % a.Nq;                    // this thread's row
+            const int full_tiles = len >> (D == 256 ? 6 : 7);
+            bool informed = false;
+            auto inform = [&]() {
+                if (!informed) mbar_wait_warp(bar(ms.info_full[ib]), (seg >> 1) & 1, g, SITE_DEC_MMA);
+                informed = true;
+            };
+            // word k of the bits of nodes that node j sees; the cached keys stand before them
+            auto sees = [&](int j, int k) -> uint32_t {
+                if (k < 0) return 0xffffffffu;
+                if (k >= kNodeWords) return 0u;
+                if (a.parents) return ms.sees[ib][j][k];
+                const int n = j + 1 - 32 * k;
+                return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+            };
+            auto is_node = [&](int j) { return j < a.Nt && (!a.parents || (ms.sees[ib][j][j >> 5] >> (j & 31) & 1u)); };
+            float m_ref = kUnseen, l = 0.f;
+            if (rows > 0) {
+#pragma unroll 1
+                for (int t = s.t0; t < s.t1; ++t, ++m) {
+                    const bool partly = t >= full_tiles;
+                    if (partly) inform();
+                    mbar_wait_warp(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+                    tc_fence_after();
+                    if (mine) {
+                        const uint32_t unit = units + (uint32_t)((t - s.t0) * nb + wg);
+                        const uint32_t t_s = tmem + lane_base + (unit & 1) * BK;
+                        uint32_t sr[BK / 32][32];
+#pragma unroll
+                        for (int c = 0; c < BK / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
+#pragma unroll
+                        for (int c = 0; c < BK / 32; ++c) tmem_wait_ld(sr[c]);
+                        float x[BK];
+#pragma unroll
+                        for (int c = 0; c < BK / 32; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(sr[c][e]);
+                        if (partly) {
+                            const int n0 = t * BK - len;  // node of the tile's first key, or below 0
+#pragma unroll
+                            for (int c = 0; c < BK / 32; ++c) {
+                                const int at = (n0 + 32 * c) >> 5, sh = (n0 + 32 * c) & 31;
+                                const uint32_t w = __funnelshift_r(sees(node, at), sees(node, at + 1), sh);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(w >> e & 1u)) x[c * 32 + e] = -INFINITY;
+                            }
+                        }
+                        float mp0 = -INFINITY, mp1 = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < BK; c += 4) {
+                            mp0 = fmax3(mp0, x[c], x[c + 1]);
+                            mp1 = fmax3(mp1, x[c + 2], x[c + 3]);
+                        }
+                        const float top = fmaxf(mp0, mp1) * c_s;
+                        float alpha = 1.f;
+                        const bool move = top > m_ref + kMoveLog2;
+                        if (move) {
+                            alpha = ex2(m_ref - top);
+                            m_ref = top;
+                        }
+                        float sp0 = 0.f, sp1 = 0.f;
+                        const uint64_t c2 = f32x2_splat(c_s), nm2 = f32x2_splat(-m_ref);
+#pragma unroll
+                        for (int c = 0; c < BK; c += 2) {
+                            fma_f32x2(x[c], x[c + 1], c2, nm2);
+                            x[c] = ex2(x[c]);
+                            x[c + 1] = ex2(x[c + 1]);
+                            add_f32x2(sp0, sp1, x[c], x[c + 1]);
+                        }
+                        l = l * alpha + (sp0 + sp1);
+#pragma unroll
+                        for (int c = 0; c < BK / 64; ++c) {  // P as bf16 pairs over the slot's first half
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]);
+                            tmem_st32(t_s + c * 32, pk);
+                        }
+                        if (t > s.t0 && __any_sync(kFull, move)) {
+                            // O <- alpha O once the product before is complete
+                            mbar_wait_warp(bar(ms.pv_done[wg]), (m - 1) & 1, g, SITE_DEC_MMA);
+                            tc_fence_after();
+                            const uint64_t a2 = f32x2_splat(alpha);
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(t_o + c * 32, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    float x0 = __uint_as_float(o[e]), x1 = __uint_as_float(o[e + 1]);
+                                    mul_f32x2(x0, x1, a2);
+                                    o[e] = __float_as_uint(x0);
+                                    o[e + 1] = __float_as_uint(x1);
+                                }
+                                tmem_st32(t_o + c * 32, o);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    if (wg == 0 && partly && kk < BK) {
+                        // P is 0 where a row does not see the key, but 0 times an infinity or NaN of
+                        // V would not be: rows of V that hold no token, whatever lies there, become 0;
+                        // so do such values of nodes, which their rows get back at the end
+                        const uint32_t i = 2 * (tiles + (uint32_t)(t - s.t0)) + 1;
+                        const int slot = (int)(i % ST), key = t * BK + kk;
+                        mbar_wait(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                        uint8_t *v0 = gbase + slot * T::SLOT + kk * 128;
+                        if (key >= len) {
+                            const bool keep = is_node(key - len);
+                            bool found = false;
+#pragma unroll 1
+                            for (int e = 0; e < NCH * 8; ++e) {
+                                uint4 *p = reinterpret_cast<uint4 *>(v0 + (e >> 3) * T::CHUNK + (e & 7) * 16);
+                                uint4 w = keep ? *p : make_uint4(0u, 0u, 0u, 0u);
+                                const uint4 f = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z),
+                                                           not_finite(w.w));
+                                const bool here = (f.x | f.y | f.z | f.w) != 0u;
+                                found |= here;
+                                if (here || !keep) *p = make_uint4(w.x & ~f.x, w.y & ~f.y, w.z & ~f.z, w.w & ~f.w);
+                            }
+                            if (found) {
+                                atomicOr(&ms.special[ib][(key - len) >> 5], 1u << ((key - len) & 31));
+                                ms.special_any[ib] = 1;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(bar(ms.p_full[wg][m & 1]));
+                }
+            }
+            // ---- the segment's rows
+            inform();
+            if (rows > 0) mbar_wait_warp(bar(ms.pv_done[wg]), (m - 1) & 1, g, SITE_DEC_MMA);
+            tc_fence_after();
+            const bool bad_page = *(volatile int *)&ms.bad_page[ib] != 0;
+            const bool bad_tree = *(volatile int *)&ms.bad_tree[ib] != 0, bad = bad_page || bad_tree;
+            if (bad && threadIdx.x == 0) {
+                atomicCAS(a.status + 1, 0, bad_page ? SITE_TREE_BAD_PAGE : SITE_TREE_BAD_PARENT);
+                atomicExch(a.status, FA_ERR_BAD_INDEX);
+            }
+            if (mine && *g.abort == 0) {
+                const bool whole = s.t0 == 0 && s.t1 == s.nt;
+                if (!bad && !is_node(node)) l = 0.f;  // a place without a node
+                const bool none = l == 0.f;
+                const float inv = none ? 0.f : 1.f / l;
+                const float l2 = none ? -INFINITY : m_ref + lg2(l);  // base 2
+                const long long row = ((long long)s.b * a.Hkv + s.kvh) * a.R + r0 + kk;
+                const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * T::RB + wg * 128 + kk;
+                const bool put = kk < rows && !bad;
+                const bool special = *(volatile int *)&ms.special_any[ib] != 0 && !none && !bad;
+                const int *bt = a.block_table + (size_t)s.b * a.max_pages;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    float y[32];
+                    __syncwarp();
+                    tmem_ld32(t_o + c * 32, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : __uint_as_float(o[e]) * inv;
+                    if (special && put) {
+#pragma unroll 1
+                        for (int j = 0; j < a.Nt; ++j) {
+                            if (!(ms.special[ib][j >> 5] & sees(node, j >> 5) & 1u << (j & 31))) continue;
+                            const uint32_t key = (uint32_t)(len + j), i = a.by_page.div(key);
+                            const __nv_bfloat16 *v =
+                                a.v_cache + (((size_t)bt[i] * a.Hkv + s.kvh) * a.page_size + (key - i * a.page_size)) * D +
+                                c * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float f = __bfloat162float(v[e]);
+                                if (!(fabsf(f) < INFINITY)) y[e] += f;
+                            }
+                        }
+                    }
+                    if (!put) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)row * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
+                                                pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    }
+                }
+                if (kk < rows) {
+                    if (!whole) a.part_l[prow] = bad ? __uint_as_float(kBadPartial) : l2;
+                    else if (!bad) a.lse[row] = l2 * kLn2;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ms.info_empty[ib]));
+            tiles += (uint32_t)(s.t1 - s.t0);
+            units += (uint32_t)((s.t1 - s.t0) * nb);
+            ++seg;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, T::TM_COLS);
+    }
+}
+
+// Tiles of all items at the longest possible lengths.
+template <int D, int NB>
+long long tree_tiles(const TreeParams &p) {
+    using T = TreeTile<D, NB>;
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    const long long nt = ((long long)p.page_size * p.max_pages + p.Nt + T::BK - 1) / T::BK;
+    const long long items = (long long)p.B * p.Hkv * ((R + T::RB - 1) / T::RB);
+    return items >= (1LL << 31) ? items : items * nt;
+}
+
+// CTAs of a launch: one per SM, or the largest number of tiles there can be.
+template <int D, int NB>
+int tree_ctas(const TreeParams &p) {
+    const long long n = tree_tiles<D, NB>(p);
+    return n < p.num_sms ? (int)n : p.num_sms;
+}
+
+template <int D, int NB>
+size_t tree_bytes(const TreeParams &p, size_t *l_offset) {
+    const size_t rows = (size_t)tree_ctas<D, NB>(p) * 2 * TreeTile<D, NB>::RB;
+    *l_offset = rows * D * sizeof(float);
+    return *l_offset + rows * sizeof(float);
+}
+
+template <int D, int NB>
+int launch_t(const TreeParams &p, cudaStream_t stream) {
+    using T = TreeTile<D, NB>;
+    TreeArgs a{};
+    a.tm_q = p.tm_q;
+    a.tm_k = p.tm_k;
+    a.tm_v = p.tm_v;
+    a.v_cache = static_cast<const __nv_bfloat16 *>(p.v_cache);
+    a.block_table = p.block_table;
+    a.seq_lens = p.seq_lens;
+    a.parents = p.parents;
+    a.o = static_cast<__nv_bfloat16 *>(p.o);
+    a.lse = p.lse;
+    size_t l_offset;
+    tree_bytes<D, NB>(p, &l_offset);
+    a.part_o = static_cast<float *>(p.workspace);
+    a.part_l = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + l_offset);
+    a.by_page = fast_div((uint32_t)p.page_size);
+    a.B = p.B;
+    a.H = p.H;
+    a.Hkv = p.Hkv;
+    a.Nq = p.Nq;
+    a.Nt = p.Nt;
+    a.d = p.d;
+    a.page_size = p.page_size;
+    a.max_pages = p.max_pages;
+    a.num_pages = p.num_pages;
+    a.R = p.H / p.Hkv * p.Nq;
+    a.row_blocks = (a.R + T::RB - 1) / T::RB;
+    a.box = tree_box_rows(p);
+    a.box_q = tree_query_box(p);
+    a.tile_log2 = T::BK == 64 ? 6 : 7;
+    a.start = 1;
+    a.scale_log2 = p.scale_log2;
+    a.status = p.status;
+    a.limit_ns = kWaitLimitNs;
+    auto kern = fa_tree_kernel<D, NB>;
+    constexpr int kSmem = (int)T::SMEM, kCols = (D + 31) / 32;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
+    const int n_cta = tree_ctas<D, NB>(p);
+    if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
+    // the merge that has fewer CTAs
+    const long long rows = (long long)p.B * p.H * p.Nq;
+    const int blocks = ((a.R < T::RB ? a.R : T::RB) + kCutRows - 1) / kCutRows;
+    if (rows <= (long long)n_cta * blocks)
+        return launch_dependent(fa_merge_row_kernel<kCols, T::RB, TreeArgs>, dim3((unsigned)rows), 32 * kRowWarps, 0,
+                                stream, 1, a, n_cta);
+    return launch_dependent(fa_merge_cut_kernel<kCols, T::RB, TreeArgs>, dim3((unsigned)n_cta, (unsigned)blocks),
+                            32 * kCutRows, 0, stream, 1, a, n_cta);
+}
+
+// Calls f with the tile that serves the call: head dimension and blocks of 128 query rows.
+template <typename F>
+auto with_tile(const TreeParams &p, F f) {
+    using std::integral_constant;
+    const bool two = (long long)(p.H / p.Hkv) * p.Nq > 128;
+    using One = integral_constant<int, 1>;
+    using Two = integral_constant<int, 2>;
+    switch (p.d) {
+        case 64: return two ? f(integral_constant<int, 64>(), Two()) : f(integral_constant<int, 64>(), One());
+        case 96: return two ? f(integral_constant<int, 96>(), Two()) : f(integral_constant<int, 96>(), One());
+        case 128: return two ? f(integral_constant<int, 128>(), Two()) : f(integral_constant<int, 128>(), One());
+        default: return f(integral_constant<int, 256>(), One());  // O of a second block has no room
+    }
+}
+
+}  // namespace
+
+int tree_box_rows(const TreeParams &p) {
+    const int most = p.d == 256 ? 64 : 128;
+    int box = 1;
+    while (box < most && p.page_size % (2 * box) == 0) box *= 2;
+    return box;
+}
+
+int tree_query_box(const TreeParams &p) {
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    return R >= 128 ? 128 : (int)(R + 7) / 8 * 8;
+}
+
+long long tree_max_tiles(const TreeParams &p) {
+    return with_tile(p, [&](auto d, auto nb) { return tree_tiles<decltype(d)::value, decltype(nb)::value>(p); });
+}
+
+size_t tree_workspace_bytes(const TreeParams &p) {
+    return with_tile(p, [&](auto d, auto nb) {
+        size_t l_offset;
+        return tree_bytes<decltype(d)::value, decltype(nb)::value>(p, &l_offset);
+    });
+}
+
+int launch_tree(const TreeParams &p, cudaStream_t stream) {
+    return with_tile(p, [&](auto d, auto nb) {
+        return launch_t<decltype(d)::value, decltype(nb)::value>(p, stream);
+    });
+}
+
+}  // namespace fa

@@ -35,7 +35,8 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_status_string", "f
             "fa_probe_unit_rates", "fa_probe_read_bandwidth", "fa_fwd_ws", "fa_fwd_workspace_bytes",
             "fa_fwd_split_segments", "fa_append_paged_fp8", "fa_decode_paged_fp8",
             "fa_decode_paged_fp8_workspace_bytes", "fa_free_pages", "fa_fork_pages",
-            "fa_compact_pages", "fa_copy_pages")
+            "fa_compact_pages", "fa_copy_pages", "fa_decode_paged_tree",
+            "fa_decode_paged_tree_workspace_bytes")
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -119,6 +120,11 @@ def load() -> ctypes.CDLL:
         lib.fa_compact_pages.restype = _int
         lib.fa_copy_pages.argtypes = [_vp, _vp, _int, _int, _vp, _vp, _int, _vp, _vp]
         lib.fa_copy_pages.restype = _int
+        lib.fa_decode_paged_tree_workspace_bytes.argtypes = [_int] * 8
+        lib.fa_decode_paged_tree_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_decode_paged_tree.argtypes = [_vp] * 8 + [_int] * 9 + [ctypes.c_float, _vp,
+                                                                     ctypes.c_size_t, _vp]
+        lib.fa_decode_paged_tree.restype = _int
         _LIB = lib
     return _LIB
 
@@ -377,6 +383,18 @@ def fa_copy_pages(caches, page_bytes, n_caches, num_pages, src, dst, n_pairs, co
     """Raw call; `caches` and `page_bytes` are ctypes arrays of void* and size_t (host)."""
     return load().fa_copy_pages(caches, page_bytes, n_caches, num_pages, src, dst, n_pairs, count,
                                 stream)
+
+
+def fa_decode_paged_tree_workspace_bytes(B, H, Hkv, Nq, Nt, d, page_size, max_pages) -> int:
+    return load().fa_decode_paged_tree_workspace_bytes(B, H, Hkv, Nq, Nt, d, page_size, max_pages)
+
+
+def fa_decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, o, lse, B, H, Hkv, Nq, Nt,
+                         d, page_size, max_pages, num_pages, scale, workspace, workspace_bytes,
+                         stream) -> int:
+    return load().fa_decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, o, lse, B, H,
+                                       Hkv, Nq, Nt, d, page_size, max_pages, num_pages, scale, workspace,
+                                       workspace_bytes, stream)
 
 
 def fa_status_string(status: int) -> str:
@@ -791,7 +809,7 @@ def forward_fp8(q8, k8, vt8, q_descale, k_descale, v_descale, causal=False, scal
     return out, lse
 
 
-# The calls on a paged e4m3 cache are made many times per decode step on kernels of a few
+# The calls on a paged cache are made many times per decode step on kernels of a few
 # microseconds, so the extension makes them: it answers with the outputs, with a status, or
 # with None when an argument is not as expected.  What follows it here names the argument
 # that is wrong (and serves the calls the extension leaves alone, tensor subclasses).  The int32
@@ -1048,3 +1066,80 @@ def copy_pages(caches, src, dst, count=None, stream=None):
                            src.shape[0], None if count is None else count.data_ptr(),
                            _stream(src, stream))
     _ok(rc, "fa_copy_pages")
+
+
+def _cache16(k_cache, v_cache, block_table, seq_lens, di):
+    """Checks of a paged bf16 cache and its table on device `di`; returns (B, num_pages, Hkv,
+    page_size, d, max_pages)."""
+    _check("k_cache", k_cache, torch.bfloat16, dev=di)
+    if k_cache.dim() != 4 or 0 in k_cache.shape:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page_size, d = k_cache.shape
+    _check("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev=di)
+    _check("block_table", block_table, torch.int32, dev=di)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _check("seq_lens", seq_lens, torch.int32, (B,), dev=di)
+    return B, num_pages, Hkv, page_size, d, max_pages
+
+
+FA_MAX_TREE_NODES = 256
+
+
+def decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents=None, scale=None, out=None,
+                      lse=None, workspace=None, stream=None):
+    """Attention of drafted tokens against a paged bf16 cache: q bf16 CUDA [B,H,Nq,d], the queries
+    of the last Nq of each sequence's Nt drafted tokens, whose keys and values lie in k_cache,
+    v_cache bf16 [num_pages, Hkv, page_size, d] (Hkv divides H) behind the sequence's seq_lens[b]
+    tokens (int32 [B], 0 allowed), through block_table int32 [B, max_pages].  parents int32 [B, Nt]:
+    the number of an earlier drafted token, -1 for one without a parent among them, below -1 where
+    there is none; None: Nt = Nq tokens drafted in a row.  A query sees the seq_lens[b] tokens,
+    itself and its ancestors; where there is no token o = 0 and lse = -inf.  Returns (o, lse)."""
+    r = native().decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, scale, out, lse,
+                                   workspace, _raw(stream, q))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_decode_paged_tree")
+    if stream is not None:
+        return _under(stream, q, decode_paged_tree, q, k_cache, v_cache, block_table, seq_lens, parents,
+                      scale, out, lse, workspace)
+    _check("q", q, torch.bfloat16)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, Nq, d]")
+    B, H, Nq, d = q.shape
+    di = q.get_device()
+    B2, num_pages, Hkv, page_size, d2, max_pages = _cache16(k_cache, v_cache, block_table, seq_lens, di)
+    if B2 != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    if d2 != d or H % Hkv:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d], Hkv dividing H")
+    Nt = Nq
+    if parents is not None:
+        _check("parents", parents, torch.int32, dev=di)
+        if parents.dim() != 2 or parents.shape[0] != B or parents.shape[1] < Nq:
+            raise ValueError("parents must be [B, Nt] with Nt >= Nq")
+        Nt = parents.shape[1]
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check("out", out, torch.bfloat16, q.shape, dev=di)
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    else:
+        _check("lse", lse, torch.float32, (B, H, Nq), dev=di)
+    with _device(di):
+        need = _memo(fa_decode_paged_tree_workspace_bytes, B, H, Hkv, Nq, Nt, d, page_size, max_pages)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            _check("workspace", workspace, torch.uint8, dev=di)
+        rc = fa_decode_paged_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                  block_table.data_ptr(), seq_lens.data_ptr(),
+                                  None if parents is None else parents.data_ptr(), out.data_ptr(),
+                                  lse.data_ptr(), B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages,
+                                  scale, workspace.data_ptr(), workspace.numel(), _stream(q, None))
+    _ok(rc, "fa_decode_paged_tree")
+    return out, lse

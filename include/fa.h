@@ -514,6 +514,46 @@ int fa_copy_pages(void *const *caches, const size_t *page_bytes, int n_caches, i
                   const int *src, const int *dst, int n_pairs, const int *count, void *stream);
 
 /*
+ * Attention of drafted tokens (speculative decoding): each sequence has a tree of Nt nodes, whose
+ * keys and values lie in the paged bf16 cache of fa_decode_paged behind the sequence's seq_lens[b]
+ * tokens, node j at token seq_lens[b] + j.  The queries are those of the tree's last Nq nodes
+ * (all of them, or a newest level while the tree is being drafted):
+ *     O[i] = softmax(q_i K^T * scale) V,   L[i] = m_i + ln(l_i)   (natural log),
+ * over the sequence's seq_lens[b] tokens, node Nt - Nq + i itself and the node's ancestors.
+ *   q        : bf16 [B][H][Nq][d];  o : bf16 [B][H][Nq][d];  lse : fp32 [B][H][Nq].
+ *   k_cache, v_cache : bf16 [num_pages][Hkv][page_size][d];  block_table : int32
+ *              [B][max_pages_per_seq];  seq_lens : int32 [B], 0 or more (device memory).  Pages are
+ *              needed for the tokens and for every node that there is.
+ *   parents  : int32 [B][Nt], device memory: an earlier node's number, -1 for a node without a
+ *              parent in the tree, below -1 where there is no node (sequences with fewer of them);
+ *              NULL: each node's parent is the one before it.
+ * A row without a node gets O = 0 and L = -infinity.  Keys that a row does not see, and what
+ * lies in the cache in places without a token or node, have no influence on it, whatever their
+ * values are.  A NaN in a key or query that a row sees makes the row NaN; a NaN or infinity in
+ * the values of a node that it sees makes that column of the row the same (infinities of both
+ * signs: NaN).
+ * Rounding: probabilities enter the product with V in bf16 (2^-8 relative), sums are fp32.
+ *   B, H, Nq >= 1; Hkv divides H; Nq <= Nt <= FA_MAX_TREE_NODES; d: 64, 96, 128 or 256;
+ *   (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, page_size * max_pages_per_seq < 2^31 - 1024, B *
+ *   max_pages_per_seq and num_pages * Hkv < 2^31, and the tiles of 128 keys (64 where d = 256) of
+ *   all sequences, heads and blocks of 256 query rows (128) at the longest lengths < 2^31.
+ *   scale    : finite and > 0.  o and lse overlap none of the inputs.
+ *   workspace : device buffer of fa_decode_paged_tree_workspace_bytes(...) bytes, 16-byte aligned,
+ *              contents on entry irrelevant; calls that share one must not overlap.
+ * The work is cut evenly over the SMs on the device, from seq_lens: a captured call replays with
+ * other lengths and trees.  A sequence with a bad length (below 0, or above page_size *
+ * max_pages_per_seq), page or parent writes nothing and is recorded as FA_ERR_BAD_INDEX.
+ */
+#define FA_MAX_TREE_NODES 256
+size_t fa_decode_paged_tree_workspace_bytes(int B, int H, int Hkv, int Nq, int Nt, int d,
+                                            int page_size, int max_pages_per_seq);
+int fa_decode_paged_tree(const void *q, const void *k_cache, const void *v_cache,
+                         const int *block_table, const int *seq_lens, const int *parents, void *o,
+                         float *lse, int B, int H, int Hkv, int Nq, int Nt, int d, int page_size,
+                         int max_pages_per_seq, int num_pages, float scale, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
  * Diagnostic: launches one warp that waits, through the same bounded wait the
  * attention kernels use, on a barrier that nothing ever arrives on.  The wait
  * gives up after `limit_ns` nanoseconds (1e3 <= limit_ns <= 5e9, else
