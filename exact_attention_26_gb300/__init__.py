@@ -8,6 +8,7 @@ from .fa import (FaError, append_paged_fp8, backward, backward_varlen, compact_p
                  fa_append_paged_fp8, fa_bwd,
                  fa_compact_pages, fa_copy_pages, fa_decode_paged_fp8,
                  fa_decode_paged_fp8_workspace_bytes, fa_decode_paged_tree,
+                 fa_keep_path, fa_verify_tree, keep_path, verify_tree,
                  fa_decode_paged_tree_workspace_bytes, fa_fork_pages, fa_free_pages, fork_pages,
                  free_pages,
                  fa_bwd_workspace_bytes, fa_decode, fa_decode_num_splits, fa_decode_paged,

@@ -21,7 +21,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfa.so")
 EXT = os.path.join(OUT_DIR, "_fa_torch.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_noalloc.cu", "fa_quant.cu",
-           "fa_probe.cu", "fa_cache.cu", "fa_decode_fp8.cu", "fa_tree.cu"]
+           "fa_probe.cu", "fa_cache.cu", "fa_decode_fp8.cu", "fa_tree.cu",
+           "fa_spec.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

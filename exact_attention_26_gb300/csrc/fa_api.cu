@@ -1273,6 +1273,78 @@ extern "C" int fa_copy_pages(void *const *caches, const size_t *page_bytes, int 
     return launch_copy(p, static_cast<cudaStream_t>(stream));
 }
 
+extern "C" int fa_verify_tree(const int *tokens, const int *parents, const void *target_probs,
+                              const void *draft_probs, const float *uniform, int *path, int *new_tokens,
+                              int *count, int B, int Nt, int V, int bf16, int replacement, void *stream) {
+    if (!tokens || !target_probs || !uniform || !path || !new_tokens || !count) return FA_ERR_INVALID_ARG;
+    if (B < 1 || Nt < 1 || V < 1 || V > (1 << 30) || (long long)B * Nt >= (1LL << 28)) return FA_ERR_INVALID_ARG;
+    if (Nt > FA_MAX_TREE_NODES) return FA_ERR_UNSUPPORTED;
+    if (!aligned16(target_probs) || !aligned16(draft_probs) || !aligned4(tokens) || !aligned4(parents) ||
+        !aligned4(uniform) || !aligned4(path) || !aligned4(new_tokens) || !aligned4(count))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    const int rc = current_device(&dc);
+    if (rc != FA_OK) return rc;
+    VerifyParams v{};
+    v.tokens = tokens;
+    v.parents = parents;
+    v.target = target_probs;
+    v.draft = draft_probs;
+    v.uniform = uniform;
+    v.path = path;
+    v.fresh = new_tokens;
+    v.count = count;
+    v.B = B;
+    v.Nt = Nt;
+    v.V = V;
+    v.bf16 = bf16 ? 1 : 0;
+    v.replacement = replacement ? 1 : 0;
+    v.status = dc->status;
+    v.num_sms = dc->num_sms;
+    return launch_verify(v, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa_keep_path(void *const *caches, int n_caches, const int *block_table, const int *seq_lens,
+                            const int *path, const int *count, int *lens, int B, int Nt, int Hkv, int d,
+                            int page_size, int max_pages_per_seq, int num_pages, void *stream) {
+    if (!caches || !block_table || !seq_lens || !path || !count || !lens) return FA_ERR_INVALID_ARG;
+    if (n_caches < 1 || n_caches > FA_MAX_COPY_CACHES || B < 1 || B > 65535 || Nt < 1 || Hkv < 1 ||
+        page_size < 1 || max_pages_per_seq < 1 || num_pages < 1)
+        return FA_ERR_INVALID_ARG;
+    if ((long long)page_size * max_pages_per_seq >= (1LL << 31) - 1024 ||
+        (long long)B * max_pages_per_seq >= (1LL << 31) || (long long)num_pages * Hkv >= (1LL << 31) ||
+        (long long)n_caches * Hkv >= (1LL << 24))
+        return FA_ERR_INVALID_ARG;
+    if (Nt > FA_MAX_TREE_NODES || (d != 64 && d != 96 && d != 128 && d != 256)) return FA_ERR_UNSUPPORTED;
+    KeepParams k{};
+    for (int c = 0; c < n_caches; ++c) {
+        if (!caches[c]) return FA_ERR_INVALID_ARG;
+        if (!aligned16(caches[c])) return FA_ERR_MISALIGNED;
+        k.cache[c] = caches[c];
+    }
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(path) || !aligned4(count) || !aligned4(lens))
+        return FA_ERR_MISALIGNED;
+    DeviceCache *dc = nullptr;
+    const int rc = current_device(&dc);
+    if (rc != FA_OK) return rc;
+    k.block_table = block_table;
+    k.seq_lens = seq_lens;
+    k.path = path;
+    k.count = count;
+    k.lens = lens;
+    k.n_caches = n_caches;
+    k.B = B;
+    k.Nt = Nt;
+    k.Hkv = Hkv;
+    k.d = d;
+    k.page_size = page_size;
+    k.max_pages = max_pages_per_seq;
+    k.num_pages = num_pages;
+    k.status = dc->status;
+    k.num_sms = dc->num_sms;
+    return launch_keep(k, static_cast<cudaStream_t>(stream));
+}
+
 extern "C" const char *fa_status_string(int status) {
     switch (status) {
         case FA_OK: return "FA_OK";

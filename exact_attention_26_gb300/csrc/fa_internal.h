@@ -51,6 +51,8 @@ enum WaitSite : int {
     SITE_TREE_BAD_LEN = 38,
     SITE_TREE_BAD_PAGE = 39,
     SITE_TREE_BAD_PARENT = 40,
+    SITE_VERIFY_BAD_TREE = 41,
+    SITE_KEEP_BAD_PATH = 42,
 };
 
 // Default limit of one in-kernel wait.
@@ -259,6 +261,29 @@ int tree_query_box(const TreeParams &p);
 long long tree_max_tiles(const TreeParams &p);
 size_t tree_workspace_bytes(const TreeParams &p);  // of its sizes and num_sms
 int launch_tree(const TreeParams &p, cudaStream_t stream);
+
+// Verification of drafted tokens.
+struct VerifyParams {
+    const int *tokens, *parents;         // [B][Nt]; parents null: a chain
+    const void *target, *draft;          // [B][Nt][V] fp32 or bf16; draft null: drafts are certain
+    const float *uniform;                // [B][Nt]
+    int *path, *fresh, *count;           // [B][Nt], [B][Nt], [B]
+    int B, Nt, V, bf16, replacement;
+    int *status;
+    int num_sms;
+};
+int launch_verify(const VerifyParams &v, cudaStream_t stream);
+
+// The accepted tokens' rows of a paged bf16 cache.
+struct KeepParams {
+    void *cache[FA_MAX_COPY_CACHES];     // bf16 [num_pages][Hkv][page_size][d]
+    const int *block_table, *seq_lens, *path, *count;
+    int *lens;                           // [B] out
+    int n_caches, B, Nt, Hkv, d, page_size, max_pages, num_pages;
+    int *status;
+    int num_sms;
+};
+int launch_keep(const KeepParams &k, cudaStream_t stream);
 
 // Devices the per-device caches of the host code cover (ordinals 0..63).
 constexpr int kMaxCachedDevices = 64;

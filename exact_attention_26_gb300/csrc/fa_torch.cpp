@@ -469,9 +469,88 @@ PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// tokens, parents, target_probs, draft_probs, uniform, replacement, stream
+PyObject *verify_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 7) return declined();
+    const Tensor *tokens = tensor(a[0], at::kInt, 2), *target = tensor(a[2], at::kFloat, 3);
+    if (!target) target = tensor(a[2], at::kBFloat16, 3);
+    if (!tokens || !target) return declined();
+    const int device = tokens->get_device();
+    const Tensor *uniform = tensor(a[4], at::kFloat, 2);
+    const int64_t B = tokens->size(0), Nt = tokens->size(1), V = target->size(2);
+    if (!on(target, device) || !on(uniform, device) || !uniform->sizes().equals(tokens->sizes()) ||
+        target->size(0) != B || target->size(1) != Nt || !is_int(B) || !is_int(Nt) || !is_int(V))
+        return declined();
+    const int *parents = nullptr;
+    if (a[1] != Py_None) {
+        const Tensor *t = tensor(a[1], at::kInt, 2);
+        if (!on(t, device) || !t->sizes().equals(tokens->sizes())) return declined();
+        parents = ptr<int>(*t);
+    }
+    const void *draft = nullptr;
+    if (a[3] != Py_None) {
+        const Tensor *t = tensor(a[3], target->scalar_type(), 3);
+        if (!on(t, device) || !t->sizes().equals(target->sizes())) return declined();
+        draft = t->data_ptr();
+    }
+    const int replacement = PyObject_IsTrue(a[5]);
+    if (replacement < 0) return nullptr;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[6], device)) return nullptr;
+    Parts parts(2 * B * Nt + B, device);
+    stream.hand_out(parts.buffer);
+    const Tensor path = parts.take({B, Nt}), fresh = parts.take({B, Nt}), count = parts.take({B});
+    const int rc = fa_verify_tree(ptr<int>(*tokens), parents, target->data_ptr(), draft, ptr<float>(*uniform),
+                                  ptr<int>(path), ptr<int>(fresh), ptr<int>(count), (int)B, (int)Nt, (int)V,
+                                  target->scalar_type() == at::kBFloat16, replacement, stream.raw);
+    return rc != FA_OK ? PyLong_FromLong(rc) : results({path, fresh, count});
+    END_HANDLE_TH_ERRORS
+}
+
+// caches (a list), block_table, seq_lens, path, count, stream
+PyObject *keep_path(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 6 || !PyList_Check(a[0])) return declined();
+    const Py_ssize_t m = PyList_GET_SIZE(a[0]);
+    const Tensor *bt = tensor(a[1], at::kInt, 2);
+    if (m < 1 || m > FA_MAX_COPY_CACHES || !bt) return declined();
+    const int device = bt->get_device();
+    const Tensor *lens = tensor(a[2], at::kInt, 1), *path = tensor(a[3], at::kInt, 2), *count = tensor(a[4], at::kInt, 1);
+    if (!on(lens, device) || !on(path, device) || !on(count, device)) return declined();
+    const int64_t B = bt->size(0);
+    if (lens->size(0) != B || path->size(0) != B || count->size(0) != B || !is_int(B) || !is_int(bt->size(1)) ||
+        !is_int(path->size(1)))
+        return declined();
+    void *caches[FA_MAX_COPY_CACHES];
+    const Tensor *first = nullptr;
+    for (Py_ssize_t i = 0; i < m; ++i) {
+        const Tensor *t = tensor(PyList_GET_ITEM(a[0], i), at::kBFloat16, 4);
+        if (!on(t, device)) return declined();
+        if (i == 0) {
+            first = t;
+            for (int64_t s : t->sizes())
+                if (s < 1 || !is_int(s)) return declined();
+        }
+        if (!t->sizes().equals(first->sizes())) return declined();
+        caches[i] = t->data_ptr();
+    }
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+    CallStream stream;
+    if (!stream.read(a[5], device)) return nullptr;
+    const Tensor out = make({B}, at::kInt, device);
+    stream.hand_out(out);
+    const int rc = fa_keep_path(caches, (int)m, ptr<int>(*bt), ptr<int>(*lens), ptr<int>(*path), ptr<int>(*count),
+                                ptr<int>(out), (int)B, (int)path->size(1), (int)first->size(1), (int)first->size(3),
+                                (int)first->size(2), (int)bt->size(1), (int)first->size(0), stream.raw);
+    return rc != FA_OK ? PyLong_FromLong(rc) : results({out});
+    END_HANDLE_TH_ERRORS
+}
+
 #define FN(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FN(decode_paged_fp8), FN(decode_paged_tree), FN(append_paged_fp8), FN(free_pages), FN(fork_pages),
-                          FN(compact_pages), FN(copy_pages), {nullptr, nullptr, 0, nullptr}};
+                          FN(compact_pages), FN(copy_pages), FN(verify_tree), FN(keep_path), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr,
                        nullptr};
 

@@ -36,7 +36,7 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_status_string", "f
             "fa_fwd_split_segments", "fa_append_paged_fp8", "fa_decode_paged_fp8",
             "fa_decode_paged_fp8_workspace_bytes", "fa_free_pages", "fa_fork_pages",
             "fa_compact_pages", "fa_copy_pages", "fa_decode_paged_tree",
-            "fa_decode_paged_tree_workspace_bytes")
+            "fa_decode_paged_tree_workspace_bytes", "fa_verify_tree", "fa_keep_path")
 
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
@@ -125,6 +125,10 @@ def load() -> ctypes.CDLL:
         lib.fa_decode_paged_tree.argtypes = [_vp] * 8 + [_int] * 9 + [ctypes.c_float, _vp,
                                                                      ctypes.c_size_t, _vp]
         lib.fa_decode_paged_tree.restype = _int
+        lib.fa_verify_tree.argtypes = [_vp] * 8 + [_int] * 5 + [_vp]
+        lib.fa_verify_tree.restype = _int
+        lib.fa_keep_path.argtypes = [_vp, _int] + [_vp] * 5 + [_int] * 7 + [_vp]
+        lib.fa_keep_path.restype = _int
         _LIB = lib
     return _LIB
 
@@ -395,6 +399,19 @@ def fa_decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, o,
     return load().fa_decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents, o, lse, B, H,
                                        Hkv, Nq, Nt, d, page_size, max_pages, num_pages, scale, workspace,
                                        workspace_bytes, stream)
+
+
+def fa_verify_tree(tokens, parents, target_probs, draft_probs, uniform, path, new_tokens, count, B, Nt, V,
+                   bf16, replacement, stream) -> int:
+    return load().fa_verify_tree(tokens, parents, target_probs, draft_probs, uniform, path, new_tokens,
+                                 count, B, Nt, V, int(bool(bf16)), int(bool(replacement)), stream)
+
+
+def fa_keep_path(caches, n_caches, block_table, seq_lens, path, count, lens, B, Nt, Hkv, d, page_size,
+                 max_pages, num_pages, stream) -> int:
+    """Raw call; `caches` is a ctypes array of void* (host)."""
+    return load().fa_keep_path(caches, n_caches, block_table, seq_lens, path, count, lens, B, Nt, Hkv, d,
+                               page_size, max_pages, num_pages, stream)
 
 
 def fa_status_string(status: int) -> str:
@@ -1143,3 +1160,88 @@ def decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents=None, 
                                   scale, workspace.data_ptr(), workspace.numel(), _stream(q, None))
     _ok(rc, "fa_decode_paged_tree")
     return out, lse
+
+
+def verify_tree(tokens, parents, target_probs, draft_probs, uniform, replacement=True, stream=None):
+    """Verification of drafted tokens: which of each sequence's tree are accepted, and one token more,
+    distributed as the target's own samples.  tokens int32 CUDA [B, Nt], node 0 standing for the
+    last certain token, the others drafted; parents int32 [B, Nt]: -1 for node 0, an earlier node's
+    number for the others, below -1 where there is no node (None: a chain); target_probs [B, Nt, V]
+    fp32 or bf16: the target's probabilities of the token after each node; draft_probs, alike: those
+    that each node's children were drawn from (independently, or with replacement=False one after
+    another without repetition), or None where drafts were not drawn; uniform fp32 [B, Nt] in [0, 1).
+    Returns int32 (path [B, Nt], new_tokens [B, Nt], count [B]): the accepted nodes from node 0 on,
+    the accepted tokens and the last one, each followed by -1, and how many there are of each."""
+    r = native().verify_tree(tokens, parents, target_probs, draft_probs, uniform, replacement,
+                             _raw(stream, tokens))
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise FaError(r, "fa_verify_tree")
+    if stream is not None:
+        return _under(stream, tokens, verify_tree, tokens, parents, target_probs, draft_probs, uniform,
+                      replacement)
+    _check("tokens", tokens, torch.int32)
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [B, Nt]")
+    B, Nt = tokens.shape
+    di = tokens.get_device()
+    if parents is not None:
+        _check("parents", parents, torch.int32, tokens.shape, dev=di)
+    dtype = target_probs.dtype if isinstance(target_probs, torch.Tensor) else None
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("target_probs must be a float32 or bfloat16 CUDA tensor")
+    _check("target_probs", target_probs, dtype, dev=di)
+    if target_probs.dim() != 3 or target_probs.shape[:2] != tokens.shape:
+        raise ValueError("target_probs must be [B, Nt, V]")
+    V = target_probs.shape[2]
+    if draft_probs is not None:
+        _check("draft_probs", draft_probs, dtype, target_probs.shape, dev=di)
+    _check("uniform", uniform, torch.float32, tokens.shape, dev=di)
+    path, new, count = (_int32(s, tokens) for s in ((B, Nt), (B, Nt), B))
+    with _device(di):
+        rc = fa_verify_tree(tokens.data_ptr(), None if parents is None else parents.data_ptr(),
+                            target_probs.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+                            uniform.data_ptr(), path.data_ptr(), new.data_ptr(), count.data_ptr(), B, Nt, V,
+                            dtype == torch.bfloat16, replacement, _stream(tokens, None))
+    _ok(rc, "fa_verify_tree")
+    return path, new, count
+
+
+def keep_path(caches, block_table, seq_lens, path, count, stream=None):
+    """Keep the accepted nodes of drafted trees in a paged bf16 cache: behind sequence b's
+    seq_lens[b] tokens (int32 CUDA [B]) the row of node path[b, i] (int32 [B, Nt], ascending) becomes
+    row i for i < count[b] (int32 [B]), in every tensor of `caches` (bf16 [num_pages, Hkv, page_size,
+    d], all of one shape: keys and values of any number of layers, up to 128 tensors), through
+    block_table int32 [B, max_pages].  Returns seq_lens + count, int32 [B]."""
+    caches = caches if isinstance(caches, list) else list(caches)
+    r = native().keep_path(caches, block_table, seq_lens, path, count, _raw(stream, block_table))
+    if r.__class__ is tuple:
+        return r[0]
+    if r is not None:
+        raise FaError(r, "fa_keep_path")
+    if stream is not None:
+        return _under(stream, block_table, lambda *a: (keep_path(*a),), caches, block_table, seq_lens, path,
+                      count)[0]
+    if not 1 <= len(caches) <= FA_MAX_COPY_CACHES:
+        raise ValueError(f"caches must be 1 to {FA_MAX_COPY_CACHES} tensors")
+    di, B, max_pages = _table(block_table, seq_lens)
+    _check("caches[0]", caches[0], torch.bfloat16, dev=di)
+    if caches[0].dim() != 4 or 0 in caches[0].shape:
+        raise ValueError("caches[0] must be [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page_size, d = caches[0].shape
+    ptrs = (_vp * len(caches))()
+    for i, t in enumerate(caches):
+        _check(f"caches[{i}]", t, torch.bfloat16, caches[0].shape, dev=di)
+        ptrs[i] = t.data_ptr()
+    _check("path", path, torch.int32, dev=di)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be [B, Nt]")
+    _check("count", count, torch.int32, (B,), dev=di)
+    lens = _int32(B, block_table)
+    with _device(di):
+        rc = fa_keep_path(ptrs, len(caches), block_table.data_ptr(), seq_lens.data_ptr(), path.data_ptr(),
+                          count.data_ptr(), lens.data_ptr(), B, path.shape[1], Hkv, d, page_size, max_pages,
+                          num_pages, _stream(block_table, None))
+    _ok(rc, "fa_keep_path")
+    return lens

@@ -554,6 +554,67 @@ int fa_decode_paged_tree(const void *q, const void *k_cache, const void *v_cache
                          size_t workspace_bytes, void *stream);
 
 /*
+ * Verification of drafted tokens, so that what is accepted is distributed as the target's own
+ * samples.  Sequence b drafted a tree of nodes: node 0 stands for the last token that is certain,
+ * the others for drafted tokens, children of a node in the order in which they are tried.  From
+ * node 0 the walk goes to the first child that is accepted, from there on in the same way, and
+ * ends where no child is: there a last token is drawn from what is left of the target.
+ *   tokens   : int32 [B][Nt], 0 .. V-1 (node 0's is not looked at).
+ *   parents  : int32 [B][Nt]: -1 for node 0, an earlier node's number for the others, below -1
+ *              where there is no node (in node 0's place: the sequence has none at all); NULL: a
+ *              chain.
+ *   target_probs, draft_probs : [B][Nt][V], fp32 or (bf16 != 0) bf16: row j holds the target's
+ *              probabilities of the token after node j, and those that node j's children were
+ *              drawn from.  Rows of nodes where the walk does not come are not read, except at their
+ *              children's tokens.  Values are taken as 0 where negative or NaN, as 1 above 1.
+ *   uniform  : fp32 [B][Nt], independent and uniform in [0, 1): entry j decides on node j, entry 0
+ *              is for the last token.
+ * With p, q the two rows of a node, a_0 = 0, t_0 = 1 and s_0 = 0, its k-th tried child (from 0), of
+ * token x, is accepted if
+ *     u q(x) / (1 - s_k) t_k < max(p(x) - a_k q(x), 0),
+ * and on its rejection a_{k+1} = a_k + t_k / (1 - s_k), t_{k+1} = sum_i max(p(i) - a_{k+1} q(i), 0).
+ *   replacement : nonzero: a node's children were drawn independently (s_k = 0); 0: one after
+ *              another, each from what the ones before it left of q (s_k = the sum of q of the
+ *              rejected ones; 1 - s_k is taken as 2^-60 at least, a_k as 2^60 at most).
+ *   draft_probs NULL: the drafts are certain, not drawn (looked up, or the most likely ones):
+ *              x is accepted if u t_k < p_k(x), and rejected it is taken out, p_{k+1}(x) = 0,
+ *              t_{k+1} = t_k - p_k(x); p_0 = p.
+ * The last token is the least i with P(0) + ... + P(i) > u (P(0) + ... + P(V-1)), P(i) = max(p(i) -
+ * a_k q(i), 0) or p_k(i) after the node's last rejection, or p itself where nothing is left.
+ * Sums over the vocabulary are exact in 2^-60 of a probability and do not depend on the machine.
+ * Outputs (int32, every element is written):
+ *   path     : [B][Nt]: the accepted nodes from node 0 on, then -1.
+ *   new_tokens : [B][Nt]: the accepted drafted tokens, then the last token, then -1.
+ *   count    : [B]: how many of each: 1 and the number of accepted drafts.
+ * A sequence without nodes gets count 0.  So does one with a bad parent or token, which is recorded
+ * as FA_ERR_BAD_INDEX.  Where the target's row holds no positive value the last token is -1.
+ *   B, Nt >= 1, Nt <= FA_MAX_TREE_NODES (FA_ERR_UNSUPPORTED), V in [1, 2^30], B * Nt < 2^28.
+ */
+int fa_verify_tree(const int *tokens, const int *parents, const void *target_probs,
+                   const void *draft_probs, const float *uniform, int *path, int *new_tokens,
+                   int *count, int B, int Nt, int V, int bf16, int replacement, void *stream);
+
+/*
+ * Keeps the accepted nodes of drafted trees in a paged bf16 cache, in all layers at once: behind
+ * sequence b's seq_lens[b] tokens, the row of node path[b][i] becomes row i, i < count[b], in every
+ * buffer and head, as if only those tokens had been stored; lens[b] = seq_lens[b] + count[b].
+ * Rows of the cache that get no node keep their bytes.
+ *   caches   : HOST array of n_caches device pointers (1 .. FA_MAX_COPY_CACHES), each bf16
+ *              [num_pages][Hkv][page_size][d], 16-byte aligned.
+ *   path     : int32 [B][Nt], its first count[b] entries ascending, 0 .. Nt-1; count int32 [B], 0 ..
+ *              Nt; block_table int32 [B][max_pages_per_seq], seq_lens int32 [B] (device memory), as
+ *              in fa_decode_paged_tree.  Pages that take a node must not be shared with another
+ *              sequence (copy them first: fa_fork_pages).
+ *   lens     : int32 [B] out; overlaps none of the inputs.
+ *   d        : 64, 96, 128 or 256.  B <= 65535.  Nt <= FA_MAX_TREE_NODES (FA_ERR_UNSUPPORTED).
+ * A sequence with a bad length, count, path or page is left as it is (lens[b] = seq_lens[b]) and
+ * recorded as FA_ERR_BAD_INDEX.
+ */
+int fa_keep_path(void *const *caches, int n_caches, const int *block_table, const int *seq_lens,
+                 const int *path, const int *count, int *lens, int B, int Nt, int Hkv, int d,
+                 int page_size, int max_pages_per_seq, int num_pages, void *stream);
+
+/*
  * Diagnostic: launches one warp that waits, through the same bounded wait the
  * attention kernels use, on a barrier that nothing ever arrives on.  The wait
  * gives up after `limit_ns` nanoseconds (1e3 <= limit_ns <= 5e9, else
