@@ -59,8 +59,9 @@ struct TreeTile {
 template <int STAGES, int NB>
 struct TreeMisc {
     unsigned long long full[STAGES], empty[STAGES];
-    // per block of rows, by its own units in turn: S is there, P is there (of two), O is there
-    unsigned long long s_full[NB][2], p_full[NB][2], pv_done[NB];
+    // per block of rows, by its own units in turn: S is there, P is there, O is there.  (A warp may
+    // come to wait for O of a unit before O of the last one is done, so these are two as well.)
+    unsigned long long s_full[NB][2], p_full[NB][2], pv_done[NB][2];
     unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done;
     uint32_t tmem;
     int abort;
@@ -143,13 +144,13 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             for (int k = 0; k < NB; ++k) {
                 mbar_init(bar(ms.s_full[k][u]), 1);
                 mbar_init(bar(ms.p_full[k][u]), 4);  // one arrival per softmax warp
+                mbar_init(bar(ms.pv_done[k][u]), 1);
             }
             mbar_init(bar(ms.q_full[u]), 1);
             mbar_init(bar(ms.q_empty[u]), 1);
             mbar_init(bar(ms.info_full[u]), 1);
             mbar_init(bar(ms.info_empty[u]), 4 * NB);
         }
-        for (int k = 0; k < NB; ++k) mbar_init(bar(ms.pv_done[k]), 1);
         mbar_init(bar(ms.done), 1);
         ms.abort = 0;
         fence_mbar_init();
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     for (int ks = 0; ks < BK / 16; ++ks)
                         mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks * 8,
                                      desc_add(dv, ks * 2048), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
-                    tc_commit_elect(bar(ms.pv_done[blk]));
+                    tc_commit_elect(bar(ms.pv_done[blk][m & 1]));
                     if (blk + 1 == nb) {
                         tc_commit_elect(bar(ms.empty[v_slot.at]));
                         v_slot.advance();
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         }
                         if (t > s.t0 && __any_sync(kFull, move)) {
                             // O <- alpha O once the product before is complete
-                            mbar_wait_warp(bar(ms.pv_done[wg]), (m - 1) & 1, g, SITE_DEC_MMA);
+                            mbar_wait_warp(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
                             tc_fence_after();
                             const uint64_t a2 = f32x2_splat(alpha);
 #pragma unroll 1
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             }
             // ---- the segment's rows
             inform();
-            if (rows > 0) mbar_wait_warp(bar(ms.pv_done[wg]), (m - 1) & 1, g, SITE_DEC_MMA);
+            if (rows > 0) mbar_wait_warp(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
             tc_fence_after();
             const bool bad_page = *(volatile int *)&ms.bad_page[ib] != 0;
             const bool bad_tree = *(volatile int *)&ms.bad_tree[ib] != 0, bad = bad_page || bad_tree;

@@ -48,6 +48,15 @@ def test_many_rows(fa, H, Hkv, Nt, d):
     run(fa, [77, 5, 400], H, Hkv, Nt, Nt, d, 32, Nt, parents="ragged")
 
 
+@pytest.mark.parametrize("H,Hkv,Nt,d", [(16, 2, 21, 256), (48, 4, 32, 128), (16, 2, 21, 64)])
+def test_many_rows_of_several_tiles(fa, H, Hkv, Nt, d):
+    """Items of different numbers of rows in turn, each of several tiles, in calls right after one another."""
+    dev, (o, lse) = run(fa, [1830, 761, 249, 1422, 353], H, Hkv, Nt, Nt, d, 48, Nt, parents="ragged")
+    for _ in range(20):
+        o2, lse2 = fa.decode_paged_tree(*dev)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("Nq", [1, 4, 19])
 def test_chain(fa, Nq):
     run(fa, [0, 1, 60, 500], 8, 2, Nq, Nq, 128, 16, Nq, parents=None)
