@@ -26,27 +26,34 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 // part of the row, so that the sums also lead to the token at the end: the CTA, the warp, the step
 // and the lane in which the running sum passes u times the whole.
 //
-// Sums are exact: probabilities are held in 64-bit fixed point, 2^-60, in which a 24-bit
-// significand is exact from 2^-37 up and smaller ones are off by less than 2^-60.  So no order of
-// summation and no number of CTAs changes a result, and where p and q are nearly equal nothing is
-// lost.  (In fp64 the sums would be ten times the work: this GPU adds two doubles per clock and SM.)
+// Sums are whole numbers: each weight p - a q is formed without a rounding in fp32 pairs and taken
+// in multiples of 2^-44, so no order of summation and no number of CTAs changes a result, and
+// where p and q are nearly equal nothing is lost.  fp64 would not do: this GPU adds two doubles per
+// clock and SM.  The numbers are cut out by adding a constant whose last place is the multiple wanted
+// and summing the bit patterns: 13 fp32 and integer operations per element, against two dozen, half
+// of them shifts, of a conversion to 64 bits (B64 Nt24 V128000, six sums one after another: 80 us).
 
 constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxNodes = FA_MAX_TREE_NODES;
 
-// floor(x 2^bits) of x >= 0, NaN and below as 0, 1 and above as 2^bits (bits 60), or one less
-// (bits 64).
-template <int BITS>
-__device__ __forceinline__ unsigned long long to_fixed(float x) {
-    if (!(x > 0.f)) return 0ull;
-    if (x >= 1.f) return BITS == 64 ? ~0ull : 1ull << (BITS & 63);
-    const uint32_t w = __float_as_uint(x);
-    const int e = (int)(w >> 23) - 150 + BITS;  // x = m 2^(e - BITS)
-    const unsigned long long m = (w & 0x7fffffu) | 0x800000u;  // a subnormal's is shifted out all the same
-    return e >= 0 ? m << e : e > -24 ? m >> -e : 0ull;
+// x as a probability: 0 for what is below 0 or NaN, 1 above 1.
+__device__ __forceinline__ float probability(float x) { return __saturatef(x); }
+
+// floor(u 2^64) of a number in [0, 1), the largest there is from 1 on.
+__device__ __forceinline__ unsigned long long unit_fixed(float u) {
+    u = probability(u);
+    const uint32_t w = __float_as_uint(u), by = 126u - (w >> 23);
+    const unsigned long long m = (unsigned long long)((w & 0x7fffffu) | 0x800000u) << 40;
+    return u >= 1.f ? ~0ull : by < 64 ? m >> by : 0ull;
 }
 
-__device__ __forceinline__ float probability(float x) { return x > 0.f ? fminf(x, 1.f) : 0.f; }
+// A weight of 0 .. 1 is k1 2^-22 + k2 2^-44: the bit patterns of kCut1 + k1 2^-22 and of kCut2 +
+// k2 2^-44, floats whose last places those are.
+constexpr float kCut1 = 3.0f, kCut2 = 1.5f * 0x1p-21f;
+constexpr uint32_t kBits1 = 0x40400000u, kBits2 = 0x35400000u;
+__device__ __forceinline__ long long weight_of(uint32_t k1, uint32_t k2) {  // of sums of up to 2^8
+    return ((long long)(int)k1 << 22) + (int)k2;
+}
 
 template <typename P>
 struct Row;  // the VEC probabilities of 16 bytes
@@ -54,25 +61,24 @@ template <>
 struct Row<float> {
     static constexpr int VEC = 4;
     __device__ static float get(const uint4 &w, int i) {
-        return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+        return probability(__uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w));
     }
-    __device__ static float one(const float *p) { return *p; }
+    __device__ static float one(const float *p) { return probability(*p); }
 };
 template <>
 struct Row<__nv_bfloat16> {
     static constexpr int VEC = 8;
     __device__ static float get(const uint4 &w, int i) {
         const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
-        return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+        return probability(__uint_as_float(i & 1 ? x & 0xffff0000u : x << 16));
     }
-    __device__ static float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    __device__ static float one(const __nv_bfloat16 *p) { return probability(__bfloat162float(*p)); }
 };
 
 // What is left of the target's probabilities: max(p - a q, 0), or p without the rejected tokens.
 struct Left {
     int cur;                     // the node after which they are
-    unsigned long long a;        // a = a_fixed 2^-shift, of 62 significant bits; shift < 0: a is 1
-    int shift;
+    float a_hi, a_lo;            // a, their sum
     int n_gone;
     int count;                   // nodes accepted so far
     int stop;                    // 1: this sum is for the token at the end
@@ -82,7 +88,7 @@ struct VerifyShared {
     int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
     float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
     unsigned long long warp_sum[kVerifyWarps];
-    unsigned long long cta_sum[2][16];  // of every CTA of the cluster, by turns
+    unsigned long long cta_sum[2][8];  // of every CTA of the cluster, by turns
     int bad;
     Left left;
 };
@@ -93,47 +99,79 @@ struct Weights {
     const P *p, *q;               // the node's rows
     const VerifyShared &sh;
     const Left &l;
-    int V, before;                // elements of the first 16 bytes that lie before the row
+    int V;
 
-    // the weights of elements i0 .. i0 + VEC - 1, which share 16 bytes; 0 outside the row
-    __device__ __forceinline__ void get(int i0, unsigned long long (&w)[VEC]) const {
-        float x[VEC], y[VEC];
+    // 16 bytes of both rows from element i0 on; 0 outside the rows (before them lies the row
+    // before, or nothing; the first unit's elements there are passed over in `get`)
+    struct Raw {
+        uint4 a, b;
+    };
+    __device__ __forceinline__ Raw load(int i0) const {
+        Raw r;
+        r.b = make_uint4(0u, 0u, 0u, 0u);
         if (i0 + VEC <= V) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p + i0));
-            const uint4 b = DRAFT ? __ldg(reinterpret_cast<const uint4 *>(q + i0)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                x[e] = i0 + e >= 0 ? Row<P>::get(a, e) : 0.f;
-                y[e] = DRAFT ? Row<P>::get(b, e) : 0.f;
-            }
+            r.a = __ldg(reinterpret_cast<const uint4 *>(p + i0));
+            if (DRAFT) r.b = __ldg(reinterpret_cast<const uint4 *>(q + i0));
         } else {
-#pragma unroll
+            uint32_t x[4] = {}, y[4] = {};
+            constexpr int PER = VEC / 4;  // elements per word
             for (int e = 0; e < VEC; ++e) {
-                const bool in = i0 + e >= 0 && i0 + e < V;
-                x[e] = in ? Row<P>::one(p + i0 + e) : 0.f;
-                y[e] = in && DRAFT ? Row<P>::one(q + i0 + e) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = to_fixed<60>(x[e]);
-        if (DRAFT) {
-            if (l.a) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    unsigned long long off = to_fixed<60>(y[e]);
-                    if (l.shift >= 0) {
-                        const unsigned long long hi = __umul64hi(l.a, off), lo = l.a * off;
-                        off = hi >> l.shift ? ~0ull : l.shift == 0 ? lo : hi << (64 - l.shift) | lo >> l.shift;
-                    }
-                    w[e] = w[e] > off ? w[e] - off : 0ull;
+                if (i0 + e >= V) break;
+                if (PER == 1) {
+                    x[e] = reinterpret_cast<const uint32_t *>(p)[i0 + e];
+                    if (DRAFT) y[e] = reinterpret_cast<const uint32_t *>(q)[i0 + e];
+                } else {
+                    x[e / PER] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[i0 + e] << 16 * (e % PER);
+                    if (DRAFT) y[e / PER] |= (uint32_t)reinterpret_cast<const uint16_t *>(q)[i0 + e] << 16 * (e % PER);
                 }
             }
-        } else {
+            r.a = make_uint4(x[0], x[1], x[2], x[3]);
+            r.b = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        return r;
+    }
+
+    // k1 and k2 of the weight of an element, as bit patterns
+    __device__ __forceinline__ void cut(float x, float y, uint32_t &k1, uint32_t &k2) const {
+        float w = x, rest = 0.f;  // the weight, as a sum
+        if (DRAFT) {
+            if (l.a_hi == 1.f && l.a_lo == 0.f) {
+                x = fmaxf(x, y);
+                w = x - y;
+                rest = (x - w) - y;
+            } else {
+                const float h = l.a_hi * y, lo = fmaf(l.a_lo, y, fmaf(l.a_hi, y, -h)), d = x - h;
+                const float e = ((x - d) - h) - lo;
+                w = d + e;
+                rest = e - (w - d);
+                if (!(x >= h && w > 0.f)) w = rest = 0.f;
+            }
+        }
+        const float t1 = w + kCut1;
+        const float t2 = ((w - (t1 - kCut1)) + rest) + kCut2;
+        k1 = __float_as_uint(t1);
+        k2 = __float_as_uint(t2);
+    }
+    // their weights
+    __device__ __forceinline__ void get(const Raw &r, int i0, uint32_t (&k1)[VEC], uint32_t (&k2)[VEC]) const {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            cut(Row<P>::get(r.a, e), DRAFT ? Row<P>::get(r.b, e) : 0.f, k1[e], k2[e]);
+            k1[e] -= kBits1;
+            k2[e] -= kBits2;
+        }
+        if (i0 < 0) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (i0 + e < 0) k1[e] = k2[e] = 0u;
+        }
+        if (!DRAFT) {
             for (int k = 0; k < l.n_gone; ++k) {
                 const int at = sh.gone[k] - i0;
+                if ((unsigned)at >= (unsigned)VEC) continue;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    if (e == at) w[e] = 0ull;
+                    if (e == at) k1[e] = k2[e] = 0u;
             }
         }
     }
@@ -145,8 +183,17 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
     return x;
 }
 
+// 1 / x of 2^-60 .. 1 by Newton's iteration from fp32's 1 / x: 2^-23, 2^-46, 2^-53 (an fp64 divide is
+// a microsecond here)
+__device__ __forceinline__ double inverse(double x) {
+    if (x == 1.0) return 1.0;
+    double r = (double)__frcp_rn((float)x);
+    r = fma(r, fma(-x, r, 1.0), r);
+    return fma(r, fma(-x, r, 1.0), r);
+}
+
 template <typename P, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyParams v) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const VerifyParams v) {
     constexpr int VEC = Row<P>::VEC;
     __shared__ VerifyShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -174,8 +221,8 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
         sh.tokens[j] = x;
         sh.u[j] = v.uniform[at];
         if (up >= 0) {
-            sh.px[j] = probability(Row<P>::one(target + (size_t)up * V + x));
-            sh.qx[j] = DRAFT ? probability(Row<P>::one(draft + (size_t)up * V + x)) : 1.f;
+            sh.px[j] = Row<P>::one(target + (size_t)up * V + x);
+            sh.qx[j] = DRAFT ? Row<P>::one(draft + (size_t)up * V + x) : 1.f;
         }
     }
     __syncthreads();
@@ -210,25 +257,17 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
                 }
                 if (next < 0 || stale) {
                     if (lane == 0) {
-                        Left l{cur, 0ull, -1, n_gone, count, next < 0};
-                        if (a > 0.0) {
-                            int e;
-                            frexp(a, &e);  // a < 2^e
-                            l.a = (unsigned long long)ldexp(a, 62 - e);
-                            l.shift = a == 1.0 ? -1 : 62 - e;
-                        }
+                        const float hi = (float)a;
+                        const Left l{cur, hi, (float)(a - (double)hi), n_gone, count, next < 0};
                         sh.left = l;
                     }
                     break;
                 }
                 const double p = (double)sh.px[next], q = (double)sh.qx[next];
-                double w, rest = 1.0, tried = q;  // q of what the draft draws from: all, or the rest
+                double w, drawn = 1.0;  // 1 - s of the definition
                 if (DRAFT) {
                     w = fmax(p - a * q, 0.0);
-                    if (!v.replacement && used > 0.0) {
-                        rest = fmax(1.0 - used, 0x1p-60);
-                        tried = q / rest;
-                    }
+                    if (!v.replacement) drawn = fmax(1.0 - used, 0x1p-60);
                 } else {
                     const int x = sh.tokens[next];
                     bool gone = false;
@@ -236,7 +275,7 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
                     w = gone ? 0.0 : p;
                 }
                 j = next;
-                if ((double)sh.u[j] * tried * total < w) {
+                if ((double)sh.u[j] * q * total < w * drawn) {
                     if (rank == 0 && lane == 0) {
                         path[count] = j;
                         fresh[count - 1] = sh.tokens[j];
@@ -247,7 +286,7 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
                     total = 1.0;
                     n_gone = 0;
                 } else if (DRAFT) {
-                    a = fmin(a + (rest == 1.0 ? total : total / rest), 0x1p60);
+                    a = fmin(a + total * inverse(drawn), 0x1p60);
                     used += q;
                     stale = true;
                 } else {
@@ -262,16 +301,31 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
         const Left l = sh.left;
         const size_t row = (size_t)l.cur * V;
         const int before = (int)(((size_t)b * Nt * V + row) % VEC);
-        const Weights<P, DRAFT> weights{target + row, DRAFT ? draft + row : nullptr, sh, l, V, before};
+        const Weights<P, DRAFT> weights{target + row, DRAFT ? draft + row : nullptr, sh, l, V};
         const int units = (V + before + VEC - 1) / VEC;
         const int per_warp = (units + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
         const int u0 = (rank * kVerifyWarps + warp) * per_warp, u1 = min(u0 + per_warp, units);
         unsigned long long sum = 0;
-        for (int i = u0 + lane; i < u1; i += 32) {
-            unsigned long long w[VEC];
-            weights.get(i * VEC - before, w);
+        constexpr int kAhead = VEC == 4 ? 4 : 2;  // loads in flight
+        int i = u0 + lane;
+        for (; i + 32 * (kAhead - 1) < u1; i += 32 * kAhead) {
+            typename Weights<P, DRAFT>::Raw raw[kAhead];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum += w[e];
+            for (int k = 0; k < kAhead; ++k) raw[k] = weights.load((i + 32 * k) * VEC - before);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                uint32_t k1[VEC], k2[VEC], s1 = 0, s2 = 0;
+                weights.get(raw[k], (i + 32 * k) * VEC - before, k1, k2);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s1 += k1[e], s2 += k2[e];
+                sum += weight_of(s1, s2);
+            }
+        }
+        for (; i < u1; i += 32) {
+            uint32_t k1[VEC], k2[VEC];
+            weights.get(weights.load(i * VEC - before), i * VEC - before, k1, k2);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum += weight_of(k1[e], k2[e]);
         }
         sum = warp_sum(sum);
         if (lane == 0) sh.warp_sum[warp] = sum;
@@ -289,11 +343,11 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
         const unsigned long long mine = sh.cta_sum[turn][rank];
         turn ^= 1;
         if (!l.stop) {
-            total = (double)whole * 0x1p-60;
+            total = (double)whole * 0x1p-44;
             stale = false;
             continue;
         }
-        if (whole == 0 && (l.a || l.n_gone)) {  // the drafts left nothing: the target's own
+        if (whole == 0 && (l.a_hi > 0.f || l.n_gone)) {  // the drafts left nothing: the target's own
             a = 0.0;
             n_gone = 0;
             stale = false;
@@ -302,7 +356,7 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
             continue;
         }
         // ---- the token whose part of the running sum holds u times the whole
-        const unsigned long long goal = __umul64hi(to_fixed<64>(sh.u[0]), whole);
+        const unsigned long long goal = __umul64hi(unit_fixed(sh.u[0]), whole);
         if (warp == 0 && rank == 0) {
             for (int i = count + lane; i < Nt; i += 32) path[i] = fresh[i] = -1;
             if (lane == 0) {
@@ -310,43 +364,54 @@ __global__ void __launch_bounds__(kVerifyThreads) fa_verify_kernel(const VerifyP
                 if (whole == 0) fresh[count - 1] = -1;
             }
         }
-        // (a CTA's own count is the same in all of them)
-        if (goal >= here && goal - here < mine) {
-            unsigned long long before_warp = here;
-            for (int w = 0; w < warp; ++w) before_warp += sh.warp_sum[w];
-            if (goal >= before_warp && goal - before_warp < sh.warp_sum[warp]) {
-                unsigned long long left = goal - before_warp;
-                for (int base = u0; base < u1; base += 32) {
-                    unsigned long long w[VEC], lane_sum = 0;
+        if (goal < here || goal - here >= mine) break;
+        // it is this CTA's: in the part of warp w, which all threads go through, a unit each
+        unsigned long long left = goal - here;
+        int w = 0;
+        while (left >= sh.warp_sum[w]) left -= sh.warp_sum[w++];
+        const int first = (rank * kVerifyWarps + w) * per_warp, end = min(first + per_warp, units);
+        for (int base = first; base < end; base += kVerifyThreads) {
+            unsigned long long x[VEC], sum = 0;
+            const int unit = base + (int)threadIdx.x, i0 = unit * VEC - before;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) w[e] = 0ull;
-                    const int i0 = (base + lane) * VEC - before;
-                    if (base + lane < u1) weights.get(i0, w);
+            for (int e = 0; e < VEC; ++e) x[e] = 0ull;
+            if (unit < end) {
+                uint32_t k1[VEC], k2[VEC];
+                weights.get(weights.load(i0), i0, k1, k2);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) lane_sum += w[e];
-                    unsigned long long incl = lane_sum;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const unsigned long long y = __shfl_up_sync(kFull, incl, o);
-                        if (lane >= o) incl += y;
-                    }
-                    const unsigned long long all = __shfl_sync(kFull, incl, 31);
-                    if (left < all) {
-                        unsigned long long run = incl - lane_sum;
-                        if (left >= run && left < incl) {
-                            int found = i0;
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e) {
-                                if (left >= run && left - run < w[e]) found = i0 + e;
-                                run += w[e];
-                            }
-                            fresh[l.count - 1] = found;
-                        }
-                        break;
-                    }
-                    left -= all;
-                }
+                for (int e = 0; e < VEC; ++e) x[e] = weight_of(k1[e], k2[e]);
             }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum += x[e];
+            unsigned long long run = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long y = __shfl_up_sync(kFull, run, o);
+                if (lane >= o) run += y;
+            }
+            __syncthreads();  // the sums below are read
+            if (lane == 31) sh.warp_sum[warp] = run;
+            __syncthreads();
+            unsigned long long all = 0;
+            run -= sum;
+            for (int k = 0; k < kVerifyWarps; ++k) {
+                if (k < warp) run += sh.warp_sum[k];
+                all += sh.warp_sum[k];
+            }
+            if (left >= all) {
+                left -= all;
+                continue;
+            }
+            if (left >= run && left - run < sum) {
+                int found = i0;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (left >= run && left - run < x[e]) found = i0 + e;
+                    run += x[e];
+                }
+                fresh[l.count - 1] = found;
+            }
+            break;
         }
         break;
     }
@@ -444,9 +509,13 @@ int launch_verify_t(const VerifyParams &v, int ctas, cudaStream_t stream) {
 }  // namespace
 
 int launch_verify(const VerifyParams &v, cudaStream_t stream) {
-    // CTAs per sequence: more while they all fit the GPU at once and have a few thousand elements
+    // CTAs per sequence: more while each still has 32 KB of a node's rows, and all of them are no
+    // more than two waves (a sequence of many sums, alone at the end, then has more of the GPU).
+    // With 1, 2, 4, 8: B1 V32000 fp32, two rows, 20, 16, 13, 10.4 us; B48 V50021 bf16, one row, 18.5,
+    // 14.2, 14.1, 17 us; B64 V128000 fp32, two rows, 129, 86, 66, 61 us.
+    const long long bytes = (long long)v.V * (v.bf16 ? 2 : 4) * (v.draft ? 2 : 1);
     int ctas = 1;
-    while (ctas < 8 && (long long)v.B * ctas * 2 <= 4LL * v.num_sms && v.V / (ctas * 2) >= 2048) ctas *= 2;
+    while (ctas < 8 && (long long)v.B * ctas * 2 <= 4LL * v.num_sms && bytes / (ctas * 2) >= 30000) ctas *= 2;
     return v.bf16 ? launch_verify_t<__nv_bfloat16>(v, ctas, stream) : launch_verify_t<float>(v, ctas, stream);
 }
 
