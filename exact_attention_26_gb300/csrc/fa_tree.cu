@@ -35,9 +35,17 @@ struct TreeTile {
     static constexpr int NCH = DP / 64;                 // 128-byte swizzle spans per row
     static constexpr int BK = D == 256 ? 64 : 128;      // keys per tile
     static constexpr int RB = 128 * NB;                 // query rows per item
-    static constexpr int THREADS = 32 * (4 * NB + 3);
-    static constexpr uint32_t CHUNK = BK * 128;
-    static constexpr uint32_t SLOT = NCH * CHUNK;
+    static constexpr int THREADS = 32 * (4 * NB + 4);
+    // Two softmax warpgroups: their threads hold a row of 128 scores, the other warps little, so
+    // the warpgroups trade registers, and every wait is inlined (a called function has one budget).
+    static constexpr bool TRADE = NB == 2;
+    static constexpr int REG_SOFTMAX = 216, REG_OTHERS = 72;
+    static_assert(!TRADE || 2 * REG_SOFTMAX + REG_OTHERS <= 3 * 168, "registers of the launch");
+    // eight rows of a span are 1024 bytes; from group to group, and from span to span
+    static constexpr bool WHOLE = D % 128 == 0;         // a group's spans lie one behind another
+    static constexpr uint32_t GROUP = WHOLE ? NCH * 1024 : 1024;
+    static constexpr uint32_t SPAN = WHOLE ? 1024 : BK * 128;
+    static constexpr uint32_t SLOT = NCH * BK * 128;
     static constexpr uint32_t Q_CHUNK = 128 * 128;
     static constexpr uint32_t Q_BLOCK = NCH * Q_CHUNK;
     static constexpr uint32_t Q_BYTES = NB * Q_BLOCK;
@@ -73,8 +81,7 @@ struct TreeMisc {
 };
 
 struct TreeArgs {
-    CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; (d, page_size, num_pages *
-                                    // Hkv), boxes 64 x box x 1
+    CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; k, v: see `grouped`
     const __nv_bfloat16 *v_cache;
     const int *block_table, *seq_lens, *parents;
     __nv_bfloat16 *o;
@@ -84,8 +91,12 @@ struct TreeArgs {
     int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
     int R, row_blocks;              // query rows per key/value head, items of RB of them
     int box, box_q;                 // rows of a TMA box
+    // 1: k, v as (64, 8, spans, page_size / 8, num_pages * Hkv), boxes of `box` rows, all spans
+    // 0 (pages that are no multiple of 8, d = 64, 96): (d, page_size, num_pages * Hkv), boxes of one
+    int grouped;
     int tile_log2;
     int start;
+    int o_aligned;                  // o begins on 32 bytes (part_o always does)
     float scale_log2;
     int *status;
     unsigned long long limit_ns;
@@ -111,11 +122,32 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// 5-D tiled load from coordinates (0, 0, 0, w, v).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint32_t bar, int w, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(tmap), "r"(bar), "r"(0), "r"(w), "r"(v)
+        : "memory");
+}
+
 // Of a pair of bf16 values, the bits of those that are infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     const uint32_t lo = (x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
     const uint32_t hi = (x & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
     return lo | hi;
+}
+
+// 32 bytes of a thread's row, a whole sector of L2 (a warp's 16-byte stores to 32 rows leave every
+// sector half written).
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 template <int D, int NB>
@@ -125,7 +157,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     constexpr int ST = T::STAGES, BK = T::BK, NCH = T::NCH, QBUF = T::QBUF;
     using Misc = TreeMisc<ST, NB>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
-    constexpr int kMmaWarp = 4 * NB, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 2;
+    constexpr int kMmaWarp = 4 * NB, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 3;  // TMA: K, then V
+    constexpr bool kIn = T::TRADE;
     extern __shared__ uint8_t tree_smem[];
     const uint32_t raw = smem_u32(tree_smem);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -181,12 +214,15 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     auto rows_of = [&](const Segment &x) { return min(T::RB, a.R - x.rb * T::RB); };
     auto blocks_of = [&](const Segment &x) { return NB == 1 ? 1 : (rows_of(x) + 127) / 128; };
 
-    if (warp == kTmaWarp) {
-        // ------------------------------------------------------------ K and V
+    if (warp == kTmaWarp || warp == kTmaWarp + 1) {
+        // ------------------------------------------------------------ K, or V
+        if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
         // A tile is a run of boxes of `box` rows (the largest power of two that divides a page's
         // rows, so a box never straddles two pages); lane i looks up and copies box i (and i +
         // 32, ... of pages that allow only tiny boxes).  Boxes behind the last node are not copied.
-        uint32_t n = 0, seg = 0;  // ring slots used so far; segments begun
+        const bool is_v = warp != kTmaWarp;
+        const CUtensorMap *map = is_v ? &a.tm_v : &a.tm_k;
+        uint32_t n = is_v, seg = 0;  // ring slots up to this warp's next; segments begun
         bool ok = true;
         const int boxes = BK / a.box;
         for (; ok && walk.next(a, &s); ++seg) {
@@ -201,52 +237,51 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             };
             auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
             int pg = lane < boxes ? page_at(s.t0, lane * a.box) : -1;
-            if (seg >= 2)  // `bad_page` of the segment before the last has been read
-                ok = mbar_wait_warp(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
-            if (!ok) break;
-            if (lane == 0) ms.bad_page[ib] = 0;
-            __syncwarp();
+            if (!is_v) {
+                if (seg >= 2)  // `bad_page` of the segment before the last has been read
+                    ok = mbar_wait_warp<kIn>(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+                if (!ok) break;
+                if (lane == 0) ms.bad_page[ib] = 0;
+                __syncwarp();
+            }
 #pragma unroll 1
-            for (int t = s.t0; ok && t < s.t1; ++t) {
+            for (int t = s.t0; ok && t < s.t1; ++t, n += 2) {
                 const int pg_next = lane < boxes ? page_at(t + 1, lane * a.box) : -1;
-                auto page_of = [&](int i) { return i < 32 ? pg : page_at(t, i * a.box); };
-                int mine = 0;
+                const int slot = (int)(n % ST);
+                ok = n < (uint32_t)ST ||
+                     mbar_wait_warp<kIn>(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
+                if (!ok) break;
+                const uint32_t fb = bar(ms.full[slot]), dst = base + slot * T::SLOT;
 #pragma unroll 1
-                for (int i = lane; i < boxes; i += 32) {
-                    const int key = t * BK + i * a.box;
-                    if (valid(page_of(i))) {
-                        ++mine;
-                    } else if (key < keys) {  // wrong if it holds a token: places without a node do not
+                for (int i0 = 0; i0 < boxes; i0 += 32) {
+                    const int i = i0 + lane, key = t * BK + i * a.box;
+                    const int page = i0 == 0 ? pg : page_at(t, i * a.box);
+                    const bool copy = i < boxes && valid(page);
+                    if (!is_v && !copy && i < boxes && key < keys) {
+                        // wrong if it holds a token: places without a node do not
                         bool token = key < len || !a.parents;
                         for (int j = key - len; !token && j < min(key - len + a.box, a.Nt); ++j)
                             token = a.parents[(size_t)s.b * a.Nt + j] >= -1;
                         if (token) ms.bad_page[ib] = 1;
                     }
-                }
-                const uint32_t bytes = (uint32_t)__reduce_add_sync(kFull, mine) * (uint32_t)a.box * 128u * NCH;
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int slot = (int)(n % ST);
-                    ok = n < (uint32_t)ST ||
-                         mbar_wait_warp(bar(ms.empty[slot]), ((n / ST) - 1) & 1, g, SITE_DEC_EMPTY);
-                    if (!ok) break;
-                    const uint32_t fb = bar(ms.full[slot]);
-                    const CUtensorMap *map = kv ? &a.tm_v : &a.tm_k;
+                    const int mine = __popc(__ballot_sync(kFull, copy));
                     if (lane == 0) {
-                        if (bytes) mbar_arrive_expect_tx(fb, bytes);
-                        else mbar_arrive(fb);
+                        // the phase's one arrival comes with its last boxes
+                        const uint32_t bytes = (uint32_t)(mine * a.box) * (uint32_t)(NCH * 128);
+                        if (i0 + 32 < boxes) mbar_expect_tx(fb, bytes);
+                        else mbar_arrive_expect_tx(fb, bytes);
                     }
                     __syncwarp();
+                    if (copy) {
+                        const int y = key - (int)a.by_page.div((uint32_t)key) * a.page_size, row = i * a.box;
+                        const int z = page * a.Hkv + s.kvh;
+                        const uint32_t to = dst + (row >> 3) * T::GROUP + (row & 7) * 128;
+                        if (a.grouped) {
+                            tma_load_5d(to, map, fb, y >> 3, z);
+                        } else {
 #pragma unroll 1
-                    for (int i = lane; i < boxes; i += 32) {
-                        const int page = page_of(i), row = i * a.box;
-                        if (!valid(page)) continue;
-                        const uint32_t key = (uint32_t)(t * BK + row);
-                        const int y = (int)(key - a.by_page.div(key) * (uint32_t)a.page_size);
-                        const uint32_t dst = base + slot * T::SLOT + row * 128;
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tma_load_3d(dst + c * T::CHUNK, map, fb, c * 64, y, page * a.Hkv + s.kvh);
+                            for (int c = 0; c < NCH; ++c) tma_load_3d(to + c * T::SPAN, map, fb, c * 64, y, z);
+                        }
                     }
                     __syncwarp();
                 }
@@ -257,11 +292,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             // let every copy still in flight land before the CTA exits
             volatile int never = 0;
             const Guard g2{a.status, &never, kWaitLimitNs};
-            for (uint32_t i = n > (uint32_t)ST ? n - ST : 0; i < n; ++i)
-                mbar_wait_warp(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
+            for (uint32_t i = n > (uint32_t)ST ? n - ST : is_v; i < n; i += 2)
+                mbar_wait_warp<kIn>(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
+        if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
         if (blockIdx.x == 0) {
             bool ok = true;
             for (int b = lane; b < a.B; b += 32) ok = ok && len_ok(a, a.seq_lens[b]);
@@ -288,14 +324,14 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             }
         };
         Slot k_slot{0, 0}, v_slot{1, 0};
-        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
-        const uint64_t d_v = sdesc_sw128(base, T::CHUNK, 1024);
+        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, T::GROUP);
+        const uint64_t d_v = sdesc_sw128(base, T::SPAN, T::GROUP);
         auto issue_s = [&]() {
             const int qb = (int)(seg % QBUF);
             if (ta == sa.t0 && ba == 0)
-                ok = mbar_wait_warp(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
+                ok = mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
             if (ok && ba == 0)
-                ok = mbar_wait_warp(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
+                ok = mbar_wait_warp<kIn>(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
             if (!ok) return;
             tc_fence_after();
             const uint64_t dq = desc_add(d_q, qb * T::Q_BYTES + ba * T::Q_BLOCK);
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
                 mma_ss_elect(tmem + (js & 1) * BK, desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32),
-                             desc_add(dk, (ks >> 2) * T::CHUNK + (ks & 3) * 32), kIdescS, ks > 0 ? 1u : 0u);
+                             desc_add(dk, (ks >> 2) * T::SPAN + (ks & 3) * 32), kIdescS, ks > 0 ? 1u : 0u);
             const uint32_t m = NB == 2 && ba == 1 ? cs[NB - 1]++ : cs[0]++;
             tc_commit_elect(bar(ms.s_full[ba][m & 1]));
             ++js;
@@ -329,19 +365,24 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             const int nb = blocks_of(s);
             for (int t = s.t0; ok && t < s.t1; ++t)
                 for (int blk = 0; ok && blk < nb; ++blk, ++jp) {
-#pragma unroll 1
-                    while (ok && more && (js == jp || (js == jp + 1 && ready()))) issue_s();
                     const uint32_t m = NB == 2 && blk == 1 ? cp[NB - 1]++ : cp[0]++;
-                    ok = ok && mbar_wait_warp(bar(ms.p_full[blk][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+                    const uint32_t pb = bar(ms.p_full[blk][m & 1]), pp = (m >> 1) & 1;
+                    while (ok && more && js == jp) issue_s();
+                    // whichever comes first, the next S's operands or this unit's P
+                    for (int k = 0; ok && more && js == jp + 1 && k < 4096; ++k) {
+                        if (ready()) issue_s();
+                        else if (__all_sync(kFull, mbar_try_wait_sleep(pb, pp, 200u))) break;
+                    }
+                    ok = ok && mbar_wait_warp<kIn>(pb, pp, g, SITE_DEC_MMA);
                     if (ok && blk == 0)
-                        ok = mbar_wait_warp(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
+                        ok = mbar_wait_warp<kIn>(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t dv = desc_add(d_v, v_slot.at * T::SLOT);
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
                         mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks * 8,
-                                     desc_add(dv, ks * 2048), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
+                                     desc_add(dv, ks * 2 * T::GROUP), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                     tc_commit_elect(bar(ms.pv_done[blk][m & 1]));
                     if (blk + 1 == nb) {
                         tc_commit_elect(bar(ms.empty[v_slot.at]));
@@ -353,9 +394,10 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         tc_commit_elect(bar(ms.done));
         volatile int never = 0;
         const Guard g2{a.status, &never, kWaitLimitNs};
-        mbar_wait_warp(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
+        mbar_wait_warp<kIn>(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
     } else if (warp == kAuxWarp) {
         // ------------------------------------------------------ queries and trees
+        if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
         uint32_t seg = 0, q_sent = 0;
         bool ok = true;
         // the segment's query rows; rows behind them in the last box are other heads', or zeros
@@ -363,7 +405,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         auto put_queries = [&]() {
             const int qb = (int)(seg % QBUF), nb = blocks_of(s);
             if (seg >= (uint32_t)QBUF)
-                ok = mbar_wait_warp(bar(ms.q_empty[qb]), ((seg / QBUF) - 1) & 1, g, SITE_DEC_EMPTY);
+                ok = mbar_wait_warp<kIn>(bar(ms.q_empty[qb]), ((seg / QBUF) - 1) & 1, g, SITE_DEC_EMPTY);
             if (!ok) return;
             if (lane == 0) {
                 const uint32_t fb = bar(ms.q_full[qb]);
@@ -382,7 +424,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             const bool first = QBUF == 2 || seg == 0;
             if (first) put_queries();
             if (ok && seg >= 2)
-                ok = mbar_wait_warp(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
+                ok = mbar_wait_warp<kIn>(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
             if (!ok) break;
             if (lane < kNodeWords) ms.special[ib][lane] = 0;
             bool bad = false;
@@ -425,10 +467,11 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             volatile int never = 0;
             const Guard g2{a.status, &never, kWaitLimitNs};
             for (uint32_t i = q_sent > (uint32_t)QBUF ? q_sent - QBUF : 0; i < q_sent; ++i)
-                mbar_wait_warp(bar(ms.q_full[i % QBUF]), (i / QBUF) & 1, g2, SITE_DEC_DRAIN);
+                mbar_wait_warp<kIn>(bar(ms.q_full[i % QBUF]), (i / QBUF) & 1, g2, SITE_DEC_DRAIN);
         }
     } else {
         // ------------------------------------------------------------ softmax, results
+        if constexpr (T::TRADE) setmaxnreg_inc<T::REG_SOFTMAX>();
         // Every warp runs every step even after a wait has given up (waits then return soon).
         const int wg = warp >> 2, w4 = warp & 3;
         const int kk = threadIdx.x & 127;  // row of the block; lane of S and O; key of a tile's V
@@ -444,7 +487,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             const int full_tiles = len >> (D == 256 ? 6 : 7);
             bool informed = false;
             auto inform = [&]() {
-                if (!informed) mbar_wait_warp(bar(ms.info_full[ib]), (seg >> 1) & 1, g, SITE_DEC_MMA);
+                if (!informed) mbar_wait_warp<kIn>(bar(ms.info_full[ib]), (seg >> 1) & 1, g, SITE_DEC_MMA);
                 informed = true;
             };
             // word k of the bits of nodes that node j sees; the cached keys stand before them
@@ -462,7 +505,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 for (int t = s.t0; t < s.t1; ++t, ++m) {
                     const bool partly = t >= full_tiles;
                     if (partly) inform();
-                    mbar_wait_warp(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+                    mbar_wait_warp<kIn>(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
                     tc_fence_after();
                     if (mine) {
                         const uint32_t unit = units + (uint32_t)((t - s.t0) * nb + wg);
@@ -520,7 +563,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         }
                         if (t > s.t0 && __any_sync(kFull, move)) {
                             // O <- alpha O once the product before is complete
-                            mbar_wait_warp(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
+                            mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
                             tc_fence_after();
                             const uint64_t a2 = f32x2_splat(alpha);
 #pragma unroll 1
@@ -546,14 +589,14 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         // so do such values of nodes, which their rows get back at the end
                         const uint32_t i = 2 * (tiles + (uint32_t)(t - s.t0)) + 1;
                         const int slot = (int)(i % ST), key = t * BK + kk;
-                        mbar_wait(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
-                        uint8_t *v0 = gbase + slot * T::SLOT + kk * 128;
+                        mbar_wait<kIn>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
+                        uint8_t *v0 = gbase + slot * T::SLOT + (kk >> 3) * T::GROUP + (kk & 7) * 128;
                         if (key >= len) {
                             const bool keep = is_node(key - len);
                             bool found = false;
 #pragma unroll 1
                             for (int e = 0; e < NCH * 8; ++e) {
-                                uint4 *p = reinterpret_cast<uint4 *>(v0 + (e >> 3) * T::CHUNK + (e & 7) * 16);
+                                uint4 *p = reinterpret_cast<uint4 *>(v0 + (e >> 3) * T::SPAN + (e & 7) * 16);
                                 uint4 w = keep ? *p : make_uint4(0u, 0u, 0u, 0u);
                                 const uint4 f = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z),
                                                            not_finite(w.w));
@@ -575,7 +618,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             }
             // ---- the segment's rows
             inform();
-            if (rows > 0) mbar_wait_warp(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
+            if (rows > 0) mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
             tc_fence_after();
             const bool bad_page = *(volatile int *)&ms.bad_page[ib] != 0;
             const bool bad_tree = *(volatile int *)&ms.bad_tree[ib] != 0, bad = bad_page || bad_tree;
@@ -594,41 +637,50 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 const bool put = kk < rows && !bad;
                 const bool special = *(volatile int *)&ms.special_any[ib] != 0 && !none && !bad;
                 const int *bt = a.block_table + (size_t)s.b * a.max_pages;
+                __nv_bfloat16 *out = a.o + (size_t)row * D;
+                float *part = a.part_o + prow * D;
+                // (code that runs once per item is kept small: fetching it costs more than running it)
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    float y[32];
                     __syncwarp();
-                    tmem_ld32(t_o + c * 32, o);
+                    tmem_ld32(t_o + c, o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = none ? 0.f : __uint_as_float(o[e]) * inv;
-                    if (special && put) {
-#pragma unroll 1
-                        for (int j = 0; j < a.Nt; ++j) {
-                            if (!(ms.special[ib][j >> 5] & sees(node, j >> 5) & 1u << (j & 31))) continue;
-                            const uint32_t key = (uint32_t)(len + j), i = a.by_page.div(key);
-                            const __nv_bfloat16 *v =
-                                a.v_cache + (((size_t)bt[i] * a.Hkv + s.kvh) * a.page_size + (key - i * a.page_size)) * D +
-                                c * 32;
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+                    if (put && !whole) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float f = __bfloat162float(v[e]);
-                                if (!(fabsf(f) < INFINITY)) y[e] += f;
-                            }
+                        for (int e = 0; e < 32; e += 8) store32(part + c + e, o + e);
+                    }
+                    if (put && whole) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        if (a.o_aligned) {
+                            store32(out + c, o);
+                            store32(out + c + 16, o + 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4 *>(out + c + 2 * e) =
+                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         }
                     }
-                    if (!put) continue;
-                    if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)row * D + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                                pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + prow * D + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                }
+                if (special && put) {  // infinities and NaN of nodes' values that the row sees
+                    for (int j = 0; j < a.Nt; ++j) {
+                        if (!(ms.special[ib][j >> 5] & sees(node, j >> 5) & 1u << (j & 31))) continue;
+                        const uint32_t key = (uint32_t)(len + j), i = a.by_page.div(key);
+                        const __nv_bfloat16 *v =
+                            a.v_cache + (((size_t)bt[i] * a.Hkv + s.kvh) * a.page_size + (key - i * a.page_size)) * D;
+#pragma unroll 1
+                        for (int c = 0; c < D; ++c) {
+                            const float f = __bfloat162float(v[c]);
+                            if (fabsf(f) < INFINITY) continue;
+                            if (whole) out[c] = __float2bfloat16(__bfloat162float(out[c]) + f);
+                            else part[c] += f;
+                        }
                     }
                 }
                 if (kk < rows) {
@@ -675,7 +727,7 @@ template <int D, int NB>
 size_t tree_bytes(const TreeParams &p, size_t *l_offset) {
     const size_t rows = (size_t)tree_ctas<D, NB>(p) * 2 * TreeTile<D, NB>::RB;
     *l_offset = rows * D * sizeof(float);
-    return *l_offset + rows * sizeof(float);
+    return *l_offset + rows * sizeof(float) + 16;  // and room to begin on 32 bytes
 }
 
 template <int D, int NB>
@@ -693,8 +745,9 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.lse = p.lse;
     size_t l_offset;
     tree_bytes<D, NB>(p, &l_offset);
-    a.part_o = static_cast<float *>(p.workspace);
-    a.part_l = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + l_offset);
+    char *const ws = static_cast<char *>(p.workspace) + (reinterpret_cast<uintptr_t>(p.workspace) % 32);
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_l = reinterpret_cast<float *>(ws + l_offset);
     a.by_page = fast_div((uint32_t)p.page_size);
     a.B = p.B;
     a.H = p.H;
@@ -709,8 +762,10 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.row_blocks = (a.R + T::RB - 1) / T::RB;
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
+    a.grouped = tree_grouped(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
     a.start = 1;
+    a.o_aligned = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
@@ -752,6 +807,8 @@ int tree_box_rows(const TreeParams &p) {
     while (box < most && p.page_size % (2 * box) == 0) box *= 2;
     return box;
 }
+
+int tree_grouped(const TreeParams &p) { return p.page_size % 8 == 0 && p.d % 128 == 0; }
 
 int tree_query_box(const TreeParams &p) {
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
