@@ -61,20 +61,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
     return fn;
 }
 
-// A tiled map of rank N (unit element strides, no interleave, 256-byte L2 promotion, zero
+// A 3-D tiled map (unit element strides, no interleave, 256-byte L2 promotion, zero
 // fill past the bounds).  A map is a pure function of its arguments, so the last
 // few encodings are kept and reused: calls that repeat a tensor and shape (every
 // step of a training loop, every decode step) skip the driver call.  Keys hold the
 // address, so a freed and reallocated tensor at the same address with the same
 // shape gets the identical map.
-template <int N>
-int encode(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const cuuint64_t (&dims)[N],
-           const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N], CUtensorMapSwizzle swizzle) {
+int encode_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const cuuint64_t (&dims)[3],
+              const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
     struct Entry {
         const void *ptr;
         int dtype, swizzle;
-        cuuint64_t dims[N], strides[N - 1];
-        cuuint32_t box[N];
+        cuuint64_t dims[3], strides[2];
+        cuuint32_t box[3];
         CUtensorMap map;
     };
     constexpr int kEntries = 32;
@@ -82,11 +81,10 @@ int encode(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const c
     static int used = 0, next = 0;
     static std::mutex m;
     auto same = [&](const Entry &e) {
-        if (e.ptr != ptr || e.dtype != (int)dtype || e.swizzle != (int)swizzle) return false;
-        for (int i = 0; i < N; ++i)
-            if (e.dims[i] != dims[i] || e.box[i] != box[i] || (i + 1 < N && e.strides[i] != strides[i]))
-                return false;
-        return true;
+        return e.ptr == ptr && e.dtype == (int)dtype && e.swizzle == (int)swizzle &&
+               e.dims[0] == dims[0] && e.dims[1] == dims[1] && e.dims[2] == dims[2] &&
+               e.strides[0] == strides[0] && e.strides[1] == strides[1] && e.box[0] == box[0] &&
+               e.box[1] == box[1] && e.box[2] == box[2];
     };
     {
         std::lock_guard<std::mutex> lock(m);
@@ -98,9 +96,11 @@ int encode(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const c
     }
     auto enc = encode_tiled();
     if (!enc) return FA_ERR_CUDA;
-    cuuint32_t elem_strides[N];
-    for (int i = 0; i < N; ++i) elem_strides[i] = 1;
-    CUresult r = enc(map, dtype, N, const_cast<void *>(ptr), dims, strides, box, elem_strides,
+    cuuint64_t d3[3] = {dims[0], dims[1], dims[2]};
+    cuuint64_t s2[2] = {strides[0], strides[1]};
+    cuuint32_t b3[3] = {box[0], box[1], box[2]};
+    cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = enc(map, dtype, 3, const_cast<void *>(ptr), d3, s2, b3, elem_strides,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return FA_ERR_CUDA;
@@ -109,17 +109,12 @@ int encode(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const c
     e.ptr = ptr;
     e.dtype = (int)dtype;
     e.swizzle = (int)swizzle;
-    for (int i = 0; i < N; ++i) e.dims[i] = dims[i], e.box[i] = box[i];
-    for (int i = 0; i + 1 < N; ++i) e.strides[i] = strides[i];
+    for (int i = 0; i < 3; ++i) e.dims[i] = dims[i], e.box[i] = box[i];
+    for (int i = 0; i < 2; ++i) e.strides[i] = strides[i];
     e.map = *map;
     next = (next + 1) % kEntries;
     if (used < kEntries) ++used;
     return FA_OK;
-}
-
-int encode_3d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, const cuuint64_t (&dims)[3],
-              const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
-    return encode<3>(map, dtype, ptr, dims, strides, box, swizzle);
 }
 
 // 3-D map over a contiguous bf16 [BH][N][d] tensor: x = column within the head
@@ -130,18 +125,6 @@ int make_bhnd_map(CUtensorMap *map, const void *ptr, int BH, int N, int d, int b
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)N * (cuuint64_t)d * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// 5-D map over the same tensor for boxes that bring whole rows, by groups of eight (d a multiple of
-// 64, N and box_rows of 8): x = column within a span of 64, y = row within its group, then span,
-// group, (batch, head).  A box lands in shared memory as [group][span][8 rows][64].
-int make_grouped_map(CUtensorMap *map, const void *ptr, int BH, int N, int d, int box_rows) {
-    const cuuint64_t row = (cuuint64_t)d * 2;
-    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)d / 64, (cuuint64_t)N / 8, (cuuint64_t)BH};
-    const cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)N * row};
-    const cuuint32_t box[5] = {64, 8, (cuuint32_t)d / 64, (cuuint32_t)box_rows / 8, 1};
-    return encode<5>(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box,
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -1164,13 +1147,8 @@ extern "C" int fa_decode_paged_tree(const void *q, const void *k_cache, const vo
     if (workspace_bytes < tree_workspace_bytes(p)) return FA_ERR_WORKSPACE;
     if ((rc = make_bhnd_map(&p.tm_q, q, 1, B * H * Nq, d, tree_query_box(p))) != FA_OK) return rc;
     const int planes = num_pages * Hkv, box = tree_box_rows(p);
-    for (int v = 0; v < 2; ++v) {
-        CUtensorMap *map = v ? &p.tm_v : &p.tm_k;
-        const void *cache = v ? v_cache : k_cache;
-        rc = tree_grouped(p) ? make_grouped_map(map, cache, planes, page_size, d, box)
-                             : make_bhnd_map(map, cache, planes, page_size, d, box);
-        if (rc != FA_OK) return rc;
-    }
+    if ((rc = make_bhnd_map(&p.tm_k, k_cache, planes, page_size, d, box)) != FA_OK) return rc;
+    if ((rc = make_bhnd_map(&p.tm_v, v_cache, planes, page_size, d, box)) != FA_OK) return rc;
     return launch_tree(p, static_cast<cudaStream_t>(stream));
 }
 

@@ -243,8 +243,7 @@ int launch_decode8(const Decode8Params &p, cudaStream_t stream);
 // Attention of drafted tokens over the paged bf16 cache.
 struct TreeParams {
     CUtensorMap tm_q, tm_k, tm_v;    // q as one plane of B * H * Nq rows, boxes of tree_query_box rows;
-                                     // k, v as num_pages * Hkv planes, boxes of tree_box_rows rows,
-                                     // with tree_grouped rows by eights and all of a row in a box
+                                     // k, v as num_pages * Hkv planes, boxes of tree_box_rows rows
     const void *v_cache;
     const int *block_table, *seq_lens;
     const int *parents;              // [B][Nt], or null: a chain
@@ -257,7 +256,6 @@ struct TreeParams {
     int num_sms;
 };
 int tree_box_rows(const TreeParams &p);
-int tree_grouped(const TreeParams &p);
 int tree_query_box(const TreeParams &p);
 // Tiles of all items at the longest possible lengths; the kernels count in ints.
 long long tree_max_tiles(const TreeParams &p);

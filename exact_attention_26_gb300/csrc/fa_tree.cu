@@ -35,22 +35,21 @@ struct TreeTile {
     static constexpr int NCH = DP / 64;                 // 128-byte swizzle spans per row
     static constexpr int BK = D == 256 ? 64 : 128;      // keys per tile
     static constexpr int RB = 128 * NB;                 // query rows per item
-    static constexpr int THREADS = 32 * (4 * NB + 4);
-    // Two softmax warpgroups: their threads hold a row of 128 scores, the other warps little, so
-    // the warpgroups trade registers, and every wait is inlined (a called function has one budget).
+    // With one block, two softmax warpgroups, a thread for one half of the tile's keys each: the ring's V
+    // slots are held for as long as a softmax takes (B32 R = 128 of 1..8192 keys: 120 -> 113 us).  With
+    // two, a warpgroup for each (four: 115 -> 137 us, the MMA warp then issues late, and registers end).
+    static constexpr int NH = NB == 1 ? 2 : 1;
+    static constexpr int CB = BK / NH;                  // keys of a thread
+    static constexpr int THREADS = 32 * 12;
     static constexpr bool TRADE = NB == 2;
     static constexpr int REG_SOFTMAX = 216, REG_OTHERS = 72;
-    static_assert(!TRADE || 2 * REG_SOFTMAX + REG_OTHERS <= 3 * 168, "registers of the launch");
-    // eight rows of a span are 1024 bytes; from group to group, and from span to span
-    static constexpr bool WHOLE = D % 128 == 0;         // a group's spans lie one behind another
-    static constexpr uint32_t GROUP = WHOLE ? NCH * 1024 : 1024;
-    static constexpr uint32_t SPAN = WHOLE ? 1024 : BK * 128;
-    static constexpr uint32_t SLOT = NCH * BK * 128;
+    static constexpr uint32_t SPAN = BK * 128;
+    static constexpr uint32_t SLOT = NCH * SPAN;
     static constexpr uint32_t Q_CHUNK = 128 * 128;
     static constexpr uint32_t Q_BLOCK = NCH * Q_CHUNK;
     static constexpr uint32_t Q_BYTES = NB * Q_BLOCK;
     static constexpr int QBUF = Q_BYTES <= 32 * 1024 ? 2 : 1;
-    static constexpr uint32_t MISC = 20 * 1024;
+    static constexpr uint32_t MISC = 24 * 1024;
     static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - MISC - 1024) / SLOT) / 2 * 2;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;    // 128 KB of keys and values
     static constexpr uint32_t OFF_Q = STAGES * SLOT;
@@ -58,7 +57,7 @@ struct TreeTile {
     static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
     static constexpr uint32_t TM_O = 2 * BK;
     static constexpr uint32_t TM_USED = TM_O + NB * DP;
-    static constexpr uint32_t TM_COLS = TM_USED <= 256 ? 256 : 512;
+    static constexpr uint32_t TM_COLS = 512;
     static_assert(STAGES >= 4, "two tiles in the ring");
     static_assert(TM_USED <= 512, "tensor memory budget");
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
@@ -73,6 +72,7 @@ struct TreeMisc {
     unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done;
     uint32_t tmem;
     int abort;
+    float trade[2][2][128];               // what the halves of a row tell each other, by turns
     // per segment of this CTA's work, in turn:
     int bad_page[2], bad_tree[2];         // a page or a parent out of range
     int special_any[2];
@@ -81,7 +81,8 @@ struct TreeMisc {
 };
 
 struct TreeArgs {
-    CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; k, v: see `grouped`
+    CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; (d, page_size, num_pages *
+                                    // Hkv), boxes 64 x box x 1
     const __nv_bfloat16 *v_cache;
     const int *block_table, *seq_lens, *parents;
     __nv_bfloat16 *o;
@@ -91,9 +92,6 @@ struct TreeArgs {
     int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
     int R, row_blocks;              // query rows per key/value head, items of RB of them
     int box, box_q;                 // rows of a TMA box
-    // 1: k, v as (64, 8, spans, page_size / 8, num_pages * Hkv), boxes of `box` rows, all spans
-    // 0 (pages that are no multiple of 8, d = 64, 96): (d, page_size, num_pages * Hkv), boxes of one
-    int grouped;
     int tile_log2;
     int start;
     int o_aligned;                  // o begins on 32 bytes (part_o always does)
@@ -126,15 +124,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// 5-D tiled load from coordinates (0, 0, 0, w, v).
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint32_t bar, int w, int v) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(tmap), "r"(bar), "r"(0), "r"(w), "r"(v)
-        : "memory");
-}
-
 // Of a pair of bf16 values, the bits of those that are infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     const uint32_t lo = (x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
@@ -154,10 +143,10 @@ template <int D, int NB>
 __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ TreeArgs a) {
     using T = TreeTile<D, NB>;
-    constexpr int ST = T::STAGES, BK = T::BK, NCH = T::NCH, QBUF = T::QBUF;
+    constexpr int ST = T::STAGES, BK = T::BK, NH = T::NH, CB = T::CB, NCH = T::NCH, QBUF = T::QBUF;
     using Misc = TreeMisc<ST, NB>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
-    constexpr int kMmaWarp = 4 * NB, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 3;  // TMA: K, then V
+    constexpr int kMmaWarp = 8, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 3;  // TMA: K, then V
     constexpr bool kIn = T::TRADE;
     extern __shared__ uint8_t tree_smem[];
     const uint32_t raw = smem_u32(tree_smem);
@@ -176,13 +165,13 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         for (int u = 0; u < 2; ++u) {
             for (int k = 0; k < NB; ++k) {
                 mbar_init(bar(ms.s_full[k][u]), 1);
-                mbar_init(bar(ms.p_full[k][u]), 4);  // one arrival per softmax warp
+                mbar_init(bar(ms.p_full[k][u]), 4 * NH);  // one arrival per softmax warp
                 mbar_init(bar(ms.pv_done[k][u]), 1);
             }
             mbar_init(bar(ms.q_full[u]), 1);
             mbar_init(bar(ms.q_empty[u]), 1);
             mbar_init(bar(ms.info_full[u]), 1);
-            mbar_init(bar(ms.info_empty[u]), 4 * NB);
+            mbar_init(bar(ms.info_empty[u]), 8);
         }
         mbar_init(bar(ms.done), 1);
         ms.abort = 0;
@@ -273,15 +262,11 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     }
                     __syncwarp();
                     if (copy) {
-                        const int y = key - (int)a.by_page.div((uint32_t)key) * a.page_size, row = i * a.box;
+                        const int y = key - (int)a.by_page.div((uint32_t)key) * a.page_size;
                         const int z = page * a.Hkv + s.kvh;
-                        const uint32_t to = dst + (row >> 3) * T::GROUP + (row & 7) * 128;
-                        if (a.grouped) {
-                            tma_load_5d(to, map, fb, y >> 3, z);
-                        } else {
-#pragma unroll 1
-                            for (int c = 0; c < NCH; ++c) tma_load_3d(to + c * T::SPAN, map, fb, c * 64, y, z);
-                        }
+                        const uint32_t to = dst + i * a.box * 128;
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c) tma_load_3d(to + c * T::SPAN, map, fb, c * 64, y, z);
                     }
                     __syncwarp();
                 }
@@ -324,8 +309,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             }
         };
         Slot k_slot{0, 0}, v_slot{1, 0};
-        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, T::GROUP);
-        const uint64_t d_v = sdesc_sw128(base, T::SPAN, T::GROUP);
+        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
+        const uint64_t d_v = sdesc_sw128(base, T::SPAN, 1024);
         auto issue_s = [&]() {
             const int qb = (int)(seg % QBUF);
             if (ta == sa.t0 && ba == 0)
@@ -381,8 +366,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     const uint64_t dv = desc_add(d_v, v_slot.at * T::SLOT);
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
-                        mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks * 8,
-                                     desc_add(dv, ks * 2 * T::GROUP), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
+                        mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks / (CB / 16) * CB + ks % (CB / 16) * 8,
+                                     desc_add(dv, ks * 2048), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
                     tc_commit_elect(bar(ms.pv_done[blk][m & 1]));
                     if (blk + 1 == nb) {
                         tc_commit_elect(bar(ms.empty[v_slot.at]));
@@ -473,8 +458,9 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         // ------------------------------------------------------------ softmax, results
         if constexpr (T::TRADE) setmaxnreg_inc<T::REG_SOFTMAX>();
         // Every warp runs every step even after a wait has given up (waits then return soon).
-        const int wg = warp >> 2, w4 = warp & 3;
+        const int wg = NH == 1 ? warp >> 2 : 0, h = NH == 1 ? 0 : warp >> 2, w4 = warp & 3;  // block of rows, half of the keys
         const int kk = threadIdx.x & 127;  // row of the block; lane of S and O; key of a tile's V
+        const int pair = 1 + w4;           // barrier of the two warps that share 32 rows
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const uint32_t t_o = tmem + lane_base + T::TM_O + wg * T::DP;
         const float c_s = a.scale_log2;
@@ -509,21 +495,21 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     tc_fence_after();
                     if (mine) {
                         const uint32_t unit = units + (uint32_t)((t - s.t0) * nb + wg);
-                        const uint32_t t_s = tmem + lane_base + (unit & 1) * BK;
-                        uint32_t sr[BK / 32][32];
+                        const uint32_t t_s = tmem + lane_base + (unit & 1) * BK + h * CB;
+                        uint32_t sr[CB / 32][32];
 #pragma unroll
-                        for (int c = 0; c < BK / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
+                        for (int c = 0; c < CB / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
 #pragma unroll
-                        for (int c = 0; c < BK / 32; ++c) tmem_wait_ld(sr[c]);
-                        float x[BK];
+                        for (int c = 0; c < CB / 32; ++c) tmem_wait_ld(sr[c]);
+                        float x[CB];
 #pragma unroll
-                        for (int c = 0; c < BK / 32; ++c)
+                        for (int c = 0; c < CB / 32; ++c)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(sr[c][e]);
                         if (partly) {
-                            const int n0 = t * BK - len;  // node of the tile's first key, or below 0
+                            const int n0 = t * BK + h * CB - len;  // node of the first key, or below 0
 #pragma unroll
-                            for (int c = 0; c < BK / 32; ++c) {
+                            for (int c = 0; c < CB / 32; ++c) {
                                 const int at = (n0 + 32 * c) >> 5, sh = (n0 + 32 * c) & 31;
                                 const uint32_t w = __funnelshift_r(sees(node, at), sees(node, at + 1), sh);
 #pragma unroll
@@ -533,11 +519,17 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         }
                         float mp0 = -INFINITY, mp1 = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < BK; c += 4) {
+                        for (int c = 0; c < CB; c += 4) {
                             mp0 = fmax3(mp0, x[c], x[c + 1]);
                             mp1 = fmax3(mp1, x[c + 2], x[c + 3]);
                         }
-                        const float top = fmaxf(mp0, mp1) * c_s;
+                        float top = fmaxf(mp0, mp1);
+                        if constexpr (NH == 2) {  // of both halves, which then take the same steps
+                            ms.trade[m & 1][h][kk] = top;
+                            named_barrier_sync(pair, 64);
+                            top = fmaxf(top, ms.trade[m & 1][h ^ 1][kk]);
+                        }
+                        top *= c_s;
                         float alpha = 1.f;
                         const bool move = top > m_ref + kMoveLog2;
                         if (move) {
@@ -547,19 +539,27 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         float sp0 = 0.f, sp1 = 0.f;
                         const uint64_t c2 = f32x2_splat(c_s), nm2 = f32x2_splat(-m_ref);
 #pragma unroll
-                        for (int c = 0; c < BK; c += 2) {
+                        for (int c = 0; c < CB; c += 2) {
                             fma_f32x2(x[c], x[c + 1], c2, nm2);
                             x[c] = ex2(x[c]);
                             x[c + 1] = ex2(x[c + 1]);
                             add_f32x2(sp0, sp1, x[c], x[c + 1]);
                         }
                         l = l * alpha + (sp0 + sp1);
+                        // P as bf16 pairs over the first half of the thread's own columns
+                        if constexpr (CB >= 64) {
 #pragma unroll
-                        for (int c = 0; c < BK / 64; ++c) {  // P as bf16 pairs over the slot's first half
-                            uint32_t pk[32];
+                            for (int c = 0; c < CB / 64; ++c) {
+                                uint32_t pk[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]);
-                            tmem_st32(t_s + c * 32, pk);
+                                for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]);
+                                tmem_st32(t_s + c * 32, pk);
+                            }
+                        } else {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                            tmem_st16(t_s, pk);
                         }
                         if (t > s.t0 && __any_sync(kFull, move)) {
                             // O <- alpha O once the product before is complete
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                             tc_fence_after();
                             const uint64_t a2 = f32x2_splat(alpha);
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
+                            for (int c = h; c < D / 32; c += NH) {
                                 uint32_t o[32];
                                 tmem_ld32(t_o + c * 32, o);
                                 tmem_wait_ld(o);
@@ -590,12 +590,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         const uint32_t i = 2 * (tiles + (uint32_t)(t - s.t0)) + 1;
                         const int slot = (int)(i % ST), key = t * BK + kk;
                         mbar_wait<kIn>(bar(ms.full[slot]), (i / ST) & 1, g, SITE_DEC_FULL);
-                        uint8_t *v0 = gbase + slot * T::SLOT + (kk >> 3) * T::GROUP + (kk & 7) * 128;
+                        uint8_t *v0 = gbase + slot * T::SLOT + kk * 128;
                         if (key >= len) {
                             const bool keep = is_node(key - len);
                             bool found = false;
 #pragma unroll 1
-                            for (int e = 0; e < NCH * 8; ++e) {
+                            for (int e = h * NCH * 8 / NH; e < (h + 1) * NCH * 8 / NH; ++e) {
                                 uint4 *p = reinterpret_cast<uint4 *>(v0 + (e >> 3) * T::SPAN + (e & 7) * 16);
                                 uint4 w = keep ? *p : make_uint4(0u, 0u, 0u, 0u);
                                 const uint4 f = make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z),
@@ -626,6 +626,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 atomicCAS(a.status + 1, 0, bad_page ? SITE_TREE_BAD_PAGE : SITE_TREE_BAD_PARENT);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
             }
+            if (NH == 2 && mine) {  // the row's sum, of both halves
+                ms.trade[m & 1][h][kk] = l;
+                named_barrier_sync(pair, 64);
+                l += ms.trade[m & 1][h ^ 1][kk];
+                named_barrier_sync(pair, 64);  // both have read
+            }
             if (mine && *g.abort == 0) {
                 const bool whole = s.t0 == 0 && s.t1 == s.nt;
                 if (!bad && !is_node(node)) l = 0.f;  // a place without a node
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 float *part = a.part_o + prow * D;
                 // (code that runs once per item is kept small: fetching it costs more than running it)
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 32 * h; c < D; c += 32 * NH) {
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld32(t_o + c, o);
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         const __nv_bfloat16 *v =
                             a.v_cache + (((size_t)bt[i] * a.Hkv + s.kvh) * a.page_size + (key - i * a.page_size)) * D;
 #pragma unroll 1
-                        for (int c = 0; c < D; ++c) {
+                        for (int c = 32 * h; c < D; c = c % 32 == 31 ? c + 32 * NH - 31 : c + 1) {
                             const float f = __bfloat162float(v[c]);
                             if (fabsf(f) < INFINITY) continue;
                             if (whole) out[c] = __float2bfloat16(__bfloat162float(out[c]) + f);
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         }
                     }
                 }
-                if (kk < rows) {
+                if (kk < rows && h == 0) {
                     if (!whole) a.part_l[prow] = bad ? __uint_as_float(kBadPartial) : l2;
                     else if (!bad) a.lse[row] = l2 * kLn2;
                 }
@@ -762,7 +768,6 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.row_blocks = (a.R + T::RB - 1) / T::RB;
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
-    a.grouped = tree_grouped(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
     a.start = 1;
     a.o_aligned = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
@@ -807,8 +812,6 @@ int tree_box_rows(const TreeParams &p) {
     while (box < most && p.page_size % (2 * box) == 0) box *= 2;
     return box;
 }
-
-int tree_grouped(const TreeParams &p) { return p.page_size % 8 == 0 && p.d % 128 == 0; }
 
 int tree_query_box(const TreeParams &p) {
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
