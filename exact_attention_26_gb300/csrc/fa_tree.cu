@@ -88,6 +88,8 @@ struct TreeArgs {
     __nv_bfloat16 *o;
     float *lse;
     float *part_o, *part_l;         // [CTA][2][RB][d], [CTA][2][RB]
+    int4 *cuts;                     // [CTA]: the item that its range begins in the middle of: sequence,
+                                    // number within it, its first CTA, its CTAs (0: none)
     FastDiv by_page;
     int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
     int R, row_blocks;              // query rows per key/value head, items of RB of them
@@ -202,6 +204,16 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     Segment s{};
     auto rows_of = [&](const Segment &x) { return min(T::RB, a.R - x.rb * T::RB); };
     auto blocks_of = [&](const Segment &x) { return NB == 1 ? 1 : (rows_of(x) + 127) / 128; };
+
+    if (warp == kAuxWarp) {  // for the merge
+        int4 item = make_int4(walk.b, walk.item, 0, 0);
+        if (walk.left > 0 && walk.tile() > 0) {
+            const int first = cut.first((int)blockIdx.x) - walk.tile();
+            item.z = cut.owner(first);
+            item.w = cut.owner(first + walk.nt - 1) - item.z + 1;
+        }
+        if (lane == 0) a.cuts[blockIdx.x] = item;
+    }
 
     if (warp == kTmaWarp || warp == kTmaWarp + 1) {
         // ------------------------------------------------------------ K, or V
@@ -712,6 +724,67 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     }
 }
 
+// The items that were cut: L = log2 sum 2^(L_s), O = sum 2^(L_s - L) O_s.  Every cut lies where one of
+// the attention kernel's CTAs begins, and each cut of an item takes its share of the item's rows, so
+// an item of many parts has many CTAs to merge it.  A thread has four columns of a row, four parts
+// in flight.
+constexpr int kMergeThreads = 256, kMergeWorkers = 16;
+template <int D, int RB>
+__global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int PER = D / 4, ROWS = kMergeThreads / PER, U = 4;
+    const int at = threadIdx.x / PER, col = (threadIdx.x - at * PER) * 4;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int4 item = a.cuts[blockIdx.x];
+    if (item.w == 0 || at >= ROWS) return;
+    const int n = item.w, c0 = item.z;
+    const int kvh = item.y / a.row_blocks, rb = item.y - kvh * a.row_blocks;
+    const int worker = ((int)blockIdx.x - c0 - 1) * kMergeWorkers + blockIdx.y;
+    const int rows = min(RB, a.R - rb * RB);
+    const long long row0 = ((long long)item.x * a.Hkv + kvh) * a.R + (long long)rb * RB;
+    for (int r = worker * ROWS + at; r < rows; r += (n - 1) * kMergeWorkers * ROWS) {
+        float m = kUnseen, sum = 0.f, acc[4] = {};
+        bool bad = false;
+        for (int k0 = 0; k0 < n; k0 += U) {
+            float w[U];
+            float4 x[U];
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const int k = k0 + v;
+                const size_t pr = ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r;
+                w[v] = k < n ? __ldcg(a.part_l + pr) : -INFINITY;
+                x[v] = k < n ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D + col))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                bad = bad || __float_as_uint(w[v]) == kBadPartial;
+                top = fmaxf(top, w[v]);
+            }
+            const float f = ex2(m - top);
+            m = top;
+            sum *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] *= f;
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+                const float p = ex2(w[v] - top);
+                sum += p;
+                acc[0] = fmaf(p, x[v].x, acc[0]);
+                acc[1] = fmaf(p, x[v].y, acc[1]);
+                acc[2] = fmaf(p, x[v].z, acc[2]);
+                acc[3] = fmaf(p, x[v].w, acc[3]);
+            }
+        }
+        if (bad) continue;  // the sequence was rejected: nothing is written
+        const float inv = sum == 0.f ? 0.f : reciprocal(sum);
+        *reinterpret_cast<uint2 *>(a.o + (row0 + r) * D + col) =
+            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        if (col == 0) a.lse[row0 + r] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+    }
+}
+
 // Tiles of all items at the longest possible lengths.
 template <int D, int NB>
 long long tree_tiles(const TreeParams &p) {
@@ -733,7 +806,7 @@ template <int D, int NB>
 size_t tree_bytes(const TreeParams &p, size_t *l_offset) {
     const size_t rows = (size_t)tree_ctas<D, NB>(p) * 2 * TreeTile<D, NB>::RB;
     *l_offset = rows * D * sizeof(float);
-    return *l_offset + rows * sizeof(float) + 16;  // and room to begin on 32 bytes
+    return *l_offset + rows * sizeof(float) + tree_ctas<D, NB>(p) * sizeof(int4) + 16;  // and room to begin on 32 bytes
 }
 
 template <int D, int NB>
@@ -754,6 +827,7 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     char *const ws = static_cast<char *>(p.workspace) + (reinterpret_cast<uintptr_t>(p.workspace) % 32);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_l = reinterpret_cast<float *>(ws + l_offset);
+    a.cuts = reinterpret_cast<int4 *>(a.part_l + (size_t)tree_ctas<D, NB>(p) * 2 * T::RB);
     a.by_page = fast_div((uint32_t)p.page_size);
     a.B = p.B;
     a.H = p.H;
@@ -769,24 +843,23 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
-    a.start = 1;
+    a.start = 2;
     a.o_aligned = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
     auto kern = fa_tree_kernel<D, NB>;
-    constexpr int kSmem = (int)T::SMEM, kCols = (D + 31) / 32;
+    constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = tree_ctas<D, NB>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
-    // the merge that has fewer CTAs
+    // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs.
     const long long rows = (long long)p.B * p.H * p.Nq;
-    const int blocks = ((a.R < T::RB ? a.R : T::RB) + kCutRows - 1) / kCutRows;
-    if (rows <= (long long)n_cta * blocks)
-        return launch_dependent(fa_merge_row_kernel<kCols, T::RB, TreeArgs>, dim3((unsigned)rows), 32 * kRowWarps, 0,
-                                stream, 1, a, n_cta);
-    return launch_dependent(fa_merge_cut_kernel<kCols, T::RB, TreeArgs>, dim3((unsigned)n_cta, (unsigned)blocks),
-                            32 * kCutRows, 0, stream, 1, a, n_cta);
+    if (rows <= 16LL * n_cta)
+        return launch_dependent(fa_merge_row_kernel<(D + 31) / 32, T::RB, TreeArgs>, dim3((unsigned)rows),
+                                32 * kRowWarps, 0, stream, 1, a, n_cta);
+    return launch_dependent(fa_tree_merge_kernel<D, T::RB>, dim3((unsigned)n_cta, kMergeWorkers), kMergeThreads, 0,
+                            stream, 1, a);
 }
 
 // Calls f with the tile that serves the call: head dimension and blocks of 128 query rows.
