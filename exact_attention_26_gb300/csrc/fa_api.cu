@@ -1321,6 +1321,8 @@ extern "C" int fa_keep_path(void *const *caches, int n_caches, const int *block_
     for (int c = 0; c < n_caches; ++c) {
         if (!caches[c]) return FA_ERR_INVALID_ARG;
         if (!aligned16(caches[c])) return FA_ERR_MISALIGNED;
+        for (int e = 0; e < c; ++e)  // moved twice at once, a row would follow its own place
+            if (caches[e] == caches[c]) return FA_ERR_INVALID_ARG;
         k.cache[c] = caches[c];
     }
     if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(path) || !aligned4(count) || !aligned4(lens))

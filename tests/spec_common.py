@@ -68,12 +68,12 @@ def check_tree(o, lse, ref, what=""):
     assert np.array_equal(np.isnan(lse), np.isnan(rl)), f"{what}: NaN in L"
     some = np.isfinite(rl)
     bl = (es + 2.0 ** -20 * (1 + np.abs(rl)))[some]
-    el = np.abs(lse - rl)[some]
+    el = np.abs(lse[some] - rl[some])
     assert np.all(el <= bl), f"{what}: L off by {el.max():.3e}, worst ratio {(el / bl).max():.2f}"
     assert np.array_equal(np.isnan(o), np.isnan(ro)), f"{what}: NaN in O"
     inf = np.isinf(ro)
     assert np.array_equal(o[inf], ro[inf]) and np.all(np.isinf(o) == inf), f"{what}: infinities in O"
     fin = np.isfinite(ro)
-    bo = 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -16 + 2 * es[..., None]) * pv * (1 + 2.0 ** -8) + 1e-30
-    eo, bo = np.abs(o - ro)[fin], bo[fin]
+    bo = 2.0 ** -8 * np.abs(np.where(fin, ro, 0)) + (2.0 ** -8 + 2.0 ** -16 + 2 * es[..., None]) * pv * (1 + 2.0 ** -8) + 1e-30
+    eo, bo = np.abs(o[fin] - ro[fin]), bo[fin]
     assert np.all(eo <= bo), f"{what}: O off by {eo.max():.3e}, worst ratio {(eo / bo).max():.2f}"
