@@ -10,7 +10,8 @@
 // key/value head), row_blocks, start, seq_lens, o, lse, part_o [CTA][2][RB][d], part_l
 // [CTA][2][RB], and, found with it, tiles_of_len(a, len): the tiles of one item of a sequence
 // (0 where the length is bad), and empty_len(a, len): has it no key, so that its rows are the
-// merge's to write?
+// merge's to write?  RB, the rows of an item, is a constant of the kernel, or 0 where it is
+// a.item_rows.
 #pragma once
 
 #include "fa_internal.h"
@@ -254,13 +255,19 @@ template <int E>
 struct RowShared {
     float acc[kRowWarps][E * 32], sum[kRowWarps], max[kRowWarps];
 };
+template <int RB, typename Args>
+__device__ __forceinline__ int item_rows_of(const Args &a) {
+    if constexpr (RB > 0) return RB;
+    else return a.item_rows;
+}
 template <int E, int RB, typename Args>
 __device__ __forceinline__ void merge_row(const Args &a, RowShared<E> &sh, int c0, int r, int n, long long row) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
     float m, sum, acc[E];
     merge_part<E, 4>(
-        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r; }, warp, kRowWarps, n, m, sum,
+        a, [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * item_rows_of<RB>(a) + r; }, warp, kRowWarps, n,
+        m, sum,
         acc, bad);
 #pragma unroll
     for (int e = 0; e < E; ++e) sh.acc[warp][lane + 32 * e] = acc[e];
@@ -303,12 +310,12 @@ __global__ void __launch_bounds__(32 * kRowWarps)
         const Cut cut((count.tiles + start * count.full) * ipb, n_cta);
         if (nt > 0) {
             const int first = (count.tiles_before + start * count.full_before) * ipb +
-                              (kvh * a.row_blocks + r / RB) * (nt + start) + start;
+                              (kvh * a.row_blocks + r / item_rows_of<RB>(a)) * (nt + start) + start;
             c0 = cut.owner(first);
             n = cut.owner(first + nt - 1) - c0 + 1;
         }
         if (lane == 0) {
-            s_row = r % RB;
+            s_row = r % item_rows_of<RB>(a);
             s_c0 = c0;
             s_n = n > 1 || empty_len(a, a.seq_lens[b]) ? n : -1;  // -1: written directly, or rejected
         }

@@ -86,7 +86,7 @@ struct Left {
 
 struct VerifyShared {
     int parents[kMaxNodes], tokens[kMaxNodes], gone[kMaxNodes];
-    float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
+    float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes], gone_p[kMaxNodes];
     unsigned long long warp_sum[kVerifyWarps];
     unsigned long long cta_sum[2][8];  // of every CTA of the cluster, by turns
     int bad;
@@ -165,14 +165,15 @@ struct Weights {
             for (int e = 0; e < VEC; ++e)
                 if (i0 + e < 0) k1[e] = k2[e] = 0u;
         }
-        if (!DRAFT) {
-            for (int k = 0; k < l.n_gone; ++k) {
-                const int at = sh.gone[k] - i0;
-                if ((unsigned)at >= (unsigned)VEC) continue;
+    }
+    // without the tokens that are out
+    __device__ __forceinline__ void drop_gone(int i0, unsigned long long (&w)[VEC]) const {
+        for (int k = 0; k < l.n_gone; ++k) {
+            const int at = sh.gone[k] - i0;
+            if ((unsigned)at >= (unsigned)VEC) continue;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (e == at) k1[e] = k2[e] = 0u;
-            }
+            for (int e = 0; e < VEC; ++e)
+                if (e == at) w[e] = 0ull;
         }
     }
 };
@@ -263,19 +264,26 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                     }
                     break;
                 }
-                const double p = (double)sh.px[next], q = (double)sh.qx[next];
-                double w, drawn = 1.0;  // 1 - s of the definition
-                if (DRAFT) {
-                    w = fmax(p - a * q, 0.0);
-                    if (!v.replacement) drawn = fmax(1.0 - used, 0x1p-60);
-                } else {
-                    const int x = sh.tokens[next];
-                    bool gone = false;
-                    for (int k = 0; k < n_gone; ++k) gone = gone || sh.gone[k] == x;
-                    w = gone ? 0.0 : p;
-                }
                 j = next;
-                if ((double)sh.u[j] * q * total < w * drawn) {
+                const double p = (double)sh.px[j], u = (double)sh.u[j];
+                double w = p, q = 1.0, drawn = 1.0;  // drawn: 1 - s of the definition
+                bool accept;
+                if (DRAFT) {
+                    q = (double)sh.qx[j];
+                    if (a > 0.0) w = fmax(p - a * q, 0.0);
+                    if (v.replacement) {
+                        accept = u * q * total < w;
+                    } else {
+                        drawn = fmax(1.0 - used, 0x1p-60);
+                        accept = u * q * total < w * drawn;
+                    }
+                } else {
+                    bool gone = false;
+                    for (int k = lane; k < n_gone; k += 32) gone = gone || sh.gone[k] == sh.tokens[j];
+                    if (__any_sync(kFull, gone)) continue;  // its weight is 0
+                    accept = u * total < w;
+                }
+                if (accept) {
                     if (rank == 0 && lane == 0) {
                         path[count] = j;
                         fresh[count - 1] = sh.tokens[j];
@@ -290,7 +298,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                     used += q;
                     stale = true;
                 } else {
-                    if (lane == 0) sh.gone[n_gone] = sh.tokens[j];
+                    if (lane == 0) {
+                        sh.gone[n_gone] = sh.tokens[j];
+                        sh.gone_p[n_gone] = sh.px[j];
+                    }
                     __syncwarp();
                     ++n_gone;
                     total -= w;
@@ -306,12 +317,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
         const int per_warp = (units + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
         const int u0 = (rank * kVerifyWarps + warp) * per_warp, u1 = min(u0 + per_warp, units);
         unsigned long long sum = 0;
-        constexpr int kAhead = VEC == 4 ? 4 : 2;  // loads in flight
-        int i = u0 + lane;
-        for (; i + 32 * (kAhead - 1) < u1; i += 32 * kAhead) {
+        constexpr int kAhead = VEC == 4 || !DRAFT ? 4 : 2;  // loads in flight
+        for (int i = u0 + lane; i - lane < u1; i += 32 * kAhead) {
             typename Weights<P, DRAFT>::Raw raw[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) raw[k] = weights.load((i + 32 * k) * VEC - before);
+            for (int k = 0; k < kAhead; ++k)
+                raw[k] = weights.load(i + 32 * k < u1 ? (i + 32 * k) * VEC - before : V);  // from V on, zeros
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 uint32_t k1[VEC], k2[VEC], s1 = 0, s2 = 0;
@@ -321,11 +332,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                 sum += weight_of(s1, s2);
             }
         }
-        for (; i < u1; i += 32) {
-            uint32_t k1[VEC], k2[VEC];
-            weights.get(weights.load(i * VEC - before), i * VEC - before, k1, k2);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum += weight_of(k1[e], k2[e]);
+        if (!DRAFT) {  // the tokens that are out, of this warp's part
+            for (int k = lane; k < l.n_gone; k += 32) {
+                const int unit = (sh.gone[k] + before) / VEC;
+                uint32_t k1, k2;
+                weights.cut(sh.gone_p[k], 0.f, k1, k2);
+                if (unit >= u0 && unit < u1) sum -= weight_of(k1 - kBits1, k2 - kBits2);
+            }
         }
         sum = warp_sum(sum);
         if (lane == 0) sh.warp_sum[warp] = sum;
@@ -380,6 +393,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                 weights.get(weights.load(i0), i0, k1, k2);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) x[e] = weight_of(k1[e], k2[e]);
+                if (!DRAFT) weights.drop_gone(i0, x);
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) sum += x[e];
@@ -471,7 +485,9 @@ __global__ void __launch_bounds__(kKeepThreads) fa_keep_kernel(const __grid_cons
     const int group = lane / lanes, col = (lane - group * lanes) * 8;
     const int batch = kKeepInFlight * at_once;
     const int heads = k.n_caches * k.Hkv;             // (cache, head) units
-    const int per = m <= batch ? batch / m : 1;       // units of a batch
+    // units of a batch: as many as there is room for, and no more than make work for every warp
+    const int share = (heads + gridDim.x * kKeepWarps - 1) / (gridDim.x * kKeepWarps);
+    const int per = m <= batch ? min(batch / m, share) : 1;
     for (int h0 = (blockIdx.x * kKeepWarps + warp) * per; h0 < heads; h0 += gridDim.x * kKeepWarps * per) {
         const int n = min(per, heads - h0) * m;       // rows of these units
         for (int r0 = 0; r0 < n; r0 += batch) {
@@ -520,11 +536,10 @@ int launch_verify(const VerifyParams &v, cudaStream_t stream) {
 }
 
 int launch_keep(const KeepParams &k, cudaStream_t stream) {
-    // CTAs per sequence: about two waves of the GPU in all
+    // CTAs per sequence: one wave of the GPU in all, three to an SM
     const int heads = k.n_caches * k.Hkv, most = (heads + kKeepWarps - 1) / kKeepWarps;
-    const int want = (8 * k.num_sms + k.B - 1) / k.B;
-    return launch_dependent(fa_keep_kernel, dim3((unsigned)(want < most ? want : most), (unsigned)k.B), kKeepThreads, 0,
-                            stream, 1, k);
+    const int want = 3 * k.num_sms / k.B, n = want < 1 ? 1 : want < most ? want : most;
+    return launch_dependent(fa_keep_kernel, dim3((unsigned)n, (unsigned)k.B), kKeepThreads, 0, stream, 1, k);
 }
 
 }  // namespace fa

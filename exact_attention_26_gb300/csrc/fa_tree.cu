@@ -41,8 +41,12 @@ struct TreeTile {
     static constexpr int NH = NB == 1 ? 2 : 1;
     static constexpr int CB = BK / NH;                  // keys of a thread
     static constexpr int THREADS = 32 * 12;
+    // (Two blocks: their softmax threads hold a row of 128 scores, the other warps little, so warpgroups
+    // trade the launch's registers, 3 x 168, and every wait is inlined, as a called function has one
+    // budget: 127 -> 113 us.)
     static constexpr bool TRADE = NB == 2;
     static constexpr int REG_SOFTMAX = 216, REG_OTHERS = 72;
+    static_assert(2 * REG_SOFTMAX + REG_OTHERS <= 3 * 168, "registers of the launch");
     static constexpr uint32_t SPAN = BK * 128;
     static constexpr uint32_t SLOT = NCH * SPAN;
     static constexpr uint32_t Q_CHUNK = 128 * 128;
@@ -87,12 +91,12 @@ struct TreeArgs {
     const int *block_table, *seq_lens, *parents;
     __nv_bfloat16 *o;
     float *lse;
-    float *part_o, *part_l;         // [CTA][2][RB][d], [CTA][2][RB]
+    float *part_o, *part_l;         // [CTA][2][item_rows][d], [CTA][2][item_rows]
     int4 *cuts;                     // [CTA]: the item that its range begins in the middle of: sequence,
                                     // number within it, its first CTA, its CTAs (0: none)
     FastDiv by_page;
     int B, H, Hkv, Nq, Nt, d, page_size, max_pages, num_pages;
-    int R, row_blocks;              // query rows per key/value head, items of RB of them
+    int R, row_blocks, item_rows;   // query rows per key/value head, items of up to RB of them
     int box, box_q;                 // rows of a TMA box
     int tile_log2;
     int start;
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     Cut cut;
     Walk walk = start_walk(a, blockIdx.x, gridDim.x, &cut);
     Segment s{};
-    auto rows_of = [&](const Segment &x) { return min(T::RB, a.R - x.rb * T::RB); };
+    auto rows_of = [&](const Segment &x) { return min(a.item_rows, a.R - x.rb * a.item_rows); };
     auto blocks_of = [&](const Segment &x) { return NB == 1 ? 1 : (rows_of(x) + 127) / 128; };
 
     if (warp == kAuxWarp) {  // for the merge
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             if (lane == 0) {
                 const uint32_t fb = bar(ms.q_full[qb]);
                 mbar_arrive_expect_tx(fb, (uint32_t)(nb * NCH * a.box_q) * 128u);
-                const int row0 = (int)(((long long)s.b * a.Hkv + s.kvh) * a.R + (long long)s.rb * T::RB);
+                const int row0 = (int)(((long long)s.b * a.Hkv + s.kvh) * a.R + (long long)s.rb * a.item_rows);
                 for (int k = 0; k < nb; ++k)
                     for (int c = 0; c < NCH; ++c)
                         tma_load_3d(sQ + qb * T::Q_BYTES + k * T::Q_BLOCK + c * T::Q_CHUNK, &a.tm_q, fb, c * 64,
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         uint32_t seg = 0, m = 0, tiles = 0, units = 0;  // this block's units; the CTA's tiles and units
         while (walk.next(a, &s)) {
             const int ib = seg & 1, len = a.seq_lens[s.b], nb = blocks_of(s);
-            const int r0 = s.rb * T::RB + wg * 128, rows = min(128, a.R - r0);  // may be none
+            const int r0 = s.rb * a.item_rows + wg * 128, rows = min(128, rows_of(s) - wg * 128);  // may be none
             const bool mine = w4 * 32 < rows;                                   // this warp has rows
             const int node = a.Nt - a.Nq + (r0 + kk) % a.Nq;                    // this thread's row
             const int full_tiles = len >> (D == 256 ? 6 : 7);
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 const float inv = none ? 0.f : 1.f / l;
                 const float l2 = none ? -INFINITY : m_ref + lg2(l);  // base 2
                 const long long row = ((long long)s.b * a.Hkv + s.kvh) * a.R + r0 + kk;
-                const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * T::RB + wg * 128 + kk;
+                const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * a.item_rows + wg * 128 + kk;
                 const bool put = kk < rows && !bad;
                 const bool special = *(volatile int *)&ms.special_any[ib] != 0 && !none && !bad;
                 const int *bt = a.block_table + (size_t)s.b * a.max_pages;
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
 // an item of many parts has many CTAs to merge it.  A thread has four columns of a row, four parts
 // in flight.
 constexpr int kMergeThreads = 256, kMergeWorkers = 16;
-template <int D, int RB>
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int PER = D / 4, ROWS = kMergeThreads / PER, U = 4;
     const int at = threadIdx.x / PER, col = (threadIdx.x - at * PER) * 4;
@@ -740,8 +744,8 @@ __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __gr
     const int n = item.w, c0 = item.z;
     const int kvh = item.y / a.row_blocks, rb = item.y - kvh * a.row_blocks;
     const int worker = ((int)blockIdx.x - c0 - 1) * kMergeWorkers + blockIdx.y;
-    const int rows = min(RB, a.R - rb * RB);
-    const long long row0 = ((long long)item.x * a.Hkv + kvh) * a.R + (long long)rb * RB;
+    const int rows = min(a.item_rows, a.R - rb * a.item_rows);
+    const long long row0 = ((long long)item.x * a.Hkv + kvh) * a.R + (long long)rb * a.item_rows;
     for (int r = worker * ROWS + at; r < rows; r += (n - 1) * kMergeWorkers * ROWS) {
         float m = kUnseen, sum = 0.f, acc[4] = {};
         bool bad = false;
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __gr
 #pragma unroll
             for (int v = 0; v < U; ++v) {
                 const int k = k0 + v;
-                const size_t pr = ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * RB + r;
+                const size_t pr = ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * a.item_rows + r;
                 w[v] = k < n ? __ldcg(a.part_l + pr) : -INFINITY;
                 x[v] = k < n ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D + col))
                              : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -840,6 +844,9 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.num_pages = p.num_pages;
     a.R = p.H / p.Hkv * p.Nq;
     a.row_blocks = (a.R + T::RB - 1) / T::RB;
+    // items of one block share the rows evenly (what a part has to write goes by its rows: B5 Hkv2 R = 168
+    // d256 28.2 -> 26.1 us); of two blocks, the fewest blocks in all are best
+    a.item_rows = NB == 1 ? (a.R + a.row_blocks - 1) / a.row_blocks : T::RB;
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
@@ -855,10 +862,10 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs.
     const long long rows = (long long)p.B * p.H * p.Nq;
-    if (rows <= 16LL * n_cta)
-        return launch_dependent(fa_merge_row_kernel<(D + 31) / 32, T::RB, TreeArgs>, dim3((unsigned)rows),
+    if (rows * D <= 16LL * 128 * n_cta)
+        return launch_dependent(fa_merge_row_kernel<(D + 31) / 32, 0, TreeArgs>, dim3((unsigned)rows),
                                 32 * kRowWarps, 0, stream, 1, a, n_cta);
-    return launch_dependent(fa_tree_merge_kernel<D, T::RB>, dim3((unsigned)n_cta, kMergeWorkers), kMergeThreads, 0,
+    return launch_dependent(fa_tree_merge_kernel<D>, dim3((unsigned)n_cta, kMergeWorkers), kMergeThreads, 0,
                             stream, 1, a);
 }
 
