@@ -184,13 +184,36 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
     return x;
 }
 
-// 1 / x of 2^-60 .. 1 by Newton's iteration from fp32's 1 / x: 2^-23, 2^-46, 2^-53 (an fp64 divide is
-// a microsecond here)
-__device__ __forceinline__ double inverse(double x) {
-    if (x == 1.0) return 1.0;
-    double r = (double)__frcp_rn((float)x);
-    r = fma(r, fma(-x, r, 1.0), r);
-    return fma(r, fma(-x, r, 1.0), r);
+// The walk's numbers as sums of two floats, 2^-47 relative (Dekker's and Knuth's exact sums, and
+// products by FMA): fp64's chains of dependent operations, at a sixteenth of the rate, were 1.5 us
+// of each step.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair join(float a, float b) {  // |a| >= |b|
+    const float s = a + b;
+    return {s, b - (s - a)};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    const float s = a.hi + b.hi, v = s - a.hi;
+    return join(s, ((a.hi - (s - v)) + (b.hi - v)) + (a.lo + b.lo));
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    const float p = a.hi * b.hi;
+    return join(p, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, fmaf(a.hi, b.hi, -p))));
+}
+__device__ __forceinline__ bool operator<(Pair a, Pair b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ Pair pair_of(float x) { return {x, 0.f}; }
+// A sum of weights, in multiples of 2^-44.
+__device__ __forceinline__ Pair pair_of(unsigned long long sum) {
+    const float hi = __ull2float_rz(sum);
+    return {hi * 0x1p-44f, __ull2float_rn(sum - (unsigned long long)hi) * 0x1p-44f};
+}
+// 1 / x by Newton's iteration.
+__device__ __forceinline__ Pair inverse(Pair x) {
+    const Pair r = pair_of(__frcp_rn(x.hi)), one = pair_of(1.f);
+    return r + r * (one - x * r);
 }
 
 template <typename P, bool DRAFT>
@@ -241,7 +264,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
 
     // the walk's state, of warp 0
     int cur = 0, count = 1, j = 0;
-    double a = 0.0, used = 0.0, total = 1.0;  // of the draft's to take off; of the rejected; left
+    const Pair zero = pair_of(0.f), one = pair_of(1.f);
+    Pair a = zero, used = zero, total = one;  // of the draft's to take off; of the rejected; left
     int n_gone = 0;
     bool stale = false;                       // `total` is not known yet
     if (warp == 0 && rank == 0 && lane == 0) path[0] = 0;
@@ -258,30 +282,28 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                 }
                 if (next < 0 || stale) {
                     if (lane == 0) {
-                        const float hi = (float)a;
-                        const Left l{cur, hi, (float)(a - (double)hi), n_gone, count, next < 0};
+                        const Left l{cur, a.hi, a.lo, n_gone, count, next < 0};
                         sh.left = l;
                     }
                     break;
                 }
                 j = next;
-                const double p = (double)sh.px[j], u = (double)sh.u[j];
-                double w = p, q = 1.0, drawn = 1.0;  // drawn: 1 - s of the definition
+                const Pair p = pair_of(sh.px[j]), u = pair_of(sh.u[j]), q = pair_of(sh.qx[j]);
+                Pair drawn = one;  // 1 - s of the definition
                 bool accept;
                 if (DRAFT) {
-                    q = (double)sh.qx[j];
-                    if (a > 0.0) w = fmax(p - a * q, 0.0);
-                    if (v.replacement) {
-                        accept = u * q * total < w;
-                    } else {
-                        drawn = fmax(1.0 - used, 0x1p-60);
+                    const Pair w = p - a * q;
+                    accept = u * q * total < w;
+                    if (!v.replacement && used.hi > 0.f) {
+                        drawn = one - used;
+                        if (drawn.hi < 0x1p-60f) drawn = pair_of(0x1p-60f);
                         accept = u * q * total < w * drawn;
                     }
                 } else {
                     bool gone = false;
                     for (int k = lane; k < n_gone; k += 32) gone = gone || sh.gone[k] == sh.tokens[j];
                     if (__any_sync(kFull, gone)) continue;  // its weight is 0
-                    accept = u * total < w;
+                    accept = u * total < p;
                 }
                 if (accept) {
                     if (rank == 0 && lane == 0) {
@@ -290,12 +312,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                     }
                     cur = j;
                     ++count;
-                    a = used = 0.0;
-                    total = 1.0;
+                    a = used = zero;
+                    total = one;
                     n_gone = 0;
                 } else if (DRAFT) {
-                    a = fmin(a + total * inverse(drawn), 0x1p60);
-                    used += q;
+                    a = a + (drawn.hi == 1.f && drawn.lo == 0.f ? total : total * inverse(drawn));
+                    if (a.hi > 0x1p60f) a = pair_of(0x1p60f);
+                    used = used + q;
                     stale = true;
                 } else {
                     if (lane == 0) {
@@ -304,7 +327,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
                     }
                     __syncwarp();
                     ++n_gone;
-                    total -= w;
+                    total = total - p;
                 }
             }
         }
@@ -356,12 +379,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
         const unsigned long long mine = sh.cta_sum[turn][rank];
         turn ^= 1;
         if (!l.stop) {
-            total = (double)whole * 0x1p-44;
+            total = pair_of(whole);
             stale = false;
             continue;
         }
         if (whole == 0 && (l.a_hi > 0.f || l.n_gone)) {  // the drafts left nothing: the target's own
-            a = 0.0;
+            a = zero;
             n_gone = 0;
             stale = false;
             j = Nt;
