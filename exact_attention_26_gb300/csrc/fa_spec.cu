@@ -484,11 +484,12 @@ __global__ void __launch_bounds__(kKeepThreads) fa_keep_kernel(const __grid_cons
             const int node = path[i], before = i > 0 ? path[i - 1] : -1;
             bool bad = node <= before || node >= k.Nt;
             if (!bad && node != i) {
-                const long long from = (long long)len + node, to = (long long)len + i;
-                const int from_page = from < room ? bt[from / k.page_size] : -1, to_page = bt[to / k.page_size];
+                const uint32_t from = (uint32_t)(len + node), to = (uint32_t)(len + i), ps = (uint32_t)k.page_size;
+                const uint32_t fp = from / ps, tp = to / ps;
+                const int from_page = fp < (uint32_t)k.max_pages ? bt[fp] : -1, to_page = bt[tp];
                 bad = from_page < 0 || from_page >= k.num_pages || to_page < 0 || to_page >= k.num_pages;
-                s_src[i] = (long long)from_page * k.Hkv * k.page_size + from % k.page_size;
-                s_dst[i] = (long long)to_page * k.Hkv * k.page_size + to % k.page_size;
+                s_src[i] = (long long)from_page * k.Hkv * k.page_size + (from - fp * ps);
+                s_dst[i] = (long long)to_page * k.Hkv * k.page_size + (to - tp * ps);
             }
             if (bad) s_bad = 1;
             if (node == i) atomicMax(&s_n, i + 1);  // the leading rows stay
@@ -521,8 +522,8 @@ __global__ void __launch_bounds__(kKeepThreads) fa_keep_kernel(const __grid_cons
                 const int r = r0 + e * at_once + group;
                 to[e] = nullptr;
                 if (group < at_once && r < n) {
-                    const int unit = r / m, i = first + r - unit * m;
-                    const int c = (h0 + unit) / k.Hkv, h = h0 + unit - c * k.Hkv;
+                    const int unit = (int)((uint32_t)r / (uint32_t)m), i = first + r - unit * m;
+                    const int c = (int)((uint32_t)(h0 + unit) / (uint32_t)k.Hkv), h = h0 + unit - c * k.Hkv;
                     __nv_bfloat16 *cache = static_cast<__nv_bfloat16 *>(k.cache[c]);
                     const long long head = (long long)h * k.page_size;
                     to[e] = cache + (s_dst[i] + head) * k.d + col;
