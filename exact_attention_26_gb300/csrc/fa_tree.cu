@@ -12,11 +12,33 @@
 // P is rounded to bf16 (2^-8 at most of each term, the sum of the row is taken before that): V is
 // bf16, the product takes both of one type, and O is rounded to bf16 at the end all the same.
 //
-// Work is cut over the CTAs as fa_cut.cuh describes.  Warps: one softmax warpgroup per block of
-// rows (they also write the results), then one each for MMA issue and tensor memory, for the TMA
-// copies of K and V, and for the queries and the trees.  Per CTA: a ring of K_0 V_0 K_1 V_1 ...,
-// two S slots, one or two query buffers.  A *unit* is one block's work on one tile; units take the
-// S slots in turn.
+// Work is cut over the CTAs as fa_cut.cuh describes.  Warps: eight of softmax, which also write the
+// results, then one each for MMA issue and tensor memory, for the TMA copies of K and of V (issued one
+// by one, a hundred clocks each: with one warp for both, pages of 16 made that the bound, B1 131072
+// keys R = 256 139 us), and for the queries and the trees.  Per CTA: a ring of K_0 V_0 K_1 V_1 ..., two S
+// slots, one or two query buffers.  A *unit* is one block's work on one tile; units take the S slots in
+// turn.
+//
+// Measured (GB300, graph replay with the merge, caches larger than L2 but for the small ones):
+//   B32 H32 Hkv8 Nq32 of 1..8192 keys   104 us  5.5 TB/s  HBM: 3.1k clocks per tile, 2.9k at its rate
+//   B1 H32 Hkv8 Nq64 131072 keys        116 us  4.6 TB/s  the chain of one block's products: P to the next
+//                                                         S takes 2.1k clocks (1k of products that share
+//                                                         shared memory's 128 bytes a clock with the
+//                                                         copies), the softmax of 128 keys 1.6k, the other
+//                                                         block fills half of it
+//   B16 H64 Hkv8 Nq48 16384..32768      540 us  3.0 TB/s  the same; 1.15 PFLOP/s
+//   B8 H32 Hkv4 Nq4 d64 5000..32768      39 us  4.1 TB/s  32 rows lie in one quarter of tensor memory, so
+//                                                         one of four schedulers does a tile's softmax,
+//                                                         1.7k clocks
+//   B5 H16 Hkv2 Nq21 d256 101..2899      26 us            parts: 3 tiles per CTA, whose results are as
+//                                                         large as the keys and values that they read
+//   B1 H32 Hkv8 Nq16 1000 keys           11 us            latency of two launches: lengths, pages, first
+//                                                         copies, results, merge
+// Tried and slower: S slots of 64 keys, two per block (products of N = 64 and 128 in turn take twice
+// their time: 116 -> 197 us); a cluster of a CTA per block with the copies shared out and multicast (two
+// tiles in the ring are too few: 150 us); one product of 256 rows by a pair of CTAs, each with half of
+// K's rows and V's columns (330 us: its products take five times theirs, the reason was not found);
+// boxes of five dimensions that bring whole rows, half the copies (no difference).
 #include <type_traits>
 
 #include "fa_cut.cuh"

@@ -75,6 +75,13 @@ def test_ragged_trees(fa, seed):
     run(fa, [17, 0, 290, 64, 1000], 8, 4, 25, 25, 128, 16, seed, parents="ragged")
 
 
+def test_several_roots(fa):
+    """Trees of their own behind one sequence, and nodes without any tokens before them."""
+    par = torch.tensor([[-1, -1, 0, 1, -2, 1, -1, 6], [-2, -1, -1, 2, 3, -2, -2, 1], [-1] * 8], dtype=torch.int32)
+    run(fa, [200, 0, 127], 4, 2, 8, 8, 128, 16, 31, parents=par)
+    run(fa, [200, 0, 127], 4, 2, 8, 3, 64, 16, 32, parents=par)
+
+
 def test_long_sequence_is_cut(fa):
     run(fa, [20000], 4, 1, 16, 16, 64, 64, 1)
     run(fa, [9000, 3], 8, 1, 20, 20, 128, 16, 2, parents="ragged")
