@@ -461,9 +461,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const Veri
 // The moves overlap (row 3's place may be row 7's new one): new places are never behind old ones
 // and both ascend, so rows taken in order, each batch read before any of it is written, stay
 // what they were.
+//
+// Measured (GB300, graph replay): 64 sequences of 24 layers (48 cache tensors), Hkv8 d128, 192 rows that
+// move, 37.7 MB read and written: 10.2 us, behind a chain of lookups of about 3; one sequence 2.9 us.
+// Small CTAs of few registers, as many as an SM holds, hide the lookups best: 128 threads with 4 loads in
+// flight 10.2 us, 64 threads 10.7, 256 threads 10.8, with 8 loads in flight 11.9.
 
-constexpr int kKeepThreads = 256, kKeepWarps = kKeepThreads / 32;
-constexpr int kKeepInFlight = 8;  // 16-byte loads of a lane before the first store
+constexpr int kKeepThreads = 128, kKeepWarps = kKeepThreads / 32;
+constexpr int kKeepInFlight = 4;  // 16-byte loads of a lane before the first store
 
 __global__ void __launch_bounds__(kKeepThreads) fa_keep_kernel(const __grid_constant__ KeepParams k) {
     __shared__ long long s_src[kMaxNodes], s_dst[kMaxNodes];  // rows of the cache, of head 0
@@ -551,8 +556,8 @@ int launch_verify_t(const VerifyParams &v, int ctas, cudaStream_t stream) {
 int launch_verify(const VerifyParams &v, cudaStream_t stream) {
     // CTAs per sequence: more while each still has 32 KB of a node's rows, and all of them are no
     // more than two waves (a sequence of many sums, alone at the end, then has more of the GPU).
-    // With 1, 2, 4, 8: B1 V32000 fp32, two rows, 20, 16, 13, 10.4 us; B48 V50021 bf16, one row, 18.5,
-    // 14.2, 14.1, 17 us; B64 V128000 fp32, two rows, 129, 86, 66, 61 us.
+    // With 1, 2, 4, 8: B1 V32000 fp32, two rows, 15.9, 12.0, 9.4, 9.6 us; B48 V50021 bf16, one row, 11.2,
+    // 9.3, 9.3, 14.4 us; B64 V128000 fp32, two rows, 127, 76, 53, 47 us.
     const long long bytes = (long long)v.V * (v.bf16 ? 2 : 4) * (v.draft ? 2 : 1);
     int ctas = 1;
     while (ctas < 8 && (long long)v.B * ctas * 2 <= 4LL * v.num_sms && bytes / (ctas * 2) >= 30000) ctas *= 2;
@@ -560,9 +565,10 @@ int launch_verify(const VerifyParams &v, cudaStream_t stream) {
 }
 
 int launch_keep(const KeepParams &k, cudaStream_t stream) {
-    // CTAs per sequence: one wave of the GPU in all, three to an SM
+    // CTAs per sequence: all that the GPU holds at once, 16 to an SM (12, 16, 24 of them: 10.3, 10.2, 10.3
+    // us for the 64 sequences above)
     const int heads = k.n_caches * k.Hkv, most = (heads + kKeepWarps - 1) / kKeepWarps;
-    const int want = 3 * k.num_sms / k.B, n = want < 1 ? 1 : want < most ? want : most;
+    const int want = 16 * k.num_sms / k.B, n = want < 1 ? 1 : want < most ? want : most;
     return launch_dependent(fa_keep_kernel, dim3((unsigned)n, (unsigned)k.B), kKeepThreads, 0, stream, 1, k);
 }
 

@@ -866,12 +866,15 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.num_pages = p.num_pages;
     a.R = p.H / p.Hkv * p.Nq;
     a.row_blocks = (a.R + T::RB - 1) / T::RB;
-    // items of one block share the rows evenly (what a part has to write goes by its rows: B5 Hkv2 R = 168
-    // d256 28.2 -> 26.1 us); of two blocks, the fewest blocks in all are best
+    // items of one block share the rows evenly, so that none of a key/value head's is left for last (d256,
+    // pages of 48: B2 Hkv2 R = 144 of 233..700 keys 16.7 -> 15.1 us, B5 Hkv2 R = 136 of up to 2900 keys 22.3
+    // -> 21.8, R = 168 no difference); of two blocks, the fewest blocks in all are best
     a.item_rows = NB == 1 ? (a.R + a.row_blocks - 1) / a.row_blocks : T::RB;
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
+    // an item's start costs as much as two tiles (B32 Hkv8 R = 128 of 1..8192 keys, with 1, 2, 3: 110, 104.2,
+    // 105 us; a single item per CTA: no difference)
     a.start = 2;
     a.o_aligned = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
     a.scale_log2 = p.scale_log2;
@@ -882,7 +885,9 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
     const int n_cta = tree_ctas<D, NB>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
-    // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs.
+    // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs; many: the
+    // listed cuts only (a CTA per row against the list: 512 rows of one sequence 11.1 and 12.5 us, of four
+    // 14.0 and 18.4, 1680 rows of d256 29.0 and 26.1, 32768 of d128 170 and 104).
     const long long rows = (long long)p.B * p.H * p.Nq;
     if (rows * D <= 16LL * 128 * n_cta)
         return launch_dependent(fa_merge_row_kernel<(D + 31) / 32, 0, TreeArgs>, dim3((unsigned)rows),
@@ -891,7 +896,9 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
                             stream, 1, a);
 }
 
-// Calls f with the tile that serves the call: head dimension and blocks of 128 query rows.
+// Calls f with the tile that serves the call: head dimension and blocks of 128 query rows (two against
+// one, which copies the keys again for each block: B1 R = 256 of 131072 keys 116 and 175 us, B16 R = 384
+// of 16384..32768 keys 545 and 692).
 template <typename F>
 auto with_tile(const TreeParams &p, F f) {
     using std::integral_constant;
