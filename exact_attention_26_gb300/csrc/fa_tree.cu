@@ -51,17 +51,23 @@ namespace {
 constexpr float kMoveLog2 = 8.0f;
 constexpr int kMaxNodes = FA_MAX_TREE_NODES, kNodeWords = kMaxNodes / 32;
 
-template <int D, int NB>
+// NB: blocks of 128 rows in a CTA.  G: copies of the rows in the block of one, 128 / G apart.
+template <int D, int NB, int G>
 struct TreeTile {
     static constexpr int DP = (D + 63) / 64 * 64;       // row width in shared memory
     static constexpr int NCH = DP / 64;                 // 128-byte swizzle spans per row
     static constexpr int BK = D == 256 ? 64 : 128;      // keys per tile
-    static constexpr int RB = 128 * NB;                 // query rows per item
+    static constexpr int RB = 128 * NB / G;             // query rows per item
     // With one block, two softmax warpgroups, a thread for one half of the tile's keys each: the ring's V
     // slots are held for as long as a softmax takes (B32 R = 128 of 1..8192 keys: 120 -> 113 us).  With
     // two, a warpgroup for each (four: 115 -> 137 us, the MMA warp then issues late, and registers end).
     static constexpr int NH = NB == 1 ? 2 : 1;
-    static constexpr int CB = BK / NH;                  // keys of a thread
+    static constexpr int CB = BK / NH;                  // keys of a warpgroup
+    // Few rows (R <= 128 / G) would lie in some quarters of tensor memory only, which the same one or two
+    // of the SM's four schedulers reach.  With a copy of them in each quarter or half all have scores to
+    // work on, a thread those of KEYS keys; P then goes through shared memory, where any warp can write it.
+    static constexpr int KEYS = CB / G, W = KEYS < 32 ? KEYS : 32;
+    static_assert(G == 1 || (NB == 1 && CB == 64), "P's rows are two swizzle spans, one from each warpgroup");
     static constexpr int THREADS = 32 * 12;
     // (Two blocks: their softmax threads hold a row of 128 scores, the other warps little, so warpgroups
     // trade the launch's registers, 3 x 168, and every wait is inlined, as a called function has one
@@ -75,11 +81,14 @@ struct TreeTile {
     static constexpr uint32_t Q_BLOCK = NCH * Q_CHUNK;
     static constexpr uint32_t Q_BYTES = NB * Q_BLOCK;
     static constexpr int QBUF = Q_BYTES <= 32 * 1024 ? 2 : 1;
+    static constexpr uint32_t P_SPAN = G > 1 ? RB * 128 : 0, P_BYTES = 2 * P_SPAN;  // of a unit
     static constexpr uint32_t MISC = 24 * 1024;
-    static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - MISC - 1024) / SLOT) / 2 * 2;
+    static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - 2 * P_BYTES - MISC - 1024) / SLOT) / 2 * 2;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;    // 128 KB of keys and values
     static constexpr uint32_t OFF_Q = STAGES * SLOT;
-    static constexpr uint32_t OFF_MISC = OFF_Q + QBUF * Q_BYTES;
+    static constexpr uint32_t OFF_P = OFF_Q + QBUF * Q_BYTES;
+    static constexpr uint32_t OFF_MISC = OFF_P + 2 * P_BYTES;
+    static_assert(G == 1 || 128 * 128 - P_SPAN <= MISC, "the product reads 128 rows from each span of P's on");
     static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
     static constexpr uint32_t TM_O = 2 * BK;
     static constexpr uint32_t TM_USED = TM_O + NB * DP;
@@ -95,15 +104,16 @@ struct TreeMisc {
     // per block of rows, by its own units in turn: S is there, P is there, O is there.  (A warp may
     // come to wait for O of a unit before O of the last one is done, so these are two as well.)
     unsigned long long s_full[NB][2], p_full[NB][2], pv_done[NB][2];
-    unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done;
+    unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done[2];
     uint32_t tmem;
     int abort;
-    float trade[2][2][128];               // what the halves of a row tell each other, by turns
+    float trade[2][256];                  // what the threads of a row tell each other, by turns
     // per segment of this CTA's work, in turn:
     int bad_page[2], bad_tree[2];         // a page or a parent out of range
     int special_any[2];
     uint32_t special[2][kNodeWords];      // nodes whose values have infinities or NaN
-    uint32_t sees[2][kMaxNodes][kNodeWords];  // the nodes that a node sees, as bits
+    short up[kMaxNodes];                  // an ancestor, or -1
+    alignas(16) uint32_t sees[2][kMaxNodes][kNodeWords];  // the nodes that a node sees, as bits
 };
 
 struct TreeArgs {
@@ -152,6 +162,56 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
+// N = 2 or 4 steps of a product of 16 columns each, by one elected lane: as mma_ss_elect and
+// mma_ts_elect, with one election for all.  Steps lie STEP_A and STEP_B units of 16 bytes apart (A in
+// tensor memory: 8 columns); all but the first accumulate.
+template <int N, uint32_t STEP_A, uint32_t STEP_B>
+__device__ __forceinline__ void mma_ss_run(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    static_assert(N == 2 || N == 4, "steps of a run");
+    if constexpr (N == 4)
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %9, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %4, %9, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %9, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %9, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "l"(a + STEP_A), "l"(b + STEP_B), "l"(a + 2 * STEP_A), "l"(b + 2 * STEP_B),
+            "l"(a + 3 * STEP_A), "l"(b + 3 * STEP_B), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %4, %5, t;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "l"(a + STEP_A), "l"(b + STEP_B), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+template <int N, uint32_t STEP_B>
+__device__ __forceinline__ void mma_ts_run(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    static_assert(N == 2 || N == 4, "steps of a run");
+    if constexpr (N == 4)
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %9, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %4, %9, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %9, t;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %9, t;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(a + 8), "l"(b + STEP_B), "r"(a + 16), "l"(b + 2 * STEP_B), "r"(a + 24),
+            "l"(b + 3 * STEP_B), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %5, p;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %4, %5, t;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(a + 8), "l"(b + STEP_B), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
 // Of a pair of bf16 values, the bits of those that are infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     const uint32_t lo = (x & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
@@ -167,14 +227,15 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
                  : "memory");
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
+template <int D, int NB, int G>
+__global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ TreeArgs a) {
-    using T = TreeTile<D, NB>;
+    using T = TreeTile<D, NB, G>;
     constexpr int ST = T::STAGES, BK = T::BK, NH = T::NH, CB = T::CB, NCH = T::NCH, QBUF = T::QBUF;
+    constexpr int KEYS = T::KEYS, W = T::W;
     using Misc = TreeMisc<ST, NB>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
-    constexpr int kMmaWarp = 8, kTmaWarp = kMmaWarp + 1, kAuxWarp = kMmaWarp + 3;  // TMA: K, then V
+    constexpr int kMmaWarp = 8, kTmaWarp = kMmaWarp + 1, kMmaWarp2 = kMmaWarp + 3;  // TMA: K, then V
     constexpr bool kIn = T::TRADE;
     extern __shared__ uint8_t tree_smem[];
     const uint32_t raw = smem_u32(tree_smem);
@@ -201,7 +262,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             mbar_init(bar(ms.info_full[u]), 1);
             mbar_init(bar(ms.info_empty[u]), 8);
         }
-        mbar_init(bar(ms.done), 1);
+        for (int u = 0; u < 2; ++u) mbar_init(bar(ms.done[u]), 1);
         ms.abort = 0;
         fence_mbar_init();
     }
@@ -231,7 +292,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     auto rows_of = [&](const Segment &x) { return min(a.item_rows, a.R - x.rb * a.item_rows); };
     auto blocks_of = [&](const Segment &x) { return NB == 1 ? 1 : (rows_of(x) + 127) / 128; };
 
-    if (warp == kAuxWarp) {  // for the merge
+    if (warp == kMmaWarp2) {  // for the merge
         int4 item = make_int4(walk.b, walk.item, 0, 0);
         if (walk.left > 0 && walk.tile() > 0) {
             const int first = cut.first((int)blockIdx.x) - walk.tile();
@@ -241,6 +302,163 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
         if (lane == 0) a.cuts[blockIdx.x] = item;
     }
 
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t kIdescS = idesc_bf16_f32(128, BK, false, false);
+    constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+    constexpr int kRun = CB / 16 < 4 ? CB / 16 : 4;
+    const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
+    const uint64_t d_v = sdesc_sw128(base, T::SPAN, 1024), d_p = sdesc_sw128(base + T::OFF_P, 16, 1024);
+    struct Slot {  // a ring slot of K or V and the parity of its round
+        int at;
+        uint32_t round;
+        __device__ __forceinline__ void advance() {
+            at += 2;
+            if (at >= ST) at -= ST, round ^= 1;
+        }
+    };
+    auto product_s = [&](int qb, int blk, uint32_t at, int ring) {
+        tc_fence_after();
+        const uint64_t dq = desc_add(d_q, qb * T::Q_BYTES + blk * T::Q_BLOCK), dk = desc_add(d_k, ring * T::SLOT);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            mma_ss_run<4, 2, 2>(tmem + at * BK, desc_add(dq, c * T::Q_CHUNK), desc_add(dk, c * T::SPAN), kIdescS,
+                                c > 0 ? 1u : 0u);
+        if constexpr (D % 64 == 32)
+            mma_ss_run<2, 2, 2>(tmem + at * BK, desc_add(dq, D / 64 * T::Q_CHUNK), desc_add(dk, D / 64 * T::SPAN),
+                                kIdescS, 1u);
+    };
+    auto product_o = [&](int blk, uint32_t at, bool first, int ring) {
+        tc_fence_after();
+        const uint64_t dv = desc_add(d_v, ring * T::SLOT);
+#pragma unroll
+        for (int ks = 0; ks < BK / 16; ks += kRun) {
+            const uint64_t dvk = desc_add(dv, ks * 2048);
+            const uint32_t more = (!first || ks > 0) ? 1u : 0u;
+            if constexpr (G > 1)
+                mma_ss_run<kRun, 2, 128>(tmem + T::TM_O, desc_add(d_p, at * T::P_BYTES + (ks >> 2) * T::P_SPAN), dvk,
+                                         kIdescO, more);
+            else
+                mma_ts_run<kRun, 128>(tmem + T::TM_O + blk * T::DP,
+                                      tmem + at * BK + ks / (CB / 16) * CB + ks % (CB / 16) * 8, dvk, kIdescO, more);
+        }
+    };
+    // Waits until every MMA that this warp has issued has completed (normal or aborted run).
+    auto drain = [&](uint32_t done) {
+        tc_commit_elect(done);
+        volatile int never = 0;
+        const Guard g2{a.status, &never, kWaitLimitNs};
+        mbar_wait_warp<kIn>(done, 0, g2, SITE_DEC_DRAIN);
+    };
+
+    // ------------------------------------------------------ queries and trees
+    // The query rows of segment n, x; rows behind them in the last box are other heads', or zeros
+    // past the tensor, and what they give is dropped.
+    auto put_queries = [&](const Segment &x, uint32_t n) {
+        const int qb = (int)(n % QBUF), nb = blocks_of(x);
+        if (n >= (uint32_t)QBUF &&
+            !mbar_wait_warp<kIn>(bar(ms.q_empty[qb]), ((n / QBUF) - 1) & 1, g, SITE_DEC_EMPTY))
+            return false;
+        if (lane == 0) {
+            const uint32_t fb = bar(ms.q_full[qb]);
+            mbar_arrive_expect_tx(fb, (uint32_t)(nb * G * NCH * a.box_q) * 128u);
+            const int row0 = (int)(((long long)x.b * a.Hkv + x.kvh) * a.R + (long long)x.rb * a.item_rows);
+            for (int k = 0; k < nb * G; ++k)  // blocks, or copies
+                for (int c = 0; c < NCH; ++c)
+                    tma_load_3d(sQ + qb * T::Q_BYTES + (G > 1 ? k * T::RB * 128 : k * T::Q_BLOCK) + c * T::Q_CHUNK,
+                                &a.tm_q, fb, c * 64, G > 1 ? row0 : row0 + 128 * k, 0);
+        }
+        __syncwarp();
+        return true;
+    };
+    // After an abort: queries under way have to land before the CTA exits.
+    auto drain_queries = [&](uint32_t sent) {
+        if (!*g.abort) return;
+        volatile int never = 0;
+        const Guard g2{a.status, &never, kWaitLimitNs};
+        for (uint32_t i = sent > (uint32_t)QBUF ? sent - QBUF : 0; i < sent; ++i)
+            mbar_wait_warp<kIn>(bar(ms.q_full[i % QBUF]), (i / QBUF) & 1, g2, SITE_DEC_DRAIN);
+    };
+    // What a node sees, as bits: itself and, in rounds that double the reach, what the farthest ancestor
+    // that it has come to sees.  Lane i has nodes i, 32 + i, ...; a parent's number is below its child's,
+    // so from the last 32 nodes to the first each round reads what the one before it left.
+    auto put_tree = [&](const Segment &x, uint32_t n) {
+        const int ib = n & 1;
+        if (n >= 2 && !mbar_wait_warp<kIn>(bar(ms.info_empty[ib]), ((n >> 1) - 1) & 1, g, SITE_DEC_EMPTY))
+            return false;
+        if (lane < kNodeWords) ms.special[ib][lane] = 0;
+        bool bad = false;
+        if (a.parents) {
+            const int *parents = a.parents + (size_t)x.b * a.Nt;
+            const int groups = (a.Nt + 31) / 32;
+            bool any = false;
+            for (int k = 0; k < groups; ++k) {
+                const int j = 32 * k + lane;
+                int up = j < a.Nt ? parents[j] : -2;
+                const bool is = up >= -1;
+                if (up >= j || (up >= 0 && parents[up] < -1)) {
+                    bad = true;
+                    up = -1;
+                }
+                if (up < -1) up = -1;
+                any = any || up >= 0;
+                ms.up[j] = (short)up;
+#pragma unroll
+                for (int w = 0; w < kNodeWords; w += 4)
+                    *reinterpret_cast<uint4 *>(&ms.sees[ib][j][w]) = make_uint4(0u, 0u, 0u, 0u);
+                if (is) ms.sees[ib][j][k] = 1u << lane;
+            }
+            bad = __any_sync(kFull, bad);
+            __syncwarp();
+            while (__any_sync(kFull, any)) {
+                any = false;
+                for (int k = groups - 1; k >= 0; --k) {
+                    const int j = 32 * k + lane, up = ms.up[j];
+                    uint4 far[kNodeWords / 4] = {};
+                    int next = -1;
+                    if (up >= 0) {
+#pragma unroll
+                        for (int w = 0; w < kNodeWords / 4; ++w)
+                            far[w] = *reinterpret_cast<const uint4 *>(&ms.sees[ib][up][4 * w]);
+                        next = ms.up[up];
+                    }
+                    __syncwarp();
+                    if (up >= 0) {
+#pragma unroll
+                        for (int w = 0; w < kNodeWords / 4; ++w) {
+                            uint4 *to = reinterpret_cast<uint4 *>(&ms.sees[ib][j][4 * w]);
+                            const uint4 y = *to;
+                            *to = make_uint4(far[w].x | y.x, far[w].y | y.y, far[w].z | y.z, far[w].w | y.w);
+                        }
+                        ms.up[j] = (short)next;
+                        any = any || next >= 0;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) {
+            ms.bad_tree[ib] = bad;
+            ms.special_any[ib] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ms.info_full[ib]));
+        return true;
+    };
+    auto check_lengths = [&]() {
+        if (blockIdx.x != 0) return;
+        bool good = true;
+        for (int b = lane; b < a.B; b += 32) good = good && len_ok(a, a.seq_lens[b]);
+        if (!__all_sync(kFull, good) && lane == 0) {
+            atomicCAS(a.status + 1, 0, SITE_TREE_BAD_LEN);
+            atomicExch(a.status, FA_ERR_BAD_INDEX);
+        }
+    };
+
+    // One block: a warp for S = Q K^T, the queries and the trees, one for O += P V.  (A warp with all
+    // products takes 1.5k to 1.9k clocks to issue those of a tile, of waits, commits and descriptors: B32
+    // R = 128 of 1..8192 keys 104 -> 101.8 us, B4 R = 32 of d96 14.0 -> 11.9.)  Two blocks: all products
+    // in one order, from one warp, the other prepares.  (Products of the two kinds from two warps, by kind
+    // or by block, mix on their way, which slows both: B1 R = 256 of 131072 keys 115 -> 128 us.)
     if (warp == kTmaWarp || warp == kTmaWarp + 1) {
         // ------------------------------------------------------------ K, or V
         if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
@@ -318,52 +536,85 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             for (uint32_t i = n > (uint32_t)ST ? n - ST : is_v; i < n; i += 2)
                 mbar_wait_warp<kIn>(bar(ms.full[i % ST]), (i / ST) & 1, g2, SITE_DEC_DRAIN);
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
-        if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
-        if (blockIdx.x == 0) {
-            bool ok = true;
-            for (int b = lane; b < a.B; b += 32) ok = ok && len_ok(a, a.seq_lens[b]);
-            if (!__all_sync(kFull, ok) && lane == 0) {
-                atomicCAS(a.status + 1, 0, SITE_TREE_BAD_LEN);
-                atomicExch(a.status, FA_ERR_BAD_INDEX);
+    } else if (NB == 1 && warp == kMmaWarp) {
+        // -------------------------------------- issuer of S = Q K^T, queries and trees
+        uint32_t seg = 0, unit = 0, sent = 0;
+        bool ok = true;
+        Slot k_slot{0, 0};
+        Segment sa{};  // one ahead, whose queries come while there is room for them
+        bool more = walk.next(a, &sa);
+        auto put_next = [&]() {
+            if (!ok || !more) return;
+            ok = put_queries(sa, sent);
+            sent += ok;
+        };
+        put_next();
+        for (; ok && more; ++seg) {
+            s = sa;
+            more = walk.next(a, &sa);
+            const int qb = (int)(seg % QBUF);
+            if (QBUF == 2) put_next();
+            if (seg == 0) ok = ok && put_tree(s, 0);  // while the first copies are under way; later ones behind the first S
+            ok = ok && mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
+#pragma unroll 1
+            for (int t = s.t0; ok && t < s.t1; ++t, ++unit) {
+                ok = mbar_wait_warp<kIn>(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
+                // the slot of S is free behind the product with V of the tile before the last
+                if (ok && unit >= 2)
+                    ok = mbar_wait_warp<kIn>(bar(ms.pv_done[0][unit & 1]), ((unit - 2) >> 1) & 1, g, SITE_DEC_MMA);
+                if (!ok) break;
+                product_s(qb, 0, unit & 1, k_slot.at);
+                tc_commit_elect(bar(ms.s_full[0][unit & 1]));
+                tc_commit_elect(bar(ms.empty[k_slot.at]));
+                k_slot.advance();
+                if (t == s.t0 && seg > 0) ok = put_tree(s, seg);
+            }
+            tc_commit_elect(bar(ms.q_empty[qb]));
+            if (QBUF == 1) put_next();
+        }
+        drain_queries(sent);
+        drain(bar(ms.done[0]));
+    } else if (NB == 1 && warp == kMmaWarp2) {
+        // ------------------------------------------------------------ issuer of O += P V
+        check_lengths();
+        uint32_t unit = 0;
+        bool ok = true;
+        Slot v_slot{1, 0};
+        while (ok && walk.next(a, &s)) {
+#pragma unroll 1
+            for (int t = s.t0; ok && t < s.t1; ++t, ++unit) {
+                ok = mbar_wait_warp<kIn>(bar(ms.p_full[0][unit & 1]), (unit >> 1) & 1, g, SITE_DEC_MMA) &&
+                     mbar_wait_warp<kIn>(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
+                if (!ok) break;
+                product_o(0, unit & 1, t == s.t0, v_slot.at);
+                tc_commit_elect(bar(ms.pv_done[0][unit & 1]));
+                tc_commit_elect(bar(ms.empty[v_slot.at]));
+                v_slot.advance();
             }
         }
-        constexpr uint32_t kIdescS = idesc_bf16_f32(128, BK, false, false);
-        constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+        drain(bar(ms.done[1]));
+    } else if (NB == 2 && warp == kMmaWarp) {
+        // ------------------------------------------------------------ issuer of all products
+        if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
+        check_lengths();
+        uint32_t seg = 0;
+        bool ok = true;
+        Slot k_slot{0, 0}, v_slot{1, 0};
         Walk ahead = walk;   // segments of S, up to two units ahead of O
         Segment sa{};
         bool more = ahead.next(a, &sa);
         int ta = sa.t0, ba = 0, nba = more ? blocks_of(sa) : 0;
-        uint32_t js = 0, jp = 0, seg = 0;              // units whose S, O is issued; segments of S begun
+        uint32_t js = 0, jp = 0;                       // units whose S, O is issued
         uint32_t cs[NB] = {}, cp[NB] = {};             // the same per block
-        bool ok = true;
-        struct Slot {  // a ring slot of K or V and the parity of its round
-            int at;
-            uint32_t round;
-            __device__ __forceinline__ void advance() {
-                at += 2;
-                if (at >= ST) at -= ST, round ^= 1;
-            }
-        };
-        Slot k_slot{0, 0}, v_slot{1, 0};
-        const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
-        const uint64_t d_v = sdesc_sw128(base, T::SPAN, 1024);
-        auto issue_s = [&]() {
+        auto issue_s = [&](bool here) {  // here: its operands have been seen to be
             const int qb = (int)(seg % QBUF);
-            if (ta == sa.t0 && ba == 0)
+            if (!here && ta == sa.t0 && ba == 0)
                 ok = mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
-            if (ok && ba == 0)
+            if (!here && ok && ba == 0)
                 ok = mbar_wait_warp<kIn>(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
             if (!ok) return;
-            tc_fence_after();
-            const uint64_t dq = desc_add(d_q, qb * T::Q_BYTES + ba * T::Q_BLOCK);
-            const uint64_t dk = desc_add(d_k, k_slot.at * T::SLOT);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss_elect(tmem + (js & 1) * BK, desc_add(dq, (ks >> 2) * T::Q_CHUNK + (ks & 3) * 32),
-                             desc_add(dk, (ks >> 2) * T::SPAN + (ks & 3) * 32), kIdescS, ks > 0 ? 1u : 0u);
-            const uint32_t m = NB == 2 && ba == 1 ? cs[NB - 1]++ : cs[0]++;
+            product_s(qb, ba, js & 1, k_slot.at);
+            const uint32_t m = ba == 1 ? cs[NB - 1]++ : cs[0]++;
             tc_commit_elect(bar(ms.s_full[ba][m & 1]));
             ++js;
             if (++ba < nba) return;
@@ -388,24 +639,19 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             const int nb = blocks_of(s);
             for (int t = s.t0; ok && t < s.t1; ++t)
                 for (int blk = 0; ok && blk < nb; ++blk, ++jp) {
-                    const uint32_t m = NB == 2 && blk == 1 ? cp[NB - 1]++ : cp[0]++;
+                    const uint32_t m = blk == 1 ? cp[NB - 1]++ : cp[0]++;
                     const uint32_t pb = bar(ms.p_full[blk][m & 1]), pp = (m >> 1) & 1;
-                    while (ok && more && js == jp) issue_s();
+                    while (ok && more && js == jp) issue_s(false);
                     // whichever comes first, the next S's operands or this unit's P
                     for (int k = 0; ok && more && js == jp + 1 && k < 4096; ++k) {
-                        if (ready()) issue_s();
+                        if (ready()) issue_s(true);
                         else if (__all_sync(kFull, mbar_try_wait_sleep(pb, pp, 200u))) break;
                     }
                     ok = ok && mbar_wait_warp<kIn>(pb, pp, g, SITE_DEC_MMA);
                     if (ok && blk == 0)
                         ok = mbar_wait_warp<kIn>(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
                     if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dv = desc_add(d_v, v_slot.at * T::SLOT);
-#pragma unroll
-                    for (int ks = 0; ks < BK / 16; ++ks)
-                        mma_ts_elect(tmem + T::TM_O + blk * T::DP, tmem + (jp & 1) * BK + ks / (CB / 16) * CB + ks % (CB / 16) * 8,
-                                     desc_add(dv, ks * 2048), kIdescO, (t > s.t0 || ks > 0) ? 1u : 0u);
+                    product_o(blk, jp & 1, t == s.t0, v_slot.at);
                     tc_commit_elect(bar(ms.pv_done[blk][m & 1]));
                     if (blk + 1 == nb) {
                         tc_commit_elect(bar(ms.empty[v_slot.at]));
@@ -413,92 +659,34 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     }
                 }
         }
-        // fires once every MMA issued above has completed (normal or aborted run)
-        tc_commit_elect(bar(ms.done));
-        volatile int never = 0;
-        const Guard g2{a.status, &never, kWaitLimitNs};
-        mbar_wait_warp<kIn>(bar(ms.done), 0, g2, SITE_DEC_DRAIN);
-    } else if (warp == kAuxWarp) {
-        // ------------------------------------------------------ queries and trees
+        drain(bar(ms.done[0]));
+    } else if (NB == 2 && warp == kMmaWarp2) {
+        // ------------------------------------------------------------ queries and trees
         if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
-        uint32_t seg = 0, q_sent = 0;
+        uint32_t sent = 0;
         bool ok = true;
-        // the segment's query rows; rows behind them in the last box are other heads', or zeros
-        // past the tensor, and what they give is dropped
-        auto put_queries = [&]() {
-            const int qb = (int)(seg % QBUF), nb = blocks_of(s);
-            if (seg >= (uint32_t)QBUF)
-                ok = mbar_wait_warp<kIn>(bar(ms.q_empty[qb]), ((seg / QBUF) - 1) & 1, g, SITE_DEC_EMPTY);
-            if (!ok) return;
-            if (lane == 0) {
-                const uint32_t fb = bar(ms.q_full[qb]);
-                mbar_arrive_expect_tx(fb, (uint32_t)(nb * NCH * a.box_q) * 128u);
-                const int row0 = (int)(((long long)s.b * a.Hkv + s.kvh) * a.R + (long long)s.rb * a.item_rows);
-                for (int k = 0; k < nb; ++k)
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(sQ + qb * T::Q_BYTES + k * T::Q_BLOCK + c * T::Q_CHUNK, &a.tm_q, fb, c * 64,
-                                    row0 + 128 * k, 0);
+        for (uint32_t seg = 0; ok && walk.next(a, &s); ++seg) {
+            if (QBUF == 2 || seg == 0) {
+                ok = put_queries(s, seg);
+                sent += ok;
             }
-            __syncwarp();
-            ++q_sent;
-        };
-        for (; ok && walk.next(a, &s); ++seg) {
-            const int ib = seg & 1;
-            const bool first = QBUF == 2 || seg == 0;
-            if (first) put_queries();
-            if (ok && seg >= 2)
-                ok = mbar_wait_warp<kIn>(bar(ms.info_empty[ib]), ((seg >> 1) - 1) & 1, g, SITE_DEC_EMPTY);
-            if (!ok) break;
-            if (lane < kNodeWords) ms.special[ib][lane] = 0;
-            bool bad = false;
-            if (a.parents) {
-                const int *parents = a.parents + (size_t)s.b * a.Nt;
-                int p[kNodeWords];
-#pragma unroll
-                for (int k = 0; k < kNodeWords; ++k) {
-                    const int j = 32 * k + lane;
-                    p[k] = j < a.Nt ? parents[j] : -2;
-                    if (p[k] >= j || (p[k] >= 0 && parents[p[k]] < -1)) {
-                        bad = true;
-                        p[k] = -1;
-                    }
-                }
-                bad = __any_sync(kFull, bad);
-                // node by node in order: what the parent sees, and itself; lane w has word w
-#pragma unroll
-                for (int k = 0; k < kNodeWords; ++k) {
-                    const int n = min(32, a.Nt - 32 * k);
-                    for (int i = 0; i < n; ++i) {
-                        const int up = __shfl_sync(kFull, p[k], i);
-                        if (lane < kNodeWords) {
-                            uint32_t w = up >= 0 ? ms.sees[ib][up][lane] : 0u;
-                            if (lane == k && up >= -1) w |= 1u << i;
-                            ms.sees[ib][32 * k + i][lane] = w;
-                        }
-                    }
-                }
+            ok = ok && put_tree(s, seg);
+            if (ok && QBUF == 1 && seg > 0) {
+                ok = put_queries(s, seg);
+                sent += ok;
             }
-            if (lane == 0) {
-                ms.bad_tree[ib] = bad;
-                ms.special_any[ib] = 0;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(ms.info_full[ib]));
-            if (!first) put_queries();
         }
-        if (*g.abort) {
-            volatile int never = 0;
-            const Guard g2{a.status, &never, kWaitLimitNs};
-            for (uint32_t i = q_sent > (uint32_t)QBUF ? q_sent - QBUF : 0; i < q_sent; ++i)
-                mbar_wait_warp<kIn>(bar(ms.q_full[i % QBUF]), (i / QBUF) & 1, g2, SITE_DEC_DRAIN);
-        }
+        drain_queries(sent);
     } else {
         // ------------------------------------------------------------ softmax, results
         if constexpr (T::TRADE) setmaxnreg_inc<T::REG_SOFTMAX>();
         // Every warp runs every step even after a wait has given up (waits then return soon).
         const int wg = NH == 1 ? warp >> 2 : 0, h = NH == 1 ? 0 : warp >> 2, w4 = warp & 3;  // block of rows, half of the keys
         const int kk = threadIdx.x & 127;  // row of the block; lane of S and O; key of a tile's V
-        const int pair = 1 + w4;           // barrier of the two warps that share 32 rows
+        const int row_warp = w4 % (4 / G), copy = w4 / (4 / G), rr = kk % (128 / G);  // its scores' row
+        const int col = h * CB + copy * KEYS;  // and first key
+        const int team = 1 + row_warp, team_threads = 32 * NH * G;  // barrier of the warps that share 32 rows
+        const int turn = (h * G + copy) * (128 / G) + rr;  // this thread's place in what they tell each other
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const uint32_t t_o = tmem + lane_base + T::TM_O + wg * T::DP;
         const float c_s = a.scale_log2;
@@ -507,7 +695,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             const int ib = seg & 1, len = a.seq_lens[s.b], nb = blocks_of(s);
             const int r0 = s.rb * a.item_rows + wg * 128, rows = min(128, rows_of(s) - wg * 128);  // may be none
             const bool mine = w4 * 32 < rows;                                   // this warp has rows
-            const int node = a.Nt - a.Nq + (r0 + kk) % a.Nq;                    // this thread's row
+            const bool scores = row_warp * 32 < rows;                           // or a copy of some
+            const int node = a.Nt - a.Nq + (r0 + rr) % a.Nq;                    // this thread's row
             const int full_tiles = len >> (D == 256 ? 6 : 7);
             bool informed = false;
             auto inform = [&]() {
@@ -531,41 +720,46 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                     if (partly) inform();
                     mbar_wait_warp<kIn>(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
                     tc_fence_after();
-                    if (mine) {
-                        const uint32_t unit = units + (uint32_t)((t - s.t0) * nb + wg);
-                        const uint32_t t_s = tmem + lane_base + (unit & 1) * BK + h * CB;
-                        uint32_t sr[CB / 32][32];
+                    if (scores) {
+                        const uint32_t at = (units + (uint32_t)((t - s.t0) * nb + wg)) & 1;  // slot of S
+                        const uint32_t t_s = tmem + lane_base + at * BK + col;
+                        uint32_t sr[KEYS / W][W];
 #pragma unroll
-                        for (int c = 0; c < CB / 32; ++c) tmem_ld32(t_s + c * 32, sr[c]);
+                        for (int c = 0; c < KEYS / W; ++c) {
+                            if constexpr (W == 32) tmem_ld32(t_s + c * 32, sr[c]);
+                            else tmem_ld16(t_s, sr[c]);
+                        }
 #pragma unroll
-                        for (int c = 0; c < CB / 32; ++c) tmem_wait_ld(sr[c]);
-                        float x[CB];
+                        for (int c = 0; c < KEYS / W; ++c) tmem_wait_ld(sr[c]);
+                        float x[KEYS];
 #pragma unroll
-                        for (int c = 0; c < CB / 32; ++c)
+                        for (int c = 0; c < KEYS / W; ++c)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(sr[c][e]);
+                            for (int e = 0; e < W; ++e) x[c * W + e] = __uint_as_float(sr[c][e]);
                         if (partly) {
-                            const int n0 = t * BK + h * CB - len;  // node of the first key, or below 0
+                            const int n0 = t * BK + col - len;  // node of the first key, or below 0
 #pragma unroll
-                            for (int c = 0; c < CB / 32; ++c) {
-                                const int at = (n0 + 32 * c) >> 5, sh = (n0 + 32 * c) & 31;
+                            for (int c = 0; c < KEYS / W; ++c) {
+                                const int at = (n0 + W * c) >> 5, sh = (n0 + W * c) & 31;
                                 const uint32_t w = __funnelshift_r(sees(node, at), sees(node, at + 1), sh);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(w >> e & 1u)) x[c * 32 + e] = -INFINITY;
+                                for (int e = 0; e < W; ++e)
+                                    if (!(w >> e & 1u)) x[c * W + e] = -INFINITY;
                             }
                         }
                         float mp0 = -INFINITY, mp1 = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < CB; c += 4) {
+                        for (int c = 0; c < KEYS; c += 4) {
                             mp0 = fmax3(mp0, x[c], x[c + 1]);
                             mp1 = fmax3(mp1, x[c + 2], x[c + 3]);
                         }
                         float top = fmaxf(mp0, mp1);
-                        if constexpr (NH == 2) {  // of both halves, which then take the same steps
-                            ms.trade[m & 1][h][kk] = top;
-                            named_barrier_sync(pair, 64);
-                            top = fmaxf(top, ms.trade[m & 1][h ^ 1][kk]);
+                        if constexpr (NH * G > 1) {  // of all of the row, whose threads then take the same steps
+                            ms.trade[m & 1][turn] = top;
+                            named_barrier_sync(team, team_threads);
+#pragma unroll
+                            for (int k = 1; k < NH * G; ++k)
+                                top = fmaxf(top, ms.trade[m & 1][(turn + k * (128 / G)) % (128 * NH)]);
                         }
                         top *= c_s;
                         float alpha = 1.f;
@@ -577,15 +771,23 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         float sp0 = 0.f, sp1 = 0.f;
                         const uint64_t c2 = f32x2_splat(c_s), nm2 = f32x2_splat(-m_ref);
 #pragma unroll
-                        for (int c = 0; c < CB; c += 2) {
+                        for (int c = 0; c < KEYS; c += 2) {
                             fma_f32x2(x[c], x[c + 1], c2, nm2);
                             x[c] = ex2(x[c]);
                             x[c + 1] = ex2(x[c + 1]);
                             add_f32x2(sp0, sp1, x[c], x[c + 1]);
                         }
                         l = l * alpha + (sp0 + sp1);
-                        // P as bf16 pairs over the first half of the thread's own columns
-                        if constexpr (CB >= 64) {
+                        if constexpr (G > 1) {
+                            // P as an operand of 128-byte rows, 16-byte chunks turned by the row
+                            uint8_t *p = gbase + T::OFF_P + at * T::P_BYTES + h * T::P_SPAN + rr * 128;
+#pragma unroll
+                            for (int e = 0; e < KEYS; e += 8)
+                                *reinterpret_cast<uint4 *>(p + ((copy * (KEYS / 8) + e / 8) ^ (rr & 7)) * 16) =
+                                    make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
+                                               pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
+                            fence_proxy_async_smem();
+                        } else if constexpr (CB >= 64) {  // as bf16 pairs over the first half of the thread's own columns
 #pragma unroll
                             for (int c = 0; c < CB / 64; ++c) {
                                 uint32_t pk[32];
@@ -599,7 +801,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                             for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
                             tmem_st16(t_s, pk);
                         }
-                        if (t > s.t0 && __any_sync(kFull, move)) {
+                        if (mine && t > s.t0 && __any_sync(kFull, move)) {
                             // O <- alpha O once the product before is complete
                             mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
                             tc_fence_after();
@@ -664,11 +866,13 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 atomicCAS(a.status + 1, 0, bad_page ? SITE_TREE_BAD_PAGE : SITE_TREE_BAD_PARENT);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
             }
-            if (NH == 2 && mine) {  // the row's sum, of both halves
-                ms.trade[m & 1][h][kk] = l;
-                named_barrier_sync(pair, 64);
-                l += ms.trade[m & 1][h ^ 1][kk];
-                named_barrier_sync(pair, 64);  // both have read
+            if (NH * G > 1 && scores) {  // the row's sum, of all its threads
+                ms.trade[m & 1][turn] = l;
+                named_barrier_sync(team, team_threads);
+                l = 0.f;
+#pragma unroll
+                for (int k = 0; k < NH * G; ++k) l += ms.trade[m & 1][k * (128 / G) + rr];  // each in the same order
+                named_barrier_sync(team, team_threads);  // all have read
             }
             if (mine && *g.abort == 0) {
                 const bool whole = s.t0 == 0 && s.t1 == s.nt;
@@ -812,9 +1016,9 @@ __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __gr
 }
 
 // Tiles of all items at the longest possible lengths.
-template <int D, int NB>
+template <int D, int NB, int G>
 long long tree_tiles(const TreeParams &p) {
-    using T = TreeTile<D, NB>;
+    using T = TreeTile<D, NB, G>;
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
     const long long nt = ((long long)p.page_size * p.max_pages + p.Nt + T::BK - 1) / T::BK;
     const long long items = (long long)p.B * p.Hkv * ((R + T::RB - 1) / T::RB);
@@ -822,22 +1026,22 @@ long long tree_tiles(const TreeParams &p) {
 }
 
 // CTAs of a launch: one per SM, or the largest number of tiles there can be.
-template <int D, int NB>
+template <int D, int NB, int G>
 int tree_ctas(const TreeParams &p) {
-    const long long n = tree_tiles<D, NB>(p);
+    const long long n = tree_tiles<D, NB, G>(p);
     return n < p.num_sms ? (int)n : p.num_sms;
 }
 
-template <int D, int NB>
+template <int D, int NB, int G>
 size_t tree_bytes(const TreeParams &p, size_t *l_offset) {
-    const size_t rows = (size_t)tree_ctas<D, NB>(p) * 2 * TreeTile<D, NB>::RB;
+    const size_t ctas = tree_ctas<D, NB, G>(p), rows = ctas * 2 * TreeTile<D, NB, G>::RB;
     *l_offset = rows * D * sizeof(float);
-    return *l_offset + rows * sizeof(float) + tree_ctas<D, NB>(p) * sizeof(int4) + 16;  // and room to begin on 32 bytes
+    return *l_offset + rows * sizeof(float) + ctas * sizeof(int4) + 16;  // and room to begin on 32 bytes
 }
 
-template <int D, int NB>
+template <int D, int NB, int G>
 int launch_t(const TreeParams &p, cudaStream_t stream) {
-    using T = TreeTile<D, NB>;
+    using T = TreeTile<D, NB, G>;
     TreeArgs a{};
     a.tm_q = p.tm_q;
     a.tm_k = p.tm_k;
@@ -849,11 +1053,11 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.lse = p.lse;
     size_t l_offset;
-    tree_bytes<D, NB>(p, &l_offset);
+    tree_bytes<D, NB, G>(p, &l_offset);
     char *const ws = static_cast<char *>(p.workspace) + (reinterpret_cast<uintptr_t>(p.workspace) % 32);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_l = reinterpret_cast<float *>(ws + l_offset);
-    a.cuts = reinterpret_cast<int4 *>(a.part_l + (size_t)tree_ctas<D, NB>(p) * 2 * T::RB);
+    a.cuts = reinterpret_cast<int4 *>(a.part_l + (size_t)tree_ctas<D, NB, G>(p) * 2 * T::RB);
     a.by_page = fast_div((uint32_t)p.page_size);
     a.B = p.B;
     a.H = p.H;
@@ -880,10 +1084,10 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
-    auto kern = fa_tree_kernel<D, NB>;
+    auto kern = fa_tree_kernel<D, NB, G>;
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
-    const int n_cta = tree_ctas<D, NB>(p);
+    const int n_cta = tree_ctas<D, NB, G>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs; many: the
     // listed cuts only (a CTA per row against the list: 512 rows of one sequence 11.1 and 12.5 us, of four
@@ -902,14 +1106,24 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
 template <typename F>
 auto with_tile(const TreeParams &p, F f) {
     using std::integral_constant;
-    const bool two = (long long)(p.H / p.Hkv) * p.Nq > 128;
+    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
     using One = integral_constant<int, 1>;
     using Two = integral_constant<int, 2>;
+    using Four = integral_constant<int, 4>;
     switch (p.d) {
-        case 64: return two ? f(integral_constant<int, 64>(), Two()) : f(integral_constant<int, 64>(), One());
-        case 96: return two ? f(integral_constant<int, 96>(), Two()) : f(integral_constant<int, 96>(), One());
-        case 128: return two ? f(integral_constant<int, 128>(), Two()) : f(integral_constant<int, 128>(), One());
-        default: return f(integral_constant<int, 256>(), One());  // O of a second block has no room
+        case 64: {
+            const integral_constant<int, 64> d;
+            return R <= 32 ? f(d, One(), Four()) : R <= 64 ? f(d, One(), Two()) : R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
+        }
+        case 96: {
+            const integral_constant<int, 96> d;
+            return R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
+        }
+        case 128: {
+            const integral_constant<int, 128> d;
+            return R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
+        }
+        default: return f(integral_constant<int, 256>(), One(), One());  // O of a second block has no room
     }
 }
 
@@ -928,19 +1142,21 @@ int tree_query_box(const TreeParams &p) {
 }
 
 long long tree_max_tiles(const TreeParams &p) {
-    return with_tile(p, [&](auto d, auto nb) { return tree_tiles<decltype(d)::value, decltype(nb)::value>(p); });
+    return with_tile(p, [&](auto d, auto nb, auto g) {
+        return tree_tiles<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p);
+    });
 }
 
 size_t tree_workspace_bytes(const TreeParams &p) {
-    return with_tile(p, [&](auto d, auto nb) {
+    return with_tile(p, [&](auto d, auto nb, auto g) {
         size_t l_offset;
-        return tree_bytes<decltype(d)::value, decltype(nb)::value>(p, &l_offset);
+        return tree_bytes<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p, &l_offset);
     });
 }
 
 int launch_tree(const TreeParams &p, cudaStream_t stream) {
-    return with_tile(p, [&](auto d, auto nb) {
-        return launch_t<decltype(d)::value, decltype(nb)::value>(p, stream);
+    return with_tile(p, [&](auto d, auto nb, auto g) {
+        return launch_t<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p, stream);
     });
 }
 
