@@ -147,17 +147,6 @@ __device__ __forceinline__ int tiles_of_len(const TreeArgs &a, int len) {
 // A sequence always has its nodes' tiles, so attention writes its rows.
 __device__ __forceinline__ bool empty_len(const TreeArgs &, int) { return false; }
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -597,67 +586,75 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
         // ------------------------------------------------------------ issuer of all products
         if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
         check_lengths();
-        uint32_t seg = 0;
+        // A fixed order: a block's P V, S of its next tile, then the same of the other block.
+        uint32_t m0 = 0, m1 = 0;  // tiles of each block
         bool ok = true;
         Slot k_slot{0, 0}, v_slot{1, 0};
-        Walk ahead = walk;   // segments of S, up to two units ahead of O
-        Segment sa{};
-        bool more = ahead.next(a, &sa);
-        int ta = sa.t0, ba = 0, nba = more ? blocks_of(sa) : 0;
-        uint32_t js = 0, jp = 0;                       // units whose S, O is issued
-        uint32_t cs[NB] = {}, cp[NB] = {};             // the same per block
-        auto issue_s = [&](bool here) {  // here: its operands have been seen to be
+        auto here = [&](const Slot &slot) {
+            return mbar_wait_warp<kIn>(bar(ms.full[slot.at]), slot.round, g, SITE_DEC_FULL);
+        };
+        auto have_p = [&](int blk, uint32_t m) {
+            return mbar_wait_warp<kIn>(bar(ms.p_full[blk][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+        };
+        for (uint32_t seg = 0; ok && walk.next(a, &s); ++seg) {
             const int qb = (int)(seg % QBUF);
-            if (!here && ta == sa.t0 && ba == 0)
-                ok = mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
-            if (!here && ok && ba == 0)
-                ok = mbar_wait_warp<kIn>(bar(ms.full[k_slot.at]), k_slot.round, g, SITE_DEC_FULL);
-            if (!ok) return;
-            product_s(qb, ba, js & 1, k_slot.at);
-            const uint32_t m = ba == 1 ? cs[NB - 1]++ : cs[0]++;
-            tc_commit_elect(bar(ms.s_full[ba][m & 1]));
-            ++js;
-            if (++ba < nba) return;
-            ba = 0;
-            tc_commit_elect(bar(ms.empty[k_slot.at]));
-            k_slot.advance();
-            if (++ta == sa.t1) {
-                tc_commit_elect(bar(ms.q_empty[qb]));
-                ++seg;
-                more = ahead.next(a, &sa);
-                ta = sa.t0;
-                nba = blocks_of(sa);
-            }
-        };
-        // S of what has not arrived is not waited for while the O before it can be issued
-        auto ready = [&]() {
-            bool r = ba > 0 || mbar_test(bar(ms.full[k_slot.at]), k_slot.round);
-            if (ta == sa.t0 && ba == 0) r = r && mbar_test(bar(ms.q_full[seg % QBUF]), (seg / QBUF) & 1);
-            return __all_sync(kFull, r);
-        };
-        while (ok && walk.next(a, &s)) {
-            const int nb = blocks_of(s);
-            for (int t = s.t0; ok && t < s.t1; ++t)
-                for (int blk = 0; ok && blk < nb; ++blk, ++jp) {
-                    const uint32_t m = blk == 1 ? cp[NB - 1]++ : cp[0]++;
-                    const uint32_t pb = bar(ms.p_full[blk][m & 1]), pp = (m >> 1) & 1;
-                    while (ok && more && js == jp) issue_s(false);
-                    // whichever comes first, the next S's operands or this unit's P
-                    for (int k = 0; ok && more && js == jp + 1 && k < 4096; ++k) {
-                        if (ready()) issue_s(true);
-                        else if (__all_sync(kFull, mbar_try_wait_sleep(pb, pp, 200u))) break;
-                    }
-                    ok = ok && mbar_wait_warp<kIn>(pb, pp, g, SITE_DEC_MMA);
-                    if (ok && blk == 0)
-                        ok = mbar_wait_warp<kIn>(bar(ms.full[v_slot.at]), v_slot.round, g, SITE_DEC_FULL);
+            ok = mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA) && here(k_slot);
+            if (!ok) break;
+            if (blocks_of(s) == 2) {  // a slot of S for each
+                product_s(qb, 0, 0, k_slot.at);
+                tc_commit_elect(bar(ms.s_full[0][m0 & 1]));
+                product_s(qb, 1, 1, k_slot.at);
+                tc_commit_elect(bar(ms.s_full[NB - 1][m1 & 1]));
+                tc_commit_elect(bar(ms.empty[k_slot.at]));
+                k_slot.advance();
+#pragma unroll 1
+                for (int t = s.t0; t < s.t1; ++t, ++m0, ++m1) {
+                    const bool next = t + 1 < s.t1;
+                    ok = have_p(0, m0) && here(v_slot);
                     if (!ok) break;
-                    product_o(blk, jp & 1, t == s.t0, v_slot.at);
-                    tc_commit_elect(bar(ms.pv_done[blk][m & 1]));
-                    if (blk + 1 == nb) {
-                        tc_commit_elect(bar(ms.empty[v_slot.at]));
-                        v_slot.advance();
+                    product_o(0, 0, t == s.t0, v_slot.at);
+                    tc_commit_elect(bar(ms.pv_done[0][m0 & 1]));
+                    if (next) {
+                        ok = here(k_slot);
+                        if (!ok) break;
+                        product_s(qb, 0, 0, k_slot.at);
+                        tc_commit_elect(bar(ms.s_full[0][(m0 + 1) & 1]));
                     }
+                    ok = have_p(NB - 1, m1);
+                    if (!ok) break;
+                    product_o(1, 1, t == s.t0, v_slot.at);
+                    tc_commit_elect(bar(ms.pv_done[NB - 1][m1 & 1]));
+                    if (next) {
+                        product_s(qb, 1, 1, k_slot.at);
+                        tc_commit_elect(bar(ms.s_full[NB - 1][(m1 + 1) & 1]));
+                        tc_commit_elect(bar(ms.empty[k_slot.at]));
+                        k_slot.advance();
+                    }
+                    tc_commit_elect(bar(ms.empty[v_slot.at]));
+                    v_slot.advance();
                 }
+            } else {  // both slots in turn, S a tile ahead
+                int ts = s.t0;
+#pragma unroll 1
+                for (int t = s.t0; t < s.t1; ++t, ++m0) {
+#pragma unroll 1
+                    for (; ts < s.t1 && ts < t + 2; ++ts) {
+                        ok = here(k_slot);
+                        if (!ok) break;
+                        product_s(qb, 0, (ts - s.t0) & 1, k_slot.at);
+                        tc_commit_elect(bar(ms.s_full[0][(m0 + (uint32_t)(ts - t)) & 1]));
+                        tc_commit_elect(bar(ms.empty[k_slot.at]));
+                        k_slot.advance();
+                    }
+                    ok = ok && have_p(0, m0) && here(v_slot);
+                    if (!ok) break;
+                    product_o(0, (t - s.t0) & 1, t == s.t0, v_slot.at);
+                    tc_commit_elect(bar(ms.pv_done[0][m0 & 1]));
+                    tc_commit_elect(bar(ms.empty[v_slot.at]));
+                    v_slot.advance();
+                }
+            }
+            tc_commit_elect(bar(ms.q_empty[qb]));
         }
         drain(bar(ms.done[0]));
     } else if (NB == 2 && warp == kMmaWarp2) {
@@ -690,7 +687,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const uint32_t t_o = tmem + lane_base + T::TM_O + wg * T::DP;
         const float c_s = a.scale_log2;
-        uint32_t seg = 0, m = 0, tiles = 0, units = 0;  // this block's units; the CTA's tiles and units
+        uint32_t seg = 0, m = 0, tiles = 0;  // this block's tiles; the CTA's
         while (walk.next(a, &s)) {
             const int ib = seg & 1, len = a.seq_lens[s.b], nb = blocks_of(s);
             const int r0 = s.rb * a.item_rows + wg * 128, rows = min(128, rows_of(s) - wg * 128);  // may be none
@@ -721,7 +718,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                     mbar_wait_warp<kIn>(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
                     tc_fence_after();
                     if (scores) {
-                        const uint32_t at = (units + (uint32_t)((t - s.t0) * nb + wg)) & 1;  // slot of S
+                        const uint32_t at = NB == 1 ? m & 1 : nb == 2 ? wg : (t - s.t0) & 1;  // slot of S
                         const uint32_t t_s = tmem + lane_base + at * BK + col;
                         uint32_t sr[KEYS / W][W];
 #pragma unroll
@@ -940,7 +937,6 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ms.info_empty[ib]));
             tiles += (uint32_t)(s.t1 - s.t0);
-            units += (uint32_t)((s.t1 - s.t0) * nb);
             ++seg;
         }
     }
