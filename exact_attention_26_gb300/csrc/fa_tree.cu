@@ -103,7 +103,7 @@ struct TreeMisc {
     unsigned long long full[STAGES], empty[STAGES];
     // per block of rows, by its own units in turn: S is there, P is there, O is there.  (A warp may
     // come to wait for O of a unit before O of the last one is done, so these are two as well.)
-    unsigned long long s_full[NB][2], p_full[NB][2], pv_done[NB][2];
+    unsigned long long s_full[NB][2], p_half[NB][2], p_full[NB][2], pv_done[NB][2];
     unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done[2];
     uint32_t tmem;
     int abort;
@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             for (int k = 0; k < NB; ++k) {
                 mbar_init(bar(ms.s_full[k][u]), 1);
                 mbar_init(bar(ms.p_full[k][u]), 4 * NH);  // one arrival per softmax warp
+                mbar_init(bar(ms.p_half[k][u]), 4);       // two blocks: P of the first half of the keys
                 mbar_init(bar(ms.pv_done[k][u]), 1);
             }
             mbar_init(bar(ms.q_full[u]), 1);
@@ -316,11 +317,11 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             mma_ss_run<2, 2, 2>(tmem + at * BK, desc_add(dq, D / 64 * T::Q_CHUNK), desc_add(dk, D / 64 * T::SPAN),
                                 kIdescS, 1u);
     };
-    auto product_o = [&](int blk, uint32_t at, bool first, int ring) {
+    auto product_o = [&](int blk, uint32_t at, bool first, int ring, int from = 0, int to = T::BK / 16) {
         tc_fence_after();
         const uint64_t dv = desc_add(d_v, ring * T::SLOT);
 #pragma unroll
-        for (int ks = 0; ks < BK / 16; ks += kRun) {
+        for (int ks = from; ks < to; ks += kRun) {
             const uint64_t dvk = desc_add(dv, ks * 2048);
             const uint32_t more = (!first || ks > 0) ? 1u : 0u;
             if constexpr (G > 1)
@@ -593,6 +594,9 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
         auto here = [&](const Slot &slot) {
             return mbar_wait_warp<kIn>(bar(ms.full[slot.at]), slot.round, g, SITE_DEC_FULL);
         };
+        auto have_half = [&](int blk, uint32_t m) {
+            return mbar_wait_warp<kIn>(bar(ms.p_half[blk][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
+        };
         auto have_p = [&](int blk, uint32_t m) {
             return mbar_wait_warp<kIn>(bar(ms.p_full[blk][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
         };
@@ -610,9 +614,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
 #pragma unroll 1
                 for (int t = s.t0; t < s.t1; ++t, ++m0, ++m1) {
                     const bool next = t + 1 < s.t1;
-                    ok = have_p(0, m0) && here(v_slot);
+                    ok = have_half(0, m0) && here(v_slot);
                     if (!ok) break;
-                    product_o(0, 0, t == s.t0, v_slot.at);
+                    product_o(0, 0, t == s.t0, v_slot.at, 0, BK / 32);
+                    ok = have_p(0, m0);
+                    if (!ok) break;
+                    product_o(0, 0, false, v_slot.at, BK / 32, BK / 16);
                     tc_commit_elect(bar(ms.pv_done[0][m0 & 1]));
                     if (next) {
                         ok = here(k_slot);
@@ -620,9 +627,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                         product_s(qb, 0, 0, k_slot.at);
                         tc_commit_elect(bar(ms.s_full[0][(m0 + 1) & 1]));
                     }
+                    ok = have_half(NB - 1, m1);
+                    if (!ok) break;
+                    product_o(1, 1, t == s.t0, v_slot.at, 0, BK / 32);
                     ok = have_p(NB - 1, m1);
                     if (!ok) break;
-                    product_o(1, 1, t == s.t0, v_slot.at);
+                    product_o(1, 1, false, v_slot.at, BK / 32, BK / 16);
                     tc_commit_elect(bar(ms.pv_done[NB - 1][m1 & 1]));
                     if (next) {
                         product_s(qb, 1, 1, k_slot.at);
@@ -765,14 +775,61 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                             alpha = ex2(m_ref - top);
                             m_ref = top;
                         }
+                        auto rescale = [&]() {
+                            if (mine && t > s.t0 && __any_sync(kFull, move)) {
+                                // O <- alpha O once the product before is complete
+                                mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
+                                tc_fence_after();
+                                const uint64_t a2 = f32x2_splat(alpha);
+    #pragma unroll 1
+                                for (int c = h; c < D / 32; c += NH) {
+                                    uint32_t o[32];
+                                    tmem_ld32(t_o + c * 32, o);
+                                    tmem_wait_ld(o);
+    #pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        float x0 = __uint_as_float(o[e]), x1 = __uint_as_float(o[e + 1]);
+                                        mul_f32x2(x0, x1, a2);
+                                        o[e] = __float_as_uint(x0);
+                                        o[e + 1] = __float_as_uint(x1);
+                                    }
+                                    tmem_st32(t_o + c * 32, o);
+                                }
+                            }
+                        };
+                        if constexpr (NB == 2) rescale();
                         float sp0 = 0.f, sp1 = 0.f;
                         const uint64_t c2 = f32x2_splat(c_s), nm2 = f32x2_splat(-m_ref);
+                        auto exponentials = [&](int from, int to) {
 #pragma unroll
-                        for (int c = 0; c < KEYS; c += 2) {
-                            fma_f32x2(x[c], x[c + 1], c2, nm2);
-                            x[c] = ex2(x[c]);
-                            x[c + 1] = ex2(x[c + 1]);
-                            add_f32x2(sp0, sp1, x[c], x[c + 1]);
+                            for (int c = from; c < to; c += 2) {
+                                fma_f32x2(x[c], x[c + 1], c2, nm2);
+                                x[c] = ex2(x[c]);
+                                x[c + 1] = ex2(x[c + 1]);
+                                add_f32x2(sp0, sp1, x[c], x[c + 1]);
+                            }
+                        };
+                        auto put_p = [&](int c) {  // as bf16 pairs over the first half of the thread's own columns
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]);
+                            tmem_st32(t_s + c * 32, pk);
+                        };
+                        if constexpr (NB == 2) {
+                            // the product with V begins on the first half of the keys while the second's
+                            // exponentials are taken
+                            exponentials(0, KEYS / 2);
+                            put_p(0);
+                            tmem_wait_st();
+                            if (!partly) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(ms.p_half[wg][m & 1]));
+                            }
+                            exponentials(KEYS / 2, KEYS);
+                            put_p(1);
+                        } else {
+                            exponentials(0, KEYS);
                         }
                         l = l * alpha + (sp0 + sp1);
                         if constexpr (G > 1) {
@@ -784,40 +841,15 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                                     make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
                                                pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
                             fence_proxy_async_smem();
-                        } else if constexpr (CB >= 64) {  // as bf16 pairs over the first half of the thread's own columns
-#pragma unroll
-                            for (int c = 0; c < CB / 64; ++c) {
-                                uint32_t pk[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(x[64 * c + 2 * e], x[64 * c + 2 * e + 1]);
-                                tmem_st32(t_s + c * 32, pk);
-                            }
-                        } else {
+                        } else if constexpr (CB == 64) {
+                            put_p(0);
+                        } else if constexpr (CB == 32) {
                             uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
                             tmem_st16(t_s, pk);
                         }
-                        if (mine && t > s.t0 && __any_sync(kFull, move)) {
-                            // O <- alpha O once the product before is complete
-                            mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
-                            tc_fence_after();
-                            const uint64_t a2 = f32x2_splat(alpha);
-#pragma unroll 1
-                            for (int c = h; c < D / 32; c += NH) {
-                                uint32_t o[32];
-                                tmem_ld32(t_o + c * 32, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    float x0 = __uint_as_float(o[e]), x1 = __uint_as_float(o[e + 1]);
-                                    mul_f32x2(x0, x1, a2);
-                                    o[e] = __float_as_uint(x0);
-                                    o[e + 1] = __float_as_uint(x1);
-                                }
-                                tmem_st32(t_o + c * 32, o);
-                            }
-                        }
+                        if constexpr (NB == 1) rescale();
                         tmem_wait_st();
                     }
                     if (wg == 0 && partly && kk < BK) {
@@ -850,6 +882,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                     }
                     __syncwarp();
                     tc_fence_before();
+                    if (NB == 2 && lane == 0 && (partly || !scores)) mbar_arrive(bar(ms.p_half[wg][m & 1]));
                     if (lane == 0) mbar_arrive(bar(ms.p_full[wg][m & 1]));
                 }
             }
