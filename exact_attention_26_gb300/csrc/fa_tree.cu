@@ -12,33 +12,32 @@
 // P is rounded to bf16 (2^-8 at most of each term, the sum of the row is taken before that): V is
 // bf16, the product takes both of one type, and O is rounded to bf16 at the end all the same.
 //
-// Work is cut over the CTAs as fa_cut.cuh describes.  Warps: eight of softmax, which also write the
-// results, then one each for MMA issue and tensor memory, for the TMA copies of K and of V (issued one
-// by one, a hundred clocks each: with one warp for both, pages of 16 made that the bound, B1 131072
-// keys R = 256 139 us), and for the queries and the trees.  Per CTA: a ring of K_0 V_0 K_1 V_1 ..., two S
-// slots, one or two query buffers.  A *unit* is one block's work on one tile; units take the S slots in
-// turn.
+// Work is cut over the CTAs as fa_cut.cuh describes.  Twelve warps: eight of softmax, which also write
+// the results, two that issue products, one of which also brings the queries and makes the trees (which,
+// below), and one each for the TMA copies of K and of V (issued one by one, a hundred clocks each: with one
+// warp for both, pages of 16 made that the bound, B1 131072 keys R = 256 139 us).  Per CTA: a ring of
+// K_0 V_0 K_1 V_1 ..., two S slots, one or two query buffers.
 //
 // Measured (GB300, graph replay with the merge, caches larger than L2 but for the small ones):
-//   B32 H32 Hkv8 Nq32 of 1..8192 keys   104 us  5.5 TB/s  HBM: 3.1k clocks per tile, 2.9k at its rate
-//   B1 H32 Hkv8 Nq64 131072 keys        116 us  4.6 TB/s  the chain of one block's products: P to the next
-//                                                         S takes 2.1k clocks (1k of products that share
-//                                                         shared memory's 128 bytes a clock with the
-//                                                         copies), the softmax of 128 keys 1.6k, the other
-//                                                         block fills half of it
-//   B16 H64 Hkv8 Nq48 16384..32768      540 us  3.0 TB/s  the same; 1.15 PFLOP/s
-//   B8 H32 Hkv4 Nq4 d64 5000..32768      39 us  4.1 TB/s  32 rows lie in one quarter of tensor memory, so
-//                                                         one of four schedulers does a tile's softmax,
-//                                                         1.7k clocks
-//   B5 H16 Hkv2 Nq21 d256 101..2899      26 us            parts: 3 tiles per CTA, whose results are as
+//   B32 H32 Hkv8 Nq32 of 1..8192 keys   101 us  5.6 TB/s  HBM between the items; 4 to 8k clocks for the
+//                                                         results at the end of each, 10k to the first S
+//   B1 H32 Hkv8 Nq64 131072 keys        111 us  4.9 TB/s  3.1k clocks a tile: the chain of one block, 1.5k
+//                                                         of softmax, 0.3k to P's being seen, 1.3k of P V
+//                                                         and the next S, and the other block's turns
+//   B16 H64 Hkv8 Nq48 16384..32768      524 us  3.1 TB/s  the same; 1.18 PFLOP/s
+//   B8 H32 Hkv4 Nq4 d64 5000..32768      36 us  4.4 TB/s  1.5k clocks a tile, of which HBM's rate needs
+//                                                         1.4k, 9k to the first S, results, merge
+//   B5 H16 Hkv2 Nq21 d256 101..2899      24 us            parts: 3 tiles per CTA, whose results are as
 //                                                         large as the keys and values that they read
-//   B1 H32 Hkv8 Nq16 1000 keys           11 us            latency of two launches: lengths, pages, first
+//   B1 H32 Hkv8 Nq16 1000 keys           10 us            latency of two launches: lengths, pages, first
 //                                                         copies, results, merge
-// Tried and slower: S slots of 64 keys, two per block (products of N = 64 and 128 in turn take twice
-// their time: 116 -> 197 us); a cluster of a CTA per block with the copies shared out and multicast (two
-// tiles in the ring are too few: 150 us); one product of 256 rows by a pair of CTAs, each with half of
-// K's rows and V's columns (330 us: its products take five times theirs, the reason was not found);
-// boxes of five dimensions that bring whole rows, half the copies (no difference).
+// Tried and slower: S slots of 64 keys, two per block (116 -> 197 us); a cluster of a CTA per block with
+// the copies shared out and multicast (two tiles in the ring are too few: 150 us); one product of 256 rows
+// by a pair of CTAs, each with half of K's rows and V's columns (330 us, the reason was not found); boxes of
+// five dimensions that bring whole rows, half the copies (no difference); for up to 64 rows of d64 copies of
+// them in every quarter of tensor memory, so that all warps share their softmax, P through shared memory
+// (no difference with a warp for S and one for P V; a single short sequence 0.3 us slower); a round of the
+// results' code before the first tile, to have it fetched (no difference in replay).
 #include <type_traits>
 
 #include "fa_cut.cuh"
@@ -51,23 +50,17 @@ namespace {
 constexpr float kMoveLog2 = 8.0f;
 constexpr int kMaxNodes = FA_MAX_TREE_NODES, kNodeWords = kMaxNodes / 32;
 
-// NB: blocks of 128 rows in a CTA.  G: copies of the rows in the block of one, 128 / G apart.
-template <int D, int NB, int G>
+template <int D, int NB>  // NB: blocks of 128 rows in a CTA
 struct TreeTile {
     static constexpr int DP = (D + 63) / 64 * 64;       // row width in shared memory
     static constexpr int NCH = DP / 64;                 // 128-byte swizzle spans per row
     static constexpr int BK = D == 256 ? 64 : 128;      // keys per tile
-    static constexpr int RB = 128 * NB / G;             // query rows per item
+    static constexpr int RB = 128 * NB;                 // query rows per item
     // With one block, two softmax warpgroups, a thread for one half of the tile's keys each: the ring's V
     // slots are held for as long as a softmax takes (B32 R = 128 of 1..8192 keys: 120 -> 113 us).  With
     // two, a warpgroup for each (four: 115 -> 137 us, the MMA warp then issues late, and registers end).
     static constexpr int NH = NB == 1 ? 2 : 1;
-    static constexpr int CB = BK / NH;                  // keys of a warpgroup
-    // Few rows (R <= 128 / G) would lie in some quarters of tensor memory only, which the same one or two
-    // of the SM's four schedulers reach.  With a copy of them in each quarter or half all have scores to
-    // work on, a thread those of KEYS keys; P then goes through shared memory, where any warp can write it.
-    static constexpr int KEYS = CB / G, W = KEYS < 32 ? KEYS : 32;
-    static_assert(G == 1 || (NB == 1 && CB == 64), "P's rows are two swizzle spans, one from each warpgroup");
+    static constexpr int CB = BK / NH;                  // keys of a thread
     static constexpr int THREADS = 32 * 12;
     // (Two blocks: their softmax threads hold a row of 128 scores, the other warps little, so warpgroups
     // trade the launch's registers, 3 x 168, and every wait is inlined, as a called function has one
@@ -81,14 +74,11 @@ struct TreeTile {
     static constexpr uint32_t Q_BLOCK = NCH * Q_CHUNK;
     static constexpr uint32_t Q_BYTES = NB * Q_BLOCK;
     static constexpr int QBUF = Q_BYTES <= 32 * 1024 ? 2 : 1;
-    static constexpr uint32_t P_SPAN = G > 1 ? RB * 128 : 0, P_BYTES = 2 * P_SPAN;  // of a unit
     static constexpr uint32_t MISC = 24 * 1024;
-    static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - 2 * P_BYTES - MISC - 1024) / SLOT) / 2 * 2;
+    static constexpr int FIT = (int)((226 * 1024 - QBUF * Q_BYTES - MISC - 1024) / SLOT) / 2 * 2;
     static constexpr int STAGES = FIT > 8 ? 8 : FIT;    // 128 KB of keys and values
     static constexpr uint32_t OFF_Q = STAGES * SLOT;
-    static constexpr uint32_t OFF_P = OFF_Q + QBUF * Q_BYTES;
-    static constexpr uint32_t OFF_MISC = OFF_P + 2 * P_BYTES;
-    static_assert(G == 1 || 128 * 128 - P_SPAN <= MISC, "the product reads 128 rows from each span of P's on");
+    static constexpr uint32_t OFF_MISC = OFF_Q + QBUF * Q_BYTES;
     static constexpr uint32_t SMEM = OFF_MISC + MISC + 1024;  // and room to align the start
     static constexpr uint32_t TM_O = 2 * BK;
     static constexpr uint32_t TM_USED = TM_O + NB * DP;
@@ -101,8 +91,8 @@ struct TreeTile {
 template <int STAGES, int NB>
 struct TreeMisc {
     unsigned long long full[STAGES], empty[STAGES];
-    // per block of rows, by its own units in turn: S is there, P is there, O is there.  (A warp may
-    // come to wait for O of a unit before O of the last one is done, so these are two as well.)
+    // per block of rows, by its own tiles in turn: S is there, half of P, all of P, O is there.  (A warp may
+    // come to wait for O of a tile before O of the last one is done, so these are two as well.)
     unsigned long long s_full[NB][2], p_half[NB][2], p_full[NB][2], pv_done[NB][2];
     unsigned long long q_full[2], q_empty[2], info_full[2], info_empty[2], done[2];
     uint32_t tmem;
@@ -216,12 +206,11 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
                  : "memory");
 }
 
-template <int D, int NB, int G>
-__global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
+template <int D, int NB>
+__global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
     fa_tree_kernel(const __grid_constant__ TreeArgs a) {
-    using T = TreeTile<D, NB, G>;
+    using T = TreeTile<D, NB>;
     constexpr int ST = T::STAGES, BK = T::BK, NH = T::NH, CB = T::CB, NCH = T::NCH, QBUF = T::QBUF;
-    constexpr int KEYS = T::KEYS, W = T::W;
     using Misc = TreeMisc<ST, NB>;
     static_assert(sizeof(Misc) <= T::MISC, "state fits behind the buffers");
     constexpr int kMmaWarp = 8, kTmaWarp = kMmaWarp + 1, kMmaWarp2 = kMmaWarp + 3;  // TMA: K, then V
@@ -297,7 +286,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
     constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
     constexpr int kRun = CB / 16 < 4 ? CB / 16 : 4;
     const uint64_t d_q = sdesc_sw128(sQ, 16, 1024), d_k = sdesc_sw128(base, 16, 1024);
-    const uint64_t d_v = sdesc_sw128(base, T::SPAN, 1024), d_p = sdesc_sw128(base + T::OFF_P, 16, 1024);
+    const uint64_t d_v = sdesc_sw128(base, T::SPAN, 1024);
     struct Slot {  // a ring slot of K or V and the parity of its round
         int at;
         uint32_t round;
@@ -324,12 +313,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
         for (int ks = from; ks < to; ks += kRun) {
             const uint64_t dvk = desc_add(dv, ks * 2048);
             const uint32_t more = (!first || ks > 0) ? 1u : 0u;
-            if constexpr (G > 1)
-                mma_ss_run<kRun, 2, 128>(tmem + T::TM_O, desc_add(d_p, at * T::P_BYTES + (ks >> 2) * T::P_SPAN), dvk,
-                                         kIdescO, more);
-            else
-                mma_ts_run<kRun, 128>(tmem + T::TM_O + blk * T::DP,
-                                      tmem + at * BK + ks / (CB / 16) * CB + ks % (CB / 16) * 8, dvk, kIdescO, more);
+            mma_ts_run<kRun, 128>(tmem + T::TM_O + blk * T::DP,
+                                  tmem + at * BK + ks / (CB / 16) * CB + ks % (CB / 16) * 8, dvk, kIdescO, more);
         }
     };
     // Waits until every MMA that this warp has issued has completed (normal or aborted run).
@@ -350,12 +335,12 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             return false;
         if (lane == 0) {
             const uint32_t fb = bar(ms.q_full[qb]);
-            mbar_arrive_expect_tx(fb, (uint32_t)(nb * G * NCH * a.box_q) * 128u);
+            mbar_arrive_expect_tx(fb, (uint32_t)(nb * NCH * a.box_q) * 128u);
             const int row0 = (int)(((long long)x.b * a.Hkv + x.kvh) * a.R + (long long)x.rb * a.item_rows);
-            for (int k = 0; k < nb * G; ++k)  // blocks, or copies
+            for (int k = 0; k < nb; ++k)
                 for (int c = 0; c < NCH; ++c)
-                    tma_load_3d(sQ + qb * T::Q_BYTES + (G > 1 ? k * T::RB * 128 : k * T::Q_BLOCK) + c * T::Q_CHUNK,
-                                &a.tm_q, fb, c * 64, G > 1 ? row0 : row0 + 128 * k, 0);
+                    tma_load_3d(sQ + qb * T::Q_BYTES + k * T::Q_BLOCK + c * T::Q_CHUNK, &a.tm_q, fb, c * 64,
+                                row0 + 128 * k, 0);
         }
         __syncwarp();
         return true;
@@ -446,9 +431,10 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
 
     // One block: a warp for S = Q K^T, the queries and the trees, one for O += P V.  (A warp with all
     // products takes 1.5k to 1.9k clocks to issue those of a tile, of waits, commits and descriptors: B32
-    // R = 128 of 1..8192 keys 104 -> 101.8 us, B4 R = 32 of d96 14.0 -> 11.9.)  Two blocks: all products
-    // in one order, from one warp, the other prepares.  (Products of the two kinds from two warps, by kind
-    // or by block, mix on their way, which slows both: B1 R = 256 of 131072 keys 115 -> 128 us.)
+    // R = 128 of 1..8192 keys 104 -> 101 us, B4 R = 32 of d96 14.0 -> 12.2.)  Two blocks: all products from
+    // one warp, in a fixed order (taken as they get ready: B1 R = 256 of 131072 keys 115 -> 111 us), the
+    // other prepares.  (From two warps, by kind or by block, products mix on their way, which slows both:
+    // 125 to 137 us.)
     if (warp == kTmaWarp || warp == kTmaWarp + 1) {
         // ------------------------------------------------------------ K, or V
         if constexpr (T::TRADE) setmaxnreg_dec<T::REG_OTHERS>();
@@ -544,7 +530,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             more = walk.next(a, &sa);
             const int qb = (int)(seg % QBUF);
             if (QBUF == 2) put_next();
-            if (seg == 0) ok = ok && put_tree(s, 0);  // while the first copies are under way; later ones behind the first S
+            // the first one while the first copies are under way, later ones behind the first S
+            if (seg == 0) ok = ok && put_tree(s, 0);
             ok = ok && mbar_wait_warp<kIn>(bar(ms.q_full[qb]), (seg / QBUF) & 1, g, SITE_DEC_MMA);
 #pragma unroll 1
             for (int t = s.t0; ok && t < s.t1; ++t, ++unit) {
@@ -690,10 +677,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
         // Every warp runs every step even after a wait has given up (waits then return soon).
         const int wg = NH == 1 ? warp >> 2 : 0, h = NH == 1 ? 0 : warp >> 2, w4 = warp & 3;  // block of rows, half of the keys
         const int kk = threadIdx.x & 127;  // row of the block; lane of S and O; key of a tile's V
-        const int row_warp = w4 % (4 / G), copy = w4 / (4 / G), rr = kk % (128 / G);  // its scores' row
-        const int col = h * CB + copy * KEYS;  // and first key
-        const int team = 1 + row_warp, team_threads = 32 * NH * G;  // barrier of the warps that share 32 rows
-        const int turn = (h * G + copy) * (128 / G) + rr;  // this thread's place in what they tell each other
+        const int pair = 1 + w4;           // barrier of the two warps that share 32 rows
+        const int turn = h * 128 + kk;     // this thread's place in what they tell each other
         const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
         const uint32_t t_o = tmem + lane_base + T::TM_O + wg * T::DP;
         const float c_s = a.scale_log2;
@@ -702,8 +687,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
             const int ib = seg & 1, len = a.seq_lens[s.b], nb = blocks_of(s);
             const int r0 = s.rb * a.item_rows + wg * 128, rows = min(128, rows_of(s) - wg * 128);  // may be none
             const bool mine = w4 * 32 < rows;                                   // this warp has rows
-            const bool scores = row_warp * 32 < rows;                           // or a copy of some
-            const int node = a.Nt - a.Nq + (r0 + rr) % a.Nq;                    // this thread's row
+            const int node = a.Nt - a.Nq + (r0 + kk) % a.Nq;                    // this thread's row
             const int full_tiles = len >> (D == 256 ? 6 : 7);
             bool informed = false;
             auto inform = [&]() {
@@ -727,46 +711,43 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                     if (partly) inform();
                     mbar_wait_warp<kIn>(bar(ms.s_full[wg][m & 1]), (m >> 1) & 1, g, SITE_DEC_MMA);
                     tc_fence_after();
-                    if (scores) {
+                    if (mine) {
                         const uint32_t at = NB == 1 ? m & 1 : nb == 2 ? wg : (t - s.t0) & 1;  // slot of S
-                        const uint32_t t_s = tmem + lane_base + at * BK + col;
-                        uint32_t sr[KEYS / W][W];
+                        const uint32_t t_s = tmem + lane_base + at * BK + h * CB;
+                        uint32_t sr[CB / 32][32];
 #pragma unroll
-                        for (int c = 0; c < KEYS / W; ++c) {
-                            if constexpr (W == 32) tmem_ld32(t_s + c * 32, sr[c]);
-                            else tmem_ld16(t_s, sr[c]);
+                        for (int c = 0; c < CB / 32; ++c) {
+                            tmem_ld32(t_s + c * 32, sr[c]);
                         }
 #pragma unroll
-                        for (int c = 0; c < KEYS / W; ++c) tmem_wait_ld(sr[c]);
-                        float x[KEYS];
+                        for (int c = 0; c < CB / 32; ++c) tmem_wait_ld(sr[c]);
+                        float x[CB];
 #pragma unroll
-                        for (int c = 0; c < KEYS / W; ++c)
+                        for (int c = 0; c < CB / 32; ++c)
 #pragma unroll
-                            for (int e = 0; e < W; ++e) x[c * W + e] = __uint_as_float(sr[c][e]);
+                            for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(sr[c][e]);
                         if (partly) {
-                            const int n0 = t * BK + col - len;  // node of the first key, or below 0
+                            const int n0 = t * BK + h * CB - len;  // node of the first key, or below 0
 #pragma unroll
-                            for (int c = 0; c < KEYS / W; ++c) {
-                                const int at = (n0 + W * c) >> 5, sh = (n0 + W * c) & 31;
+                            for (int c = 0; c < CB / 32; ++c) {
+                                const int at = (n0 + 32 * c) >> 5, sh = (n0 + 32 * c) & 31;
                                 const uint32_t w = __funnelshift_r(sees(node, at), sees(node, at + 1), sh);
 #pragma unroll
-                                for (int e = 0; e < W; ++e)
-                                    if (!(w >> e & 1u)) x[c * W + e] = -INFINITY;
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(w >> e & 1u)) x[c * 32 + e] = -INFINITY;
                             }
                         }
                         float mp0 = -INFINITY, mp1 = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < KEYS; c += 4) {
+                        for (int c = 0; c < CB; c += 4) {
                             mp0 = fmax3(mp0, x[c], x[c + 1]);
                             mp1 = fmax3(mp1, x[c + 2], x[c + 3]);
                         }
                         float top = fmaxf(mp0, mp1);
-                        if constexpr (NH * G > 1) {  // of all of the row, whose threads then take the same steps
+                        if constexpr (NH == 2) {  // of both halves, which then take the same steps
                             ms.trade[m & 1][turn] = top;
-                            named_barrier_sync(team, team_threads);
-#pragma unroll
-                            for (int k = 1; k < NH * G; ++k)
-                                top = fmaxf(top, ms.trade[m & 1][(turn + k * (128 / G)) % (128 * NH)]);
+                            named_barrier_sync(pair, 64);
+                            top = fmaxf(top, ms.trade[m & 1][turn ^ 128]);
                         }
                         top *= c_s;
                         float alpha = 1.f;
@@ -776,7 +757,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                             m_ref = top;
                         }
                         auto rescale = [&]() {
-                            if (mine && t > s.t0 && __any_sync(kFull, move)) {
+                            if (t > s.t0 && __any_sync(kFull, move)) {
                                 // O <- alpha O once the product before is complete
                                 mbar_wait_warp<kIn>(bar(ms.pv_done[wg][(m - 1) & 1]), ((m - 1) >> 1) & 1, g, SITE_DEC_MMA);
                                 tc_fence_after();
@@ -818,7 +799,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                         if constexpr (NB == 2) {
                             // the product with V begins on the first half of the keys while the second's
                             // exponentials are taken
-                            exponentials(0, KEYS / 2);
+                            exponentials(0, CB / 2);
                             put_p(0);
                             tmem_wait_st();
                             if (!partly) {
@@ -826,22 +807,13 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive(bar(ms.p_half[wg][m & 1]));
                             }
-                            exponentials(KEYS / 2, KEYS);
+                            exponentials(CB / 2, CB);
                             put_p(1);
                         } else {
-                            exponentials(0, KEYS);
+                            exponentials(0, CB);
                         }
                         l = l * alpha + (sp0 + sp1);
-                        if constexpr (G > 1) {
-                            // P as an operand of 128-byte rows, 16-byte chunks turned by the row
-                            uint8_t *p = gbase + T::OFF_P + at * T::P_BYTES + h * T::P_SPAN + rr * 128;
-#pragma unroll
-                            for (int e = 0; e < KEYS; e += 8)
-                                *reinterpret_cast<uint4 *>(p + ((copy * (KEYS / 8) + e / 8) ^ (rr & 7)) * 16) =
-                                    make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
-                                               pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
-                            fence_proxy_async_smem();
-                        } else if constexpr (CB == 64) {
+                        if constexpr (CB == 64) {
                             put_p(0);
                         } else if constexpr (CB == 32) {
                             uint32_t pk[16];
@@ -882,7 +854,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                     }
                     __syncwarp();
                     tc_fence_before();
-                    if (NB == 2 && lane == 0 && (partly || !scores)) mbar_arrive(bar(ms.p_half[wg][m & 1]));
+                    if (NB == 2 && lane == 0 && (partly || !mine)) mbar_arrive(bar(ms.p_half[wg][m & 1]));
                     if (lane == 0) mbar_arrive(bar(ms.p_full[wg][m & 1]));
                 }
             }
@@ -896,13 +868,11 @@ __global__ void __launch_bounds__(TreeTile<D, NB, G>::THREADS, 1)
                 atomicCAS(a.status + 1, 0, bad_page ? SITE_TREE_BAD_PAGE : SITE_TREE_BAD_PARENT);
                 atomicExch(a.status, FA_ERR_BAD_INDEX);
             }
-            if (NH * G > 1 && scores) {  // the row's sum, of all its threads
+            if (NH == 2 && mine) {  // the row's sum, of both halves
                 ms.trade[m & 1][turn] = l;
-                named_barrier_sync(team, team_threads);
-                l = 0.f;
-#pragma unroll
-                for (int k = 0; k < NH * G; ++k) l += ms.trade[m & 1][k * (128 / G) + rr];  // each in the same order
-                named_barrier_sync(team, team_threads);  // all have read
+                named_barrier_sync(pair, 64);
+                l += ms.trade[m & 1][turn ^ 128];
+                named_barrier_sync(pair, 64);  // both have read
             }
             if (mine && *g.abort == 0) {
                 const bool whole = s.t0 == 0 && s.t1 == s.nt;
@@ -1045,9 +1015,9 @@ __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __gr
 }
 
 // Tiles of all items at the longest possible lengths.
-template <int D, int NB, int G>
+template <int D, int NB>
 long long tree_tiles(const TreeParams &p) {
-    using T = TreeTile<D, NB, G>;
+    using T = TreeTile<D, NB>;
     const long long R = (long long)(p.H / p.Hkv) * p.Nq;
     const long long nt = ((long long)p.page_size * p.max_pages + p.Nt + T::BK - 1) / T::BK;
     const long long items = (long long)p.B * p.Hkv * ((R + T::RB - 1) / T::RB);
@@ -1055,22 +1025,22 @@ long long tree_tiles(const TreeParams &p) {
 }
 
 // CTAs of a launch: one per SM, or the largest number of tiles there can be.
-template <int D, int NB, int G>
+template <int D, int NB>
 int tree_ctas(const TreeParams &p) {
-    const long long n = tree_tiles<D, NB, G>(p);
+    const long long n = tree_tiles<D, NB>(p);
     return n < p.num_sms ? (int)n : p.num_sms;
 }
 
-template <int D, int NB, int G>
+template <int D, int NB>
 size_t tree_bytes(const TreeParams &p, size_t *l_offset) {
-    const size_t ctas = tree_ctas<D, NB, G>(p), rows = ctas * 2 * TreeTile<D, NB, G>::RB;
+    const size_t ctas = tree_ctas<D, NB>(p), rows = ctas * 2 * TreeTile<D, NB>::RB;
     *l_offset = rows * D * sizeof(float);
     return *l_offset + rows * sizeof(float) + ctas * sizeof(int4) + 16;  // and room to begin on 32 bytes
 }
 
-template <int D, int NB, int G>
+template <int D, int NB>
 int launch_t(const TreeParams &p, cudaStream_t stream) {
-    using T = TreeTile<D, NB, G>;
+    using T = TreeTile<D, NB>;
     TreeArgs a{};
     a.tm_q = p.tm_q;
     a.tm_k = p.tm_k;
@@ -1082,11 +1052,11 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.lse = p.lse;
     size_t l_offset;
-    tree_bytes<D, NB, G>(p, &l_offset);
+    tree_bytes<D, NB>(p, &l_offset);
     char *const ws = static_cast<char *>(p.workspace) + (reinterpret_cast<uintptr_t>(p.workspace) % 32);
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_l = reinterpret_cast<float *>(ws + l_offset);
-    a.cuts = reinterpret_cast<int4 *>(a.part_l + (size_t)tree_ctas<D, NB, G>(p) * 2 * T::RB);
+    a.cuts = reinterpret_cast<int4 *>(a.part_l + (size_t)tree_ctas<D, NB>(p) * 2 * T::RB);
     a.by_page = fast_div((uint32_t)p.page_size);
     a.B = p.B;
     a.H = p.H;
@@ -1100,29 +1070,30 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
     a.R = p.H / p.Hkv * p.Nq;
     a.row_blocks = (a.R + T::RB - 1) / T::RB;
     // items of one block share the rows evenly, so that none of a key/value head's is left for last (d256,
-    // pages of 48: B2 Hkv2 R = 144 of 233..700 keys 16.7 -> 15.1 us, B5 Hkv2 R = 136 of up to 2900 keys 22.3
-    // -> 21.8, R = 168 no difference); of two blocks, the fewest blocks in all are best
+    // pages of 48: B2 Hkv2 R = 144 of 233..700 keys 16.8 -> 15.1 us, B5 Hkv2 R = 136 of up to 2900 keys 22.2
+    // -> 21.5, R = 168 no difference); of two blocks, the fewest blocks in all are best
     a.item_rows = NB == 1 ? (a.R + a.row_blocks - 1) / a.row_blocks : T::RB;
     a.box = tree_box_rows(p);
     a.box_q = tree_query_box(p);
     a.tile_log2 = T::BK == 64 ? 6 : 7;
-    // an item's start costs as much as two tiles (B32 Hkv8 R = 128 of 1..8192 keys, with 1, 2, 3: 110, 104.2,
-    // 105 us; a single item per CTA: no difference)
+    // an item's start costs as much as two tiles (B32 Hkv8 R = 128 of 1..8192 keys, with 1, 2, 3: 107, 101.7,
+    // 102 us; one sequence of 131072 keys 108, 110, 109)
     a.start = 2;
     a.o_aligned = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
     a.scale_log2 = p.scale_log2;
     a.status = p.status;
     a.limit_ns = kWaitLimitNs;
-    auto kern = fa_tree_kernel<D, NB, G>;
+    auto kern = fa_tree_kernel<D, NB>;
     constexpr int kSmem = (int)T::SMEM;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmem) != FA_OK) return FA_ERR_CUDA;
-    const int n_cta = tree_ctas<D, NB, G>(p);
+    const int n_cta = tree_ctas<D, NB>(p);
     if (launch_dependent(kern, dim3((unsigned)n_cta), T::THREADS, kSmem, stream, 1, a) != FA_OK) return FA_ERR_CUDA;
     // Few rows: a CTA for each, which looks for its parts while the attention kernel still runs; many: the
-    // listed cuts only (a CTA per row against the list: 512 rows of one sequence 11.1 and 12.5 us, of four
-    // 14.0 and 18.4, 1680 rows of d256 29.0 and 26.1, 32768 of d128 170 and 104).
+    // listed cuts only (a CTA per row against the list: 512 rows of one sequence 10.0 and 11.0 us, of four
+    // 11.5 and 16.3, 1024 rows of one sequence 19.8 and 22.2, 2048 rows of sixteen 30.9 and 28.1, 32768 rows
+    // 167 and 101).
     const long long rows = (long long)p.B * p.H * p.Nq;
-    if (rows * D <= 16LL * 128 * n_cta)
+    if (rows <= 8LL * p.num_sms)
         return launch_dependent(fa_merge_row_kernel<(D + 31) / 32, 0, TreeArgs>, dim3((unsigned)rows),
                                 32 * kRowWarps, 0, stream, 1, a, n_cta);
     return launch_dependent(fa_tree_merge_kernel<D>, dim3((unsigned)n_cta, kMergeWorkers), kMergeThreads, 0,
@@ -1130,29 +1101,19 @@ int launch_t(const TreeParams &p, cudaStream_t stream) {
 }
 
 // Calls f with the tile that serves the call: head dimension and blocks of 128 query rows (two against
-// one, which copies the keys again for each block: B1 R = 256 of 131072 keys 116 and 175 us, B16 R = 384
-// of 16384..32768 keys 545 and 692).
+// one, which copies the keys again for each block: B1 R = 256 of 131072 keys 111 and 171 us, B16 R = 384
+// of 16384..32768 keys 528 and 677).
 template <typename F>
 auto with_tile(const TreeParams &p, F f) {
     using std::integral_constant;
-    const long long R = (long long)(p.H / p.Hkv) * p.Nq;
+    const bool two = (long long)(p.H / p.Hkv) * p.Nq > 128;
     using One = integral_constant<int, 1>;
     using Two = integral_constant<int, 2>;
-    using Four = integral_constant<int, 4>;
     switch (p.d) {
-        case 64: {
-            const integral_constant<int, 64> d;
-            return R <= 32 ? f(d, One(), Four()) : R <= 64 ? f(d, One(), Two()) : R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
-        }
-        case 96: {
-            const integral_constant<int, 96> d;
-            return R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
-        }
-        case 128: {
-            const integral_constant<int, 128> d;
-            return R <= 128 ? f(d, One(), One()) : f(d, Two(), One());
-        }
-        default: return f(integral_constant<int, 256>(), One(), One());  // O of a second block has no room
+        case 64: return two ? f(integral_constant<int, 64>(), Two()) : f(integral_constant<int, 64>(), One());
+        case 96: return two ? f(integral_constant<int, 96>(), Two()) : f(integral_constant<int, 96>(), One());
+        case 128: return two ? f(integral_constant<int, 128>(), Two()) : f(integral_constant<int, 128>(), One());
+        default: return f(integral_constant<int, 256>(), One());  // O of a second block has no room
     }
 }
 
@@ -1171,21 +1132,21 @@ int tree_query_box(const TreeParams &p) {
 }
 
 long long tree_max_tiles(const TreeParams &p) {
-    return with_tile(p, [&](auto d, auto nb, auto g) {
-        return tree_tiles<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p);
+    return with_tile(p, [&](auto d, auto nb) {
+        return tree_tiles<decltype(d)::value, decltype(nb)::value>(p);
     });
 }
 
 size_t tree_workspace_bytes(const TreeParams &p) {
-    return with_tile(p, [&](auto d, auto nb, auto g) {
+    return with_tile(p, [&](auto d, auto nb) {
         size_t l_offset;
-        return tree_bytes<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p, &l_offset);
+        return tree_bytes<decltype(d)::value, decltype(nb)::value>(p, &l_offset);
     });
 }
 
 int launch_tree(const TreeParams &p, cudaStream_t stream) {
-    return with_tile(p, [&](auto d, auto nb, auto g) {
-        return launch_t<decltype(d)::value, decltype(nb)::value, decltype(g)::value>(p, stream);
+    return with_tile(p, [&](auto d, auto nb) {
+        return launch_t<decltype(d)::value, decltype(nb)::value>(p, stream);
     });
 }
 
