@@ -582,7 +582,8 @@ int fa_decode_paged_tree(const void *q, const void *k_cache, const void *v_cache
  * The last token is the least i with P(0) + ... + P(i) > u (P(0) + ... + P(V-1)), P(i) = max(p(i) -
  * a_k q(i), 0) or p_k(i) after the node's last rejection, or p itself where nothing is left.
  * Sums over the vocabulary are those of the addends taken in multiples of 2^-44, without error: no
- * order of summation and no device changes a result.
+ * order of summation and no device changes a result.  The values of a row, taken so, sum to less
+ * than 2^20 (probabilities sum to 1).
  * Outputs (int32, every element is written):
  *   path     : [B][Nt]: the accepted nodes from node 0 on, then -1.
  *   new_tokens : [B][Nt]: the accepted drafted tokens, then the last token, then -1.

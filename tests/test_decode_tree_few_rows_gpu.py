@@ -68,3 +68,20 @@ def test_values_that_are_not_finite(fa, value, G):
         for key, c in ((7, 3), (length - 1, 40), (length + 2, 63), (length + 6, 5)):
             v[table[b, key // page], :, key % page, c] = value
     check(fa, (q, k, v, table, n, par))
+
+
+@pytest.mark.parametrize("Nt", [32, 33, 200, 256])
+@pytest.mark.parametrize("d", [64, 128])
+def test_deep_trees(fa, d, Nt):
+    """A path as long as the tree, a comb of it (each second node a leaf), and one that ends early; the
+    path is what no parents at all stand for."""
+    j = torch.arange(Nt)
+    comb = torch.where(j % 2 == 1, j - 1, j - 2).clamp(min=-1)
+    short = torch.where(j < Nt - 7, j - 1, -2)
+    par = torch.stack([j - 1, comb, short]).to(torch.int32)
+    args = inputs([130, 5, 0], 1, 2, Nt, Nt, d, 16, Nt, par)
+    check(fa, args)
+    dev = [t.to(DEV) for t in args]
+    o, lse = fa.decode_paged_tree(*dev)
+    o2, lse2 = fa.decode_paged_tree(*dev[:5])
+    assert torch.equal(o[0], o2[0]) and torch.equal(lse[0], lse2[0])
