@@ -33,7 +33,12 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 // and summing the bit patterns: 13 fp32 and integer operations per element, against two dozen, half
 // of them shifts, of a conversion to 64 bits (B64 Nt24 V128000, six sums one after another: 80 us).
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
+//
+// Measured (GB300, graph replay): B1 Nt16 V32000 fp32 7.7 us, B64 Nt24 V128000 fp32 without repetition 45
+// us, B48 Nt9 V50021 bf16 certain drafts 8.4 us.  CTAs of 256 threads, four to an SM: a wave holds twice
+// the sequences that it held with 512 threads, two to an SM (9.7, 47.5 and 9.2 us).
+
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxNodes = FA_MAX_TREE_NODES;
 
 // x as a probability: 0 for what is below 0 or NaN, 1 above 1.
@@ -217,7 +222,7 @@ __device__ __forceinline__ Pair inverse(Pair x) {
 }
 
 template <typename P, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, 2) fa_verify_kernel(const VerifyParams v) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const VerifyParams v) {
     constexpr int VEC = Row<P>::VEC;
     __shared__ VerifyShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -554,13 +559,15 @@ int launch_verify_t(const VerifyParams &v, int ctas, cudaStream_t stream) {
 }  // namespace
 
 int launch_verify(const VerifyParams &v, cudaStream_t stream) {
-    // CTAs per sequence: more while each still has 32 KB of a node's rows, and all of them are no
-    // more than two waves (a sequence of many sums, alone at the end, then has more of the GPU).
-    // With 1, 2, 4, 8: B1 V32000 fp32, two rows, 15.9, 12.0, 9.4, 9.6 us; B48 V50021 bf16, one row, 11.2,
-    // 9.3, 9.3, 14.4 us; B64 V128000 fp32, two rows, 127, 76, 53, 47 us.
+    // CTAs per sequence: more while each still has 24 KB of a node's rows, and all of them are no more than
+    // two waves (a sequence of many sums, alone at the end, then has more of the GPU), or, where drafts are
+    // certain and a sequence has one sum, than one.  With 1, 2, 4, 8: V1000 fp32, two rows, B64 12.6, 14.8,
+    // 14.7, 17.0 us; V8000 B64 32.8, 29.9, 30.5, 32.3; V32000 B1 19.4, 12.9, 9.1, 7.7, B256 88, 61, 55, 60;
+    // V128000 B64 172, 98, 60, 45; V50021 bf16, one row, B48 12.3, 9.6, 8.4, 8.2, B256 16.7, 16.7, 20.9, 30.3.
     const long long bytes = (long long)v.V * (v.bf16 ? 2 : 4) * (v.draft ? 2 : 1);
+    const long long most = (v.draft ? 7LL : 4LL) * v.num_sms;
     int ctas = 1;
-    while (ctas < 8 && (long long)v.B * ctas * 2 <= 4LL * v.num_sms && bytes / (ctas * 2) >= 30000) ctas *= 2;
+    while (ctas < 8 && (long long)v.B * ctas * 2 <= most && bytes / (ctas * 2) >= 24000) ctas *= 2;
     return v.bf16 ? launch_verify_t<__nv_bfloat16>(v, ctas, stream) : launch_verify_t<float>(v, ctas, stream);
 }
 
