@@ -166,6 +166,10 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The two halves of a barrier over the cluster's threads: all of them take both.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Tiled bulk add of a shared-memory box into global memory through a tensor map
 // (fp32 elements; rows outside the tensor are skipped).  Completes in a bulk group.
 __device__ __forceinline__ void tma_reduce_add_3d(const void *tmap, uint32_t src, int x, int y,

@@ -231,6 +231,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const P *target = static_cast<const P *>(v.target) + (size_t)b * Nt * V;
     const P *draft = DRAFT ? static_cast<const P *>(v.draft) + (size_t)b * Nt * V : nullptr;
+    // The CTAs write into each other's shared memory, which takes that they run: every CTA says here
+    // that it does, and waits for the others in front of its first write (`met`).
+    cluster_arrive();
+    bool met = false;
     griddep_wait();
     griddep_launch_dependents();
 
@@ -264,6 +268,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
                 if (sh.bad) flag_index(v.status, SITE_VERIFY_BAD_TREE);
             }
         }
+        cluster_wait();
         return;
     }
 
@@ -371,6 +376,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
         sum = warp_sum(sum);
         if (lane == 0) sh.warp_sum[warp] = sum;
         __syncthreads();
+        if (!met) cluster_wait();
+        met = true;
         if (warp == 0) {
             const unsigned long long all = warp_sum(lane < kVerifyWarps ? sh.warp_sum[lane] : 0ull);
             if (lane < ctas) cluster.map_shared_rank(&sh, lane)->cta_sum[turn][rank] = all;
