@@ -145,11 +145,13 @@ struct Weights {
                 w = x - y;
                 rest = (x - w) - y;
             } else {
+                // x - (h + lo); (x - d) - h is what d = x - h was rounded by, exactly so from x = h / 2 on,
+                // and below that d decides.  The sign is the pair's: lo may outweigh an x below h.
                 const float h = l.a_hi * y, lo = fmaf(l.a_lo, y, fmaf(l.a_hi, y, -h)), d = x - h;
                 const float e = ((x - d) - h) - lo;
                 w = d + e;
                 rest = e - (w - d);
-                if (!(x >= h && w > 0.f)) w = rest = 0.f;
+                if (!(w > 0.f)) w = rest = 0.f;
             }
         }
         const float t1 = w + kCut1;
