@@ -44,12 +44,12 @@ constexpr int kMaxNodes = FA_MAX_TREE_NODES;
 // x as a probability: 0 for what is below 0 or NaN, 1 above 1.
 __device__ __forceinline__ float probability(float x) { return __saturatef(x); }
 
-// floor(u 2^64) of a number in [0, 1), the largest there is from 1 on.
-__device__ __forceinline__ unsigned long long unit_fixed(float u) {
+// floor(u whole), for u of any size; below `whole` also from u = 1 on.
+__device__ __forceinline__ unsigned long long share_of(float u, unsigned long long whole) {
     u = probability(u);
-    const uint32_t w = __float_as_uint(u), by = 126u - (w >> 23);
+    const uint32_t w = __float_as_uint(u), by = 126u - (w >> 23);  // u = m 2^-64-by
     const unsigned long long m = (unsigned long long)((w & 0x7fffffu) | 0x800000u) << 40;
-    return u >= 1.f ? ~0ull : by < 64 ? m >> by : 0ull;
+    return u >= 1.f ? __umul64hi(~0ull, whole) : by < 64 ? __umul64hi(m, whole) >> by : 0ull;
 }
 
 // A weight of 0 .. 1 is k1 2^-22 + k2 2^-44: the bit patterns of kCut1 + k1 2^-22 and of kCut2 +
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
             continue;
         }
         // ---- the token whose part of the running sum holds u times the whole
-        const unsigned long long goal = __umul64hi(unit_fixed(sh.u[0]), whole);
+        const unsigned long long goal = share_of(sh.u[0], whole);
         if (warp == 0 && rank == 0) {
             for (int i = count + lane; i < Nt; i += 32) path[i] = fresh[i] = -1;
             if (lane == 0) {

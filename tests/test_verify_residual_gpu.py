@@ -41,3 +41,17 @@ def truncated(B, V, keep, kids, seed):
 @pytest.mark.parametrize("keep,kids", [(38, 3), (38, 5), (38, 6), (34, 7), (28, 9)])
 def test_truncated_targets(fa, keep, kids, replacement):
     check(fa, *truncated(200, 40, keep, kids, keep + kids), replacement)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_smallest_uniforms(fa, dtype):
+    """Uniforms of 2^-45 to 2^-39, each with all its bits, and first tokens of a few 2^-44."""
+    B, V = 256, 9
+    g = torch.Generator().manual_seed(1)
+    target = torch.zeros((B, 1, V))
+    target[:, 0, :-1] = torch.randint(0, 4, (B, V - 1), generator=g) * 2.0 ** -44
+    target[:, 0, -1] = 1 - 2.0 ** -24
+    u = (1 + torch.rand((B, 1), generator=g)) * 2.0 ** -torch.randint(40, 46, (B, 1), generator=g)
+    target[0, 0], u[0] = torch.tensor([2.0 ** -44] + [0] * 7 + [1 - 2.0 ** -24]), (1 + 2.0 ** -23) * 2.0 ** -44
+    zeros = torch.zeros((B, 1), dtype=torch.int32)
+    check(fa, zeros, zeros - 1, target.to(dtype), None, u)
