@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kKeepThreads) fa_keep_kernel(const __grid_cons
         for (int i = threadIdx.x; i < count; i += kKeepThreads) {
             const int node = path[i], before = i > 0 ? path[i - 1] : -1;
             bool bad = node <= before || node >= k.Nt;
-            if (!bad && node != i) {
+            if (!bad) {  // also of a row that stays
                 const uint32_t from = (uint32_t)(len + node), to = (uint32_t)(len + i), ps = (uint32_t)k.page_size;
                 const uint32_t fp = from / ps, tp = to / ps;
                 const int from_page = fp < (uint32_t)k.max_pages ? bt[fp] : -1, to_page = bt[tp];
