@@ -11,7 +11,8 @@
 // [CTA][2][RB], and, found with it, tiles_of_len(a, len): the tiles of one item of a sequence
 // (0 where the length is bad), and empty_len(a, len): has it no key, so that its rows are the
 // merge's to write?  RB, the rows of an item, is a constant of the kernel, or 0 where it is
-// a.item_rows.
+// a.item_rows.  Args::kKeepInfinities: an infinity in a part is the row's, however little the part
+// weighs; d is a multiple of 32 then.
 #pragma once
 
 #include "fa_internal.h"
@@ -193,6 +194,30 @@ __device__ __forceinline__ Walk start_walk(const Args &a, int c, int n_cta, Cut 
 // wait is seq_lens only, written by nothing later than the kernels before the attention kernel,
 // which has waited for those before it lets a merge start.)
 
+template <int RB, typename Args>
+__device__ __forceinline__ int item_rows_of(const Args &a) {
+    if constexpr (RB > 0) return RB;
+    else return a.item_rows;
+}
+
+// Of COLUMNS columns of a row of D, STEP apart from `col` (at o) on, those that the merge of its n parts
+// made NaN although no weight is: an infinity has met a weight of 0.  They become the sum of the
+// parts' infinities (and NaN) as they are.  Part 0 is row pr0 of part_o, part k row pr1 and 2 k items' rows
+// more.  (A function of its own, behind the merge and the stores: factors that spare infinities, in
+// the merge, or this in line cost 1 to 2 us of B32 R = 128 of 1..8192 keys, B1 R = 256 of 131072
+// keys and B5 Hkv2 R = 168 of d256; so it costs none.)
+template <int RB, int D, int COLUMNS, int STEP, typename Args>
+__device__ __noinline__ void put_infinities(const Args &a, size_t pr0, size_t pr1, int n, int col, __nv_bfloat16 *o) {
+    for (int e = 0; e < COLUMNS * STEP; e += STEP) {
+        float kept = 0.f;
+        for (int k = 0; k < n; ++k) {
+            const float x = __ldcg(a.part_o + (k == 0 ? pr0 : pr1 + (size_t)(2 * k) * item_rows_of<RB>(a)) * D + col + e);
+            if (!(fabsf(x) < INFINITY)) kept += x;
+        }
+        if (kept != 0.f) o[e] = __float2bfloat16(kept);
+    }
+}
+
 // The running result of one warp over partials first, first + step, ... of a row's n: reference,
 // sum and output columns lane, lane + 32, ...; U partials with their L in flight at a time.
 template <int E, int U, typename Args, typename Row>
@@ -255,11 +280,6 @@ template <int E>
 struct RowShared {
     float acc[kRowWarps][E * 32], sum[kRowWarps], max[kRowWarps];
 };
-template <int RB, typename Args>
-__device__ __forceinline__ int item_rows_of(const Args &a) {
-    if constexpr (RB > 0) return RB;
-    else return a.item_rows;
-}
 template <int E, int RB, typename Args>
 __device__ __forceinline__ void merge_row(const Args &a, RowShared<E> &sh, int c0, int r, int n, long long row) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -291,6 +311,14 @@ __device__ __forceinline__ void merge_row(const Args &a, RowShared<E> &sh, int c
         for (int e = 0; e < E; ++e) acc[e] = fmaf(sh.acc[v][lane + 32 * e], f, acc[e]);
     }
     merge_out(a, row, m, sum, acc);  // an empty sequence: sum 0
+    if constexpr (Args::kKeepInfinities) {
+        float any = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) any += acc[e];
+        if (any != any && sum == sum)
+            put_infinities<RB, 32 * E, E, 32>(a, ((size_t)c0 * 2 + 1) * item_rows_of<RB>(a) + r,
+                                              (size_t)c0 * 2 * item_rows_of<RB>(a) + r, n, lane, a.o + row * a.d + lane);
+    }
 }
 
 // A CTA for each row, which may have dozens of partials (a long sequence alone in the launch).

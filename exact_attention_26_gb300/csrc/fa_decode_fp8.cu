@@ -149,6 +149,7 @@ struct Dec8Misc {
 };
 
 struct Dec8Args {
+    static constexpr bool kKeepInfinities = false;  // codes have none
     CUtensorMap tm_k, tm_v;         // bytes (d, page_size, num_pages * Hkv), boxes 128 x box x 1;
                                     // packed (2 d, page_size / 2, num_pages * Hkv)
     const __nv_bfloat16 *q;

@@ -107,6 +107,7 @@ struct TreeMisc {
 };
 
 struct TreeArgs {
+    static constexpr bool kKeepInfinities = true;  // a node's values may have them
     CUtensorMap tm_q, tm_k, tm_v;   // (d, B * H * Nq), box 64 x box_q; (d, page_size, num_pages *
                                     // Hkv), boxes 64 x box x 1
     const __nv_bfloat16 *v_cache;
@@ -883,7 +884,8 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                 const long long row = ((long long)s.b * a.Hkv + s.kvh) * a.R + r0 + kk;
                 const size_t prow = ((size_t)blockIdx.x * 2 + (s.t0 == 0 ? 1 : 0)) * a.item_rows + wg * 128 + kk;
                 const bool put = kk < rows && !bad;
-                const bool special = *(volatile int *)&ms.special_any[ib] != 0 && !none && !bad;
+                // (also into a part whose keys all have a score of -infinity: it weighs nothing, they stay)
+                const bool special = *(volatile int *)&ms.special_any[ib] != 0 && !bad;
                 const int *bt = a.block_table + (size_t)s.b * a.max_pages;
                 __nv_bfloat16 *out = a.o + (size_t)row * D;
                 float *part = a.part_o + prow * D;
@@ -1010,6 +1012,10 @@ __global__ void __launch_bounds__(kMergeThreads) fa_tree_merge_kernel(const __gr
         const float inv = sum == 0.f ? 0.f : reciprocal(sum);
         *reinterpret_cast<uint2 *>(a.o + (row0 + r) * D + col) =
             make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        const float any = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if (any != any && sum == sum)
+            put_infinities<0, D, 4, 1>(a, ((size_t)c0 * 2 + 1) * a.item_rows + r, (size_t)c0 * 2 * a.item_rows + r, n,
+                                       col, a.o + (row0 + r) * D + col);
         if (col == 0) a.lse[row0 + r] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
     }
 }

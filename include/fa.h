@@ -530,8 +530,9 @@ int fa_copy_pages(void *const *caches, const size_t *page_bytes, int n_caches, i
  * A row without a node gets O = 0 and L = -infinity.  Keys that a row does not see, and what
  * lies in the cache in places without a token or node, have no influence on it, whatever their
  * values are.  A NaN in a key or query that a row sees makes the row NaN; a NaN or infinity in
- * the values of a node that it sees makes that column of the row the same (infinities of both
- * signs: NaN).
+ * the values of a node that it sees makes that column of the row the same, however small the node's
+ * probability is (infinities of both signs: NaN).  So does one of a cached token, but where its
+ * probability is below fp32's smallest an infinity may become NaN.
  * Rounding: probabilities enter the product with V in bf16 (2^-8 relative), sums are fp32.
  *   B, H, Nq >= 1; Hkv divides H; Nq <= Nt <= FA_MAX_TREE_NODES; d: 64, 96, 128 or 256;
  *   (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, page_size * max_pages_per_seq < 2^31 - 1024, B *
