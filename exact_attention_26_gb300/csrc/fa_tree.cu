@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
                         if (token) ms.bad_page[ib] = 1;
                     }
                     const int mine = __popc(__ballot_sync(kFull, copy));
+                    __syncwarp();  // lane 0's arrival passes on what any lane has found
                     if (lane == 0) {
                         // the phase's one arrival comes with its last boxes
                         const uint32_t bytes = (uint32_t)(mine * a.box) * (uint32_t)(NCH * 128);
