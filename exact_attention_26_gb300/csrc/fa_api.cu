@@ -1318,11 +1318,14 @@ extern "C" int fa_keep_path(void *const *caches, int n_caches, const int *block_
         return FA_ERR_INVALID_ARG;
     if (Nt > FA_MAX_TREE_NODES || (d != 64 && d != 96 && d != 128 && d != 256)) return FA_ERR_UNSUPPORTED;
     KeepParams k{};
+    const unsigned long long bytes = 2ull * (unsigned)(num_pages * Hkv) * page_size * d;
     for (int c = 0; c < n_caches; ++c) {
         if (!caches[c]) return FA_ERR_INVALID_ARG;
         if (!aligned16(caches[c])) return FA_ERR_MISALIGNED;
-        for (int e = 0; e < c; ++e)  // moved twice at once, a row would follow its own place
-            if (caches[e] == caches[c]) return FA_ERR_INVALID_ARG;
+        for (int e = 0; e < c; ++e) {  // moved twice at once, a row would follow its own place
+            const uintptr_t x = reinterpret_cast<uintptr_t>(caches[e]), y = reinterpret_cast<uintptr_t>(caches[c]);
+            if ((x < y ? y - x : x - y) < bytes) return FA_ERR_INVALID_ARG;
+        }
         k.cache[c] = caches[c];
     }
     if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(path) || !aligned4(count) || !aligned4(lens))

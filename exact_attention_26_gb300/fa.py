@@ -1212,7 +1212,7 @@ def keep_path(caches, block_table, seq_lens, path, count, stream=None):
     """Keep the accepted nodes of drafted trees in a paged bf16 cache: behind sequence b's
     seq_lens[b] tokens (int32 CUDA [B]) the row of node path[b, i] (int32 [B, Nt], ascending) becomes
     row i for i < count[b] (int32 [B]), in every tensor of `caches` (bf16 [num_pages, Hkv, page_size,
-    d], all of one shape, none twice: keys and values of any number of layers, up to 128), through
+    d], all of one shape, no two overlapping: keys and values of any number of layers, up to 128), through
     block_table int32 [B, max_pages].  Returns seq_lens + count, int32 [B]."""
     caches = caches if isinstance(caches, list) else list(caches)
     r = native().keep_path(caches, block_table, seq_lens, path, count, _raw(stream, block_table))

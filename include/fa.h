@@ -603,7 +603,7 @@ int fa_verify_tree(const int *tokens, const int *parents, const void *target_pro
  * buffer and head, as if only those tokens had been stored; lens[b] = seq_lens[b] + count[b].
  * Rows of the cache that get no node keep their bytes.
  *   caches   : HOST array of n_caches device pointers (1 .. FA_MAX_COPY_CACHES), each bf16
- *              [num_pages][Hkv][page_size][d], 16-byte aligned, none of them twice.
+ *              [num_pages][Hkv][page_size][d], 16-byte aligned; no two overlap.
  *   path     : int32 [B][Nt], its first count[b] entries ascending, 0 .. Nt-1; count int32 [B], 0 ..
  *              Nt; block_table int32 [B][max_pages_per_seq], seq_lens int32 [B] (device memory), as
  *              in fa_decode_paged_tree.  Pages that take a node must not be shared with another
