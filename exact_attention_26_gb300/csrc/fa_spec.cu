@@ -281,8 +281,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
     int n_gone = 0;
     bool stale = false;                       // `total` is not known yet
     if (warp == 0 && rank == 0 && lane == 0) path[0] = 0;
-    // this CTA's, and this warp's, part of a row in units of 16 bytes
-    int turn = 0;
+    int turn = 0;  // of cta_sum
     for (;;) {
         if (warp == 0) {
             for (;;) {
@@ -348,6 +347,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
         const size_t row = (size_t)l.cur * V;
         const int before = (int)(((size_t)b * Nt * V + row) % VEC);
         const Weights<P, DRAFT> weights{target + row, DRAFT ? draft + row : nullptr, sh, l, V};
+        // this CTA's, and this warp's, part of the row in units of 16 bytes
         const int units = (V + before + VEC - 1) / VEC;
         const int per_warp = (units + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
         const int u0 = (rank * kVerifyWarps + warp) * per_warp, u1 = min(u0 + per_warp, units);

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(TreeTile<D, NB>::THREADS, 1)
             for (int k = 0; k < NB; ++k) {
                 mbar_init(bar(ms.s_full[k][u]), 1);
                 mbar_init(bar(ms.p_full[k][u]), 4 * NH);  // one arrival per softmax warp
-                mbar_init(bar(ms.p_half[k][u]), 4);       // two blocks: P of the first half of the keys
+                if (NB == 2) mbar_init(bar(ms.p_half[k][u]), 4);  // P of the first half of the keys
                 mbar_init(bar(ms.pv_done[k][u]), 1);
             }
             mbar_init(bar(ms.q_full[u]), 1);

@@ -1101,9 +1101,6 @@ def _cache16(k_cache, v_cache, block_table, seq_lens, di):
     return B, num_pages, Hkv, page_size, d, max_pages
 
 
-FA_MAX_TREE_NODES = 256
-
-
 def decode_paged_tree(q, k_cache, v_cache, block_table, seq_lens, parents=None, scale=None, out=None,
                       lse=None, workspace=None, stream=None):
     """Attention of drafted tokens against a paged bf16 cache: q bf16 CUDA [B,H,Nq,d], the queries
