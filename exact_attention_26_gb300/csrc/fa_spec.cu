@@ -26,16 +26,16 @@ __device__ __forceinline__ void flag_index(int *status, int site) {
 // part of the row, so that the sums also lead to the token at the end: the CTA, the warp, the step
 // and the lane in which the running sum passes u times the whole.
 //
-// Sums are whole numbers: each weight p - a q is formed without a rounding in fp32 pairs and taken
+// Sums are whole numbers: each weight p - a q is formed in fp32 pairs, to 2^-46 of p, and taken
 // in multiples of 2^-44, so no order of summation and no number of CTAs changes a result, and
-// where p and q are nearly equal nothing is lost.  fp64 would not do: this GPU adds two doubles per
+// where p and a q are nearly equal what is left of them is kept.  fp64 would not do: this GPU adds two doubles per
 // clock and SM.  The numbers are cut out by adding a constant whose last place is the multiple wanted
 // and summing the bit patterns: 13 fp32 and integer operations per element, against two dozen, half
 // of them shifts, of a conversion to 64 bits (B64 Nt24 V128000, six sums one after another: 80 us).
-
 //
-// Measured (GB300, graph replay): B1 Nt16 V32000 fp32 7.7 us, B64 Nt24 V128000 fp32 without repetition 45
-// us, B48 Nt9 V50021 bf16 certain drafts 8.4 us.  CTAs of 256 threads, four to an SM: a wave holds twice
+// Measured (GB300; graph replay of one input, whose rows are then in L2, and calls on inputs that
+// change): B1 Nt16 V32000 fp32 7.7 and 6.4 to 8.7 us, B64 Nt24 V128000 fp32 without repetition 45 and
+// 61 to 63, B48 Nt9 V50021 bf16 certain drafts 8.3 and 8.8.  CTAs of 256 threads, four to an SM: a wave holds twice
 // the sequences that it held with 512 threads, two to an SM (9.7, 47.5 and 9.2 us).
 
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) fa_verify_kernel(const Veri
 // what they were.
 //
 // Measured (GB300, graph replay): 64 sequences of 24 layers (48 cache tensors), Hkv8 d128, 192 rows that
-// move, 37.7 MB read and written: 10.2 us, behind a chain of lookups of about 3; one sequence 2.9 us.
+// move, 37.7 MB read and written: 10.2 us, behind a chain of lookups of about 3; one sequence 2.9 us (calls on inputs that change: 12 and 5.6 to
+// 6.4).
 // Small CTAs of few registers, as many as an SM holds, hide the lookups best: 128 threads with 4 loads in
 // flight 10.2 us, 64 threads 10.7, 256 threads 10.8, with 8 loads in flight 11.9.
 

@@ -10,7 +10,9 @@
 // bits of the nodes that it sees (a tile before them is not masked at all).  The reference of a
 // row's exponents moves only when a score passes it by 2^8; then the thread rescales its row of O.
 // P is rounded to bf16 (2^-8 at most of each term, the sum of the row is taken before that): V is
-// bf16, the product takes both of one type, and O is rounded to bf16 at the end all the same.
+// bf16, the product takes both of one type, and O is rounded to bf16 at the end all the same (2-norm
+// error of O 2.1 to 2.4e-3, and 1.65e-3 where P is in fp32; a second product with what the rounding left
+// would double the work of P V, which two blocks of rows are bound by).
 //
 // Work is cut over the CTAs as fa_cut.cuh describes.  Twelve warps: eight of softmax, which also write
 // the results, two that issue products, one of which also brings the queries and makes the trees (which,
@@ -18,19 +20,23 @@
 // warp for both, pages of 16 made that the bound, B1 131072 keys R = 256 139 us).  Per CTA: a ring of
 // K_0 V_0 K_1 V_1 ..., two S slots, one or two query buffers.
 //
-// Measured (GB300, graph replay with the merge, caches larger than L2 but for the small ones):
-//   B32 H32 Hkv8 Nq32 of 1..8192 keys   101 us  5.6 TB/s  HBM between the items; 4 to 8k clocks for the
-//                                                         results at the end of each, 10k to the first S
-//   B1 H32 Hkv8 Nq64 131072 keys        111 us  4.9 TB/s  3.1k clocks a tile: the chain of one block, 1.5k
-//                                                         of softmax, 0.3k to P's being seen, 1.3k of P V
-//                                                         and the next S, and the other block's turns
-//   B16 H64 Hkv8 Nq48 16384..32768      524 us  3.1 TB/s  the same; 1.18 PFLOP/s
-//   B8 H32 Hkv4 Nq4 d64 5000..32768      36 us  4.4 TB/s  1.5k clocks a tile, of which HBM's rate needs
-//                                                         1.4k, 9k to the first S, results, merge
-//   B5 H16 Hkv2 Nq21 d256 101..2899      24 us            parts: 3 tiles per CTA, whose results are as
-//                                                         large as the keys and values that they read
-//   B1 H32 Hkv8 Nq16 1000 keys           10 us            latency of two launches: lengths, pages, first
-//                                                         copies, results, merge
+// Measured (GB300, with the merge; graph replay of one input, of which L2 keeps a part, then calls on
+// inputs that change, and their rate):
+//   B32 H32 Hkv8 Nq32 of 1..8192 keys   102 us, 103  5.5 TB/s  HBM between the items; 4 to 8k clocks for the
+//                                                              results at the end of each, 10k to the first S
+//   B1 H32 Hkv8 Nq64 131072 keys        110 us, 119  4.5 TB/s  3.1k clocks a tile: the chain of one block, 1.5k
+//                                                              of softmax, 0.3k to P's being seen, 1.3k of P V
+//                                                              and the next S, and the other block's turns;
+//                                                              that is 81 to 87 us of 54 tiles, HBM alone takes
+//                                                              80, and the ring holds two tiles only
+//   B16 H64 Hkv8 Nq48 16384..32768      531 us, 573  2.9 TB/s  the same, 1.08 PFLOP/s; items of R = 256 and 128
+//                                                              in turn, the latter with one block in flight
+//   B8 H32 Hkv4 Nq4 d64 5000..32768      36 us, 37.7 4.3 TB/s  1.5k clocks a tile, of which HBM's rate needs
+//                                                              1.4k, 9k to the first S, results, merge
+//   B5 H16 Hkv2 Nq21 d256 101..2899      24 us, 24.5           parts: 3 tiles per CTA, whose results are as
+//                                                              large as the keys and values that they read
+//   B1 H32 Hkv8 Nq16 1000 keys         10.4 us, 10.8           latency of two launches: lengths, pages, first
+//                                                              copies, results, merge
 // Tried and slower: S slots of 64 keys, two per block (116 -> 197 us); a cluster of a CTA per block with
 // the copies shared out and multicast (two tiles in the ring are too few: 150 us); one product of 256 rows
 // by a pair of CTAs, each with half of K's rows and V's columns (330 us, the reason was not found); boxes of

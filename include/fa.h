@@ -534,6 +534,7 @@ int fa_copy_pages(void *const *caches, const size_t *page_bytes, int n_caches, i
  * probability is (infinities of both signs: NaN).  So does one of a cached token, but where its
  * probability is below fp32's smallest an infinity may become NaN.
  * Rounding: probabilities enter the product with V in bf16 (2^-8 relative), sums are fp32.
+ * (fa_decode_paged, for queries that all see the same keys, keeps probabilities in fp32.)
  *   B, H, Nq >= 1; Hkv divides H; Nq <= Nt <= FA_MAX_TREE_NODES; d: 64, 96, 128 or 256;
  *   (H / Hkv) * Nq <= 65535, B * H * Nq < 2^31, page_size * max_pages_per_seq < 2^31 - 1024, B *
  *   max_pages_per_seq and num_pages * Hkv < 2^31, and the tiles of 128 keys (64 where d = 256) of
@@ -582,8 +583,9 @@ int fa_decode_paged_tree(const void *q, const void *k_cache, const void *v_cache
  *              t_{k+1} = t_k - p_k(x); p_0 = p.
  * The last token is the least i with P(0) + ... + P(i) > u (P(0) + ... + P(V-1)), P(i) = max(p(i) -
  * a_k q(i), 0) or p_k(i) after the node's last rejection, or p itself where nothing is left.
- * Sums over the vocabulary are those of the addends taken in multiples of 2^-44, without error: no
- * order of summation and no device changes a result.  The values of a row, taken so, sum to less
+ * Sums over the vocabulary are those of the addends, formed to 2^-46 of p(i), taken in multiples of
+ * 2^-44, without error: no order of summation and no device changes a result.  a_k, s_k, t_k and their
+ * products are kept to 2^-46 of themselves.  The values of a row, taken so, sum to less
  * than 2^20 (probabilities sum to 1).
  * Outputs (int32, every element is written):
  *   path     : [B][Nt]: the accepted nodes from node 0 on, then -1.
