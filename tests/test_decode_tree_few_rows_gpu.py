@@ -1,5 +1,5 @@
-"""Attention of drafted trees whose rows fill a part of a block only: their scores are shared out to
-all warps, by the number of rows, against the float64 oracle."""
+"""Attention of drafted trees whose rows fill a part of a block only, so that some warps have few rows
+or none, against the float64 oracle."""
 from __future__ import annotations
 
 import pytest
